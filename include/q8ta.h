@@ -466,6 +466,63 @@ q8_status q8_conv2d_packed_acc32(const int8_t* x, const q8_conv2d_shape* shape,
                                  int32_t input_zero_point, const void* packed_weight, int32_t* acc,
                                  void* workspace, size_t workspace_bytes, q8_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Rows of one batch that go through different weights                       */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages have no counterpart for the entry points below; their guards are
+ * all this library's.  They serve the two places where the rows of one batch
+ * of an int8 model meet different weights: the experts of a mixture layer,
+ * and the low-rank adapters of many requests beside a shared projection.
+ */
+typedef enum q8_dtype { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2, Q8_I8 = 3 } q8_dtype;
+
+/*
+ * Tokens sorted by expert and back.  Each of T tokens chooses k experts:
+ * slot f = t*k + j holds expert_ids[t, j].  A slot whose id lies outside
+ * [0, E) is dropped: it has no row, adds nothing and gets zero gradients.
+ *   q8_expert_sort  stable by id:
+ *     offsets  int32 [E + 1]: rows offsets[e] .. offsets[e+1]-1 are expert e's,
+ *              offsets[E] the number of kept slots
+ *     order    int32 [T*k]: the slot at each sorted row, -1 from offsets[E] on
+ *     position int32 [T, k]: each slot's sorted row, -1 when dropped
+ *   q8_expert_gather  xs[row] = x[order[row] / k] (any dtype), zeros in the
+ *     rows from offsets[E] on.  x [T, H], xs [T*k, H].
+ *   q8_expert_dispatch  the sort, then the gather.
+ *   q8_expert_gather_backward  dx[t] = sum_j dxs[position[t,j]].
+ *   q8_expert_combine  y[t] = sum_j weights[t,j] * z[position[t,j]]; a token
+ *     whose slots are all dropped gets zeros.  weights float [T, k].
+ *   q8_expert_combine_backward  dz[row] = weights[order[row]] *
+ *     dy[order[row] / k], zeros from offsets[E] on; dweights[t,j] =
+ *     <dy[t], z[position[t,j]]>, 0 when dropped.
+ * Rows of float dtype are summed in f32 in slot order and rounded once; the
+ * results do not depend on timing.  A dropped slot's rows are never read.
+ * Guards: T >= 0 (0: only offsets are written, as zeros), k, H >= 1,
+ * 1 <= E <= 1024, T*k <= INT32_MAX, T*k*H within int64; Q8_I8 for the gather
+ * only (Q8_ERR_UNSUPPORTED elsewhere).  Positions that lie outside [0, T*k)
+ * count as dropped.  Rows of any length and alignment of the element type
+ * are taken; rows of a multiple of 16 bytes on 16-byte aligned bases are
+ * the fast form.
+ */
+q8_status q8_expert_sort(const int32_t* expert_ids, int64_t T, int64_t k, int64_t E,
+                         int32_t* order, int32_t* position, int32_t* offsets, q8_stream_t stream);
+q8_status q8_expert_gather(const void* x, q8_dtype dtype, int64_t T, int64_t k, int64_t H,
+                           int64_t E, const int32_t* position, const int32_t* offsets, void* xs,
+                           q8_stream_t stream);
+q8_status q8_expert_dispatch(const void* x, q8_dtype dtype, int64_t T, int64_t H,
+                             const int32_t* expert_ids, int64_t k, int64_t E, int32_t* order,
+                             int32_t* position, int32_t* offsets, void* xs, q8_stream_t stream);
+q8_status q8_expert_gather_backward(const void* dxs, q8_dtype dtype, int64_t T, int64_t k,
+                                    int64_t H, const int32_t* position, void* dx,
+                                    q8_stream_t stream);
+q8_status q8_expert_combine(const void* z, q8_dtype dtype, const float* weights, int64_t T,
+                            int64_t k, int64_t H, const int32_t* position, void* y,
+                            q8_stream_t stream);
+q8_status q8_expert_combine_backward(const void* dy, const void* z, q8_dtype dtype,
+                                     const float* weights, int64_t T, int64_t k, int64_t H,
+                                     int64_t E, const int32_t* position, const int32_t* offsets,
+                                     void* dz, float* dweights, q8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,8 @@ EXPORTS = (
     "q8_conv2d_workspace_bytes", "q8_conv2d", "q8_conv2d_acc32", "q8_conv2d_packed_weight_bytes",
     "q8_conv2d_packed_workspace_bytes", "q8_conv2d_pack_weight", "q8_conv2d_packed",
     "q8_conv2d_packed_acc32",
+    "q8_expert_sort", "q8_expert_gather", "q8_expert_dispatch", "q8_expert_gather_backward",
+    "q8_expert_combine", "q8_expert_combine_backward",
 )
 
 
@@ -126,6 +128,13 @@ def _load() -> ctypes.CDLL:
         "q8_conv2d_pack_weight": (ctypes.c_int, [P, DP, P, S, P]),
         "q8_conv2d_packed": (ctypes.c_int, [P, DP, D, I32, P, P, P, D, I32, C, P, P, S, P]),
         "q8_conv2d_packed_acc32": (ctypes.c_int, [P, DP, I32, P, P, P, S, P]),
+        "q8_expert_sort": (ctypes.c_int, [P, I64, I64, I64, P, P, P, P]),
+        "q8_expert_gather": (ctypes.c_int, [P, I32, I64, I64, I64, I64, P, P, P, P]),
+        "q8_expert_dispatch": (ctypes.c_int, [P, I32, I64, I64, P, I64, I64, P, P, P, P, P]),
+        "q8_expert_gather_backward": (ctypes.c_int, [P, I32, I64, I64, I64, P, P, P]),
+        "q8_expert_combine": (ctypes.c_int, [P, I32, P, I64, I64, I64, P, P, P]),
+        "q8_expert_combine_backward": (ctypes.c_int, [P, P, I32, P, I64, I64, I64, I64, P, P, P, P,
+                                                      P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -819,3 +828,10 @@ def conv2d_packed_acc32(x, input_zero_point, packed: PackedConvWeight, output_si
                                        _ptr(packed.data), _ptr(out), _ptr(ws), nbytes, _stream(x)),
            "q8_conv2d_packed_acc32")
     return out
+
+
+# ---------------------------------------------------------------------------
+# rows of one batch that go through different weights
+# ---------------------------------------------------------------------------
+from .rows import (ExpertRoute, expert_combine, expert_combine_backward, expert_dispatch,  # noqa: E402
+                   expert_gather, expert_gather_backward, expert_sort)

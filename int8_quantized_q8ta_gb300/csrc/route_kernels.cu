@@ -1,0 +1,407 @@
+// route_kernels.cu -- tokens sorted by expert and back, with weights applied,
+// and the gradients (sm_103a).
+//
+// T tokens choose k experts each; slot f = t*k + j holds the id e_f.  A slot
+// whose id lies outside [0, E) is dropped.
+//   sort     stable by id: offsets[e] = #{f : 0 <= e_f < e}; position[f] is
+//            slot f's row, order[row] its inverse; -1 marks a dropped slot in
+//            position and the rows from offsets[E] on in order
+//   gather   xs[row] = x[order[row] / k], zeros from row offsets[E] on
+//   spread   the sum that brings rows back to tokens, with weights (combine)
+//            or without (the gather's gradient):
+//            y[t] = sum_j w[t,j] * z[position[t,j]] over the kept slots
+//   combine's gradient  dz[row] = w[order[row]] * dy[order[row] / k] and
+//            dw[t,j] = <dy[t], z[position[t,j]]>
+// Sums are f32, taken in slot order j = 0, 1, ..., rounded once to the row
+// type.  No atomics on global memory: results do not depend on timing.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+#include <type_traits>
+
+#include "device_common.cuh"
+#include "q8ta_internal.h"
+#include "rows_internal.h"
+
+namespace q8 {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// sort: a counting sort by one cluster.  Each CTA owns a contiguous run of
+// slots and each of its warps a contiguous part of that run, so a slot's row
+// is (all slots of lower experts) + (its expert's slots in earlier CTAs) +
+// (in earlier warps of its CTA) + (earlier in its warp): stable by
+// construction.  The CTAs exchange their E + 1 totals through distributed
+// shared memory; nothing but the ids is read from global memory.
+// ---------------------------------------------------------------------------
+constexpr int kSortMaxWarps = 32;
+
+__device__ __forceinline__ int sort_key(const int32_t* ids, int64_t f, int E) {
+  const int e = __ldg(ids + f);
+  return (e >= 0 && e < E) ? e : E;
+}
+
+__global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __restrict__ ids,
+                                                           int64_t R, int E,
+                                                           int32_t* __restrict__ order,
+                                                           int32_t* __restrict__ position,
+                                                           int32_t* __restrict__ offsets) {
+  extern __shared__ int32_t sm[];
+  const int G = E + 1;                        // groups: the experts and the dropped slots
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* hist = sm;                         // [warps][G]
+  int32_t* total = sm + warps * G;            // [G], read by the other CTAs
+  int32_t* start = total + G;                 // [G]
+  __shared__ int32_t carry[kSortMaxWarps + 1];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+
+  for (int i = threadIdx.x; i < warps * G; i += blockDim.x) hist[i] = 0;
+  // slots per warp, a multiple of 32 so that only the last run is ragged
+  const int64_t per = ((R + static_cast<int64_t>(ctas) * warps * 32 - 1) /
+                       (static_cast<int64_t>(ctas) * warps * 32)) * 32;
+  const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * per;
+  const int64_t hi = min(R, lo + per);
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t* mine = hist + warp * G;
+  for (int64_t f = lo + lane; f < hi; f += 32) atomicAdd(&mine[sort_key(ids, f, E)], 1);
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
+    int32_t sum = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int32_t c = hist[w * G + g];
+      hist[w * G + g] = sum;
+      sum += c;
+    }
+    total[g] = sum;
+  }
+  cluster.sync();
+  // exclusive scan over the groups of the cluster's totals, a block of
+  // threads at a time
+  int32_t before_all = 0;
+  for (int g0 = 0; g0 < G; g0 += blockDim.x) {
+    const int g = g0 + threadIdx.x;
+    int32_t all = 0, earlier = 0;
+    if (g < G)
+      for (int c = 0; c < ctas; ++c) {
+        const int32_t v = *cluster.map_shared_rank(total + g, c);
+        if (c < rank) earlier += v;
+        all += v;
+      }
+    int32_t incl = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) carry[warp] = incl;
+    __syncthreads();
+    int32_t add = before_all, whole = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) add += carry[w];
+      whole += carry[w];
+    }
+    before_all += whole;
+    const int32_t excl = add + incl - all;
+    if (g < G) {
+      start[g] = excl + earlier;
+      if (rank == 0) offsets[g] = excl;       // offsets[E]: the kept slots
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < warps * G; i += blockDim.x) hist[i] += start[i % G];
+  cluster.sync();                             // totals stay readable until every CTA is done
+  for (int64_t f0 = lo; f0 < hi; f0 += 32) {
+    const int64_t f = f0 + lane;
+    const bool in = f < hi;
+    const int key = in ? sort_key(ids, f, E) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, key);
+    const int rank_in = __popc(peers & ((1u << lane) - 1u));
+    int32_t row = 0;
+    if (in) row = mine[key] + rank_in;
+    __syncwarp();
+    if (in && rank_in == 0) mine[key] += __popc(peers);
+    __syncwarp();
+    if (in) {
+      order[row] = key < E ? static_cast<int32_t>(f) : -1;
+      position[f] = key < E ? row : -1;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows as vectors: VB bytes of T at a time
+// ---------------------------------------------------------------------------
+template <int VB> struct VecOf;
+template <> struct VecOf<16> { using type = uint4; };
+template <> struct VecOf<8> { using type = uint2; };
+template <> struct VecOf<4> { using type = uint32_t; };
+template <> struct VecOf<2> { using type = uint16_t; };
+template <> struct VecOf<1> { using type = uint8_t; };
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+template <typename T, int VB>
+union Pack {
+  typename VecOf<VB>::type v;
+  T e[VB / sizeof(T)];
+  __device__ Pack() {}
+};
+
+// Zeros in the rows from offsets[E] on (dropped slots), by whole warps.
+template <int VB>
+__device__ __forceinline__ void zero_tail(typename VecOf<VB>::type* rows, int64_t V, int64_t R,
+                                          const int32_t* offsets, int E, int64_t warp_id,
+                                          int64_t num_warps, int lane) {
+  typename VecOf<VB>::type zero{};
+  for (int64_t s = max(0, __ldg(offsets + E)) + warp_id; s < R; s += num_warps)
+    for (int64_t c = lane; c < V; c += 32) rows[s * V + c] = zero;
+}
+
+// gather: a warp takes U*32 vectors of one token's row, read once and written
+// to each of the token's kept rows.
+template <int VB, int U>
+__global__ void __launch_bounds__(256) expert_gather_kernel(
+    const typename VecOf<VB>::type* __restrict__ x, int64_t T, int k, int64_t V,
+    const int32_t* __restrict__ position, const int32_t* __restrict__ offsets, int E,
+    typename VecOf<VB>::type* __restrict__ xs) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp_id = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t num_warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  const int64_t segs = (V + U * 32 - 1) / (U * 32);
+  for (int64_t u = warp_id; u < T * segs; u += num_warps) {
+    const int64_t t = u / segs, c0 = (u - t * segs) * (U * 32) + lane;
+    typename VecOf<VB>::type v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c0 + i * 32 < V) v[i] = __ldg(x + t * V + c0 + i * 32);
+    for (int j = 0; j < k; ++j) {
+      const int64_t s = __ldg(position + t * k + j);
+      if (s < 0 || s >= T * k) continue;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * 32 < V) xs[s * V + c0 + i * 32] = v[i];
+    }
+  }
+  zero_tail<VB>(xs, V, T * k, offsets, E, warp_id, num_warps, lane);
+}
+
+// spread: a warp takes U*32 vectors of one token's sum.  w: null for ones.
+template <typename T, int VB, int U>
+__global__ void __launch_bounds__(256) expert_spread_kernel(
+    const typename VecOf<VB>::type* __restrict__ z, const float* __restrict__ w, int64_t Tn, int k,
+    int64_t V, const int32_t* __restrict__ position, typename VecOf<VB>::type* __restrict__ y) {
+  constexpr int N = VB / sizeof(T);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp_id = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t num_warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  const int64_t segs = (V + U * 32 - 1) / (U * 32);
+  for (int64_t u = warp_id; u < Tn * segs; u += num_warps) {
+    const int64_t t = u / segs, c0 = (u - t * segs) * (U * 32) + lane;
+    float acc[U][N];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[i][n] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int64_t s = __ldg(position + t * k + j);
+      if (s < 0 || s >= Tn * k) continue;
+      const float wj = w != nullptr ? __ldg(w + t * k + j) : 1.0f;
+      Pack<T, VB> p[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * 32 < V) p[i].v = __ldg(z + s * V + c0 + i * 32);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * 32 < V)
+#pragma unroll
+          for (int n = 0; n < N; ++n) acc[i][n] = fmaf(wj, to_f32<T>(p[i].e[n]), acc[i][n]);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c0 + i * 32 < V) {
+        Pack<T, VB> p;
+#pragma unroll
+        for (int n = 0; n < N; ++n) p.e[n] = from_f32<T>(acc[i][n]);
+        y[t * V + c0 + i * 32] = p.v;
+      }
+  }
+}
+
+// combine's gradient: a warp takes one slot, its whole row: dz is the token's
+// dy times the slot's weight, dw the dot of dy with the slot's z.
+template <typename T, int VB>
+__global__ void __launch_bounds__(256) expert_combine_bwd_kernel(
+    const typename VecOf<VB>::type* __restrict__ dy, const typename VecOf<VB>::type* __restrict__ z,
+    const float* __restrict__ w, int64_t R, int k, int64_t V, const int32_t* __restrict__ position,
+    const int32_t* __restrict__ offsets, int E, typename VecOf<VB>::type* __restrict__ dz,
+    float* __restrict__ dw) {
+  constexpr int N = VB / sizeof(T);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp_id = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t num_warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  for (int64_t f = warp_id; f < R; f += num_warps) {
+    const int64_t s = __ldg(position + f), t = f / k;
+    float dot = 0.0f;
+    if (s >= 0 && s < R) {
+      const float wf = __ldg(w + f);
+      for (int64_t c = lane; c < V; c += 32) {
+        Pack<T, VB> a, b, o;
+        a.v = __ldg(dy + t * V + c);
+        b.v = __ldg(z + s * V + c);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const float g = to_f32<T>(a.e[n]);
+          dot = fmaf(g, to_f32<T>(b.e[n]), dot);
+          o.e[n] = from_f32<T>(wf * g);
+        }
+        dz[s * V + c] = o.v;
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (lane == 0) dw[f] = dot;
+  }
+  zero_tail<VB>(dz, V, R, offsets, E, warp_id, num_warps, lane);
+}
+
+// The widest vector that divides the row and every base address.
+int vec_bytes(int64_t row_bytes, std::initializer_list<const void*> ptrs) {
+  uintptr_t bits = static_cast<uintptr_t>(row_bytes);
+  for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+  for (int v = 16; v > 1; v >>= 1)
+    if (bits % v == 0) return v;
+  return 1;
+}
+
+int warp_grid(int64_t units) {
+  const int64_t blocks = (units + 7) / 8;
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(blocks, static_cast<int64_t>(device_sm_count()) * 8)));
+}
+
+}  // namespace
+
+size_t expert_sort_smem(int threads, int E) {
+  return (static_cast<size_t>(threads / 32) + 2) * (E + 1) * sizeof(int32_t);
+}
+
+cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* order,
+                               int32_t* position, int32_t* offsets, cudaStream_t s) {
+  // one CTA up to 4096 slots (4 rounds of its 32 warps), then up to 8
+  const int threads = R <= 256 ? 256 : 1024;
+  int ctas = 1;
+  while (ctas < 8 && R > 4096ll * ctas) ctas *= 2;
+  const size_t smem = expert_sort_smem(threads, E);
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(expert_sort_smem(1024, kMaxExperts)));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(expert_sort_kernel, ctas, threads, smem, ctas, s, ids, R, E, order,
+                            position, offsets);
+}
+
+cudaError_t launch_expert_gather(const void* x, int64_t T, int k, int64_t row_bytes,
+                                 const int32_t* position, const int32_t* offsets, int E, void* xs,
+                                 cudaStream_t s) {
+  auto go = [&](auto tag) {
+    constexpr int VB = decltype(tag)::value;
+    using V = typename VecOf<VB>::type;
+    constexpr int U = 4;
+    const int64_t vecs = row_bytes / VB;
+    return launch_pdl(expert_gather_kernel<VB, U>, warp_grid(T * ((vecs + U * 32 - 1) / (U * 32))),
+                      256, 0, s, static_cast<const V*>(x), T, k, vecs, position, offsets, E,
+                      static_cast<V*>(xs));
+  };
+  switch (vec_bytes(row_bytes, {x, xs})) {
+    case 16: return go(std::integral_constant<int, 16>());
+    case 8: return go(std::integral_constant<int, 8>());
+    case 4: return go(std::integral_constant<int, 4>());
+    case 2: return go(std::integral_constant<int, 2>());
+    default: return go(std::integral_constant<int, 1>());
+  }
+}
+
+namespace {
+
+// fn(type tag, vector width) for the row type and the widest usable vector;
+// narrower than 16 bytes one element at a time.
+template <typename T, typename F>
+cudaError_t with_vec(int vb, F&& fn) {
+  if (vb == 16) return fn(T{}, std::integral_constant<int, 16>());
+  return fn(T{}, std::integral_constant<int, sizeof(T)>());
+}
+
+template <typename F>
+cudaError_t with_type(q8_dtype dt, int vb, F&& fn) {
+  switch (dt) {
+    case Q8_F32: return with_vec<float>(vb, fn);
+    case Q8_F16: return with_vec<__half>(vb, fn);
+    default: return with_vec<__nv_bfloat16>(vb, fn);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_expert_spread(const void* z, q8_dtype dt, const float* w, int64_t T, int k,
+                                 int64_t H, const int32_t* position, void* y, cudaStream_t s) {
+  const int64_t row_bytes = H * dtype_bytes(dt);
+  return with_type(dt, vec_bytes(row_bytes, {z, y}), [&](auto elem, auto vb) {
+    using T_ = decltype(elem);
+    constexpr int VB = decltype(vb)::value;
+    using V = typename VecOf<VB>::type;
+    constexpr int U = VB == 16 ? 2 : 4;
+    const int64_t vecs = row_bytes / VB;
+    return launch_pdl(expert_spread_kernel<T_, VB, U>,
+                      warp_grid(T * ((vecs + U * 32 - 1) / (U * 32))), 256, 0, s,
+                      static_cast<const V*>(z), w, T, k, vecs, position, static_cast<V*>(y));
+  });
+}
+
+cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt, const float* w,
+                                      int64_t T, int k, int64_t H, const int32_t* position,
+                                      const int32_t* offsets, int E, void* dz, float* dw,
+                                      cudaStream_t s) {
+  const int64_t row_bytes = H * dtype_bytes(dt);
+  return with_type(dt, vec_bytes(row_bytes, {dy, z, dz}), [&](auto elem, auto vb) {
+    using T_ = decltype(elem);
+    constexpr int VB = decltype(vb)::value;
+    using V = typename VecOf<VB>::type;
+    return launch_pdl(expert_combine_bwd_kernel<T_, VB>, warp_grid(T * k), 256, 0, s,
+                      static_cast<const V*>(dy), static_cast<const V*>(z), w, T * k, k,
+                      row_bytes / VB, position, offsets, E, static_cast<V*>(dz), dw);
+  });
+}
+
+}  // namespace q8

@@ -1,0 +1,184 @@
+"""Rows of one batch that go through different weights (the last part of
+include/q8ta.h): tokens sorted by expert and back, with weights applied, and
+the gradients.
+
+Argument marshalling only, like the rest of the package; imported by it.
+"""
+from __future__ import annotations
+
+import dataclasses
+from typing import Optional, Tuple
+
+import torch
+
+from . import _check, _lib, _need, _ptr, _stream
+
+_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16, bfloat16 or int8, got {t.dtype}")
+    return code
+
+
+def _shape(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _out(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out") -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, dtype, name)
+    _shape(out, shape, name)
+    return out
+
+
+@dataclasses.dataclass
+class ExpertRoute:
+    """Slots sorted by expert (see q8_expert_sort): ``order`` int32 [T*k],
+    ``position`` int32 [T, k], ``offsets`` int32 [E + 1]."""
+    order: torch.Tensor
+    position: torch.Tensor
+    offsets: torch.Tensor
+
+    @property
+    def T(self) -> int:
+        return self.position.shape[0]
+
+    @property
+    def k(self) -> int:
+        return self.position.shape[1]
+
+    @property
+    def E(self) -> int:
+        return self.offsets.shape[0] - 1
+
+
+def _need_route(route: ExpertRoute) -> ExpertRoute:
+    _need(route.order, torch.int32, "route.order")
+    _need(route.position, torch.int32, "route.position")
+    _need(route.offsets, torch.int32, "route.offsets")
+    if route.position.dim() != 2 or route.offsets.dim() != 1 or route.E < 1:
+        raise ValueError("route.position must be [T, k] and route.offsets [E + 1]")
+    _shape(route.order, (route.T * route.k,), "route.order")
+    return route
+
+
+def _empty_route(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
+    _need(expert_ids, torch.int32, "expert_ids")
+    if expert_ids.dim() != 2:
+        raise ValueError(f"expert_ids must be [T, k], got {tuple(expert_ids.shape)}")
+    if not 1 <= num_experts <= 1024:
+        raise ValueError(f"num_experts must lie in [1, 1024], got {num_experts}")
+    # one allocation for the three parts, each of them contiguous
+    T, k = expert_ids.shape
+    R = T * k
+    buf = torch.empty(2 * R + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
+    return ExpertRoute(buf[:R], buf[R:2 * R].view(T, k), buf[2 * R:])
+
+
+def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
+    """Slots of int32 expert_ids [T, k] sorted by expert, stable; ids outside
+    [0, num_experts) are dropped slots."""
+    route = _empty_route(expert_ids, num_experts)
+    T, k = expert_ids.shape
+    _check(_lib.q8_expert_sort(_ptr(expert_ids), T, k, num_experts, _ptr(route.order),
+                               _ptr(route.position), _ptr(route.offsets), _stream(expert_ids)),
+           "q8_expert_sort")
+    return route
+
+
+def expert_gather(x: torch.Tensor, route: ExpertRoute,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of x [T, H] (float32, float16, bfloat16 or int8) in sorted order,
+    [T*k, H]; zeros from row offsets[E] on."""
+    code = _dtype_code(x, "x")
+    _need(x, x.dtype, "x")
+    _need_route(route)
+    T, k = route.T, route.k
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError(f"x must be [{T}, H], got {tuple(x.shape)}")
+    H = x.shape[1]
+    out = _out(out, (T * k, H), x.dtype, x.device)
+    _check(_lib.q8_expert_gather(_ptr(x), code, T, k, H, route.E, _ptr(route.position),
+                                 _ptr(route.offsets), _ptr(out), _stream(x)), "q8_expert_gather")
+    return out
+
+
+def expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: int,
+                    out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ExpertRoute]:
+    """expert_sort, then expert_gather: returns (rows, route)."""
+    code = _dtype_code(x, "x")
+    _need(x, x.dtype, "x")
+    route = _empty_route(expert_ids, num_experts)
+    T, k = expert_ids.shape
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError(f"x must be [{T}, H], got {tuple(x.shape)}")
+    H = x.shape[1]
+    out = _out(out, (T * k, H), x.dtype, x.device)
+    _check(_lib.q8_expert_dispatch(_ptr(x), code, T, H, _ptr(expert_ids), k, num_experts,
+                                   _ptr(route.order), _ptr(route.position), _ptr(route.offsets),
+                                   _ptr(out), _stream(x)), "q8_expert_dispatch")
+    return out, route
+
+
+def _need_rows(t: torch.Tensor, route: ExpertRoute, name: str) -> int:
+    code = _dtype_code(t, name)
+    _need(t, t.dtype, name)
+    if t.dim() != 2 or t.shape[0] != route.T * route.k:
+        raise ValueError(f"{name} must be [{route.T * route.k}, H], got {tuple(t.shape)}")
+    return code
+
+
+def expert_gather_backward(d_rows: torch.Tensor, route: ExpertRoute,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gather's gradient: each token's kept rows added up in f32, [T, H]."""
+    _need_route(route)
+    code = _need_rows(d_rows, route, "d_rows")
+    T, k, H = route.T, route.k, d_rows.shape[1]
+    out = _out(out, (T, H), d_rows.dtype, d_rows.device)
+    _check(_lib.q8_expert_gather_backward(_ptr(d_rows), code, T, k, H, _ptr(route.position),
+                                          _ptr(out), _stream(d_rows)),
+           "q8_expert_gather_backward")
+    return out
+
+
+def _need_weights(weights: torch.Tensor, route: ExpertRoute) -> None:
+    _need(weights, torch.float32, "weights")
+    _shape(weights, (route.T, route.k), "weights")
+
+
+def expert_combine(z: torch.Tensor, weights: torch.Tensor, route: ExpertRoute,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] * (slot (t, j)'s row of z), [T, H]."""
+    _need_route(route)
+    code = _need_rows(z, route, "z")
+    _need_weights(weights, route)
+    T, k, H = route.T, route.k, z.shape[1]
+    out = _out(out, (T, H), z.dtype, z.device)
+    _check(_lib.q8_expert_combine(_ptr(z), code, _ptr(weights), T, k, H, _ptr(route.position),
+                                  _ptr(out), _stream(z)), "q8_expert_combine")
+    return out
+
+
+def expert_combine_backward(dy: torch.Tensor, z: torch.Tensor, weights: torch.Tensor,
+                            route: ExpertRoute) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The combine's gradients (dz like z, dweights float32 [T, k])."""
+    _need_route(route)
+    code = _need_rows(z, route, "z")
+    _need_weights(weights, route)
+    _need(dy, z.dtype, "dy")
+    T, k, H = route.T, route.k, z.shape[1]
+    _shape(dy, (T, H), "dy")
+    dz = torch.empty_like(z)
+    dw = torch.empty((T, k), dtype=torch.float32, device=z.device)
+    _check(_lib.q8_expert_combine_backward(_ptr(dy), _ptr(z), code, _ptr(weights), T, k, H,
+                                           route.E, _ptr(route.position), _ptr(route.offsets),
+                                           _ptr(dz), _ptr(dw), _stream(z)),
+           "q8_expert_combine_backward")
+    return dz, dw

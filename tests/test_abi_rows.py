@@ -1,0 +1,80 @@
+"""Host-side guards of the entry points for rows that go through different
+weights (no GPU needed: every call is refused, or has nothing to do, before
+anything is enqueued)."""
+import ctypes
+
+import pytest
+
+q8 = pytest.importorskip("int8_quantized_q8ta_gb300")
+lib = q8.lib()
+
+FAKE = ctypes.c_void_p(0x10000)  # never dereferenced
+ODD = ctypes.c_void_p(0x10002)
+F32, F16, BF16, I8 = range(4)
+
+
+def test_sort_guards():
+    f = lib.q8_expert_sort
+    assert f(None, 4, 2, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert f(FAKE, 4, 2, 8, None, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert f(FAKE, 4, 2, 8, FAKE, None, FAKE, None) == q8.Q8_ERR_NULL
+    assert f(None, 0, 2, 8, None, None, None, None) == q8.Q8_ERR_NULL   # offsets are written
+    assert f(FAKE, -1, 2, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert f(FAKE, 4, 0, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert f(FAKE, 4, 2, 0, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert f(FAKE, 4, 2, 1025, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert f(FAKE, 2 ** 30, 2, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE   # T*k > INT32_MAX
+    assert f(FAKE, 2 ** 62, 4, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert f(FAKE, 4, 2, 8, ODD, FAKE, FAKE, None) == q8.Q8_ERR_ALIGN
+
+
+def test_gather_and_dispatch_guards():
+    g = lib.q8_expert_gather
+    assert g(FAKE, 7, 4, 2, 16, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_ARG
+    assert g(None, F32, 4, 2, 16, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert g(FAKE, F32, 4, 2, 16, 8, None, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert g(FAKE, F32, 4, 2, 0, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert g(FAKE, F32, 2 ** 20, 2, 2 ** 50, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert g(ODD, F32, 4, 2, 16, 8, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_ALIGN
+    assert g(None, F32, 0, 2, 16, 8, None, None, None, None) == q8.Q8_OK       # nothing to move
+    d = lib.q8_expert_dispatch
+    assert d(None, I8, 4, 16, FAKE, 2, 8, FAKE, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert d(FAKE, I8, 4, 16, FAKE, 2, 8, FAKE, FAKE, FAKE, None, None) == q8.Q8_ERR_NULL
+    assert d(FAKE, 9, 4, 16, FAKE, 2, 8, FAKE, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_ARG
+    assert d(FAKE, F16, 4, 16, FAKE, 2, 2000, FAKE, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    assert d(FAKE, F16, 4, 16, None, 2, 8, FAKE, FAKE, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+
+
+def test_combine_and_gradient_guards():
+    c = lib.q8_expert_combine
+    assert c(FAKE, I8, FAKE, 4, 2, 16, FAKE, FAKE, None) == q8.Q8_ERR_UNSUPPORTED
+    assert c(FAKE, -1, FAKE, 4, 2, 16, FAKE, FAKE, None) == q8.Q8_ERR_ARG
+    assert c(FAKE, F32, None, 4, 2, 16, FAKE, FAKE, None) == q8.Q8_ERR_NULL
+    assert c(FAKE, F32, FAKE, 4, 2, 16, FAKE, ODD, None) == q8.Q8_ERR_ALIGN
+    assert c(FAKE, BF16, FAKE, 4, 2, -1, FAKE, FAKE, None) == q8.Q8_ERR_SHAPE
+    b = lib.q8_expert_gather_backward
+    assert b(FAKE, I8, 4, 2, 16, FAKE, FAKE, None) == q8.Q8_ERR_UNSUPPORTED
+    assert b(FAKE, F32, 4, 2, 16, None, FAKE, None) == q8.Q8_ERR_NULL
+    assert b(ODD, F32, 4, 2, 16, FAKE, FAKE, None) == q8.Q8_ERR_ALIGN
+    w = lib.q8_expert_combine_backward
+    ok = [FAKE, FAKE, F32, FAKE, 4, 2, 16, 8, FAKE, FAKE, FAKE, FAKE, None]
+
+    def call(**at):
+        a = list(ok)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return w(*a)
+    for i in (0, 1, 3, 8, 9, 10, 11):
+        assert call(**{f"a{i}": None}) == q8.Q8_ERR_NULL
+        assert call(**{f"a{i}": ODD}) == q8.Q8_ERR_ALIGN
+    assert call(a2=I8) == q8.Q8_ERR_UNSUPPORTED
+    assert call(a7=0) == q8.Q8_ERR_SHAPE
+
+
+def test_binding_refuses_cpu_tensors():
+    torch = pytest.importorskip("torch")
+    ids = torch.zeros((2, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        q8.expert_sort(ids, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        q8.expert_dispatch(torch.zeros(2, 8), ids, 4)
