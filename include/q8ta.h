@@ -523,6 +523,46 @@ q8_status q8_expert_combine_backward(const void* dy, const void* z, q8_dtype dty
                                      int64_t E, const int32_t* position, const int32_t* offsets,
                                      void* dz, float* dweights, q8_stream_t stream);
 
+/*
+ * The experts' int8 products: each sorted row times the int8 weight of its
+ * expert, with the epilogue of q8_linear,
+ *   acc[s,n] = sum_k (x[row(s),k] - input_zero_point) * weight[e(s)][n,k],
+ * exact int32, scales and bias of the row's expert.
+ *   x             int8 [T, K] (x_sorted 0: sorted row s reads token
+ *                 order[s] / k) or [T*k, K] already in sorted order
+ *                 (x_sorted 1, order is not read)
+ *   order, offsets  as q8_expert_sort leaves them (device)
+ *   weight_scales float [E, N]; bias float [E, N] or NULL
+ *   out           [T*k, N] of out_dtype: Q8_I8 requantizes as q8_linear
+ *                 does; Q8_F32 / Q8_F16 / Q8_BF16 round the dequantized
+ *                 (and, for "relu", raised) value once.  Rows from
+ *                 offsets[E] on hold the value 0 (int8: output_zero_point).
+ * The weight is packed once, at load time, and stays int8: for each block of
+ * 128 output channels and 64 inputs one contiguous 8 KB tile, and a 256-byte
+ * trailer whose first int32 is the largest sum of |w| over 64 consecutive
+ * inputs of one row (results never depend on it).  q8_tile_pack_weight
+ * takes [E, N, K] (E = 1: one weight), waits for the packing, and a packed
+ * buffer is rewritten only by packing into it again.
+ * Guards: those of q8_expert_sort; N, K >= 1; E*N*K within int64; the scale
+ * and zero-point ranges; activation "none" or "relu"; workspace of
+ * q8_linear_experts_workspace_bytes(T*k, K, E) bytes and the packed weight
+ * 256-byte aligned.  Order entries outside the rows of x leave their sorted
+ * row undefined; offsets are clamped to [0, T*k].  The kernels' bounded
+ * waits report device error codes 0x10A .. 0x10C.
+ */
+size_t q8_tile_packed_weight_bytes(int64_t E, int64_t N, int64_t K);
+q8_status q8_tile_pack_weight(const int8_t* weight, int64_t E, int64_t N, int64_t K, void* packed,
+                              size_t packed_bytes, q8_stream_t stream);
+size_t q8_linear_experts_workspace_bytes(int64_t R, int64_t K, int64_t E);
+q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k, int64_t K,
+                            double input_scale, int32_t input_zero_point,
+                            const void* packed_weight, int64_t E, int64_t N,
+                            const float* weight_scales, const float* bias, const int32_t* order,
+                            const int32_t* offsets, double output_scale,
+                            int32_t output_zero_point, const char* activation, q8_dtype out_dtype,
+                            void* out, void* workspace, size_t workspace_bytes,
+                            q8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,6 +44,8 @@ EXPORTS = (
     "q8_conv2d_packed_acc32",
     "q8_expert_sort", "q8_expert_gather", "q8_expert_dispatch", "q8_expert_gather_backward",
     "q8_expert_combine", "q8_expert_combine_backward",
+    "q8_tile_packed_weight_bytes", "q8_tile_pack_weight", "q8_linear_experts_workspace_bytes",
+    "q8_linear_experts",
 )
 
 
@@ -135,6 +137,11 @@ def _load() -> ctypes.CDLL:
         "q8_expert_combine": (ctypes.c_int, [P, I32, P, I64, I64, I64, P, P, P]),
         "q8_expert_combine_backward": (ctypes.c_int, [P, P, I32, P, I64, I64, I64, I64, P, P, P, P,
                                                       P]),
+        "q8_tile_packed_weight_bytes": (S, [I64, I64, I64]),
+        "q8_tile_pack_weight": (ctypes.c_int, [P, I64, I64, I64, P, S, P]),
+        "q8_linear_experts_workspace_bytes": (S, [I64, I64, I64]),
+        "q8_linear_experts": (ctypes.c_int, [P, I32, I64, I64, I64, D, I32, P, I64, I64, P, P, P,
+                                             P, D, I32, C, I32, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -833,5 +840,6 @@ def conv2d_packed_acc32(x, input_zero_point, packed: PackedConvWeight, output_si
 # ---------------------------------------------------------------------------
 # rows of one batch that go through different weights
 # ---------------------------------------------------------------------------
-from .rows import (ExpertRoute, expert_combine, expert_combine_backward, expert_dispatch,  # noqa: E402
-                   expert_gather, expert_gather_backward, expert_sort)
+from .rows import (ExpertRoute, PackedTileWeight, expert_combine,  # noqa: E402
+                   expert_combine_backward, expert_dispatch, expert_gather,
+                   expert_gather_backward, expert_sort, linear_experts, pack_tile_weight)

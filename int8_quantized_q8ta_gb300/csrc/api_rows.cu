@@ -27,6 +27,44 @@ bool aligned(const void* p, int64_t bytes) {
   return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
 }
 
+// ---- grouped int8 contraction ----------------------------------------------
+size_t tile_weight_bytes(int64_t E, int64_t N, int64_t K) {
+  return static_cast<size_t>(E) * ((N + 127) / 128) * ((K + 63) / 64) * 8192;
+}
+
+bool tile_sizes_ok(int64_t E, int64_t N, int64_t K) {
+  return E >= 1 && E <= q8::kMaxExperts && N >= 1 && K >= 1 && N <= INT32_MAX / 2 &&
+         K <= INT32_MAX / 2 && mul_ok(N, K) && mul_ok(E, N * K) && E * N * K <= INT64_MAX / 64;
+}
+
+// Tile height, ring layout and grid of a problem of R rows in E groups.
+struct TilePlan {
+  int TN, KD, grid;
+  size_t operand, parts, counts, total;
+};
+
+TilePlan plan_tiles(int64_t R, int64_t K, int64_t E) {
+  TilePlan t{};
+  // tiles hold twice the average group, so that few groups need a second one
+  // (which reads the weights again)
+  const int64_t groups = std::min(E, R), avg = (R + groups - 1) / groups;
+  const int64_t want = E == 1 ? avg : 2 * avg;
+  t.TN = static_cast<int>(std::min<int64_t>(q8::kMaxTileRows, q8::round_up(want, 16)));
+  t.KD = t.TN <= 64 ? 2 : 1;
+  t.grid = q8::device_sm_count();
+  t.operand = q8::align_ws(static_cast<size_t>(R) * q8::round_up(K, q8::kTileK) * 2);
+  t.parts = q8::align_ws(static_cast<size_t>(t.grid) * 3 * t.TN * 512);
+  t.counts = q8::align_ws(static_cast<size_t>(t.grid) * q8::kTileEpiWarps * 4);
+  t.total = t.operand + t.parts + t.counts;
+  return t;
+}
+
+// The k-blocks of all units are numbered in 32 bits.
+bool units_ok(int64_t R, int64_t E, int64_t N, int64_t K, const TilePlan& t) {
+  const int64_t tiles = R / t.TN + std::min(E, R), blocks = (N + 127) / 128, kbs = (K + 63) / 64;
+  return mul_ok(blocks, kbs) && mul_ok(tiles, blocks * kbs) && tiles * blocks * kbs <= INT32_MAX;
+}
+
 // float rows (everything but the gather)
 q8_status check_float(q8_dtype dt) {
   if (!dtype_ok(dt)) return Q8_ERR_ARG;
@@ -124,6 +162,105 @@ q8_status q8_expert_combine_backward(const void* dy, const void* z, q8_dtype dty
   return cuda_status(q8::launch_expert_combine_bwd(dy, z, dtype, weights, T, static_cast<int>(k),
                                                    H, position, offsets, static_cast<int>(E), dz,
                                                    dweights, cs(stream)));
+}
+
+size_t q8_tile_packed_weight_bytes(int64_t E, int64_t N, int64_t K) {
+  return tile_sizes_ok(E, N, K) ? tile_weight_bytes(E, N, K) + q8::kWorkspaceAlign : 0;
+}
+
+q8_status q8_tile_pack_weight(const int8_t* weight, int64_t E, int64_t N, int64_t K, void* packed,
+                              size_t packed_bytes, q8_stream_t stream) {
+  if (!weight || !packed) return Q8_ERR_NULL;
+  if (!tile_sizes_ok(E, N, K)) return Q8_ERR_SHAPE;
+  if (packed_bytes < q8_tile_packed_weight_bytes(E, N, K)) return Q8_ERR_WORKSPACE;
+  if (!aligned(packed, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
+  auto* dst = static_cast<uint8_t*>(packed);
+  cudaError_t e = q8::launch_pack_tile_weight(weight, E, N, K, dst, cs(stream));
+  if (e == cudaSuccess)
+    e = q8::launch_weight_block_bound(weight, E * N, K, 1, K,
+                                      reinterpret_cast<int32_t*>(dst + tile_weight_bytes(E, N, K)),
+                                      cs(stream));
+  // finished before the call returns: later kernels read a packed weight
+  // without waiting for the kernel before them
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cs(stream));
+  return cuda_status(e);
+}
+
+size_t q8_linear_experts_workspace_bytes(int64_t R, int64_t K, int64_t E) {
+  if (R < 1 || R > INT32_MAX || K < 1 || K > INT32_MAX / 2 || E < 1 || E > q8::kMaxExperts)
+    return 0;
+  return plan_tiles(R, K, E).total;
+}
+
+q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k, int64_t K,
+                            double input_scale, int32_t input_zero_point,
+                            const void* packed_weight, int64_t E, int64_t N,
+                            const float* weight_scales, const float* bias, const int32_t* order,
+                            const int32_t* offsets, double output_scale,
+                            int32_t output_zero_point, const char* activation, q8_dtype out_dtype,
+                            void* out, void* workspace, size_t workspace_bytes,
+                            q8_stream_t stream) {
+  if (!activation) return Q8_ERR_NULL;
+  if (!dtype_ok(out_dtype)) return Q8_ERR_ARG;
+  q8_status st = check_route(T, k, 1, E);
+  if (st != Q8_OK) return st;
+  if (!tile_sizes_ok(E, N, K)) return Q8_ERR_SHAPE;
+  const int64_t R = T * k;
+  if (!mul_ok(R, q8::round_up(K, 64) * 2) || !mul_ok(R, N * 4)) return Q8_ERR_SHAPE;
+  const int relu = parse_activation(activation);
+  if (relu < 0) return Q8_ERR_UNSUPPORTED;
+  if (!scale_ok(input_scale) || !scale_ok(output_scale) || !zp_ok(input_zero_point) ||
+      !zp_ok(output_zero_point))
+    return Q8_ERR_ARG;
+  if (R == 0) return Q8_OK;
+  if (!x || !packed_weight || !weight_scales || !order || !offsets || !out) return Q8_ERR_NULL;
+  if (!aligned(packed_weight, q8::kWorkspaceAlign) || !aligned(weight_scales, 4) ||
+      !aligned(bias, 4) || !aligned(order, 4) || !aligned(offsets, 4) ||
+      !aligned(out, q8::dtype_bytes(out_dtype)))
+    return Q8_ERR_ALIGN;
+  const TilePlan plan = plan_tiles(R, K, E);
+  if (!units_ok(R, E, N, K, plan)) return Q8_ERR_SHAPE;
+  if (!workspace || workspace_bytes < plan.total) return Q8_ERR_WORKSPACE;
+  if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
+  auto* ws = static_cast<uint8_t*>(workspace);
+
+  q8::TileParams p{};
+  p.R = static_cast<int>(R);
+  p.N = static_cast<int>(N);
+  p.NB = static_cast<int>((N + 127) / 128);
+  p.KB = static_cast<int>((K + 63) / 64);
+  p.E = static_cast<int>(E);
+  p.offsets = offsets;
+  p.TN = plan.TN;
+  p.KD = plan.KD;
+  p.grid = plan.grid;
+  p.min_run = 4;
+  p.w = static_cast<const uint8_t*>(packed_weight);
+  p.w_bound = reinterpret_cast<const int32_t*>(p.w + tile_weight_bytes(E, N, K));
+  p.a_bound = a_bound_of(input_zero_point);
+  p.ws = weight_scales;
+  p.bias = bias;
+  p.rq = make_rq(input_scale, output_scale, output_zero_point, relu);
+  p.relu = relu;
+  p.out = out;
+  p.parts = reinterpret_cast<int32_t*>(ws + plan.operand);
+  p.counts = reinterpret_cast<int32_t*>(ws + plan.operand + plan.parts);
+
+  q8::OperandJob job{};
+  job.x = x;
+  job.x_rows = x_sorted ? R : T;
+  job.K = K;
+  job.R = p.R;
+  job.k = static_cast<int>(k);
+  job.KB = p.KB;
+  job.zp = input_zero_point;
+  job.order = x_sorted ? nullptr : order;
+  job.dst = reinterpret_cast<uint4*>(ws);
+  job.counts = p.counts;
+  job.count_words = plan.grid * q8::kTileEpiWarps;
+  cudaError_t e = q8::launch_tile_operand(job, cs(stream));
+  if (e == cudaSuccess) e = q8::launch_tile_gemm(p, ws, out_dtype, cs(stream));
+  return cuda_status(e);
 }
 
 }  // extern "C"

@@ -75,4 +75,67 @@ cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt
                                       const int32_t* offsets, int E, void* dz, float* dw,
                                       cudaStream_t s);
 
+// ---- grouped int8 contraction (tile_gemm.cu, tile_prep.cu) -----------------
+constexpr int kMaxTileRows = 192;       // rows of one tile: two accumulators fit TMEM
+constexpr int kTileEpiWarps = 12;
+constexpr int kTileSmem = 225 * 1024;
+constexpr int kMaxRank = 256;
+
+// Rows of each tile of a group of `count` rows cut into `tiles`: equal
+// shares in steps of 16 (at most kMaxTileRows, as tiles >= count / that).
+__host__ __device__ inline int tile_rows(int count, int tiles) {
+  return ((count + tiles - 1) / tiles + 15) & ~15;
+}
+
+struct TileParams {
+  int R, N, NB, KB;         // rows, output channels, blocks of 128 of them, k-blocks of 64
+  int E;                    // groups
+  const int32_t* offsets;   // [E + 1] group bounds on the device, or null: one group of R rows
+  int TN;                   // rows of a tile at most (a multiple of 16)
+  int KD;                   // k-blocks per ring stage: 1 or 2
+  int stages;               // ring stages (set by the launcher)
+  int grid, min_run;        // CTAs; k-blocks a CTA's run holds at least
+  const uint8_t* w;         // packed weights (see launch_pack_tile_weight)
+  const int32_t* w_bound;   // largest sum of |w| over 64 inputs
+  int a_bound;              // largest |x - zp|
+  const float* ws;          // [E, N]
+  const float* bias;        // [E, N] or null
+  Requant rq;
+  int relu;
+  void* out;
+  const int32_t* out_rows;  // output row of each row, or null
+  uint32_t* err;
+  int32_t* parts;           // [grid][3][TN][128]: parts of units cut by a run's end
+  int32_t* counts;          // [grid][kTileEpiWarps], zeroed by the kernel before
+  // adapters (L == 0: none)
+  int L, rank16, lora_f16;  // adapters, blocks of 16 ranks, f16 (1) or bf16 (0)
+  const uint8_t* lora_b;    // packed B (see launch_pack_lora)
+  const float* h;           // [R][rank16 * 16]: s_in * scaling * (x - zp) A^T
+  const int32_t* ids;       // [R] adapter of each row
+  const int32_t* lists;     // per row tile: adapter count, then the adapters
+  int list_stride;
+};
+cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
+                             cudaStream_t s);
+
+// Weights [E][N][K] -> [E][NB][KB][4][128][16] bytes: for each block of 128
+// output channels and 64 inputs, 16-input chunks of all 128 rows; top bits
+// flipped, zeros beyond N and K.
+cudaError_t launch_pack_tile_weight(const int8_t* w, int64_t E, int64_t N, int64_t K, uint8_t* dst,
+                                    cudaStream_t s);
+
+// Token operand: dst[kb][s][64] = f16(x[row(s)][64 kb ..] - zp), zeros beyond
+// K; row(s) = order[s] / k, or s when order is null; rows whose order is out
+// of range are left alone.  Also zeroes `counts` (count_words of them).
+struct OperandJob {
+  const int8_t* x;
+  int64_t x_rows, K;
+  int R, k, KB, zp;
+  const int32_t* order;
+  uint4* dst;
+  int32_t* counts;
+  int count_words;
+};
+cudaError_t launch_tile_operand(const OperandJob& job, cudaStream_t s);
+
 }  // namespace q8

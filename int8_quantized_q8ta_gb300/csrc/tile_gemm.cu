@@ -1,0 +1,689 @@
+// tile_gemm.cu -- the grouped int8 contraction on tcgen05 (sm_103a): rows of
+// one batch, sorted into groups, each group times its own int8 weight; and
+// the shared projection with low-rank adapters, which is one group whose
+// tiles get an extra term.
+//
+//   acc[s, n] = sum_k (x[s, k] - zp) * w[e(s)][n, k]      exact in int32
+//   v = ((float)acc * s_in) * ws[e, n] + b[e, n]  (+ delta[s, n])
+//   delta[s, n] = sum_j h[s, j] * B[a(s)][n, j]
+// then the activation and either the requantization to int8 or one rounding
+// to the float output type.
+//
+// Weights stay int8 in memory (1 byte read per weight, half of the bf16 copy
+// the plain linear keeps): a tile of 128 output channels x 64 inputs is one
+// contiguous 8 KB run, copied to shared memory in bulk, turned into f16 by
+// four warps (a byte permute and half a packed subtraction per value) and put
+// into TENSOR MEMORY as the MMA's A operand.  Tokens are the B operand, f16
+// copies of x - zp in K-blocked rows that TMA fetches 128-byte swizzled.  So
+// weights are on the MMA's M side (always 128 lanes, however few tokens a
+// group has) and tokens on N, 16 to 192 of them in steps of 16; the shared
+// memory traffic of a k-block is the tokens' tile and 2 bytes per weight.
+//
+// Exactness: |x - zp| <= a and sum |w| over 64 inputs <= W give f32 sums that
+// are exact integers for 2^24 / (a W) k-blocks; such a chunk is then drained
+// from TMEM into int32 registers while the other accumulator fills.
+//
+// Work split: all (tile, output block) units times their k-blocks form one
+// line, cut into equal runs, one per CTA, so that a few wide units and many
+// small ones fill the SMs alike.  A unit cut by a run's end is summed by
+// whichever of its CTAs comes last, warp by warp, from the int32 parts the
+// others left in the workspace: integer sums, the same in any order.  No CTA
+// waits for another.
+//
+// Adapters: after a unit's k-blocks, its last run multiplies B[a] by the rows'
+// h for each adapter the tile holds, into an accumulator of its own: tf32
+// MMAs, B exact (f16 and bf16 both fit tf32), h as the sum of two tf32 terms
+// (22 significant bits), rows of other adapters as zeros.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "rows_internal.h"
+#include "tile_device.cuh"
+
+namespace q8 {
+
+namespace {
+
+enum : uint32_t { kErrTileRing = 0x10A, kErrTileAcc = 0x10B, kErrTileOperand = 0x10C };
+
+constexpr int kMaxRing = 12;
+constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
+constexpr int kConvWarps = 4;
+constexpr int kFirstConv = 4;           // warps 0 and 1: copies, MMAs; 2 and 3 idle
+constexpr int kFirstEpi = kFirstConv + kConvWarps;
+constexpr int kEpiWarps = kTileEpiWarps;
+constexpr int kTileThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kMaxCols = 64;            // accumulator columns of one epilogue warp
+// TMEM: two accumulators of 192 columns, then 128 columns of A operands
+constexpr int kAccCols = kMaxTileRows;
+constexpr int kTmemCols = 512;
+static_assert(kMaxCols * kEpiWarps / 4 == kMaxTileRows, "a third of a tile per epilogue warp");
+
+struct TileShared {
+  uint64_t full[kMaxRing];
+  uint64_t empty[kMaxRing];
+  uint64_t ready[4];      // A operand in TMEM (and, for adapters, B in shared memory)
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  uint32_t abort;
+  int32_t tiles;          // row tiles of all groups
+};
+
+// Ring stages per exact f32 chunk.
+__device__ __forceinline__ int chunk_stages_of(const TileParams& p) {
+  int wb = __ldg(p.w_bound);
+  if (wb < 1 || wb > kWorstWBound) wb = wb < 1 ? 1 : kWorstWBound;
+  return max(1, (1 << 24) / (p.a_bound * wb) / p.KD);
+}
+
+// One run's part of a unit.
+struct Seg {
+  int e, row0, rows, nb, tile;   // group, first row, rows, output block, index of the row tile
+  int kb0, kb1;
+  int unit;
+};
+
+// Rows of group e.  Offsets come from device memory: whatever they hold, no
+// row outside [0, R) is touched.
+__device__ __forceinline__ int group_end(const TileParams& p, int e) {
+  return min(p.R, max(0, __ldg(p.offsets + e)));
+}
+__device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start) {
+  start = group_end(p, e);
+  return max(0, group_end(p, e + 1) - start);
+}
+
+// The CTA's run of the line of all units' k-blocks (32-bit: the host checks).
+struct Walk {
+  const TileParams& p;
+  const int32_t* prefix;   // row tiles before each group (shared memory), or null: one group
+  int pos, end, q;         // q: k-blocks of every run but the last
+  __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix_, int tiles)
+      : p(p_), prefix(prefix_) {
+    const int total = tiles * p.NB * p.KB;
+    q = max(p.min_run, (total - 1) / static_cast<int>(gridDim.x) + 1);
+    pos = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * blockIdx.x));
+    end = min(total - pos, q) + pos;
+  }
+  __device__ bool next(Seg& s) {
+    if (pos >= end) return false;
+    s.unit = pos / p.KB;
+    s.kb0 = pos - s.unit * p.KB;
+    s.kb1 = min(p.KB, s.kb0 + (end - pos));
+    pos += s.kb1 - s.kb0;
+    int t0 = 0, tiles, start = 0, count = p.R;
+    s.e = 0;
+    if (prefix != nullptr) {
+      // the group whose units hold this one
+      int lo = 0, hi = p.E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] * p.NB <= s.unit) lo = mid; else hi = mid - 1;
+      }
+      s.e = lo;
+      t0 = prefix[lo];
+      count = group_rows(p, lo, start);
+    }
+    tiles = (count + p.TN - 1) / p.TN;
+    const int local = s.unit - t0 * p.NB;
+    const int i = local % tiles;       // the tiles of one output block follow one another
+    s.nb = local / tiles;
+    const int per = tile_rows(count, tiles);
+    s.row0 = start + i * per;
+    s.rows = min(per, count - i * per);
+    s.tile = t0 + i;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int adapters_of(const TileParams& p, const Seg& s) {
+  return (p.L > 0 && s.kb1 == p.KB) ? __ldg(p.lists + static_cast<int64_t>(s.tile) * p.list_stride)
+                                    : 0;
+}
+
+// v of one accumulator, in the order of the header's epilogue.
+__device__ __forceinline__ float dequant(int32_t acc, float ws, float b, float d,
+                                         const Requant& rq) {
+  float t = __fmul_rn(__int2float_rn(acc), rq.s_in);
+  t = __fmul_rn(t, ws);
+  return __fadd_rn(__fadd_rn(t, b), d);
+}
+
+template <int OUT>
+__device__ __forceinline__ void store_out(void* out, int64_t at, float v, const TileParams& p) {
+  if constexpr (OUT == Q8_I8) {
+    const int32_t q = round_clamp_first(__fmul_rn(v, p.rq.inv_out), p.rq.ozp_i, p.rq.lo_f,
+                                        p.rq.hi_f);
+    static_cast<int8_t*>(out)[at] = static_cast<int8_t>(q);
+  } else {
+    if (p.relu && v < 0.0f) v = 0.0f;   // NaN stays
+    if constexpr (OUT == Q8_F32) static_cast<float*>(out)[at] = v;
+    if constexpr (OUT == Q8_F16) static_cast<__half*>(out)[at] = __float2half_rn(v);
+    if constexpr (OUT == Q8_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const TileParams p) {
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ TileShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring0 = (smem_u32(dyn) + 1023u) & ~1023u;
+  const int KD = p.KD, S = p.stages, NA = 4 / KD;
+  const uint32_t tok_bytes = static_cast<uint32_t>(p.TN) * 128u;
+  const uint32_t stage_bytes = static_cast<uint32_t>(KD) * (tok_bytes + kTileWBytes);
+  int32_t* prefix = p.offsets != nullptr
+                        ? reinterpret_cast<int32_t*>(dyn + (ring0 - smem_u32(dyn)) +
+                                                     static_cast<size_t>(S) * stage_bytes)
+                        : nullptr;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.ready[i]), kConvWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.acc_full[i]), 1);
+      mbar_init(smem_u32(&sh.acc_empty[i]), kEpiWarps);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    fence_mbar_init();
+    sh.abort = 0;
+    tma_prefetch_desc(&map_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  if (prefix != nullptr) {
+    // row tiles before each group, by one warp
+    pdl_wait();
+    if (warp == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        int n = 0, start;
+        if (e < p.E) n = (group_rows(p, e, start) + p.TN - 1) / p.TN;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        if (e < p.E) prefix[e] = before + incl - n;
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) sh.tiles = before;
+    }
+  } else if (threadIdx.x == 0) {
+    sh.tiles = (p.R + p.TN - 1) / p.TN;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t a_base = tmem + 2 * kAccCols;
+  volatile uint32_t* abort_flag = &sh.abort;
+  const int tiles = sh.tiles;
+
+  if (warp == 0) {
+    // ---- copies: one thread ------------------------------------------------
+    if (lane == 0) {
+      Walk walk(p, prefix, tiles);
+      Seg sg;
+      const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
+      int it = 0;
+      bool ok = true;
+      // the first ring of weights of a single group does not depend on the
+      // kernel before this one: a packed weight is written at load time
+      int early = 0;
+      if (prefix == nullptr) {
+        Walk w2 = walk;
+        Seg s2;
+        while (early < S && w2.next(s2)) {
+          for (int kb = s2.kb0; kb < s2.kb1 && early < S; kb += KD, ++early) {
+            const int nk = min(KD, s2.kb1 - kb);
+            const uint32_t st = ring0 + early * stage_bytes, bar = smem_u32(&sh.full[early]);
+            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
+            bulk_load(st + KD * tok_bytes,
+                      p.w + static_cast<int64_t>(s2.nb) * w_rows +
+                          static_cast<int64_t>(kb) * kTileWBytes,
+                      nk * kTileWBytes, bar);
+          }
+          if (p.L > 0) break;   // adapter stages follow: their list is not known yet
+        }
+        pdl_wait();
+      }
+      while (ok && walk.next(sg)) {
+        const uint8_t* w = p.w + (static_cast<int64_t>(sg.e) * p.NB + sg.nb) * w_rows;
+        for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it) {
+          const int slot = it % S;
+          const int nk = min(KD, sg.kb1 - kb);
+          const uint32_t st = ring0 + slot * stage_bytes, bar = smem_u32(&sh.full[slot]);
+          if (it >= early) {
+            ok = tile_wait(smem_u32(&sh.empty[slot]), ((it / S) & 1) ^ 1, abort_flag, kErrTileRing,
+                           p.err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
+            bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
+                      nk * kTileWBytes, bar);
+          }
+          tma_load_3d(st, &map_x, bar, 0, sg.row0, kb);
+        }
+        if (!ok) break;
+        const int na = adapters_of(p, sg);
+        const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
+        for (int i = 0; i < na && ok; ++i) {
+          const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(__ldg(list + i)) * p.NB + sg.nb) *
+                                          p.rank16) * 4096;
+          for (int c = 0; c < p.rank16; ++c, ++it) {
+            const int slot = it % S;
+            ok = tile_wait(smem_u32(&sh.empty[slot]), ((it / S) & 1) ^ 1, abort_flag, kErrTileRing,
+                           p.err);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&sh.full[slot]);
+            mbar_arrive_expect_tx(bar, 4096);
+            bulk_load(ring0 + slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
+          }
+        }
+      }
+      if (!ok || *abort_flag) {
+        // copies issued but not waited for by anyone still land in this CTA
+        for (int i = max(0, it - S); i < it; ++i)
+          tile_wait_final(smem_u32(&sh.full[i % S]), (i / S) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMAs: one thread --------------------------------------------------
+    pdl_wait();
+    if (lane == 0) {
+      Walk walk(p, prefix, tiles);
+      Seg sg;
+      int it = 0, ac = 0;
+      bool ok = true;
+      const int chunk = chunk_stages_of(p);
+      while (ok && walk.next(sg)) {
+        const uint32_t n16 = (sg.rows + 15) & ~15;
+        const uint32_t idesc = idesc_f16(n16);
+        const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
+        int kb = sg.kb0;
+        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
+          const int buf = ac & 1;
+          ok = tile_wait(smem_u32(&sh.acc_empty[buf]), ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc,
+                         p.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kAccCols;
+          uint32_t accumulate = 0;
+          const int c1 = min(stages, c0 + chunk);
+          for (int s = c0; s < c1; ++s, ++it, kb += KD) {
+            const int slot = it % S, as = it % NA;
+            ok = tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
+                           p.err) &&
+                 tile_wait(smem_u32(&sh.ready[as]), (it / NA) & 1, abort_flag, kErrTileOperand,
+                           p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const int nk = min(KD, sg.kb1 - kb);
+            for (int k = 0; k < nk; ++k) {
+              const uint64_t b = sw128_kmajor_desc(ring0 + slot * stage_bytes + k * tok_bytes);
+              const uint32_t a = a_base + (as * KD + k) * 32;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                umma_f16_ta(d, a + j * 8, b + j * 2, idesc, accumulate);
+                accumulate = 1;
+              }
+            }
+            umma_commit(smem_u32(&sh.empty[slot]));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&sh.acc_full[buf]));
+        }
+        const int na = ok ? adapters_of(p, sg) : 0;
+        if (na > 0) {
+          const int buf = ac & 1;
+          ok = tile_wait(smem_u32(&sh.acc_empty[buf]), ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc,
+                         p.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kAccCols;
+          const uint32_t id32 = idesc_tf32(n16);
+          uint32_t accumulate = 0;
+          for (int i = 0; i < na * p.rank16; ++i, ++it) {
+            const int slot = it % S, as = it % NA;
+            ok = tile_wait(smem_u32(&sh.ready[as]), (it / NA) & 1, abort_flag, kErrTileOperand,
+                           p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = sw128_kmajor_desc(ring0 + slot * stage_bytes);
+            const uint32_t a = a_base + as * KD * 32;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // h's leading terms, then its trailing ones
+              umma_tf32_ta(d, a + (j & 1) * 8, b + j * 2, id32, accumulate);
+              accumulate = 1;
+            }
+            umma_commit(smem_u32(&sh.empty[slot]));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&sh.acc_full[buf]));
+          ++ac;
+        }
+      }
+      if (!ok || *abort_flag) {
+        umma_commit(smem_u32(&sh.drain));
+        tile_wait_final(smem_u32(&sh.drain), 0);
+      }
+    }
+  } else if (warp >= kFirstConv && warp < kFirstEpi) {
+    // ---- A operand: shared memory -> f16 -> TMEM ---------------------------
+    pdl_wait();
+    Walk walk(p, prefix, tiles);
+    Seg sg;
+    const int row = (warp & 3) * 32 + lane;           // a warp reaches the lanes of its quarter
+    const uint32_t a_lane = a_base + (static_cast<uint32_t>(warp & 3) << 21);
+    const int t0 = (warp - kFirstConv) * 32 + lane;   // this thread among the 128
+    const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    int it = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it) {
+        const int slot = it % S, as = it % NA;
+        ok = it < NA || tile_wait(smem_u32(&sh.empty[(it - NA) % S]), ((it - NA) / S) & 1,
+                                  abort_flag, kErrTileOperand, p.err);
+        ok = ok && tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
+                             p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int nk = min(KD, sg.kb1 - kb);
+        for (int k = 0; k < nk; ++k) {
+          const uint32_t w = ring0 + slot * stage_bytes + KD * tok_bytes + k * kTileWBytes +
+                             row * 16;
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = lds128(w + c * 2048);
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
+              r[c * 8 + j * 2 + 1] = biased_to_f16x2(q[j], 0x4342, minus);
+            }
+          }
+          tmem_st_32cols(a_lane + (as * KD + k) * 32, r);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ready[as]));
+      }
+      if (!ok) break;
+      const int na = adapters_of(p, sg);
+      const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
+      const int n16 = (sg.rows + 15) & ~15;
+      for (int i = 0; i < na && ok; ++i) {
+        const int a_id = __ldg(list + i);
+        for (int c = 0; c < p.rank16; ++c, ++it) {
+          const int slot = it % S, as = it % NA;
+          ok = it < NA || tile_wait(smem_u32(&sh.empty[(it - NA) % S]), ((it - NA) / S) & 1,
+                                    abort_flag, kErrTileOperand, p.err);
+          ok = ok && tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
+                               p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = ring0 + slot * stage_bytes;
+          uint32_t r[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint4 v = lds128(st + KD * tok_bytes + g * 2048 + row * 16);
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (p.lora_f16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+                r[g * 8 + j * 2] = __float_as_uint(f.x);
+                r[g * 8 + j * 2 + 1] = __float_as_uint(f.y);
+              } else {
+                r[g * 8 + j * 2] = q[j] << 16;
+                r[g * 8 + j * 2 + 1] = q[j] & 0xffff0000u;
+              }
+            }
+          }
+          tmem_st_16cols(a_lane + as * KD * 32, r);
+          // B: row t = h's 16 leading tf32 terms, then its 16 trailing ones,
+          // in the 128-byte swizzle; zeros where the row has another adapter
+          for (int t = t0; t < n16; t += 128) {
+            const bool mine = t < sg.rows && __ldg(p.ids + sg.row0 + t) == a_id;
+            const float4* h = reinterpret_cast<const float4*>(
+                p.h + static_cast<int64_t>(sg.row0 + t) * p.rank16 * 16 + c * 16);
+            const uint32_t at = st + t * 128;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float4 v = mine ? __ldg(h + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float f[4] = {v.x, v.y, v.z, v.w};
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                hi[j] = __float_as_uint(f[j]) & 0xffffe000u;
+                lo[j] = __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
+              }
+              sts128(at + ((g ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+              sts128(at + (((g + 4) ^ (t & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.ready[as]));
+        }
+      }
+    }
+  } else if (warp >= kFirstEpi) {
+    // ---- epilogue ------------------------------------------------------------
+    pdl_wait();
+    Walk walk(p, prefix, tiles);
+    Seg sg;
+    const int ew = warp - kFirstEpi;
+    const int quarter = warp & 3;
+    // columns of this warp: a third of the tile's
+    const int cols = ((p.TN + 47) / 48) * 16;
+    const int col0 = (ew / 4) * cols;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter) << 21) + col0;
+    const int chunk = chunk_stages_of(p);
+    int ac = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int mine = max(0, min(cols, sg.rows - col0));    // columns with a row behind them
+      const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
+      int32_t acc[kMaxCols];
+#pragma unroll
+      for (int j = 0; j < kMaxCols; ++j) acc[j] = 0;
+      for (int c0 = 0; c0 < stages; c0 += chunk, ++ac) {
+        const int buf = ac & 1;
+        ok = __all_sync(0xffffffffu,
+                        tile_wait(smem_u32(&sh.acc_full[buf]), (ac >> 1) & 1, abort_flag,
+                                  kErrTileAcc, p.err));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < kMaxCols / 16; ++b)
+          if (b * 16 < mine) {
+            uint32_t r[16];
+            tmem_ld_16cols(lane_addr + buf * kAccCols + b * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[b * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+      }
+      if (!ok) break;
+      // the adapters' term stays in TMEM until it is used
+      const bool has_d = adapters_of(p, sg) > 0;
+      const int dbuf = ac & 1;
+      if (has_d) {
+        ok = __all_sync(0xffffffffu,
+                        tile_wait(smem_u32(&sh.acc_full[dbuf]), (ac >> 1) & 1, abort_flag,
+                                  kErrTileAcc, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        ++ac;
+      }
+      bool last = true;
+      int first_cta = 0, end_cta = 0;
+      if (sg.kb0 != 0 || sg.kb1 != p.KB) {
+        // this run holds part of the unit: leave it, and go on only as the last
+        first_cta = sg.unit * p.KB / walk.q;
+        end_cta = ((sg.unit + 1) * p.KB - 1) / walk.q;
+        const int side = static_cast<int>(blockIdx.x) == first_cta ? 1 : 0;
+        int32_t* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 3 + side) * p.TN * 128 +
+                        quarter * 32 + lane;
+        float* dpart = reinterpret_cast<float*>(p.parts) +
+                       (static_cast<int64_t>(blockIdx.x) * 3 + 2) * p.TN * 128 + quarter * 32 + lane;
+#pragma unroll
+        for (int b = 0; b < kMaxCols / 16; ++b)
+          if (b * 16 < mine) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) part[(col0 + b * 16 + j) * 128] = acc[b * 16 + j];
+            if (has_d) {
+              uint32_t r[16];
+              tmem_ld_16cols(lane_addr + dbuf * kAccCols + b * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                dpart[(col0 + b * 16 + j) * 128] = __uint_as_float(r[j]);
+            }
+          }
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(p.counts + first_cta * kEpiWarps + ew, 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        __threadfence();
+        last = before == end_cta - first_cta;
+      }
+      if (last) {
+        const int n = sg.nb * 128 + quarter * 32 + lane;
+        const bool in = n < p.N;
+        const int64_t en = static_cast<int64_t>(sg.e) * p.N + n;
+        const float ws = in ? __ldg(p.ws + en) : 0.0f;
+        const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
+        const bool parted = sg.kb0 != 0 || sg.kb1 != p.KB;
+        // the unit's adapter term: in this CTA's TMEM, or left by the CTA
+        // that ran the unit's end
+        const bool unit_d =
+            p.L > 0 && __ldg(p.lists + static_cast<int64_t>(sg.tile) * p.list_stride) > 0;
+        const float* dother = reinterpret_cast<const float*>(p.parts) +
+                              (static_cast<int64_t>(end_cta) * 3 + 2) * p.TN * 128 + quarter * 32 + lane;
+#pragma unroll
+        for (int b = 0; b < kMaxCols / 16; ++b)
+          if (b * 16 < mine) {
+            if (parted)
+              for (int c = first_cta; c <= end_cta; ++c) {
+                if (c == static_cast<int>(blockIdx.x)) continue;
+                const int32_t* part = p.parts +
+                                      (static_cast<int64_t>(c) * 3 + (c == first_cta ? 1 : 0)) * p.TN *
+                                          128 +
+                                      quarter * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  acc[b * 16 + j] += __ldcg(part + (col0 + b * 16 + j) * 128);
+              }
+            float d[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) d[j] = 0.0f;
+            if (has_d) {
+              uint32_t r[16];
+              tmem_ld_16cols(lane_addr + dbuf * kAccCols + b * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) d[j] = __uint_as_float(r[j]);
+            } else if (unit_d) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) d[j] = __ldcg(dother + (col0 + b * 16 + j) * 128);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (b * 16 + j < mine && in) {
+                const int s = sg.row0 + col0 + b * 16 + j;
+                const int64_t to = p.out_rows != nullptr ? __ldg(p.out_rows + s) : s;
+                store_out<OUT>(p.out, to * p.N + n, dequant(acc[b * 16 + j], ws, bias, d[j], p.rq),
+                               p);
+              }
+          }
+      }
+      if (has_d) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[dbuf]));
+      }
+    }
+    // rows of dropped slots hold zeros
+    if (prefix != nullptr) {
+      const int64_t step = static_cast<int64_t>(gridDim.x) * kEpiWarps * 32;
+      const int64_t total = static_cast<int64_t>(p.R) * p.N;
+      for (int64_t i = group_end(p, p.E) * static_cast<int64_t>(p.N) +
+                       static_cast<int64_t>(blockIdx.x) * kEpiWarps * 32 + ew * 32 + lane;
+           i < total; i += step) {
+        if constexpr (OUT == Q8_I8) static_cast<int8_t*>(p.out)[i] = static_cast<int8_t>(p.rq.ozp_i);
+        else if constexpr (OUT == Q8_F32) static_cast<float*>(p.out)[i] = 0.0f;
+        else static_cast<uint16_t*>(p.out)[i] = 0;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int OUT>
+cudaError_t launch_one(const CUtensorMap& map, const TileParams& p, int grid, size_t smem,
+                       cudaStream_t s) {
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(tile_gemm_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kTileSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tile_gemm_kernel<OUT>, grid, kTileThreads, smem, s, map, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
+                             cudaStream_t s) {
+  CUtensorMap map;
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(p.R), static_cast<uint64_t>(p.KB)};
+  const uint64_t str[2] = {128, static_cast<uint64_t>(p.R) * 128};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(p.TN), static_cast<uint32_t>(p.KD)};
+  // (16-bit elements; the map's element type only matters for reductions)
+  if (!encode_bf16_tmap(&map, operand, 3, dims, str, box)) return cudaErrorInvalidValue;
+  p.err = device_error_word();
+  if (p.err == nullptr) return cudaErrorUnknown;
+  const size_t stage = static_cast<size_t>(p.KD) * (static_cast<size_t>(p.TN) * 128 + kTileWBytes);
+  const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
+  p.stages = static_cast<int>(std::min<size_t>(kMaxRing, (kTileSmem - 1024 - table) / stage));
+  const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
+  switch (out_dtype) {
+    case Q8_I8: return launch_one<Q8_I8>(map, p, p.grid, smem, s);
+    case Q8_F32: return launch_one<Q8_F32>(map, p, p.grid, smem, s);
+    case Q8_F16: return launch_one<Q8_F16>(map, p, p.grid, smem, s);
+    default: return launch_one<Q8_BF16>(map, p, p.grid, smem, s);
+  }
+}
+
+}  // namespace q8

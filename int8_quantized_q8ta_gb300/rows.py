@@ -11,7 +11,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _lib, _need, _ptr, _stream
+from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _ptr, _stream, _workspace
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
 
@@ -182,3 +182,62 @@ def expert_combine_backward(dy: torch.Tensor, z: torch.Tensor, weights: torch.Te
                                            _ptr(dz), _ptr(dw), _stream(z)),
            "q8_expert_combine_backward")
     return dz, dw
+
+
+# ---------------------------------------------------------------------------
+# the experts' int8 products
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class PackedTileWeight:
+    """int8 weights [E, N, K] in 8 KB tiles (see q8_tile_pack_weight):
+    ``data`` is a uint8 CUDA buffer."""
+    data: torch.Tensor
+    E: int
+    N: int
+    K: int
+
+
+def pack_tile_weight(weight: torch.Tensor) -> PackedTileWeight:
+    """Pack int8 [E, N, K], or one weight [N, K], once."""
+    _need(weight, torch.int8, "weight")
+    if weight.dim() not in (2, 3):
+        raise ValueError(f"weight must be [E, N, K] or [N, K], got {tuple(weight.shape)}")
+    E, N, K = weight.shape if weight.dim() == 3 else (1, *weight.shape)
+    nbytes = _lib.q8_tile_packed_weight_bytes(E, N, K)
+    if nbytes == 0:
+        raise Q8Error(Q8_ERR_SHAPE, "q8_tile_packed_weight_bytes")
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=weight.device)
+    _check(_lib.q8_tile_pack_weight(_ptr(weight), E, N, K, _ptr(buf), nbytes, _stream(weight)),
+           "q8_tile_pack_weight")
+    return PackedTileWeight(buf, E, N, K)
+
+
+def linear_experts(x, input_scale, input_zero_point, packed: PackedTileWeight, weight_scales, bias,
+                   route: ExpertRoute, output_scale, output_zero_point, activation="none",
+                   x_sorted=False, out_dtype=torch.int8, out=None, workspace=None):
+    """Sorted rows times the int8 weight of their expert (see
+    q8_linear_experts): int8 x [T, K], or [T*k, K] in sorted order with
+    ``x_sorted``; weight_scales and bias float32 [E, N]; out [T*k, N]."""
+    _need(x, torch.int8, "x")
+    _need_route(route)
+    T, k, E, N = route.T, route.k, packed.E, packed.N
+    if route.E != E:
+        raise ValueError(f"the route has {route.E} experts, the packed weight {E}")
+    _shape(x, (T * k if x_sorted else T, packed.K), "x")
+    _need(weight_scales, torch.float32, "weight_scales")
+    _shape(weight_scales, (E, N), "weight_scales")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _shape(bias, (E, N), "bias")
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype must be float32, float16, bfloat16 or int8, got {out_dtype}")
+    out = _out(out, (T * k, N), out_dtype, x.device)
+    nbytes = _lib.q8_linear_experts_workspace_bytes(T * k, packed.K, E)
+    ws = _workspace(nbytes, x.device, workspace)
+    _check(_lib.q8_linear_experts(
+        _ptr(x), int(x_sorted), T, k, packed.K, float(input_scale), int(input_zero_point),
+        _ptr(packed.data), E, N, _ptr(weight_scales), _ptr(bias), _ptr(route.order),
+        _ptr(route.offsets), float(output_scale), int(output_zero_point), activation.encode(),
+        _DTYPE[out_dtype], _ptr(out), _ptr(ws), nbytes, _stream(x)), "q8_linear_experts")
+    return out

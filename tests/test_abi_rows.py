@@ -78,3 +78,48 @@ def test_binding_refuses_cpu_tensors():
         q8.expert_sort(ids, 4)
     with pytest.raises(ValueError, match="CUDA"):
         q8.expert_dispatch(torch.zeros(2, 8), ids, 4)
+
+
+def test_tile_pack_guards():
+    size = lib.q8_tile_packed_weight_bytes
+    assert size(1, 128, 64) == 8192 + 256
+    assert size(3, 129, 65) == 3 * 2 * 2 * 8192 + 256
+    assert size(0, 128, 64) == size(1, 0, 64) == size(1, 128, 0) == size(1025, 1, 1) == 0
+    assert size(1024, 2 ** 30, 2 ** 30) == 0
+    p = lib.q8_tile_pack_weight
+    assert p(None, 1, 128, 64, FAKE, 1 << 20, None) == q8.Q8_ERR_NULL
+    assert p(FAKE, 1, 128, 64, None, 1 << 20, None) == q8.Q8_ERR_NULL
+    assert p(FAKE, 0, 128, 64, FAKE, 1 << 20, None) == q8.Q8_ERR_SHAPE
+    assert p(FAKE, 1, 128, 64, FAKE, 8192, None) == q8.Q8_ERR_WORKSPACE
+    assert p(FAKE, 1, 128, 64, ctypes.c_void_p(0x10010), 1 << 20, None) == q8.Q8_ERR_ALIGN
+
+
+def test_linear_experts_guards():
+    f = lib.q8_linear_experts
+    need = lib.q8_linear_experts_workspace_bytes(8, 64, 4)
+    assert need > 0 and need % 256 == 0
+    assert lib.q8_linear_experts_workspace_bytes(0, 64, 4) == 0
+    names = ["x", "sorted", "T", "k", "K", "s_in", "zp", "w", "E", "N", "ws", "b", "order",
+             "offsets", "s_out", "ozp", "act", "dt", "out", "space", "bytes", "stream"]
+    ok = dict(zip(names, [FAKE, 0, 4, 2, 64, 0.02, 0, FAKE, 4, 32, FAKE, None, FAKE, FAKE, 0.1, 0,
+                          b"none", I8, FAKE, FAKE, need, None]))
+
+    def call(**kw):
+        return f(*dict(ok, **kw).values())
+    for n in ("x", "w", "ws", "order", "offsets", "out", "act"):
+        assert call(**{n: None}) == q8.Q8_ERR_NULL, n
+    for n in ("T", "k", "K", "E", "N"):
+        assert call(**{n: -1}) == q8.Q8_ERR_SHAPE, n
+    assert call(E=1025) == q8.Q8_ERR_SHAPE
+    assert call(act=b"gelu") == q8.Q8_ERR_UNSUPPORTED
+    assert call(dt=4) == q8.Q8_ERR_ARG
+    assert call(s_in=0.0) == call(s_out=float("nan")) == q8.Q8_ERR_ARG
+    assert call(zp=128) == call(ozp=-129) == q8.Q8_ERR_ARG
+    assert call(bytes=need - 1) == call(space=None) == q8.Q8_ERR_WORKSPACE
+    for n in ("w", "space"):
+        assert call(**{n: ctypes.c_void_p(0x10010)}) == q8.Q8_ERR_ALIGN, n
+    assert call(ws=ODD) == call(order=ODD) == q8.Q8_ERR_ALIGN
+    assert call(out=ctypes.c_void_p(0x10001), dt=BF16) == q8.Q8_ERR_ALIGN
+    assert call(T=0, x=None, out=None) == q8.Q8_OK
+    # the k-blocks of all units have to fit 32 bits
+    assert call(T=2 ** 22, k=8, N=2 ** 16, K=2 ** 16, bytes=2 ** 62) == q8.Q8_ERR_SHAPE
