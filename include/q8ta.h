@@ -563,6 +563,42 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
                             void* out, void* workspace, size_t workspace_bytes,
                             q8_stream_t stream);
 
+/*
+ * Low-rank adapters of many requests beside one shared int8 projection: row m
+ * uses adapter a = adapter_ids[m], or none when a lies outside [0, L),
+ *   v = ((float)acc * input_scale) * weight_scales[n] + bias[n]
+ *     + sum_j h[m,j] * B[a][n,j],
+ *   h[m,j] = input_scale * scaling[a] * sum_k (x[m,k] - input_zero_point) * A[a][j,k],
+ * acc exact as in q8_linear, then the activation and the output as in
+ * q8_linear_experts.  Rows without an adapter give exactly q8_linear's v.
+ *   A float16 or bfloat16 [L, r, K]; B the same type [L, N, r]; scaling
+ *   float [L].  q8_lora_pack lays them out once, at load time, and waits (an
+ *   adapter is exchanged by packing again).
+ * The adapter sums are f32; h enters the second product as two tf32 terms (22
+ * significant bits), A, B and x - input_zero_point exactly.  Results do not
+ * depend on timing.  Infinities and NaN stay with the rows of their adapter:
+ * one in A gives what the formula gives, one in B makes every channel of its
+ * adapter's rows NaN.
+ *   weight       packed by q8_tile_pack_weight with E = 1
+ *   out          [M, N] of out_dtype
+ * Guards: M >= 0 (0: nothing to do), N, K >= 1, 1 <= L <= 1024, 1 <= r <= 256,
+ * adapters Q8_F16 or Q8_BF16 (else Q8_ERR_UNSUPPORTED), the scale and
+ * zero-point ranges; workspace of q8_linear_lora_workspace_bytes(M, K, L, r)
+ * bytes, packed weight and packed adapters 256-byte aligned.
+ */
+size_t q8_lora_packed_bytes(int64_t L, int64_t N, int64_t K, int64_t r);
+q8_status q8_lora_pack(const void* A, const void* B, const float* scaling, q8_dtype dtype,
+                       int64_t L, int64_t r, int64_t N, int64_t K, void* packed,
+                       size_t packed_bytes, q8_stream_t stream);
+size_t q8_linear_lora_workspace_bytes(int64_t M, int64_t K, int64_t L, int64_t r);
+q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
+                         int32_t input_zero_point, const void* packed_weight, int64_t N,
+                         const float* weight_scales, const float* bias, const void* packed_lora,
+                         q8_dtype lora_dtype, int64_t L, int64_t r, const int32_t* adapter_ids,
+                         double output_scale, int32_t output_zero_point, const char* activation,
+                         q8_dtype out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                         q8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

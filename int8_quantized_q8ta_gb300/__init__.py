@@ -46,6 +46,7 @@ EXPORTS = (
     "q8_expert_combine", "q8_expert_combine_backward",
     "q8_tile_packed_weight_bytes", "q8_tile_pack_weight", "q8_linear_experts_workspace_bytes",
     "q8_linear_experts",
+    "q8_lora_packed_bytes", "q8_lora_pack", "q8_linear_lora_workspace_bytes", "q8_linear_lora",
 )
 
 
@@ -142,6 +143,11 @@ def _load() -> ctypes.CDLL:
         "q8_linear_experts_workspace_bytes": (S, [I64, I64, I64]),
         "q8_linear_experts": (ctypes.c_int, [P, I32, I64, I64, I64, D, I32, P, I64, I64, P, P, P,
                                              P, D, I32, C, I32, P, P, S, P]),
+        "q8_lora_packed_bytes": (S, [I64, I64, I64, I64]),
+        "q8_lora_pack": (ctypes.c_int, [P, P, P, I32, I64, I64, I64, I64, P, S, P]),
+        "q8_linear_lora_workspace_bytes": (S, [I64, I64, I64, I64]),
+        "q8_linear_lora": (ctypes.c_int, [P, I64, I64, D, I32, P, I64, P, P, P, I32, I64, I64, P, D,
+                                          I32, C, I32, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -840,6 +846,7 @@ def conv2d_packed_acc32(x, input_zero_point, packed: PackedConvWeight, output_si
 # ---------------------------------------------------------------------------
 # rows of one batch that go through different weights
 # ---------------------------------------------------------------------------
-from .rows import (ExpertRoute, PackedTileWeight, expert_combine,  # noqa: E402
+from .rows import (ExpertRoute, PackedLora, PackedTileWeight, expert_combine,  # noqa: E402
                    expert_combine_backward, expert_dispatch, expert_gather,
-                   expert_gather_backward, expert_sort, linear_experts, pack_tile_weight)
+                   expert_gather_backward, expert_sort, linear_experts, linear_lora, pack_lora,
+                   pack_tile_weight)

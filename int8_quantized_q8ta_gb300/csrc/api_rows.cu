@@ -65,6 +65,40 @@ bool units_ok(int64_t R, int64_t E, int64_t N, int64_t K, const TilePlan& t) {
   return mul_ok(blocks, kbs) && mul_ok(tiles, blocks * kbs) && tiles * blocks * kbs <= INT32_MAX;
 }
 
+// ---- adapters --------------------------------------------------------------
+bool lora_sizes_ok(int64_t L, int64_t N, int64_t K, int64_t r) {
+  return L >= 1 && L <= q8::kMaxExperts && r >= 1 && r <= q8::kMaxRank && tile_sizes_ok(1, N, K);
+}
+
+// Packed adapters: B tiles, A rows, scaling (byte offsets).
+struct LoraLayout {
+  size_t a, scaling, total;
+};
+LoraLayout lora_layout(int64_t L, int64_t N, int64_t K, int64_t r) {
+  const size_t rank16 = (r + 15) / 16;
+  LoraLayout t{};
+  t.a = static_cast<size_t>(L) * ((N + 127) / 128) * rank16 * 4096;
+  t.scaling = t.a + static_cast<size_t>(L) * rank16 * 16 * q8::round_up(K, 64) * 2;
+  t.total = q8::align_ws(t.scaling + static_cast<size_t>(L) * 4);
+  return t;
+}
+
+// Workspace of the projection with adapters (byte offsets).
+struct LoraSpace {
+  TilePlan plan;
+  size_t h, lists, sort, total;
+};
+LoraSpace lora_space(int64_t M, int64_t K, int64_t L, int64_t r) {
+  LoraSpace t{};
+  t.plan = plan_tiles(M, K, 1);
+  const int64_t tiles = (M + t.plan.TN - 1) / t.plan.TN;
+  t.h = t.plan.total;
+  t.lists = t.h + q8::align_ws(static_cast<size_t>(M) * ((r + 15) / 16) * 64);
+  t.sort = t.lists + q8::align_ws(static_cast<size_t>(tiles) * (t.plan.TN + 1) * 4);
+  t.total = t.sort + (tiles > 1 ? q8::align_ws((3 * static_cast<size_t>(M) + L + 1) * 4) : 0);
+  return t;
+}
+
 // float rows (everything but the gather)
 q8_status check_float(q8_dtype dt) {
   if (!dtype_ok(dt)) return Q8_ERR_ARG;
@@ -259,6 +293,138 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
   job.counts = p.counts;
   job.count_words = plan.grid * q8::kTileEpiWarps;
   cudaError_t e = q8::launch_tile_operand(job, cs(stream));
+  if (e == cudaSuccess) e = q8::launch_tile_gemm(p, ws, out_dtype, cs(stream));
+  return cuda_status(e);
+}
+
+// ---- low-rank adapters beside a shared projection ---------------------------
+size_t q8_lora_packed_bytes(int64_t L, int64_t N, int64_t K, int64_t r) {
+  return lora_sizes_ok(L, N, K, r) ? lora_layout(L, N, K, r).total : 0;
+}
+
+q8_status q8_lora_pack(const void* A, const void* B, const float* scaling, q8_dtype dtype,
+                       int64_t L, int64_t r, int64_t N, int64_t K, void* packed,
+                       size_t packed_bytes, q8_stream_t stream) {
+  if (!A || !B || !scaling || !packed) return Q8_ERR_NULL;
+  if (!dtype_ok(dtype)) return Q8_ERR_ARG;
+  if (dtype != Q8_F16 && dtype != Q8_BF16) return Q8_ERR_UNSUPPORTED;
+  if (!lora_sizes_ok(L, N, K, r)) return Q8_ERR_SHAPE;
+  const LoraLayout lay = lora_layout(L, N, K, r);
+  if (packed_bytes < lay.total) return Q8_ERR_WORKSPACE;
+  if (!aligned(packed, q8::kWorkspaceAlign) || !aligned(A, 2) || !aligned(B, 2) ||
+      !aligned(scaling, 4))
+    return Q8_ERR_ALIGN;
+  auto* dst = static_cast<uint8_t*>(packed);
+  cudaError_t e = q8::launch_pack_lora(A, B, scaling, dtype == Q8_F16, L, r, N, K, dst + lay.a, dst,
+                                       reinterpret_cast<float*>(dst + lay.scaling), cs(stream));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cs(stream));   // load time, as for weights
+  return cuda_status(e);
+}
+
+size_t q8_linear_lora_workspace_bytes(int64_t M, int64_t K, int64_t L, int64_t r) {
+  if (M < 1 || M > INT32_MAX || K < 1 || K > INT32_MAX / 2 || L < 1 || L > q8::kMaxExperts ||
+      r < 1 || r > q8::kMaxRank)
+    return 0;
+  return lora_space(M, K, L, r).total;
+}
+
+q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
+                         int32_t input_zero_point, const void* packed_weight, int64_t N,
+                         const float* weight_scales, const float* bias, const void* packed_lora,
+                         q8_dtype lora_dtype, int64_t L, int64_t r, const int32_t* adapter_ids,
+                         double output_scale, int32_t output_zero_point, const char* activation,
+                         q8_dtype out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                         q8_stream_t stream) {
+  if (!activation) return Q8_ERR_NULL;
+  if (!dtype_ok(out_dtype) || !dtype_ok(lora_dtype)) return Q8_ERR_ARG;
+  if (lora_dtype != Q8_F16 && lora_dtype != Q8_BF16) return Q8_ERR_UNSUPPORTED;
+  if (M < 0 || M > INT32_MAX || !lora_sizes_ok(L, N, K, r)) return Q8_ERR_SHAPE;
+  if (!mul_ok(M, q8::round_up(K, 64) * 2) || !mul_ok(M, N * 4)) return Q8_ERR_SHAPE;
+  const int relu = parse_activation(activation);
+  if (relu < 0) return Q8_ERR_UNSUPPORTED;
+  if (!scale_ok(input_scale) || !scale_ok(output_scale) || !zp_ok(input_zero_point) ||
+      !zp_ok(output_zero_point))
+    return Q8_ERR_ARG;
+  if (M == 0) return Q8_OK;
+  if (!x || !packed_weight || !weight_scales || !packed_lora || !adapter_ids || !out)
+    return Q8_ERR_NULL;
+  if (!aligned(packed_weight, q8::kWorkspaceAlign) || !aligned(packed_lora, q8::kWorkspaceAlign) ||
+      !aligned(weight_scales, 4) || !aligned(bias, 4) || !aligned(adapter_ids, 4) ||
+      !aligned(out, q8::dtype_bytes(out_dtype)))
+    return Q8_ERR_ALIGN;
+  const LoraSpace sp = lora_space(M, K, L, r);
+  if (!units_ok(M, 1, N, K, sp.plan)) return Q8_ERR_SHAPE;
+  if ((M / 32 + q8::kMaxTileRows) * ((r + 15) / 16) > INT32_MAX / 16) return Q8_ERR_SHAPE;
+  if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
+  if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
+  auto* ws = static_cast<uint8_t*>(workspace);
+  const LoraLayout lay = lora_layout(L, N, K, r);
+  const auto* lora = static_cast<const uint8_t*>(packed_lora);
+
+  q8::TileParams p{};
+  p.R = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.NB = static_cast<int>((N + 127) / 128);
+  p.KB = static_cast<int>((K + 63) / 64);
+  p.E = 1;
+  p.TN = sp.plan.TN;
+  p.KD = sp.plan.KD;
+  p.grid = sp.plan.grid;
+  p.min_run = 4;
+  p.w = static_cast<const uint8_t*>(packed_weight);
+  p.w_bound = reinterpret_cast<const int32_t*>(p.w + tile_weight_bytes(1, N, K));
+  p.a_bound = a_bound_of(input_zero_point);
+  p.ws = weight_scales;
+  p.bias = bias;
+  p.rq = make_rq(input_scale, output_scale, output_zero_point, relu);
+  p.relu = relu;
+  p.out = out;
+  p.parts = reinterpret_cast<int32_t*>(ws + sp.plan.operand);
+  p.counts = reinterpret_cast<int32_t*>(ws + sp.plan.operand + sp.plan.parts);
+  p.L = static_cast<int>(L);
+  p.rank16 = static_cast<int>((r + 15) / 16);
+  p.lora_f16 = lora_dtype == Q8_F16;
+  p.lora_b = lora;
+  p.h = reinterpret_cast<const float*>(ws + sp.h);
+  p.lists = reinterpret_cast<const int32_t*>(ws + sp.lists);
+  p.list_stride = p.TN + 1;
+
+  q8::LoraJob job{};
+  job.op.x = x;
+  job.op.x_rows = M;
+  job.op.K = K;
+  job.op.R = p.R;
+  job.op.k = 1;
+  job.op.KB = p.KB;
+  job.op.zp = input_zero_point;
+  job.op.dst = reinterpret_cast<uint4*>(ws);
+  job.op.counts = p.counts;
+  job.op.count_words = p.grid * q8::kTileEpiWarps;
+  job.adapter_ids = adapter_ids;
+  job.L = p.L;
+  job.rank16 = p.rank16;
+  job.tiles = (p.R + p.TN - 1) / p.TN;
+  job.list_stride = p.list_stride;
+  job.a = reinterpret_cast<const uint16_t*>(lora + lay.a);
+  job.scaling = reinterpret_cast<const float*>(lora + lay.scaling);
+  job.s_in = static_cast<float>(input_scale);
+  job.h = reinterpret_cast<float*>(ws + sp.h);
+  job.lists = reinterpret_cast<int32_t*>(ws + sp.lists);
+  cudaError_t e = cudaSuccess;
+  if (job.tiles == 1) {
+    p.ids = adapter_ids;
+  } else {
+    // several row tiles: rows sorted by adapter, so that a tile meets few
+    auto* sorted = reinterpret_cast<int32_t*>(ws + sp.sort);
+    int32_t *order = sorted, *position = sorted + M, *ids = sorted + 2 * M,
+            *offsets = sorted + 3 * M;
+    e = q8::launch_expert_sort(adapter_ids, M, p.L, order, position, offsets, cs(stream), true);
+    job.op.order = order;
+    job.ids_out = ids;
+    p.ids = ids;
+    p.out_rows = order;
+  }
+  if (e == cudaSuccess) e = q8::launch_lora_front(job, lora_dtype == Q8_F16, cs(stream));
   if (e == cudaSuccess) e = q8::launch_tile_gemm(p, ws, out_dtype, cs(stream));
   return cuda_status(e);
 }

@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __rest
                                                            int64_t R, int E,
                                                            int32_t* __restrict__ order,
                                                            int32_t* __restrict__ position,
-                                                           int32_t* __restrict__ offsets) {
+                                                           int32_t* __restrict__ offsets,
+                                                           bool keep_dropped) {
   extern __shared__ int32_t sm[];
   const int G = E + 1;                        // groups: the experts and the dropped slots
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __rest
     if (in && rank_in == 0) mine[key] += __popc(peers);
     __syncwarp();
     if (in) {
-      order[row] = key < E ? static_cast<int32_t>(f) : -1;
+      order[row] = key < E || keep_dropped ? static_cast<int32_t>(f) : -1;
       position[f] = key < E ? row : -1;
     }
   }
@@ -316,7 +317,8 @@ size_t expert_sort_smem(int threads, int E) {
 }
 
 cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* order,
-                               int32_t* position, int32_t* offsets, cudaStream_t s) {
+                               int32_t* position, int32_t* offsets, cudaStream_t s,
+                               bool keep_dropped) {
   // one CTA up to 4096 slots (4 rounds of its 32 warps), then up to 8
   const int threads = R <= 256 ? 256 : 1024;
   int ctas = 1;
@@ -329,7 +331,7 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* or
   });
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(expert_sort_kernel, ctas, threads, smem, ctas, s, ids, R, E, order,
-                            position, offsets);
+                            position, offsets, keep_dropped);
 }
 
 cudaError_t launch_expert_gather(const void* x, int64_t T, int k, int64_t row_bytes,

@@ -62,8 +62,10 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
 }
 
 // ---- expert sort and row moves (route_kernels.cu) -------------------------
+// keep_dropped: the dropped slots keep their places at the end of order.
 cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* order,
-                               int32_t* position, int32_t* offsets, cudaStream_t s);
+                               int32_t* position, int32_t* offsets, cudaStream_t s,
+                               bool keep_dropped = false);
 cudaError_t launch_expert_gather(const void* x, int64_t T, int k, int64_t row_bytes,
                                  const int32_t* position, const int32_t* offsets, int E, void* xs,
                                  cudaStream_t s);
@@ -137,5 +139,28 @@ struct OperandJob {
   int count_words;
 };
 cudaError_t launch_tile_operand(const OperandJob& job, cudaStream_t s);
+
+// Adapters A [L][r][K], B [L][N][r] (16-bit) and scaling [L] in the layouts
+// the kernels read.
+cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling, bool f16,
+                             int64_t L, int64_t r, int64_t N, int64_t K, void* a_out, void* b_out,
+                             float* s_out, cudaStream_t s);
+
+// Everything the contraction with adapters needs before it, in one launch:
+// the operand (op.k == 1; op.order null when the rows come as they are), each
+// row's h, each row tile's adapters, and the rows' adapters in their order.
+struct LoraJob {
+  OperandJob op;
+  const int32_t* adapter_ids;   // [R], in the order of x
+  int L, rank16, tiles, list_stride;
+  const uint16_t* a;            // packed A
+  const float* scaling;
+  float s_in;
+  float* h;
+  int32_t* lists;
+  int32_t* ids_out;             // [R] in sorted order, or null
+  int shrink_ctas;              // set by the launcher
+};
+cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s);
 
 }  // namespace q8

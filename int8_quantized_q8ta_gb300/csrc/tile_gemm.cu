@@ -476,7 +476,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 hi[j] = __float_as_uint(f[j]) & 0xffffe000u;
-                lo[j] = __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
+                lo[j] = (hi[j] & 0x7f800000u) == 0x7f800000u   // inf - inf would be NaN
+                            ? 0u
+                            : __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
               }
               sts128(at + ((g ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
               sts128(at + (((g + 4) ^ (t & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);

@@ -1,5 +1,9 @@
 // tile_prep.cu -- what the grouped int8 contraction (tile_gemm.cu) reads:
-// load-time packing of weights, and the token operand.  Bandwidth-bound.
+// load-time packing of weights and adapters, the token operand, and for
+// adapters the rows' low-rank products h and each tile's list of adapters.
+// Bandwidth-bound.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -10,6 +14,8 @@
 #include "tile_device.cuh"
 
 namespace q8 {
+
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -95,6 +101,276 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job,
   for (int64_t i = t; i < total; i += step) operand_item(job, i, vec, minus);
 }
 
+// ---------------------------------------------------------------------------
+// Adapters: h[s, j] = s_in * scaling[a] * sum_k (x[row(s), k] - zp) A[a][j, k]
+// for the rows with an adapter.  A cluster of 8 CTAs takes 16 ranks of one
+// adapter and up to 32 of its rows at a time; its 64 warps split K in steps of
+// 32 and multiply with m16n8k16 MMAs, ranks on M and rows on N.  The sum over
+// k may take any order, so a thread's fragments are 8 consecutive inputs: one
+// 16-byte load of A and one 8-byte load of x per row, no shared memory.  The
+// warps' f32 sums are added in a fixed order, first in the CTA, then over the
+// cluster through distributed shared memory.
+//   Up to kMaxTileRows rows (one row tile) the rows come as they are, and the
+// cluster of an adapter's first row takes all of that adapter's rows, so that
+// A is read once.  More rows come sorted by adapter, and a cluster takes the
+// runs inside 32 of them.
+// ---------------------------------------------------------------------------
+constexpr int kFrontThreads = 256;
+constexpr int kFrontCluster = 8;
+constexpr int kFrontRows = 32;
+
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct FrontShared {
+  float part[kFrontThreads / 32][16][kFrontRows + 1];
+  float sum[16][kFrontRows];      // read by the cluster's other CTAs
+  int32_t rows[kMaxTileRows];     // the rows this cluster takes
+  int32_t warp_count[kFrontThreads / 32];
+};
+
+// Eight inputs of a row from k0 on, minus zp, in the adapters' type (bf16 and
+// f16 both hold integers up to 255 exactly); zeros beyond K.
+template <bool F16>
+__device__ __forceinline__ void load_x8(const LoraJob& job, int64_t row, int k0, bool vec,
+                                        uint32_t (&v)[4]) {
+  uint2 w = make_uint2(0, 0);
+  const int8_t* src = job.op.x + row * job.op.K + k0;
+  if (vec) {
+    if (k0 < job.op.K) w = __ldg(reinterpret_cast<const uint2*>(src));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < job.op.K) {
+        const uint32_t b = static_cast<uint32_t>(static_cast<uint8_t>(__ldg(src + j)))
+                           << (8 * (j & 3));
+        if (j < 4) w.x |= b; else w.y |= b;
+      }
+  }
+  if constexpr (F16) {
+    const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
+    v[0] = biased_to_f16x2(w.x ^ 0x80808080u, 0x4140, minus);
+    v[1] = biased_to_f16x2(w.x ^ 0x80808080u, 0x4342, minus);
+    v[2] = biased_to_f16x2(w.y ^ 0x80808080u, 0x4140, minus);
+    v[3] = biased_to_f16x2(w.y ^ 0x80808080u, 0x4342, minus);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t h = j < 2 ? w.x >> (16 * j) : w.y >> (16 * (j - 2));
+      v[j] = bf16x2_from_ints(static_cast<int8_t>(h & 0xff) - job.op.zp,
+                              static_cast<int8_t>((h >> 8) & 0xff) - job.op.zp);
+    }
+  }
+}
+
+// 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
+template <bool F16>
+__device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
+                           int c, const int32_t* rows, int row0, int count, bool vec) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = cluster.block_rank();
+  const int Kp = job.op.KB * 64;
+  const uint16_t* A = job.a + (static_cast<int64_t>(a) * job.rank16 + c) * 16 * Kp;
+  float acc[4][4] = {};
+  int64_t from[4];
+  const int tiles = (count + 7) / 8;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int i = n * 8 + g;
+    from[n] = -1;
+    if (i < count) {
+      const int s = rows != nullptr ? rows[i] : row0 + i;
+      from[n] = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+    }
+  }
+#pragma unroll 2
+  for (int k0 = (rank * (kFrontThreads / 32) + warp) * 32 + t * 8; k0 < Kp;
+       k0 += kFrontCluster * kFrontThreads) {
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g) * Kp + k0));
+    const uint4 hi =
+        __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g + 8) * Kp + k0));
+    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (n < tiles) {
+        uint32_t v[4] = {0, 0, 0, 0};
+        if (from[n] >= 0) load_x8<F16>(job, from[n], k0, vec, v);
+        mma_16816<F16>(acc[n], a0, v[0], v[1]);
+        mma_16816<F16>(acc[n], a1, v[2], v[3]);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sh.part[warp][g + (j >> 1) * 8][n * 8 + t * 2 + (j & 1)] = acc[n][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * kFrontRows; i += kFrontThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFrontThreads / 32; ++w) v += sh.part[w][i / kFrontRows][i % kFrontRows];
+    sh.sum[i / kFrontRows][i % kFrontRows] = v;
+  }
+  cluster.sync();
+  if (threadIdx.x < 16 * kFrontRows / kFrontCluster) {
+    // this CTA's 4 rows of the 32, 16 ranks each
+    const int j = threadIdx.x & 15, i = rank * (kFrontRows / kFrontCluster) + (threadIdx.x >> 4);
+    if (i < count) {
+      float v = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kFrontCluster; ++r) v += *cluster.map_shared_rank(&sh.sum[j][i], r);
+      const int s = rows != nullptr ? rows[i] : row0 + i;
+      job.h[static_cast<int64_t>(s) * job.rank16 * 16 + c * 16 + j] =
+          v * job.s_in * __ldg(job.scaling + a);
+    }
+  }
+  cluster.sync();   // the sums may be overwritten now
+}
+
+__device__ __forceinline__ int adapter_of(const LoraJob& job, int s) {
+  const int row = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+  const int a = __ldg(job.adapter_ids + row);
+  return a >= 0 && a < job.L ? a : -1;
+}
+
+// Indices i < n whose flag is set, in order, into list; returns how many.
+__device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t* list) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t m = __ballot_sync(0xffffffffu, flag);
+  if (lane == 0) sh.warp_count[warp] = __popc(m);
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kFrontThreads / 32; ++w) {
+    if (w < warp) before += sh.warp_count[w];
+    total += sh.warp_count[w];
+  }
+  if (flag) list[before + __popc(m & ((1u << lane) - 1u))] = value;
+  __syncthreads();
+  return total;
+}
+
+// Blocks: job.shrink_ctas for h, then one per row tile for its list, the rest
+// for the operand.
+template <bool F16>
+__global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob job, bool vec) {
+  __shared__ FrontShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int R = job.op.R;
+  int b = blockIdx.x;
+  if (b < job.shrink_ctas) {
+    const int u = b / kFrontCluster, c = u % job.rank16, w = u / job.rank16;
+    if (job.op.order == nullptr) {
+      // row w's adapter, if no earlier row has it
+      const int a = adapter_of(job, w);
+      const int mine = static_cast<int>(threadIdx.x) < R ? adapter_of(job, threadIdx.x) : -1;
+      const bool same = a >= 0 && mine == a;
+      if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
+      const int n = block_compact(sh, same, threadIdx.x, sh.rows);
+      for (int i = 0; i < n; i += kFrontRows)
+        front_rows<F16>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i), vec);
+    } else {
+      const int hi = min(R, (w + 1) * kFrontRows);
+      for (int s = w * kFrontRows; s < hi;) {
+        const int a = adapter_of(job, s);
+        int e = s + 1;
+        while (e < hi && adapter_of(job, e) == a) ++e;
+        if (a >= 0) front_rows<F16>(job, sh, cluster, a, c, nullptr, s, e - s, vec);
+        s = e;
+      }
+    }
+    return;
+  }
+  b -= job.shrink_ctas;
+  if (b < job.tiles) {
+    // the tile's adapters, each once, in the order of their first rows
+    const int per = tile_rows(R, job.tiles), row0 = b * per, n = min(per, R - row0);
+    const int t = threadIdx.x;
+    const int a = t < n ? adapter_of(job, row0 + t) : -1;
+    if (t < n) sh.rows[t] = a;
+    __syncthreads();
+    bool first = a >= 0;
+    for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
+    __syncthreads();
+    int32_t* list = job.lists + static_cast<int64_t>(b) * job.list_stride;
+    const int count = block_compact(sh, first, a, list + 1);
+    if (t == 0) list[0] = count;
+    if (job.ids_out != nullptr && t < n) job.ids_out[row0 + t] = a;
+    return;
+  }
+  b -= job.tiles;
+  const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
+  const int64_t step =
+      static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.tiles) * kFrontThreads;
+  for (int64_t i = t; i < job.op.count_words; i += step) job.op.counts[i] = 0;
+  const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
+  const int64_t total = static_cast<int64_t>(R) * job.op.KB * 8;
+  for (int64_t i = t; i < total; i += step) operand_item(job.op, i, vec, minus);
+}
+
+// Adapter matrices, padded with zeros: A -> [L][16 rank16][64 KB], and
+// B -> [L][NB][rank16][2][128][8] (8-rank chunks of all 128 channels).  A tile
+// multiplies every adapter it holds by all of its rows, zeros standing for the
+// rows of others, so an infinity or NaN of B must not enter the product:
+// those entries become zeros, and the adapter's scaling NaN
+// (lora_scaling_kernel), which makes its own rows NaN and no others.
+__device__ __forceinline__ bool finite16(uint16_t v, uint32_t exponent) {
+  return (v & exponent) != exponent;
+}
+
+__global__ void __launch_bounds__(256) lora_scaling_kernel(const uint16_t* __restrict__ B,
+                                                           const float* __restrict__ scaling,
+                                                           int64_t per, uint32_t exponent,
+                                                           float* __restrict__ s_out) {
+  pdl_wait();
+  bool bad = false;
+  for (int64_t i = threadIdx.x; i < per; i += blockDim.x)
+    bad |= !finite16(B[blockIdx.x * per + i], exponent);
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0)
+    s_out[blockIdx.x] = bad ? __int_as_float(0x7fffffff) : scaling[blockIdx.x];
+}
+
+__global__ void __launch_bounds__(256) pack_lora_kernel(const uint16_t* __restrict__ A,
+                                                        const uint16_t* __restrict__ B,
+                                                        uint32_t exponent, int64_t L, int64_t r, int64_t N, int64_t K,
+                                                        int64_t rank16, int64_t NB, int64_t Kp,
+                                                        uint16_t* __restrict__ a_out,
+                                                        uint16_t* __restrict__ b_out) {
+  pdl_wait();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t rp = rank16 * 16;
+  for (int64_t i = t; i < L * rp * Kp; i += step) {
+    const int64_t k = i % Kp, j = i / Kp % rp, l = i / Kp / rp;
+    a_out[i] = (k < K && j < r) ? A[(l * r + j) * K + k] : 0;
+  }
+  for (int64_t i = t; i < L * NB * rank16 * 2048; i += step) {
+    const int64_t w = i & 7, row = (i >> 3) & 127, half = (i >> 10) & 1;
+    int64_t q = i >> 11;
+    const int64_t c = q % rank16;
+    q /= rank16;
+    const int64_t n = (q % NB) * 128 + row, l = q / NB, j = c * 16 + half * 8 + w;
+    const uint16_t v = (n < N && j < r) ? B[(l * N + n) * r + j] : 0;
+    b_out[i] = finite16(v, exponent) ? v : 0;
+  }
+}
+
 bool rows_vec8(const OperandJob& job) {
   return job.K % 8 == 0 && reinterpret_cast<uintptr_t>(job.x) % 8 == 0;
 }
@@ -113,6 +389,30 @@ cudaError_t launch_tile_operand(const OperandJob& job, cudaStream_t s) {
                     blocks_for(std::max<int64_t>(static_cast<int64_t>(job.R) * job.KB * 8,
                                                  job.count_words)),
                     256, 0, s, job, rows_vec8(job));
+}
+
+cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling, bool f16,
+                             int64_t L, int64_t r, int64_t N, int64_t K, void* a_out, void* b_out,
+                             float* s_out, cudaStream_t s) {
+  const int64_t rank16 = (r + 15) / 16, NB = (N + 127) / 128, Kp = round_up(K, 64);
+  const uint32_t exponent = f16 ? 0x7c00u : 0x7f80u;
+  const auto* b = static_cast<const uint16_t*>(B);
+  cudaError_t e = launch_pdl(lora_scaling_kernel, static_cast<int>(L), 256, 0, s, b, scaling, N * r,
+                             exponent, s_out);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(pack_lora_kernel, blocks_for(L * rank16 * 16 * Kp), 256, 0, s,
+                    static_cast<const uint16_t*>(A), b, exponent, L, r, N, K, rank16, NB, Kp,
+                    static_cast<uint16_t*>(a_out), static_cast<uint16_t*>(b_out));
+}
+
+cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
+  const int groups = job.op.order == nullptr ? job.op.R : (job.op.R + kFrontRows - 1) / kFrontRows;
+  job.shrink_ctas = groups * job.rank16 * kFrontCluster;
+  const int copy = blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
+                                                job.op.count_words));
+  const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, kFrontCluster));
+  return launch_pdl_cluster(f16 ? lora_front_kernel<true> : lora_front_kernel<false>, grid,
+                            kFrontThreads, 0, kFrontCluster, s, job, rows_vec8(job.op));
 }
 
 }  // namespace q8

@@ -241,3 +241,77 @@ def linear_experts(x, input_scale, input_zero_point, packed: PackedTileWeight, w
         _ptr(route.offsets), float(output_scale), int(output_zero_point), activation.encode(),
         _DTYPE[out_dtype], _ptr(out), _ptr(ws), nbytes, _stream(x)), "q8_linear_experts")
     return out
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters beside a shared projection
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class PackedLora:
+    """Adapters in the kernels' layout (see q8_lora_pack): ``data`` is a uint8
+    CUDA buffer, ``dtype`` the type A and B came in."""
+    data: torch.Tensor
+    L: int
+    N: int
+    K: int
+    r: int
+    dtype: torch.dtype
+
+
+def pack_lora(A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor) -> PackedLora:
+    """Pack adapters A [L, r, K], B [L, N, r] (float16 or bfloat16) and
+    scaling float32 [L] once."""
+    if _dtype_code(A, "A") not in (1, 2):
+        raise TypeError(f"A must be float16 or bfloat16, got {A.dtype}")
+    _need(A, A.dtype, "A")
+    _need(B, A.dtype, "B")
+    _need(scaling, torch.float32, "scaling")
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [L, r, K] and B [L, N, r]")
+    L, r, K = A.shape
+    N = B.shape[1]
+    _shape(B, (L, N, r), "B")
+    _shape(scaling, (L,), "scaling")
+    nbytes = _lib.q8_lora_packed_bytes(L, N, K, r)
+    if nbytes == 0:
+        raise Q8Error(Q8_ERR_SHAPE, "q8_lora_packed_bytes")
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=A.device)
+    _check(_lib.q8_lora_pack(_ptr(A), _ptr(B), _ptr(scaling), _DTYPE[A.dtype], L, r, N, K,
+                             _ptr(buf), nbytes, _stream(A)), "q8_lora_pack")
+    return PackedLora(buf, L, N, K, r, A.dtype)
+
+
+def linear_lora(x, input_scale, input_zero_point, packed: PackedTileWeight, weight_scales, bias,
+                lora: PackedLora, adapter_ids, output_scale, output_zero_point,
+                activation="none", out_dtype=torch.int8, out=None, workspace=None):
+    """int8 x [M, K] times a shared int8 weight [N, K], plus each row's
+    low-rank adapter (see q8_linear_lora): adapter_ids int32 [M], ids outside
+    [0, L) for none; weight_scales and bias float32 [N]; out [M, N]."""
+    _need(x, torch.int8, "x")
+    if packed.E != 1:
+        raise ValueError(f"the packed weight has {packed.E} groups, the shared projection one")
+    N, K = packed.N, packed.K
+    if (lora.N, lora.K) != (N, K):
+        raise ValueError(f"adapters are for {lora.N}x{lora.K}, the weight is {N}x{K}")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [M, {K}], got {tuple(x.shape)}")
+    M = x.shape[0]
+    _need(weight_scales, torch.float32, "weight_scales")
+    _shape(weight_scales, (N,), "weight_scales")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _shape(bias, (N,), "bias")
+    _need(adapter_ids, torch.int32, "adapter_ids")
+    _shape(adapter_ids, (M,), "adapter_ids")
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype must be float32, float16, bfloat16 or int8, got {out_dtype}")
+    out = _out(out, (M, N), out_dtype, x.device)
+    nbytes = _lib.q8_linear_lora_workspace_bytes(M, K, lora.L, lora.r)
+    ws = _workspace(nbytes, x.device, workspace)
+    _check(_lib.q8_linear_lora(
+        _ptr(x), M, K, float(input_scale), int(input_zero_point), _ptr(packed.data), N,
+        _ptr(weight_scales), _ptr(bias), _ptr(lora.data), _DTYPE[lora.dtype], lora.L, lora.r,
+        _ptr(adapter_ids), float(output_scale), int(output_zero_point), activation.encode(),
+        _DTYPE[out_dtype], _ptr(out), _ptr(ws), nbytes, _stream(x)), "q8_linear_lora")
+    return out

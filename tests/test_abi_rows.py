@@ -123,3 +123,48 @@ def test_linear_experts_guards():
     assert call(T=0, x=None, out=None) == q8.Q8_OK
     # the k-blocks of all units have to fit 32 bits
     assert call(T=2 ** 22, k=8, N=2 ** 16, K=2 ** 16, bytes=2 ** 62) == q8.Q8_ERR_SHAPE
+
+
+def test_lora_pack_guards():
+    size = lib.q8_lora_packed_bytes
+    # B tiles of 4 KB, A rows of 64-padded K, scaling
+    assert size(2, 128, 64, 16) == 2 * 4096 + 2 * 16 * 64 * 2 + 256
+    assert size(0, 128, 64, 16) == size(1025, 128, 64, 16) == size(1, 128, 64, 257) == 0
+    p = lib.q8_lora_pack
+    big = 1 << 20
+    assert p(None, FAKE, FAKE, F16, 2, 16, 128, 64, FAKE, big, None) == q8.Q8_ERR_NULL
+    assert p(FAKE, FAKE, None, F16, 2, 16, 128, 64, FAKE, big, None) == q8.Q8_ERR_NULL
+    assert p(FAKE, FAKE, FAKE, F32, 2, 16, 128, 64, FAKE, big, None) == q8.Q8_ERR_UNSUPPORTED
+    assert p(FAKE, FAKE, FAKE, 5, 2, 16, 128, 64, FAKE, big, None) == q8.Q8_ERR_ARG
+    assert p(FAKE, FAKE, FAKE, BF16, 2, 0, 128, 64, FAKE, big, None) == q8.Q8_ERR_SHAPE
+    assert p(FAKE, FAKE, FAKE, BF16, 2, 16, 128, 64, FAKE, 100, None) == q8.Q8_ERR_WORKSPACE
+    assert p(ctypes.c_void_p(0x10001), FAKE, FAKE, BF16, 2, 16, 128, 64, FAKE, big,
+             None) == q8.Q8_ERR_ALIGN
+
+
+def test_linear_lora_guards():
+    f = lib.q8_linear_lora
+    need = lib.q8_linear_lora_workspace_bytes(8, 64, 4, 16)
+    assert need > 0 and need % 256 == 0
+    assert lib.q8_linear_lora_workspace_bytes(8, 64, 0, 16) == 0
+    names = ["x", "M", "K", "s_in", "zp", "w", "N", "ws", "b", "lora", "ldt", "L", "r", "ids",
+             "s_out", "ozp", "act", "dt", "out", "space", "bytes", "stream"]
+    ok = dict(zip(names, [FAKE, 8, 64, 0.02, 0, FAKE, 32, FAKE, None, FAKE, BF16, 4, 16, FAKE, 0.1,
+                          0, b"none", I8, FAKE, FAKE, need, None]))
+
+    def call(**kw):
+        return f(*dict(ok, **kw).values())
+    for n in ("x", "w", "ws", "lora", "ids", "out", "act"):
+        assert call(**{n: None}) == q8.Q8_ERR_NULL, n
+    for n in ("M", "K", "N", "L", "r"):
+        assert call(**{n: -1}) == q8.Q8_ERR_SHAPE, n
+    assert call(r=257) == call(L=1025) == q8.Q8_ERR_SHAPE
+    assert call(ldt=F32) == q8.Q8_ERR_UNSUPPORTED
+    assert call(act=b"tanh") == q8.Q8_ERR_UNSUPPORTED
+    assert call(dt=-1) == q8.Q8_ERR_ARG
+    assert call(s_in=-1.0) == call(ozp=200) == q8.Q8_ERR_ARG
+    assert call(bytes=need - 1) == call(space=None) == q8.Q8_ERR_WORKSPACE
+    for n in ("w", "lora", "space"):
+        assert call(**{n: ctypes.c_void_p(0x10010)}) == q8.Q8_ERR_ALIGN, n
+    assert call(ids=ODD) == call(out=ODD, dt=F32) == q8.Q8_ERR_ALIGN
+    assert call(M=0, x=None, ids=None) == q8.Q8_OK
