@@ -100,46 +100,92 @@ __device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start
   return max(0, group_end(p, e + 1) - start);
 }
 
-// The CTA's run of the line of all units' k-blocks (32-bit: the host checks).
+// The CTA's run of the line of all units' k-blocks (32-bit: the host checks),
+// unit by unit.  The divisions that place its start are done once: one integer
+// division by a runtime value takes longer than a k-block's MMAs.
 struct Walk {
   const TileParams& p;
-  const int32_t* prefix;   // row tiles before each group (shared memory), or null: one group
-  int pos, end, q;         // q: k-blocks of every run but the last
-  __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix_, int tiles)
-      : p(p_), prefix(prefix_) {
-    const int total = tiles * p.NB * p.KB;
+  int q;                   // k-blocks of every run but the last
+  int left, unit, kb;      // k-blocks still to take; the unit and where in it
+  int e, start, count;     // the unit's group and its rows
+  int tiles, per, t0;      // the group's row tiles, rows of each, tiles before them
+  int i, nb;               // row tile and output block: tiles of one block follow one another
+
+  __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix, int all_tiles)
+      : p(p_) {
+    const int total = all_tiles * p.NB * p.KB;
     q = max(p.min_run, (total - 1) / static_cast<int>(gridDim.x) + 1);
-    pos = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * blockIdx.x));
-    end = min(total - pos, q) + pos;
-  }
-  __device__ bool next(Seg& s) {
-    if (pos >= end) return false;
-    s.unit = pos / p.KB;
-    s.kb0 = pos - s.unit * p.KB;
-    s.kb1 = min(p.KB, s.kb0 + (end - pos));
-    pos += s.kb1 - s.kb0;
-    int t0 = 0, tiles, start = 0, count = p.R;
-    s.e = 0;
+    const int pos =
+        static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * blockIdx.x));
+    left = min(total - pos, q);
+    unit = pos / p.KB;
+    kb = pos - unit * p.KB;
+    e = 0;
+    start = 0;
+    count = p.R;
+    t0 = 0;
+    if (left <= 0) return;
     if (prefix != nullptr) {
-      // the group whose units hold this one
+      // the last group that starts at or before this unit (groups without
+      // rows have no units)
       int lo = 0, hi = p.E - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] * p.NB <= s.unit) lo = mid; else hi = mid - 1;
+        if (prefix[mid] * p.NB <= unit) lo = mid; else hi = mid - 1;
       }
-      s.e = lo;
+      e = lo;
       t0 = prefix[lo];
-      count = group_rows(p, lo, start);
+      count = group_rows(p, e, start);
     }
+    cut();
+    const int local = unit - t0 * p.NB;
+    nb = local / tiles;
+    i = local - nb * tiles;
+  }
+  __device__ __forceinline__ void cut() {
     tiles = (count + p.TN - 1) / p.TN;
-    const int local = s.unit - t0 * p.NB;
-    const int i = local % tiles;       // the tiles of one output block follow one another
-    s.nb = local / tiles;
-    const int per = tile_rows(count, tiles);
+    per = tile_rows(count, tiles);
+  }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (left <= 0) return false;
+    s.e = e;
+    s.nb = nb;
     s.row0 = start + i * per;
     s.rows = min(per, count - i * per);
     s.tile = t0 + i;
+    s.unit = unit;
+    s.kb0 = kb;
+    s.kb1 = min(p.KB, kb + left);
+    left -= s.kb1 - s.kb0;
+    if (left > 0) {
+      kb = 0;
+      ++unit;
+      if (++i == tiles) {
+        i = 0;
+        if (++nb == p.NB) {
+          nb = 0;
+          t0 += tiles;
+          do {
+            ++e;
+            count = group_rows(p, e, start);
+          } while (count == 0 && e + 1 < p.E);
+          cut();
+        }
+      }
+    }
     return true;
+  }
+};
+
+// A place in the ring and the parity of its current round.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int stages) {
+    if (++slot == stages) {
+      slot = 0;
+      phase ^= 1u;
+    }
   }
 };
 
@@ -177,9 +223,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ TileShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring0 = (smem_u32(dyn) + 1023u) & ~1023u;
-  const int KD = p.KD, S = p.stages, NA = 4 / KD;
+  const int KD = p.KD, S = p.stages, NAb = KD == 2 ? 1 : 2, NA = 1 << NAb;
   const uint32_t tok_bytes = static_cast<uint32_t>(p.TN) * 128u;
   const uint32_t stage_bytes = static_cast<uint32_t>(KD) * (tok_bytes + kTileWBytes);
+  // NA = 4 / KD stages of A operands fit their 128 TMEM columns
   int32_t* prefix = p.offsets != nullptr
                         ? reinterpret_cast<int32_t*>(dyn + (ring0 - smem_u32(dyn)) +
                                                      static_cast<size_t>(S) * stage_bytes)
@@ -242,6 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       Walk walk(p, prefix, tiles);
       Seg sg;
       const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
+      Ring ring;
       int it = 0;
       bool ok = true;
       // the first ring of weights of a single group does not depend on the
@@ -266,12 +314,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       while (ok && walk.next(sg)) {
         const uint8_t* w = p.w + (static_cast<int64_t>(sg.e) * p.NB + sg.nb) * w_rows;
-        for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it) {
-          const int slot = it % S;
+        for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it, ring.advance(S)) {
+          const int slot = ring.slot;
           const int nk = min(KD, sg.kb1 - kb);
           const uint32_t st = ring0 + slot * stage_bytes, bar = smem_u32(&sh.full[slot]);
           if (it >= early) {
-            ok = tile_wait(smem_u32(&sh.empty[slot]), ((it / S) & 1) ^ 1, abort_flag, kErrTileRing,
+            ok = tile_wait(smem_u32(&sh.empty[slot]), ring.phase ^ 1, abort_flag, kErrTileRing,
                            p.err);
             if (!ok) break;
             mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
@@ -286,9 +334,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < na && ok; ++i) {
           const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(__ldg(list + i)) * p.NB + sg.nb) *
                                           p.rank16) * 4096;
-          for (int c = 0; c < p.rank16; ++c, ++it) {
-            const int slot = it % S;
-            ok = tile_wait(smem_u32(&sh.empty[slot]), ((it / S) & 1) ^ 1, abort_flag, kErrTileRing,
+          for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+            const int slot = ring.slot;
+            ok = tile_wait(smem_u32(&sh.empty[slot]), ring.phase ^ 1, abort_flag, kErrTileRing,
                            p.err);
             if (!ok) break;
             const uint32_t bar = smem_u32(&sh.full[slot]);
@@ -309,6 +357,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane == 0) {
       Walk walk(p, prefix, tiles);
       Seg sg;
+      Ring ring;
       int it = 0, ac = 0;
       bool ok = true;
       const int chunk = chunk_stages_of(p);
@@ -326,11 +375,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t d = tmem + buf * kAccCols;
           uint32_t accumulate = 0;
           const int c1 = min(stages, c0 + chunk);
-          for (int s = c0; s < c1; ++s, ++it, kb += KD) {
-            const int slot = it % S, as = it % NA;
-            ok = tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
+          for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
+            const int slot = ring.slot, as = it & (NA - 1);
+            ok = tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag, kErrTileRing,
                            p.err) &&
-                 tile_wait(smem_u32(&sh.ready[as]), (it / NA) & 1, abort_flag, kErrTileOperand,
+                 tile_wait(smem_u32(&sh.ready[as]), (it >> NAb) & 1, abort_flag, kErrTileOperand,
                            p.err);
             if (!ok) break;
             tc_fence_after();
@@ -359,9 +408,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t d = tmem + buf * kAccCols;
           const uint32_t id32 = idesc_tf32(n16);
           uint32_t accumulate = 0;
-          for (int i = 0; i < na * p.rank16; ++i, ++it) {
-            const int slot = it % S, as = it % NA;
-            ok = tile_wait(smem_u32(&sh.ready[as]), (it / NA) & 1, abort_flag, kErrTileOperand,
+          for (int i = 0; i < na * p.rank16; ++i, ++it, ring.advance(S)) {
+            const int slot = ring.slot, as = it & (NA - 1);
+            ok = tile_wait(smem_u32(&sh.ready[as]), (it >> NAb) & 1, abort_flag, kErrTileOperand,
                            p.err);
             if (!ok) break;
             tc_fence_after();
@@ -393,15 +442,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t a_lane = a_base + (static_cast<uint32_t>(warp & 3) << 21);
     const int t0 = (warp - kFirstConv) * 32 + lane;   // this thread among the 128
     const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    Ring ring, used;   // this stage; the one whose A operand lay where this one's goes
     int it = 0;
     bool ok = true;
+    const auto place_free = [&]() {
+      if (it < NA) return true;
+      const bool free = tile_wait(smem_u32(&sh.empty[used.slot]), used.phase, abort_flag,
+                                  kErrTileOperand, p.err);
+      used.advance(S);
+      return free;
+    };
     while (ok && walk.next(sg)) {
-      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it) {
-        const int slot = it % S, as = it % NA;
-        ok = it < NA || tile_wait(smem_u32(&sh.empty[(it - NA) % S]), ((it - NA) / S) & 1,
-                                  abort_flag, kErrTileOperand, p.err);
-        ok = ok && tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
-                             p.err);
+      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it, ring.advance(S)) {
+        const int slot = ring.slot, as = it & (NA - 1);
+        ok = place_free() && tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag,
+                                       kErrTileRing, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -433,12 +488,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int n16 = (sg.rows + 15) & ~15;
       for (int i = 0; i < na && ok; ++i) {
         const int a_id = __ldg(list + i);
-        for (int c = 0; c < p.rank16; ++c, ++it) {
-          const int slot = it % S, as = it % NA;
-          ok = it < NA || tile_wait(smem_u32(&sh.empty[(it - NA) % S]), ((it - NA) / S) & 1,
-                                    abort_flag, kErrTileOperand, p.err);
-          ok = ok && tile_wait(smem_u32(&sh.full[slot]), (it / S) & 1, abort_flag, kErrTileRing,
-                               p.err);
+        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+          const int slot = ring.slot, as = it & (NA - 1);
+          ok = place_free() && tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag,
+                                         kErrTileRing, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
