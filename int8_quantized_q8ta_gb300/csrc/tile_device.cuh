@@ -130,6 +130,27 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity,
     }
   }
 }
+// tile_wait by a whole warp, the same answer in every lane.
+__device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile uint32_t* abort_flag, uint32_t code,
+                                               uint32_t* err) {
+  return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag, code, err));
+}
+// True in one lane of a converged warp.  The issuing warps run their loops in
+// every lane and elect one for the copies and MMAs alone: addresses and
+// descriptors then live in uniform registers, where code under `lane == 0`
+// moves each operand there again for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
 // The same while winding down: ignores the abort flag.
 __device__ __forceinline__ void tile_wait_final(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const TileParams p) {
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TileShared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t ring0 = (smem_u32(dyn) + 1023u) & ~1023u;
   const int KD = p.KD, S = p.stages, NAb = KD == 2 ? 1 : 2, NA = 1 << NAb;
   const uint32_t tok_bytes = static_cast<uint32_t>(p.TN) * 128u;
@@ -284,154 +284,166 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tiles = sh.tiles;
 
   if (warp == 0) {
-    // ---- copies: one thread ------------------------------------------------
-    if (lane == 0) {
-      Walk walk(p, prefix, tiles);
-      Seg sg;
-      const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
-      Ring ring;
-      int it = 0;
-      bool ok = true;
-      // the first ring of weights of a single group does not depend on the
-      // kernel before this one: a packed weight is written at load time
-      int early = 0;
-      if (prefix == nullptr) {
-        Walk w2 = walk;
-        Seg s2;
-        while (early < S && w2.next(s2)) {
-          for (int kb = s2.kb0; kb < s2.kb1 && early < S; kb += KD, ++early) {
-            const int nk = min(KD, s2.kb1 - kb);
-            const uint32_t st = ring0 + early * stage_bytes, bar = smem_u32(&sh.full[early]);
-            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
-            bulk_load(st + KD * tok_bytes,
-                      p.w + static_cast<int64_t>(s2.nb) * w_rows +
-                          static_cast<int64_t>(kb) * kTileWBytes,
-                      nk * kTileWBytes, bar);
-          }
-          if (p.L > 0) break;   // adapter stages follow: their list is not known yet
-        }
-        pdl_wait();
-      }
-      while (ok && walk.next(sg)) {
-        const uint8_t* w = p.w + (static_cast<int64_t>(sg.e) * p.NB + sg.nb) * w_rows;
-        for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it, ring.advance(S)) {
-          const int slot = ring.slot;
-          const int nk = min(KD, sg.kb1 - kb);
-          const uint32_t st = ring0 + slot * stage_bytes, bar = smem_u32(&sh.full[slot]);
-          if (it >= early) {
-            ok = tile_wait(smem_u32(&sh.empty[slot]), ring.phase ^ 1, abort_flag, kErrTileRing,
-                           p.err);
-            if (!ok) break;
+    // ---- copies: one elected lane of a warp that runs in step ----------------
+    Walk walk(p, prefix, tiles);
+    Seg sg;
+    const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
+    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+    Ring ring;
+    int it = 0;
+    bool ok = true;
+    // the first ring of weights of a single group does not depend on the
+    // kernel before this one: a packed weight is written at load time
+    int early = 0;
+    if (prefix == nullptr) {
+      Walk w2 = walk;
+      while (early < S && w2.next(sg)) {
+        const uint8_t* w = p.w + uniform(sg.nb) * w_rows;
+        const int kb1 = uniform(sg.kb1);
+        for (int kb = uniform(sg.kb0); kb < kb1 && early < S; kb += KD, ++early) {
+          const uint32_t nk = min(KD, kb1 - kb);
+          const uint32_t st = ring0 + early * stage_bytes, bar = full0 + early * 8;
+          if (elect_one()) {
             mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
             bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
                       nk * kTileWBytes, bar);
           }
-          tma_load_3d(st, &map_x, bar, 0, sg.row0, kb);
+          __syncwarp();
         }
-        if (!ok) break;
-        const int na = adapters_of(p, sg);
-        const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
-        for (int i = 0; i < na && ok; ++i) {
-          const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(__ldg(list + i)) * p.NB + sg.nb) *
-                                          p.rank16) * 4096;
-          for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
-            const int slot = ring.slot;
-            ok = tile_wait(smem_u32(&sh.empty[slot]), ring.phase ^ 1, abort_flag, kErrTileRing,
-                           p.err);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(&sh.full[slot]);
-            mbar_arrive_expect_tx(bar, 4096);
-            bulk_load(ring0 + slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
-          }
-        }
+        if (p.L > 0) break;   // adapter stages follow: their list is not known yet
       }
-      if (!ok || *abort_flag) {
-        // copies issued but not waited for by anyone still land in this CTA
-        for (int i = max(0, it - S); i < it; ++i)
-          tile_wait_final(smem_u32(&sh.full[i % S]), (i / S) & 1);
+      pdl_wait();
+    }
+    while (ok && walk.next(sg)) {
+      const int nb = uniform(sg.nb), row0 = uniform(sg.row0), kb1 = uniform(sg.kb1);
+      const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg.e)) * p.NB + nb) * w_rows;
+      for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
+        const uint32_t nk = min(KD, kb1 - kb);
+        const uint32_t st = ring0 + ring.slot * stage_bytes, bar = full0 + ring.slot * 8;
+        if (it >= early) {
+          ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                              p.err);
+          if (!ok) break;
+        }
+        if (elect_one()) {
+          if (it >= early) {
+            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
+            bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
+                      nk * kTileWBytes, bar);
+          }
+          tma_load_3d(st, &map_x, bar, 0, row0, kb);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      const int na = uniform(adapters_of(p, sg));
+      const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
+      for (int i = 0; i < na && ok; ++i) {
+        const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb) *
+                                        p.rank16) * 4096;
+        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+          ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                              p.err);
+          if (!ok) break;
+          const uint32_t bar = full0 + ring.slot * 8;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, 4096);
+            bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
+          }
+          __syncwarp();
+        }
       }
     }
+    if (!ok || *abort_flag) {
+      // copies issued but not waited for by anyone still land in this CTA
+      for (int i = max(0, it - S); i < it; ++i)
+        tile_wait_final(smem_u32(&sh.full[i % S]), (i / S) & 1);
+    }
   } else if (warp == 1) {
-    // ---- MMAs: one thread --------------------------------------------------
+    // ---- MMAs: one elected lane of a warp that runs in step ------------------
     pdl_wait();
-    if (lane == 0) {
-      Walk walk(p, prefix, tiles);
-      Seg sg;
-      Ring ring;
-      int it = 0, ac = 0;
-      bool ok = true;
-      const int chunk = chunk_stages_of(p);
-      while (ok && walk.next(sg)) {
-        const uint32_t n16 = (sg.rows + 15) & ~15;
-        const uint32_t idesc = idesc_f16(n16);
-        const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
-        int kb = sg.kb0;
-        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
-          const int buf = ac & 1;
-          ok = tile_wait(smem_u32(&sh.acc_empty[buf]), ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc,
-                         p.err);
+    Walk walk(p, prefix, tiles);
+    Seg sg;
+    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t ready0 = smem_u32(&sh.ready[0]);
+    const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
+    const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * kAccCols;
+    const uint64_t desc0 = sw128_kmajor_desc(0);
+    Ring ring;
+    int it = 0, ac = 0;
+    bool ok = true;
+    const int chunk = uniform(chunk_stages_of(p));
+    while (ok && walk.next(sg)) {
+      const uint32_t n16 = uniform((sg.rows + 15) & ~15);
+      const uint32_t idesc = idesc_f16(n16);
+      int kb = uniform(sg.kb0);
+      const int kb1 = uniform(sg.kb1);
+      const int stages = (kb1 - kb + KD - 1) / KD;
+      for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
+        const uint32_t buf = ac & 1;
+        ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = d0 + buf * kAccCols;
+        const int c1 = min(stages, c0 + chunk);
+        for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
+          const uint32_t as = it & (NA - 1);
+          ok = tile_wait_warp(full0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing, p.err) &&
+               tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand, p.err);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + buf * kAccCols;
-          uint32_t accumulate = 0;
-          const int c1 = min(stages, c0 + chunk);
-          for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
-            const int slot = ring.slot, as = it & (NA - 1);
-            ok = tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag, kErrTileRing,
-                           p.err) &&
-                 tile_wait(smem_u32(&sh.ready[as]), (it >> NAb) & 1, abort_flag, kErrTileOperand,
-                           p.err);
-            if (!ok) break;
-            tc_fence_after();
-            const int nk = min(KD, sg.kb1 - kb);
-            for (int k = 0; k < nk; ++k) {
-              const uint64_t b = sw128_kmajor_desc(ring0 + slot * stage_bytes + k * tok_bytes);
-              const uint32_t a = a_base + (as * KD + k) * 32;
+          const uint32_t st = ring0 + ring.slot * stage_bytes;
+          const bool two = KD == 2 && kb + 1 < kb1;
+          if (elect_one()) {
+            const uint64_t b = desc0 + (st >> 4);
+            const uint32_t a = a0 + as * KD * 32;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                umma_f16_ta(d, a + j * 8, b + j * 2, idesc, accumulate);
-                accumulate = 1;
-              }
-            }
-            umma_commit(smem_u32(&sh.empty[slot]));
-          }
-          if (!ok) break;
-          umma_commit(smem_u32(&sh.acc_full[buf]));
-        }
-        const int na = ok ? adapters_of(p, sg) : 0;
-        if (na > 0) {
-          const int buf = ac & 1;
-          ok = tile_wait(smem_u32(&sh.acc_empty[buf]), ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc,
-                         p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + buf * kAccCols;
-          const uint32_t id32 = idesc_tf32(n16);
-          uint32_t accumulate = 0;
-          for (int i = 0; i < na * p.rank16; ++i, ++it, ring.advance(S)) {
-            const int slot = ring.slot, as = it & (NA - 1);
-            ok = tile_wait(smem_u32(&sh.ready[as]), (it >> NAb) & 1, abort_flag, kErrTileOperand,
-                           p.err);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = sw128_kmajor_desc(ring0 + slot * stage_bytes);
-            const uint32_t a = a_base + as * KD * 32;
+            for (int j = 0; j < 4; ++j) umma_f16_ta(d, a + j * 8, b + j * 2, idesc, s > c0 || j > 0);
+            if (two) {
+              const uint64_t b1 = b + (tok_bytes >> 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {   // h's leading terms, then its trailing ones
-              umma_tf32_ta(d, a + (j & 1) * 8, b + j * 2, id32, accumulate);
-              accumulate = 1;
+              for (int j = 0; j < 4; ++j) umma_f16_ta(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
             }
-            umma_commit(smem_u32(&sh.empty[slot]));
+            umma_commit(empty0 + ring.slot * 8);
+            if (s + 1 == c1) umma_commit(accf0 + buf * 8);
           }
-          if (!ok) break;
-          umma_commit(smem_u32(&sh.acc_full[buf]));
-          ++ac;
+          __syncwarp();
         }
       }
-      if (!ok || *abort_flag) {
+      const int na = ok ? uniform(adapters_of(p, sg)) : 0;
+      if (na > 0) {
+        const uint32_t buf = ac & 1;
+        ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = d0 + buf * kAccCols;
+        const uint32_t id32 = idesc_tf32(n16);
+        const int total = na * p.rank16;
+        for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
+          const uint32_t as = it & (NA - 1);
+          ok = tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t b = desc0 + ((ring0 + ring.slot * stage_bytes) >> 4);
+            const uint32_t a = a0 + as * KD * 32;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // h's leading terms, then its trailing ones
+              umma_tf32_ta(d, a + (j & 1) * 8, b + j * 2, id32, i > 0 || j > 0);
+            umma_commit(empty0 + ring.slot * 8);
+            if (i + 1 == total) umma_commit(accf0 + buf * 8);
+          }
+          __syncwarp();
+        }
+        ++ac;
+      }
+    }
+    if (!ok || *abort_flag) {
+      if (elect_one()) {
         umma_commit(smem_u32(&sh.drain));
         tile_wait_final(smem_u32(&sh.drain), 0);
       }
+      __syncwarp();
     }
   } else if (warp >= kFirstConv && warp < kFirstEpi) {
     // ---- A operand: shared memory -> f16 -> TMEM ---------------------------
