@@ -113,6 +113,19 @@ __device__ __forceinline__ uint32_t idesc_tf32(uint32_t n) {
 // Bounded waits: about one second, then the CTA's abort flag and the library's
 // device error word are set and every role winds down.
 // ---------------------------------------------------------------------------
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 constexpr uint64_t kTileWaitNs = 1000ull * 1000ull * 1000ull;
 
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity,

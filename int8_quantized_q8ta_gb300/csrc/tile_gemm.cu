@@ -59,8 +59,9 @@ constexpr int kFirstEpi = kFirstConv + kConvWarps;
 constexpr int kEpiWarps = kTileEpiWarps;
 constexpr int kTileThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kMaxCols = 64;            // accumulator columns of one epilogue warp
-// TMEM: two accumulators of 192 columns, then 128 columns of A operands
-constexpr int kAccCols = kMaxTileRows;
+// TMEM: two accumulators of TN columns, then four stages of A operands, 32
+// columns a k-block (TN <= 64 with two k-blocks a stage: 128 + 256; TN <= 192
+// with one: 384 + 128)
 constexpr int kTmemCols = 512;
 static_assert(kMaxCols * kEpiWarps / 4 == kMaxTileRows, "a third of a tile per epilogue warp");
 
@@ -223,10 +224,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ TileShared sh;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t ring0 = (smem_u32(dyn) + 1023u) & ~1023u;
-  const int KD = p.KD, S = p.stages, NAb = KD == 2 ? 1 : 2, NA = 1 << NAb;
+  const int KD = p.KD, S = p.stages;
   const uint32_t tok_bytes = static_cast<uint32_t>(p.TN) * 128u;
   const uint32_t stage_bytes = static_cast<uint32_t>(KD) * (tok_bytes + kTileWBytes);
-  // NA = 4 / KD stages of A operands fit their 128 TMEM columns
+  // two accumulators at 0 and acc_cols, then the A operands of NA = 4 stages
+  const uint32_t acc_cols = p.TN;
+  constexpr int NAb = 2, NA = 1 << NAb;
   int32_t* prefix = p.offsets != nullptr
                         ? reinterpret_cast<int32_t*>(dyn + (ring0 - smem_u32(dyn)) +
                                                      static_cast<size_t>(S) * stage_bytes)
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t a_base = tmem + 2 * kAccCols;
+  const uint32_t a_base = tmem + 2 * acc_cols;
   volatile uint32_t* abort_flag = &sh.abort;
   const int tiles = sh.tiles;
 
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t ready0 = smem_u32(&sh.ready[0]);
     const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
-    const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * kAccCols;
+    const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * acc_cols;
     const uint64_t desc0 = sw128_kmajor_desc(0);
     Ring ring;
     int it = 0, ac = 0;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = d0 + buf * kAccCols;
+        const uint32_t d = d0 + buf * acc_cols;
         const int c1 = min(stages, c0 + chunk);
         for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
           const uint32_t as = it & (NA - 1);
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = d0 + buf * kAccCols;
+        const uint32_t d = d0 + buf * acc_cols;
         const uint32_t id32 = idesc_tf32(n16);
         const int total = na * p.rank16;
         for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
@@ -464,36 +467,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       used.advance(S);
       return free;
     };
+    // A stage is announced once its stores have landed; the wait for them is
+    // put behind the next stage's loads and conversions, where it is over.
+    int pending = -1;
+    const auto announce = [&]() {
+      if (pending < 0) return;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[pending]));
+      pending = -1;
+    };
+    const auto convert = [&](uint32_t w, uint32_t (&r)[32]) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = lds128(w + c * 2048);
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
+          r[c * 8 + j * 2 + 1] = biased_to_f16x2(q[j], 0x4342, minus);
+        }
+      }
+    };
     while (ok && walk.next(sg)) {
       for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it, ring.advance(S)) {
-        const int slot = ring.slot, as = it & (NA - 1);
-        ok = place_free() && tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag,
-                                       kErrTileRing, p.err);
+        const int as = it & (NA - 1);
+        const uint32_t full = smem_u32(&sh.full[ring.slot]);
+        if (!__all_sync(0xffffffffu, mbar_test(full, ring.phase))) announce();
+        ok = tile_wait(full, ring.phase, abort_flag, kErrTileRing, p.err) && place_free();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int nk = min(KD, sg.kb1 - kb);
-        for (int k = 0; k < nk; ++k) {
-          const uint32_t w = ring0 + slot * stage_bytes + KD * tok_bytes + k * kTileWBytes +
-                             row * 16;
-          uint32_t r[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 v = lds128(w + c * 2048);
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
-              r[c * 8 + j * 2 + 1] = biased_to_f16x2(q[j], 0x4342, minus);
-            }
-          }
-          tmem_st_32cols(a_lane + (as * KD + k) * 32, r);
+        const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
+        uint32_t r[32];
+        convert(w, r);
+        announce();
+        tmem_st_32cols(a_lane + as * KD * 32, r);
+        if (KD == 2 && kb + 1 < sg.kb1) {
+          convert(w + kTileWBytes, r);
+          tmem_st_32cols(a_lane + as * KD * 32 + 32, r);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.ready[as]));
+        pending = as;
       }
+      announce();
       if (!ok) break;
       const int na = adapters_of(p, sg);
       const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
@@ -502,8 +519,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int a_id = __ldg(list + i);
         for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
           const int slot = ring.slot, as = it & (NA - 1);
-          ok = place_free() && tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag,
-                                         kErrTileRing, p.err);
+          ok = tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag, kErrTileRing, p.err) &&
+               place_free();
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int b = 0; b < kMaxCols / 16; ++b)
           if (b * 16 < mine) {
             uint32_t r[16];
-            tmem_ld_16cols(lane_addr + buf * kAccCols + b * 16, r);
+            tmem_ld_16cols(lane_addr + buf * acc_cols + b * 16, r);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[b * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
@@ -627,7 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 16; ++j) part[(col0 + b * 16 + j) * 128] = acc[b * 16 + j];
             if (has_d) {
               uint32_t r[16];
-              tmem_ld_16cols(lane_addr + dbuf * kAccCols + b * 16, r);
+              tmem_ld_16cols(lane_addr + dbuf * acc_cols + b * 16, r);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 16; ++j) d[j] = 0.0f;
             if (has_d) {
               uint32_t r[16];
-              tmem_ld_16cols(lane_addr + dbuf * kAccCols + b * 16, r);
+              tmem_ld_16cols(lane_addr + dbuf * acc_cols + b * 16, r);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) d[j] = __uint_as_float(r[j]);
