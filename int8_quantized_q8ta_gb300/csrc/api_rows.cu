@@ -43,13 +43,20 @@ struct TilePlan {
   size_t operand, parts, counts, total;
 };
 
-TilePlan plan_tiles(int64_t R, int64_t K, int64_t E) {
+// Adapters row by row in the epilogue, or by MMAs per adapter and tile.  Row
+// by row costs a tile rows * r multiply-adds a channel, hidden behind the
+// unit's weights while rows are few; an MMA stage per adapter costs the same
+// however few rows it has.
+constexpr int kRowsPerAdapter = 12;
+bool lora_by_row(int64_t M, int64_t L) { return M < kRowsPerAdapter * L; }
+
+TilePlan plan_tiles(int64_t R, int64_t K, int64_t E, int64_t max_rows = q8::kMaxTileRows) {
   TilePlan t{};
   // tiles hold twice the average group, so that few groups need a second one
   // (which reads the weights again)
   const int64_t groups = std::min(E, R), avg = (R + groups - 1) / groups;
   const int64_t want = E == 1 ? avg : 2 * avg;
-  t.TN = static_cast<int>(std::min<int64_t>(q8::kMaxTileRows, q8::round_up(want, 16)));
+  t.TN = static_cast<int>(std::min<int64_t>(max_rows, q8::round_up(want, 16)));
   t.KD = t.TN <= 64 ? 2 : 1;
   t.grid = q8::device_sm_count();
   t.operand = q8::align_ws(static_cast<size_t>(R) * q8::round_up(K, q8::kTileK) * 2);
@@ -90,7 +97,7 @@ struct LoraSpace {
 };
 LoraSpace lora_space(int64_t M, int64_t K, int64_t L, int64_t r) {
   LoraSpace t{};
-  t.plan = plan_tiles(M, K, 1);
+  t.plan = plan_tiles(M, K, 1, lora_by_row(M, L) ? 128 : q8::kMaxTileRows);
   const int64_t tiles = (M + t.plan.TN - 1) / t.plan.TN;
   t.h = t.plan.total;
   t.lists = t.h + q8::align_ws(static_cast<size_t>(M) * ((r + 15) / 16) * 64);
@@ -384,6 +391,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   p.L = static_cast<int>(L);
   p.rank16 = static_cast<int>((r + 15) / 16);
   p.lora_f16 = lora_dtype == Q8_F16;
+  p.by_row = lora_by_row(M, L);
   p.lora_b = lora;
   p.h = reinterpret_cast<const float*>(ws + sp.h);
   p.lists = reinterpret_cast<const int32_t*>(ws + sp.lists);

@@ -75,6 +75,7 @@ struct TileShared {
   uint32_t tmem;
   uint32_t abort;
   int32_t tiles;          // row tiles of all groups
+  alignas(16) float corner[kEpiWarps][8][16];   // h of the rows a warp is at
 };
 
 // Ring stages per exact f32 chunk.
@@ -190,9 +191,72 @@ struct Ring {
   }
 };
 
+// Adapters of the unit's rows, where this run holds the unit's end and MMAs
+// take them.
 __device__ __forceinline__ int adapters_of(const TileParams& p, const Seg& s) {
-  return (p.L > 0 && s.kb1 == p.KB) ? __ldg(p.lists + static_cast<int64_t>(s.tile) * p.list_stride)
-                                    : 0;
+  return (p.L > 0 && !p.by_row && s.kb1 == p.KB)
+             ? __ldg(p.lists + static_cast<int64_t>(s.tile) * p.list_stride)
+             : 0;
+}
+
+// sum_j h[s, j] B[a(s)][n, j] for one channel and 8 rows a call, by a whole
+// warp: lane u < 8 holds row u's index my_s and adapter my_a (out of range:
+// none).  B comes from global memory, 16 bytes a thread; the rows' h, 16
+// ranks at a time, through the warp's corner of shared memory, from where all
+// lanes read the same words.  row: the channel's place among its block's 128.
+__device__ __forceinline__ void row_deltas(const TileParams& p, int nb, int row, int my_a, int my_s,
+                                           float (*corner)[16], float (&d)[8]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t have = 0;
+  int64_t at[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int a = __shfl_sync(0xffffffffu, my_a, u);
+    const bool in = a >= 0 && a < p.L;
+    have |= static_cast<uint32_t>(in) << u;
+    at[u] = (static_cast<int64_t>(in ? a : 0) * p.NB + nb) * p.rank16 * 4096 + row * 16;
+    d[u] = 0.0f;
+  }
+  // this lane's quarter of 16 ranks of row lane / 4 (rows without an adapter
+  // have no h)
+  const bool h_in = (have >> (lane >> 2)) & 1;
+  const float4* h = reinterpret_cast<const float4*>(
+      p.h + static_cast<int64_t>(__shfl_sync(0xffffffffu, my_s, lane >> 2)) * p.rank16 * 16);
+  for (int c = 0; c < p.rank16; ++c) {
+    const float4 hv = h_in ? __ldg(h + c * 4 + (lane & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    uint4 v[8][2];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        v[u][g] = (have >> u) & 1 ? __ldg(reinterpret_cast<const uint4*>(
+                                        p.lora_b + at[u] + c * 4096 + g * 2048))
+                                  : make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    *reinterpret_cast<float4*>(&corner[lane >> 2][(lane & 3) * 4]) = hv;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float4 h0 = *reinterpret_cast<const float4*>(&corner[u][g * 8]);
+        const float4 h1 = *reinterpret_cast<const float4*>(&corner[u][g * 8 + 4]);
+        const uint32_t q[4] = {v[u][g].x, v[u][g].y, v[u][g].z, v[u][g].w};
+        const float f[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 w;
+          if (p.lora_f16) {
+            w = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+          } else {
+            w.x = __uint_as_float(q[j] << 16);
+            w.y = __uint_as_float(q[j] & 0xffff0000u);
+          }
+          d[u] = fmaf(f[j * 2], w.x, d[u]);
+          d[u] = fmaf(f[j * 2 + 1], w.y, d[u]);
+        }
+      }
+  }
 }
 
 // v of one accumulator, in the order of the header's epilogue.
@@ -313,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           __syncwarp();
         }
-        if (p.L > 0) break;   // adapter stages follow: their list is not known yet
+        if (p.L > 0 && !p.by_row) break;   // adapter stages follow, not known yet
       }
       pdl_wait();
     }
@@ -413,7 +477,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           __syncwarp();
         }
       }
-      const int na = ok ? uniform(adapters_of(p, sg)) : 0;
+      if (!ok) break;
+      const int na = uniform(adapters_of(p, sg));
       if (na > 0) {
         const uint32_t buf = ac & 1;
         ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
@@ -591,6 +656,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     while (ok && walk.next(sg)) {
       const int mine = max(0, min(cols, sg.rows - col0));    // columns with a row behind them
       const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
+      // Few rows an adapter: each row's own dot products, put into TMEM columns
+      // of their own while the unit's MMAs run
+      const bool by_row = p.by_row && sg.kb1 == p.KB;
+      if (by_row) {
+        for (int j = 0; j < mine; j += 8) {
+          // (rows past the tile's end repeat its last)
+          const int my_s = sg.row0 + min(col0 + j + (lane & 7), sg.rows - 1);
+          float d[8];
+          row_deltas(p, sg.nb, quarter * 32 + lane, __ldg(p.ids + my_s), my_s, sh.corner[ew], d);
+          tmem_st_8cols(lane_addr + 2 * acc_cols + NA * KD * 32 + j, d);
+        }
+        tmem_st_wait();
+      }
       int32_t acc[kMaxCols];
 #pragma unroll
       for (int j = 0; j < kMaxCols; ++j) acc[j] = 0;
@@ -615,10 +693,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[buf]));
       }
       if (!ok) break;
-      // the adapters' term stays in TMEM until it is used
-      const bool has_d = adapters_of(p, sg) > 0;
+      // the MMAs' adapter term stays in its accumulator until it is used
+      const bool by_mma = adapters_of(p, sg) > 0;
       const int dbuf = ac & 1;
-      if (has_d) {
+      if (by_mma) {
         ok = __all_sync(0xffffffffu,
                         tile_wait(smem_u32(&sh.acc_full[dbuf]), (ac >> 1) & 1, abort_flag,
                                   kErrTileAcc, p.err));
@@ -626,6 +704,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_after();
         ++ac;
       }
+      const bool has_d = by_row || by_mma;
+      const uint32_t d_addr = lane_addr + (by_row ? 2 * acc_cols + NA * KD * 32 : dbuf * acc_cols);
       bool last = true;
       int first_cta = 0, end_cta = 0;
       if (sg.kb0 != 0 || sg.kb1 != p.KB) {
@@ -644,19 +724,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 16; ++j) part[(col0 + b * 16 + j) * 128] = acc[b * 16 + j];
             if (has_d) {
               uint32_t r[16];
-              tmem_ld_16cols(lane_addr + dbuf * acc_cols + b * 16, r);
+              tmem_ld_16cols(d_addr + b * 16, r);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 dpart[(col0 + b * 16 + j) * 128] = __uint_as_float(r[j]);
             }
           }
-        __threadfence();
+        // release this warp's part, acquire the others'
         __syncwarp();
         int before = 0;
-        if (lane == 0) before = atomicAdd(p.counts + first_cta * kEpiWarps + ew, 1);
+        if (lane == 0) before = atomic_add_acq_rel(p.counts + first_cta * kEpiWarps + ew, 1);
         before = __shfl_sync(0xffffffffu, before, 0);
-        __threadfence();
         last = before == end_cta - first_cta;
       }
       if (last) {
@@ -669,7 +748,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // the unit's adapter term: in this CTA's TMEM, or left by the CTA
         // that ran the unit's end
         const bool unit_d =
-            p.L > 0 && __ldg(p.lists + static_cast<int64_t>(sg.tile) * p.list_stride) > 0;
+            p.L > 0 &&
+            (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg.tile) * p.list_stride) > 0);
         const float* dother = reinterpret_cast<const float*>(p.parts) +
                               (static_cast<int64_t>(end_cta) * 3 + 2) * p.TN * 128 + quarter * 32 + lane;
 #pragma unroll
@@ -691,7 +771,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 16; ++j) d[j] = 0.0f;
             if (has_d) {
               uint32_t r[16];
-              tmem_ld_16cols(lane_addr + dbuf * acc_cols + b * 16, r);
+              tmem_ld_16cols(d_addr + b * 16, r);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) d[j] = __uint_as_float(r[j]);
@@ -709,7 +789,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               }
           }
       }
-      if (has_d) {
+      if (by_mma) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[dbuf]));

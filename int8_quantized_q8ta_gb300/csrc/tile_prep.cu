@@ -285,13 +285,15 @@ __global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob
       for (int i = 0; i < n; i += kFrontRows)
         front_rows<F16>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i), vec);
     } else {
-      const int hi = min(R, (w + 1) * kFrontRows);
-      for (int s = w * kFrontRows; s < hi;) {
-        const int a = adapter_of(job, s);
-        int e = s + 1;
-        while (e < hi && adapter_of(job, e) == a) ++e;
-        if (a >= 0) front_rows<F16>(job, sh, cluster, a, c, nullptr, s, e - s, vec);
-        s = e;
+      // the runs among the window's 32 rows, found by every warp for itself
+      const int s0 = w * kFrontRows, n = min(kFrontRows, R - s0), lane = threadIdx.x & 31;
+      const int mine = lane < n ? adapter_of(job, s0 + lane) : -2;
+      for (int i = 0; i < n;) {
+        const int a = __shfl_sync(0xffffffffu, mine, i);
+        const uint32_t other = __ballot_sync(0xffffffffu, mine != a) & (0xffffffffu << i);
+        const int e = other != 0 ? __ffs(other) - 1 : 32;
+        if (a >= 0) front_rows<F16>(job, sh, cluster, a, c, nullptr, s0 + i, e - i, vec);
+        i = e;
       }
     }
     return;

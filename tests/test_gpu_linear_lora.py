@@ -145,6 +145,17 @@ def test_output_types_and_relu(M, out_dtype):
            out_dtype, act="relu")
 
 
+# Many units for each CTA one after the other, so that the two accumulators
+# take turns between sums and adapter terms in every order: few rows an
+# adapter, many, none, and tiles of both kinds side by side
+@pytest.mark.parametrize("M,N,K,L,ids,bare", [
+    (20, 40000, 64, 20, "random", 0.3), (48, 36000, 320, 2, "random", 0.0),
+    (130, 20000, 192, 1, "one", 0.0), (500, 8192, 128, 60, "random", 0.1),
+    (900, 6000, 64, 5, "runs", 0.5), (400, 8192, 704, 3, "random", 0.9)])
+def test_many_units_in_a_row(M, N, K, L, ids, bare):
+    _check(Problem(M + L, M, N, K, L, 16, torch.float16, zp=3, ids=ids, bare=bare))
+
+
 @pytest.mark.parametrize("ids", ["runs", "one"])
 @pytest.mark.parametrize("M", [20, 150, 450])
 def test_runs_of_one_adapter(M, ids):
