@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job,
 
 // ---------------------------------------------------------------------------
 // Adapters: h[s, j] = s_in * scaling[a] * sum_k (x[row(s), k] - zp) A[a][j, k]
-// for the rows with an adapter.  A cluster of 8 CTAs takes 16 ranks of one
-// adapter and up to 32 of its rows at a time; its 64 warps split K in steps of
-// 32 and multiply with m16n8k16 MMAs, ranks on M and rows on N.  The sum over
+// for the rows with an adapter.  A CTA, or a cluster of 8 while there are few,
+// takes 16 ranks of one adapter and up to 32 of its rows at a time; its warps
+// split K in steps of 32 and multiply with m16n8k16 MMAs, ranks on M and rows on N.  The sum over
 // k may take any order, so a thread's fragments are 8 consecutive inputs: one
 // 16-byte load of A and one 8-byte load of x per row, no shared memory.  The
 // warps' f32 sums are added in a fixed order, first in the CTA, then over the
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job,
 // runs inside 32 of them.
 // ---------------------------------------------------------------------------
 constexpr int kFrontThreads = 256;
-constexpr int kFrontCluster = 8;
+constexpr int kFrontCluster = 8;   // CTAs that share one unit's K while units are few
 constexpr int kFrontRows = 32;
 
 template <bool F16>
@@ -178,11 +178,11 @@ __device__ __forceinline__ void load_x8(const LoraJob& job, int64_t row, int k0,
 }
 
 // 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
-template <bool F16>
+template <bool F16, int CL>
 __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
                            int c, const int32_t* rows, int row0, int count, bool vec) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rank = cluster.block_rank();
+  const int rank = CL > 1 ? cluster.block_rank() : 0;
   const int Kp = job.op.KB * 64;
   const uint16_t* A = job.a + (static_cast<int64_t>(a) * job.rank16 + c) * 16 * Kp;
   float acc[4][4] = {};
@@ -199,7 +199,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
   }
 #pragma unroll 2
   for (int k0 = (rank * (kFrontThreads / 32) + warp) * 32 + t * 8; k0 < Kp;
-       k0 += kFrontCluster * kFrontThreads) {
+       k0 += CL * kFrontThreads) {
     const uint4 lo = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g) * Kp + k0));
     const uint4 hi =
         __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g + 8) * Kp + k0));
@@ -224,20 +224,25 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
     for (int w = 0; w < kFrontThreads / 32; ++w) v += sh.part[w][i / kFrontRows][i % kFrontRows];
     sh.sum[i / kFrontRows][i % kFrontRows] = v;
   }
-  cluster.sync();
-  if (threadIdx.x < 16 * kFrontRows / kFrontCluster) {
-    // this CTA's 4 rows of the 32, 16 ranks each
-    const int j = threadIdx.x & 15, i = rank * (kFrontRows / kFrontCluster) + (threadIdx.x >> 4);
+  if constexpr (CL > 1) cluster.sync(); else __syncthreads();
+  // this CTA's share of the rows, 16 ranks each
+  for (int i0 = threadIdx.x; i0 < 16 * kFrontRows / CL; i0 += kFrontThreads) {
+    const int j = i0 & 15, i = rank * (kFrontRows / CL) + (i0 >> 4);
     if (i < count) {
       float v = 0.0f;
+      if constexpr (CL > 1) {
 #pragma unroll
-      for (int r = 0; r < kFrontCluster; ++r) v += *cluster.map_shared_rank(&sh.sum[j][i], r);
+        for (int r = 0; r < CL; ++r) v += *cluster.map_shared_rank(&sh.sum[j][i], r);
+      } else {
+        v = sh.sum[j][i];
+      }
       const int s = rows != nullptr ? rows[i] : row0 + i;
       job.h[static_cast<int64_t>(s) * job.rank16 * 16 + c * 16 + j] =
           v * job.s_in * __ldg(job.scaling + a);
     }
   }
-  cluster.sync();   // the sums may be overwritten now
+  // the sums may be overwritten now
+  if constexpr (CL > 1) cluster.sync(); else __syncthreads();
 }
 
 __device__ __forceinline__ int adapter_of(const LoraJob& job, int s) {
@@ -265,8 +270,8 @@ __device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t*
 
 // Blocks: job.shrink_ctas for h, then one per row tile for its list, the rest
 // for the operand.
-template <bool F16>
-__global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob job, bool vec) {
+template <bool F16, int CL>
+__global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const LoraJob job, bool vec) {
   __shared__ FrontShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob
   const int R = job.op.R;
   int b = blockIdx.x;
   if (b < job.shrink_ctas) {
-    const int u = b / kFrontCluster, c = u % job.rank16, w = u / job.rank16;
+    const int u = b / CL, c = u % job.rank16, w = u / job.rank16;
     if (job.op.order == nullptr) {
       // row w's adapter, if no earlier row has it
       const int a = adapter_of(job, w);
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob
       if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
       const int n = block_compact(sh, same, threadIdx.x, sh.rows);
       for (int i = 0; i < n; i += kFrontRows)
-        front_rows<F16>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i), vec);
+        front_rows<F16, CL>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i), vec);
     } else {
       // the runs among the window's 32 rows, found by every warp for itself
       const int s0 = w * kFrontRows, n = min(kFrontRows, R - s0), lane = threadIdx.x & 31;
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kFrontThreads) lora_front_kernel(const LoraJob
         const int a = __shfl_sync(0xffffffffu, mine, i);
         const uint32_t other = __ballot_sync(0xffffffffu, mine != a) & (0xffffffffu << i);
         const int e = other != 0 ? __ffs(other) - 1 : 32;
-        if (a >= 0) front_rows<F16>(job, sh, cluster, a, c, nullptr, s0 + i, e - i, vec);
+        if (a >= 0) front_rows<F16, CL>(job, sh, cluster, a, c, nullptr, s0 + i, e - i, vec);
         i = e;
       }
     }
@@ -409,12 +414,19 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
 
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
   const int groups = job.op.order == nullptr ? job.op.R : (job.op.R + kFrontRows - 1) / kFrontRows;
-  job.shrink_ctas = groups * job.rank16 * kFrontCluster;
+  // K is cut over 8 CTAs while the units alone would leave SMs without one
+  const int cl = groups * job.rank16 < 2 * device_sm_count() ? kFrontCluster : 1;
+  job.shrink_ctas = groups * job.rank16 * cl;
   const int copy = blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
                                                 job.op.count_words));
-  const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, kFrontCluster));
-  return launch_pdl_cluster(f16 ? lora_front_kernel<true> : lora_front_kernel<false>, grid,
-                            kFrontThreads, 0, kFrontCluster, s, job, rows_vec8(job.op));
+  const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, cl));
+  const bool vec = rows_vec8(job.op);
+  if (cl == 1)
+    return launch_pdl(f16 ? lora_front_kernel<true, 1> : lora_front_kernel<false, 1>, grid,
+                      kFrontThreads, 0, s, job, vec);
+  return launch_pdl_cluster(
+      f16 ? lora_front_kernel<true, kFrontCluster> : lora_front_kernel<false, kFrontCluster>, grid,
+      kFrontThreads, 0, kFrontCluster, s, job, vec);
 }
 
 }  // namespace q8
