@@ -37,9 +37,9 @@ bool tile_sizes_ok(int64_t E, int64_t N, int64_t K) {
          K <= INT32_MAX / 2 && mul_ok(N, K) && mul_ok(E, N * K) && E * N * K <= INT64_MAX / 64;
 }
 
-// Tile height, ring layout and grid of a problem of R rows in E groups.
+// Tile height and grid of a problem of R rows in E groups.
 struct TilePlan {
-  int TN, KD, grid;
+  int TN, grid;
   size_t operand, parts, counts, total;
 };
 
@@ -57,10 +57,9 @@ TilePlan plan_tiles(int64_t R, int64_t K, int64_t E, int64_t max_rows = q8::kMax
   const int64_t groups = std::min(E, R), avg = (R + groups - 1) / groups;
   const int64_t want = E == 1 ? avg : 2 * avg;
   t.TN = static_cast<int>(std::min<int64_t>(max_rows, q8::round_up(want, 16)));
-  t.KD = t.TN <= 64 ? 2 : 1;
   t.grid = q8::device_sm_count();
   t.operand = q8::align_ws(static_cast<size_t>(R) * q8::round_up(K, q8::kTileK) * 2);
-  t.parts = q8::align_ws(static_cast<size_t>(t.grid) * 3 * t.TN * 512);
+  t.parts = q8::align_ws(static_cast<size_t>(t.grid) * 3 * q8::kTilePartWords * 4);
   t.counts = q8::align_ws(static_cast<size_t>(t.grid) * q8::kTileEpiWarps * 4);
   t.total = t.operand + t.parts + t.counts;
   return t;
@@ -273,7 +272,6 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
   p.E = static_cast<int>(E);
   p.offsets = offsets;
   p.TN = plan.TN;
-  p.KD = plan.KD;
   p.grid = plan.grid;
   p.min_run = 4;
   p.w = static_cast<const uint8_t*>(packed_weight);
@@ -375,7 +373,6 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   p.KB = static_cast<int>((K + 63) / 64);
   p.E = 1;
   p.TN = sp.plan.TN;
-  p.KD = sp.plan.KD;
   p.grid = sp.plan.grid;
   p.min_run = 4;
   p.w = static_cast<const uint8_t*>(packed_weight);

@@ -79,7 +79,8 @@ cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt
 
 // ---- grouped int8 contraction (tile_gemm.cu, tile_prep.cu) -----------------
 constexpr int kMaxTileRows = 192;       // rows of one tile: two accumulators fit TMEM
-constexpr int kTileEpiWarps = 12;
+constexpr int kTileEpiWarps = 12;       // epilogue warps at most
+constexpr int kTilePartWords = kMaxTileRows * 128;   // int32 words of one CTA's part of a unit
 constexpr int kTileSmem = 218 * 1024;   // beside it some 7 KB of static shared memory
 constexpr int kMaxRank = 256;
 
@@ -94,7 +95,6 @@ struct TileParams {
   int E;                    // groups
   const int32_t* offsets;   // [E + 1] group bounds on the device, or null: one group of R rows
   int TN;                   // rows of a tile at most (a multiple of 16)
-  int KD;                   // k-blocks per ring stage: 1 or 2
   int stages;               // ring stages (set by the launcher)
   int grid, min_run;        // CTAs; k-blocks a CTA's run holds at least
   const uint8_t* w;         // packed weights (see launch_pack_tile_weight)
@@ -107,7 +107,7 @@ struct TileParams {
   void* out;
   const int32_t* out_rows;  // output row of each row, or null
   uint32_t* err;
-  int32_t* parts;           // [grid][3][TN][128]: parts of units cut by a run's end
+  int32_t* parts;           // [grid][3][words]: parts of units cut by a run's end
   int32_t* counts;          // [grid][kTileEpiWarps], zeroed by the kernel before
   // adapters (L == 0: none)
   int L, rank16, lora_f16;  // adapters, blocks of 16 ranks, f16 (1) or bf16 (0)

@@ -93,32 +93,64 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, M = 128: f16 inputs (K = 16, A two values
-// per 32-bit column) or tf32 inputs (K = 8, A one value per column), f32 sums.
+// D[tmem] (+)= A[tmem] * B[smem]^T, 128 rows of A a CTA: f16 inputs (K = 16, A
+// two values per 32-bit column) or tf32 inputs (K = 8, A one value per column),
+// f32 sums.  CG 2: the 2-SM MMA of a CTA pair, issued by its leader; each CTA
+// supplies 128 rows of A and half of B's rows from the same places.
+template <int CG>
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
+template <int CG>
 __device__ __forceinline__ void umma_tf32_ta(uint32_t d, uint32_t a, uint64_t b_desc,
                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
-// Instruction descriptors: f32 sums, both operands K-major, M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc_f16(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// Arrive at a barrier once the MMAs issued so far are done: in every CTA of
+// the group, or in this one alone.
+template <int CG>
+__device__ __forceinline__ void umma_commit_all(uint32_t bar) {
+  if constexpr (CG == 1) umma_commit(bar);
+  else umma_commit_pair(bar, 0x3);
 }
-__device__ __forceinline__ uint32_t idesc_tf32(uint32_t n) {
-  return (1u << 4) | (2u << 7) | (2u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+template <int CG>
+__device__ __forceinline__ void umma_commit_own(uint32_t bar) {
+  if constexpr (CG == 1) umma_commit(bar);
+  else umma_commit_pair(bar, 0x1);
+}
+// Instruction descriptors: f32 sums, both operands K-major, M = m, N = n.
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t m, uint32_t n) {
+  return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_tf32(uint32_t m, uint32_t n) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // ---------------------------------------------------------------------------

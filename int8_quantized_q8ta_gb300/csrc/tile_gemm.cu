@@ -53,36 +53,58 @@ enum : uint32_t { kErrTileRing = 0x10A, kErrTileAcc = 0x10B, kErrTileOperand = 0
 
 constexpr int kMaxRing = 12;
 constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
-constexpr int kConvWarps = 4;
 constexpr int kFirstConv = 4;           // warps 0 and 1: copies, MMAs; 2 and 3 idle
-constexpr int kFirstEpi = kFirstConv + kConvWarps;
-constexpr int kEpiWarps = kTileEpiWarps;
-constexpr int kTileThreads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kMaxCols = 64;            // accumulator columns of one epilogue warp
-// TMEM: two accumulators of TN columns, then four stages of A operands, 32
-// columns a k-block (TN <= 64 with two k-blocks a stage: 128 + 256; TN <= 192
-// with one: 384 + 128)
+constexpr int kTileThreads = 640;
 constexpr int kTmemCols = 512;
-static_assert(kMaxCols * kEpiWarps / 4 == kMaxTileRows, "a third of a tile per epilogue warp");
+// Stages of A operands in tensor memory, behind the two accumulators.
+constexpr int NAb = 2, NA = 1 << NAb;
+
+// The two forms of the kernel.
+//   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
+// a tile through the 2-SM MMA, each with its own 128 output channels and half
+// of the rows in its shared memory.  What bounds long batches is the bytes an
+// SM can pull from L2 (some 47 a cycle measured here): 12 KB of tokens and
+// 8 KB of weights for 384 cycles of MMAs, where one CTA alone needs 32 KB.
+//   Narrow (up to 64 rows): one CTA; two k-blocks a stage and twice the
+// converting warps, since the weights' way through them is what such tiles
+// wait for once memory is busy.
+template <bool PAIR>
+struct Form {
+  static constexpr int CG = PAIR ? 2 : 1;
+  static constexpr int KD = PAIR ? 1 : 2;          // k-blocks a stage
+  static constexpr int kConv = PAIR ? 4 : 8;       // converting warps
+  static constexpr int kGroups = kConv / 4;        // groups of four take turns
+  static constexpr int kEpi = PAIR ? 12 : 8;       // epilogue warps
+  static constexpr int kCols = PAIR ? 64 : 32;     // accumulator columns of each
+  static constexpr int kFirstEpi = kFirstConv + kConv;
+  static_assert(32 * (kFirstEpi + kEpi) == kTileThreads, "one block size");
+  static constexpr int kMaxRows = kCols * kEpi / 4;
+  // int32 words of one CTA's part of a unit
+  static constexpr int kPart = kEpi * kCols * 32;
+  static_assert(kPart <= kTilePartWords, "workspace");
+  static_assert(kEpi <= kTileEpiWarps, "workspace");
+};
 
 struct TileShared {
-  uint64_t full[kMaxRing];
-  uint64_t empty[kMaxRing];
-  uint64_t ready[4];      // A operand in TMEM (and, for adapters, B in shared memory)
+  uint64_t wfull[kMaxRing];   // weights of a stage have landed
+  uint64_t tfull[kMaxRing];   // tokens of a stage have landed (in a pair: both halves, at the leader)
+  uint64_t empty[kMaxRing];   // a stage's MMAs are done
+  uint64_t ready[NA];         // A operand in TMEM (and, for adapters, B in shared memory)
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
   uint32_t abort;
-  int32_t tiles;          // row tiles of all groups
-  alignas(16) float corner[kEpiWarps][8][16];   // h of the rows a warp is at
+  int32_t tiles;              // row tiles of all groups
+  alignas(16) float corner[kTileEpiWarps][8][16];   // h of the rows a warp is at
 };
 
 // Ring stages per exact f32 chunk.
+template <int KD>
 __device__ __forceinline__ int chunk_stages_of(const TileParams& p) {
   int wb = __ldg(p.w_bound);
   if (wb < 1 || wb > kWorstWBound) wb = wb < 1 ? 1 : kWorstWBound;
-  return max(1, (1 << 24) / (p.a_bound * wb) / p.KD);
+  return max(1, (1 << 24) / (p.a_bound * wb) / KD);
 }
 
 // One run's part of a unit.
@@ -102,11 +124,13 @@ __device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start
   return max(0, group_end(p, e + 1) - start);
 }
 
-// The CTA's run of the line of all units' k-blocks (32-bit: the host checks),
-// unit by unit.  The divisions that place its start are done once: one integer
+// The CTA's (or pair's) run of the line of all units' k-blocks (32-bit: the
+// host checks), unit by unit; a unit is a row tile times 128 (256) channels.  The divisions that place its start are done once: one integer
 // division by a runtime value takes longer than a k-block's MMAs.
+template <int CG>
 struct Walk {
   const TileParams& p;
+  int NB;                  // blocks of 128 * CG channels
   int q;                   // k-blocks of every run but the last
   int left, unit, kb;      // k-blocks still to take; the unit and where in it
   int e, start, count;     // the unit's group and its rows
@@ -114,11 +138,11 @@ struct Walk {
   int i, nb;               // row tile and output block: tiles of one block follow one another
 
   __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix, int all_tiles)
-      : p(p_) {
-    const int total = all_tiles * p.NB * p.KB;
-    q = max(p.min_run, (total - 1) / static_cast<int>(gridDim.x) + 1);
-    const int pos =
-        static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * blockIdx.x));
+      : p(p_), NB((p_.NB + CG - 1) / CG) {
+    const int total = all_tiles * NB * p.KB;
+    q = max(p.min_run, (total - 1) / static_cast<int>(gridDim.x / CG) + 1);
+    const int pos = static_cast<int>(
+        min(static_cast<int64_t>(total), static_cast<int64_t>(q) * (blockIdx.x / CG)));
     left = min(total - pos, q);
     unit = pos / p.KB;
     kb = pos - unit * p.KB;
@@ -133,14 +157,14 @@ struct Walk {
       int lo = 0, hi = p.E - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] * p.NB <= unit) lo = mid; else hi = mid - 1;
+        if (prefix[mid] * NB <= unit) lo = mid; else hi = mid - 1;
       }
       e = lo;
       t0 = prefix[lo];
       count = group_rows(p, e, start);
     }
     cut();
-    const int local = unit - t0 * p.NB;
+    const int local = unit - t0 * NB;
     nb = local / tiles;
     i = local - nb * tiles;
   }
@@ -164,7 +188,7 @@ struct Walk {
       ++unit;
       if (++i == tiles) {
         i = 0;
-        if (++nb == p.NB) {
+        if (++nb == NB) {
           nb = 0;
           t0 += tiles;
           do {
@@ -281,19 +305,22 @@ __device__ __forceinline__ void store_out(void* out, int64_t at, float v, const 
   }
 }
 
-template <int OUT>
+// Two halves of a token tile have rows that are multiples of 8.
+template <int OUT, bool PAIR>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const TileParams p) {
+  using F = Form<PAIR>;
+  constexpr int CG = F::CG, KD = F::KD, kCols = F::kCols;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TileShared sh;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool leader = rank == 0;
   const uint32_t ring0 = (smem_u32(dyn) + 1023u) & ~1023u;
-  const int KD = p.KD, S = p.stages;
-  const uint32_t tok_bytes = static_cast<uint32_t>(p.TN) * 128u;
-  const uint32_t stage_bytes = static_cast<uint32_t>(KD) * (tok_bytes + kTileWBytes);
-  // two accumulators at 0 and acc_cols, then the A operands of NA = 4 stages
+  const int S = p.stages;
   const uint32_t acc_cols = p.TN;
-  constexpr int NAb = 2, NA = 1 << NAb;
+  const uint32_t tok_bytes = static_cast<uint32_t>(p.TN / CG) * 128u;
+  const uint32_t stage_bytes = static_cast<uint32_t>(KD) * (tok_bytes + kTileWBytes);
   int32_t* prefix = p.offsets != nullptr
                         ? reinterpret_cast<int32_t*>(dyn + (ring0 - smem_u32(dyn)) +
                                                      static_cast<size_t>(S) * stage_bytes)
@@ -301,13 +328,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.wfull[i]), 1);
+      mbar_init(smem_u32(&sh.tfull[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.ready[i]), kConvWarps);
+    for (int i = 0; i < NA; ++i) mbar_init(smem_u32(&sh.ready[i]), 4 * CG);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.acc_full[i]), 1);
-      mbar_init(smem_u32(&sh.acc_empty[i]), kEpiWarps);
+      mbar_init(smem_u32(&sh.acc_empty[i]), F::kEpi * CG);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     fence_mbar_init();
@@ -315,8 +343,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tma_prefetch_desc(&map_x);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&sh.tmem), kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
+      tmem_relinquish();
+    }
   }
   pdl_launch_dependents();
   if (prefix != nullptr) {
@@ -344,6 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();   // the peer's barriers exist before any use
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t a_base = tmem + 2 * acc_cols;
@@ -352,10 +386,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == 0) {
     // ---- copies: one elected lane of a warp that runs in step ----------------
-    Walk walk(p, prefix, tiles);
+    Walk<CG> walk(p, prefix, tiles);
     Seg sg;
     const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
-    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t wfull0 = smem_u32(&sh.wfull[0]), tfull0 = smem_u32(&sh.tfull[0]);
+    const uint32_t empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
     Ring ring;
     int it = 0;
     bool ok = true;
@@ -363,15 +399,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // kernel before this one: a packed weight is written at load time
     int early = 0;
     if (prefix == nullptr) {
-      Walk w2 = walk;
+      Walk<CG> w2 = walk;
       while (early < S && w2.next(sg)) {
-        const uint8_t* w = p.w + uniform(sg.nb) * w_rows;
+        const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
+        const uint8_t* w = p.w + nb * w_rows;
         const int kb1 = uniform(sg.kb1);
         for (int kb = uniform(sg.kb0); kb < kb1 && early < S; kb += KD, ++early) {
           const uint32_t nk = min(KD, kb1 - kb);
-          const uint32_t st = ring0 + early * stage_bytes, bar = full0 + early * 8;
+          const uint32_t st = ring0 + early * stage_bytes, bar = wfull0 + early * 8;
           if (elect_one()) {
-            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
+            mbar_arrive_expect_tx(bar, nk * kTileWBytes);
             bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
                       nk * kTileWBytes, bar);
           }
@@ -382,11 +419,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       pdl_wait();
     }
     while (ok && walk.next(sg)) {
-      const int nb = uniform(sg.nb), row0 = uniform(sg.row0), kb1 = uniform(sg.kb1);
+      // (an odd last block of a pair repeats the one before and stores nothing)
+      const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
+      const int kb1 = uniform(sg.kb1);
+      const int row0 = uniform(sg.row0) + rank * (((uniform(sg.rows) + 15) & ~15) / CG);
       const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg.e)) * p.NB + nb) * w_rows;
       for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
         const uint32_t nk = min(KD, kb1 - kb);
-        const uint32_t st = ring0 + ring.slot * stage_bytes, bar = full0 + ring.slot * 8;
+        const uint32_t st = ring0 + ring.slot * stage_bytes;
         if (it >= early) {
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
@@ -394,11 +434,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (elect_one()) {
           if (it >= early) {
-            mbar_arrive_expect_tx(bar, KD * tok_bytes + nk * kTileWBytes);
+            const uint32_t bar = wfull0 + ring.slot * 8;
+            mbar_arrive_expect_tx(bar, nk * kTileWBytes);
             bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
                       nk * kTileWBytes, bar);
           }
-          tma_load_3d(st, &map_x, bar, 0, row0, kb);
+          if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * KD * tok_bytes);
+          if constexpr (PAIR)
+            tma_load_3d_pair(st, &map_x, tfull_lead + ring.slot * 8, 0, row0, kb);
+          else
+            tma_load_3d(st, &map_x, tfull0 + ring.slot * 8, 0, row0, kb);
         }
         __syncwarp();
       }
@@ -412,10 +457,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
           if (!ok) break;
-          const uint32_t bar = full0 + ring.slot * 8;
+          const uint32_t bar = wfull0 + ring.slot * 8;
           if (elect_one()) {
             mbar_arrive_expect_tx(bar, 4096);
             bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
+            if (leader) mbar_arrive(tfull0 + ring.slot * 8);   // no tokens in this round
           }
           __syncwarp();
         }
@@ -423,131 +469,145 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (!ok || *abort_flag) {
       // copies issued but not waited for by anyone still land in this CTA
-      for (int i = max(0, it - S); i < it; ++i)
-        tile_wait_final(smem_u32(&sh.full[i % S]), (i / S) & 1);
+      for (int i = max(0, it - S); i < it; ++i) {
+        tile_wait_final(smem_u32(&sh.wfull[i % S]), (i / S) & 1);
+        if (leader) tile_wait_final(smem_u32(&sh.tfull[i % S]), (i / S) & 1);
+      }
     }
   } else if (warp == 1) {
     // ---- MMAs: one elected lane of a warp that runs in step ------------------
-    pdl_wait();
-    Walk walk(p, prefix, tiles);
-    Seg sg;
-    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
-    const uint32_t ready0 = smem_u32(&sh.ready[0]);
-    const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
-    const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * acc_cols;
-    const uint64_t desc0 = sw128_kmajor_desc(0);
-    Ring ring;
-    int it = 0, ac = 0;
-    bool ok = true;
-    const int chunk = uniform(chunk_stages_of(p));
-    while (ok && walk.next(sg)) {
-      const uint32_t n16 = uniform((sg.rows + 15) & ~15);
-      const uint32_t idesc = idesc_f16(n16);
-      int kb = uniform(sg.kb0);
-      const int kb1 = uniform(sg.kb1);
-      const int stages = (kb1 - kb + KD - 1) / KD;
-      for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
-        const uint32_t buf = ac & 1;
-        ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = d0 + buf * acc_cols;
-        const int c1 = min(stages, c0 + chunk);
-        for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
-          const uint32_t as = it & (NA - 1);
-          ok = tile_wait_warp(full0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing, p.err) &&
-               tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand, p.err);
+    if (leader) {
+      pdl_wait();
+      Walk<CG> walk(p, prefix, tiles);
+      Seg sg;
+      const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
+      const uint32_t ready0 = smem_u32(&sh.ready[0]);
+      const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
+      const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * acc_cols;
+      const uint64_t desc0 = sw128_kmajor_desc(0);
+      Ring ring;
+      int it = 0, ac = 0;
+      bool ok = true;
+      const int chunk = uniform(chunk_stages_of<KD>(p));
+      while (ok && walk.next(sg)) {
+        const uint32_t n16 = uniform((sg.rows + 15) & ~15);
+        const uint32_t idesc = idesc_f16(128 * CG, n16);
+        int kb = uniform(sg.kb0);
+        const int kb1 = uniform(sg.kb1);
+        const int stages = (kb1 - kb + KD - 1) / KD;
+        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
+          const uint32_t buf = ac & 1;
+          ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = ring0 + ring.slot * stage_bytes;
-          const bool two = KD == 2 && kb + 1 < kb1;
-          if (elect_one()) {
-            const uint64_t b = desc0 + (st >> 4);
-            const uint32_t a = a0 + as * KD * 32;
+          const uint32_t d = d0 + buf * acc_cols;
+          const int c1 = min(stages, c0 + chunk);
+          for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
+            const uint32_t as = it & (NA - 1);
+            ok = tile_wait_warp(tfull0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing,
+                                p.err) &&
+                 tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
+                                p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = ring0 + ring.slot * stage_bytes;
+            const bool two = KD == 2 && kb + 1 < kb1;
+            if (elect_one()) {
+              const uint64_t b = desc0 + (st >> 4);
+              const uint32_t a = a0 + as * KD * 32;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) umma_f16_ta(d, a + j * 8, b + j * 2, idesc, s > c0 || j > 0);
-            if (two) {
-              const uint64_t b1 = b + (tok_bytes >> 4);
+              for (int j = 0; j < 4; ++j)
+                umma_f16_ta<CG>(d, a + j * 8, b + j * 2, idesc, s > c0 || j > 0);
+              if (two) {
+                const uint64_t b1 = b + (tok_bytes >> 4);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) umma_f16_ta(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
+                for (int j = 0; j < 4; ++j) umma_f16_ta<CG>(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
+              }
+              umma_commit_all<CG>(empty0 + ring.slot * 8);
+              if (s + 1 == c1) umma_commit_all<CG>(accf0 + buf * 8);
             }
-            umma_commit(empty0 + ring.slot * 8);
-            if (s + 1 == c1) umma_commit(accf0 + buf * 8);
+            __syncwarp();
           }
-          __syncwarp();
         }
-      }
-      if (!ok) break;
-      const int na = uniform(adapters_of(p, sg));
-      if (na > 0) {
-        const uint32_t buf = ac & 1;
-        ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = d0 + buf * acc_cols;
-        const uint32_t id32 = idesc_tf32(n16);
-        const int total = na * p.rank16;
-        for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
-          const uint32_t as = it & (NA - 1);
-          ok = tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand, p.err);
+        const int na = uniform(adapters_of(p, sg));
+        if (na > 0) {
+          const uint32_t buf = ac & 1;
+          ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint64_t b = desc0 + ((ring0 + ring.slot * stage_bytes) >> 4);
-            const uint32_t a = a0 + as * KD * 32;
+          const uint32_t d = d0 + buf * acc_cols;
+          const uint32_t id32 = idesc_tf32(128 * CG, n16);
+          const int total = na * p.rank16;
+          for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
+            const uint32_t as = it & (NA - 1);
+            ok = tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
+                                p.err);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = desc0 + ((ring0 + ring.slot * stage_bytes) >> 4);
+              const uint32_t a = a0 + as * KD * 32;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)   // h's leading terms, then its trailing ones
-              umma_tf32_ta(d, a + (j & 1) * 8, b + j * 2, id32, i > 0 || j > 0);
-            umma_commit(empty0 + ring.slot * 8);
-            if (i + 1 == total) umma_commit(accf0 + buf * 8);
+              for (int j = 0; j < 4; ++j)   // h's leading terms, then its trailing ones
+                umma_tf32_ta<CG>(d, a + (j & 1) * 8, b + j * 2, id32, i > 0 || j > 0);
+              umma_commit_all<CG>(empty0 + ring.slot * 8);
+              if (i + 1 == total) umma_commit_all<CG>(accf0 + buf * 8);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          ++ac;
         }
-        ++ac;
+      }
+      if (!ok || *abort_flag) {
+        if (elect_one()) {
+          umma_commit_own<CG>(smem_u32(&sh.drain));
+          tile_wait_final(smem_u32(&sh.drain), 0);
+        }
+        __syncwarp();
       }
     }
-    if (!ok || *abort_flag) {
-      if (elect_one()) {
-        umma_commit(smem_u32(&sh.drain));
-        tile_wait_final(smem_u32(&sh.drain), 0);
-      }
-      __syncwarp();
-    }
-  } else if (warp >= kFirstConv && warp < kFirstEpi) {
+  } else if (warp >= kFirstConv && warp < F::kFirstEpi) {
     // ---- A operand: shared memory -> f16 -> TMEM ---------------------------
-    pdl_wait();
-    Walk walk(p, prefix, tiles);
-    Seg sg;
+    const int group = (warp - kFirstConv) >> 2;       // groups take stages in turn
     const int row = (warp & 3) * 32 + lane;           // a warp reaches the lanes of its quarter
     const uint32_t a_lane = a_base + (static_cast<uint32_t>(warp & 3) << 21);
-    const int t0 = (warp - kFirstConv) * 32 + lane;   // this thread among the 128
     const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t ready0 = PAIR ? map_to_cta(smem_u32(&sh.ready[0]), 0) : smem_u32(&sh.ready[0]);
+    // weights of a single group need nothing of the kernel before this one
+    if (p.L > 0 && !p.by_row) pdl_wait();
+    Walk<CG> walk(p, prefix, tiles);
+    Seg sg;
     Ring ring, used;   // this stage; the one whose A operand lay where this one's goes
     int it = 0;
     bool ok = true;
     const auto place_free = [&]() {
-      if (it < NA) return true;
-      const bool free = tile_wait(smem_u32(&sh.empty[used.slot]), used.phase, abort_flag,
+      return it < NA || tile_wait(smem_u32(&sh.empty[used.slot]), used.phase, abort_flag,
                                   kErrTileOperand, p.err);
-      used.advance(S);
-      return free;
+    };
+    const auto advance = [&]() {
+      ring.advance(S);
+      if (it >= NA) used.advance(S);
+      ++it;
     };
     // A stage is announced once its stores have landed; the wait for them is
-    // put behind the next stage's loads and conversions, where it is over.
+    // put behind the next stage's loads, where it is over.
     int pending = -1;
     const auto announce = [&]() {
       if (pending < 0) return;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[pending]));
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(ready0 + pending * 8);
+        else mbar_arrive(ready0 + pending * 8);
+      }
       pending = -1;
     };
-    const auto convert = [&](uint32_t w, uint32_t (&r)[32]) {
+    const auto convert = [&](const uint4 (&v)[4], uint32_t (&r)[32]) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 v = lds128(w + c * 2048);
-        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t q[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
@@ -556,21 +616,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     };
     while (ok && walk.next(sg)) {
-      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, ++it, ring.advance(S)) {
+      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, advance()) {
+        if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
-        const uint32_t full = smem_u32(&sh.full[ring.slot]);
+        const uint32_t full = smem_u32(&sh.wfull[ring.slot]);
         if (!__all_sync(0xffffffffu, mbar_test(full, ring.phase))) announce();
-        ok = tile_wait(full, ring.phase, abort_flag, kErrTileRing, p.err) && place_free();
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, tile_wait(full, ring.phase, abort_flag, kErrTileRing, p.err));
+        if (!ok) break;
+        const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
+        const bool two = KD == 2 && kb + 1 < sg.kb1;
+        uint4 v[4], v1[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = lds128(w + c * 2048);
+        if (two) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v1[c] = lds128(w + kTileWBytes + c * 2048);
+        }
+        announce();
+        uint32_t r[32];
+        convert(v, r);
+        ok = __all_sync(0xffffffffu, place_free());
         if (!ok) break;
         tc_fence_after();
-        const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
-        uint32_t r[32];
-        convert(w, r);
-        announce();
         tmem_st_32cols(a_lane + as * KD * 32, r);
-        if (KD == 2 && kb + 1 < sg.kb1) {
-          convert(w + kTileWBytes, r);
+        if (two) {
+          convert(v1, r);
           tmem_st_32cols(a_lane + as * KD * 32 + 32, r);
         }
         pending = as;
@@ -579,17 +649,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       const int na = adapters_of(p, sg);
       const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
-      const int n16 = (sg.rows + 15) & ~15;
+      const int half = ((sg.rows + 15) & ~15) / CG, first = rank * half;
+      const int t0 = (warp & 3) * 32 + lane;          // this thread among the group's 128
       for (int i = 0; i < na && ok; ++i) {
         const int a_id = __ldg(list + i);
-        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
-          const int slot = ring.slot, as = it & (NA - 1);
-          ok = tile_wait(smem_u32(&sh.full[slot]), ring.phase, abort_flag, kErrTileRing, p.err) &&
+        for (int c = 0; c < p.rank16; ++c, advance()) {
+          if (F::kGroups == 2 && (it & 1) != group) continue;
+          const int as = it & (NA - 1);
+          ok = tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag, kErrTileRing,
+                         p.err) &&
                place_free();
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = ring0 + slot * stage_bytes;
+          const uint32_t st = ring0 + ring.slot * stage_bytes;
           uint32_t r[16];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -608,12 +681,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           tmem_st_16cols(a_lane + as * KD * 32, r);
-          // B: row t = h's 16 leading tf32 terms, then its 16 trailing ones,
-          // in the 128-byte swizzle; zeros where the row has another adapter
-          for (int t = t0; t < n16; t += 128) {
-            const bool mine = t < sg.rows && __ldg(p.ids + sg.row0 + t) == a_id;
+          // B (this CTA's share of the rows): row t = h's 16 leading tf32
+          // terms, then its 16 trailing ones, in the 128-byte swizzle; zeros
+          // where the row has another adapter
+          for (int t = t0; t < half; t += 128) {
+            const int s = first + t;
+            const bool mine = s < sg.rows && __ldg(p.ids + sg.row0 + s) == a_id;
             const float4* h = reinterpret_cast<const float4*>(
-                p.h + static_cast<int64_t>(sg.row0 + t) * p.rank16 * 16 + c * 16);
+                p.h + static_cast<int64_t>(sg.row0 + s) * p.rank16 * 16 + c * 16);
             const uint32_t at = st + t * 128;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -632,30 +707,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.ready[as]));
+          pending = as;
+          announce();
         }
       }
     }
-  } else if (warp >= kFirstEpi) {
+  } else if (warp >= F::kFirstEpi) {
     // ---- epilogue ------------------------------------------------------------
     pdl_wait();
-    Walk walk(p, prefix, tiles);
+    Walk<CG> walk(p, prefix, tiles);
     Seg sg;
-    const int ew = warp - kFirstEpi;
+    const int ew = warp - F::kFirstEpi;
     const int quarter = warp & 3;
-    // columns of this warp: a third of the tile's
-    const int cols = ((p.TN + 47) / 48) * 16;
+    // columns of this warp: an equal share of the tile's, in steps of 16
+    constexpr int kShares = F::kEpi / 4;
+    const int cols = (p.TN + 16 * kShares - 1) / (16 * kShares) * 16;
     const int col0 = (ew / 4) * cols;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter) << 21) + col0;
-    const int chunk = chunk_stages_of(p);
+    const uint32_t acce0 =
+        PAIR ? map_to_cta(smem_u32(&sh.acc_empty[0]), 0) : smem_u32(&sh.acc_empty[0]);
+    const auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(acce0 + buf * 8);
+        else mbar_arrive(acce0 + buf * 8);
+      }
+    };
+    const int chunk = chunk_stages_of<KD>(p);
+    const int me = blockIdx.x / CG;
+    // a CTA's parts: [head of its run, tail, adapter term][kPart]; a warp's
+    // words in it as [16 columns][4][lane][4]
+    const auto part_at = [&](int cluster, int which) {
+      return p.parts + (static_cast<int64_t>(cluster * CG + rank) * 3 + which) * F::kPart +
+             ew * (kCols * 32) + lane * 4;
+    };
     int ac = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int mine = max(0, min(cols, sg.rows - col0));    // columns with a row behind them
       const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
+      const int nb = sg.nb * CG + rank;
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
       const bool by_row = p.by_row && sg.kb1 == p.KB;
@@ -664,14 +756,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // (rows past the tile's end repeat its last)
           const int my_s = sg.row0 + min(col0 + j + (lane & 7), sg.rows - 1);
           float d[8];
-          row_deltas(p, sg.nb, quarter * 32 + lane, __ldg(p.ids + my_s), my_s, sh.corner[ew], d);
+          row_deltas(p, min(nb, p.NB - 1), quarter * 32 + lane, __ldg(p.ids + my_s), my_s,
+                     sh.corner[ew], d);
           tmem_st_8cols(lane_addr + 2 * acc_cols + NA * KD * 32 + j, d);
         }
         tmem_st_wait();
       }
-      int32_t acc[kMaxCols];
+      int32_t acc[kCols];
 #pragma unroll
-      for (int j = 0; j < kMaxCols; ++j) acc[j] = 0;
+      for (int j = 0; j < kCols; ++j) acc[j] = 0;
       for (int c0 = 0; c0 < stages; c0 += chunk, ++ac) {
         const int buf = ac & 1;
         ok = __all_sync(0xffffffffu,
@@ -680,7 +773,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < kMaxCols / 16; ++b)
+        for (int b = 0; b < kCols / 16; ++b)
           if (b * 16 < mine) {
             uint32_t r[16];
             tmem_ld_16cols(lane_addr + buf * acc_cols + b * 16, r);
@@ -688,9 +781,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[b * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
           }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+        release(buf);
       }
       if (!ok) break;
       // the MMAs' adapter term stays in its accumulator until it is used
@@ -706,101 +797,119 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const bool has_d = by_row || by_mma;
       const uint32_t d_addr = lane_addr + (by_row ? 2 * acc_cols + NA * KD * 32 : dbuf * acc_cols);
-      bool last = true;
-      int first_cta = 0, end_cta = 0;
-      if (sg.kb0 != 0 || sg.kb1 != p.KB) {
-        // this run holds part of the unit: leave it, and go on only as the last
-        first_cta = sg.unit * p.KB / walk.q;
-        end_cta = ((sg.unit + 1) * p.KB - 1) / walk.q;
-        const int side = static_cast<int>(blockIdx.x) == first_cta ? 1 : 0;
-        int32_t* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 3 + side) * p.TN * 128 +
-                        quarter * 32 + lane;
-        float* dpart = reinterpret_cast<float*>(p.parts) +
-                       (static_cast<int64_t>(blockIdx.x) * 3 + 2) * p.TN * 128 + quarter * 32 + lane;
+      // The loops below take 16 columns a round and stay rolled: code that a
+      // CTA runs once or twice costs more to fetch than to execute.  The
+      // registers move up by 16 instead.
+      const auto rotate = [&]() {
+        if constexpr (kCols > 16) {
+          int32_t t[16];
 #pragma unroll
-        for (int b = 0; b < kMaxCols / 16; ++b)
+          for (int j = 0; j < 16; ++j) t[j] = acc[j];
+#pragma unroll
+          for (int j = 0; j < kCols - 16; ++j) acc[j] = acc[j + 16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[kCols - 16 + j] = t[j];
+        }
+      };
+      const bool parted = sg.kb0 != 0 || sg.kb1 != p.KB;
+      int first = me, end = me;
+      bool last = true;
+      if (parted) {
+        // this run holds part of the unit: leave it, and go on only as the last
+        first = sg.unit * p.KB / walk.q;
+        end = ((sg.unit + 1) * p.KB - 1) / walk.q;
+        int32_t* part = part_at(me, me == first ? 1 : 0);
+        int32_t* dpart = part_at(me, 2);
+#pragma unroll 1
+        for (int b = 0; b < kCols / 16; ++b) {
           if (b * 16 < mine) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) part[(col0 + b * 16 + j) * 128] = acc[b * 16 + j];
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<int4*>(part + (b * 4 + q) * 128) =
+                  make_int4(acc[q * 4], acc[q * 4 + 1], acc[q * 4 + 2], acc[q * 4 + 3]);
             if (has_d) {
               uint32_t r[16];
               tmem_ld_16cols(d_addr + b * 16, r);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                dpart[(col0 + b * 16 + j) * 128] = __uint_as_float(r[j]);
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dpart + (b * 4 + q) * 128) =
+                    make_uint4(r[q * 4], r[q * 4 + 1], r[q * 4 + 2], r[q * 4 + 3]);
             }
           }
+          rotate();
+        }
         // release this warp's part, acquire the others'
         __syncwarp();
         int before = 0;
-        if (lane == 0) before = atomic_add_acq_rel(p.counts + first_cta * kEpiWarps + ew, 1);
+        if (lane == 0)
+          before = atomic_add_acq_rel(p.counts + (first * CG + rank) * kTileEpiWarps + ew, 1);
         before = __shfl_sync(0xffffffffu, before, 0);
-        last = before == end_cta - first_cta;
+        last = before == end - first;
       }
       if (last) {
-        const int n = sg.nb * 128 + quarter * 32 + lane;
+        const int n = nb * 128 + quarter * 32 + lane;
         const bool in = n < p.N;
         const int64_t en = static_cast<int64_t>(sg.e) * p.N + n;
         const float ws = in ? __ldg(p.ws + en) : 0.0f;
         const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
-        const bool parted = sg.kb0 != 0 || sg.kb1 != p.KB;
         // the unit's adapter term: in this CTA's TMEM, or left by the CTA
         // that ran the unit's end
-        const bool unit_d =
-            p.L > 0 &&
+        const bool other_d =
+            !has_d && p.L > 0 &&
             (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg.tile) * p.list_stride) > 0);
-        const float* dother = reinterpret_cast<const float*>(p.parts) +
-                              (static_cast<int64_t>(end_cta) * 3 + 2) * p.TN * 128 + quarter * 32 + lane;
-#pragma unroll
-        for (int b = 0; b < kMaxCols / 16; ++b)
+#pragma unroll 1
+        for (int b = 0; b < kCols / 16; ++b) {
           if (b * 16 < mine) {
-            if (parted)
-              for (int c = first_cta; c <= end_cta; ++c) {
-                if (c == static_cast<int>(blockIdx.x)) continue;
-                const int32_t* part = p.parts +
-                                      (static_cast<int64_t>(c) * 3 + (c == first_cta ? 1 : 0)) * p.TN *
-                                          128 +
-                                      quarter * 32 + lane;
+            for (int c = first; c <= end; ++c) {
+              if (c == me) continue;
+              const int32_t* part = part_at(c, c == first ? 1 : 0);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  acc[b * 16 + j] += __ldcg(part + (col0 + b * 16 + j) * 128);
+              for (int q = 0; q < 4; ++q) {
+                const int4 v = __ldcg(reinterpret_cast<const int4*>(part + (b * 4 + q) * 128));
+                acc[q * 4] += v.x;
+                acc[q * 4 + 1] += v.y;
+                acc[q * 4 + 2] += v.z;
+                acc[q * 4 + 3] += v.w;
               }
-            float d[16];
+            }
+            uint32_t r[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) d[j] = 0.0f;
+            for (int j = 0; j < 16; ++j) r[j] = 0;
             if (has_d) {
-              uint32_t r[16];
               tmem_ld_16cols(d_addr + b * 16, r);
               tmem_ld_wait();
+            } else if (other_d) {
+              const int32_t* dpart = part_at(end, 2);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) d[j] = __uint_as_float(r[j]);
-            } else if (unit_d) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) d[j] = __ldcg(dother + (col0 + b * 16 + j) * 128);
+              for (int q = 0; q < 4; ++q) {
+                const int4 v = __ldcg(reinterpret_cast<const int4*>(dpart + (b * 4 + q) * 128));
+                r[q * 4] = v.x;
+                r[q * 4 + 1] = v.y;
+                r[q * 4 + 2] = v.z;
+                r[q * 4 + 3] = v.w;
+              }
             }
+            const int s0 = sg.row0 + col0 + b * 16;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (b * 16 + j < mine && in) {
-                const int s = sg.row0 + col0 + b * 16 + j;
-                const int64_t to = p.out_rows != nullptr ? __ldg(p.out_rows + s) : s;
-                store_out<OUT>(p.out, to * p.N + n, dequant(acc[b * 16 + j], ws, bias, d[j], p.rq),
-                               p);
+                const int64_t to = p.out_rows != nullptr ? __ldg(p.out_rows + s0 + j) : s0 + j;
+                store_out<OUT>(p.out, to * p.N + n,
+                               dequant(acc[j], ws, bias, __uint_as_float(r[j]), p.rq), p);
               }
           }
+          rotate();
+        }
       }
-      if (by_mma) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[dbuf]));
-      }
+      if (by_mma) release(dbuf);
     }
     // rows of dropped slots hold zeros
     if (prefix != nullptr) {
-      const int64_t step = static_cast<int64_t>(gridDim.x) * kEpiWarps * 32;
+      const int64_t step = static_cast<int64_t>(gridDim.x) * F::kEpi * 32;
       const int64_t total = static_cast<int64_t>(p.R) * p.N;
       for (int64_t i = group_end(p, p.E) * static_cast<int64_t>(p.N) +
-                       static_cast<int64_t>(blockIdx.x) * kEpiWarps * 32 + ew * 32 + lane;
+                       static_cast<int64_t>(blockIdx.x) * F::kEpi * 32 + ew * 32 + lane;
            i < total; i += step) {
         if constexpr (OUT == Q8_I8) static_cast<int8_t*>(p.out)[i] = static_cast<int8_t>(p.rq.ozp_i);
         else if constexpr (OUT == Q8_F32) static_cast<float*>(p.out)[i] = 0.0f;
@@ -810,44 +919,86 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA of a pair leaves while the leader's MMAs may still read the
+  // peer's memories or arrive at its barriers
+  if constexpr (PAIR) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
-template <int OUT>
-cudaError_t launch_one(const CUtensorMap& map, const TileParams& p, int grid, size_t smem,
-                       cudaStream_t s) {
+template <int OUT, bool PAIR>
+cudaError_t launch_one(const CUtensorMap& map, const TileParams& p, size_t smem, cudaStream_t s) {
+  constexpr int CG = Form<PAIR>::CG;
+  auto kernel = tile_gemm_kernel<OUT, PAIR>;
   static DeviceOnce once;
-  cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(tile_gemm_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kTileSmem);
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(tile_gemm_kernel<OUT>, grid, kTileThreads, smem, s, map, p);
+  if constexpr (PAIR) {
+    // pairs that fit the GPU at once (both CTAs of one share a GPC)
+    static int fit[64] = {0};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    int& pairs = fit[dev & 63];
+    if (pairs == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = p.grid / CG * CG;
+      cfg.blockDim = kTileThreads;
+      cfg.dynamicSmemBytes = kTileSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = CG;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = p.grid / CG;
+      }
+      pairs = n;
+    }
+    const int grid = std::max(1, std::min(pairs, p.grid / CG)) * CG;
+    return launch_pdl_cluster(kernel, grid, kTileThreads, smem, CG, s, map, p);
+  } else {
+    return launch_pdl(kernel, p.grid, kTileThreads, smem, s, map, p);
+  }
+}
+
+template <bool PAIR>
+cudaError_t launch_form(TileParams p, const void* operand, q8_dtype out_dtype, cudaStream_t s) {
+  using F = Form<PAIR>;
+  CUtensorMap map;
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(p.R), static_cast<uint64_t>(p.KB)};
+  const uint64_t str[2] = {128, static_cast<uint64_t>(p.R) * 128};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(p.TN / F::CG), F::KD};
+  // (16-bit elements; the map's element type only matters for reductions)
+  if (!encode_bf16_tmap(&map, operand, 3, dims, str, box)) return cudaErrorInvalidValue;
+  const size_t stage = static_cast<size_t>(F::KD) * (p.TN / F::CG * 128 + kTileWBytes);
+  const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
+  p.stages = static_cast<int>(std::min<size_t>(kMaxRing, (kTileSmem - 1024 - table) / stage));
+  const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
+  switch (out_dtype) {
+    case Q8_I8: return launch_one<Q8_I8, PAIR>(map, p, smem, s);
+    case Q8_F32: return launch_one<Q8_F32, PAIR>(map, p, smem, s);
+    case Q8_F16: return launch_one<Q8_F16, PAIR>(map, p, smem, s);
+    default: return launch_one<Q8_BF16, PAIR>(map, p, smem, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
                              cudaStream_t s) {
-  CUtensorMap map;
-  const uint64_t dims[3] = {64, static_cast<uint64_t>(p.R), static_cast<uint64_t>(p.KB)};
-  const uint64_t str[2] = {128, static_cast<uint64_t>(p.R) * 128};
-  const uint32_t box[3] = {64, static_cast<uint32_t>(p.TN), static_cast<uint32_t>(p.KD)};
-  // (16-bit elements; the map's element type only matters for reductions)
-  if (!encode_bf16_tmap(&map, operand, 3, dims, str, box)) return cudaErrorInvalidValue;
   p.err = device_error_word();
   if (p.err == nullptr) return cudaErrorUnknown;
-  const size_t stage = static_cast<size_t>(p.KD) * (static_cast<size_t>(p.TN) * 128 + kTileWBytes);
-  const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
-  p.stages = static_cast<int>(std::min<size_t>(kMaxRing, (kTileSmem - 1024 - table) / stage));
-  const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
-  switch (out_dtype) {
-    case Q8_I8: return launch_one<Q8_I8>(map, p, p.grid, smem, s);
-    case Q8_F32: return launch_one<Q8_F32>(map, p, p.grid, smem, s);
-    case Q8_F16: return launch_one<Q8_F16>(map, p, p.grid, smem, s);
-    default: return launch_one<Q8_BF16>(map, p, p.grid, smem, s);
-  }
+  return p.TN > Form<false>::kMaxRows ? launch_form<true>(p, operand, out_dtype, s)
+                                      : launch_form<false>(p, operand, out_dtype, s);
 }
 
 }  // namespace q8
