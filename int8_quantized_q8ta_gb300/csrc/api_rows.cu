@@ -280,7 +280,7 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
   p.ws = weight_scales;
   p.bias = bias;
   p.rq = make_rq(input_scale, output_scale, output_zero_point, relu);
-  p.relu = relu;
+  p.floor_f = relu ? 0.0f : -INFINITY;
   p.out = out;
   p.parts = reinterpret_cast<int32_t*>(ws + plan.operand);
   p.counts = reinterpret_cast<int32_t*>(ws + plan.operand + plan.parts);
@@ -381,7 +381,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   p.ws = weight_scales;
   p.bias = bias;
   p.rq = make_rq(input_scale, output_scale, output_zero_point, relu);
-  p.relu = relu;
+  p.floor_f = relu ? 0.0f : -INFINITY;
   p.out = out;
   p.parts = reinterpret_cast<int32_t*>(ws + sp.plan.operand);
   p.counts = reinterpret_cast<int32_t*>(ws + sp.plan.operand + sp.plan.parts);

@@ -103,7 +103,7 @@ struct TileParams {
   const float* ws;          // [E, N]
   const float* bias;        // [E, N] or null
   Requant rq;
-  int relu;
+  float floor_f;            // float outputs below it become 0: 0 for relu, -inf for none
   void* out;
   const int32_t* out_rows;  // output row of each row, or null
   uint32_t* err;

@@ -49,6 +49,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(p)));
+}
 __device__ __forceinline__ int atomic_add_acq_rel(int* p, int v) {
   int old;
   asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
@@ -157,19 +160,6 @@ __device__ __forceinline__ uint32_t idesc_tf32(uint32_t m, uint32_t n) {
 // Bounded waits: about one second, then the CTA's abort flag and the library's
 // device error word are set and every role winds down.
 // ---------------------------------------------------------------------------
-// Whether the phase is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 constexpr uint64_t kTileWaitNs = 1000ull * 1000ull * 1000ull;
 
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity,

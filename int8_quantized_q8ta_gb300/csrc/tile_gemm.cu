@@ -53,7 +53,7 @@ enum : uint32_t { kErrTileRing = 0x10A, kErrTileAcc = 0x10B, kErrTileOperand = 0
 
 constexpr int kMaxRing = 12;
 constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
-constexpr int kFirstConv = 4;           // warps 0 and 1: copies, MMAs; 2 and 3 idle
+constexpr int kFirstConv = 4;           // warps 0 to 2: weights, MMAs, tokens; 3 idle
 constexpr int kTileThreads = 640;
 constexpr int kTmemCols = 512;
 // Stages of A operands in tensor memory, behind the two accumulators.
@@ -291,19 +291,29 @@ __device__ __forceinline__ float dequant(int32_t acc, float ws, float b, float d
   return __fadd_rn(__fadd_rn(t, b), d);
 }
 
+template <int OUT> struct OutType { using type = uint16_t; };
+template <> struct OutType<Q8_I8> { using type = int8_t; };
+template <> struct OutType<Q8_F32> { using type = float; };
+
+// Where an output goes, and its last step: requantize, or activate and round.
 template <int OUT>
-__device__ __forceinline__ void store_out(void* out, int64_t at, float v, const TileParams& p) {
-  if constexpr (OUT == Q8_I8) {
-    const int32_t q = round_clamp_first(__fmul_rn(v, p.rq.inv_out), p.rq.ozp_i, p.rq.lo_f,
-                                        p.rq.hi_f);
-    static_cast<int8_t*>(out)[at] = static_cast<int8_t>(q);
-  } else {
-    if (p.relu && v < 0.0f) v = 0.0f;   // NaN stays
-    if constexpr (OUT == Q8_F32) static_cast<float*>(out)[at] = v;
-    if constexpr (OUT == Q8_F16) static_cast<__half*>(out)[at] = __float2half_rn(v);
-    if constexpr (OUT == Q8_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+struct OutPtr {
+  typename OutType<OUT>::type* at;
+  __device__ __forceinline__ OutPtr(void* out, int64_t i)
+      : at(static_cast<typename OutType<OUT>::type*>(out) + i) {}
+  __device__ __forceinline__ void step(int64_t n) { at += n; }
+  __device__ __forceinline__ void store(float v, const TileParams& p) const {
+    if constexpr (OUT == Q8_I8) {
+      *at = static_cast<int8_t>(round_clamp_first(__fmul_rn(v, p.rq.inv_out), p.rq.ozp_i,
+                                                  p.rq.lo_f, p.rq.hi_f));
+    } else {
+      v = v < p.floor_f ? 0.0f : v;   // relu: floor 0, else -inf; NaN stays
+      if constexpr (OUT == Q8_F32) *at = v;
+      if constexpr (OUT == Q8_F16) *at = __half_as_ushort(__float2half_rn(v));
+      if constexpr (OUT == Q8_BF16) *at = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
   }
-}
+};
 
 // Two halves of a token tile have rows that are multiples of 8.
 template <int OUT, bool PAIR>
@@ -385,65 +395,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tiles = sh.tiles;
 
   if (warp == 0) {
-    // ---- copies: one elected lane of a warp that runs in step ----------------
+    // ---- weights: one elected lane of a warp that runs in step ---------------
+    // (a stage's two copies come from two warps: issuing one takes some 200
+    // cycles, and a wide stage lasts 384)
     Walk<CG> walk(p, prefix, tiles);
     Seg sg;
     const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
-    const uint32_t wfull0 = smem_u32(&sh.wfull[0]), tfull0 = smem_u32(&sh.tfull[0]);
-    const uint32_t empty0 = smem_u32(&sh.empty[0]);
-    const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
+    const uint32_t wfull0 = smem_u32(&sh.wfull[0]), empty0 = smem_u32(&sh.empty[0]);
+    // the weights of a single group need nothing of the kernel before this
+    // one: a packed weight is written at load time
+    if (p.L > 0 && !p.by_row) pdl_wait();
     Ring ring;
     int it = 0;
     bool ok = true;
-    // the first ring of weights of a single group does not depend on the
-    // kernel before this one: a packed weight is written at load time
-    int early = 0;
-    if (prefix == nullptr) {
-      Walk<CG> w2 = walk;
-      while (early < S && w2.next(sg)) {
-        const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
-        const uint8_t* w = p.w + nb * w_rows;
-        const int kb1 = uniform(sg.kb1);
-        for (int kb = uniform(sg.kb0); kb < kb1 && early < S; kb += KD, ++early) {
-          const uint32_t nk = min(KD, kb1 - kb);
-          const uint32_t st = ring0 + early * stage_bytes, bar = wfull0 + early * 8;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(bar, nk * kTileWBytes);
-            bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
-                      nk * kTileWBytes, bar);
-          }
-          __syncwarp();
-        }
-        if (p.L > 0 && !p.by_row) break;   // adapter stages follow, not known yet
-      }
-      pdl_wait();
-    }
     while (ok && walk.next(sg)) {
       // (an odd last block of a pair repeats the one before and stores nothing)
       const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
       const int kb1 = uniform(sg.kb1);
-      const int row0 = uniform(sg.row0) + rank * (((uniform(sg.rows) + 15) & ~15) / CG);
       const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg.e)) * p.NB + nb) * w_rows;
       for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
-        const uint32_t nk = min(KD, kb1 - kb);
-        const uint32_t st = ring0 + ring.slot * stage_bytes;
-        if (it >= early) {
-          ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
-                              p.err);
-          if (!ok) break;
-        }
+        const uint32_t bytes = min(KD, kb1 - kb) * kTileWBytes;
+        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
+        if (!ok) break;
         if (elect_one()) {
-          if (it >= early) {
-            const uint32_t bar = wfull0 + ring.slot * 8;
-            mbar_arrive_expect_tx(bar, nk * kTileWBytes);
-            bulk_load(st + KD * tok_bytes, w + static_cast<int64_t>(kb) * kTileWBytes,
-                      nk * kTileWBytes, bar);
-          }
-          if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * KD * tok_bytes);
-          if constexpr (PAIR)
-            tma_load_3d_pair(st, &map_x, tfull_lead + ring.slot * 8, 0, row0, kb);
-          else
-            tma_load_3d(st, &map_x, tfull0 + ring.slot * 8, 0, row0, kb);
+          const uint32_t bar = wfull0 + ring.slot * 8;
+          mbar_arrive_expect_tx(bar, bytes);
+          bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes,
+                    w + static_cast<int64_t>(kb) * kTileWBytes, bytes, bar);
         }
         __syncwarp();
       }
@@ -457,23 +435,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
           if (!ok) break;
-          const uint32_t bar = wfull0 + ring.slot * 8;
           if (elect_one()) {
+            const uint32_t bar = wfull0 + ring.slot * 8;
             mbar_arrive_expect_tx(bar, 4096);
             bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
-            if (leader) mbar_arrive(tfull0 + ring.slot * 8);   // no tokens in this round
           }
           __syncwarp();
         }
       }
     }
-    if (!ok || *abort_flag) {
-      // copies issued but not waited for by anyone still land in this CTA
-      for (int i = max(0, it - S); i < it; ++i) {
+    if (!ok || *abort_flag)   // copies issued but not waited for still land in this CTA
+      for (int i = max(0, it - S); i < it; ++i)
         tile_wait_final(smem_u32(&sh.wfull[i % S]), (i / S) & 1);
-        if (leader) tile_wait_final(smem_u32(&sh.tfull[i % S]), (i / S) & 1);
+  } else if (warp == 2) {
+    // ---- tokens: likewise ----------------------------------------------------
+    pdl_wait();
+    Walk<CG> walk(p, prefix, tiles);
+    Seg sg;
+    const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
+    Ring ring;
+    int it = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int kb1 = uniform(sg.kb1);
+      const int row0 = uniform(sg.row0) + rank * (((uniform(sg.rows) + 15) & ~15) / CG);
+      for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
+        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t st = ring0 + ring.slot * stage_bytes;
+          if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * KD * tok_bytes);
+          if constexpr (PAIR)
+            tma_load_3d_pair(st, &map_x, tfull_lead + ring.slot * 8, 0, row0, kb);
+          else
+            tma_load_3d(st, &map_x, tfull0 + ring.slot * 8, 0, row0, kb);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      const int rounds = uniform(adapters_of(p, sg)) * p.rank16;   // without tokens
+      for (int i = 0; i < rounds; ++i, ++it, ring.advance(S)) {
+        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
+        if (!ok) break;
+        if (leader && elect_one()) mbar_arrive(tfull0 + ring.slot * 8);
+        __syncwarp();
       }
     }
+    if ((!ok || *abort_flag) && leader)
+      for (int i = max(0, it - S); i < it; ++i)
+        tile_wait_final(smem_u32(&sh.tfull[i % S]), (i / S) & 1);
   } else if (warp == 1) {
     // ---- MMAs: one elected lane of a warp that runs in step ------------------
     if (leader) {
@@ -590,19 +601,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (it >= NA) used.advance(S);
       ++it;
     };
-    // A stage is announced once its stores have landed; the wait for them is
-    // put behind the next stage's loads, where it is over.
-    int pending = -1;
-    const auto announce = [&]() {
-      if (pending < 0) return;
+    const auto announce = [&](int as) {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(ready0 + pending * 8);
-        else mbar_arrive(ready0 + pending * 8);
+        if constexpr (PAIR) mbar_arrive_cluster(ready0 + as * 8);
+        else mbar_arrive(ready0 + as * 8);
       }
-      pending = -1;
     };
     const auto convert = [&](const uint4 (&v)[4], uint32_t (&r)[32]) {
 #pragma unroll
@@ -619,9 +625,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int kb = sg.kb0; kb < sg.kb1; kb += KD, advance()) {
         if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
-        const uint32_t full = smem_u32(&sh.wfull[ring.slot]);
-        if (!__all_sync(0xffffffffu, mbar_test(full, ring.phase))) announce();
-        ok = __all_sync(0xffffffffu, tile_wait(full, ring.phase, abort_flag, kErrTileRing, p.err));
+        ok = __all_sync(0xffffffffu, tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase,
+                                               abort_flag, kErrTileRing, p.err));
         if (!ok) break;
         const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
         const bool two = KD == 2 && kb + 1 < sg.kb1;
@@ -632,7 +637,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) v1[c] = lds128(w + kTileWBytes + c * 2048);
         }
-        announce();
         uint32_t r[32];
         convert(v, r);
         ok = __all_sync(0xffffffffu, place_free());
@@ -643,9 +647,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           convert(v1, r);
           tmem_st_32cols(a_lane + as * KD * 32 + 32, r);
         }
-        pending = as;
+        announce(as);
       }
-      announce();
       if (!ok) break;
       const int na = adapters_of(p, sg);
       const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
@@ -707,8 +710,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          pending = as;
-          announce();
+          announce(as);
         }
       }
     }
@@ -752,6 +754,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // of their own while the unit's MMAs run
       const bool by_row = p.by_row && sg.kb1 == p.KB;
       if (by_row) {
+        // the adapters' lines of these channels on their way before the first
+        // is used: eight lanes a row, 4 lines of 128 bytes to each 8 ranks
+        for (int j = 0; j < mine; j += 4) {
+          const int a = __ldg(p.ids + sg.row0 + min(col0 + j + (lane >> 3), sg.rows - 1));
+          if (a >= 0 && a < p.L)
+            for (int c = 0; c < p.rank16; ++c)
+              prefetch_l2(p.lora_b +
+                          ((static_cast<int64_t>(a) * p.NB + min(nb, p.NB - 1)) * p.rank16 + c) * 4096 +
+                          ((lane >> 2) & 1) * 2048 + quarter * 512 + (lane & 3) * 128);
+        }
         for (int j = 0; j < mine; j += 8) {
           // (rows past the tile's end repeat its last)
           const int my_s = sg.row0 + min(col0 + j + (lane & 7), sg.rows - 1);
@@ -890,14 +902,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 r[q * 4 + 3] = v.w;
               }
             }
-            const int s0 = sg.row0 + col0 + b * 16;
+            float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              if (b * 16 + j < mine && in) {
-                const int64_t to = p.out_rows != nullptr ? __ldg(p.out_rows + s0 + j) : s0 + j;
-                store_out<OUT>(p.out, to * p.N + n,
-                               dequant(acc[j], ws, bias, __uint_as_float(r[j]), p.rq), p);
-              }
+              v[j] = dequant(acc[j], ws, bias, __uint_as_float(r[j]), p.rq);
+            const int s0 = sg.row0 + col0 + b * 16;
+            const int rows = in ? mine - b * 16 : 0;
+            if (p.out_rows == nullptr) {
+              OutPtr<OUT> to(p.out, static_cast<int64_t>(s0) * p.N + n);
+#pragma unroll
+              for (int j = 0; j < 16; ++j, to.step(p.N))
+                if (j < rows) to.store(v[j], p);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j < rows)
+                  OutPtr<OUT>(p.out, static_cast<int64_t>(__ldg(p.out_rows + s0 + j)) * p.N + n)
+                      .store(v[j], p);
+            }
           }
           rotate();
         }
