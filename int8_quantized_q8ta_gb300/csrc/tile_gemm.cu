@@ -23,9 +23,9 @@
 // are exact integers for 2^24 / (a W) k-blocks; such a chunk is then drained
 // from TMEM into int32 registers while the other accumulator fills.
 //
-// Work split: all (tile, output block) units times their k-blocks form one
-// line, cut into equal runs, one per CTA, so that a few wide units and many
-// small ones fill the SMs alike.  A unit cut by a run's end is summed by
+// Work split: whole waves of (tile, output block) units, then the last one to
+// two waves' k-blocks as one line cut into equal runs, one per CTA, so that a
+// few wide units and many small ones fill the SMs alike.  A unit cut by a run's end is summed by
 // whichever of its CTAs comes last, warp by warp, from the int32 parts the
 // others left in the workspace: integer sums, the same in any order.  No CTA
 // waits for another.
@@ -53,7 +53,7 @@ enum : uint32_t { kErrTileRing = 0x10A, kErrTileAcc = 0x10B, kErrTileOperand = 0
 
 constexpr int kMaxRing = 12;
 constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
-constexpr int kFirstConv = 4;           // warps 0 to 2: weights, MMAs, tokens; 3 idle
+constexpr int kFirstConv = 4;           // warps 0 to 3: weights, MMAs, tokens, schedule
 constexpr int kTileThreads = 640;
 constexpr int kTmemCols = 512;
 // Stages of A operands in tensor memory, behind the two accumulators.
@@ -85,6 +85,16 @@ struct Form {
   static_assert(kEpi <= kTileEpiWarps, "workspace");
 };
 
+// One run's part of a unit, as the scheduling warp hands it to the others.
+struct alignas(16) Seg {
+  int e, row0, rows, nb;       // group, first row, rows, output block (of 128 * CG)
+  int tile, kb0, kb1, unit;    // index of the row tile; k-blocks; kb1 0: no more
+  int na;                      // adapters whose MMAs follow (see adapters_of)
+  int first, end;              // CTAs (pairs) that share the unit
+  int pad;
+};
+constexpr int kSegs = 4;       // parts on their way
+
 struct TileShared {
   uint64_t wfull[kMaxRing];   // weights of a stage have landed
   uint64_t tfull[kMaxRing];   // tokens of a stage have landed (in a pair: both halves, at the leader)
@@ -93,6 +103,9 @@ struct TileShared {
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
+  uint64_t seg_full[kSegs];   // a part is described
+  uint64_t seg_empty[kSegs];  // every warp has read it
+  Seg seg[kSegs];
   uint32_t tmem;
   uint32_t abort;
   int32_t tiles;              // row tiles of all groups
@@ -107,13 +120,6 @@ __device__ __forceinline__ int chunk_stages_of(const TileParams& p) {
   return max(1, (1 << 24) / (p.a_bound * wb) / KD);
 }
 
-// One run's part of a unit.
-struct Seg {
-  int e, row0, rows, nb, tile;   // group, first row, rows, output block, index of the row tile
-  int kb0, kb1;
-  int unit;
-};
-
 // Rows of group e.  Offsets come from device memory: whatever they hold, no
 // row outside [0, R) is touched.
 __device__ __forceinline__ int group_end(const TileParams& p, int e) {
@@ -124,64 +130,97 @@ __device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start
   return max(0, group_end(p, e + 1) - start);
 }
 
-// The CTA's (or pair's) run of the line of all units' k-blocks (32-bit: the
-// host checks), unit by unit; a unit is a row tile times 128 (256) channels.  The divisions that place its start are done once: one integer
-// division by a runtime value takes longer than a k-block's MMAs.
+// The units of a CTA (or pair), a unit being a row tile times 128 (256)
+// channels.  While whole waves of units remain, the CTAs take neighbouring
+// ones, the row tiles of one output block after another: what runs at the same
+// time then shares its weights and tokens in L2 (contiguous runs for each CTA
+// kept every expert's weights in flight at once, more than L2 holds).  The
+// last one to two waves form a line of k-blocks cut into equal runs.
+//   (All counts fit 32 bits: the host checks.)
 template <int CG>
 struct Walk {
   const TileParams& p;
+  const int32_t* prefix;   // row tiles before each group, or null: one group
   int NB;                  // blocks of 128 * CG channels
-  int q;                   // k-blocks of every run but the last
-  int left, unit, kb;      // k-blocks still to take; the unit and where in it
+  int ctas, me;            // CTAs (pairs) and this one
+  int waves, wave;         // whole waves, and those behind
+  int base, q;             // the line's first unit, and k-blocks of a run
+  int left, unit, kb;      // the run's k-blocks still to take; its unit and where in it
   int e, start, count;     // the unit's group and its rows
   int tiles, per, t0;      // the group's row tiles, rows of each, tiles before them
-  int i, nb;               // row tile and output block: tiles of one block follow one another
+  int i, nb;               // row tile and output block
 
-  __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix, int all_tiles)
-      : p(p_), NB((p_.NB + CG - 1) / CG) {
-    const int total = all_tiles * NB * p.KB;
-    q = max(p.min_run, (total - 1) / static_cast<int>(gridDim.x / CG) + 1);
-    const int pos = static_cast<int>(
-        min(static_cast<int64_t>(total), static_cast<int64_t>(q) * (blockIdx.x / CG)));
-    left = min(total - pos, q);
-    unit = pos / p.KB;
-    kb = pos - unit * p.KB;
+  __device__ __forceinline__ Walk(const TileParams& p_, const int32_t* prefix_, int all_tiles)
+      : p(p_), prefix(prefix_), NB((p_.NB + CG - 1) / CG) {
+    ctas = gridDim.x / CG;
+    me = blockIdx.x / CG;
+    const int units = all_tiles * NB, full = units / ctas;
+    waves = units == full * ctas ? full : max(full - 1, 0);
+    wave = 0;
+    base = waves * ctas;
+    const int total = (units - base) * p.KB;
+    q = max(p.min_run, (total - 1) / ctas + 1);
+    kb = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * me));
+    left = min(total - kb, q);
+    unit = -1;             // the run is not begun
+  }
+  __device__ __forceinline__ void cut() {
+    tiles = (count + p.TN - 1) / p.TN;
+    per = tile_rows(count, tiles);
+  }
+  // Divisions and a search, once a whole unit or run.
+  __device__ __forceinline__ void locate(int u) {
     e = 0;
     start = 0;
     count = p.R;
     t0 = 0;
-    if (left <= 0) return;
     if (prefix != nullptr) {
       // the last group that starts at or before this unit (groups without
       // rows have no units)
       int lo = 0, hi = p.E - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] * NB <= unit) lo = mid; else hi = mid - 1;
+        if (prefix[mid] * NB <= u) lo = mid; else hi = mid - 1;
       }
       e = lo;
       t0 = prefix[lo];
       count = group_rows(p, e, start);
     }
     cut();
-    const int local = unit - t0 * NB;
+    const int local = u - t0 * NB;
     nb = local / tiles;
     i = local - nb * tiles;
   }
-  __device__ __forceinline__ void cut() {
-    tiles = (count + p.TN - 1) / p.TN;
-    per = tile_rows(count, tiles);
-  }
-  __device__ __forceinline__ bool next(Seg& s) {
-    if (left <= 0) return false;
+  __device__ __forceinline__ void fill(Seg& s) const {
     s.e = e;
     s.nb = nb;
     s.row0 = start + i * per;
     s.rows = min(per, count - i * per);
     s.tile = t0 + i;
+  }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (wave < waves) {
+      s.unit = wave++ * ctas + me;
+      locate(s.unit);
+      fill(s);
+      s.kb0 = 0;
+      s.kb1 = p.KB;
+      s.first = s.end = me;
+      return true;
+    }
+    if (left <= 0) return false;
+    if (unit < 0) {
+      const int skip = kb / p.KB;
+      unit = base + skip;
+      kb -= skip * p.KB;
+      locate(unit);
+    }
+    fill(s);
     s.unit = unit;
     s.kb0 = kb;
     s.kb1 = min(p.KB, kb + left);
+    s.first = (unit - base) * p.KB / q;
+    s.end = ((unit - base + 1) * p.KB - 1) / q;
     left -= s.kb1 - s.kb0;
     if (left > 0) {
       kb = 0;
@@ -212,6 +251,21 @@ struct Ring {
       slot = 0;
       phase ^= 1u;
     }
+  }
+};
+
+// The parts in turn, for a whole warp.
+struct Feed {
+  TileShared& sh;
+  Ring ring;
+  __device__ __forceinline__ bool next(Seg& s, volatile uint32_t* abort_flag, uint32_t* err) {
+    if (!tile_wait_warp(smem_u32(&sh.seg_full[ring.slot]), ring.phase, abort_flag, kErrTileRing, err))
+      return false;
+    s = sh.seg[ring.slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.seg_empty[ring.slot]));
+    ring.advance(kSegs);
+    return s.kb1 > 0;
   }
 };
 
@@ -348,6 +402,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(smem_u32(&sh.acc_empty[i]), F::kEpi * CG);
     }
     mbar_init(smem_u32(&sh.drain), 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_u32(&sh.seg_full[i]), 1);
+      // copies, MMAs (one CTA of a pair), conversions, epilogue
+      mbar_init(smem_u32(&sh.seg_empty[i]), 2 + (leader ? 1 : 0) + F::kConv + F::kEpi);
+    }
     fence_mbar_init();
     sh.abort = 0;
     tma_prefetch_desc(&map_x);
@@ -398,17 +457,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- weights: one elected lane of a warp that runs in step ---------------
     // (a stage's two copies come from two warps: issuing one takes some 200
     // cycles, and a wide stage lasts 384)
-    Walk<CG> walk(p, prefix, tiles);
+    Feed feed{sh};
     Seg sg;
     const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
     const uint32_t wfull0 = smem_u32(&sh.wfull[0]), empty0 = smem_u32(&sh.empty[0]);
-    // the weights of a single group need nothing of the kernel before this
-    // one: a packed weight is written at load time
-    if (p.L > 0 && !p.by_row) pdl_wait();
+    // (the weights of a single group need nothing of the kernel before this
+    // one: a packed weight is written at load time)
     Ring ring;
     int it = 0;
     bool ok = true;
-    while (ok && walk.next(sg)) {
+    while (ok && feed.next(sg, abort_flag, p.err)) {
       // (an odd last block of a pair repeats the one before and stores nothing)
       const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
       const int kb1 = uniform(sg.kb1);
@@ -426,7 +484,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const int na = uniform(adapters_of(p, sg));
+      const int na = uniform(sg.na);
+      if (na > 0) pdl_wait();
       const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
       for (int i = 0; i < na && ok; ++i) {
         const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb) *
@@ -450,14 +509,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp == 2) {
     // ---- tokens: likewise ----------------------------------------------------
     pdl_wait();
-    Walk<CG> walk(p, prefix, tiles);
+    Feed feed{sh};
     Seg sg;
     const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
     Ring ring;
     int it = 0;
     bool ok = true;
-    while (ok && walk.next(sg)) {
+    while (ok && feed.next(sg, abort_flag, p.err)) {
       const int kb1 = uniform(sg.kb1);
       const int row0 = uniform(sg.row0) + rank * (((uniform(sg.rows) + 15) & ~15) / CG);
       for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
@@ -474,7 +533,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const int rounds = uniform(adapters_of(p, sg)) * p.rank16;   // without tokens
+      const int rounds = uniform(sg.na) * p.rank16;   // without tokens
       for (int i = 0; i < rounds; ++i, ++it, ring.advance(S)) {
         ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
         if (!ok) break;
@@ -489,7 +548,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- MMAs: one elected lane of a warp that runs in step ------------------
     if (leader) {
       pdl_wait();
-      Walk<CG> walk(p, prefix, tiles);
+      Feed feed{sh};
       Seg sg;
       const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
       const uint32_t ready0 = smem_u32(&sh.ready[0]);
@@ -500,7 +559,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int it = 0, ac = 0;
       bool ok = true;
       const int chunk = uniform(chunk_stages_of<KD>(p));
-      while (ok && walk.next(sg)) {
+      while (ok && feed.next(sg, abort_flag, p.err)) {
         const uint32_t n16 = uniform((sg.rows + 15) & ~15);
         const uint32_t idesc = idesc_f16(128 * CG, n16);
         int kb = uniform(sg.kb0);
@@ -541,7 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (!ok) break;
-        const int na = uniform(adapters_of(p, sg));
+        const int na = uniform(sg.na);
         if (na > 0) {
           const uint32_t buf = ac & 1;
           ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
@@ -578,6 +637,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
     }
+  } else if (warp == 3) {
+    // ---- schedule: the parts of this CTA's units, described for the others ---
+    if (p.L > 0 && !p.by_row) pdl_wait();   // the tiles' adapters
+    Walk<CG> walk(p, prefix, tiles);
+    Ring ring;
+    bool more = true;
+    while (more) {
+      Seg sg = {};
+      more = walk.next(sg);
+      if (more) sg.na = adapters_of(p, sg);
+      if (!tile_wait_warp(smem_u32(&sh.seg_empty[ring.slot]), ring.phase ^ 1, abort_flag,
+                          kErrTileRing, p.err))
+        break;
+      if (lane == 0) {
+        sh.seg[ring.slot] = sg;
+        mbar_arrive(smem_u32(&sh.seg_full[ring.slot]));
+      }
+      __syncwarp();
+      ring.advance(kSegs);
+    }
   } else if (warp >= kFirstConv && warp < F::kFirstEpi) {
     // ---- A operand: shared memory -> f16 -> TMEM ---------------------------
     const int group = (warp - kFirstConv) >> 2;       // groups take stages in turn
@@ -585,9 +664,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t a_lane = a_base + (static_cast<uint32_t>(warp & 3) << 21);
     const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
     const uint32_t ready0 = PAIR ? map_to_cta(smem_u32(&sh.ready[0]), 0) : smem_u32(&sh.ready[0]);
-    // weights of a single group need nothing of the kernel before this one
-    if (p.L > 0 && !p.by_row) pdl_wait();
-    Walk<CG> walk(p, prefix, tiles);
+    // (waits for the kernel before this one only where adapters follow)
+    Feed feed{sh};
     Seg sg;
     Ring ring, used;   // this stage; the one whose A operand lay where this one's goes
     int it = 0;
@@ -621,7 +699,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     };
-    while (ok && walk.next(sg)) {
+    while (ok && feed.next(sg, abort_flag, p.err)) {
       for (int kb = sg.kb0; kb < sg.kb1; kb += KD, advance()) {
         if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
@@ -650,7 +728,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         announce(as);
       }
       if (!ok) break;
-      const int na = adapters_of(p, sg);
+      const int na = sg.na;
+      if (na > 0) pdl_wait();
       const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
       const int half = ((sg.rows + 15) & ~15) / CG, first = rank * half;
       const int t0 = (warp & 3) * 32 + lane;          // this thread among the group's 128
@@ -717,7 +796,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp >= F::kFirstEpi) {
     // ---- epilogue ------------------------------------------------------------
     pdl_wait();
-    Walk<CG> walk(p, prefix, tiles);
+    Feed feed{sh};
     Seg sg;
     const int ew = warp - F::kFirstEpi;
     const int quarter = warp & 3;
@@ -746,7 +825,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     int ac = 0;
     bool ok = true;
-    while (ok && walk.next(sg)) {
+    while (ok && feed.next(sg, abort_flag, p.err)) {
       const int mine = max(0, min(cols, sg.rows - col0));    // columns with a row behind them
       const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
       const int nb = sg.nb * CG + rank;
@@ -797,7 +876,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) break;
       // the MMAs' adapter term stays in its accumulator until it is used
-      const bool by_mma = adapters_of(p, sg) > 0;
+      const bool by_mma = sg.na > 0;
       const int dbuf = ac & 1;
       if (by_mma) {
         ok = __all_sync(0xffffffffu,
@@ -824,12 +903,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       };
       const bool parted = sg.kb0 != 0 || sg.kb1 != p.KB;
-      int first = me, end = me;
+      const int first = sg.first, end = sg.end;
       bool last = true;
       if (parted) {
         // this run holds part of the unit: leave it, and go on only as the last
-        first = sg.unit * p.KB / walk.q;
-        end = ((sg.unit + 1) * p.KB - 1) / walk.q;
         int32_t* part = part_at(me, me == first ? 1 : 0);
         int32_t* dpart = part_at(me, 2);
 #pragma unroll 1
