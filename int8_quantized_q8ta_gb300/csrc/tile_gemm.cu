@@ -254,18 +254,22 @@ struct Ring {
   }
 };
 
-// The parts in turn, for a whole warp.
+// The parts in turn, for a whole warp; a part stays where it is, in shared
+// memory, until the next is asked for.
 struct Feed {
   TileShared& sh;
   Ring ring;
-  __device__ __forceinline__ bool next(Seg& s, volatile uint32_t* abort_flag, uint32_t* err) {
-    if (!tile_wait_warp(smem_u32(&sh.seg_full[ring.slot]), ring.phase, abort_flag, kErrTileRing, err))
-      return false;
-    s = sh.seg[ring.slot];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.seg_empty[ring.slot]));
+  int last = -1;
+  __device__ __forceinline__ const Seg* next(volatile uint32_t* abort_flag, uint32_t* err) {
+    if (last >= 0) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.seg_empty[last]));
+    }
+    last = ring.slot;
+    if (!tile_wait_warp(smem_u32(&sh.seg_full[last]), ring.phase, abort_flag, kErrTileRing, err))
+      return nullptr;
     ring.advance(kSegs);
-    return s.kb1 > 0;
+    return sh.seg[last].kb1 > 0 ? &sh.seg[last] : nullptr;
   }
 };
 
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // (a stage's two copies come from two warps: issuing one takes some 200
     // cycles, and a wide stage lasts 384)
     Feed feed{sh};
-    Seg sg;
+    const Seg* sg;
     const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
     const uint32_t wfull0 = smem_u32(&sh.wfull[0]), empty0 = smem_u32(&sh.empty[0]);
     // (the weights of a single group need nothing of the kernel before this
@@ -466,12 +470,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Ring ring;
     int it = 0;
     bool ok = true;
-    while (ok && feed.next(sg, abort_flag, p.err)) {
+    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
       // (an odd last block of a pair repeats the one before and stores nothing)
-      const int nb = min(uniform(sg.nb) * CG + rank, p.NB - 1);
-      const int kb1 = uniform(sg.kb1);
-      const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg.e)) * p.NB + nb) * w_rows;
-      for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
+      const int nb = min(uniform(sg->nb) * CG + rank, p.NB - 1);
+      const int kb1 = uniform(sg->kb1);
+      const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg->e)) * p.NB + nb) * w_rows;
+      for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
         const uint32_t bytes = min(KD, kb1 - kb) * kTileWBytes;
         ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
         if (!ok) break;
@@ -484,9 +488,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const int na = uniform(sg.na);
+      const int na = uniform(sg->na);
       if (na > 0) pdl_wait();
-      const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
+      const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
       for (int i = 0; i < na && ok; ++i) {
         const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb) *
                                         p.rank16) * 4096;
@@ -510,16 +514,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- tokens: likewise ----------------------------------------------------
     pdl_wait();
     Feed feed{sh};
-    Seg sg;
+    const Seg* sg;
     const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
     Ring ring;
     int it = 0;
     bool ok = true;
-    while (ok && feed.next(sg, abort_flag, p.err)) {
-      const int kb1 = uniform(sg.kb1);
-      const int row0 = uniform(sg.row0) + rank * (((uniform(sg.rows) + 15) & ~15) / CG);
-      for (int kb = uniform(sg.kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
+    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+      const int kb1 = uniform(sg->kb1);
+      const int row0 = uniform(sg->row0) + rank * (((uniform(sg->rows) + 15) & ~15) / CG);
+      for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
         ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
         if (!ok) break;
         if (elect_one()) {
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const int rounds = uniform(sg.na) * p.rank16;   // without tokens
+      const int rounds = uniform(sg->na) * p.rank16;   // without tokens
       for (int i = 0; i < rounds; ++i, ++it, ring.advance(S)) {
         ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
         if (!ok) break;
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (leader) {
       pdl_wait();
       Feed feed{sh};
-      Seg sg;
+      const Seg* sg;
       const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
       const uint32_t ready0 = smem_u32(&sh.ready[0]);
       const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
@@ -559,11 +563,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int it = 0, ac = 0;
       bool ok = true;
       const int chunk = uniform(chunk_stages_of<KD>(p));
-      while (ok && feed.next(sg, abort_flag, p.err)) {
-        const uint32_t n16 = uniform((sg.rows + 15) & ~15);
+      while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+        const uint32_t n16 = uniform((sg->rows + 15) & ~15);
         const uint32_t idesc = idesc_f16(128 * CG, n16);
-        int kb = uniform(sg.kb0);
-        const int kb1 = uniform(sg.kb1);
+        int kb = uniform(sg->kb0);
+        const int kb1 = uniform(sg->kb1);
         const int stages = (kb1 - kb + KD - 1) / KD;
         for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
           const uint32_t buf = ac & 1;
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (!ok) break;
-        const int na = uniform(sg.na);
+        const int na = uniform(sg->na);
         if (na > 0) {
           const uint32_t buf = ac & 1;
           ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
@@ -666,7 +670,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t ready0 = PAIR ? map_to_cta(smem_u32(&sh.ready[0]), 0) : smem_u32(&sh.ready[0]);
     // (waits for the kernel before this one only where adapters follow)
     Feed feed{sh};
-    Seg sg;
+    const Seg* sg;
     Ring ring, used;   // this stage; the one whose A operand lay where this one's goes
     int it = 0;
     bool ok = true;
@@ -699,15 +703,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     };
-    while (ok && feed.next(sg, abort_flag, p.err)) {
-      for (int kb = sg.kb0; kb < sg.kb1; kb += KD, advance()) {
+    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+      for (int kb = sg->kb0; kb < sg->kb1; kb += KD, advance()) {
         if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
         ok = __all_sync(0xffffffffu, tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase,
                                                abort_flag, kErrTileRing, p.err));
         if (!ok) break;
         const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
-        const bool two = KD == 2 && kb + 1 < sg.kb1;
+        const bool two = KD == 2 && kb + 1 < sg->kb1;
         uint4 v[4], v1[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] = lds128(w + c * 2048);
@@ -728,10 +732,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         announce(as);
       }
       if (!ok) break;
-      const int na = sg.na;
+      const int na = sg->na;
       if (na > 0) pdl_wait();
-      const int32_t* list = p.lists + static_cast<int64_t>(sg.tile) * p.list_stride + 1;
-      const int half = ((sg.rows + 15) & ~15) / CG, first = rank * half;
+      const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
+      const int half = ((sg->rows + 15) & ~15) / CG, first = rank * half;
       const int t0 = (warp & 3) * 32 + lane;          // this thread among the group's 128
       for (int i = 0; i < na && ok; ++i) {
         const int a_id = __ldg(list + i);
@@ -768,9 +772,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // where the row has another adapter
           for (int t = t0; t < half; t += 128) {
             const int s = first + t;
-            const bool mine = s < sg.rows && __ldg(p.ids + sg.row0 + s) == a_id;
+            const bool mine = s < sg->rows && __ldg(p.ids + sg->row0 + s) == a_id;
             const float4* h = reinterpret_cast<const float4*>(
-                p.h + static_cast<int64_t>(sg.row0 + s) * p.rank16 * 16 + c * 16);
+                p.h + static_cast<int64_t>(sg->row0 + s) * p.rank16 * 16 + c * 16);
             const uint32_t at = st + t * 128;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- epilogue ------------------------------------------------------------
     pdl_wait();
     Feed feed{sh};
-    Seg sg;
+    const Seg* sg;
     const int ew = warp - F::kFirstEpi;
     const int quarter = warp & 3;
     // columns of this warp: an equal share of the tile's, in steps of 16
@@ -825,18 +829,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     int ac = 0;
     bool ok = true;
-    while (ok && feed.next(sg, abort_flag, p.err)) {
-      const int mine = max(0, min(cols, sg.rows - col0));    // columns with a row behind them
-      const int stages = (sg.kb1 - sg.kb0 + KD - 1) / KD;
-      const int nb = sg.nb * CG + rank;
+    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+      const int mine = max(0, min(cols, sg->rows - col0));    // columns with a row behind them
+      const int stages = (sg->kb1 - sg->kb0 + KD - 1) / KD;
+      const int nb = sg->nb * CG + rank;
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
-      const bool by_row = p.by_row && sg.kb1 == p.KB;
+      const bool by_row = p.by_row && sg->kb1 == p.KB;
       if (by_row) {
         // the adapters' lines of these channels on their way before the first
         // is used: eight lanes a row, 4 lines of 128 bytes to each 8 ranks
         for (int j = 0; j < mine; j += 4) {
-          const int a = __ldg(p.ids + sg.row0 + min(col0 + j + (lane >> 3), sg.rows - 1));
+          const int a = __ldg(p.ids + sg->row0 + min(col0 + j + (lane >> 3), sg->rows - 1));
           if (a >= 0 && a < p.L)
             for (int c = 0; c < p.rank16; ++c)
               prefetch_l2(p.lora_b +
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int j = 0; j < mine; j += 8) {
           // (rows past the tile's end repeat its last)
-          const int my_s = sg.row0 + min(col0 + j + (lane & 7), sg.rows - 1);
+          const int my_s = sg->row0 + min(col0 + j + (lane & 7), sg->rows - 1);
           float d[8];
           row_deltas(p, min(nb, p.NB - 1), quarter * 32 + lane, __ldg(p.ids + my_s), my_s,
                      sh.corner[ew], d);
@@ -876,7 +880,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) break;
       // the MMAs' adapter term stays in its accumulator until it is used
-      const bool by_mma = sg.na > 0;
+      const bool by_mma = sg->na > 0;
       const int dbuf = ac & 1;
       if (by_mma) {
         ok = __all_sync(0xffffffffu,
@@ -902,8 +906,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int j = 0; j < 16; ++j) acc[kCols - 16 + j] = t[j];
         }
       };
-      const bool parted = sg.kb0 != 0 || sg.kb1 != p.KB;
-      const int first = sg.first, end = sg.end;
+      const bool parted = sg->kb0 != 0 || sg->kb1 != p.KB;
+      const int first = sg->first, end = sg->end;
       bool last = true;
       if (parted) {
         // this run holds part of the unit: leave it, and go on only as the last
@@ -939,14 +943,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (last) {
         const int n = nb * 128 + quarter * 32 + lane;
         const bool in = n < p.N;
-        const int64_t en = static_cast<int64_t>(sg.e) * p.N + n;
+        const int64_t en = static_cast<int64_t>(sg->e) * p.N + n;
         const float ws = in ? __ldg(p.ws + en) : 0.0f;
         const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
         // the unit's adapter term: in this CTA's TMEM, or left by the CTA
         // that ran the unit's end
         const bool other_d =
             !has_d && p.L > 0 &&
-            (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg.tile) * p.list_stride) > 0);
+            (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg->tile) * p.list_stride) > 0);
 #pragma unroll 1
         for (int b = 0; b < kCols / 16; ++b) {
           if (b * 16 < mine) {
@@ -983,7 +987,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               v[j] = dequant(acc[j], ws, bias, __uint_as_float(r[j]), p.rq);
-            const int s0 = sg.row0 + col0 + b * 16;
+            const int s0 = sg->row0 + col0 + b * 16;
             const int rows = in ? mine - b * 16 : 0;
             if (p.out_rows == nullptr) {
               OutPtr<OUT> to(p.out, static_cast<int64_t>(s0) * p.N + n);
