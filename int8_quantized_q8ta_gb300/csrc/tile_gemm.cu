@@ -59,6 +59,11 @@ constexpr int kTmemCols = 512;
 // Stages of A operands in tensor memory, behind the two accumulators.
 constexpr int NAb = 2, NA = 1 << NAb;
 
+// What joining the parts of cut units costs a run, in k-blocks' time (4,000 to
+// 6,000 cycles against 350 a narrow k-block, 10,000 to 14,000 against 400 a
+// wide one).
+constexpr int kJoinNarrow = 14, kJoinWide = 28;
+
 // The two forms of the kernel.
 //   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
 // a tile through the 2-SM MMA, each with its own 128 output channels and half
@@ -76,6 +81,7 @@ struct Form {
   static constexpr int kGroups = kConv / 4;        // groups of four take turns
   static constexpr int kEpi = PAIR ? 12 : 8;       // epilogue warps
   static constexpr int kCols = PAIR ? 64 : 32;     // accumulator columns of each
+  static constexpr int kRing = PAIR ? kMaxRing : 6;   // stages at most
   static constexpr int kFirstEpi = kFirstConv + kConv;
   static_assert(32 * (kFirstEpi + kEpi) == kTileThreads, "one block size");
   static constexpr int kMaxRows = kCols * kEpi / 4;
@@ -160,6 +166,9 @@ struct Walk {
     base = waves * ctas;
     const int total = (units - base) * p.KB;
     q = max(p.min_run, (total - 1) / ctas + 1);
+    // whole units where cutting them would not gain what joining parts costs
+    const int whole = (units - base + ctas - 1) / ctas * p.KB;
+    if (whole <= q + (CG == 1 ? kJoinNarrow : kJoinWide)) q = max(whole, 1);
     kb = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * me));
     left = min(total - kb, q);
     unit = -1;             // the run is not begun
@@ -578,11 +587,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int c1 = min(stages, c0 + chunk);
           for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
             const uint32_t as = it & (NA - 1);
-            ok = tile_wait_warp(tfull0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing,
-                                p.err) &&
-                 tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
-                                p.err);
-            if (!ok) break;
+            const uint32_t tfull = tfull0 + ring.slot * 8, ready = ready0 + as * 8;
+            const uint32_t rphase = (it >> NAb) & 1;
+            const bool here = mbar_try_wait(tfull, ring.phase), done = mbar_try_wait(ready, rphase);
+            if (!__all_sync(0xffffffffu, here && done)) {
+              ok = tile_wait_warp(tfull, ring.phase, abort_flag, kErrTileRing, p.err) &&
+                   tile_wait_warp(ready, rphase, abort_flag, kErrTileOperand, p.err);
+              if (!ok) break;
+            }
             tc_fence_after();
             const uint32_t st = ring0 + ring.slot * stage_bytes;
             const bool two = KD == 2 && kb + 1 < kb1;
@@ -707,8 +719,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int kb = sg->kb0; kb < sg->kb1; kb += KD, advance()) {
         if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
-        ok = __all_sync(0xffffffffu, tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase,
-                                               abort_flag, kErrTileRing, p.err));
+        // The place first: it is free once the MMAs of the stage NA back are
+        // done, so the slot's last weights, S >= NA stages back, have landed,
+        // and the parity below cannot be that of the round before them (which a
+        // group that leaves every other stage to its partner has not seen).
+        ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
+                                       kErrTileRing, p.err);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
         const bool two = KD == 2 && kb + 1 < sg->kb1;
@@ -721,8 +738,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         uint32_t r[32];
         convert(v, r);
-        ok = __all_sync(0xffffffffu, place_free());
-        if (!ok) break;
         tc_fence_after();
         tmem_st_32cols(a_lane + as * KD * 32, r);
         if (two) {
@@ -742,9 +757,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int c = 0; c < p.rank16; ++c, advance()) {
           if (F::kGroups == 2 && (it & 1) != group) continue;
           const int as = it & (NA - 1);
-          ok = tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag, kErrTileRing,
-                         p.err) &&
-               place_free();
+          ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
+                                         kErrTileRing, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -799,7 +813,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= F::kFirstEpi) {
     // ---- epilogue ------------------------------------------------------------
-    pdl_wait();
     Feed feed{sh};
     const Seg* sg;
     const int ew = warp - F::kFirstEpi;
@@ -827,26 +840,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       return p.parts + (static_cast<int64_t>(cluster * CG + rank) * 3 + which) * F::kPart +
              ew * (kCols * 32) + lane * 4;
     };
+    // The adapters' lines of a part's channels on their way to L2 before they
+    // are used: eight lanes a row, 4 lines of 128 bytes to each 8 ranks
+    const auto fetch_adapters = [&](const Seg* part, int mine, int nb) {
+      for (int j = 0; j < mine; j += 4) {
+        const int a = __ldg(p.ids + part->row0 + min(col0 + j + (lane >> 3), part->rows - 1));
+        if (a >= 0 && a < p.L)
+          for (int c = 0; c < p.rank16; ++c)
+            prefetch_l2(p.lora_b +
+                        ((static_cast<int64_t>(a) * p.NB + min(nb, p.NB - 1)) * p.rank16 + c) * 4096 +
+                        ((lane >> 2) & 1) * 2048 + quarter * 512 + (lane & 3) * 128);
+      }
+    };
     int ac = 0;
-    bool ok = true;
+    bool ok = true, first_seg = true;
     while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
       const int mine = max(0, min(cols, sg->rows - col0));    // columns with a row behind them
       const int stages = (sg->kb1 - sg->kb0 + KD - 1) / KD;
       const int nb = sg->nb * CG + rank;
+      if (first_seg) {
+        // for the first part even before the kernel before this one is done:
+        // whatever its ids then are, a prefetch changes no result
+        if (p.by_row && sg->kb1 == p.KB) fetch_adapters(sg, mine, nb);
+        pdl_wait();
+      }
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
       const bool by_row = p.by_row && sg->kb1 == p.KB;
       if (by_row) {
-        // the adapters' lines of these channels on their way before the first
-        // is used: eight lanes a row, 4 lines of 128 bytes to each 8 ranks
-        for (int j = 0; j < mine; j += 4) {
-          const int a = __ldg(p.ids + sg->row0 + min(col0 + j + (lane >> 3), sg->rows - 1));
-          if (a >= 0 && a < p.L)
-            for (int c = 0; c < p.rank16; ++c)
-              prefetch_l2(p.lora_b +
-                          ((static_cast<int64_t>(a) * p.NB + min(nb, p.NB - 1)) * p.rank16 + c) * 4096 +
-                          ((lane >> 2) & 1) * 2048 + quarter * 512 + (lane & 3) * 128);
-        }
+        if (!first_seg) fetch_adapters(sg, mine, nb);
         for (int j = 0; j < mine; j += 8) {
           // (rows past the tile's end repeat its last)
           const int my_s = sg->row0 + min(col0 + j + (lane & 7), sg->rows - 1);
@@ -1006,7 +1028,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (by_mma) release(dbuf);
+      first_seg = false;
     }
+    if (first_seg) pdl_wait();
     // rows of dropped slots hold zeros
     if (prefix != nullptr) {
       const int64_t step = static_cast<int64_t>(gridDim.x) * F::kEpi * 32;
@@ -1084,7 +1108,7 @@ cudaError_t launch_form(TileParams p, const void* operand, q8_dtype out_dtype, c
   if (!encode_bf16_tmap(&map, operand, 3, dims, str, box)) return cudaErrorInvalidValue;
   const size_t stage = static_cast<size_t>(F::KD) * (p.TN / F::CG * 128 + kTileWBytes);
   const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
-  p.stages = static_cast<int>(std::min<size_t>(kMaxRing, (kTileSmem - 1024 - table) / stage));
+  p.stages = static_cast<int>(std::min<size_t>(F::kRing, (kTileSmem - 1024 - table) / stage));
   const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
   switch (out_dtype) {
     case Q8_I8: return launch_one<Q8_I8, PAIR>(map, p, smem, s);
