@@ -7,13 +7,30 @@ Argument marshalling only, like the rest of the package; imported by it.
 from __future__ import annotations
 
 import dataclasses
+import functools
 from typing import Optional, Tuple
 
 import torch
 
-from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _ptr, _stream, _workspace
+from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _workspace
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+
+
+# These calls are short on the GPU (some 5 to 20 us), so the host's part is
+# kept short too: addresses go to ctypes as plain integers, one combined check
+# a tensor (the slow one, which names what is wrong, only where it fails), the
+# stream's raw handle, sizes of workspaces remembered by shape.
+
+def _arg(t: torch.Tensor, dtype, name: str) -> int:
+    """The address of a contiguous CUDA tensor of this dtype."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        _need(t, dtype, name)
+    return t.data_ptr()
+
+
+def _stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -26,7 +43,7 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
 
 
 def _shape(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -36,6 +53,12 @@ def _out(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out") -
     _need(out, dtype, name)
     _shape(out, shape, name)
     return out
+
+
+def _space(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace(nbytes, device, workspace)
 
 
 @dataclasses.dataclass
@@ -59,14 +82,18 @@ class ExpertRoute:
         return self.offsets.shape[0] - 1
 
 
-def _need_route(route: ExpertRoute) -> ExpertRoute:
-    _need(route.order, torch.int32, "route.order")
-    _need(route.position, torch.int32, "route.position")
-    _need(route.offsets, torch.int32, "route.offsets")
-    if route.position.dim() != 2 or route.offsets.dim() != 1 or route.E < 1:
+def _route_args(route: ExpertRoute):
+    """(T, k, E) and the addresses of order, position and offsets."""
+    order, position, offsets = route.order, route.position, route.offsets
+    o = _arg(order, torch.int32, "route.order")
+    p = _arg(position, torch.int32, "route.position")
+    f = _arg(offsets, torch.int32, "route.offsets")
+    shape, bounds = position.shape, offsets.shape
+    if len(shape) != 2 or len(bounds) != 1 or bounds[0] < 2:
         raise ValueError("route.position must be [T, k] and route.offsets [E + 1]")
-    _shape(route.order, (route.T * route.k,), "route.order")
-    return route
+    T, k = shape
+    _shape(order, (T * k,), "route.order")
+    return T, k, bounds[0] - 1, o, p, f
 
 
 def _empty_route(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
@@ -75,11 +102,11 @@ def _empty_route(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
         raise ValueError(f"expert_ids must be [T, k], got {tuple(expert_ids.shape)}")
     if not 1 <= num_experts <= 1024:
         raise ValueError(f"num_experts must lie in [1, 1024], got {num_experts}")
-    # one allocation for the three parts, each of them contiguous
     T, k = expert_ids.shape
-    R = T * k
-    buf = torch.empty(2 * R + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
-    return ExpertRoute(buf[:R], buf[R:2 * R].view(T, k), buf[2 * R:])
+    dev = expert_ids.device
+    return ExpertRoute(torch.empty(T * k, dtype=torch.int32, device=dev),
+                       torch.empty((T, k), dtype=torch.int32, device=dev),
+                       torch.empty(num_experts + 1, dtype=torch.int32, device=dev))
 
 
 def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
@@ -87,9 +114,9 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
     [0, num_experts) are dropped slots."""
     route = _empty_route(expert_ids, num_experts)
     T, k = expert_ids.shape
-    _check(_lib.q8_expert_sort(_ptr(expert_ids), T, k, num_experts, _ptr(route.order),
-                               _ptr(route.position), _ptr(route.offsets), _stream(expert_ids)),
-           "q8_expert_sort")
+    _check(_lib.q8_expert_sort(expert_ids.data_ptr(), T, k, num_experts, route.order.data_ptr(),
+                               route.position.data_ptr(), route.offsets.data_ptr(),
+                               _stream(expert_ids)), "q8_expert_sort")
     return route
 
 
@@ -98,15 +125,14 @@ def expert_gather(x: torch.Tensor, route: ExpertRoute,
     """Rows of x [T, H] (float32, float16, bfloat16 or int8) in sorted order,
     [T*k, H]; zeros from row offsets[E] on."""
     code = _dtype_code(x, "x")
-    _need(x, x.dtype, "x")
-    _need_route(route)
-    T, k = route.T, route.k
+    at = _arg(x, x.dtype, "x")
+    T, k, E, _, position, offsets = _route_args(route)
     if x.dim() != 2 or x.shape[0] != T:
         raise ValueError(f"x must be [{T}, H], got {tuple(x.shape)}")
     H = x.shape[1]
     out = _out(out, (T * k, H), x.dtype, x.device)
-    _check(_lib.q8_expert_gather(_ptr(x), code, T, k, H, route.E, _ptr(route.position),
-                                 _ptr(route.offsets), _ptr(out), _stream(x)), "q8_expert_gather")
+    _check(_lib.q8_expert_gather(at, code, T, k, H, E, position, offsets, out.data_ptr(),
+                                 _stream(x)), "q8_expert_gather")
     return out
 
 
@@ -114,72 +140,66 @@ def expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: int,
                     out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ExpertRoute]:
     """expert_sort, then expert_gather: returns (rows, route)."""
     code = _dtype_code(x, "x")
-    _need(x, x.dtype, "x")
+    at = _arg(x, x.dtype, "x")
     route = _empty_route(expert_ids, num_experts)
     T, k = expert_ids.shape
     if x.dim() != 2 or x.shape[0] != T:
         raise ValueError(f"x must be [{T}, H], got {tuple(x.shape)}")
     H = x.shape[1]
     out = _out(out, (T * k, H), x.dtype, x.device)
-    _check(_lib.q8_expert_dispatch(_ptr(x), code, T, H, _ptr(expert_ids), k, num_experts,
-                                   _ptr(route.order), _ptr(route.position), _ptr(route.offsets),
-                                   _ptr(out), _stream(x)), "q8_expert_dispatch")
+    _check(_lib.q8_expert_dispatch(at, code, T, H, expert_ids.data_ptr(), k, num_experts,
+                                   route.order.data_ptr(), route.position.data_ptr(),
+                                   route.offsets.data_ptr(), out.data_ptr(), _stream(x)),
+           "q8_expert_dispatch")
     return out, route
 
 
-def _need_rows(t: torch.Tensor, route: ExpertRoute, name: str) -> int:
+def _rows_arg(t: torch.Tensor, rows: int, name: str):
+    """(dtype code, address, H) of sorted rows [rows, H]."""
     code = _dtype_code(t, name)
-    _need(t, t.dtype, name)
-    if t.dim() != 2 or t.shape[0] != route.T * route.k:
-        raise ValueError(f"{name} must be [{route.T * route.k}, H], got {tuple(t.shape)}")
-    return code
+    at = _arg(t, t.dtype, name)
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, H], got {tuple(t.shape)}")
+    return code, at, t.shape[1]
 
 
 def expert_gather_backward(d_rows: torch.Tensor, route: ExpertRoute,
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gather's gradient: each token's kept rows added up in f32, [T, H]."""
-    _need_route(route)
-    code = _need_rows(d_rows, route, "d_rows")
-    T, k, H = route.T, route.k, d_rows.shape[1]
+    T, k, _, _, position, _ = _route_args(route)
+    code, at, H = _rows_arg(d_rows, T * k, "d_rows")
     out = _out(out, (T, H), d_rows.dtype, d_rows.device)
-    _check(_lib.q8_expert_gather_backward(_ptr(d_rows), code, T, k, H, _ptr(route.position),
-                                          _ptr(out), _stream(d_rows)),
-           "q8_expert_gather_backward")
+    _check(_lib.q8_expert_gather_backward(at, code, T, k, H, position, out.data_ptr(),
+                                          _stream(d_rows)), "q8_expert_gather_backward")
     return out
-
-
-def _need_weights(weights: torch.Tensor, route: ExpertRoute) -> None:
-    _need(weights, torch.float32, "weights")
-    _shape(weights, (route.T, route.k), "weights")
 
 
 def expert_combine(z: torch.Tensor, weights: torch.Tensor, route: ExpertRoute,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] * (slot (t, j)'s row of z), [T, H]."""
-    _need_route(route)
-    code = _need_rows(z, route, "z")
-    _need_weights(weights, route)
-    T, k, H = route.T, route.k, z.shape[1]
+    T, k, _, _, position, _ = _route_args(route)
+    code, at, H = _rows_arg(z, T * k, "z")
+    w = _arg(weights, torch.float32, "weights")
+    _shape(weights, (T, k), "weights")
     out = _out(out, (T, H), z.dtype, z.device)
-    _check(_lib.q8_expert_combine(_ptr(z), code, _ptr(weights), T, k, H, _ptr(route.position),
-                                  _ptr(out), _stream(z)), "q8_expert_combine")
+    _check(_lib.q8_expert_combine(at, code, w, T, k, H, position, out.data_ptr(), _stream(z)),
+           "q8_expert_combine")
     return out
 
 
 def expert_combine_backward(dy: torch.Tensor, z: torch.Tensor, weights: torch.Tensor,
                             route: ExpertRoute) -> Tuple[torch.Tensor, torch.Tensor]:
     """The combine's gradients (dz like z, dweights float32 [T, k])."""
-    _need_route(route)
-    code = _need_rows(z, route, "z")
-    _need_weights(weights, route)
-    _need(dy, z.dtype, "dy")
-    T, k, H = route.T, route.k, z.shape[1]
+    T, k, E, _, position, offsets = _route_args(route)
+    code, at, H = _rows_arg(z, T * k, "z")
+    w = _arg(weights, torch.float32, "weights")
+    _shape(weights, (T, k), "weights")
+    g = _arg(dy, z.dtype, "dy")
     _shape(dy, (T, H), "dy")
-    dz = torch.empty_like(z)
+    dz = torch.empty((T * k, H), dtype=z.dtype, device=z.device)
     dw = torch.empty((T, k), dtype=torch.float32, device=z.device)
-    _check(_lib.q8_expert_combine_backward(_ptr(dy), _ptr(z), code, _ptr(weights), T, k, H,
-                                           route.E, _ptr(route.position), _ptr(route.offsets),
-                                           _ptr(dz), _ptr(dw), _stream(z)),
+    _check(_lib.q8_expert_combine_backward(g, at, code, w, T, k, H, E, position, offsets,
+                                           dz.data_ptr(), dw.data_ptr(), _stream(z)),
            "q8_expert_combine_backward")
     return dz, dw
 
@@ -208,9 +228,30 @@ def pack_tile_weight(weight: torch.Tensor) -> PackedTileWeight:
     if nbytes == 0:
         raise Q8Error(Q8_ERR_SHAPE, "q8_tile_packed_weight_bytes")
     buf = torch.empty(nbytes, dtype=torch.uint8, device=weight.device)
-    _check(_lib.q8_tile_pack_weight(_ptr(weight), E, N, K, _ptr(buf), nbytes, _stream(weight)),
+    _check(_lib.q8_tile_pack_weight(weight.data_ptr(), E, N, K, buf.data_ptr(), nbytes, _stream(weight)),
            "q8_tile_pack_weight")
     return PackedTileWeight(buf, E, N, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_space(R: int, K: int, E: int) -> int:
+    return _lib.q8_linear_experts_workspace_bytes(R, K, E)
+
+
+def _out_code(out_dtype) -> int:
+    code = _DTYPE.get(out_dtype)
+    if code is None:
+        raise TypeError(f"out_dtype must be float32, float16, bfloat16 or int8, got {out_dtype}")
+    return code
+
+
+def _vector_arg(t: Optional[torch.Tensor], shape, name: str) -> int:
+    """The address of a float32 tensor of this shape, 0 for None."""
+    if t is None:
+        return 0
+    at = _arg(t, torch.float32, name)
+    _shape(t, shape, name)
+    return at
 
 
 def linear_experts(x, input_scale, input_zero_point, packed: PackedTileWeight, weight_scales, bias,
@@ -219,27 +260,24 @@ def linear_experts(x, input_scale, input_zero_point, packed: PackedTileWeight, w
     """Sorted rows times the int8 weight of their expert (see
     q8_linear_experts): int8 x [T, K], or [T*k, K] in sorted order with
     ``x_sorted``; weight_scales and bias float32 [E, N]; out [T*k, N]."""
-    _need(x, torch.int8, "x")
-    _need_route(route)
-    T, k, E, N = route.T, route.k, packed.E, packed.N
-    if route.E != E:
-        raise ValueError(f"the route has {route.E} experts, the packed weight {E}")
-    _shape(x, (T * k if x_sorted else T, packed.K), "x")
+    at = _arg(x, torch.int8, "x")
+    T, k, E, order, _, offsets = _route_args(route)
+    N, K = packed.N, packed.K
+    if packed.E != E:
+        raise ValueError(f"the route has {E} experts, the packed weight {packed.E}")
+    _shape(x, (T * k if x_sorted else T, K), "x")
     _need(weight_scales, torch.float32, "weight_scales")
-    _shape(weight_scales, (E, N), "weight_scales")
-    if bias is not None:
-        _need(bias, torch.float32, "bias")
-        _shape(bias, (E, N), "bias")
-    if out_dtype not in _DTYPE:
-        raise TypeError(f"out_dtype must be float32, float16, bfloat16 or int8, got {out_dtype}")
+    scales = _vector_arg(weight_scales, (E, N), "weight_scales")
+    b = _vector_arg(bias, (E, N), "bias")
+    code = _out_code(out_dtype)
     out = _out(out, (T * k, N), out_dtype, x.device)
-    nbytes = _lib.q8_linear_experts_workspace_bytes(T * k, packed.K, E)
-    ws = _workspace(nbytes, x.device, workspace)
+    nbytes = _experts_space(T * k, K, E)
+    ws = _space(nbytes, x.device, workspace)
     _check(_lib.q8_linear_experts(
-        _ptr(x), int(x_sorted), T, k, packed.K, float(input_scale), int(input_zero_point),
-        _ptr(packed.data), E, N, _ptr(weight_scales), _ptr(bias), _ptr(route.order),
-        _ptr(route.offsets), float(output_scale), int(output_zero_point), activation.encode(),
-        _DTYPE[out_dtype], _ptr(out), _ptr(ws), nbytes, _stream(x)), "q8_linear_experts")
+        at, int(x_sorted), T, k, K, float(input_scale), int(input_zero_point),
+        packed.data.data_ptr(), E, N, scales, b, order, offsets, float(output_scale),
+        int(output_zero_point), activation.encode(), code, out.data_ptr(), ws.data_ptr(), nbytes,
+        _stream(x)), "q8_linear_experts")
     return out
 
 
@@ -277,9 +315,14 @@ def pack_lora(A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor) -> Packed
     if nbytes == 0:
         raise Q8Error(Q8_ERR_SHAPE, "q8_lora_packed_bytes")
     buf = torch.empty(nbytes, dtype=torch.uint8, device=A.device)
-    _check(_lib.q8_lora_pack(_ptr(A), _ptr(B), _ptr(scaling), _DTYPE[A.dtype], L, r, N, K,
-                             _ptr(buf), nbytes, _stream(A)), "q8_lora_pack")
+    _check(_lib.q8_lora_pack(A.data_ptr(), B.data_ptr(), scaling.data_ptr(), _DTYPE[A.dtype], L, r, N, K,
+                             buf.data_ptr(), nbytes, _stream(A)), "q8_lora_pack")
     return PackedLora(buf, L, N, K, r, A.dtype)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_space(M: int, K: int, L: int, r: int) -> int:
+    return _lib.q8_linear_lora_workspace_bytes(M, K, L, r)
 
 
 def linear_lora(x, input_scale, input_zero_point, packed: PackedTileWeight, weight_scales, bias,
@@ -288,30 +331,27 @@ def linear_lora(x, input_scale, input_zero_point, packed: PackedTileWeight, weig
     """int8 x [M, K] times a shared int8 weight [N, K], plus each row's
     low-rank adapter (see q8_linear_lora): adapter_ids int32 [M], ids outside
     [0, L) for none; weight_scales and bias float32 [N]; out [M, N]."""
-    _need(x, torch.int8, "x")
+    at = _arg(x, torch.int8, "x")
+    N, K = packed.N, packed.K
     if packed.E != 1:
         raise ValueError(f"the packed weight has {packed.E} groups, the shared projection one")
-    N, K = packed.N, packed.K
     if (lora.N, lora.K) != (N, K):
         raise ValueError(f"adapters are for {lora.N}x{lora.K}, the weight is {N}x{K}")
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M, {K}], got {tuple(x.shape)}")
     M = x.shape[0]
     _need(weight_scales, torch.float32, "weight_scales")
-    _shape(weight_scales, (N,), "weight_scales")
-    if bias is not None:
-        _need(bias, torch.float32, "bias")
-        _shape(bias, (N,), "bias")
-    _need(adapter_ids, torch.int32, "adapter_ids")
+    scales = _vector_arg(weight_scales, (N,), "weight_scales")
+    b = _vector_arg(bias, (N,), "bias")
+    ids = _arg(adapter_ids, torch.int32, "adapter_ids")
     _shape(adapter_ids, (M,), "adapter_ids")
-    if out_dtype not in _DTYPE:
-        raise TypeError(f"out_dtype must be float32, float16, bfloat16 or int8, got {out_dtype}")
+    code = _out_code(out_dtype)
     out = _out(out, (M, N), out_dtype, x.device)
-    nbytes = _lib.q8_linear_lora_workspace_bytes(M, K, lora.L, lora.r)
-    ws = _workspace(nbytes, x.device, workspace)
+    nbytes = _lora_space(M, K, lora.L, lora.r)
+    ws = _space(nbytes, x.device, workspace)
     _check(_lib.q8_linear_lora(
-        _ptr(x), M, K, float(input_scale), int(input_zero_point), _ptr(packed.data), N,
-        _ptr(weight_scales), _ptr(bias), _ptr(lora.data), _DTYPE[lora.dtype], lora.L, lora.r,
-        _ptr(adapter_ids), float(output_scale), int(output_zero_point), activation.encode(),
-        _DTYPE[out_dtype], _ptr(out), _ptr(ws), nbytes, _stream(x)), "q8_linear_lora")
+        at, M, K, float(input_scale), int(input_zero_point), packed.data.data_ptr(), N, scales, b,
+        lora.data.data_ptr(), _DTYPE[lora.dtype], lora.L, lora.r, ids, float(output_scale),
+        int(output_zero_point), activation.encode(), code, out.data_ptr(), ws.data_ptr(), nbytes,
+        _stream(x)), "q8_linear_lora")
     return out
