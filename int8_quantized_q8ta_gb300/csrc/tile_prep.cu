@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "rows_internal.h"
 #include "tile_device.cuh"
@@ -52,53 +53,80 @@ __global__ void __launch_bounds__(256) pack_tile_weight_kernel(const int8_t* __r
   }
 }
 
-// Eight inputs of one row per item.
-__device__ __forceinline__ void operand_item(const OperandJob& job, int64_t i, bool vec,
-                                             __half2 minus) {
-  // consecutive items: the 8 chunks of a row's 64 inputs, then the next k-block
-  const int per_row = job.KB * 8;
-  const int64_t s = i / per_row;
-  const int c = static_cast<int>(i - s * per_row);
+// The row of x behind sorted row s, or -1.
+__device__ __forceinline__ int64_t operand_row(const OperandJob& job, int64_t s) {
   int64_t row = s;
   if (job.order != nullptr) {
     const int slot = __ldg(job.order + s);
-    if (slot < 0) return;
-    row = slot / job.k;
+    if (slot < 0) return -1;
+    row = job.k == 1 ? slot : slot / job.k;
   }
-  if (row >= job.x_rows) return;
-  const int8_t* src = job.x + row * job.K + c * 8;
-  uint2 w = make_uint2(0, 0);
-  if (vec && c * 8 < job.K) {
-    w = __ldg(reinterpret_cast<const uint2*>(src));
-  } else {
-    uint32_t v[2] = {0, 0};
+  return row < job.x_rows ? row : -1;
+}
+// Inputs 8c .. 8c + 7 of a row; those past K are zeros (their weights are too).
+__device__ __forceinline__ uint2 operand_load(const int8_t* src, int64_t c, int64_t K, bool vec) {
+  if (vec)
+    return c * 8 < K ? __ldg(reinterpret_cast<const uint2*>(src + c * 8)) : make_uint2(0, 0);
+  uint32_t v[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c * 8 + j < job.K)
-        v[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(src + j))) << (8 * (j % 4));
-    w = make_uint2(v[0], v[1]);
-  }
-  // inputs past K give -zp here; their weights are zero
+  for (int j = 0; j < 8; ++j)
+    if (c * 8 + j < K)
+      v[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(src + c * 8 + j)))
+                  << (8 * (j % 4));
+  return make_uint2(v[0], v[1]);
+}
+__device__ __forceinline__ uint4 operand_f16(uint2 w, __half2 minus) {
   w.x ^= 0x80808080u;
   w.y ^= 0x80808080u;
-  uint4 o;
-  o.x = biased_to_f16x2(w.x, 0x4140, minus);
-  o.y = biased_to_f16x2(w.x, 0x4342, minus);
-  o.z = biased_to_f16x2(w.y, 0x4140, minus);
-  o.w = biased_to_f16x2(w.y, 0x4342, minus);
-  job.dst[(static_cast<int64_t>(c >> 3) * job.R + s) * 8 + (c & 7)] = o;
+  return make_uint4(biased_to_f16x2(w.x, 0x4140, minus), biased_to_f16x2(w.x, 0x4342, minus),
+                    biased_to_f16x2(w.y, 0x4140, minus), biased_to_f16x2(w.y, 0x4342, minus));
 }
 
+// The operand by whole warps: 32 x 8 inputs of a row a step, U steps at a time
+// (their loads in flight together), the row looked up once for them; a step
+// writes four whole 128-byte lines.
+template <int U>
 __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = t; i < job.count_words; i += step) job.counts[i] = 0;
   // x - zp = (1024 + u) - (1152 + zp): integers below 2048, exact in f16
   const __half2 minus = __half2half2(__int2half_rn(1152 + job.zp));
-  const int64_t total = static_cast<int64_t>(job.R) * job.KB * 8;
-  for (int64_t i = t; i < total; i += step) operand_item(job, i, vec, minus);
+  const uint32_t chunks = job.KB * 8;               // of 8 inputs
+  const uint32_t segs = (chunks + U * 32 - 1) / (U * 32);
+  const int64_t units = static_cast<int64_t>(job.R) * segs;
+  int64_t s = (t >> 5) / segs;
+  uint32_t seg = static_cast<uint32_t>((t >> 5) - s * segs);
+  const int64_t rows_step = (step >> 5) / segs;
+  const uint32_t seg_step = static_cast<uint32_t>((step >> 5) - rows_step * segs);
+  for (int64_t u = t >> 5; u < units; u += step >> 5) {
+    const int64_t row = operand_row(job, s);
+    if (row >= 0) {
+      const int8_t* src = job.x + row * job.K;
+      uint2 w[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = (seg * U + i) * 32 + lane;
+        w[i] = c < chunks ? operand_load(src, c, job.K, vec) : make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = (seg * U + i) * 32 + lane;
+        if (c < chunks)
+          job.dst[(static_cast<int64_t>(c >> 3) * job.R + s) * 8 + (c & 7)] =
+              operand_f16(w[i], minus);
+      }
+    }
+    s += rows_step;
+    seg += seg_step;
+    if (seg >= segs) {
+      seg -= segs;
+      ++s;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -268,8 +296,8 @@ __device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t*
   return total;
 }
 
-// Blocks: job.shrink_ctas for h, then one per row tile for its list, the rest
-// for the operand.
+// Blocks: job.shrink_ctas for h, then one per row tile for its list, and for
+// rows that come as they are (at most one row tile) the rest for the operand.
 template <bool F16, int CL>
 __global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const LoraJob job, bool vec) {
   __shared__ FrontShared sh;
@@ -321,13 +349,18 @@ __global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const Lora
     return;
   }
   b -= job.tiles;
+  if (job.op.order != nullptr) return;   // (the operand has a launch of its own)
   const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
   const int64_t step =
       static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.tiles) * kFrontThreads;
   for (int64_t i = t; i < job.op.count_words; i += step) job.op.counts[i] = 0;
   const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
-  const int64_t total = static_cast<int64_t>(R) * job.op.KB * 8;
-  for (int64_t i = t; i < total; i += step) operand_item(job.op, i, vec, minus);
+  const uint32_t chunks = job.op.KB * 8;
+  for (int64_t i = t; i < static_cast<int64_t>(R) * chunks; i += step) {
+    const uint32_t s = static_cast<uint32_t>(i) / chunks, c = static_cast<uint32_t>(i) - s * chunks;
+    job.op.dst[(static_cast<int64_t>(c >> 3) * R + s) * 8 + (c & 7)] =
+        operand_f16(operand_load(job.op.x + s * job.op.K, c, job.op.K, vec), minus);
+  }
 }
 
 // Adapter matrices, padded with zeros: A -> [L][16 rank16][64 KB], and
@@ -392,10 +425,17 @@ cudaError_t launch_pack_tile_weight(const int8_t* w, int64_t E, int64_t N, int64
 }
 
 cudaError_t launch_tile_operand(const OperandJob& job, cudaStream_t s) {
-  return launch_pdl(tile_operand_kernel,
-                    blocks_for(std::max<int64_t>(static_cast<int64_t>(job.R) * job.KB * 8,
-                                                 job.count_words)),
-                    256, 0, s, job, rows_vec8(job));
+  const bool vec = rows_vec8(job);
+  const auto go = [&](auto tag) {
+    constexpr int U = decltype(tag)::value;
+    const int64_t units = static_cast<int64_t>(job.R) * ((job.KB * 8 + U * 32 - 1) / (U * 32));
+    return launch_pdl(tile_operand_kernel<U>, blocks_for(std::max<int64_t>(units * 32, job.count_words)),
+                      256, 0, s, job, vec);
+  };
+  // one step a warp while that still leaves SMs idle
+  return static_cast<int64_t>(job.R) * job.KB < 64 * device_sm_count()
+             ? go(std::integral_constant<int, 1>())
+             : go(std::integral_constant<int, 4>());
 }
 
 cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling, bool f16,
@@ -413,14 +453,20 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
 }
 
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
-  const int groups = job.op.order == nullptr ? job.op.R : (job.op.R + kFrontRows - 1) / kFrontRows;
+  const bool vec = rows_vec8(job.op), sorted = job.op.order != nullptr;
+  if (sorted) {
+    cudaError_t e = launch_tile_operand(job.op, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int groups = sorted ? (job.op.R + kFrontRows - 1) / kFrontRows : job.op.R;
   // K is cut over 8 CTAs while the units alone would leave SMs without one
-  const int cl = groups * job.rank16 < 2 * device_sm_count() ? kFrontCluster : 1;
+  const int cl = groups * job.rank16 <= device_sm_count() ? kFrontCluster : 1;
   job.shrink_ctas = groups * job.rank16 * cl;
-  const int copy = blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
-                                                job.op.count_words));
+  const int copy =
+      sorted ? 0
+             : blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
+                                            job.op.count_words));
   const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, cl));
-  const bool vec = rows_vec8(job.op);
   if (cl == 1)
     return launch_pdl(f16 ? lora_front_kernel<true, 1> : lora_front_kernel<false, 1>, grid,
                       kFrontThreads, 0, s, job, vec);
