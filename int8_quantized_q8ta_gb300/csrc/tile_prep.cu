@@ -64,8 +64,9 @@ __device__ __forceinline__ int64_t operand_row(const OperandJob& job, int64_t s)
   return row < job.x_rows ? row : -1;
 }
 // Inputs 8c .. 8c + 7 of a row; those past K are zeros (their weights are too).
-__device__ __forceinline__ uint2 operand_load(const int8_t* src, int64_t c, int64_t K, bool vec) {
-  if (vec)
+template <bool VEC>
+__device__ __forceinline__ uint2 operand_load(const int8_t* src, int64_t c, int64_t K) {
+  if constexpr (VEC)
     return c * 8 < K ? __ldg(reinterpret_cast<const uint2*>(src + c * 8)) : make_uint2(0, 0);
   uint32_t v[2] = {0, 0};
 #pragma unroll
@@ -85,8 +86,8 @@ __device__ __forceinline__ uint4 operand_f16(uint2 w, __half2 minus) {
 // The operand by whole warps: 32 x 8 inputs of a row a step, U steps at a time
 // (their loads in flight together), the row looked up once for them; a step
 // writes four whole 128-byte lines.
-template <int U>
-__global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job, bool vec) {
+template <int U, bool VEC>
+__global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job,
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const uint32_t c = (seg * U + i) * 32 + lane;
-        w[i] = c < chunks ? operand_load(src, c, job.K, vec) : make_uint2(0, 0);
+        w[i] = c < chunks ? operand_load<VEC>(src, c, job.K) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -171,76 +172,84 @@ struct FrontShared {
   int32_t warp_count[kFrontThreads / 32];
 };
 
-// Eight inputs of a row from k0 on, minus zp, in the adapters' type (bf16 and
-// f16 both hold integers up to 255 exactly); zeros beyond K.
+// Eight int8 inputs minus zp in the adapters' type (bf16 and f16 both hold
+// integers up to 255 exactly).
 template <bool F16>
-__device__ __forceinline__ void load_x8(const LoraJob& job, int64_t row, int k0, bool vec,
-                                        uint32_t (&v)[4]) {
-  uint2 w = make_uint2(0, 0);
-  const int8_t* src = job.op.x + row * job.op.K + k0;
-  if (vec) {
-    if (k0 < job.op.K) w = __ldg(reinterpret_cast<const uint2*>(src));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k0 + j < job.op.K) {
-        const uint32_t b = static_cast<uint32_t>(static_cast<uint8_t>(__ldg(src + j)))
-                           << (8 * (j & 3));
-        if (j < 4) w.x |= b; else w.y |= b;
-      }
-  }
+__device__ __forceinline__ void widen_x8(uint2 w, int zp, uint32_t (&v)[4]) {
   if constexpr (F16) {
-    const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
-    v[0] = biased_to_f16x2(w.x ^ 0x80808080u, 0x4140, minus);
-    v[1] = biased_to_f16x2(w.x ^ 0x80808080u, 0x4342, minus);
-    v[2] = biased_to_f16x2(w.y ^ 0x80808080u, 0x4140, minus);
-    v[3] = biased_to_f16x2(w.y ^ 0x80808080u, 0x4342, minus);
+    const uint4 h = operand_f16(w, __half2half2(__int2half_rn(1152 + zp)));
+    v[0] = h.x;
+    v[1] = h.y;
+    v[2] = h.z;
+    v[3] = h.w;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t h = j < 2 ? w.x >> (16 * j) : w.y >> (16 * (j - 2));
-      v[j] = bf16x2_from_ints(static_cast<int8_t>(h & 0xff) - job.op.zp,
-                              static_cast<int8_t>((h >> 8) & 0xff) - job.op.zp);
+      v[j] = bf16x2_from_ints(static_cast<int8_t>(h & 0xff) - zp,
+                              static_cast<int8_t>((h >> 8) & 0xff) - zp);
     }
   }
 }
 
-// 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
-template <bool F16, int CL>
-__device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
-                           int c, const int32_t* rows, int row0, int count, bool vec) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rank = CL > 1 ? cluster.block_rank() : 0;
+// This warp's share of K for 16 ranks and 8 * NT rows: the loads of U steps of
+// 32 inputs go out together before any is used.
+template <bool F16, int CL, bool VEC, int NT, int U>
+__device__ __forceinline__ void front_products(const LoraJob& job, const uint16_t* A,
+                                               const int64_t (&from)[4], int first,
+                                               float (&acc)[4][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int Kp = job.op.KB * 64;
-  const uint16_t* A = job.a + (static_cast<int64_t>(a) * job.rank16 + c) * 16 * Kp;
-  float acc[4][4] = {};
-  int64_t from[4];
-  const int tiles = (count + 7) / 8;
+  constexpr int kStep = CL * kFrontThreads;
+  for (int k = first; k < Kp; k += U * kStep) {
+    uint4 lo[U], hi[U];
+    uint2 x[U][NT];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int i = n * 8 + g;
-    from[n] = -1;
-    if (i < count) {
-      const int s = rows != nullptr ? rows[i] : row0 + i;
-      from[n] = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+    for (int u = 0; u < U; ++u) {
+      const int k0 = k + u * kStep + t * 8;
+      if (k + u * kStep < Kp) {
+        lo[u] = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g) * Kp + k0));
+        hi[u] = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g + 8) * Kp + k0));
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          x[u][n] = operand_load<VEC>(job.op.x + from[n] * job.op.K, k0 >> 3, job.op.K);
+      }
     }
-  }
-#pragma unroll 2
-  for (int k0 = (rank * (kFrontThreads / 32) + warp) * 32 + t * 8; k0 < Kp;
-       k0 += CL * kFrontThreads) {
-    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g) * Kp + k0));
-    const uint4 hi =
-        __ldg(reinterpret_cast<const uint4*>(A + static_cast<int64_t>(g + 8) * Kp + k0));
-    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      if (n < tiles) {
-        uint32_t v[4] = {0, 0, 0, 0};
-        if (from[n] >= 0) load_x8<F16>(job, from[n], k0, vec, v);
-        mma_16816<F16>(acc[n], a0, v[0], v[1]);
-        mma_16816<F16>(acc[n], a1, v[2], v[3]);
+    for (int u = 0; u < U; ++u)
+      if (k + u * kStep < Kp) {
+        const uint32_t a0[4] = {lo[u].x, hi[u].x, lo[u].y, hi[u].y};
+        const uint32_t a1[4] = {lo[u].z, hi[u].z, lo[u].w, hi[u].w};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t v[4];
+          widen_x8<F16>(x[u][n], job.op.zp, v);
+          mma_16816<F16>(acc[n], a0, v[0], v[1]);
+          mma_16816<F16>(acc[n], a1, v[2], v[3]);
+        }
       }
   }
+}
+
+// 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
+template <bool F16, int CL, bool VEC>
+__device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
+                           int c, const int32_t* rows, int row0, int count) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = CL > 1 ? cluster.block_rank() : 0;
+  const uint16_t* A =
+      job.a + (static_cast<int64_t>(a) * job.rank16 + c) * 16 * (job.op.KB * 64);
+  float acc[4][4] = {};
+  int64_t from[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int i = min(n * 8 + g, count - 1);   // rows past the last repeat it, unused
+    const int s = rows != nullptr ? rows[i] : row0 + i;
+    from[n] = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+  }
+  const int first = (rank * (kFrontThreads / 32) + warp) * 32;
+  if (count <= 8) front_products<F16, CL, VEC, 1, 4>(job, A, from, first, acc);
+  else front_products<F16, CL, VEC, 4, 2>(job, A, from, first, acc);
 #pragma unroll
   for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -298,8 +307,8 @@ __device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t*
 
 // Blocks: job.shrink_ctas for h, then one per row tile for its list, and for
 // rows that come as they are (at most one row tile) the rest for the operand.
-template <bool F16, int CL>
-__global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const LoraJob job, bool vec) {
+template <bool F16, int CL, bool VEC>
+__global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const LoraJob job) {
   __shared__ FrontShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const Lora
       if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
       const int n = block_compact(sh, same, threadIdx.x, sh.rows);
       for (int i = 0; i < n; i += kFrontRows)
-        front_rows<F16, CL>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i), vec);
+        front_rows<F16, CL, VEC>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i));
     } else {
       // the runs among the window's 32 rows, found by every warp for itself
       const int s0 = w * kFrontRows, n = min(kFrontRows, R - s0), lane = threadIdx.x & 31;
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const Lora
         const int a = __shfl_sync(0xffffffffu, mine, i);
         const uint32_t other = __ballot_sync(0xffffffffu, mine != a) & (0xffffffffu << i);
         const int e = other != 0 ? __ffs(other) - 1 : 32;
-        if (a >= 0) front_rows<F16, CL>(job, sh, cluster, a, c, nullptr, s0 + i, e - i, vec);
+        if (a >= 0) front_rows<F16, CL, VEC>(job, sh, cluster, a, c, nullptr, s0 + i, e - i);
         i = e;
       }
     }
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kFrontThreads, 3) lora_front_kernel(const Lora
   for (int64_t i = t; i < static_cast<int64_t>(R) * chunks; i += step) {
     const uint32_t s = static_cast<uint32_t>(i) / chunks, c = static_cast<uint32_t>(i) - s * chunks;
     job.op.dst[(static_cast<int64_t>(c >> 3) * R + s) * 8 + (c & 7)] =
-        operand_f16(operand_load(job.op.x + s * job.op.K, c, job.op.K, vec), minus);
+        operand_f16(operand_load<VEC>(job.op.x + s * job.op.K, c, job.op.K), minus);
   }
 }
 
@@ -425,17 +434,19 @@ cudaError_t launch_pack_tile_weight(const int8_t* w, int64_t E, int64_t N, int64
 }
 
 cudaError_t launch_tile_operand(const OperandJob& job, cudaStream_t s) {
-  const bool vec = rows_vec8(job);
-  const auto go = [&](auto tag) {
-    constexpr int U = decltype(tag)::value;
+  const auto go = [&](auto u, auto vec) {
+    constexpr int U = decltype(u)::value;
     const int64_t units = static_cast<int64_t>(job.R) * ((job.KB * 8 + U * 32 - 1) / (U * 32));
-    return launch_pdl(tile_operand_kernel<U>, blocks_for(std::max<int64_t>(units * 32, job.count_words)),
-                      256, 0, s, job, vec);
+    return launch_pdl(tile_operand_kernel<U, decltype(vec)::value>,
+                      blocks_for(std::max<int64_t>(units * 32, job.count_words)), 256, 0, s, job);
   };
-  // one step a warp while that still leaves SMs idle
-  return static_cast<int64_t>(job.R) * job.KB < 64 * device_sm_count()
-             ? go(std::integral_constant<int, 1>())
-             : go(std::integral_constant<int, 4>());
+  const auto with = [&](auto vec) {
+    // one step a warp while that still leaves SMs idle
+    return static_cast<int64_t>(job.R) * job.KB < 64 * device_sm_count()
+               ? go(std::integral_constant<int, 1>(), vec)
+               : go(std::integral_constant<int, 4>(), vec);
+  };
+  return rows_vec8(job) ? with(std::true_type()) : with(std::false_type());
 }
 
 cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling, bool f16,
@@ -453,7 +464,7 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
 }
 
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
-  const bool vec = rows_vec8(job.op), sorted = job.op.order != nullptr;
+  const bool sorted = job.op.order != nullptr;
   if (sorted) {
     cudaError_t e = launch_tile_operand(job.op, s);
     if (e != cudaSuccess) return e;
@@ -467,12 +478,16 @@ cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
              : blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
                                             job.op.count_words));
   const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, cl));
-  if (cl == 1)
-    return launch_pdl(f16 ? lora_front_kernel<true, 1> : lora_front_kernel<false, 1>, grid,
-                      kFrontThreads, 0, s, job, vec);
-  return launch_pdl_cluster(
-      f16 ? lora_front_kernel<true, kFrontCluster> : lora_front_kernel<false, kFrontCluster>, grid,
-      kFrontThreads, 0, kFrontCluster, s, job, vec);
+  const auto go = [&](auto half, auto vec) {
+    constexpr bool F16 = decltype(half)::value, VEC = decltype(vec)::value;
+    return cl == 1 ? launch_pdl(lora_front_kernel<F16, 1, VEC>, grid, kFrontThreads, 0, s, job)
+                   : launch_pdl_cluster(lora_front_kernel<F16, kFrontCluster, VEC>, grid,
+                                        kFrontThreads, 0, kFrontCluster, s, job);
+  };
+  const auto with = [&](auto half) {
+    return rows_vec8(job.op) ? go(half, std::true_type()) : go(half, std::false_type());
+  };
+  return f16 ? with(std::true_type()) : with(std::false_type());
 }
 
 }  // namespace q8
