@@ -747,69 +747,82 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         announce(as);
       }
       if (!ok) break;
-      const int na = sg->na;
-      if (na > 0) pdl_wait();
+      if (sg->na == 0) continue;
+      pdl_wait();
+      // Adapters.  This thread fills one row of B (of this CTA's share): h's 16
+      // leading tf32 terms, then its 16 trailing ones, in the 128-byte swizzle;
+      // zeros in the rounds of other adapters.  A round's h is fetched before
+      // the round before it is waited for.
       const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
-      const int half = ((sg->rows + 15) & ~15) / CG, first = rank * half;
-      const int t0 = (warp & 3) * 32 + lane;          // this thread among the group's 128
-      for (int i = 0; i < na && ok; ++i) {
-        const int a_id = __ldg(list + i);
-        for (int c = 0; c < p.rank16; ++c, advance()) {
-          if (F::kGroups == 2 && (it & 1) != group) continue;
-          const int as = it & (NA - 1);
-          ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
-                                         kErrTileRing, p.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t st = ring0 + ring.slot * stage_bytes;
-          uint32_t r[16];
+      const int half = ((sg->rows + 15) & ~15) / CG;
+      static_assert(F::kMaxRows / CG <= 128, "one row a thread");
+      const int t = (warp & 3) * 32 + lane, s = rank * half + t;
+      const bool in = t < half && s < sg->rows;
+      const int64_t at_row = static_cast<int64_t>(sg->row0 + (in ? s : 0));
+      const int my_a = in ? __ldg(p.ids + at_row) : -1;
+      const float4* h = reinterpret_cast<const float4*>(p.h + at_row * p.rank16 * 16);
+      const int rounds = sg->na * p.rank16;
+      float4 hv[4];
+      const auto fetch = [&](int round) {
+        const bool mine = round < rounds && my_a >= 0 && __ldg(list + round / p.rank16) == my_a;
+        const int c = round % p.rank16;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint4 v = lds128(st + KD * tok_bytes + g * 2048 + row * 16);
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+        for (int g = 0; g < 4; ++g)
+          hv[g] = mine ? __ldg(h + c * 4 + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      int round = F::kGroups == 2 && (it & 1) != group ? 1 : 0;
+      if (round == 1) advance();
+      fetch(round);
+      while (round < rounds) {
+        const int as = it & (NA - 1);
+        ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
+                                       kErrTileRing, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = ring0 + ring.slot * stage_bytes;
+        uint32_t r[16];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint4 v = lds128(st + KD * tok_bytes + g * 2048 + row * 16);
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (p.lora_f16) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+              r[g * 8 + j * 2] = __float_as_uint(f.x);
+              r[g * 8 + j * 2 + 1] = __float_as_uint(f.y);
+            } else {
+              r[g * 8 + j * 2] = q[j] << 16;
+              r[g * 8 + j * 2 + 1] = q[j] & 0xffff0000u;
+            }
+          }
+        }
+        tmem_st_16cols(a_lane + as * KD * 32, r);
+        if (t < half) {
+          const uint32_t at = st + t * 128;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float f[4] = {hv[g].x, hv[g].y, hv[g].z, hv[g].w};
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              if (p.lora_f16) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
-                r[g * 8 + j * 2] = __float_as_uint(f.x);
-                r[g * 8 + j * 2 + 1] = __float_as_uint(f.y);
-              } else {
-                r[g * 8 + j * 2] = q[j] << 16;
-                r[g * 8 + j * 2 + 1] = q[j] & 0xffff0000u;
-              }
+              hi[j] = __float_as_uint(f[j]) & 0xffffe000u;
+              lo[j] = (hi[j] & 0x7f800000u) == 0x7f800000u   // inf - inf would be NaN
+                          ? 0u
+                          : __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
             }
+            sts128(at + ((g ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+            sts128(at + (((g + 4) ^ (t & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
           }
-          tmem_st_16cols(a_lane + as * KD * 32, r);
-          // B (this CTA's share of the rows): row t = h's 16 leading tf32
-          // terms, then its 16 trailing ones, in the 128-byte swizzle; zeros
-          // where the row has another adapter
-          for (int t = t0; t < half; t += 128) {
-            const int s = first + t;
-            const bool mine = s < sg->rows && __ldg(p.ids + sg->row0 + s) == a_id;
-            const float4* h = reinterpret_cast<const float4*>(
-                p.h + static_cast<int64_t>(sg->row0 + s) * p.rank16 * 16 + c * 16);
-            const uint32_t at = st + t * 128;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 v = mine ? __ldg(h + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-              const float f[4] = {v.x, v.y, v.z, v.w};
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                hi[j] = __float_as_uint(f[j]) & 0xffffe000u;
-                lo[j] = (hi[j] & 0x7f800000u) == 0x7f800000u   // inf - inf would be NaN
-                            ? 0u
-                            : __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
-              }
-              sts128(at + ((g ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-              sts128(at + (((g + 4) ^ (t & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-            }
-          }
-          fence_proxy_async_smem();
-          announce(as);
         }
+        fence_proxy_async_smem();
+        announce(as);
+        for (int k = 0; k < F::kGroups; ++k)   // past this round and the partner's
+          if (round++ < rounds) advance();
+        fetch(round);
       }
+      if (!ok) break;
     }
   } else if (warp >= F::kFirstEpi) {
     // ---- epilogue ------------------------------------------------------------
@@ -1017,11 +1030,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               for (int j = 0; j < 16; ++j, to.step(p.N))
                 if (j < rows) to.store(v[j], p);
             } else {
+              // a lane looks up one column's row for all of them
+              const int mapped =
+                  __ldg(p.out_rows + s0 + min(lane & 15, mine - b * 16 - 1));
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j < rows)
-                  OutPtr<OUT>(p.out, static_cast<int64_t>(__ldg(p.out_rows + s0 + j)) * p.N + n)
-                      .store(v[j], p);
+              for (int j = 0; j < 16; ++j) {
+                const int64_t row = __shfl_sync(0xffffffffu, mapped, j);
+                if (j < rows) OutPtr<OUT>(p.out, row * p.N + n).store(v[j], p);
+              }
             }
           }
           rotate();
