@@ -96,7 +96,7 @@ struct LoraSpace {
 };
 LoraSpace lora_space(int64_t M, int64_t K, int64_t L, int64_t r) {
   LoraSpace t{};
-  t.plan = plan_tiles(M, K, 1, lora_by_row(M, L) ? 128 : q8::kMaxTileRows);
+  t.plan = plan_tiles(M, K, 1, lora_by_row(M, L) ? q8::kMaxByRow : q8::kMaxTileRows);
   const int64_t tiles = (M + t.plan.TN - 1) / t.plan.TN;
   t.h = t.plan.total;
   t.lists = t.h + q8::align_ws(static_cast<size_t>(M) * ((r + 15) / 16) * 64);

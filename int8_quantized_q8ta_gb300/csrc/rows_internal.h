@@ -79,6 +79,7 @@ cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt
 
 // ---- grouped int8 contraction (tile_gemm.cu, tile_prep.cu) -----------------
 constexpr int kMaxTileRows = 192;       // rows of one tile: two accumulators fit TMEM
+constexpr int kMaxByRow = 64;           // rows of a tile whose adapter terms go row by row
 constexpr int kTileEpiWarps = 12;       // epilogue warps at most
 constexpr int kTilePartWords = kMaxTileRows * 128;   // int32 words of one CTA's part of a unit
 constexpr int kTileSmem = 218 * 1024;   // beside it some 7 KB of static shared memory
@@ -111,7 +112,7 @@ struct TileParams {
   int32_t* counts;          // [grid][kTileEpiWarps], zeroed by the kernel before
   // adapters (L == 0: none)
   int L, rank16, lora_f16;  // adapters, blocks of 16 ranks, f16 (1) or bf16 (0)
-  int by_row;               // the term row by row in the epilogue (TN <= 128), not by MMAs
+  int by_row;               // the term row by row in the epilogue (TN <= kMaxByRow), not by MMAs
   const uint8_t* lora_b;    // packed B (see launch_pack_lora)
   const float* h;           // [R][rank16 * 16]: s_in * scaling * (x - zp) A^T
   const int32_t* ids;       // [R] adapter of each row

@@ -292,22 +292,18 @@ __device__ __forceinline__ int adapters_of(const TileParams& p, const Seg& s) {
 
 // sum_j h[s, j] B[a(s)][n, j] for one channel and 8 rows a call, by a whole
 // warp: lane u < 8 holds row u's index my_s and adapter my_a (out of range:
-// none).  B comes from global memory, 16 bytes a thread; the rows' h, 16
-// ranks at a time, through the warp's corner of shared memory, from where all
-// lanes read the same words.  row: the channel's place among its block's 128.
+// none).  B comes from global memory, 16 bytes a thread, four rows' loads at a
+// time; the rows' h, 16 ranks at a time, through the warp's corner of shared
+// memory, from where all lanes read the same words.  row: the channel's place
+// among its block's 128.
 __device__ __forceinline__ void row_deltas(const TileParams& p, int nb, int row, int my_a, int my_s,
                                            float (*corner)[16], float (&d)[8]) {
   const int lane = threadIdx.x & 31;
-  uint32_t have = 0;
-  int64_t at[8];
+  const bool mine = my_a >= 0 && my_a < p.L;
+  const uint32_t have = __ballot_sync(0xffffffffu, mine);
+  const int my_at = mine ? my_a * p.NB + nb : 0;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int a = __shfl_sync(0xffffffffu, my_a, u);
-    const bool in = a >= 0 && a < p.L;
-    have |= static_cast<uint32_t>(in) << u;
-    at[u] = (static_cast<int64_t>(in ? a : 0) * p.NB + nb) * p.rank16 * 4096 + row * 16;
-    d[u] = 0.0f;
-  }
+  for (int u = 0; u < 8; ++u) d[u] = 0.0f;
   // this lane's quarter of 16 ranks of row lane / 4 (rows without an adapter
   // have no h)
   const bool h_in = (have >> (lane >> 2)) & 1;
@@ -315,47 +311,53 @@ __device__ __forceinline__ void row_deltas(const TileParams& p, int nb, int row,
       p.h + static_cast<int64_t>(__shfl_sync(0xffffffffu, my_s, lane >> 2)) * p.rank16 * 16);
   for (int c = 0; c < p.rank16; ++c) {
     const float4 hv = h_in ? __ldg(h + c * 4 + (lane & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    uint4 v[8][2];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        v[u][g] = (have >> u) & 1 ? __ldg(reinterpret_cast<const uint4*>(
-                                        p.lora_b + at[u] + c * 4096 + g * 2048))
-                                  : make_uint4(0, 0, 0, 0);
     __syncwarp();
     *reinterpret_cast<float4*>(&corner[lane >> 2][(lane & 3) * 4]) = hv;
     __syncwarp();
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u0 = 0; u0 < 8; u0 += 4) {
+      uint4 v[4][2];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float4 h0 = *reinterpret_cast<const float4*>(&corner[u][g * 8]);
-        const float4 h1 = *reinterpret_cast<const float4*>(&corner[u][g * 8 + 4]);
-        const uint32_t q[4] = {v[u][g].x, v[u][g].y, v[u][g].z, v[u][g].w};
-        const float f[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+      for (int u = 0; u < 4; ++u) {
+        const int64_t at = __shfl_sync(0xffffffffu, my_at, u0 + u);
+        const uint8_t* b = p.lora_b + (at * p.rank16 + c) * 4096 + row * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 w;
-          if (p.lora_f16) {
-            w = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
-          } else {
-            w.x = __uint_as_float(q[j] << 16);
-            w.y = __uint_as_float(q[j] & 0xffff0000u);
-          }
-          d[u] = fmaf(f[j * 2], w.x, d[u]);
-          d[u] = fmaf(f[j * 2 + 1], w.y, d[u]);
-        }
+        for (int g = 0; g < 2; ++g)
+          v[u][g] = (have >> (u0 + u)) & 1
+                        ? __ldg(reinterpret_cast<const uint4*>(b + g * 2048))
+                        : make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float4 h0 = *reinterpret_cast<const float4*>(&corner[u0 + u][g * 8]);
+          const float4 h1 = *reinterpret_cast<const float4*>(&corner[u0 + u][g * 8 + 4]);
+          const uint32_t q[4] = {v[u][g].x, v[u][g].y, v[u][g].z, v[u][g].w};
+          const float f[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 w;
+            if (p.lora_f16) {
+              w = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+            } else {
+              w.x = __uint_as_float(q[j] << 16);
+              w.y = __uint_as_float(q[j] & 0xffff0000u);
+            }
+            d[u0 + u] = fmaf(f[j * 2], w.x, d[u0 + u]);
+            d[u0 + u] = fmaf(f[j * 2 + 1], w.y, d[u0 + u]);
+          }
+        }
+    }
   }
 }
 
-// v of one accumulator, in the order of the header's epilogue.
-__device__ __forceinline__ float dequant(int32_t acc, float ws, float b, float d,
-                                         const Requant& rq) {
+// v of one accumulator without its adapter term, in the order of the header's
+// epilogue.
+__device__ __forceinline__ float dequant(int32_t acc, float ws, float b, const Requant& rq) {
   float t = __fmul_rn(__int2float_rn(acc), rq.s_in);
   t = __fmul_rn(t, ws);
-  return __fadd_rn(__fadd_rn(t, b), d);
+  return __fadd_rn(t, b);
 }
 
 template <int OUT> struct OutType { using type = uint16_t; };
@@ -874,12 +876,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (first_seg) {
         // for the first part even before the kernel before this one is done:
         // whatever its ids then are, a prefetch changes no result
-        if (p.by_row && sg->kb1 == p.KB) fetch_adapters(sg, mine, nb);
+        if (!PAIR && p.by_row && sg->kb1 == p.KB) fetch_adapters(sg, mine, nb);
         pdl_wait();
       }
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
-      const bool by_row = p.by_row && sg->kb1 == p.KB;
+      const bool by_row = !PAIR && p.by_row && sg->kb1 == p.KB;
       if (by_row) {
         if (!first_seg) fetch_adapters(sg, mine, nb);
         for (int j = 0; j < mine; j += 8) {
@@ -903,13 +905,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < kCols / 16; ++b)
-          if (b * 16 < mine) {
-            uint32_t r[16];
-            tmem_ld_16cols(lane_addr + buf * acc_cols + b * 16, r);
-            tmem_ld_wait();
+        for (int b = 0; b < kCols / 8; ++b)
+          if (b * 8 < mine) {
+            uint32_t r[8];
+            tmem_ld_8cols(lane_addr + buf * acc_cols + b * 8, r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[b * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+            for (int j = 0; j < 8; ++j) acc[b * 8 + j] += __float2int_rn(__uint_as_float(r[j]));
           }
         release(buf);
       }
@@ -956,13 +957,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               *reinterpret_cast<int4*>(part + (b * 4 + q) * 128) =
                   make_int4(acc[q * 4], acc[q * 4 + 1], acc[q * 4 + 2], acc[q * 4 + 3]);
             if (has_d) {
-              uint32_t r[16];
-              tmem_ld_16cols(d_addr + b * 16, r);
-              tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4*>(dpart + (b * 4 + q) * 128) =
-                    make_uint4(r[q * 4], r[q * 4 + 1], r[q * 4 + 2], r[q * 4 + 3]);
+              for (int half = 0; half < 2; ++half) {
+                uint32_t r[8];
+                tmem_ld_8cols(d_addr + b * 16 + half * 8, r);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                  *reinterpret_cast<uint4*>(dpart + (b * 4 + half * 2 + q) * 128) =
+                      make_uint4(r[q * 4], r[q * 4 + 1], r[q * 4 + 2], r[q * 4 + 3]);
+              }
             }
           }
           rotate();
@@ -1001,34 +1004,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 acc[q * 4 + 3] += v.w;
               }
             }
-            uint32_t r[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = 0;
-            if (has_d) {
-              tmem_ld_16cols(d_addr + b * 16, r);
-              tmem_ld_wait();
-            } else if (other_d) {
-              const int32_t* dpart = part_at(end, 2);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int4 v = __ldcg(reinterpret_cast<const int4*>(dpart + (b * 4 + q) * 128));
-                r[q * 4] = v.x;
-                r[q * 4 + 1] = v.y;
-                r[q * 4 + 2] = v.z;
-                r[q * 4 + 3] = v.w;
-              }
-            }
-            float v[16];
+            // In place from here on: registers beyond the 64 sums are few, and
+            // what spills finds no L1 beside this much shared memory.
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              v[j] = dequant(acc[j], ws, bias, __uint_as_float(r[j]), p.rq);
+              acc[j] = __float_as_int(dequant(acc[j], ws, bias, p.rq));
+            if (has_d || other_d) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t r[8];
+                if (has_d) {
+                  tmem_ld_8cols(d_addr + b * 16 + half * 8, r);
+                } else {
+                  const int32_t* dpart = part_at(end, 2) + (b * 4 + half * 2) * 128;
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) {
+                    const int4 v = __ldcg(reinterpret_cast<const int4*>(dpart + q * 128));
+                    r[q * 4] = v.x;
+                    r[q * 4 + 1] = v.y;
+                    r[q * 4 + 2] = v.z;
+                    r[q * 4 + 3] = v.w;
+                  }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  acc[half * 8 + j] = __float_as_int(
+                      __fadd_rn(__int_as_float(acc[half * 8 + j]), __uint_as_float(r[j])));
+              }
+            }
             const int s0 = sg->row0 + col0 + b * 16;
             const int rows = in ? mine - b * 16 : 0;
             if (p.out_rows == nullptr) {
               OutPtr<OUT> to(p.out, static_cast<int64_t>(s0) * p.N + n);
 #pragma unroll
               for (int j = 0; j < 16; ++j, to.step(p.N))
-                if (j < rows) to.store(v[j], p);
+                if (j < rows) to.store(__int_as_float(acc[j]), p);
             } else {
               // a lane looks up one column's row for all of them
               const int mapped =
@@ -1036,7 +1046,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const int64_t row = __shfl_sync(0xffffffffu, mapped, j);
-                if (j < rows) OutPtr<OUT>(p.out, row * p.N + n).store(v[j], p);
+                if (j < rows) OutPtr<OUT>(p.out, row * p.N + n).store(__int_as_float(acc[j]), p);
               }
             }
           }
