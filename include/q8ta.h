@@ -543,7 +543,7 @@ q8_status q8_expert_combine_backward(const void* dy, const void* z, q8_dtype dty
  * inputs of one row (results never depend on it).  q8_tile_pack_weight
  * takes [E, N, K] (E = 1: one weight), waits for the packing, and a packed
  * buffer is rewritten only by packing into it again.
- * Guards: those of q8_expert_sort; N, K >= 1; E*N*K within int64; the scale
+ * Guards: those of q8_expert_sort; 1 <= N <= 2^24, K >= 1; E*N*K within int64; the scale
  * and zero-point ranges; activation "none" or "relu"; workspace of
  * q8_linear_experts_workspace_bytes(T*k, K, E) bytes and the packed weight
  * 256-byte aligned.  Order entries outside the rows of x leave their sorted
@@ -581,7 +581,7 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
  * adapter's rows NaN.
  *   weight       packed by q8_tile_pack_weight with E = 1
  *   out          [M, N] of out_dtype
- * Guards: M >= 0 (0: nothing to do), N, K >= 1, 1 <= L <= 1024, 1 <= r <= 256,
+ * Guards: M >= 0 (0: nothing to do), 1 <= N <= 2^24, K >= 1, 1 <= L <= 1024, 1 <= r <= 256,
  * adapters Q8_F16 or Q8_BF16 (else Q8_ERR_UNSUPPORTED), the scale and
  * zero-point ranges; workspace of q8_linear_lora_workspace_bytes(M, K, L, r)
  * bytes, packed weight and packed adapters 256-byte aligned.

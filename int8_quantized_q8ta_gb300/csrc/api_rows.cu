@@ -33,7 +33,7 @@ size_t tile_weight_bytes(int64_t E, int64_t N, int64_t K) {
 }
 
 bool tile_sizes_ok(int64_t E, int64_t N, int64_t K) {
-  return E >= 1 && E <= q8::kMaxExperts && N >= 1 && K >= 1 && N <= INT32_MAX / 2 &&
+  return E >= 1 && E <= q8::kMaxExperts && N >= 1 && K >= 1 && N <= (1 << 24) &&
          K <= INT32_MAX / 2 && mul_ok(N, K) && mul_ok(E, N * K) && E * N * K <= INT64_MAX / 64;
 }
 

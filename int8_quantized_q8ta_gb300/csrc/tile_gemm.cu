@@ -364,25 +364,19 @@ template <int OUT> struct OutType { using type = uint16_t; };
 template <> struct OutType<Q8_I8> { using type = int8_t; };
 template <> struct OutType<Q8_F32> { using type = float; };
 
-// Where an output goes, and its last step: requantize, or activate and round.
+// An output's last step: requantize, or activate and round.
 template <int OUT>
-struct OutPtr {
-  typename OutType<OUT>::type* at;
-  __device__ __forceinline__ OutPtr(void* out, int64_t i)
-      : at(static_cast<typename OutType<OUT>::type*>(out) + i) {}
-  __device__ __forceinline__ void step(int64_t n) { at += n; }
-  __device__ __forceinline__ void store(float v, const TileParams& p) const {
-    if constexpr (OUT == Q8_I8) {
-      *at = static_cast<int8_t>(round_clamp_first(__fmul_rn(v, p.rq.inv_out), p.rq.ozp_i,
-                                                  p.rq.lo_f, p.rq.hi_f));
-    } else {
-      v = v < p.floor_f ? 0.0f : v;   // relu: floor 0, else -inf; NaN stays
-      if constexpr (OUT == Q8_F32) *at = v;
-      if constexpr (OUT == Q8_F16) *at = __half_as_ushort(__float2half_rn(v));
-      if constexpr (OUT == Q8_BF16) *at = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
+__device__ __forceinline__ typename OutType<OUT>::type finish(float v, const TileParams& p) {
+  if constexpr (OUT == Q8_I8) {
+    return static_cast<int8_t>(round_clamp_first(__fmul_rn(v, p.rq.inv_out), p.rq.ozp_i, p.rq.lo_f,
+                                                 p.rq.hi_f));
+  } else {
+    v = max_nan(v, p.floor_f);   // relu: floor 0, else -inf
+    if constexpr (OUT == Q8_F32) return v;
+    else if constexpr (OUT == Q8_F16) return __half_as_ushort(__float2half_rn(v));
+    else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
-};
+}
 
 // Two halves of a token tile have rows that are multiples of 8.
 template <int OUT, bool PAIR>
@@ -928,9 +922,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const bool has_d = by_row || by_mma;
       const uint32_t d_addr = lane_addr + (by_row ? 2 * acc_cols + NA * KD * 32 : dbuf * acc_cols);
-      // The loops below take 16 columns a round and stay rolled: code that a
-      // CTA runs once or twice costs more to fetch than to execute.  The
-      // registers move up by 16 instead.
+      // Loops over parts, which a CTA runs once or twice, take 16 columns a
+      // round and stay rolled (code that runs once costs more to fetch than to
+      // execute): the registers move up by 16 instead.
       const auto rotate = [&]() {
         if constexpr (kCols > 16) {
           int32_t t[16];
@@ -977,83 +971,105 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           before = atomic_add_acq_rel(p.counts + (first * CG + rank) * kTileEpiWarps + ew, 1);
         before = __shfl_sync(0xffffffffu, before, 0);
         last = before == end - first;
+        if (last) {
+#pragma unroll 1
+          for (int b = 0; b < kCols / 16; ++b) {
+            if (b * 16 < mine)
+              for (int c = first; c <= end; ++c) {
+                if (c == me) continue;
+                const int32_t* other = part_at(c, c == first ? 1 : 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int4 v = __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128));
+                  acc[q * 4] += v.x;
+                  acc[q * 4 + 1] += v.y;
+                  acc[q * 4 + 2] += v.z;
+                  acc[q * 4 + 3] += v.w;
+                }
+              }
+            rotate();
+          }
+        }
       }
+      const int n = nb * 128 + quarter * 32 + lane;
+      const bool in = n < p.N;
       if (last) {
-        const int n = nb * 128 + quarter * 32 + lane;
-        const bool in = n < p.N;
+        // In place from here on: registers beyond the sums are few, and what
+        // spills finds no L1 beside this much shared memory.
         const int64_t en = static_cast<int64_t>(sg->e) * p.N + n;
         const float ws = in ? __ldg(p.ws + en) : 0.0f;
         const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) acc[j] = __float_as_int(dequant(acc[j], ws, bias, p.rq));
         // the unit's adapter term: in this CTA's TMEM, or left by the CTA
         // that ran the unit's end
         const bool other_d =
             !has_d && p.L > 0 &&
             (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg->tile) * p.list_stride) > 0);
+        if (has_d) {
+#pragma unroll
+          for (int b = 0; b < kCols / 8; ++b)
+            if (b * 8 < mine) {
+              uint32_t r[8];
+              tmem_ld_8cols(d_addr + b * 8, r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                acc[b * 8 + j] = __float_as_int(
+                    __fadd_rn(__int_as_float(acc[b * 8 + j]), __uint_as_float(r[j])));
+            }
+        } else if (other_d) {
+          const int32_t* dpart = part_at(end, 2);
 #pragma unroll 1
-        for (int b = 0; b < kCols / 16; ++b) {
-          if (b * 16 < mine) {
-            for (int c = first; c <= end; ++c) {
-              if (c == me) continue;
-              const int32_t* part = part_at(c, c == first ? 1 : 0);
+          for (int b = 0; b < kCols / 16; ++b) {
+            if (b * 16 < mine) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const int4 v = __ldcg(reinterpret_cast<const int4*>(part + (b * 4 + q) * 128));
-                acc[q * 4] += v.x;
-                acc[q * 4 + 1] += v.y;
-                acc[q * 4 + 2] += v.z;
-                acc[q * 4 + 3] += v.w;
+                const int4 v = __ldcg(reinterpret_cast<const int4*>(dpart + (b * 4 + q) * 128));
+                const int32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  acc[q * 4 + j] = __float_as_int(
+                      __fadd_rn(__int_as_float(acc[q * 4 + j]), __int_as_float(r[j])));
               }
             }
-            // In place from here on: registers beyond the 64 sums are few, and
-            // what spills finds no L1 beside this much shared memory.
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[j] = __float_as_int(dequant(acc[j], ws, bias, p.rq));
-            if (has_d || other_d) {
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t r[8];
-                if (has_d) {
-                  tmem_ld_8cols(d_addr + b * 16 + half * 8, r);
-                } else {
-                  const int32_t* dpart = part_at(end, 2) + (b * 4 + half * 2) * 128;
-#pragma unroll
-                  for (int q = 0; q < 2; ++q) {
-                    const int4 v = __ldcg(reinterpret_cast<const int4*>(dpart + q * 128));
-                    r[q * 4] = v.x;
-                    r[q * 4 + 1] = v.y;
-                    r[q * 4 + 2] = v.z;
-                    r[q * 4 + 3] = v.w;
-                  }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  acc[half * 8 + j] = __float_as_int(
-                      __fadd_rn(__int_as_float(acc[half * 8 + j]), __uint_as_float(r[j])));
-              }
-            }
-            const int s0 = sg->row0 + col0 + b * 16;
-            const int rows = in ? mine - b * 16 : 0;
-            if (p.out_rows == nullptr) {
-              OutPtr<OUT> to(p.out, static_cast<int64_t>(s0) * p.N + n);
-#pragma unroll
-              for (int j = 0; j < 16; ++j, to.step(p.N))
-                if (j < rows) to.store(__int_as_float(acc[j]), p);
-            } else {
-              // a lane looks up one column's row for all of them
-              const int mapped =
-                  __ldg(p.out_rows + s0 + min(lane & 15, mine - b * 16 - 1));
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int64_t row = __shfl_sync(0xffffffffu, mapped, j);
-                if (j < rows) OutPtr<OUT>(p.out, row * p.N + n).store(__int_as_float(acc[j]), p);
-              }
-            }
+            rotate();
           }
-          rotate();
         }
       }
-      if (by_mma) release(dbuf);
+      if (by_mma) release(dbuf);   // before the stores, which take longest
+      if (last && mine > 0) {
+        using T = typename OutType<OUT>::type;
+        if (p.out_rows == nullptr) {
+          // one address for the tile and 32-bit distances from it (a tile's
+          // rows span less than 4 GB: N <= 2^24)
+          char* base = static_cast<char*>(p.out) +
+                       static_cast<int64_t>(sg->row0 + col0) * p.N * sizeof(T);
+          const uint32_t step = static_cast<uint32_t>(p.N) * sizeof(T);
+          uint32_t off = static_cast<uint32_t>(n) * sizeof(T);
+          if (mine == kCols && in) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j, off += step)
+              *reinterpret_cast<T*>(base + off) = finish<OUT>(__int_as_float(acc[j]), p);
+          } else {
+            const int rows = in ? mine : 0;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j, off += step)
+              if (j < rows)
+                *reinterpret_cast<T*>(base + off) = finish<OUT>(__int_as_float(acc[j]), p);
+          }
+        } else {
+          // a lane looks up one or two columns' rows for all of them
+          T* to = static_cast<T*>(p.out) + n;
+          const int32_t* map = p.out_rows + sg->row0 + col0;
+          const int m0 = __ldg(map + min(lane, mine - 1));
+          const int m1 = kCols > 32 ? __ldg(map + min(lane + 32, mine - 1)) : 0;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            const int64_t row = __shfl_sync(0xffffffffu, j < 32 ? m0 : m1, j & 31);
+            if (in && j < mine) to[row * p.N] = finish<OUT>(__int_as_float(acc[j]), p);
+          }
+        }
+      }
       first_seg = false;
     }
     if (first_seg) pdl_wait();
