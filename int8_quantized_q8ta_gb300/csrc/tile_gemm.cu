@@ -151,6 +151,7 @@ struct Walk {
   int ctas, me;            // CTAs (pairs) and this one
   int waves, wave;         // whole waves, and those behind
   int base, q;             // the line's first unit, and k-blocks of a run
+  int share;               // CTAs to each of the line's units, where runs end with units; or 0
   int left, unit, kb;      // the run's k-blocks still to take; its unit and where in it
   int e, start, count;     // the unit's group and its rows
   int tiles, per, t0;      // the group's row tiles, rows of each, tiles before them
@@ -167,8 +168,21 @@ struct Walk {
     const int total = (units - base) * p.KB;
     q = max(p.min_run, (total - 1) / ctas + 1);
     // whole units where cutting them would not gain what joining parts costs
-    const int whole = (units - base + ctas - 1) / ctas * p.KB;
+    const int rest = units - base, whole = (rest + ctas - 1) / ctas * p.KB;
     if (whole <= q + (CG == 1 ? kJoinNarrow : kJoinWide)) q = max(whole, 1);
+    // Few units: as many CTAs to each as there are, no run across two of them
+    // (its CTA would join parts twice)
+    share = rest > 0 && 2 * rest <= ctas && q < p.KB
+                ? max(1, min(ctas / rest, p.KB / max(1, p.min_run)))
+                : 0;
+    if (share > 0) {
+      unit = base + me / share;
+      const int part = me % share;
+      kb = part * p.KB / share;
+      left = me / share < rest ? (part + 1) * p.KB / share - kb : 0;
+      if (left > 0) locate(unit);
+      return;
+    }
     kb = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * me));
     left = min(total - kb, q);
     unit = -1;             // the run is not begun
@@ -228,8 +242,13 @@ struct Walk {
     s.unit = unit;
     s.kb0 = kb;
     s.kb1 = min(p.KB, kb + left);
-    s.first = (unit - base) * p.KB / q;
-    s.end = ((unit - base + 1) * p.KB - 1) / q;
+    if (share > 0) {
+      s.first = (unit - base) * share;
+      s.end = s.first + share - 1;
+    } else {
+      s.first = (unit - base) * p.KB / q;
+      s.end = ((unit - base + 1) * p.KB - 1) / q;
+    }
     left -= s.kb1 - s.kb0;
     if (left > 0) {
       kb = 0;
@@ -974,19 +993,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (last) {
 #pragma unroll 1
           for (int b = 0; b < kCols / 16; ++b) {
-            if (b * 16 < mine)
-              for (int c = first; c <= end; ++c) {
-                if (c == me) continue;
-                const int32_t* other = part_at(c, c == first ? 1 : 0);
+            if (b * 16 < mine) {
+              // the narrow form has registers for three parts' loads at once
+              // (this CTA's own place, and places past the last, are zeros)
+              constexpr int kAtOnce = 3;
+              if constexpr (PAIR) {
+                for (int c = first; c <= end; ++c) {
+                  if (c == me) continue;
+                  const int32_t* other = part_at(c, c == first ? 1 : 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const int4 v = __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128));
-                  acc[q * 4] += v.x;
-                  acc[q * 4 + 1] += v.y;
-                  acc[q * 4 + 2] += v.z;
-                  acc[q * 4 + 3] += v.w;
+                  for (int q = 0; q < 4; ++q) {
+                    const int4 v = __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128));
+                    acc[q * 4] += v.x;
+                    acc[q * 4 + 1] += v.y;
+                    acc[q * 4 + 2] += v.z;
+                    acc[q * 4 + 3] += v.w;
+                  }
+                }
+              } else {
+                for (int c0 = first; c0 <= end; c0 += kAtOnce) {
+                  int4 v[kAtOnce][4];
+#pragma unroll
+                  for (int k = 0; k < kAtOnce; ++k) {
+                    const int c = c0 + k;
+                    const bool use = c <= end && c != me;
+                    const int32_t* other = part_at(use ? c : me, c == first ? 1 : 0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                      v[k][q] = use ? __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128))
+                                    : make_int4(0, 0, 0, 0);
+                  }
+#pragma unroll
+                  for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                      acc[q * 4] += v[k][q].x;
+                      acc[q * 4 + 1] += v[k][q].y;
+                      acc[q * 4 + 2] += v[k][q].z;
+                      acc[q * 4 + 3] += v[k][q].w;
+                    }
                 }
               }
+            }
             rotate();
           }
         }
@@ -999,8 +1047,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int64_t en = static_cast<int64_t>(sg->e) * p.N + n;
         const float ws = in ? __ldg(p.ws + en) : 0.0f;
         const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
+        // (the narrow form skips columns without rows; in the wide one the
+        // branches cost registers that spill)
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) acc[j] = __float_as_int(dequant(acc[j], ws, bias, p.rq));
+        for (int b = 0; b < kCols; b += 16)
+          if (PAIR || b < mine)
+#pragma unroll
+            for (int j = b; j < b + 16; ++j)
+              acc[j] = __float_as_int(dequant(acc[j], ws, bias, p.rq));
         // the unit's adapter term: in this CTA's TMEM, or left by the CTA
         // that ran the unit's end
         const bool other_d =
@@ -1053,9 +1107,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           } else {
             const int rows = in ? mine : 0;
 #pragma unroll
-            for (int j = 0; j < kCols; ++j, off += step)
-              if (j < rows)
-                *reinterpret_cast<T*>(base + off) = finish<OUT>(__int_as_float(acc[j]), p);
+            for (int b = 0; b < kCols; b += 8)
+              if (PAIR || b < mine)
+#pragma unroll
+                for (int j = b; j < b + 8; ++j, off += step)
+                  if (j < rows)
+                    *reinterpret_cast<T*>(base + off) = finish<OUT>(__int_as_float(acc[j]), p);
           }
         } else {
           // a lane looks up one or two columns' rows for all of them
