@@ -238,8 +238,9 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(
   zero_tail<VB>(xs, V, T * k, offsets, E, warp_id, num_warps, lane);
 }
 
-// spread: a warp takes U*32 vectors of one token's sum.  w: null for ones.
-template <typename T, int VB, int U>
+// spread: a warp takes U*32 vectors of one token's sum, S slots' loads in
+// flight.  w: null for ones.
+template <typename T, int VB, int U, int S>
 __global__ void __launch_bounds__(256) expert_spread_kernel(
     const typename VecOf<VB>::type* __restrict__ z, const float* __restrict__ w, int64_t Tn, int k,
     int64_t V, const int32_t* __restrict__ position, typename VecOf<VB>::type* __restrict__ y) {
@@ -257,19 +258,38 @@ __global__ void __launch_bounds__(256) expert_spread_kernel(
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int n = 0; n < N; ++n) acc[i][n] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int64_t s = __ldg(position + t * k + j);
-      if (s < 0 || s >= Tn * k) continue;
-      const float wj = w != nullptr ? __ldg(w + t * k + j) : 1.0f;
-      Pack<T, VB> p[U];
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      // 32 slots' rows and weights, a lane each
+      int32_t row = -1;
+      float weight = 1.0f;
+      if (j0 + lane < k) {
+        row = __ldg(position + t * k + j0 + lane);
+        if (w != nullptr) weight = __ldg(w + t * k + j0 + lane);
+      }
+      if (row >= Tn * k) row = -1;
+      for (int j = 0; j < min(32, k - j0); j += S) {
+        int32_t from[S];
+        Pack<T, VB> p[S][U];
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (c0 + i * 32 < V) p[i].v = __ldg(z + s * V + c0 + i * 32);
+        for (int q = 0; q < S; ++q) {
+          from[q] = __shfl_sync(0xffffffffu, row, j + q);   // -1 past the last slot
+          if (from[q] >= 0)
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (c0 + i * 32 < V)
+            for (int i = 0; i < U; ++i)
+              if (c0 + i * 32 < V) p[q][i].v = __ldg(z + from[q] * V + c0 + i * 32);
+        }
 #pragma unroll
-          for (int n = 0; n < N; ++n) acc[i][n] = fmaf(wj, to_f32<T>(p[i].e[n]), acc[i][n]);
+        for (int q = 0; q < S; ++q) {
+          const float wj = __shfl_sync(0xffffffffu, weight, j + q);
+          if (from[q] >= 0)
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+              if (c0 + i * 32 < V)
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                  acc[i][n] = fmaf(wj, to_f32<T>(p[q][i].e[n]), acc[i][n]);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -419,9 +439,9 @@ cudaError_t launch_expert_spread(const void* z, q8_dtype dt, const float* w, int
     using T_ = decltype(elem);
     constexpr int VB = decltype(vb)::value;
     using V = typename VecOf<VB>::type;
-    constexpr int U = VB == 16 ? 2 : 4;
+    constexpr int U = VB == 16 ? 2 : 4, S = 4;
     const int64_t vecs = row_bytes / VB;
-    return launch_pdl(expert_spread_kernel<T_, VB, U>,
+    return launch_pdl(expert_spread_kernel<T_, VB, U, S>,
                       warp_grid(T * ((vecs + U * 32 - 1) / (U * 32))), 256, 0, s,
                       static_cast<const V*>(z), w, T, k, vecs, position, static_cast<V*>(y));
   });
@@ -436,7 +456,7 @@ cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt
     using T_ = decltype(elem);
     constexpr int VB = decltype(vb)::value;
     using V = typename VecOf<VB>::type;
-    constexpr int U = VB == 16 ? 2 : 4;
+    constexpr int U = VB == 16 ? 2 : 8;
     return launch_pdl(expert_combine_bwd_kernel<T_, VB, U>, warp_grid(T * k), 256, 0, s,
                       static_cast<const V*>(dy), static_cast<const V*>(z), w, T * k, k,
                       row_bytes / VB, position, offsets, E, static_cast<V*>(dz), dw);
