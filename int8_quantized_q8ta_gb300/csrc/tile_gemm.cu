@@ -59,10 +59,17 @@ constexpr int kTmemCols = 512;
 // Stages of A operands in tensor memory, behind the two accumulators.
 constexpr int NAb = 2, NA = 1 << NAb;
 
-// What joining the parts of cut units costs a run, in k-blocks' time (4,000 to
-// 6,000 cycles against 350 a narrow k-block, 10,000 to 14,000 against 400 a
-// wide one).
-constexpr int kJoinNarrow = 14, kJoinWide = 28;
+// Whole units to each CTA while that lengthens the longest run by no more than
+// this many k-blocks over equal runs, which cut units and then join their
+// parts (5,000 to 10,000 cycles a join, against 350 a narrow k-block and 400 a
+// wide one; a run across two units joins twice).  Measured, whole against cut,
+// K 4096: 64 rows x 11008 (27 k-blocks more) 19.9 against 22.9 us, x 28672 (33)
+// 31.6 against 34.4, x 8192 (37) 19.0 against 18.7, 8 rows x 22016 (55) 26.8
+// against 26.0, x 6144 (43) 16.9 against 15.1; wide, 192 rows x 11008 (27) 27.3
+// against 37.2, 100 rows x 4096 (37) 24.9 against 22.3.  With adapters row by
+// row a second unit's terms are made once its first is joined, and whole units
+// win further: 8 and 64 rows x 22016 25.8 against 28.4 and 44 against 50.
+constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
 
 // The two forms of the kernel.
 //   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
@@ -167,12 +174,13 @@ struct Walk {
     base = waves * ctas;
     const int total = (units - base) * p.KB;
     q = max(p.min_run, (total - 1) / ctas + 1);
-    // whole units where cutting them would not gain what joining parts costs
     const int rest = units - base, whole = (rest + ctas - 1) / ctas * p.KB;
-    if (whole <= q + (CG == 1 ? kJoinNarrow : kJoinWide)) q = max(whole, 1);
+    const bool few = 2 * rest <= ctas;
+    const int join = CG == 2 ? kJoinWide : p.by_row && !few ? kJoinByRow : kJoinNarrow;
+    if (whole <= q + join) q = max(whole, 1);
     // Few units: as many CTAs to each as there are, no run across two of them
     // (its CTA would join parts twice)
-    share = rest > 0 && 2 * rest <= ctas && q < p.KB
+    share = rest > 0 && few && q < p.KB
                 ? max(1, min(ctas / rest, p.KB / max(1, p.min_run)))
                 : 0;
     if (share > 0) {
