@@ -425,6 +425,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
             *offsets = sorted + 3 * M;
     e = q8::launch_expert_sort(adapter_ids, M, p.L, order, position, offsets, cs(stream), true);
     job.op.order = order;
+    job.offsets = offsets;
     job.ids_out = ids;
     p.ids = ids;
     p.out_rows = order;

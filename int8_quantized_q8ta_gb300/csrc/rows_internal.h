@@ -161,6 +161,7 @@ struct LoraJob {
   float* h;
   int32_t* lists;
   int32_t* ids_out;             // [R] in sorted order, or null
+  const int32_t* offsets;       // [L + 1] first sorted row of each adapter (with op.order)
   int shrink_ctas;              // set by the launcher
 };
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s);

@@ -132,17 +132,20 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job)
 
 // ---------------------------------------------------------------------------
 // Adapters: h[s, j] = s_in * scaling[a] * sum_k (x[row(s), k] - zp) A[a][j, k]
-// for the rows with an adapter.  A CTA, or a cluster of 8 while there are few,
-// takes 16 ranks of one adapter and up to 32 of its rows at a time; its warps
-// split K in steps of 32 and multiply with m16n8k16 MMAs, ranks on M and rows on N.  The sum over
-// k may take any order, so a thread's fragments are 8 consecutive inputs: one
-// 16-byte load of A and one 8-byte load of x per row, no shared memory.  The
-// warps' f32 sums are added in a fixed order, first in the CTA, then over the
-// cluster through distributed shared memory.
-//   Up to kMaxTileRows rows (one row tile) the rows come as they are, and the
-// cluster of an adapter's first row takes all of that adapter's rows, so that
-// A is read once.  More rows come sorted by adapter, and a cluster takes the
-// runs inside 32 of them.
+// for the rows with an adapter, by m16n8k16 MMAs with ranks on M and rows on
+// N.  The sum over k may take any order, so a thread's fragments of two MMAs
+// are 8 consecutive inputs.  A CTA's warps, and the CTAs of a cluster while
+// there are few, share K; their f32 sums are added in a fixed order, across
+// the cluster through distributed shared memory.
+//   lora_front_kernel, up to kMaxTileRows rows (one row tile): the rows come as
+// they are, and 16 ranks of one adapter are a unit, taken where its first row
+// is, for all of its rows, so that A is read once.  Loads go straight to
+// registers, 4 steps of 32 inputs at once: what bounds it is latency.  The
+// same launch writes the tile's operand and list.
+//   lora_shrink_kernel, more rows: they come sorted by adapter, in the operand,
+// and a unit is up to 32 rows of one adapter and all its ranks, 64 at a time.
+// A's and the rows' k-blocks go through a ring in shared memory, their 16-byte
+// chunks swizzled so that eight lanes' loads meet no bank twice.
 // ---------------------------------------------------------------------------
 constexpr int kFrontThreads = 256;
 constexpr int kFrontCluster = 8;   // CTAs that share one unit's K while units are few
@@ -165,11 +168,16 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int kFrontWarps = kFrontThreads / 32;
+
+struct ListShared {
+  int32_t rows[kMaxTileRows];     // the rows this cluster takes, or a tile's adapters
+  int32_t warp_count[kFrontWarps];
+};
 struct FrontShared {
-  float part[kFrontThreads / 32][16][kFrontRows + 1];
+  float part[kFrontWarps][16][kFrontRows + 1];
   float sum[16][kFrontRows];      // read by the cluster's other CTAs
-  int32_t rows[kMaxTileRows];     // the rows this cluster takes
-  int32_t warp_count[kFrontThreads / 32];
+  ListShared list;
 };
 
 // Eight int8 inputs minus zp in the adapters' type (bf16 and f16 both hold
@@ -234,7 +242,7 @@ __device__ __forceinline__ void front_products(const LoraJob& job, const uint16_
 // 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
 template <bool F16, int CL, bool VEC>
 __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
-                           int c, const int32_t* rows, int row0, int count) {
+                           int c, const int32_t* rows, int count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = CL > 1 ? cluster.block_rank() : 0;
   const uint16_t* A =
@@ -244,8 +252,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int i = min(n * 8 + g, count - 1);   // rows past the last repeat it, unused
-    const int s = rows != nullptr ? rows[i] : row0 + i;
-    from[n] = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+    from[n] = rows[i];
   }
   const int first = (rank * (kFrontThreads / 32) + warp) * 32;
   if (count <= 8) front_products<F16, CL, VEC, 1, 4>(job, A, from, first, acc);
@@ -273,8 +280,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
       } else {
         v = sh.sum[j][i];
       }
-      const int s = rows != nullptr ? rows[i] : row0 + i;
-      job.h[static_cast<int64_t>(s) * job.rank16 * 16 + c * 16 + j] =
+      job.h[static_cast<int64_t>(rows[i]) * job.rank16 * 16 + c * 16 + j] =
           v * job.s_in * __ldg(job.scaling + a);
     }
   }
@@ -289,7 +295,7 @@ __device__ __forceinline__ int adapter_of(const LoraJob& job, int s) {
 }
 
 // Indices i < n whose flag is set, in order, into list; returns how many.
-__device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t* list) {
+__device__ int block_compact(ListShared& sh, bool flag, int32_t value, int32_t* list) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t m = __ballot_sync(0xffffffffu, flag);
   if (lane == 0) sh.warp_count[warp] = __popc(m);
@@ -305,8 +311,24 @@ __device__ int block_compact(FrontShared& sh, bool flag, int32_t value, int32_t*
   return total;
 }
 
-// Blocks: job.shrink_ctas for h, then one per row tile for its list, and for
-// rows that come as they are (at most one row tile) the rest for the operand.
+// A tile's adapters, each once, in the order of their first rows.
+__device__ void list_tile(const LoraJob& job, ListShared& sh, int tile) {
+  const int per = tile_rows(job.op.R, job.tiles), row0 = tile * per, n = min(per, job.op.R - row0);
+  const int t = threadIdx.x;
+  const int a = t < n ? adapter_of(job, row0 + t) : -1;
+  if (t < n) sh.rows[t] = a;
+  __syncthreads();
+  bool first = a >= 0;
+  for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
+  __syncthreads();
+  int32_t* list = job.lists + static_cast<int64_t>(tile) * job.list_stride;
+  const int count = block_compact(sh, first, a, list + 1);
+  if (t == 0) list[0] = count;
+  if (job.ids_out != nullptr && t < n) job.ids_out[row0 + t] = a;
+}
+
+// Blocks: job.shrink_ctas for h, then one for the list, the rest for the
+// operand.
 template <bool F16, int CL, bool VEC>
 __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const LoraJob job) {
   __shared__ FrontShared sh;
@@ -316,49 +338,23 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
   const int R = job.op.R;
   int b = blockIdx.x;
   if (b < job.shrink_ctas) {
+    // row w's adapter, if no earlier row has it
     const int u = b / CL, c = u % job.rank16, w = u / job.rank16;
-    if (job.op.order == nullptr) {
-      // row w's adapter, if no earlier row has it
-      const int a = adapter_of(job, w);
-      const int mine = static_cast<int>(threadIdx.x) < R ? adapter_of(job, threadIdx.x) : -1;
-      const bool same = a >= 0 && mine == a;
-      if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
-      const int n = block_compact(sh, same, threadIdx.x, sh.rows);
-      for (int i = 0; i < n; i += kFrontRows)
-        front_rows<F16, CL, VEC>(job, sh, cluster, a, c, sh.rows + i, 0, min(kFrontRows, n - i));
-    } else {
-      // the runs among the window's 32 rows, found by every warp for itself
-      const int s0 = w * kFrontRows, n = min(kFrontRows, R - s0), lane = threadIdx.x & 31;
-      const int mine = lane < n ? adapter_of(job, s0 + lane) : -2;
-      for (int i = 0; i < n;) {
-        const int a = __shfl_sync(0xffffffffu, mine, i);
-        const uint32_t other = __ballot_sync(0xffffffffu, mine != a) & (0xffffffffu << i);
-        const int e = other != 0 ? __ffs(other) - 1 : 32;
-        if (a >= 0) front_rows<F16, CL, VEC>(job, sh, cluster, a, c, nullptr, s0 + i, e - i);
-        i = e;
-      }
-    }
+    const int a = adapter_of(job, w);
+    const int mine = static_cast<int>(threadIdx.x) < R ? adapter_of(job, threadIdx.x) : -1;
+    const bool same = a >= 0 && mine == a;
+    if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
+    const int n = block_compact(sh.list, same, threadIdx.x, sh.list.rows);
+    for (int i = 0; i < n; i += kFrontRows)
+      front_rows<F16, CL, VEC>(job, sh, cluster, a, c, sh.list.rows + i, min(kFrontRows, n - i));
     return;
   }
   b -= job.shrink_ctas;
   if (b < job.tiles) {
-    // the tile's adapters, each once, in the order of their first rows
-    const int per = tile_rows(R, job.tiles), row0 = b * per, n = min(per, R - row0);
-    const int t = threadIdx.x;
-    const int a = t < n ? adapter_of(job, row0 + t) : -1;
-    if (t < n) sh.rows[t] = a;
-    __syncthreads();
-    bool first = a >= 0;
-    for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
-    __syncthreads();
-    int32_t* list = job.lists + static_cast<int64_t>(b) * job.list_stride;
-    const int count = block_compact(sh, first, a, list + 1);
-    if (t == 0) list[0] = count;
-    if (job.ids_out != nullptr && t < n) job.ids_out[row0 + t] = a;
+    list_tile(job, sh.list, b);
     return;
   }
   b -= job.tiles;
-  if (job.op.order != nullptr) return;   // (the operand has a launch of its own)
   const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
   const int64_t step =
       static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.tiles) * kFrontThreads;
@@ -369,6 +365,172 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
     const uint32_t s = static_cast<uint32_t>(i) / chunks, c = static_cast<uint32_t>(i) - s * chunks;
     job.op.dst[(static_cast<int64_t>(c >> 3) * R + s) * 8 + (c & 7)] =
         operand_f16(operand_load<VEC>(job.op.x + s * job.op.K, c, job.op.K), minus);
+  }
+}
+
+// 16 ranks of 4 blocks, and 32 rows, of one k-block
+constexpr int kShrinkBlocks = 4, kShrinkStages = 4;
+constexpr int kShrinkStage = (kShrinkBlocks * 16 + kFrontRows) * 128;
+
+struct ShrinkShared {
+  float part[kFrontWarps][16][kFrontRows + 1];
+  float sum[kShrinkBlocks * 16][kFrontRows];   // read by the cluster's other CTAs
+  ListShared list;
+  int32_t piece[3];                            // adapter, first row, rows
+};
+
+// Where a row's 16-byte chunk of a 128-byte k-block lies: rows 2i and 2i + 1
+// keep their chunks 0 to 3 in different halves.
+__device__ __forceinline__ uint32_t shrink_at(int row, int chunk) {
+  return row * 128 + ((chunk ^ ((row & 1) << 2 | ((row >> 1) & 3))) << 4);
+}
+
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);   // integers up to 255: exact
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Unit u's piece of 32 rows at most: adapters in turn, each cut into pieces.
+__device__ bool find_piece(const LoraJob& job, ShrinkShared& sh, int u) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int before = 0;
+  for (int a0 = 0; a0 < job.L; a0 += kFrontThreads) {
+    const int a = a0 + threadIdx.x;
+    int first = 0, rows = 0;
+    if (a < job.L) {
+      first = __ldg(job.offsets + a);
+      rows = __ldg(job.offsets + a + 1) - first;
+    }
+    const int n = (rows + kFrontRows - 1) / kFrontRows;
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) sh.list.warp_count[warp] = incl;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kFrontWarps; ++w) {
+      if (w < warp) incl += sh.list.warp_count[w];
+      all += sh.list.warp_count[w];
+    }
+    const int i = u - (before + incl - n);
+    if (i >= 0 && i < n) {
+      sh.piece[0] = a;
+      sh.piece[1] = first + i * kFrontRows;
+      sh.piece[2] = min(kFrontRows, rows - i * kFrontRows);
+    }
+    __syncthreads();
+    before += all;
+    if (u < before) return true;
+  }
+  return false;
+}
+
+// Blocks: job.shrink_ctas for h, in clusters, then one per row tile for its
+// list.
+template <bool F16>
+__global__ void __launch_bounds__(kFrontThreads, 2)
+    lora_shrink_kernel(const __grid_constant__ LoraJob job) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ ShrinkShared sh;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= job.shrink_ctas) {
+    if (static_cast<int>(blockIdx.x) - job.shrink_ctas < job.tiles)
+      list_tile(job, sh.list, blockIdx.x - job.shrink_ctas);
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CL = cluster.num_blocks(), rank = cluster.block_rank();
+  if (!find_piece(job, sh, blockIdx.x / CL)) return;
+  const int a = sh.piece[0], row0 = sh.piece[1], count = sh.piece[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int KB = job.op.KB, kb0 = rank * KB / CL, steps = (rank + 1) * KB / CL - kb0;
+  const int64_t Kp = static_cast<int64_t>(KB) * 64;
+  const uint32_t ring0 = smem_u32(ring);
+  for (int c0 = 0; c0 < job.rank16; c0 += kShrinkBlocks) {
+    // a block of 16 ranks to each warp, the warps of one sharing K
+    const int blocks = min(kShrinkBlocks, job.rank16 - c0);
+    const int spread = blocks == 3 ? 4 : blocks, mine = warp % spread, k_of = warp / spread;
+    const int shares = kFrontWarps / spread;
+    const uint16_t* A = job.a + (static_cast<int64_t>(a) * job.rank16 + c0) * 16 * Kp;
+    const auto fill = [&](int i) {
+      if (i < steps) {
+        const uint32_t st = ring0 + (i % kShrinkStages) * kShrinkStage;
+        const int row = threadIdx.x >> 3, chunk = threadIdx.x & 7;
+        const uint4* x = job.op.dst +
+                         (static_cast<int64_t>(kb0 + i) * job.op.R + row0 + min(row, count - 1)) * 8;
+        cp_async16(st + shrink_at(row, chunk), x + chunk);
+#pragma unroll
+        for (int j = 0; j < kShrinkBlocks / 2; ++j) {
+          const int r = row + j * 32;
+          if (r < blocks * 16)
+            cp_async16(st + shrink_at(kFrontRows + r, chunk),
+                       A + r * Kp + (kb0 + i) * 64 + chunk * 8);
+        }
+      }
+      cp_async_commit();
+    };
+    float acc[4][4] = {};
+    for (int i = 0; i < kShrinkStages - 1; ++i) fill(i);
+    for (int i = 0; i < steps; ++i) {
+      cp_async_wait<kShrinkStages - 2>();
+      __syncthreads();
+      fill(i + kShrinkStages - 1);
+      const uint32_t st = ring0 + (i % kShrinkStages) * kShrinkStage;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (mine >= blocks || (i * 2 + half) % shares != k_of) continue;
+        const int chunk = half * 4 + t;
+        const uint4 lo = lds128(st + shrink_at(kFrontRows + mine * 16 + g, chunk));
+        const uint4 hi = lds128(st + shrink_at(kFrontRows + mine * 16 + g + 8, chunk));
+        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint4 x = lds128(st + shrink_at(n * 8 + g, chunk));
+          if constexpr (!F16) {
+            x.x = f16x2_to_bf16x2(x.x);
+            x.y = f16x2_to_bf16x2(x.y);
+            x.z = f16x2_to_bf16x2(x.z);
+            x.w = f16x2_to_bf16x2(x.w);
+          }
+          mma_16816<F16>(acc[n], a0, x.x, x.y);
+          mma_16816<F16>(acc[n], a1, x.z, x.w);
+        }
+      }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        sh.part[warp][g + (j >> 1) * 8][n * 8 + t * 2 + (j & 1)] = acc[n][j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < blocks * 16 * kFrontRows; i += kFrontThreads) {
+      const int j = i / kFrontRows, col = i % kFrontRows;
+      float v = 0.0f;
+      for (int k = 0; k < shares; ++k) v += sh.part[k * spread + j / 16][j % 16][col];
+      sh.sum[j][col] = v;
+    }
+    cluster.sync();
+    // this CTA's share of the rows
+    const int ranks = blocks * 16, rows = kFrontRows / CL;
+    for (int i0 = threadIdx.x; i0 < ranks * rows; i0 += kFrontThreads) {
+      const int j = i0 % ranks, i = rank * rows + i0 / ranks;
+      if (i < count) {
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kFrontCluster; ++q)
+          if (q < CL) v += *cluster.map_shared_rank(&sh.sum[j][i], q);
+        job.h[static_cast<int64_t>(row0 + i) * job.rank16 * 16 + c0 * 16 + j] =
+            v * job.s_in * __ldg(job.scaling + a);
+      }
+    }
+    cluster.sync();   // the sums may be overwritten now, or this CTA leave
   }
 }
 
@@ -397,8 +559,9 @@ __global__ void __launch_bounds__(256) lora_scaling_kernel(const uint16_t* __res
 
 __global__ void __launch_bounds__(256) pack_lora_kernel(const uint16_t* __restrict__ A,
                                                         const uint16_t* __restrict__ B,
-                                                        uint32_t exponent, int64_t L, int64_t r, int64_t N, int64_t K,
-                                                        int64_t rank16, int64_t NB, int64_t Kp,
+                                                        uint32_t exponent, int64_t L, int64_t r,
+                                                        int64_t N, int64_t K, int64_t rank16,
+                                                        int64_t NB, int64_t Kp,
                                                         uint16_t* __restrict__ a_out,
                                                         uint16_t* __restrict__ b_out) {
   pdl_wait();
@@ -463,20 +626,40 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
                     static_cast<uint16_t*>(a_out), static_cast<uint16_t*>(b_out));
 }
 
+namespace {
+
+// Rows sorted by adapter: the operand, then h from it.
+template <bool F16>
+cudaError_t launch_sorted(LoraJob job, cudaStream_t s) {
+  cudaError_t e = launch_tile_operand(job.op, s);
+  if (e != cudaSuccess) return e;
+  static DeviceOnce once;
+  e = once.run([] {
+    return cudaFuncSetAttribute(lora_shrink_kernel<F16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kShrinkStages * kShrinkStage);
+  });
+  if (e != cudaSuccess) return e;
+  const int units = job.op.R / kFrontRows + std::min(job.L, job.op.R);
+  // K is cut over a cluster while that leaves every SM no more than two CTAs
+  int cl = kFrontCluster;
+  while (cl > 1 && units * cl > 2 * device_sm_count()) cl /= 2;
+  job.shrink_ctas = units * cl;
+  return launch_pdl_cluster(lora_shrink_kernel<F16>,
+                            static_cast<int>(round_up(job.shrink_ctas + job.tiles, cl)),
+                            kFrontThreads, kShrinkStages * kShrinkStage, cl, s, job);
+}
+
+}  // namespace
+
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
-  const bool sorted = job.op.order != nullptr;
-  if (sorted) {
-    cudaError_t e = launch_tile_operand(job.op, s);
-    if (e != cudaSuccess) return e;
-  }
-  const int groups = sorted ? (job.op.R + kFrontRows - 1) / kFrontRows : job.op.R;
+  if (job.op.order != nullptr)
+    return f16 ? launch_sorted<true>(job, s) : launch_sorted<false>(job, s);
   // K is cut over 8 CTAs while the units alone would leave SMs without one
-  const int cl = groups * job.rank16 <= device_sm_count() ? kFrontCluster : 1;
-  job.shrink_ctas = groups * job.rank16 * cl;
-  const int copy =
-      sorted ? 0
-             : blocks_for(std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8,
-                                            job.op.count_words));
+  const int cl = job.op.R * job.rank16 <= device_sm_count() ? kFrontCluster : 1;
+  job.shrink_ctas = job.op.R * job.rank16 * cl;
+  const int copy = blocks_for(
+      std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8, job.op.count_words));
   const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, cl));
   const auto go = [&](auto half, auto vec) {
     constexpr bool F16 = decltype(half)::value, VEC = decltype(vec)::value;
