@@ -774,34 +774,55 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       pdl_wait();
       // Adapters.  This thread fills one row of B (of this CTA's share): h's 16
       // leading tf32 terms, then its 16 trailing ones, in the 128-byte swizzle;
-      // zeros in the rounds of other adapters.  A round's h is fetched before
-      // the round before it is waited for.
+      // zeros in the rounds of other adapters.  h is fetched two rounds before
+      // it is used, whosever the round: what that takes must not wait for the
+      // tile's list (a round took 2,000 cycles when it did, one ahead).
       const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
+      const int na = uniform(sg->na), rank16 = p.rank16;
       const int half = ((sg->rows + 15) & ~15) / CG;
       static_assert(F::kMaxRows / CG <= 128, "one row a thread");
       const int t = (warp & 3) * 32 + lane, s = rank * half + t;
       const bool in = t < half && s < sg->rows;
       const int64_t at_row = static_cast<int64_t>(sg->row0 + (in ? s : 0));
       const int my_a = in ? __ldg(p.ids + at_row) : -1;
-      const float4* h = reinterpret_cast<const float4*>(p.h + at_row * p.rank16 * 16);
-      const int rounds = sg->na * p.rank16;
-      float4 hv[4];
-      const auto fetch = [&](int round) {
-        const bool mine = round < rounds && my_a >= 0 && __ldg(list + round / p.rank16) == my_a;
-        const int c = round % p.rank16;
+      const bool some = my_a >= 0 && my_a < p.L;
+      const float4* h = reinterpret_cast<const float4*>(p.h + at_row * rank16 * 16);
+      const int rounds = na * rank16, skip = F::kGroups == 2 && (it & 1) != group ? 1 : 0;
+      // adapter and block of 16 ranks of a round, the next of this group's
+      struct Place {
+        int i, c;
+      };
+      const auto step = [&](Place& q, int by) {
+        q.c += by;
+        while (q.c >= rank16) {
+          q.c -= rank16;
+          ++q.i;
+        }
+      };
+      Place use{0, 0}, get{0, 0};
+      step(use, skip);
+      step(get, skip);
+      const auto fetch = [&](float4 (&hv)[4]) {
+        const bool want = some && get.i < na;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          hv[g] = mine ? __ldg(h + c * 4 + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+          hv[g] = want ? __ldg(h + get.c * 4 + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+        step(get, F::kGroups);
       };
-      int round = F::kGroups == 2 && (it & 1) != group ? 1 : 0;
-      if (round == 1) advance();
-      fetch(round);
-      while (round < rounds) {
+      int round = 0;
+      int ids = -1, ids_at = -1;   // a lane an entry of the list, 32 of them
+      const auto take = [&](float4 (&hv)[4]) {
+        if (use.i >> 5 != ids_at) {
+          ids_at = use.i >> 5;
+          ids = ids_at * 32 + lane < na ? __ldg(list + ids_at * 32 + lane) : -1;
+        }
+        const int whose = __shfl_sync(0xffffffffu, ids, use.i & 31);   // (by every lane)
+        const bool mine = some && whose == my_a;
         const int as = it & (NA - 1);
         ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
                                        kErrTileRing, p.err);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
         const uint32_t st = ring0 + ring.slot * stage_bytes;
         uint32_t r[16];
@@ -826,7 +847,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t at = st + t * 128;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float f[4] = {hv[g].x, hv[g].y, hv[g].z, hv[g].w};
+            const float f[4] = {mine ? hv[g].x : 0.0f, mine ? hv[g].y : 0.0f,
+                                mine ? hv[g].z : 0.0f, mine ? hv[g].w : 0.0f};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -841,9 +863,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         fence_proxy_async_smem();
         announce(as);
+        fetch(hv);
+        step(use, F::kGroups);
         for (int k = 0; k < F::kGroups; ++k)   // past this round and the partner's
           if (round++ < rounds) advance();
-        fetch(round);
+      };
+      float4 h0[4], h1[4];
+      fetch(h0);
+      fetch(h1);
+      if (skip == 1) advance();
+      round = skip;
+      while (round < rounds) {
+        take(h0);
+        if (!ok || round >= rounds) break;
+        take(h1);
+        if (!ok) break;
       }
       if (!ok) break;
     }
