@@ -99,7 +99,9 @@ LoraSpace lora_space(int64_t M, int64_t K, int64_t L, int64_t r) {
   t.plan = plan_tiles(M, K, 1, lora_by_row(M, L) ? q8::kMaxByRow : q8::kMaxTileRows);
   const int64_t tiles = (M + t.plan.TN - 1) / t.plan.TN;
   t.h = t.plan.total;
-  t.lists = t.h + q8::align_ws(static_cast<size_t>(M) * ((r + 15) / 16) * 64);
+  const size_t rank16 = (r + 15) / 16;
+  t.lists = t.h + q8::align_ws(lora_by_row(M, L) ? static_cast<size_t>(M) * rank16 * 64
+                                                 : static_cast<size_t>(tiles + L) * rank16 * t.plan.TN * 128);
   t.sort = t.lists + q8::align_ws(static_cast<size_t>(tiles) * (t.plan.TN + 1) * 4);
   t.total = t.sort + (tiles > 1 ? q8::align_ws((3 * static_cast<size_t>(M) + L + 1) * 4) : 0);
   return t;
@@ -414,6 +416,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   job.scaling = reinterpret_cast<const float*>(lora + lay.scaling);
   job.s_in = static_cast<float>(input_scale);
   job.h = reinterpret_cast<float*>(ws + sp.h);
+  job.TN = p.by_row ? 0 : p.TN;
   job.lists = reinterpret_cast<int32_t*>(ws + sp.lists);
   cudaError_t e = cudaSuccess;
   if (job.tiles == 1) {

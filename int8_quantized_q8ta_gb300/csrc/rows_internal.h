@@ -114,7 +114,7 @@ struct TileParams {
   int L, rank16, lora_f16;  // adapters, blocks of 16 ranks, f16 (1) or bf16 (0)
   int by_row;               // the term row by row in the epilogue (TN <= kMaxByRow), not by MMAs
   const uint8_t* lora_b;    // packed B (see launch_pack_lora)
-  const float* h;           // [R][rank16 * 16]: s_in * scaling * (x - zp) A^T
+  const float* h;           // s_in * scaling * (x - zp) A^T, as by_row wants it (store_h)
   const int32_t* ids;       // [R] adapter of each row
   const int32_t* lists;     // per row tile: adapter count, then the adapters
   int list_stride;
@@ -158,7 +158,8 @@ struct LoraJob {
   const uint16_t* a;            // packed A
   const float* scaling;
   float s_in;
-  float* h;
+  float* h;                     // [R][rank16 * 16], or blocks for MMAs (store_h)
+  int TN;                       // rows of such a block, or 0
   int32_t* lists;
   int32_t* ids_out;             // [R] in sorted order, or null
   const int32_t* offsets;       // [L + 1] first sorted row of each adapter (with op.order)

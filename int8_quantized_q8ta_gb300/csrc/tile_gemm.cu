@@ -33,7 +33,10 @@
 // Adapters: after a unit's k-blocks, its last run multiplies B[a] by the rows'
 // h for each adapter the tile holds, into an accumulator of its own: tf32
 // MMAs, B exact (f16 and bf16 both fit tf32), h as the sum of two tf32 terms
-// (22 significant bits), rows of other adapters as zeros.
+// (22 significant bits), rows of other adapters as zeros.  The kernel before
+// this one lays h out so, and it comes through the ring like tokens: fetched
+// by the converting warps it queued behind the next unit's copies (a round of
+// 16 ranks 1,350 cycles, and 2,000 before the first).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -112,7 +115,7 @@ struct TileShared {
   uint64_t wfull[kMaxRing];   // weights of a stage have landed
   uint64_t tfull[kMaxRing];   // tokens of a stage have landed (in a pair: both halves, at the leader)
   uint64_t empty[kMaxRing];   // a stage's MMAs are done
-  uint64_t ready[NA];         // A operand in TMEM (and, for adapters, B in shared memory)
+  uint64_t ready[NA];         // A operand in TMEM
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
@@ -408,7 +411,8 @@ __device__ __forceinline__ typename OutType<OUT>::type finish(float v, const Til
 // Two halves of a token tile have rows that are multiples of 8.
 template <int OUT, bool PAIR>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const TileParams p) {
+    tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_h, const TileParams p) {
   using F = Form<PAIR>;
   constexpr int CG = F::CG, KD = F::KD, kCols = F::kCols;
   extern __shared__ __align__(1024) uint8_t dyn[];
@@ -446,6 +450,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     fence_mbar_init();
     sh.abort = 0;
     tma_prefetch_desc(&map_x);
+    if (p.L > 0 && !p.by_row) tma_prefetch_desc(&map_h);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -569,12 +574,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const int rounds = uniform(sg->na) * p.rank16;   // without tokens
-      for (int i = 0; i < rounds; ++i, ++it, ring.advance(S)) {
-        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
-        if (!ok) break;
-        if (leader && elect_one()) mbar_arrive(tfull0 + ring.slot * 8);
-        __syncwarp();
+      // adapters: the tile's h, blocks of 16 ranks in place of k-blocks
+      const int na = uniform(sg->na), tile = uniform(sg->tile);
+      const int32_t* list = p.lists + static_cast<int64_t>(tile) * p.list_stride + 1;
+      const int h0 = row0 - uniform(sg->row0);
+      for (int i = 0; i < na && ok; ++i) {
+        const int at = (tile + uniform(__ldg(list + i))) * p.rank16;
+        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+          ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                              p.err);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t st = ring0 + ring.slot * stage_bytes;
+            if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * tok_bytes);
+            if constexpr (PAIR)
+              tma_load_3d_pair(st, &map_h, tfull_lead + ring.slot * 8, 0, h0, at + c);
+            else
+              tma_load_3d(st, &map_h, tfull0 + ring.slot * 8, 0, h0, at + c);
+          }
+          __syncwarp();
+        }
       }
     }
     if ((!ok || *abort_flag) && leader)
@@ -650,7 +669,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int total = na * p.rank16;
           for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
             const uint32_t as = it & (NA - 1);
-            ok = tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
+            ok = tile_wait_warp(tfull0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing,
+                                p.err) &&
+                 tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
                                 p.err);
             if (!ok) break;
             tc_fence_after();
@@ -703,7 +724,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t a_lane = a_base + (static_cast<uint32_t>(warp & 3) << 21);
     const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
     const uint32_t ready0 = PAIR ? map_to_cta(smem_u32(&sh.ready[0]), 0) : smem_u32(&sh.ready[0]);
-    // (waits for the kernel before this one only where adapters follow)
     Feed feed{sh};
     const Seg* sg;
     Ring ring, used;   // this stage; the one whose A operand lay where this one's goes
@@ -770,59 +790,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         announce(as);
       }
       if (!ok) break;
-      if (sg->na == 0) continue;
-      pdl_wait();
-      // Adapters.  This thread fills one row of B (of this CTA's share): h's 16
-      // leading tf32 terms, then its 16 trailing ones, in the 128-byte swizzle;
-      // zeros in the rounds of other adapters.  h is fetched two rounds before
-      // it is used, whosever the round: what that takes must not wait for the
-      // tile's list (a round took 2,000 cycles when it did, one ahead).
-      const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
-      const int na = uniform(sg->na), rank16 = p.rank16;
-      const int half = ((sg->rows + 15) & ~15) / CG;
-      static_assert(F::kMaxRows / CG <= 128, "one row a thread");
-      const int t = (warp & 3) * 32 + lane, s = rank * half + t;
-      const bool in = t < half && s < sg->rows;
-      const int64_t at_row = static_cast<int64_t>(sg->row0 + (in ? s : 0));
-      const int my_a = in ? __ldg(p.ids + at_row) : -1;
-      const bool some = my_a >= 0 && my_a < p.L;
-      const float4* h = reinterpret_cast<const float4*>(p.h + at_row * rank16 * 16);
-      const int rounds = na * rank16, skip = F::kGroups == 2 && (it & 1) != group ? 1 : 0;
-      // adapter and block of 16 ranks of a round, the next of this group's
-      struct Place {
-        int i, c;
-      };
-      const auto step = [&](Place& q, int by) {
-        q.c += by;
-        while (q.c >= rank16) {
-          q.c -= rank16;
-          ++q.i;
-        }
-      };
-      Place use{0, 0}, get{0, 0};
-      step(use, skip);
-      step(get, skip);
-      const auto fetch = [&](float4 (&hv)[4]) {
-        const bool want = some && get.i < na;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          hv[g] = want ? __ldg(h + get.c * 4 + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-        step(get, F::kGroups);
-      };
-      int round = 0;
-      int ids = -1, ids_at = -1;   // a lane an entry of the list, 32 of them
-      const auto take = [&](float4 (&hv)[4]) {
-        if (use.i >> 5 != ids_at) {
-          ids_at = use.i >> 5;
-          ids = ids_at * 32 + lane < na ? __ldg(list + ids_at * 32 + lane) : -1;
-        }
-        const int whose = __shfl_sync(0xffffffffu, ids, use.i & 31);   // (by every lane)
-        const bool mine = some && whose == my_a;
+      // adapters: B[a]'s blocks of 16 ranks, in tf32
+      const int rounds = sg->na * p.rank16;
+      for (int round = 0; round < rounds; ++round, advance()) {
+        if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
         ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
                                        kErrTileRing, p.err);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+        if (!ok) break;
         tc_fence_after();
         const uint32_t st = ring0 + ring.slot * stage_bytes;
         uint32_t r[16];
@@ -843,41 +819,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         tmem_st_16cols(a_lane + as * KD * 32, r);
-        if (t < half) {
-          const uint32_t at = st + t * 128;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float f[4] = {mine ? hv[g].x : 0.0f, mine ? hv[g].y : 0.0f,
-                                mine ? hv[g].z : 0.0f, mine ? hv[g].w : 0.0f};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              hi[j] = __float_as_uint(f[j]) & 0xffffe000u;
-              lo[j] = (hi[j] & 0x7f800000u) == 0x7f800000u   // inf - inf would be NaN
-                          ? 0u
-                          : __float_as_uint(__fsub_rn(f[j], __uint_as_float(hi[j])));
-            }
-            sts128(at + ((g ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-            sts128(at + (((g + 4) ^ (t & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        fence_proxy_async_smem();
         announce(as);
-        fetch(hv);
-        step(use, F::kGroups);
-        for (int k = 0; k < F::kGroups; ++k)   // past this round and the partner's
-          if (round++ < rounds) advance();
-      };
-      float4 h0[4], h1[4];
-      fetch(h0);
-      fetch(h1);
-      if (skip == 1) advance();
-      round = skip;
-      while (round < rounds) {
-        take(h0);
-        if (!ok || round >= rounds) break;
-        take(h1);
-        if (!ok) break;
       }
       if (!ok) break;
     }
@@ -1198,7 +1140,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 template <int OUT, bool PAIR>
-cudaError_t launch_one(const CUtensorMap& map, const TileParams& p, size_t smem, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap& map, const CUtensorMap& map_h, const TileParams& p, size_t smem, cudaStream_t s) {
   constexpr int CG = Form<PAIR>::CG;
   auto kernel = tile_gemm_kernel<OUT, PAIR>;
   static DeviceOnce once;
@@ -1232,9 +1174,9 @@ cudaError_t launch_one(const CUtensorMap& map, const TileParams& p, size_t smem,
       pairs = n;
     }
     const int grid = std::max(1, std::min(pairs, p.grid / CG)) * CG;
-    return launch_pdl_cluster(kernel, grid, kTileThreads, smem, CG, s, map, p);
+    return launch_pdl_cluster(kernel, grid, kTileThreads, smem, CG, s, map, map_h, p);
   } else {
-    return launch_pdl(kernel, p.grid, kTileThreads, smem, s, map, p);
+    return launch_pdl(kernel, p.grid, kTileThreads, smem, s, map, map_h, p);
   }
 }
 
@@ -1247,15 +1189,25 @@ cudaError_t launch_form(TileParams p, const void* operand, q8_dtype out_dtype, c
   const uint32_t box[3] = {64, static_cast<uint32_t>(p.TN / F::CG), F::KD};
   // (16-bit elements; the map's element type only matters for reductions)
   if (!encode_bf16_tmap(&map, operand, 3, dims, str, box)) return cudaErrorInvalidValue;
+  CUtensorMap map_h = map;
+  if (p.L > 0 && !p.by_row) {
+    // h in rows of 16 leading and 16 trailing f32 terms
+    const int64_t blocks =
+        (static_cast<int64_t>((p.R + p.TN - 1) / p.TN) + p.L) * p.rank16;
+    const uint64_t dims_h[3] = {64, static_cast<uint64_t>(p.TN), static_cast<uint64_t>(blocks)};
+    const uint64_t str_h[2] = {128, static_cast<uint64_t>(p.TN) * 128};
+    const uint32_t box_h[3] = {64, static_cast<uint32_t>(p.TN / F::CG), 1};
+    if (!encode_bf16_tmap(&map_h, p.h, 3, dims_h, str_h, box_h)) return cudaErrorInvalidValue;
+  }
   const size_t stage = static_cast<size_t>(F::KD) * (p.TN / F::CG * 128 + kTileWBytes);
   const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
   p.stages = static_cast<int>(std::min<size_t>(F::kRing, (kTileSmem - 1024 - table) / stage));
   const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
   switch (out_dtype) {
-    case Q8_I8: return launch_one<Q8_I8, PAIR>(map, p, smem, s);
-    case Q8_F32: return launch_one<Q8_F32, PAIR>(map, p, smem, s);
-    case Q8_F16: return launch_one<Q8_F16, PAIR>(map, p, smem, s);
-    default: return launch_one<Q8_BF16, PAIR>(map, p, smem, s);
+    case Q8_I8: return launch_one<Q8_I8, PAIR>(map, map_h, p, smem, s);
+    case Q8_F32: return launch_one<Q8_F32, PAIR>(map, map_h, p, smem, s);
+    case Q8_F16: return launch_one<Q8_F16, PAIR>(map, map_h, p, smem, s);
+    default: return launch_one<Q8_BF16, PAIR>(map, map_h, p, smem, s);
   }
 }
 

@@ -171,7 +171,8 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 constexpr int kFrontWarps = kFrontThreads / 32;
 
 struct ListShared {
-  int32_t rows[kMaxTileRows];     // the rows this cluster takes, or a tile's adapters
+  int32_t rows[kMaxTileRows];     // the rows this cluster takes, or a tile's rows' adapters
+  int32_t held[kMaxTileRows];     // a tile's adapters
   int32_t warp_count[kFrontWarps];
 };
 struct FrontShared {
@@ -239,6 +240,26 @@ __device__ __forceinline__ void front_products(const LoraJob& job, const uint16_
   }
 }
 
+// h[s, j].  For dot products row by row: [R][ranks].  For MMAs: a block of
+// [TN rows][16 leading terms, 16 trailing ones] for each adapter a tile t holds
+// and 16 ranks, at (t + a) * rank16 + c (with the rows sorted by adapter,
+// either t or a grows from one such pair to the next), both terms f32 of which
+// the MMAs read the 10 leading bits of the fraction.
+__device__ __forceinline__ void store_h(const LoraJob& job, int s, int a, int j, float v) {
+  if (job.TN == 0) {
+    job.h[static_cast<int64_t>(s) * job.rank16 * 16 + j] = v;
+    return;
+  }
+  const int per = tile_rows(job.op.R, job.tiles), t = s / per;
+  float* at = job.h +
+              ((static_cast<int64_t>(t + a) * job.rank16 + (j >> 4)) * job.TN + (s - t * per)) * 32 +
+              (j & 15);
+  const float hi = __uint_as_float(__float_as_uint(v) & 0xffffe000u);
+  at[0] = hi;
+  // (inf - inf would be NaN)
+  at[16] = (__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u ? 0.0f : __fsub_rn(v, hi);
+}
+
 // 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
 template <bool F16, int CL, bool VEC>
 __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
@@ -280,8 +301,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
       } else {
         v = sh.sum[j][i];
       }
-      job.h[static_cast<int64_t>(rows[i]) * job.rank16 * 16 + c * 16 + j] =
-          v * job.s_in * __ldg(job.scaling + a);
+      store_h(job, rows[i], a, c * 16 + j, v * job.s_in * __ldg(job.scaling + a));
     }
   }
   // the sums may be overwritten now
@@ -311,8 +331,13 @@ __device__ int block_compact(ListShared& sh, bool flag, int32_t value, int32_t* 
   return total;
 }
 
-// A tile's adapters, each once, in the order of their first rows.
-__device__ void list_tile(const LoraJob& job, ListShared& sh, int tile) {
+// A tile's adapters, each once, in the order of their first rows; and, where
+// MMAs take them, zeros in the rows of h's blocks that are other adapters'.
+// kListCtas CTAs share a tile's blocks.
+constexpr int kListCtas = 4;
+
+__device__ void list_tile(const LoraJob& job, ListShared& sh, int cta) {
+  const int tile = cta / kListCtas, part = cta % kListCtas;
   const int per = tile_rows(job.op.R, job.tiles), row0 = tile * per, n = min(per, job.op.R - row0);
   const int t = threadIdx.x;
   const int a = t < n ? adapter_of(job, row0 + t) : -1;
@@ -322,12 +347,25 @@ __device__ void list_tile(const LoraJob& job, ListShared& sh, int tile) {
   for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
   __syncthreads();
   int32_t* list = job.lists + static_cast<int64_t>(tile) * job.list_stride;
-  const int count = block_compact(sh, first, a, list + 1);
-  if (t == 0) list[0] = count;
-  if (job.ids_out != nullptr && t < n) job.ids_out[row0 + t] = a;
+  if (part == 0) {
+    const int count = block_compact(sh, first, a, list + 1);
+    if (t == 0) list[0] = count;
+    if (job.ids_out != nullptr && t < n) job.ids_out[row0 + t] = a;
+  }
+  if (job.TN == 0) return;
+  const int held = block_compact(sh, first, a, sh.held);
+  const int blocks = held * job.rank16, rows = (n + 15) & ~15, lane = t & 31;
+  // a warp a block, 4 rows of 128 bytes at a time
+  for (int b = part * kFrontWarps + (t >> 5); b < blocks; b += kListCtas * kFrontWarps) {
+    const int own = sh.held[b / job.rank16];
+    float4* to = reinterpret_cast<float4*>(
+        job.h + (static_cast<int64_t>(tile + own) * job.rank16 + b % job.rank16) * job.TN * 32);
+    for (int i = lane >> 3; i < rows; i += 4)
+      if (i >= n || sh.rows[i] != own) to[i * 8 + (lane & 7)] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 }
 
-// Blocks: job.shrink_ctas for h, then one for the list, the rest for the
+// Blocks: job.shrink_ctas for h, then kListCtas for the list, the rest for the
 // operand.
 template <bool F16, int CL, bool VEC>
 __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const LoraJob job) {
@@ -350,14 +388,14 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
     return;
   }
   b -= job.shrink_ctas;
-  if (b < job.tiles) {
+  if (b < kListCtas) {
     list_tile(job, sh.list, b);
     return;
   }
-  b -= job.tiles;
+  b -= kListCtas;
   const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
   const int64_t step =
-      static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.tiles) * kFrontThreads;
+      static_cast<int64_t>(gridDim.x - job.shrink_ctas - kListCtas) * kFrontThreads;
   for (int64_t i = t; i < job.op.count_words; i += step) job.op.counts[i] = 0;
   const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
   const uint32_t chunks = job.op.KB * 8;
@@ -430,8 +468,8 @@ __device__ bool find_piece(const LoraJob& job, ShrinkShared& sh, int u) {
   return false;
 }
 
-// Blocks: job.shrink_ctas for h, in clusters, then one per row tile for its
-// list.
+// Blocks: job.shrink_ctas for h, in clusters, then kListCtas per row tile for
+// its list.
 template <bool F16>
 __global__ void __launch_bounds__(kFrontThreads, 2)
     lora_shrink_kernel(const __grid_constant__ LoraJob job) {
@@ -440,7 +478,7 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
   pdl_wait();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) >= job.shrink_ctas) {
-    if (static_cast<int>(blockIdx.x) - job.shrink_ctas < job.tiles)
+    if (static_cast<int>(blockIdx.x) - job.shrink_ctas < job.tiles * kListCtas)
       list_tile(job, sh.list, blockIdx.x - job.shrink_ctas);
     return;
   }
@@ -526,8 +564,7 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
 #pragma unroll
         for (int q = 0; q < kFrontCluster; ++q)
           if (q < CL) v += *cluster.map_shared_rank(&sh.sum[j][i], q);
-        job.h[static_cast<int64_t>(row0 + i) * job.rank16 * 16 + c0 * 16 + j] =
-            v * job.s_in * __ldg(job.scaling + a);
+        store_h(job, row0 + i, a, c0 * 16 + j, v * job.s_in * __ldg(job.scaling + a));
       }
     }
     cluster.sync();   // the sums may be overwritten now, or this CTA leave
@@ -646,7 +683,7 @@ cudaError_t launch_sorted(LoraJob job, cudaStream_t s) {
   while (cl > 1 && units * cl > 2 * device_sm_count()) cl /= 2;
   job.shrink_ctas = units * cl;
   return launch_pdl_cluster(lora_shrink_kernel<F16>,
-                            static_cast<int>(round_up(job.shrink_ctas + job.tiles, cl)),
+                            static_cast<int>(round_up(job.shrink_ctas + job.tiles * kListCtas, cl)),
                             kFrontThreads, kShrinkStages * kShrinkStage, cl, s, job);
 }
 
@@ -660,7 +697,7 @@ cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
   job.shrink_ctas = job.op.R * job.rank16 * cl;
   const int copy = blocks_for(
       std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8, job.op.count_words));
-  const int grid = static_cast<int>(round_up(job.shrink_ctas + job.tiles + copy, cl));
+  const int grid = static_cast<int>(round_up(job.shrink_ctas + kListCtas + copy, cl));
   const auto go = [&](auto half, auto vec) {
     constexpr bool F16 = decltype(half)::value, VEC = decltype(vec)::value;
     return cl == 1 ? launch_pdl(lora_front_kernel<F16, 1, VEC>, grid, kFrontThreads, 0, s, job)
