@@ -252,3 +252,22 @@ def test_binding_refusals():
         call(activation="gelu")
     with pytest.raises(ValueError):
         q8.pack_tile_weight(T(w)[0, 0])
+
+
+# Output blocks cut between CTAs, and joined: two or more CTAs to each of a few
+# blocks; runs that end one block and begin the next, in both forms
+@pytest.mark.parametrize("M,N,K", [(8, 1024, 4096), (20, 25600, 3456), (64, 6144, 4100),
+                                   (100, 25600, 2688), (150, 2048, 4096)])
+def test_blocks_cut_between_ctas(M, N, K):
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x = torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    ws = torch.rand(1, N, generator=g, device=DEV) * 0.004 + 0.001
+    route = q8.expert_sort(torch.zeros(M, 1, dtype=torch.int32, device=DEV), 1)
+    packed = q8.pack_tile_weight(w)
+    acc = torch.cat([(x.double() + 7) @ part.double().T for part in w.split(4096)], 1)
+    v = acc.float() * torch.tensor(np.float32(0.01), device=DEV) * ws
+    for _ in range(3):   # (joins depend on which CTA comes last, results must not)
+        got = q8.linear_experts(x, 0.01, -7, packed, ws, None, route, 1.0, 0,
+                                out_dtype=torch.float32)
+        assert torch.equal(got, v + 0.0)

@@ -290,3 +290,19 @@ def test_binding_refusals():
     with pytest.raises(q8.Q8Error):
         q8.pack_lora(torch.zeros((1, 257, 8), dtype=torch.float16, device=DEV),
                      torch.zeros((1, 8, 257), dtype=torch.float16, device=DEV), s[:1])
+
+
+@pytest.mark.parametrize("M,L,r", [(1, 3, 16), (20, 20, 16), (40, 2, 24), (300, 100, 16),
+                                   (300, 5, 40)])
+def test_workspace_contents_do_not_matter(M, L, r):
+    p = Problem(M + L, M, 260, 320, L, r, torch.float16, zp=4, bare=0.2)
+    n = q8.lib().q8_linear_lora_workspace_bytes(p.M, p.K, p.L, p.r)
+    _check(p, workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV))
+
+
+def test_a_tile_of_many_adapters():
+    """One adapter has most rows, some eighty others one each."""
+    p = Problem(11, 700, 132, 192, 90, 16, torch.float16, zp=1)
+    p.a[:] = 40
+    p.a[np.arange(0, 700, 8)] = np.arange(88)
+    _check(p)
