@@ -543,7 +543,8 @@ q8_status q8_expert_combine_backward(const void* dy, const void* z, q8_dtype dty
  * inputs of one row (results never depend on it).  q8_tile_pack_weight
  * takes [E, N, K] (E = 1: one weight), waits for the packing, and a packed
  * buffer is rewritten only by packing into it again.
- * Guards: those of q8_expert_sort; 1 <= N <= 2^24, K >= 1; E*N*K within int64; the scale
+ * Guards: those of q8_expert_sort; 1 <= N <= 2^24, K >= 1; E*N*K within
+ * int64; (row tiles) * (output blocks) * (k-blocks) within int32; the scale
  * and zero-point ranges; activation "none" or "relu"; workspace of
  * q8_linear_experts_workspace_bytes(T*k, K, E) bytes and the packed weight
  * 256-byte aligned.  Order entries outside the rows of x leave their sorted
@@ -575,15 +576,15 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
  *   float [L].  q8_lora_pack lays them out once, at load time, and waits (an
  *   adapter is exchanged by packing again).
  * The adapter sums are f32; h enters the second product as two tf32 terms (22
- * significant bits), A, B and x - input_zero_point exactly.  Results do not
- * depend on timing.  Infinities and NaN stay with the rows of their adapter:
+ * significant bits; with fewer than 7 rows an adapter, as it is), A, B and
+ * x - input_zero_point exactly.  Results do not depend on timing.  Infinities and NaN stay with the rows of their adapter:
  * one in A gives what the formula gives, one in B makes every channel of its
  * adapter's rows NaN.
  *   weight       packed by q8_tile_pack_weight with E = 1
  *   out          [M, N] of out_dtype
- * Guards: M >= 0 (0: nothing to do), 1 <= N <= 2^24, K >= 1, 1 <= L <= 1024, 1 <= r <= 256,
- * adapters Q8_F16 or Q8_BF16 (else Q8_ERR_UNSUPPORTED), the scale and
- * zero-point ranges; workspace of q8_linear_lora_workspace_bytes(M, K, L, r)
+ * Guards: M >= 0 (0: nothing to do), K >= 1, 1 <= L <= 1024, 1 <= r <= 256,
+ * N and the tiles' count as in q8_linear_experts, adapters Q8_F16 or Q8_BF16
+ * (else Q8_ERR_UNSUPPORTED), the scale and zero-point ranges; workspace of q8_linear_lora_workspace_bytes(M, K, L, r)
  * bytes, packed weight and packed adapters 256-byte aligned.
  */
 size_t q8_lora_packed_bytes(int64_t L, int64_t N, int64_t K, int64_t r);

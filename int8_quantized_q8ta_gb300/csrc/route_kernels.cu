@@ -14,6 +14,13 @@
 //            dw[t,j] = <dy[t], z[position[t,j]]>
 // Sums are f32, taken in slot order j = 0, 1, ..., rounded once to the row
 // type.  No atomics on global memory: results do not depend on timing.
+//   All but the sort are bound by HBM in long batches and by the latency of
+// position -> row -> row in short ones.  Measured (cold, one launch, of 6.7
+// TB/s copied): rows of 4096 bf16, 2048 tokens of 4 experts: gather 12.3 us
+// (84 MB, 6.8 TB/s), its gradient 16 us (5.2 TB/s); 4096 tokens of 8: combine
+// 48.5 us (302 MB, 6.2 TB/s), its gradient 85 us (573 MB, 6.7 TB/s).  Rows that
+// are no multiple of 16 bytes go element by element: 3885 rows of 1001 halfs,
+// combine 7.3 and its gradient 7.8 us (1.3 and 2.2 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,7 +47,11 @@ namespace {
 // is (all slots of lower experts) + (its expert's slots in earlier CTAs) +
 // (in earlier warps of its CTA) + (earlier in its warp): stable by
 // construction.  The CTAs exchange their E + 1 totals through distributed
-// shared memory; nothing but the ids is read from global memory.
+// shared memory; nothing but the ids is read from global memory.  A warp's
+// slots of one expert are found by one ballot for each bit of the id (a match
+// instruction takes as long as there are different ids).  Latency bounds it:
+// 8 slots 3.0 us, 1024 4.2, 8192 5.0, 32768 6.6, and from there on the 8 CTAs'
+// own work, 262144 slots 26 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortKeys = 4;              // ids a thread has in flight
@@ -209,7 +220,8 @@ __device__ __forceinline__ void zero_tail(typename VecOf<VB>::type* rows, int64_
 }
 
 // gather: a warp takes U*32 vectors of one token's row, read once and written
-// to each of the token's kept rows.
+// to each of the token's kept rows (k writes to one read: slots in sorted order
+// would read every row k times).
 template <int VB, int U>
 __global__ void __launch_bounds__(256) expert_gather_kernel(
     const typename VecOf<VB>::type* __restrict__ x, int64_t T, int k, int64_t V,
@@ -239,7 +251,9 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(
 }
 
 // spread: a warp takes U*32 vectors of one token's sum, S slots' loads in
-// flight.  w: null for ones.
+// flight (one slot after another took 15 instead of 10.7 us for 777 tokens'
+// combine and its gradient, 37 instead of 35 for 2048 tokens' dispatch and
+// its).  w: null for ones.
 template <typename T, int VB, int U, int S>
 __global__ void __launch_bounds__(256) expert_spread_kernel(
     const typename VecOf<VB>::type* __restrict__ z, const float* __restrict__ w, int64_t Tn, int k,
@@ -302,8 +316,9 @@ __global__ void __launch_bounds__(256) expert_spread_kernel(
   }
 }
 
-// combine's gradient: a warp takes one slot, its whole row: dz is the token's
-// dy times the slot's weight, dw the dot of dy with the slot's z.
+// combine's gradient: a warp takes one slot, its whole row, U vectors at a time:
+// dz is the token's dy times the slot's weight, dw the dot of dy with the
+// slot's z.  dy comes from L2 for all but a token's first slot.
 template <typename T, int VB, int U>
 __global__ void __launch_bounds__(256) expert_combine_bwd_kernel(
     const typename VecOf<VB>::type* __restrict__ dy, const typename VecOf<VB>::type* __restrict__ z,

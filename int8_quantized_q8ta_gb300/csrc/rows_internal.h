@@ -148,9 +148,10 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
                              int64_t L, int64_t r, int64_t N, int64_t K, void* a_out, void* b_out,
                              float* s_out, cudaStream_t s);
 
-// Everything the contraction with adapters needs before it, in one launch:
-// the operand (op.k == 1; op.order null when the rows come as they are), each
-// row's h, each row tile's adapters, and the rows' adapters in their order.
+// Everything the contraction with adapters needs before it, in one launch, two
+// for sorted rows: the operand (op.k == 1; op.order null when the rows come as
+// they are), each row's h, each row tile's adapters, and the rows' adapters in
+// their order.
 struct LoraJob {
   OperandJob op;
   const int32_t* adapter_ids;   // [R], in the order of x

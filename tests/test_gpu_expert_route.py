@@ -167,6 +167,12 @@ def test_combine_and_gradients(T, k, E, H, drop, dtype):
     assert torch.all(dw.cpu()[~kept] == 0)
 
 
+@pytest.mark.parametrize("k", [31, 33, 70])
+def test_more_slots_than_a_warp_has_lanes(k):
+    test_combine_and_gradients(6, k, 80, 40, 0.2, torch.float32)
+    test_combine_and_gradients(6, k, 80, 41, 0.2, torch.float16)
+
+
 def test_gradients_against_differences():
     """<dy, combine> is linear in z and in w: a central difference along a
     direction equals the gradient's product with it, up to f32 rounding of
