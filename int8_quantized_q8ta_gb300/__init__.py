@@ -181,11 +181,11 @@ _lib = _LazyLib()
 # ---------------------------------------------------------------------------
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need(t: torch.Tensor, dtype, name: str):

@@ -12,25 +12,20 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _workspace
+from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _stream, _workspace
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
 
 
 # These calls are short on the GPU (some 5 to 20 us), so the host's part is
-# kept short too: addresses go to ctypes as plain integers, one combined check
-# a tensor (the slow one, which names what is wrong, only where it fails), the
-# stream's raw handle, sizes of workspaces remembered by shape.
+# kept short too: one combined check a tensor (the slow one, which names what is
+# wrong, only where it fails), sizes of workspaces remembered by shape.
 
 def _arg(t: torch.Tensor, dtype, name: str) -> int:
     """The address of a contiguous CUDA tensor of this dtype."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
         _need(t, dtype, name)
     return t.data_ptr()
-
-
-def _stream(t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -103,10 +98,8 @@ def _empty_route(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
     if not 1 <= num_experts <= 1024:
         raise ValueError(f"num_experts must lie in [1, 1024], got {num_experts}")
     T, k = expert_ids.shape
-    dev = expert_ids.device
-    return ExpertRoute(torch.empty(T * k, dtype=torch.int32, device=dev),
-                       torch.empty((T, k), dtype=torch.int32, device=dev),
-                       torch.empty(num_experts + 1, dtype=torch.int32, device=dev))
+    return ExpertRoute(expert_ids.new_empty(T * k), torch.empty_like(expert_ids),
+                       expert_ids.new_empty(num_experts + 1))
 
 
 def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
