@@ -21,7 +21,7 @@
 //
 // Exactness: |x - zp| <= a and sum |w| over 64 inputs <= W give f32 sums that
 // are exact integers for 2^24 / (a W) k-blocks; such a chunk is then drained
-// from TMEM into int32 registers while the other accumulator fills.
+// from TMEM into int32 registers while another accumulator fills.
 //
 // Work split: whole waves of (tile, output block) units, then the last one to
 // two waves' k-blocks as one line cut into equal runs, one per CTA, so that a
@@ -59,7 +59,7 @@ constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
 constexpr int kFirstConv = 4;           // warps 0 to 3: weights, MMAs, tokens, schedule
 constexpr int kTileThreads = 640;
 constexpr int kTmemCols = 512;
-// Stages of A operands in tensor memory, behind the two accumulators.
+// Stages of A operands in tensor memory, behind the accumulators.
 constexpr int NAb = 2, NA = 1 << NAb;
 
 // Whole units to each CTA while that lengthens the longest run by no more than
@@ -97,10 +97,15 @@ struct Form {
   static constexpr int kGroups = kConv / 4;        // groups of four take turns
   static constexpr int kEpi = PAIR ? 12 : 8;       // epilogue warps
   static constexpr int kCols = PAIR ? 64 : 32;     // accumulator columns of each
+  // Accumulators (a third one while the epilogue's first dot products take
+  // longer than two exact chunks: 64 rows x 11008 x 4096 waited 3 us)
+  static constexpr int kAcc = PAIR ? 2 : 3;
   static constexpr int kRing = PAIR ? kMaxRing : 6;   // stages at most
   static constexpr int kFirstEpi = kFirstConv + kConv;
   static_assert(32 * (kFirstEpi + kEpi) == kTileThreads, "one block size");
   static constexpr int kMaxRows = kCols * kEpi / 4;
+  // accumulators, A operands, and row by row the adapters' terms
+  static_assert(kAcc * kMaxRows + NA * KD * 32 + (PAIR ? 0 : kMaxRows) <= kTmemCols, "TMEM");
   // int32 words of one CTA's part of a unit
   static constexpr int kPart = kEpi * kCols * 32;
   static_assert(kPart <= kTilePartWords, "workspace");
@@ -119,11 +124,11 @@ constexpr int kSegs = 4;       // parts on their way
 
 struct TileShared {
   uint64_t wfull[kMaxRing];   // weights of a stage have landed
-  uint64_t tfull[kMaxRing];   // tokens of a stage have landed (in a pair: both halves, at the leader)
+  uint64_t tfull[kMaxRing];   // tokens of a stage have landed (a pair's halves: at the leader)
   uint64_t empty[kMaxRing];   // a stage's MMAs are done
   uint64_t ready[NA];         // A operand in TMEM
-  uint64_t acc_full[2];
-  uint64_t acc_empty[2];
+  uint64_t acc_full[3];
+  uint64_t acc_empty[3];
   uint64_t drain;
   uint64_t seg_full[kSegs];   // a part is described
   uint64_t seg_empty[kSegs];  // every warp has read it
@@ -340,6 +345,7 @@ __device__ __forceinline__ void row_deltas(const TileParams& p, int nb, int row,
   const int my_at = mine ? my_a * p.NB + nb : 0;
 #pragma unroll
   for (int u = 0; u < 8; ++u) d[u] = 0.0f;
+  if (have == 0) return;
   // this lane's quarter of 16 ranks of row lane / 4 (rows without an adapter
   // have no h)
   const bool h_in = (have >> (lane >> 2)) & 1;
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < NA; ++i) mbar_init(smem_u32(&sh.ready[i]), 4 * CG);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < F::kAcc; ++i) {
       mbar_init(smem_u32(&sh.acc_full[i]), 1);
       mbar_init(smem_u32(&sh.acc_empty[i]), F::kEpi * CG);
     }
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if constexpr (PAIR) cluster_sync_all();   // the peer's barriers exist before any use
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t a_base = tmem + 2 * acc_cols;
+  const uint32_t a_base = tmem + F::kAcc * acc_cols;
   volatile uint32_t* abort_flag = &sh.abort;
   const int tiles = sh.tiles;
 
@@ -520,7 +526,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg->e)) * p.NB + nb) * w_rows;
       for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
         const uint32_t bytes = min(KD, kb1 - kb) * kTileWBytes;
-        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
+        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                            p.err);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t bar = wfull0 + ring.slot * 8;
@@ -535,8 +542,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (na > 0) pdl_wait();
       const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
       for (int i = 0; i < na && ok; ++i) {
-        const uint8_t* lb = p.lora_b + ((static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb) *
-                                        p.rank16) * 4096;
+        const int64_t at = static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb;
+        const uint8_t* lb = p.lora_b + at * p.rank16 * 4096;
         for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
@@ -567,7 +574,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int kb1 = uniform(sg->kb1);
       const int row0 = uniform(sg->row0) + rank * (((uniform(sg->rows) + 15) & ~15) / CG);
       for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
-        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing, p.err);
+        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                            p.err);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t st = ring0 + ring.slot * stage_bytes;
@@ -614,10 +622,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
       const uint32_t ready0 = smem_u32(&sh.ready[0]);
       const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
-      const uint32_t d0 = uniform(tmem), a0 = d0 + 2 * acc_cols;
+      const uint32_t d0 = uniform(tmem), a0 = d0 + F::kAcc * acc_cols;
       const uint64_t desc0 = sw128_kmajor_desc(0);
-      Ring ring;
-      int it = 0, ac = 0;
+      Ring ring, ac;   // stages, accumulators
+      int it = 0;
       bool ok = true;
       const int chunk = uniform(chunk_stages_of<KD>(p));
       while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
@@ -626,9 +634,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int kb = uniform(sg->kb0);
         const int kb1 = uniform(sg->kb1);
         const int stages = (kb1 - kb + KD - 1) / KD;
-        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ++ac) {
-          const uint32_t buf = ac & 1;
-          ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
+        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ac.advance(F::kAcc)) {
+          const uint32_t buf = ac.slot;
+          ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = d0 + buf * acc_cols;
@@ -655,7 +663,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (two) {
                 const uint64_t b1 = b + (tok_bytes >> 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) umma_f16_ta<CG>(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
+                for (int j = 0; j < 4; ++j)
+                  umma_f16_ta<CG>(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
               }
               umma_commit_all<CG>(empty0 + ring.slot * 8);
               if (s + 1 == c1) umma_commit_all<CG>(accf0 + buf * 8);
@@ -666,8 +675,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         const int na = uniform(sg->na);
         if (na > 0) {
-          const uint32_t buf = ac & 1;
-          ok = tile_wait_warp(acce0 + buf * 8, ((ac >> 1) & 1) ^ 1, abort_flag, kErrTileAcc, p.err);
+          const uint32_t buf = ac.slot;
+          ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = d0 + buf * acc_cols;
@@ -692,7 +701,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             __syncwarp();
           }
-          ++ac;
+          ac.advance(F::kAcc);
         }
       }
       if (!ok || *abort_flag) {
@@ -865,12 +874,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int a = __ldg(p.ids + part->row0 + min(col0 + j + (lane >> 3), part->rows - 1));
         if (a >= 0 && a < p.L)
           for (int c = 0; c < p.rank16; ++c)
-            prefetch_l2(p.lora_b +
-                        ((static_cast<int64_t>(a) * p.NB + min(nb, p.NB - 1)) * p.rank16 + c) * 4096 +
-                        ((lane >> 2) & 1) * 2048 + quarter * 512 + (lane & 3) * 128);
+            prefetch_l2(
+                p.lora_b +
+                ((static_cast<int64_t>(a) * p.NB + min(nb, p.NB - 1)) * p.rank16 + c) * 4096 +
+                ((lane >> 2) & 1) * 2048 + quarter * 512 + (lane & 3) * 128);
       }
     };
-    int ac = 0;
+    Ring ac;   // accumulators
     bool ok = true, first_seg = true;
     while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
       const int mine = max(0, min(cols, sg->rows - col0));    // columns with a row behind them
@@ -893,17 +903,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           float d[8];
           row_deltas(p, min(nb, p.NB - 1), quarter * 32 + lane, __ldg(p.ids + my_s), my_s,
                      sh.corner[ew], d);
-          tmem_st_8cols(lane_addr + 2 * acc_cols + NA * KD * 32 + j, d);
+          tmem_st_8cols(lane_addr + F::kAcc * acc_cols + NA * KD * 32 + j, d);
         }
         tmem_st_wait();
       }
       int32_t acc[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[j] = 0;
-      for (int c0 = 0; c0 < stages; c0 += chunk, ++ac) {
-        const int buf = ac & 1;
+      for (int c0 = 0; c0 < stages; c0 += chunk, ac.advance(F::kAcc)) {
+        const int buf = ac.slot;
         ok = __all_sync(0xffffffffu,
-                        tile_wait(smem_u32(&sh.acc_full[buf]), (ac >> 1) & 1, abort_flag,
+                        tile_wait(smem_u32(&sh.acc_full[buf]), ac.phase, abort_flag,
                                   kErrTileAcc, p.err));
         if (!ok) break;
         tc_fence_after();
@@ -920,17 +930,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       // the MMAs' adapter term stays in its accumulator until it is used
       const bool by_mma = sg->na > 0;
-      const int dbuf = ac & 1;
+      const int dbuf = ac.slot;
       if (by_mma) {
         ok = __all_sync(0xffffffffu,
-                        tile_wait(smem_u32(&sh.acc_full[dbuf]), (ac >> 1) & 1, abort_flag,
+                        tile_wait(smem_u32(&sh.acc_full[dbuf]), ac.phase, abort_flag,
                                   kErrTileAcc, p.err));
         if (!ok) break;
         tc_fence_after();
-        ++ac;
+        ac.advance(F::kAcc);
       }
       const bool has_d = by_row || by_mma;
-      const uint32_t d_addr = lane_addr + (by_row ? 2 * acc_cols + NA * KD * 32 : dbuf * acc_cols);
+      const uint32_t d_addr =
+          lane_addr + (by_row ? F::kAcc * acc_cols + NA * KD * 32 : dbuf * acc_cols);
       // Loops over parts, which a CTA runs once or twice, take 16 columns a
       // round and stay rolled (code that runs once costs more to fetch than to
       // execute): the registers move up by 16 instead.
@@ -1010,8 +1021,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     const int32_t* other = part_at(use ? c : me, c == first ? 1 : 0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                      v[k][q] = use ? __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128))
-                                    : make_int4(0, 0, 0, 0);
+                      v[k][q] =
+                          use ? __ldcg(reinterpret_cast<const int4*>(other + (b * 4 + q) * 128))
+                              : make_int4(0, 0, 0, 0);
                   }
 #pragma unroll
                   for (int k = 0; k < kAtOnce; ++k)
@@ -1127,7 +1139,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int64_t i = group_end(p, p.E) * static_cast<int64_t>(p.N) +
                        static_cast<int64_t>(blockIdx.x) * F::kEpi * 32 + ew * 32 + lane;
            i < total; i += step) {
-        if constexpr (OUT == Q8_I8) static_cast<int8_t*>(p.out)[i] = static_cast<int8_t>(p.rq.ozp_i);
+        if constexpr (OUT == Q8_I8)
+          static_cast<int8_t*>(p.out)[i] = static_cast<int8_t>(p.rq.ozp_i);
         else if constexpr (OUT == Q8_F32) static_cast<float*>(p.out)[i] = 0.0f;
         else static_cast<uint16_t*>(p.out)[i] = 0;
       }
@@ -1146,7 +1159,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 template <int OUT, bool PAIR>
-cudaError_t launch_one(const CUtensorMap& map, const CUtensorMap& map_h, const TileParams& p, size_t smem, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap& map, const CUtensorMap& map_h, const TileParams& p,
+                       size_t smem, cudaStream_t s) {
   constexpr int CG = Form<PAIR>::CG;
   auto kernel = tile_gemm_kernel<OUT, PAIR>;
   static DeviceOnce once;

@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(256) pack_tile_weight_kernel(const int8_t* __r
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (k0 + j < K) {
-          const uint32_t b = static_cast<uint8_t>(src[k0 + j]);   // 0x80 ^ b replaces the zero's byte
+          // 0x80 ^ b replaces the zero's byte
+          const uint32_t b = static_cast<uint8_t>(src[k0 + j]);
           v[j / 4] ^= b << (8 * (j % 4));
         }
     }

@@ -306,3 +306,8 @@ def test_a_tile_of_many_adapters():
     p.a[:] = 40
     p.a[np.arange(0, 700, 8)] = np.arange(88)
     _check(p)
+
+
+@pytest.mark.parametrize("M,L", [(20, 20), (40, 2), (100, 3)])
+def test_more_exact_chunks_than_accumulators(M, L):
+    _check(Problem(M, M, 132, 12000, L, 16, zp=-100, bare=0.1))
