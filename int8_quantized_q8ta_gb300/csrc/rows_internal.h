@@ -164,7 +164,7 @@ struct LoraJob {
   int32_t* lists;
   int32_t* ids_out;             // [R] in sorted order, or null
   const int32_t* offsets;       // [L + 1] first sorted row of each adapter (with op.order)
-  int shrink_ctas;              // set by the launcher
+  int shrink_ctas, list_ctas;   // set by the launcher
 };
 cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s);
 

@@ -182,7 +182,9 @@ struct ListShared {
 };
 struct FrontShared {
   float part[kFrontWarps][16][kFrontRows + 1];
-  float sum[16][kFrontRows];      // read by the cluster's other CTAs
+  // the cluster's sums of this CTA's rows: [CTA][row][rank], written by each
+  // (reading the others' took 10,000 cycles where writing to them takes 4,000)
+  float sums[kFrontRows][16 + 1];
   ListShared list;
 };
 
@@ -250,15 +252,15 @@ __device__ __forceinline__ void front_products(const LoraJob& job, const uint16_
 // and 16 ranks, at (t + a) * rank16 + c (with the rows sorted by adapter,
 // either t or a grows from one such pair to the next), both terms f32 of which
 // the MMAs read the 10 leading bits of the fraction.
-__device__ __forceinline__ void store_h(const LoraJob& job, int s, int a, int j, float v) {
+// s is row `local` of tile t.
+__device__ __forceinline__ void store_h(const LoraJob& job, int s, int t, int local, int a, int j,
+                                        float v) {
   if (job.TN == 0) {
     job.h[static_cast<int64_t>(s) * job.rank16 * 16 + j] = v;
     return;
   }
-  const int per = tile_rows(job.op.R, job.tiles), t = s / per;
-  float* at = job.h +
-              ((static_cast<int64_t>(t + a) * job.rank16 + (j >> 4)) * job.TN + (s - t * per)) * 32 +
-              (j & 15);
+  const int64_t block = static_cast<int64_t>(t + a) * job.rank16 + (j >> 4);
+  float* at = job.h + (block * job.TN + local) * 32 + (j & 15);
   const float hi = __uint_as_float(__float_as_uint(v) & 0xffffe000u);
   at[0] = hi;
   // (inf - inf would be NaN)
@@ -288,25 +290,24 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
 #pragma unroll
     for (int j = 0; j < 4; ++j) sh.part[warp][g + (j >> 1) * 8][n * 8 + t * 2 + (j & 1)] = acc[n][j];
   __syncthreads();
+  constexpr int kRows = kFrontRows / CL;   // this CTA's share of the rows
   for (int i = threadIdx.x; i < 16 * kFrontRows; i += kFrontThreads) {
+    const int j = i / kFrontRows, col = i % kFrontRows;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFrontThreads / 32; ++w) v += sh.part[w][i / kFrontRows][i % kFrontRows];
-    sh.sum[i / kFrontRows][i % kFrontRows] = v;
+    for (int w = 0; w < kFrontWarps; ++w) v += sh.part[w][j][col];
+    float* to = &sh.sums[rank * kRows + col % kRows][j];
+    if constexpr (CL > 1) to = cluster.map_shared_rank(to, col / kRows);
+    if (col < count) *to = v;
   }
   if constexpr (CL > 1) cluster.sync(); else __syncthreads();
-  // this CTA's share of the rows, 16 ranks each
-  for (int i0 = threadIdx.x; i0 < 16 * kFrontRows / CL; i0 += kFrontThreads) {
-    const int j = i0 & 15, i = rank * (kFrontRows / CL) + (i0 >> 4);
+  for (int i0 = threadIdx.x; i0 < 16 * kRows; i0 += kFrontThreads) {
+    const int j = i0 & 15, i = rank * kRows + (i0 >> 4);
     if (i < count) {
       float v = 0.0f;
-      if constexpr (CL > 1) {
 #pragma unroll
-        for (int r = 0; r < CL; ++r) v += *cluster.map_shared_rank(&sh.sum[j][i], r);
-      } else {
-        v = sh.sum[j][i];
-      }
-      store_h(job, rows[i], a, c * 16 + j, v * job.s_in * __ldg(job.scaling + a));
+      for (int q = 0; q < CL; ++q) v += sh.sums[q * kRows + (i0 >> 4)][j];
+      store_h(job, rows[i], 0, rows[i], a, c * 16 + j, v * job.s_in * __ldg(job.scaling + a));
     }
   }
   // the sums may be overwritten now
@@ -338,18 +339,18 @@ __device__ int block_compact(ListShared& sh, bool flag, int32_t value, int32_t* 
 
 // A tile's adapters, each once, in the order of their first rows; and, where
 // MMAs take them, zeros in the rows of h's blocks that are other adapters'.
-// kListCtas CTAs share a tile's blocks.
-constexpr int kListCtas = 4;
-
+// job.list_ctas CTAs share a tile's blocks.
 __device__ void list_tile(const LoraJob& job, ListShared& sh, int cta) {
-  const int tile = cta / kListCtas, part = cta % kListCtas;
+  const int tile = cta / job.list_ctas, part = cta % job.list_ctas;
   const int per = tile_rows(job.op.R, job.tiles), row0 = tile * per, n = min(per, job.op.R - row0);
   const int t = threadIdx.x;
   const int a = t < n ? adapter_of(job, row0 + t) : -1;
   if (t < n) sh.rows[t] = a;
   __syncthreads();
   bool first = a >= 0;
-  for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
+  if (job.op.order != nullptr) first = first && (t == 0 || sh.rows[t - 1] != a);
+  else
+    for (int i = 0; i < t && first; ++i) first = sh.rows[i] != a;
   __syncthreads();
   int32_t* list = job.lists + static_cast<int64_t>(tile) * job.list_stride;
   if (part == 0) {
@@ -361,7 +362,7 @@ __device__ void list_tile(const LoraJob& job, ListShared& sh, int cta) {
   const int held = block_compact(sh, first, a, sh.held);
   const int blocks = held * job.rank16, rows = (n + 15) & ~15, lane = t & 31;
   // a warp a block, 4 rows of 128 bytes at a time
-  for (int b = part * kFrontWarps + (t >> 5); b < blocks; b += kListCtas * kFrontWarps) {
+  for (int b = part * kFrontWarps + (t >> 5); b < blocks; b += job.list_ctas * kFrontWarps) {
     const int own = sh.held[b / job.rank16];
     float4* to = reinterpret_cast<float4*>(
         job.h + (static_cast<int64_t>(tile + own) * job.rank16 + b % job.rank16) * job.TN * 32);
@@ -370,8 +371,8 @@ __device__ void list_tile(const LoraJob& job, ListShared& sh, int cta) {
   }
 }
 
-// Blocks: job.shrink_ctas for h, then kListCtas for the list, the rest for the
-// operand.
+// Blocks: job.shrink_ctas for h, then job.list_ctas for the list, the rest for
+// the operand.
 template <bool F16, int CL, bool VEC>
 __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const LoraJob job) {
   __shared__ FrontShared sh;
@@ -393,14 +394,14 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
     return;
   }
   b -= job.shrink_ctas;
-  if (b < kListCtas) {
+  if (b < job.list_ctas) {
     list_tile(job, sh.list, b);
     return;
   }
-  b -= kListCtas;
+  b -= job.list_ctas;
   const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
   const int64_t step =
-      static_cast<int64_t>(gridDim.x - job.shrink_ctas - kListCtas) * kFrontThreads;
+      static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.list_ctas) * kFrontThreads;
   for (int64_t i = t; i < job.op.count_words; i += step) job.op.counts[i] = 0;
   const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
   const uint32_t chunks = job.op.KB * 8;
@@ -417,7 +418,7 @@ constexpr int kShrinkStage = (kShrinkBlocks * 16 + kFrontRows) * 128;
 
 struct ShrinkShared {
   float part[kFrontWarps][16][kFrontRows + 1];
-  float sum[kShrinkBlocks * 16][kFrontRows];   // read by the cluster's other CTAs
+  float sums[kFrontRows][kShrinkBlocks * 16 + 1];   // as in FrontShared
   ListShared list;
   int32_t piece[3];                            // adapter, first row, rows
 };
@@ -473,8 +474,8 @@ __device__ bool find_piece(const LoraJob& job, ShrinkShared& sh, int u) {
   return false;
 }
 
-// Blocks: job.shrink_ctas for h, in clusters, then kListCtas per row tile for
-// its list.
+// Blocks: job.shrink_ctas for h, in clusters, then job.list_ctas per row tile
+// for its list.
 template <bool F16>
 __global__ void __launch_bounds__(kFrontThreads, 2)
     lora_shrink_kernel(const __grid_constant__ LoraJob job) {
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
   pdl_wait();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) >= job.shrink_ctas) {
-    if (static_cast<int>(blockIdx.x) - job.shrink_ctas < job.tiles * kListCtas)
+    if (static_cast<int>(blockIdx.x) - job.shrink_ctas < job.tiles * job.list_ctas)
       list_tile(job, sh.list, blockIdx.x - job.shrink_ctas);
     return;
   }
@@ -491,7 +492,10 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
   const int CL = cluster.num_blocks(), rank = cluster.block_rank();
   if (!find_piece(job, sh, blockIdx.x / CL)) return;
   const int a = sh.piece[0], row0 = sh.piece[1], count = sh.piece[2];
+  const float scale = job.s_in * __ldg(job.scaling + a);
+  const int per = tile_rows(job.op.R, job.tiles), tile0 = row0 / per;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rows = kFrontRows / CL;
   const int KB = job.op.KB, kb0 = rank * KB / CL, steps = (rank + 1) * KB / CL - kb0;
   const int64_t Kp = static_cast<int64_t>(KB) * 64;
   const uint32_t ring0 = smem_u32(ring);
@@ -557,21 +561,26 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
       const int j = i / kFrontRows, col = i % kFrontRows;
       float v = 0.0f;
       for (int k = 0; k < shares; ++k) v += sh.part[k * spread + j / 16][j % 16][col];
-      sh.sum[j][col] = v;
+      if (col < count)
+        *cluster.map_shared_rank(&sh.sums[rank * rows + col % rows][j], col / rows) = v;
     }
     cluster.sync();
-    // this CTA's share of the rows
-    const int ranks = blocks * 16, rows = kFrontRows / CL;
-    for (int i0 = threadIdx.x; i0 < ranks * rows; i0 += kFrontThreads) {
-      const int j = i0 % ranks, i = rank * rows + i0 / ranks;
-      if (i < count) {
+    // this CTA's share of the rows, a rank a thread (code that runs once: few
+    // instructions, for they cost more to fetch than to execute)
+    const int j = threadIdx.x % (kShrinkBlocks * 16);
+    const int i1 = min(count, (rank + 1) * rows);
+    if (j < blocks * 16)
+      for (int i = rank * rows + threadIdx.x / (kShrinkBlocks * 16); i < i1;
+           i += kFrontThreads / (kShrinkBlocks * 16)) {
         float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kFrontCluster; ++q)
-          if (q < CL) v += *cluster.map_shared_rank(&sh.sum[j][i], q);
-        store_h(job, row0 + i, a, c0 * 16 + j, v * job.s_in * __ldg(job.scaling + a));
+        for (int q = 0; q < CL; ++q) v += sh.sums[q * rows + i % rows][j];
+        int t = tile0, local = row0 - tile0 * per + i;
+        while (local >= per) {
+          local -= per;
+          ++t;
+        }
+        store_h(job, row0 + i, t, local, a, c0 * 16 + j, v * scale);
       }
-    }
     cluster.sync();   // the sums may be overwritten now, or this CTA leave
   }
 }
@@ -683,12 +692,16 @@ cudaError_t launch_sorted(LoraJob job, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const int units = job.op.R / kFrontRows + std::min(job.L, job.op.R);
-  // K is cut over a cluster while that leaves every SM no more than two CTAs
+  // K is cut over a cluster while all CTAs are resident at once, two an SM
+  // (the lists' behind those for h cost their whole time again), and a tile's
+  // list is shared by those that are left
+  const int slots = 2 * device_sm_count();
   int cl = kFrontCluster;
-  while (cl > 1 && units * cl > 2 * device_sm_count()) cl /= 2;
+  while (cl > 1 && units * cl + job.tiles > slots) cl /= 2;
   job.shrink_ctas = units * cl;
+  job.list_ctas = std::max(1, std::min(4, (slots - job.shrink_ctas) / job.tiles));
   return launch_pdl_cluster(lora_shrink_kernel<F16>,
-                            static_cast<int>(round_up(job.shrink_ctas + job.tiles * kListCtas, cl)),
+                            static_cast<int>(round_up(job.shrink_ctas + job.tiles * job.list_ctas, cl)),
                             kFrontThreads, kShrinkStages * kShrinkStage, cl, s, job);
 }
 
@@ -700,9 +713,10 @@ cudaError_t launch_lora_front(LoraJob job, bool f16, cudaStream_t s) {
   // K is cut over 8 CTAs while the units alone would leave SMs without one
   const int cl = job.op.R * job.rank16 <= device_sm_count() ? kFrontCluster : 1;
   job.shrink_ctas = job.op.R * job.rank16 * cl;
+  job.list_ctas = 4;
   const int copy = blocks_for(
       std::max<int64_t>(static_cast<int64_t>(job.op.R) * job.op.KB * 8, job.op.count_words));
-  const int grid = static_cast<int>(round_up(job.shrink_ctas + kListCtas + copy, cl));
+  const int grid = static_cast<int>(round_up(job.shrink_ctas + job.list_ctas + copy, cl));
   const auto go = [&](auto half, auto vec) {
     constexpr bool F16 = decltype(half)::value, VEC = decltype(vec)::value;
     return cl == 1 ? launch_pdl(lora_front_kernel<F16, 1, VEC>, grid, kFrontThreads, 0, s, job)
