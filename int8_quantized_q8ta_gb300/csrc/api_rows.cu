@@ -157,9 +157,14 @@ q8_status q8_expert_dispatch(const void* x, q8_dtype dtype, int64_t T, int64_t H
   if (T > 0 && (!x || !xs)) return Q8_ERR_NULL;
   const int64_t b = q8::dtype_bytes(dtype);
   if (!aligned(x, b) || !aligned(xs, b)) return Q8_ERR_ALIGN;
-  st = q8_expert_sort(expert_ids, T, k, E, order, position, offsets, stream);
-  if (st != Q8_OK) return st;
-  return q8_expert_gather(x, dtype, T, k, H, E, position, offsets, xs, stream);
+  if (T == 0) return q8_expert_sort(expert_ids, T, k, E, order, position, offsets, stream);
+  if (!expert_ids || !order || !position || !offsets) return Q8_ERR_NULL;
+  if (!aligned(expert_ids, 4) || !aligned(order, 4) || !aligned(position, 4) ||
+      !aligned(offsets, 4))
+    return Q8_ERR_ALIGN;
+  return cuda_status(q8::launch_expert_dispatch(x, T, static_cast<int>(k), H * b, expert_ids,
+                                                static_cast<int>(E), order, position, offsets, xs,
+                                                cs(stream)));
 }
 
 q8_status q8_expert_gather_backward(const void* dxs, q8_dtype dtype, int64_t T, int64_t k,

@@ -50,7 +50,7 @@ namespace {
 // shared memory; nothing but the ids is read from global memory.  A warp's
 // slots of one expert are found by one ballot for each bit of the id (a match
 // instruction takes as long as there are different ids).  Latency bounds it:
-// 8 slots 3.0 us, 1024 4.2, 8192 5.0, 32768 6.6, and from there on the 8 CTAs'
+// 8 slots 2.6 us, 1024 4.2, 8192 5.1, 32768 6.6, and from there on the 8 CTAs'
 // own work, 262144 slots 26 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortMaxWarps = 32;
@@ -66,13 +66,13 @@ __device__ __forceinline__ void sort_keys(const int32_t* ids, int64_t f, int64_t
     key[i] = f + i * 32 >= hi ? -1 : key[i] >= 0 && key[i] < E ? key[i] : E;
 }
 
-__global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __restrict__ ids,
-                                                           int64_t R, int E,
-                                                           int32_t* __restrict__ order,
-                                                           int32_t* __restrict__ position,
-                                                           int32_t* __restrict__ offsets,
-                                                           bool keep_dropped) {
-  extern __shared__ int32_t sm[];
+// The sort by this cluster.  write: into global memory; rows, if not null, gets
+// each slot's position too.  Returns the kept slots.
+__device__ __forceinline__ int sort_slots(const int32_t* __restrict__ ids, int64_t R, int E,
+                                          int32_t* __restrict__ order,
+                                          int32_t* __restrict__ position,
+                                          int32_t* __restrict__ offsets, bool keep_dropped,
+                                          bool write, int32_t* sm, int32_t* rows) {
   const int G = E + 1;                        // groups: the experts and the dropped slots
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* hist = sm;                         // [warps][G]
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __rest
     const int32_t excl = add + incl - all;
     if (g < G) {
       start[g] = excl + earlier;
-      if (rank == 0) offsets[g] = excl;       // offsets[E]: the kept slots
+      if (rank == 0 && write) offsets[g] = excl;   // offsets[E]: the kept slots
     }
     __syncthreads();
   }
@@ -170,11 +170,26 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __rest
       __syncwarp();
       if (key[i] >= 0) {
         const int64_t f = f0 + i * 32 + lane;
-        order[row] = key[i] < E || keep_dropped ? static_cast<int32_t>(f) : -1;
-        position[f] = key[i] < E ? row : -1;
+        const int32_t at = key[i] < E ? row : -1;
+        if (write) {
+          order[row] = key[i] < E || keep_dropped ? static_cast<int32_t>(f) : -1;
+          position[f] = at;
+        }
+        if (rows != nullptr) rows[f] = at;
       }
     }
   }
+  return start[E];
+}
+
+__global__ void __launch_bounds__(1024) expert_sort_kernel(const int32_t* __restrict__ ids,
+                                                           int64_t R, int E,
+                                                           int32_t* __restrict__ order,
+                                                           int32_t* __restrict__ position,
+                                                           int32_t* __restrict__ offsets,
+                                                           bool keep_dropped) {
+  extern __shared__ int32_t sm[];
+  sort_slots(ids, R, E, order, position, offsets, keep_dropped, true, sm, nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -209,13 +224,12 @@ union Pack {
   __device__ Pack() {}
 };
 
-// Zeros in the rows from offsets[E] on (dropped slots), by whole warps.
+// Zeros in the rows from `kept` on (dropped slots), by whole warps.
 template <int VB>
 __device__ __forceinline__ void zero_tail(typename VecOf<VB>::type* rows, int64_t V, int64_t R,
-                                          const int32_t* offsets, int E, int64_t warp_id,
-                                          int64_t num_warps, int lane) {
+                                          int kept, int64_t warp_id, int64_t num_warps, int lane) {
   typename VecOf<VB>::type zero{};
-  for (int64_t s = max(0, __ldg(offsets + E)) + warp_id; s < R; s += num_warps)
+  for (int64_t s = max(0, kept) + warp_id; s < R; s += num_warps)
     for (int64_t c = lane; c < V; c += 32) rows[s * V + c] = zero;
 }
 
@@ -223,12 +237,9 @@ __device__ __forceinline__ void zero_tail(typename VecOf<VB>::type* rows, int64_
 // to each of the token's kept rows (k writes to one read: slots in sorted order
 // would read every row k times).
 template <int VB, int U>
-__global__ void __launch_bounds__(256) expert_gather_kernel(
-    const typename VecOf<VB>::type* __restrict__ x, int64_t T, int k, int64_t V,
-    const int32_t* __restrict__ position, const int32_t* __restrict__ offsets, int E,
-    typename VecOf<VB>::type* __restrict__ xs) {
-  pdl_wait();
-  pdl_launch_dependents();
+__device__ __forceinline__ void gather_rows(const typename VecOf<VB>::type* __restrict__ x,
+                                            int64_t T, int k, int64_t V, const int32_t* position,
+                                            int kept, typename VecOf<VB>::type* __restrict__ xs) {
   const int lane = threadIdx.x & 31;
   const int64_t warp_id = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t num_warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
@@ -240,14 +251,42 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(
     for (int i = 0; i < U; ++i)
       if (c0 + i * 32 < V) v[i] = __ldg(x + t * V + c0 + i * 32);
     for (int j = 0; j < k; ++j) {
-      const int64_t s = __ldg(position + t * k + j);
+      const int64_t s = position[t * k + j];
       if (s < 0 || s >= T * k) continue;
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (c0 + i * 32 < V) xs[s * V + c0 + i * 32] = v[i];
     }
   }
-  zero_tail<VB>(xs, V, T * k, offsets, E, warp_id, num_warps, lane);
+  zero_tail<VB>(xs, V, T * k, kept, warp_id, num_warps, lane);
+}
+
+template <int VB, int U>
+__global__ void __launch_bounds__(256) expert_gather_kernel(
+    const typename VecOf<VB>::type* __restrict__ x, int64_t T, int k, int64_t V,
+    const int32_t* __restrict__ position, const int32_t* __restrict__ offsets, int E,
+    typename VecOf<VB>::type* __restrict__ xs) {
+  pdl_wait();
+  pdl_launch_dependents();
+  gather_rows<VB, U>(x, T, k, V, position, __ldg(offsets + E), xs);
+}
+
+// Both for few slots: every CTA sorts them all for itself and moves its share
+// of the rows, one launch instead of two in a row (8 slots of 4096 bytes 3.9
+// instead of 4.7 us).
+constexpr int kDispatchSlots = 256;
+
+template <int VB, int U>
+__global__ void __launch_bounds__(256) expert_dispatch_kernel(
+    const typename VecOf<VB>::type* __restrict__ x, const int32_t* __restrict__ ids, int64_t T,
+    int k, int64_t V, int E, int32_t* __restrict__ order, int32_t* __restrict__ position,
+    int32_t* __restrict__ offsets, typename VecOf<VB>::type* __restrict__ xs) {
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t rows[kDispatchSlots];
+  const int kept = sort_slots(ids, T * k, E, order, position, offsets, false, blockIdx.x == 0, sm,
+                              rows);
+  __syncthreads();
+  gather_rows<VB, U>(x, T, k, V, rows, kept, xs);
 }
 
 // spread: a warp takes U*32 vectors of one token's sum, S slots' loads in
@@ -362,7 +401,7 @@ __global__ void __launch_bounds__(256) expert_combine_bwd_kernel(
     for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
     if (lane == 0) dw[f] = dot;
   }
-  zero_tail<VB>(dz, V, R, offsets, E, warp_id, num_warps, lane);
+  zero_tail<VB>(dz, V, R, __ldg(offsets + E), warp_id, num_warps, lane);
 }
 
 // The widest vector that divides the row and every base address.
@@ -405,25 +444,57 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* or
                             position, offsets, keep_dropped);
 }
 
+namespace {
+
+// fn(vector width) for the widest vector of rows and bases.
+template <typename F>
+cudaError_t with_width(int vb, F&& fn) {
+  switch (vb) {
+    case 16: return fn(std::integral_constant<int, 16>());
+    case 8: return fn(std::integral_constant<int, 8>());
+    case 4: return fn(std::integral_constant<int, 4>());
+    case 2: return fn(std::integral_constant<int, 2>());
+    default: return fn(std::integral_constant<int, 1>());
+  }
+}
+
+constexpr int kGatherU = 4;
+int gather_grid(int64_t T, int64_t vecs) {
+  return warp_grid(T * ((vecs + kGatherU * 32 - 1) / (kGatherU * 32)));
+}
+
+}  // namespace
+
 cudaError_t launch_expert_gather(const void* x, int64_t T, int k, int64_t row_bytes,
                                  const int32_t* position, const int32_t* offsets, int E, void* xs,
                                  cudaStream_t s) {
-  auto go = [&](auto tag) {
-    constexpr int VB = decltype(tag)::value;
+  return with_width(vec_bytes(row_bytes, {x, xs}), [&](auto width) {
+    constexpr int VB = decltype(width)::value;
     using V = typename VecOf<VB>::type;
-    constexpr int U = 4;
     const int64_t vecs = row_bytes / VB;
-    return launch_pdl(expert_gather_kernel<VB, U>, warp_grid(T * ((vecs + U * 32 - 1) / (U * 32))),
-                      256, 0, s, static_cast<const V*>(x), T, k, vecs, position, offsets, E,
+    return launch_pdl(expert_gather_kernel<VB, kGatherU>, gather_grid(T, vecs), 256, 0, s,
+                      static_cast<const V*>(x), T, k, vecs, position, offsets, E,
                       static_cast<V*>(xs));
-  };
-  switch (vec_bytes(row_bytes, {x, xs})) {
-    case 16: return go(std::integral_constant<int, 16>());
-    case 8: return go(std::integral_constant<int, 8>());
-    case 4: return go(std::integral_constant<int, 4>());
-    case 2: return go(std::integral_constant<int, 2>());
-    default: return go(std::integral_constant<int, 1>());
+  });
+}
+
+cudaError_t launch_expert_dispatch(const void* x, int64_t T, int k, int64_t row_bytes,
+                                   const int32_t* ids, int E, int32_t* order, int32_t* position,
+                                   int32_t* offsets, void* xs, cudaStream_t s) {
+  if (T * k > kDispatchSlots) {
+    cudaError_t e = launch_expert_sort(ids, T * k, E, order, position, offsets, s);
+    if (e != cudaSuccess) return e;
+    return launch_expert_gather(x, T, k, row_bytes, position, offsets, E, xs, s);
   }
+  return with_width(vec_bytes(row_bytes, {x, xs}), [&](auto width) {
+    constexpr int VB = decltype(width)::value;
+    using V = typename VecOf<VB>::type;
+    const int64_t vecs = row_bytes / VB;
+    const int grid = std::min(gather_grid(T, vecs), device_sm_count());
+    return launch_pdl_cluster(expert_dispatch_kernel<VB, kGatherU>, grid, 256,
+                              expert_sort_smem(256, E), 1, s, static_cast<const V*>(x), ids, T, k,
+                              vecs, E, order, position, offsets, static_cast<V*>(xs));
+  });
 }
 
 namespace {

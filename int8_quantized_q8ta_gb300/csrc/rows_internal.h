@@ -69,6 +69,9 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* or
 cudaError_t launch_expert_gather(const void* x, int64_t T, int k, int64_t row_bytes,
                                  const int32_t* position, const int32_t* offsets, int E, void* xs,
                                  cudaStream_t s);
+cudaError_t launch_expert_dispatch(const void* x, int64_t T, int k, int64_t row_bytes,
+                                   const int32_t* ids, int E, int32_t* order, int32_t* position,
+                                   int32_t* offsets, void* xs, cudaStream_t s);
 // y[t] = sum_j w[t,j] * z[position[t,j]]; w null: ones.
 cudaError_t launch_expert_spread(const void* z, q8_dtype dt, const float* w, int64_t T, int k,
                                  int64_t H, const int32_t* position, void* y, cudaStream_t s);

@@ -82,13 +82,13 @@ constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
 // 8 KB of weights for 384 cycles of MMAs, where one CTA alone needs 32 KB.
 // 8192 rows of 16 experts x 4096 x 4096: 180 us, 44 bytes a cycle and SM, 69%
 // of the tensor pipe's cycles; 2048 rows x 11008 x 4096 with 8 adapters of rank
-// 64 141 us, 118 without.
+// 64 140 us, 118 without.
 //   Narrow (up to 64 rows): one CTA; two k-blocks a stage and twice the
 // converting warps, since the weights' way through them is what such tiles
 // wait for once memory is busy.  128 rows of 56 experts x 2048 x 2048: 37.9 us
 // with the operand before it, 35.0 at the copy rate; 64 rows x 11008 x 4096 20
-// us, 26 with 32 adapters of rank 16; one row x 4096 x 4096 with its adapter
-// 10.5 to 11.3 us.
+// us, 24.3 with 32 adapters of rank 16; one row x 4096 x 4096 with its adapter
+// 10.5 us.
 template <bool PAIR>
 struct Form {
   static constexpr int CG = PAIR ? 2 : 1;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) tile_operand_kernel(const OperandJob job)
 // and a unit is up to 32 rows of one adapter and all its ranks, 64 at a time.
 // A's and the rows' k-blocks go through a ring in shared memory, their 16-byte
 // chunks swizzled so that eight lanes' loads meet no bank twice (2048 rows x
-// 4096, 8 adapters of rank 64, 21 us from cold memory, 31 when each 16 ranks
+// 4096, 8 adapters of rank 64, 20 us from cold memory, 31 when each 16 ranks
 // were loaded straight to registers).
 // ---------------------------------------------------------------------------
 constexpr int kFrontThreads = 256;
