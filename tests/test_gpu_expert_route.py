@@ -167,6 +167,12 @@ def test_combine_and_gradients(T, k, E, H, drop, dtype):
     assert torch.all(dw.cpu()[~kept] == 0)
 
 
+@pytest.mark.parametrize("T,k", [(32, 8), (257, 1), (20, 8)])
+def test_dispatch_around_one_launch_and_two(T, k):
+    test_gather_copies_rows(T, k, 1024, 40, 0.1, torch.float16)
+    test_gather_copies_rows(T, k, 9, 4100, 0.0, torch.int8)
+
+
 @pytest.mark.parametrize("k", [31, 33, 70])
 def test_more_slots_than_a_warp_has_lanes(k):
     test_combine_and_gradients(6, k, 80, 40, 0.2, torch.float32)
