@@ -525,6 +525,9 @@ cudaError_t launch_expert_spread(const void* z, q8_dtype dt, const float* w, int
     using T_ = decltype(elem);
     constexpr int VB = decltype(vb)::value;
     using V = typename VecOf<VB>::type;
+    // (2048 x 4 dispatch and its gradient, 4096 x 8 combine and its: U 2, S 4
+    // 34.8 and 137.6 us; 1, 4 39.0 and 147; 4, 2 36.7 and 139.8; 2, 8 37.8 and
+    // 138.4; 4, 4 35.7 and 136.8)
     constexpr int U = VB == 16 ? 2 : 4, S = 4;
     const int64_t vecs = row_bytes / VB;
     return launch_pdl(expert_spread_kernel<T_, VB, U, S>,
