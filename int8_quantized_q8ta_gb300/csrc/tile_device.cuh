@@ -62,6 +62,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// The cluster's barrier in two halves, counted by threads: one CTA's shared
+// memory may be reached from another once both have arrived (before that it
+// need not have started).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // The larger of two, NaN where either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

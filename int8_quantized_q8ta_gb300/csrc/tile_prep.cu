@@ -267,7 +267,9 @@ __device__ __forceinline__ void store_h(const LoraJob& job, int s, int t, int lo
   at[16] = (__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u ? 0.0f : __fsub_rn(v, hi);
 }
 
-// 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.
+// 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.  Every
+// CTA of a cluster has arrived at its barrier once more than it has waited,
+// here and on return: the others run, and their sums may be overwritten.
 template <bool F16, int CL, bool VEC>
 __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_group& cluster, int a,
                            int c, const int32_t* rows, int count) {
@@ -290,6 +292,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
 #pragma unroll
     for (int j = 0; j < 4; ++j) sh.part[warp][g + (j >> 1) * 8][n * 8 + t * 2 + (j & 1)] = acc[n][j];
   __syncthreads();
+  if constexpr (CL > 1) cluster_wait();
   constexpr int kRows = kFrontRows / CL;   // this CTA's share of the rows
   for (int i = threadIdx.x; i < 16 * kFrontRows; i += kFrontThreads) {
     const int j = i / kFrontRows, col = i % kFrontRows;
@@ -310,8 +313,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
       store_h(job, rows[i], 0, rows[i], a, c * 16 + j, v * job.s_in * __ldg(job.scaling + a));
     }
   }
-  // the sums may be overwritten now
-  if constexpr (CL > 1) cluster.sync(); else __syncthreads();
+  if constexpr (CL > 1) cluster_arrive(); else __syncthreads();
 }
 
 __device__ __forceinline__ int adapter_of(const LoraJob& job, int s) {
@@ -388,9 +390,11 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
     const int mine = static_cast<int>(threadIdx.x) < R ? adapter_of(job, threadIdx.x) : -1;
     const bool same = a >= 0 && mine == a;
     if (__syncthreads_or(same && static_cast<int>(threadIdx.x) < w) || a < 0) return;
+    if constexpr (CL > 1) cluster_arrive();
     const int n = block_compact(sh.list, same, threadIdx.x, sh.list.rows);
     for (int i = 0; i < n; i += kFrontRows)
       front_rows<F16, CL, VEC>(job, sh, cluster, a, c, sh.list.rows + i, min(kFrontRows, n - i));
+    if constexpr (CL > 1) cluster_wait();
     return;
   }
   b -= job.shrink_ctas;
@@ -490,7 +494,8 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
   }
   cg::cluster_group cluster = cg::this_cluster();
   const int CL = cluster.num_blocks(), rank = cluster.block_rank();
-  if (!find_piece(job, sh, blockIdx.x / CL)) return;
+  if (!find_piece(job, sh, blockIdx.x / CL)) return;   // (all of a cluster or none)
+  cluster_arrive();
   const int a = sh.piece[0], row0 = sh.piece[1], count = sh.piece[2];
   const float scale = job.s_in * __ldg(job.scaling + a);
   const int per = tile_rows(job.op.R, job.tiles), tile0 = row0 / per;
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
       for (int j = 0; j < 4; ++j)
         sh.part[warp][g + (j >> 1) * 8][n * 8 + t * 2 + (j & 1)] = acc[n][j];
     __syncthreads();
+    cluster_wait();   // the others run, and have read the sums of the ranks before
     for (int i = threadIdx.x; i < blocks * 16 * kFrontRows; i += kFrontThreads) {
       const int j = i / kFrontRows, col = i % kFrontRows;
       float v = 0.0f;
@@ -581,8 +587,9 @@ __global__ void __launch_bounds__(kFrontThreads, 2)
         }
         store_h(job, row0 + i, t, local, a, c0 * 16 + j, v * scale);
       }
-    cluster.sync();   // the sums may be overwritten now, or this CTA leave
+    cluster_arrive();
   }
+  cluster_wait();
 }
 
 // Adapter matrices, padded with zeros: A -> [L][16 rank16][64 KB], and

@@ -311,3 +311,21 @@ def test_a_tile_of_many_adapters():
 @pytest.mark.parametrize("M,L", [(20, 20), (40, 2), (100, 3)])
 def test_more_exact_chunks_than_accumulators(M, L):
     _check(Problem(M, M, 132, 12000, L, 16, zp=-100, bare=0.1))
+
+
+# Clusters of 8 CTAs that share a K of one or two blocks, so that most have
+# nothing to multiply and reach the exchange of their sums at once: one row tile
+# (rows x blocks of 16 ranks up to the SMs) and rows sorted by adapter, one and
+# several passes of 64 ranks.  The same bits every time.
+@pytest.mark.parametrize("M,L,r", [(1, 1, 16), (2, 2, 256), (9, 3, 16), (64, 1, 24), (70, 2, 16),
+                                   (70, 30, 64), (200, 3, 200), (500, 9, 8)])
+@pytest.mark.parametrize("K", [20, 64, 128])
+def test_clusters_with_little_to_multiply(M, L, r, K):
+    p = Problem(M + K, M, 132, K, L, r, zp=3, bare=0.1)
+    _check(p)
+    first = p.run()
+    packed = q8.pack_tile_weight(T(p.w))
+    lora = q8.pack_lora(p.A.to(DEV), p.B.to(DEV), p.s.to(DEV))
+    args = (T(p.x), p.s_in, p.zp, packed, T(p.ws), T(p.b), lora, T(p.a), 0.05, 3)
+    for got in [q8.linear_lora(*args, out_dtype=torch.float32) for _ in range(50)]:
+        assert torch.equal(got, first)
