@@ -887,16 +887,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int stages = (sg->kb1 - sg->kb0 + KD - 1) / KD;
       const int nb = sg->nb * CG + rank;
       if (first_seg) {
-        // for the first part even before the kernel before this one is done:
-        // whatever its ids then are, a prefetch changes no result
-        if (!PAIR && p.by_row && sg->kb1 == p.KB) fetch_adapters(sg, mine, nb);
+        // for the first part even before the kernel before this one is done,
+        // where the ids are the caller's; sorted ones are that kernel's, and read
+        // now they would lie in L1 as they were before it
+        if (!PAIR && p.by_row && p.out_rows == nullptr && sg->kb1 == p.KB)
+          fetch_adapters(sg, mine, nb);
         pdl_wait();
       }
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
       const bool by_row = !PAIR && p.by_row && sg->kb1 == p.KB;
       if (by_row) {
-        if (!first_seg) fetch_adapters(sg, mine, nb);
+        if (!first_seg || p.out_rows != nullptr) fetch_adapters(sg, mine, nb);
         for (int j = 0; j < mine; j += 8) {
           // (rows past the tile's end repeat its last)
           const int my_s = sg->row0 + min(col0 + j + (lane & 7), sg->rows - 1);

@@ -329,3 +329,33 @@ def test_clusters_with_little_to_multiply(M, L, r, K):
     args = (T(p.x), p.s_in, p.zp, packed, T(p.ws), T(p.b), lora, T(p.a), 0.05, 3)
     for got in [q8.linear_lora(*args, out_dtype=torch.float32) for _ in range(50)]:
         assert torch.equal(got, first)
+
+
+# Rows sorted by adapter, their terms row by row: the workspace holds the ids
+# of the call before, all of them adapters.  320 blocks, more than CTAs, so that
+# a CTA's first part holds a block's end.
+def test_ids_of_the_call_before_do_not_matter():
+    p = Problem(40, 300, 8192, 128, 100, 16, zp=2)
+    packed = q8.pack_tile_weight(T(p.w))
+    lora = q8.pack_lora(p.A.to(DEV), p.B.to(DEV), p.s.to(DEV))
+    x, ws, b = T(p.x), T(p.ws), T(p.b)
+    rng = np.random.default_rng(41)
+    ids = [T(rng.permutation(p.a)) for _ in range(2)] + [T(((p.a + 50) % 100).astype(np.int32))]
+    n = q8.lib().q8_linear_lora_workspace_bytes(p.M, p.K, p.L, p.r)
+    space = torch.empty(n, dtype=torch.uint8, device=DEV)
+
+    def call(a, space=None):
+        return q8.linear_lora(x, p.s_in, p.zp, packed, ws, b, lora, a, 0.05, 3,
+                              out_dtype=torch.float32, workspace=space)
+    want = []
+    for a in ids:
+        want.append(call(a, torch.zeros(n, dtype=torch.uint8, device=DEV)))
+        torch.cuda.synchronize()
+    for _ in range(12):
+        got = [call(a, space) for a in ids]
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+    p.a = ids[2].cpu().numpy()
+    v, bound = p.exact()
+    u = UNIT[torch.float32]
+    assert np.all(np.abs(got[2].double().cpu().numpy() - v) <= bound * (1 + u) + u * np.abs(v))
