@@ -992,6 +992,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0)
           before = atomic_add_acq_rel(p.counts + (first * CG + rank) * kTileEpiWarps + ew, 1);
         before = __shfl_sync(0xffffffffu, before, 0);
+        __syncwarp();   // lane 0's acquire holds for the others' reads (a shuffle orders none)
         last = before == end - first;
         if (last) {
 #pragma unroll 1

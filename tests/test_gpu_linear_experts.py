@@ -271,3 +271,27 @@ def test_blocks_cut_between_ctas(M, N, K):
         got = q8.linear_experts(x, 0.01, -7, packed, ws, None, route, 1.0, 0,
                                 out_dtype=torch.float32)
         assert torch.equal(got, v + 0.0)
+
+
+# Joined parts are those of this call: problems with other sums in turn on one
+# workspace, so that a part read early would be one of the call before.  Units
+# shared by several CTAs, and runs that end one unit and begin the next, in both
+# forms.
+@pytest.mark.parametrize("M,N,K", [(3, 512, 8192), (20, 25600, 4096), (100, 2048, 4096),
+                                   (100, 25600, 4096)])
+def test_parts_of_the_call_before_do_not_matter(M, N, K):
+    g = torch.Generator(device=DEV).manual_seed(M + 1)
+    x = [torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int8)
+         for _ in range(2)]
+    w = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    ones = torch.ones(1, N, device=DEV)
+    route = q8.expert_sort(torch.zeros(M, 1, dtype=torch.int32, device=DEV), 1)
+    packed = q8.pack_tile_weight(w)
+    n = q8.lib().q8_linear_experts_workspace_bytes(M, K, 1)
+    space = torch.empty(n, dtype=torch.uint8, device=DEV)
+    want = [(a.double() @ w.double().T).float() for a in x]
+    for _ in range(20):
+        got = [q8.linear_experts(a, 1.0, 0, packed, ones, None, route, 1.0, 0,
+                                 out_dtype=torch.float32, workspace=space) for a in x]
+        for v, ref in zip(got, want):
+            assert torch.equal(v, ref)
