@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "row_split.h"
 #include "rows_internal.h"
 #include "tile_device.cuh"
 
@@ -403,16 +404,15 @@ __global__ void __launch_bounds__(kFrontThreads, 2) lora_front_kernel(const Lora
     return;
   }
   b -= job.list_ctas;
-  const int64_t t = static_cast<int64_t>(b) * kFrontThreads + threadIdx.x;
-  const int64_t step =
-      static_cast<int64_t>(gridDim.x - job.shrink_ctas - job.list_ctas) * kFrontThreads;
+  const uint32_t t = b * kFrontThreads + threadIdx.x;   // (some thousand CTAs at most)
+  const uint32_t step = (gridDim.x - job.shrink_ctas - job.list_ctas) * kFrontThreads;
   for (int64_t i = t; i < job.op.count_words; i += step) job.op.counts[i] = 0;
   const __half2 minus = __half2half2(__int2half_rn(1152 + job.op.zp));
   const uint32_t chunks = job.op.KB * 8;
-  for (int64_t i = t; i < static_cast<int64_t>(R) * chunks; i += step) {
-    const uint32_t s = static_cast<uint32_t>(i) / chunks, c = static_cast<uint32_t>(i) - s * chunks;
-    job.op.dst[(static_cast<int64_t>(c >> 3) * R + s) * 8 + (c & 7)] =
-        operand_f16(operand_load<VEC>(job.op.x + s * job.op.K, c, job.op.K), minus);
+  for (RowItems at(t, step, chunks); at.row < R; at.next()) {
+    const uint32_t c = at.item;
+    job.op.dst[(static_cast<int64_t>(c >> 3) * R + at.row) * 8 + (c & 7)] =
+        operand_f16(operand_load<VEC>(job.op.x + at.row * job.op.K, c, job.op.K), minus);
   }
 }
 
