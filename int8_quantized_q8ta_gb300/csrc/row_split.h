@@ -32,4 +32,10 @@ struct RowItems {
   }
 };
 
+// part * n / parts, 0 <= part <= parts <= 2^15: where part `part` of n steps cut
+// into equal `parts` begins.  No product passes n or parts^2.
+Q8_HOST_DEVICE int part_start(int part, int n, int parts) {
+  return part * (n / parts) + part * (n % parts) / parts;
+}
+
 }  // namespace q8

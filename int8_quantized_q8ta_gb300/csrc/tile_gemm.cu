@@ -45,6 +45,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "row_split.h"
 #include "rows_internal.h"
 #include "tile_device.cuh"
 
@@ -200,8 +201,8 @@ struct Walk {
     if (share > 0) {
       unit = base + me / share;
       const int part = me % share;
-      kb = part * p.KB / share;
-      left = me / share < rest ? (part + 1) * p.KB / share - kb : 0;
+      kb = part_start(part, p.KB, share);
+      left = me / share < rest ? part_start(part + 1, p.KB, share) - kb : 0;
       if (left > 0) locate(unit);
       return;
     }

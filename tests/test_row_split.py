@@ -27,6 +27,10 @@ int main() {
       q8::RowItems at(static_cast<uint32_t>(a), static_cast<uint32_t>(b), static_cast<uint32_t>(c));
       for (long long i = 0; i < d; ++i) at.next();
       std::printf("%" PRId64 " %u\n", at.row, at.item);
+    } else if (std::strcmp(what, "part") == 0) { // part, n, parts
+      if (std::scanf("%lld %lld %lld", &a, &b, &c) != 3) return 1;
+      std::printf("%d\n", q8::part_start(static_cast<int>(a), static_cast<int>(b),
+                                         static_cast<int>(c)));
     }
   }
   return 0;
@@ -63,3 +67,14 @@ def test_items_of_rows(prog):
     got = prog([f"items {f} {s} {w} {n}" for f, s, w, n in cases])
     for (f, s, w, n), pair in zip(cases, got, strict=True):
         assert pair == divmod(f + n * s, w), (f, s, w, n)
+
+
+def test_parts_of_a_line(prog):
+    """A unit's k-blocks, up to 2^30 inputs' worth, shared by up to all SMs: the
+    product of the two passes 32 bits."""
+    cases = [(part, n, parts) for n in (1, 4, 63, 64, 1000, 2 ** 24 - 1, 2 ** 24, 2 ** 31 - 1)
+             for parts in (1, 2, 3, 38, 75, 151, 152, 1000) for part in range(0, parts + 1, 1)]
+    assert max(part * n for part, n, _ in cases) > 2 ** 31
+    got = prog([f"part {part} {n} {parts}" for part, n, parts in cases])
+    for (part, n, parts), (at,) in zip(cases, got, strict=True):
+        assert at == part * n // parts, (part, n, parts)
