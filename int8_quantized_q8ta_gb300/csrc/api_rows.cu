@@ -68,9 +68,12 @@ TilePlan plan_tiles(int64_t R, int64_t K, int64_t E, int64_t max_rows = q8::kMax
   return t;
 }
 
+// Row tiles that R rows in E groups need at most.
+int64_t max_tiles(int64_t R, int64_t E, const TilePlan& t) { return R / t.TN + std::min(E, R); }
+
 // The k-blocks of all units are numbered in 32 bits.
 bool units_ok(int64_t R, int64_t E, int64_t N, int64_t K, const TilePlan& t) {
-  const int64_t tiles = R / t.TN + std::min(E, R), blocks = (N + 127) / 128, kbs = (K + 63) / 64;
+  const int64_t tiles = max_tiles(R, E, t), blocks = (N + 127) / 128, kbs = (K + 63) / 64;
   return mul_ok(blocks, kbs) && mul_ok(tiles, blocks * kbs) && tiles * blocks * kbs <= INT32_MAX;
 }
 
@@ -282,6 +285,7 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
   p.E = static_cast<int>(E);
   p.offsets = offsets;
   p.TN = plan.TN;
+  p.max_tiles = static_cast<int>(max_tiles(R, E, plan));
   p.grid = plan.grid;
   p.min_run = 4;
   p.w = static_cast<const uint8_t*>(packed_weight);
@@ -383,6 +387,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   p.KB = static_cast<int>((K + 63) / 64);
   p.E = 1;
   p.TN = sp.plan.TN;
+  p.max_tiles = static_cast<int>(max_tiles(M, 1, sp.plan));
   p.grid = sp.plan.grid;
   p.min_run = 4;
   p.w = static_cast<const uint8_t*>(packed_weight);

@@ -99,6 +99,7 @@ struct TileParams {
   int E;                    // groups
   const int32_t* offsets;   // [E + 1] group bounds on the device, or null: one group of R rows
   int TN;                   // rows of a tile at most (a multiple of 16)
+  int max_tiles;            // row tiles of all groups at most: R / TN + min(E, R)
   int stages;               // ring stages (set by the launcher)
   int grid, min_run;        // CTAs; k-blocks a CTA's run holds at least
   const uint8_t* w;         // packed weights (see launch_pack_tile_weight)

@@ -476,7 +476,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   pdl_launch_dependents();
   if (prefix != nullptr) {
-    // row tiles before each group, by one warp
+    // row tiles before each group, by one warp.  Groups of a sort's offsets are
+    // disjoint and have max_tiles at most; of offsets that overlap, the tiles
+    // from there on are left out, so that the units' k-blocks fit 32 bits.  (A
+    // group has R / TN + 1 at most, R / 192 or some 6,000: 32 of them fit too.)
     pdl_wait();
     if (warp == 0) {
       int before = 0;
@@ -490,8 +493,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int v = __shfl_up_sync(0xffffffffu, incl, d);
           if (lane >= d) incl += v;
         }
-        if (e < p.E) prefix[e] = before + incl - n;
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        if (e < p.E) prefix[e] = min(before + incl - n, p.max_tiles);
+        before = min(before + __shfl_sync(0xffffffffu, incl, 31), p.max_tiles);
       }
       if (lane == 0) sh.tiles = before;
     }

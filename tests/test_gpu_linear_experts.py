@@ -295,3 +295,32 @@ def test_parts_of_the_call_before_do_not_matter(M, N, K):
                                  out_dtype=torch.float32, workspace=space) for a in x]
         for v, ref in zip(got, want):
             assert torch.equal(v, ref)
+
+
+def test_offsets_that_overlap():
+    """Offsets that fall again give groups far more tiles than disjoint ones have
+    (512 groups of all 1024 rows: 32768 tiles instead of 1087 at most, whose k-blocks
+    pass 32 bits in large problems).  Rows outside the output stay as they
+    are, and the next call is right."""
+    R, E, N, K = 1024, 1023, 132, 200
+    rng = np.random.default_rng(60)
+    x = rng.integers(-128, 128, (R, K)).astype(np.int8)
+    w = rng.integers(-127, 128, (E, N, K)).astype(np.int8)
+    ws = np.full((E, N), 0.01, np.float32)
+    route = q8.expert_sort(T(rng.integers(0, E, (R, 1)).astype(np.int32)), E)
+    packed = q8.pack_tile_weight(T(w))
+    fallen = torch.tensor([0, R] * (E // 2 + 1), dtype=torch.int32, device=DEV)[:E + 1]
+    wrong = q8.ExpertRoute(route.order, route.position, fallen.contiguous())
+    space = torch.full((R + 64, N), 1e30, device=DEV)
+    q8.linear_experts(T(x), 0.02, 3, packed, T(ws), None, wrong, 1.0, 0, out_dtype=torch.float32,
+                      out=space[32:-32])
+    untouched = space == torch.tensor(1e30, device=DEV)
+    assert bool(untouched[:32].all()) and bool(untouched[-32:].all())
+    assert not bool(untouched[32:-32].any())
+    got = q8.linear_experts(T(x), 0.02, 3, packed, T(ws), None, route, 1.0, 0,
+                            out_dtype=torch.float32)
+    order = route.order.cpu().numpy()
+    who = np.searchsorted(route.offsets.cpu().numpy()[1:], np.arange(R), side="right")
+    acc = np.einsum("rk,rnk->rn", x[order].astype(np.float64) - 3, w[who].astype(np.float64))
+    v = acc.astype(np.float32) * np.float32(0.02) * ws[who] + np.float32(0)
+    np.testing.assert_array_equal(got.cpu().numpy(), v)
