@@ -422,6 +422,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
   job.op.count_words = p.grid * q8::kTileEpiWarps;
   job.adapter_ids = adapter_ids;
   job.L = p.L;
+  job.r = static_cast<int>(r);
   job.rank16 = p.rank16;
   job.tiles = (p.R + p.TN - 1) / p.TN;
   job.list_stride = p.list_stride;

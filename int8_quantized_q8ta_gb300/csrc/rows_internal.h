@@ -159,7 +159,7 @@ cudaError_t launch_pack_lora(const void* A, const void* B, const float* scaling,
 struct LoraJob {
   OperandJob op;
   const int32_t* adapter_ids;   // [R], in the order of x
-  int L, rank16, tiles, list_stride;
+  int L, r, rank16, tiles, list_stride;
   const uint16_t* a;            // packed A
   const float* scaling;
   float s_in;

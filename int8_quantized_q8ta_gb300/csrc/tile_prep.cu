@@ -252,10 +252,12 @@ __device__ __forceinline__ void front_products(const LoraJob& job, const uint16_
 // [TN rows][16 leading terms, 16 trailing ones] for each adapter a tile t holds
 // and 16 ranks, at (t + a) * rank16 + c (with the rows sorted by adapter,
 // either t or a grows from one such pair to the next), both terms f32 of which
-// the MMAs read the 10 leading bits of the fraction.
+// the MMAs read the 10 leading bits of the fraction.  Ranks from r on are zeros
+// whatever the scaling is (0 times an infinite one would be NaN).
 // s is row `local` of tile t.
 __device__ __forceinline__ void store_h(const LoraJob& job, int s, int t, int local, int a, int j,
                                         float v) {
+  if (j >= job.r) v = 0.0f;
   if (job.TN == 0) {
     job.h[static_cast<int64_t>(s) * job.rank16 * 16 + j] = v;
     return;

@@ -359,3 +359,21 @@ def test_ids_of_the_call_before_do_not_matter():
     v, bound = p.exact()
     u = UNIT[torch.float32]
     assert np.all(np.abs(got[2].double().cpu().numpy() - v) <= bound * (1 + u) + u * np.abs(v))
+
+
+# Every product positive, so that an infinite scaling makes every channel of its
+# adapter's rows infinite, and no others; ranks that fill no block of 16.
+@pytest.mark.parametrize("M", [3, 24, 60, 90, 300])
+@pytest.mark.parametrize("r", [5, 16, 41])
+def test_infinite_scaling(M, r):
+    p = Problem(50, M, 132, 200, 5, r, zp=-128)
+    p.a[:2] = 2
+    p.x = np.maximum(p.x, -127).astype(np.int8)
+    p.A, p.B = p.A.abs(), p.B.abs()
+    clean = p.run().cpu()
+    for s in (float("inf"), -float("inf")):
+        p.s[2] = s
+        got = p.run().cpu()
+        mine = torch.from_numpy(p.a == 2)
+        assert bool((got[mine] == s).all())
+        assert torch.equal(got[~mine], clean[~mine])
