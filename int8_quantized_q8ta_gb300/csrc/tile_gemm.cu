@@ -1171,35 +1171,37 @@ cudaError_t launch_one(const CUtensorMap& map, const CUtensorMap& map_h, const T
   constexpr int CG = Form<PAIR>::CG;
   auto kernel = tile_gemm_kernel<OUT, PAIR>;
   static DeviceOnce once;
-  cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+  static int fit[64];   // by device; written once, under the lock that every reader takes first
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int pairs = 0;
+  e = once.run([&] {
+    const cudaError_t set =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    if (!PAIR || set != cudaSuccess) return set;
+    // pairs that fit the GPU at once (both CTAs of one share a GPC)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = p.grid / CG * CG;
+    cfg.blockDim = kTileThreads;
+    cfg.dynamicSmemBytes = kTileSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0) {
+      cudaGetLastError();
+      pairs = p.grid / CG;
+    }
+    if (dev >= 0 && dev < 64) fit[dev] = pairs;
+    return cudaSuccess;
   });
   if (e != cudaSuccess) return e;
   if constexpr (PAIR) {
-    // pairs that fit the GPU at once (both CTAs of one share a GPC)
-    static int fit[64] = {0};
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    int& pairs = fit[dev & 63];
-    if (pairs == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = p.grid / CG * CG;
-      cfg.blockDim = kTileThreads;
-      cfg.dynamicSmemBytes = kTileSmem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = CG;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = p.grid / CG;
-      }
-      pairs = n;
-    }
+    if (pairs == 0) pairs = fit[dev];
     const int grid = std::max(1, std::min(pairs, p.grid / CG)) * CG;
     return launch_pdl_cluster(kernel, grid, kTileThreads, smem, CG, s, map, map_h, p);
   } else {

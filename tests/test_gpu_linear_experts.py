@@ -5,6 +5,10 @@ epilogue is the oracle's sequence of f32 steps.  Float outputs are the same f32
 value v before the requantization, rounded once: v is rebuilt from the exact
 accumulator with numpy float32 in the same order, and compared bit for bit.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -324,3 +328,43 @@ def test_offsets_that_overlap():
     acc = np.einsum("rk,rnk->rn", x[order].astype(np.float64) - 3, w[who].astype(np.float64))
     v = acc.astype(np.float32) * np.float32(0.02) * ws[who] + np.float32(0)
     np.testing.assert_array_equal(got.cpu().numpy(), v)
+
+
+FIRST_CALLS = r"""
+import sys, threading
+sys.path.insert(0, sys.argv[1])
+import torch
+import int8_quantized_q8ta_gb300 as q8
+dev = torch.device("cuda:0")
+g = torch.Generator(device=dev).manual_seed(1)
+x = torch.randint(-128, 128, (150, 512), generator=g, device=dev, dtype=torch.int8)
+w = torch.randint(-127, 128, (384, 512), generator=g, device=dev, dtype=torch.int8)
+ones = torch.ones(1, 384, device=dev)
+route = q8.expert_sort(torch.zeros(150, 1, dtype=torch.int32, device=dev), 1)
+packed = q8.pack_tile_weight(w)
+want = (x.double() @ w.double().T).float()
+torch.cuda.synchronize()
+start, good = threading.Barrier(8), []
+
+def call():
+    with torch.cuda.stream(torch.cuda.Stream()):
+        start.wait()
+        out = [q8.linear_experts(x, 1.0, 0, packed, ones, None, route, 1.0, 0,
+                                 out_dtype=torch.float32) for _ in range(5)]
+        torch.cuda.current_stream().synchronize()
+        good.append(all(torch.equal(v, want) for v in out))
+
+threads = [threading.Thread(target=call) for _ in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert good == [True] * 8, good
+assert q8.device_error() == 0
+"""
+
+
+def test_first_calls_of_several_threads():
+    """A process whose first calls of the wide form come from eight threads."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True,
+                          timeout=120)
+    assert done.returncode == 0, done.stderr[-2000:]
