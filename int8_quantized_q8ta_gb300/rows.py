@@ -226,9 +226,11 @@ def pack_tile_weight(weight: torch.Tensor) -> PackedTileWeight:
     return PackedTileWeight(buf, E, N, K)
 
 
+# (sizes depend on the device's SMs)
 @functools.lru_cache(maxsize=4096)
-def _experts_space(R: int, K: int, E: int) -> int:
-    return _lib.q8_linear_experts_workspace_bytes(R, K, E)
+def _experts_space(R: int, K: int, E: int, device: int) -> int:
+    with torch.cuda.device(device):
+        return _lib.q8_linear_experts_workspace_bytes(R, K, E)
 
 
 def _out_code(out_dtype) -> int:
@@ -264,7 +266,7 @@ def linear_experts(x, input_scale, input_zero_point, packed: PackedTileWeight, w
     b = _vector_arg(bias, (E, N), "bias")
     code = _out_code(out_dtype)
     out = _out(out, (T * k, N), out_dtype, x.device)
-    nbytes = _experts_space(T * k, K, E)
+    nbytes = _experts_space(T * k, K, E, x.get_device())
     ws = _space(nbytes, x.device, workspace)
     _check(_lib.q8_linear_experts(
         at, int(x_sorted), T, k, K, float(input_scale), int(input_zero_point),
@@ -314,8 +316,9 @@ def pack_lora(A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor) -> Packed
 
 
 @functools.lru_cache(maxsize=4096)
-def _lora_space(M: int, K: int, L: int, r: int) -> int:
-    return _lib.q8_linear_lora_workspace_bytes(M, K, L, r)
+def _lora_space(M: int, K: int, L: int, r: int, device: int) -> int:
+    with torch.cuda.device(device):
+        return _lib.q8_linear_lora_workspace_bytes(M, K, L, r)
 
 
 def linear_lora(x, input_scale, input_zero_point, packed: PackedTileWeight, weight_scales, bias,
@@ -340,7 +343,7 @@ def linear_lora(x, input_scale, input_zero_point, packed: PackedTileWeight, weig
     _shape(adapter_ids, (M,), "adapter_ids")
     code = _out_code(out_dtype)
     out = _out(out, (M, N), out_dtype, x.device)
-    nbytes = _lora_space(M, K, lora.L, lora.r)
+    nbytes = _lora_space(M, K, lora.L, lora.r, x.get_device())
     ws = _space(nbytes, x.device, workspace)
     _check(_lib.q8_linear_lora(
         at, M, K, float(input_scale), int(input_zero_point), packed.data.data_ptr(), N, scales, b,

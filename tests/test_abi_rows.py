@@ -168,3 +168,40 @@ def test_linear_lora_guards():
         assert call(**{n: ctypes.c_void_p(0x10010)}) == q8.Q8_ERR_ALIGN, n
     assert call(ids=ODD) == call(out=ODD, dt=F32) == q8.Q8_ERR_ALIGN
     assert call(M=0, x=None, ids=None) == q8.Q8_OK
+
+
+def test_binding_remembers_workspace_sizes_by_device(monkeypatch):
+    """They depend on the device's SMs: a size found on one device is not another's."""
+    torch = pytest.importorskip("torch")
+    from int8_quantized_q8ta_gb300 import rows
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Lib:
+        def q8_linear_experts_workspace_bytes(self, R, K, E):
+            return 1000 * (current[0] + 1) + R
+
+        def q8_linear_lora_workspace_bytes(self, M, K, L, r):
+            return 5000 * (current[0] + 1) + M
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(rows, "_lib", Lib())
+    for sizes in (rows._experts_space, rows._lora_space):
+        sizes.cache_clear()
+    try:
+        for _ in range(2):
+            for device in (0, 1):
+                assert rows._experts_space(7, 64, 4, device) == 1000 * (device + 1) + 7
+                assert rows._lora_space(9, 64, 4, 16, device) == 5000 * (device + 1) + 9
+    finally:
+        for sizes in (rows._experts_space, rows._lora_space):
+            sizes.cache_clear()
