@@ -51,7 +51,7 @@ def _out(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out") -
 
 
 def _space(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
-    if workspace is None:
+    if workspace is None or nbytes == 0:   # (no rows need none, whatever was given)
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     return _workspace(nbytes, device, workspace)
 

@@ -377,3 +377,14 @@ def test_infinite_scaling(M, r):
         mine = torch.from_numpy(p.a == 2)
         assert bool((got[mine] == s).all())
         assert torch.equal(got[~mine], clean[~mine])
+
+
+def test_no_rows_with_a_workspace():
+    p = Problem(5, 0, 128, 64, 2, 4)
+    space = torch.empty(4096, dtype=torch.uint8, device=DEV)
+    assert p.run(workspace=space).shape == (0, 128)
+    route = q8.expert_sort(torch.zeros((0, 2), dtype=torch.int32, device=DEV), 3)
+    packed = q8.pack_tile_weight(torch.zeros((3, 128, 64), dtype=torch.int8, device=DEV))
+    got = q8.linear_experts(torch.zeros((0, 64), dtype=torch.int8, device=DEV), 0.02, 0, packed,
+                            torch.ones((3, 128), device=DEV), None, route, 0.1, 0, workspace=space)
+    assert got.shape == (0, 128)
