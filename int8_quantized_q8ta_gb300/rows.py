@@ -2,7 +2,10 @@
 include/q8ta.h): tokens sorted by expert and back, with weights applied, and
 the gradients.
 
-Argument marshalling only, like the rest of the package; imported by it.
+Argument marshalling only, like the rest of the package; imported by it.  Float
+rows and weights that require a gradient get it: expert_gather, expert_dispatch
+and expert_combine are recorded for autograd, with the gradient calls below.
+The int8 products have no gradient.
 """
 from __future__ import annotations
 
@@ -102,6 +105,37 @@ def _empty_route(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
                        expert_ids.new_empty(num_experts + 1))
 
 
+# What is recorded for autograd: the result, already computed, as a function of
+# the inputs that require a gradient.
+
+class _Gathered(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rows, route):
+        ctx.route = route
+        ctx.mark_dirty(rows)
+        return rows
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_rows):
+        return expert_gather_backward(d_rows.contiguous(), ctx.route), None, None
+
+
+class _Combined(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, z, weights, y, route):
+        ctx.route = route
+        ctx.save_for_backward(z, weights)
+        ctx.mark_dirty(y)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dz, dw = expert_combine_backward(dy.contiguous(), *ctx.saved_tensors, ctx.route)
+        return dz, dw, None, None
+
+
 def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertRoute:
     """Slots of int32 expert_ids [T, k] sorted by expert, stable; ids outside
     [0, num_experts) are dropped slots."""
@@ -126,6 +160,8 @@ def expert_gather(x: torch.Tensor, route: ExpertRoute,
     out = _out(out, (T * k, H), x.dtype, x.device)
     _check(_lib.q8_expert_gather(at, code, T, k, H, E, position, offsets, out.data_ptr(),
                                  _stream(x)), "q8_expert_gather")
+    if x.requires_grad and torch.is_grad_enabled():
+        out = _Gathered.apply(x, out, route)
     return out
 
 
@@ -144,6 +180,8 @@ def expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: int,
                                    route.order.data_ptr(), route.position.data_ptr(),
                                    route.offsets.data_ptr(), out.data_ptr(), _stream(x)),
            "q8_expert_dispatch")
+    if x.requires_grad and torch.is_grad_enabled():
+        out = _Gathered.apply(x, out, route)
     return out, route
 
 
@@ -177,6 +215,8 @@ def expert_combine(z: torch.Tensor, weights: torch.Tensor, route: ExpertRoute,
     out = _out(out, (T, H), z.dtype, z.device)
     _check(_lib.q8_expert_combine(at, code, w, T, k, H, position, out.data_ptr(), _stream(z)),
            "q8_expert_combine")
+    if (z.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+        out = _Combined.apply(z, weights, out, route)
     return out
 
 

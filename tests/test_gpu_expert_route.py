@@ -303,3 +303,58 @@ def test_binding_refusals():
         q8.expert_combine_backward(x.half(), rows, w, route)
     with pytest.raises(ValueError):
         q8.expert_gather_backward(rows.t(), route)
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("fused", [False, True])
+def test_gradients_through_autograd(dtype, fused):
+    """dispatch, then combine: y = sum of the token's row times its kept slots'
+    weights.  dz is w dy rounded once (u), dx the f32 sum of at most k of those
+    rounded once, dw a dot over H elements."""
+    T, k, E, H = 90, 4, 7, 72
+    ids = torch.from_numpy(_ids(21, T, k, E, 0.2)).to(DEV)
+    x = _rand(1, (T, H), dtype).requires_grad_()
+    w = torch.rand((T, k), generator=torch.Generator().manual_seed(4)).to(DEV).requires_grad_()
+    if fused:
+        rows, route = q8.expert_dispatch(x, ids, E)
+    else:
+        route = q8.expert_sort(ids, E)
+        rows = q8.expert_gather(x, route)
+    y = q8.expert_combine(rows, w, route)
+    dy = _rand(2, (H, T), dtype).t()                  # not contiguous
+    y.backward(dy)
+    kept = (route.position >= 0).double().cpu()
+    w64, x64, d64 = w.detach().double().cpu(), x.detach().double().cpu(), dy.double().cpu()
+    u, tiny = UNIT[dtype], 2.0 ** -25 if dtype == torch.float16 else 0.0
+    each = (w64 * kept)[:, :, None] * d64[:, None, :]
+    size = each.abs().sum(1)
+    _close(x.grad, each.sum(1), 2 * (u + 2.0 ** -23) * (1 + u) * size + (k + 1) * 2.0 ** -23 * size
+           + (k + 1) * tiny)
+    dot = x64 * d64
+    ref = kept * dot.sum(1, keepdim=True)
+    _close(w.grad, ref, (H + 1) * 2.0 ** -23 * kept * dot.abs().sum(1, keepdim=True))
+
+
+def test_autograd_records_only_what_needs_it():
+    T, k, E, H = 20, 2, 5, 16
+    ids = torch.from_numpy(_ids(22, T, k, E)).to(DEV)
+    x, w = _rand(1, (T, H), torch.float32), torch.full((T, k), 0.5, device=DEV)
+    rows, route = q8.expert_dispatch(x, ids, E)
+    y = q8.expert_combine(rows, w, route)
+    assert not rows.requires_grad and not y.requires_grad
+    w.requires_grad_()
+    with torch.no_grad():
+        assert not q8.expert_combine(rows, w, route).requires_grad
+    out = torch.empty((T, H), device=DEV)
+    got = q8.expert_combine(rows, w, route, out=out)   # the weights' gradient alone, and into out
+    assert got is out and torch.equal(got, y)
+    got.sum().backward()
+    ref = x.double().sum(1).cpu()
+    size = x.double().abs().sum(1).cpu()
+    _close(w.grad, ref[:, None].expand(T, k), (H + 1) * 2.0 ** -23 * size[:, None])
+    x.requires_grad_()
+    kept = torch.empty((T * k, H), device=DEV)
+    q8.expert_gather(x, route, out=kept)
+    assert torch.equal(kept, rows) and kept.requires_grad
+    (g,) = torch.autograd.grad(kept.sum(), x)
+    assert torch.equal(g, torch.full_like(g, k))
