@@ -66,8 +66,11 @@ class ExpertBlock:
                    "up": up, "z": z}
 
     def backward(self, dy, kept):
-        """Gradients of the experts' outputs, the router's weights, and (through
-        the gather) of the tokens for given gradients of the sorted rows."""
+        """(dz, dweights, dx): the gradients of the experts' outputs and of the
+        router's weights, and the gather's gradient taken of dz.  The int8
+        products between rows and z have no gradient, so dz stands in for the
+        rows' own: dx shows the move back to tokens and is not the block's
+        gradient of them."""
         dz, dw = q8.expert_combine_backward(dy, kept["z"], kept["weights"], kept["route"])
         return dz, dw, q8.expert_gather_backward(dz, kept["route"])
 
