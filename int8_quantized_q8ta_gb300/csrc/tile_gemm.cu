@@ -116,10 +116,10 @@ struct Form {
 // One run's part of a unit, as the scheduling warp hands it to the others.
 struct alignas(16) Seg {
   int e, row0, rows, nb;       // group, first row, rows, output block (of 128 * CG)
-  int tile, kb0, kb1, unit;    // index of the row tile; k-blocks; kb1 0: no more
+  int tile, kb0, kb1;          // index of the row tile; k-blocks; kb1 0: no more
   int na;                      // adapters whose MMAs follow (see adapters_of)
   int first, end;              // CTAs (pairs) that share the unit
-  int pad;
+  int pad[2];
 };
 constexpr int kSegs = 4;       // parts on their way
 
@@ -246,8 +246,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (wave < waves) {
-      s.unit = wave++ * ctas + me;
-      locate(s.unit);
+      locate(wave++ * ctas + me);
       fill(s);
       s.kb0 = 0;
       s.kb1 = p.KB;
@@ -262,7 +261,6 @@ struct Walk {
       locate(unit);
     }
     fill(s);
-    s.unit = unit;
     s.kb0 = kb;
     s.kb1 = min(p.KB, kb + left);
     if (share > 0) {
