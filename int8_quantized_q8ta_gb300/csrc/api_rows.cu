@@ -46,10 +46,13 @@ struct TilePlan {
 // Adapters row by row in the epilogue, or by MMAs for each adapter and tile.
 // Row by row costs a row's own dot products, a round of MMAs the same however
 // few rows an adapter has.  Measured by row against by MMAs, ranks 16, 32
-// adapters, K 4096: 64 rows x 11008 25 against 28 us, 192 rows x 4096 33
-// against 41, x 11008 51 against 41; 4 adapters, 64 rows x 4096 20 against 18;
-// 64 adapters, 512 rows x 11008 105 against 75.  Over some sixty such sizes
-// the best multiple is 7 (the chosen one 2.6% behind the faster on average).
+// adapters, K 4096: 64 rows x 11008 25.1 against 29.5 us, 192 rows x 4096 34.2
+// against 42, x 11008 49.7 against 42.3; 4 adapters, 64 rows x 4096 17.3 both;
+// 100 adapters, 512 rows x 11008 100 against 79, 300 rows x 8192 of K 2048 58
+// against 44.  Over some sixty such sizes the best multiple is 7 (the chosen one
+// 2.6% behind the faster on average); it sees neither N nor the row tiles, whose
+// number is what makes row by row lose, and is up to 30% behind between 65 rows
+// and 7 an adapter.
 constexpr int kRowsPerAdapter = 7;
 bool lora_by_row(int64_t M, int64_t L) { return M < kRowsPerAdapter * L; }
 

@@ -15,12 +15,13 @@
 // Sums are f32, taken in slot order j = 0, 1, ..., rounded once to the row
 // type.  No atomics on global memory: results do not depend on timing.
 //   All but the sort are bound by HBM in long batches and by the latency of
-// position -> row -> row in short ones.  Measured (cold, one launch, of 6.7
-// TB/s copied): rows of 4096 bf16, 2048 tokens of 4 experts: gather 12.3 us
-// (84 MB, 6.8 TB/s), its gradient 16 us (5.2 TB/s); 4096 tokens of 8: combine
-// 48.5 us (302 MB, 6.2 TB/s), its gradient 85 us (573 MB, 6.7 TB/s).  Rows that
-// are no multiple of 16 bytes go element by element: 3885 rows of 1001 halfs,
-// combine 7.3 and its gradient 7.8 us (1.3 and 2.2 TB/s).
+// position -> row -> row in short ones.  Measured (calls one after another in a
+// graph, three sets of inputs in turn; 6.8 TB/s is a plain copy): rows of 4096
+// bf16, 2048 tokens of 4 experts: gather 14.3 us (84 MB, 5.9 TB/s), its gradient
+// 16.3 (5.2); 4096 tokens of 8: gather 49.0 us (302 MB, 6.2 TB/s), combine 49.0
+// (6.2), its gradient 88.5 (570 MB, 6.4).  Rows that are no multiple of 16 bytes
+// are combined element by element: 3885 rows of 1001 halfs, combine 4.4 and its
+// gradient 7.2 us (2.1 and 2.4 TB/s), of 1008 halfs 2.95 and 4.2.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,9 +50,9 @@ namespace {
 // construction.  The CTAs exchange their E + 1 totals through distributed
 // shared memory; nothing but the ids is read from global memory.  A warp's
 // slots of one expert are found by one ballot for each bit of the id (a match
-// instruction takes as long as there are different ids).  Latency bounds it:
-// 8 slots 2.6 us, 1024 4.2, 8192 5.1, 32768 6.6, and from there on the 8 CTAs'
-// own work, 262144 slots 26 us.
+// instruction takes as long as there are different ids).  Latency bounds it (in a
+// graph, as above): 8 slots 3.0 us, 1024 4.8, 8192 5.1, 32768 6.6, and from there
+// on the work of 8 CTAs, the most a portable cluster has: 262144 slots 26 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortKeys = 4;              // ids a thread has in flight
@@ -428,8 +429,8 @@ size_t expert_sort_smem(int threads, int E) {
 cudaError_t launch_expert_sort(const int32_t* ids, int64_t R, int E, int32_t* order,
                                int32_t* position, int32_t* offsets, cudaStream_t s,
                                bool keep_dropped) {
-  // a slot a thread while 8 CTAs have that many: 8192 slots 6.2 us with 8,
-  // 7.5 with 2 CTAs; 3111 slots 5.8 with 4, 6.4 with one
+  // a slot a thread while 8 CTAs have that many: 8192 slots 5.1 us with 8 CTAs,
+  // 5.6 with 4, 6.5 with 2, 9.8 with one; 3111 slots 4.65 with 4, 4.8 with one
   const int threads = R <= 256 ? 256 : 1024;
   int ctas = 1;
   while (ctas < 8 && R > 1024ll * ctas) ctas *= 2;

@@ -334,7 +334,8 @@ class PackedLora:
 
 def pack_lora(A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor) -> PackedLora:
     """Pack adapters A [L, r, K], B [L, N, r] (float16 or bfloat16) and
-    scaling float32 [L] once."""
+    scaling float32 [L] once.  An infinity or NaN in B makes every channel of
+    its adapter's rows NaN."""
     if _dtype_code(A, "A") not in (1, 2):
         raise TypeError(f"A must be float16 or bfloat16, got {A.dtype}")
     _need(A, A.dtype, "A")
