@@ -575,8 +575,8 @@ q8_status q8_linear_experts(const int8_t* x, int x_sorted, int64_t T, int64_t k,
  *   A float16 or bfloat16 [L, r, K]; B the same type [L, N, r]; scaling
  *   float [L].  q8_lora_pack lays them out once, at load time, and waits (an
  *   adapter is exchanged by packing again).
- * The adapter sums are f32; h enters the second product as two tf32 terms (22
- * significant bits; with fewer than 7 rows an adapter, as it is), A, B and
+ * The adapter sums are f32; h enters the second product as two tf32 terms,
+ * within its last place (with fewer than 7 rows an adapter, as it is), A, B and
  * x - input_zero_point exactly.  Results do not depend on timing.  Infinities and NaN stay with the rows of their adapter:
  * one in A gives what the formula gives, one in B makes every channel of its
  * adapter's rows NaN.

@@ -33,7 +33,7 @@
 // Adapters: after a unit's k-blocks, its last run multiplies B[a] by the rows'
 // h for each adapter the tile holds, into an accumulator of its own: tf32
 // MMAs, B exact (f16 and bf16 both fit tf32), h as the sum of two tf32 terms
-// (22 significant bits), rows of other adapters as zeros.  The kernel before
+// (within its last place), rows of other adapters as zeros.  The kernel before
 // this one lays h out so, and it comes through the ring like tokens: fetched
 // by the converting warps it queued behind the next unit's copies (a round of
 // 16 ranks 1,350 cycles, and 2,000 before the first).

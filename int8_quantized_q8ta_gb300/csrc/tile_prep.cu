@@ -251,9 +251,12 @@ __device__ __forceinline__ void front_products(const LoraJob& job, const uint16_
 // h[s, j].  For dot products row by row: [R][ranks].  For MMAs: a block of
 // [TN rows][16 leading terms, 16 trailing ones] for each adapter a tile t holds
 // and 16 ranks, at (t + a) * rank16 + c (with the rows sorted by adapter,
-// either t or a grows from one such pair to the next), both terms f32 of which
-// the MMAs read the 10 leading bits of the fraction.  Ranks from r on are zeros
-// whatever the scaling is (0 times an infinite one would be NaN).
+// either t or a grows from one such pair to the next).  The MMAs read 10 bits of
+// a term's fraction and cut off the rest, so both are rounded to that here: they
+// miss h by its last place at most (not rounded, by three, and always towards
+// zero).  From 2^127 on, where rounding could make an infinity, they are cut.
+// Ranks from r on are zeros whatever the scaling is (0 times an infinite one
+// would be NaN).
 // s is row `local` of tile t.
 __device__ __forceinline__ void store_h(const LoraJob& job, int s, int t, int local, int a, int j,
                                         float v) {
@@ -264,10 +267,14 @@ __device__ __forceinline__ void store_h(const LoraJob& job, int s, int t, int lo
   }
   const int64_t block = static_cast<int64_t>(t + a) * job.rank16 + (j >> 4);
   float* at = job.h + (block * job.TN + local) * 32 + (j & 15);
-  const float hi = __uint_as_float(__float_as_uint(v) & 0xffffe000u);
+  const uint32_t half = (__float_as_uint(v) & 0x7f000000u) == 0x7f000000u ? 0u : 0x1000u;
+  const auto tf32 = [&](float f) {
+    return __uint_as_float((__float_as_uint(f) + half) & 0xffffe000u);
+  };
+  const float hi = tf32(v);
   at[0] = hi;
   // (inf - inf would be NaN)
-  at[16] = (__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u ? 0.0f : __fsub_rn(v, hi);
+  at[16] = (__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u ? 0.0f : tf32(__fsub_rn(v, hi));
 }
 
 // 16 ranks (block c) of adapter a for `count` <= 32 rows of the batch.  Every

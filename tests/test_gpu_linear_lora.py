@@ -388,3 +388,31 @@ def test_no_rows_with_a_workspace():
     got = q8.linear_experts(torch.zeros((0, 64), dtype=torch.int8, device=DEV), 0.02, 0, packed,
                             torch.ones((3, 128), device=DEV), None, route, 0.1, 0, workspace=space)
     assert got.shape == (0, 128)
+
+
+# h as it is: one input of 1 against A = 1, so that h is the scaling, and B = 1
+# (r 1, w 0).  MMAs take h as two terms, which miss it by its last place at most:
+# 2^-23 of the power of two below it.  One row tile, narrow and wide, and sorted
+# rows; the largest number stays finite (from 2^127 on bits may be cut off), an
+# infinity comes through.
+@pytest.mark.parametrize("M,L", [(64, 9), (150, 20), (300, 40), (1500, 200)])
+def test_h_keeps_its_bits(M, L):
+    p = Problem(M, M, 130, 64, L, 1, bias=False)
+    p.s_in = 1.0
+    p.x[:], p.w[:] = 0, 0
+    p.x[:, 3] = 1
+    p.A, p.B = torch.zeros_like(p.A), torch.ones_like(p.B)
+    p.A[:, 0, 3] = 1
+    rng = np.random.default_rng(M)
+    s = (rng.uniform(1, 2, L) * 2.0 ** rng.integers(-20, 20, L)).astype(np.float32)
+    s[::2] *= -1
+    s[:2] = np.float32(3.4028235e38), np.float32("inf")
+    p.s = torch.from_numpy(s)
+    p.a[:2] = 0, 1
+    got = p.run().cpu().numpy()
+    want = np.broadcast_to(s[p.a][:, None], got.shape)
+    fine = np.isfinite(want)
+    assert np.array_equal(got[~fine], want[~fine]) and np.isfinite(got[fine]).all()
+    fine &= np.abs(want) < 2.0 ** 127
+    place = 2.0 ** (np.floor(np.log2(np.abs(want[fine].astype(np.float64)))) - 23)
+    assert (np.abs(got[fine].astype(np.float64) - want[fine]) <= place).all()
