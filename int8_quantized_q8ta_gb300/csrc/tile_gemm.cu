@@ -75,6 +75,10 @@ constexpr int NAb = 2, NA = 1 << NAb;
 // win further: 8 and 64 rows x 22016 25.8 against 28.4 and 44 against 50.
 constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
 
+// What the kernels before this one write while it may already run (offsets,
+// ids, lists, h, output rows) is read with ordinary loads, not as data that is
+// constant for the kernel's life.
+
 // The two forms of the kernel.
 //   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
 // a tile through the 2-SM MMA, each with its own 128 output channels and half
@@ -151,7 +155,7 @@ __device__ __forceinline__ int chunk_stages_of(const TileParams& p) {
 // Rows of group e.  Offsets come from device memory: whatever they hold, no
 // row outside [0, R) is touched.
 __device__ __forceinline__ int group_end(const TileParams& p, int e) {
-  return min(p.R, max(0, __ldg(p.offsets + e)));
+  return min(p.R, max(0, p.offsets[e]));
 }
 __device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start) {
   start = group_end(p, e);
@@ -326,7 +330,7 @@ struct Feed {
 // take them.
 __device__ __forceinline__ int adapters_of(const TileParams& p, const Seg& s) {
   return (p.L > 0 && !p.by_row && s.kb1 == p.KB)
-             ? __ldg(p.lists + static_cast<int64_t>(s.tile) * p.list_stride)
+             ? p.lists[static_cast<int64_t>(s.tile) * p.list_stride]
              : 0;
 }
 
@@ -351,7 +355,7 @@ __device__ __forceinline__ void row_deltas(const TileParams& p, int nb, int row,
   const float4* h = reinterpret_cast<const float4*>(
       p.h + static_cast<int64_t>(__shfl_sync(0xffffffffu, my_s, lane >> 2)) * p.rank16 * 16);
   for (int c = 0; c < p.rank16; ++c) {
-    const float4 hv = h_in ? __ldg(h + c * 4 + (lane & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 hv = h_in ? h[c * 4 + (lane & 3)] : make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
     *reinterpret_cast<float4*>(&corner[lane >> 2][(lane & 3) * 4]) = hv;
     __syncwarp();
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (na > 0) pdl_wait();
       const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
       for (int i = 0; i < na && ok; ++i) {
-        const int64_t at = static_cast<int64_t>(uniform(__ldg(list + i))) * p.NB + nb;
+        const int64_t at = static_cast<int64_t>(uniform(list[i])) * p.NB + nb;
         const uint8_t* lb = p.lora_b + at * p.rank16 * 4096;
         for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
@@ -595,7 +599,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int32_t* list = p.lists + static_cast<int64_t>(tile) * p.list_stride + 1;
       const int h0 = row0 - uniform(sg->row0);
       for (int i = 0; i < na && ok; ++i) {
-        const int at = (tile + uniform(__ldg(list + i))) * p.rank16;
+        const int at = (tile + uniform(list[i])) * p.rank16;
         for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
@@ -873,7 +877,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // are used: eight lanes a row, 4 lines of 128 bytes to each 8 ranks
     const auto fetch_adapters = [&](const Seg* part, int mine, int nb) {
       for (int j = 0; j < mine; j += 4) {
-        const int a = __ldg(p.ids + part->row0 + min(col0 + j + (lane >> 3), part->rows - 1));
+        const int a = p.ids[part->row0 + min(col0 + j + (lane >> 3), part->rows - 1)];
         if (a >= 0 && a < p.L)
           for (int c = 0; c < p.rank16; ++c)
             prefetch_l2(
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // (rows past the tile's end repeat its last)
           const int my_s = sg->row0 + min(col0 + j + (lane & 7), sg->rows - 1);
           float d[8];
-          row_deltas(p, min(nb, p.NB - 1), quarter * 32 + lane, __ldg(p.ids + my_s), my_s,
+          row_deltas(p, min(nb, p.NB - 1), quarter * 32 + lane, p.ids[my_s], my_s,
                      sh.corner[ew], d);
           tmem_st_8cols(lane_addr + F::kAcc * acc_cols + NA * KD * 32 + j, d);
         }
@@ -1066,7 +1070,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // that ran the unit's end
         const bool other_d =
             !has_d && p.L > 0 &&
-            (p.by_row || __ldg(p.lists + static_cast<int64_t>(sg->tile) * p.list_stride) > 0);
+            (p.by_row || p.lists[static_cast<int64_t>(sg->tile) * p.list_stride] > 0);
         if (has_d) {
 #pragma unroll
           for (int b = 0; b < kCols / 8; ++b)
@@ -1125,8 +1129,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // a lane looks up one or two columns' rows for all of them
           T* to = static_cast<T*>(p.out) + n;
           const int32_t* map = p.out_rows + sg->row0 + col0;
-          const int m0 = __ldg(map + min(lane, mine - 1));
-          const int m1 = kCols > 32 ? __ldg(map + min(lane + 32, mine - 1)) : 0;
+          const int m0 = map[min(lane, mine - 1)];
+          const int m1 = kCols > 32 ? map[min(lane + 32, mine - 1)] : 0;
 #pragma unroll
           for (int j = 0; j < kCols; ++j) {
             const int64_t row = __shfl_sync(0xffffffffu, j < 32 ? m0 : m1, j & 31);

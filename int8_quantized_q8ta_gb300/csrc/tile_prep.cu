@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256) pack_tile_weight_kernel(const int8_t* __r
 __device__ __forceinline__ int64_t operand_row(const OperandJob& job, int64_t s) {
   int64_t row = s;
   if (job.order != nullptr) {
-    const int slot = __ldg(job.order + s);
+    const int slot = job.order[s];   // (written by the kernel before: no __ldg)
     if (slot < 0) return -1;
     row = job.k == 1 ? slot : slot / job.k;
   }
@@ -327,7 +327,7 @@ __device__ void front_rows(const LoraJob& job, FrontShared& sh, cg::cluster_grou
 }
 
 __device__ __forceinline__ int adapter_of(const LoraJob& job, int s) {
-  const int row = job.op.order != nullptr ? __ldg(job.op.order + s) : s;
+  const int row = job.op.order != nullptr ? job.op.order[s] : s;
   const int a = __ldg(job.adapter_ids + row);
   return a >= 0 && a < job.L ? a : -1;
 }
@@ -456,8 +456,8 @@ __device__ bool find_piece(const LoraJob& job, ShrinkShared& sh, int u) {
     const int a = a0 + threadIdx.x;
     int first = 0, rows = 0;
     if (a < job.L) {
-      first = __ldg(job.offsets + a);
-      rows = __ldg(job.offsets + a + 1) - first;
+      first = job.offsets[a];
+      rows = job.offsets[a + 1] - first;
     }
     const int n = (rows + kFrontRows - 1) / kFrontRows;
     int incl = n;
