@@ -134,7 +134,8 @@ def main():
     end.record()
     torch.cuda.synchronize()
     assert q8.device_error() == 0
-    print(f"forward and gradient calls of {tokens} tokens: {start.elapsed_time(end) / 50 * 1e3:.0f} us")
+    took = start.elapsed_time(end) / 50 * 1e3
+    print(f"forward and gradient calls of {tokens} tokens: {took:.0f} us")
 
 
 if __name__ == "__main__":
