@@ -60,7 +60,8 @@ def test_items_of_rows(prog):
     """Up to 192 rows of (2^30 / 8) chunks: item numbers beyond 2^32."""
     cases = []
     for width in (8, 24, 512, 1000, 2 ** 22, 2 ** 25 - 8, 2 ** 27):
-        for first, step in ((0, 256), (255, 1024), (311295, 311296), (7, width), (1, 2 * width + 3)):
+        for first, step in ((0, 256), (255, 1024), (311295, 311296), (7, width),
+                            (1, 2 * width + 3)):
             for n in (0, 1, 5, 1000, 80000):
                 cases.append((first, step, width, n))
     assert max((f + n * s) for f, s, _, n in cases) > 2 ** 34
