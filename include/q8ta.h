@@ -66,8 +66,9 @@ typedef enum q8_status {
   Q8_ERR_NULL = 1,        /* a required pointer is NULL */
   Q8_ERR_SHAPE = 2,       /* a size or shape guard failed */
   Q8_ERR_ALIGN = 3,       /* a pointer misses a documented alignment */
-  Q8_ERR_UNSUPPORTED = 4, /* activation other than "none"/"relu", dilation or
-                             groups < 1, conv2d stride > 8 */
+  Q8_ERR_UNSUPPORTED = 4, /* activation that the call does not name, a dtype
+                             that it does not take, dilation or groups < 1,
+                             conv2d stride > 8 */
   Q8_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than required */
   Q8_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
   Q8_ERR_DEVICE = 7,      /* a kernel raised the library's device error word */
@@ -599,6 +600,110 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
                          double output_scale, int32_t output_zero_point, const char* activation,
                          q8_dtype out_dtype, void* out, void* workspace, size_t workspace_bytes,
                          q8_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rows with a scale for each token                                          */
+/* ------------------------------------------------------------------------ */
+/*
+ * Activations quantized as they come, each row (token) with its own scale, the
+ * products and the gated pair of projections on them, and the gradients
+ * through int8 weights.  The pages have no counterpart; all guards are this
+ * library's.
+ *
+ *   q8_quantize_per_token  x [M, K] of a float dtype -> q int8 [M, K] and
+ *     scales float [M]:  a = max_k |x[m,k]|, s = a / 127,
+ *     q[m,k] = rint(x[m,k] * (1 / s)), every step rounded once to f32: the
+ *     integers of q8_quantize_per_tensor with scale s and zero point 0.  Rows
+ *     whose s would be below f32's normal numbers (a row of zeros among them)
+ *     get s = 0 and zeros.  A row that holds an infinity or NaN gets that as
+ *     its scale and int8 values without meaning, so that all that is computed
+ *     of it is infinite or NaN; other rows are as without it.
+ *   q8_dequantize_per_token  out[m,k] = (float)q[m,k] * scales[m], rounded to
+ *     the float dtype.
+ * Guards: 0 <= M <= INT32_MAX (0: nothing to do), K >= 1, M*K*4 within int64;
+ * pointers aligned to their element; Q8_I8 is Q8_ERR_UNSUPPORTED.  Rows of a
+ * multiple of 8 values on 16-byte aligned bases are the fast form.
+ */
+q8_status q8_quantize_per_token(const void* x, q8_dtype dtype, int64_t M, int64_t K, int8_t* q,
+                                float* scales, q8_stream_t stream);
+q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t M, int64_t K,
+                                  q8_dtype dtype, void* out, q8_stream_t stream);
+
+/*
+ * The int8 product with scales for each token and channel:
+ *   acc[m,n] = sum_k q[m,k] * weight[n,k]                    exact int32
+ *   v[m,n] = ((float)acc * x_scales[m]) * weight_scales[n] + bias[n]
+ * one f32 rounding a step, then "none" or "relu" and one rounding to
+ * out_dtype (Q8_F32, Q8_F16 or Q8_BF16).
+ *   x          x_dtype Q8_I8: q [M, K], x_scales [M] read, x_q not used; a
+ *              float dtype: rows to quantize first as q8_quantize_per_token
+ *              does, whose result goes to x_q and x_scales where these are
+ *              not NULL
+ *   weight     packed by q8_tile_pack_weight with E = 1
+ *   bias       float [N] or NULL;  out [M, N]
+ * q8_linear_per_token_backward is the gradient of the rows, taken straight
+ * through the quantizer (as if x were q * x_scales, and the scales constants):
+ *   dx[m,k] = sum_n (dy[m,n] * weight_scales[n]) * weight[n,k]
+ * with dy taken as 0 where y is given and y[m,n] is not above 0 (relu: y the
+ * forward output).  dy, y [M, N] and dx [M, K] are all Q8_F16 or all Q8_BF16
+ * (others Q8_ERR_UNSUPPORTED).  The product dy * weight_scale is rounded to
+ * that type (Q8_F16: after division by the largest scale's power of two, and
+ * beyond 65504 it is infinite), the weight is exact, sums are f32.
+ *   packed_transposed  q8_tile_pack_weight of the transposed weight [K, N]
+ * Results do not depend on timing.
+ * Guards: M and K as above, 1 <= N <= 2^24 (backward: K), the tiles' count
+ * and products of sizes as in q8_linear_experts; workspace of the matching
+ * number of bytes and the packed weights 256-byte aligned.
+ */
+size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N);
+q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,
+                              float* x_scales, const void* packed_weight, int64_t N,
+                              const float* weight_scales, const float* bias,
+                              const char* activation, q8_dtype out_dtype, void* out,
+                              void* workspace, size_t workspace_bytes, q8_stream_t stream);
+size_t q8_linear_per_token_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M, int64_t N,
+                                       const void* y, const void* packed_transposed, int64_t K,
+                                       const float* weight_scales, void* dx, void* workspace,
+                                       size_t workspace_bytes, q8_stream_t stream);
+
+/*
+ * The gated pair of a feed-forward block in one product:
+ *   g, u[m,n] = v of q8_linear_per_token with the gate's and the up
+ *               projection's weight, scales and bias
+ *   h[m,n] = act(g) * u, f32, rounded once to out_dtype
+ * act "silu" (g / (1 + exp(-g))), "gelu" (g (1 + erf(g / sqrt 2)) / 2) or
+ * "relu".  weight_scales float [2, N] and bias float [2, N] or NULL: the
+ * gate's first.
+ * q8_linear_gated_backward computes g and u again from the int8 rows and their
+ * scales, which are all that a forward pass has to keep, and then the gradient
+ * of the rows, straight through the quantizer:
+ *   dg = dh * u * act'(g), du = dh * act(g)
+ *   dx[m,k] = sum_n (dg ws[0,n]) * gate[n,k] + (du ws[1,n]) * up[n,k]
+ * (relu's slope at 0 is 0).  dh [M, N] and dx [M, K] are both Q8_F16 or both
+ * Q8_BF16; dg ws and du ws are rounded as dy * weight_scale is above.
+ * q8_gated_pack_weight packs gate and up, int8 [N, K] each, in the layout of
+ * the forward pass (transposed 0) or of the gradient (not 0); it waits, as
+ * q8_tile_pack_weight does.
+ * Guards: as above with 1 <= N <= 2^23.
+ */
+size_t q8_gated_packed_weight_bytes(int64_t N, int64_t K, int transposed);
+q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, int64_t K,
+                               int transposed, void* packed, size_t packed_bytes,
+                               q8_stream_t stream);
+size_t q8_linear_gated_workspace_bytes(int64_t M, int64_t K, int64_t N);
+q8_status q8_linear_gated(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,
+                          float* x_scales, const void* packed_weight, int64_t N,
+                          const float* weight_scales, const float* bias, const char* activation,
+                          q8_dtype out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                          q8_stream_t stream);
+size_t q8_linear_gated_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
+q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, int64_t N,
+                                   const int8_t* x_q, const float* x_scales, int64_t K,
+                                   const void* packed_weight, const void* packed_transposed,
+                                   const float* weight_scales, const float* bias,
+                                   const char* activation, void* dx, void* workspace,
+                                   size_t workspace_bytes, q8_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -47,6 +47,12 @@ EXPORTS = (
     "q8_tile_packed_weight_bytes", "q8_tile_pack_weight", "q8_linear_experts_workspace_bytes",
     "q8_linear_experts",
     "q8_lora_packed_bytes", "q8_lora_pack", "q8_linear_lora_workspace_bytes", "q8_linear_lora",
+    "q8_quantize_per_token", "q8_dequantize_per_token",
+    "q8_linear_per_token_workspace_bytes", "q8_linear_per_token",
+    "q8_linear_per_token_backward_workspace_bytes", "q8_linear_per_token_backward",
+    "q8_gated_packed_weight_bytes", "q8_gated_pack_weight",
+    "q8_linear_gated_workspace_bytes", "q8_linear_gated",
+    "q8_linear_gated_backward_workspace_bytes", "q8_linear_gated_backward",
 )
 
 
@@ -148,6 +154,20 @@ def _load() -> ctypes.CDLL:
         "q8_linear_lora_workspace_bytes": (S, [I64, I64, I64, I64]),
         "q8_linear_lora": (ctypes.c_int, [P, I64, I64, D, I32, P, I64, P, P, P, I32, I64, I64, P, D,
                                           I32, C, I32, P, P, S, P]),
+        "q8_quantize_per_token": (ctypes.c_int, [P, I32, I64, I64, P, P, P]),
+        "q8_dequantize_per_token": (ctypes.c_int, [P, P, I64, I64, I32, P, P]),
+        "q8_linear_per_token_workspace_bytes": (S, [I64, I64, I64]),
+        "q8_linear_per_token": (ctypes.c_int, [P, I32, I64, I64, P, P, P, I64, P, P, C, I32, P, P, S,
+                                               P]),
+        "q8_linear_per_token_backward_workspace_bytes": (S, [I64, I64, I64]),
+        "q8_linear_per_token_backward": (ctypes.c_int, [P, I32, I64, I64, P, P, I64, P, P, P, S, P]),
+        "q8_gated_packed_weight_bytes": (S, [I64, I64, ctypes.c_int]),
+        "q8_gated_pack_weight": (ctypes.c_int, [P, P, I64, I64, ctypes.c_int, P, S, P]),
+        "q8_linear_gated_workspace_bytes": (S, [I64, I64, I64]),
+        "q8_linear_gated": (ctypes.c_int, [P, I32, I64, I64, P, P, P, I64, P, P, C, I32, P, P, S, P]),
+        "q8_linear_gated_backward_workspace_bytes": (S, [I64, I64, I64]),
+        "q8_linear_gated_backward": (ctypes.c_int, [P, I32, I64, I64, P, P, I64, P, P, P, P, C, P, P,
+                                                    S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -850,3 +870,10 @@ from .rows import (ExpertRoute, PackedLora, PackedTileWeight, expert_combine,  #
                    expert_combine_backward, expert_dispatch, expert_gather,
                    expert_gather_backward, expert_sort, linear_experts, linear_lora, pack_lora,
                    pack_tile_weight)
+
+# ---------------------------------------------------------------------------
+# rows with a scale for each token
+# ---------------------------------------------------------------------------
+from .tokens import (PackedGatedWeight, dequantize_per_token, linear_gated,  # noqa: E402
+                     linear_gated_backward, linear_per_token, linear_per_token_backward,
+                     pack_gated_weight, pack_gated_weight_t, quantize_per_token)

@@ -122,9 +122,33 @@ struct TileParams {
   const int32_t* ids;       // [R] adapter of each row
   const int32_t* lists;     // per row tile: adapter count, then the adapters
   int list_stride;
+  // rows with a scale for each token (L == 0, offsets null, E == 1)
+  const float* row_scale;   // [R]
+  int act;                  // Activation of the gated forms
+  const void* dh;           // [R, N] the gated output's gradient
+  uint16_t* operand_out;    // [2 NB][R][64] the gradient's operand
+  const float* rescale;     // what its values are multiplied by, and the sums
+  const float* unscale;     // after it: powers of two on the device, or null for 1
 };
 cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
                              cudaStream_t s);
+
+// The forms for rows with a scale for each token (see TileForm): float outputs;
+// the gated ones take N output channels and NB blocks of 128 packed rows, two
+// rows a channel (see gated_rows); the last two f16 or bf16 alone, the very last
+// an operand of that type.
+enum Activation { kActNone, kActRelu, kActSilu, kActGelu };
+cudaError_t launch_tile_token(TileParams p, const void* operand, q8_dtype out_dtype,
+                              cudaStream_t s);
+cudaError_t launch_tile_gated(TileParams p, const void* operand, q8_dtype out_dtype,
+                              cudaStream_t s);
+cudaError_t launch_tile_gated_grad(TileParams p, const void* operand, q8_dtype dtype,
+                                   cudaStream_t s);
+cudaError_t launch_tile_grad(TileParams p, const void* operand, q8_dtype dtype, cudaStream_t s);
+
+// Rows of a packed gated weight: 16 of the gate, 16 of the up projection in
+// turn, both padded with zeros to a multiple of 16 channels.
+inline int64_t gated_rows(int64_t N) { return 2 * round_up(N, 16); }
 
 // Weights [E][N][K] -> [E][NB][KB][4][128][16] bytes: for each block of 128
 // output channels and 64 inputs, 16-input chunks of all 128 rows; top bits
