@@ -646,9 +646,9 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
  *   dx[m,k] = sum_n (dy[m,n] * weight_scales[n]) * weight[n,k]
  * with dy taken as 0 where y is given and y[m,n] is not above 0 (relu: y the
  * forward output).  dy, y [M, N] and dx [M, K] are all Q8_F16 or all Q8_BF16
- * (others Q8_ERR_UNSUPPORTED).  The product dy * weight_scale is rounded to
- * that type (Q8_F16: after division by the largest scale's power of two, and
- * beyond 65504 it is infinite), the weight is exact, sums are f32.
+ * (others Q8_ERR_UNSUPPORTED).  Each product dy * weight_scale is rounded to 11
+ * bits (f16, under a power of two of its row that keeps it in range: a value
+ * some 2^-28 of its row's bound keeps fewer), the weight is exact, sums are f32.
  *   packed_transposed  q8_tile_pack_weight of the transposed weight [K, N]
  * Results do not depend on timing.
  * Guards: M and K as above, 1 <= N <= 2^24 (backward: K), the tiles' count

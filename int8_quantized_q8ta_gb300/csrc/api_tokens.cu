@@ -55,10 +55,10 @@ bool gated_sizes_ok(int64_t N, int64_t K) {
 }
 
 // Two contractions one after the other: the rows' operand and the gradients',
-// one set of parts, both counts.
+// one set of parts, both counts, and each row's powers of two.
 struct GradSpace {
   TilePlan rows, grads;
-  size_t grad_operand, parts, counts, norm, total;
+  size_t grad_operand, parts, counts, powers, total;
 };
 GradSpace gated_grad_space(int64_t M, int64_t N, int64_t K) {
   GradSpace t{};
@@ -67,8 +67,8 @@ GradSpace gated_grad_space(int64_t M, int64_t N, int64_t K) {
   t.grad_operand = t.rows.operand;
   t.parts = t.grad_operand + t.grads.operand;
   t.counts = t.parts + t.grads.parts;
-  t.norm = t.counts + 2 * t.grads.counts;
-  t.total = t.norm + q8::kWorkspaceAlign;
+  t.powers = t.counts + 2 * t.grads.counts;
+  t.total = t.powers + 2 * q8::align_ws(static_cast<size_t>(M) * 4);
   return t;
 }
 
@@ -141,6 +141,23 @@ q8_status token_product(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, i
       !aligned(out, q8::dtype_bytes(out_dtype)))
     return Q8_ERR_ALIGN;
   const int64_t rows = gated ? q8::gated_rows(N) : N;
+  if (q8::token_rows_fit(M, K)) {
+    q8::TokenRowsJob job{};
+    job.x = x;
+    job.x_dtype = x_dtype;
+    job.M = M;
+    job.K = K;
+    job.q = x_q;
+    job.scales = x_scales;
+    job.w = static_cast<const uint8_t*>(packed);
+    job.N = N;
+    job.ws = ws;
+    job.bias = bias;
+    job.act = act;
+    job.out_dtype = out_dtype;
+    job.out = out;
+    return cuda_status(q8::launch_token_rows(job, gated, s));
+  }
   const TokenSpace sp = token_space(M, K);
   if (!units_ok(M, 1, rows, K, sp.plan)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
@@ -199,7 +216,7 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
 
 // ---- products with scales for each token and channel ------------------------
 size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K)) return 0;
+  if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K) || q8::token_rows_fit(M, K)) return 0;
   return token_space(M, K).total;
 }
 
@@ -222,7 +239,7 @@ q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_
 
 size_t q8_linear_per_token_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || !rows_ok(M, N) || !tile_sizes_ok(1, K, N)) return 0;
-  return plan_tiles(M, N, 1).total + q8::kWorkspaceAlign;
+  return token_space(M, N).total;
 }
 
 q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M, int64_t N,
@@ -237,32 +254,29 @@ q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M
   if (!aligned(dy, 2) || !aligned(y, 2) || !aligned(dx, 2) || !aligned(weight_scales, 4) ||
       !aligned(packed_transposed, q8::kWorkspaceAlign))
     return Q8_ERR_ALIGN;
-  const TilePlan plan = plan_tiles(M, N, 1);
-  if (!units_ok(M, 1, K, N, plan)) return Q8_ERR_SHAPE;
-  if (!workspace || workspace_bytes < plan.total + q8::kWorkspaceAlign) return Q8_ERR_WORKSPACE;
+  const TokenSpace sp = token_space(M, N);
+  if (!units_ok(M, 1, K, N, sp.plan)) return Q8_ERR_SHAPE;
+  if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
   auto* space = static_cast<uint8_t*>(workspace);
-  // f16 has few exponents: the channels' scales relative to the largest
-  float* norm = dtype == Q8_F16 ? reinterpret_cast<float*>(space + plan.total) : nullptr;
-  q8::TileParams p = tile_params(M, K, K, N, plan, packed_transposed);
+  auto* unscale = reinterpret_cast<float*>(space + sp.scales);
+  q8::TileParams p = tile_params(M, K, K, N, sp.plan, packed_transposed);
   p.out = dx;
-  p.unscale = norm != nullptr ? norm + 1 : nullptr;
-  p.parts = reinterpret_cast<int32_t*>(space + plan.operand);
-  p.counts = reinterpret_cast<int32_t*>(space + plan.operand + plan.parts);
+  p.unscale = unscale;
+  p.parts = reinterpret_cast<int32_t*>(space + sp.plan.operand);
+  p.counts = reinterpret_cast<int32_t*>(space + sp.plan.operand + sp.plan.parts);
   q8::GradOperandJob job{};
   job.dy = dy;
   job.y = y;
   job.ws = weight_scales;
-  job.rescale = norm;
   job.M = M;
   job.N = N;
   job.dst = reinterpret_cast<uint16_t*>(space);
+  job.unscale = unscale;
   job.KB = p.KB;
   job.counts = p.counts;
   job.count_words = p.grid * q8::kTileEpiWarps;
-  cudaError_t e = cudaSuccess;
-  if (norm != nullptr) e = q8::launch_channel_norm(weight_scales, N, norm, cs(stream));
-  if (e == cudaSuccess) e = q8::launch_grad_operand(job, dtype, cs(stream));
+  cudaError_t e = q8::launch_grad_operand(job, dtype, cs(stream));
   if (e == cudaSuccess) e = q8::launch_tile_grad(p, space, dtype, cs(stream));
   return cuda_status(e);
 }
@@ -297,7 +311,7 @@ q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, 
 }
 
 size_t q8_linear_gated_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K)) return 0;
+  if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || q8::token_rows_fit(M, K)) return 0;
   return token_space(M, K).total;
 }
 
@@ -349,7 +363,8 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
   auto* space = static_cast<uint8_t*>(workspace);
-  float* norm = dtype == Q8_F16 ? reinterpret_cast<float*>(space + sp.norm) : nullptr;
+  auto* rescale = reinterpret_cast<float*>(space + sp.powers);
+  auto* unscale = reinterpret_cast<float*>(space + sp.powers + q8::align_ws(static_cast<size_t>(M) * 4));
   auto* counts = reinterpret_cast<int32_t*>(space + sp.counts);
   const int count_words = static_cast<int>(sp.grads.counts / 4);
 
@@ -360,19 +375,31 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
   p.act = act;
   p.dh = dh;
   p.operand_out = reinterpret_cast<uint16_t*>(space + sp.grad_operand);
-  p.rescale = norm;
+  p.rescale = rescale;
   p.parts = reinterpret_cast<int32_t*>(space + sp.parts);
   p.counts = counts;
   q8::TileParams g = tile_params(M, K, K, inputs, sp.grads, packed_transposed);
   g.out = dx;
-  g.unscale = norm != nullptr ? norm + 1 : nullptr;
+  g.unscale = unscale;
   g.parts = p.parts;
   g.counts = counts + count_words;
 
-  cudaError_t e = cudaSuccess;
-  if (norm != nullptr) e = q8::launch_channel_norm(weight_scales, 2 * N, norm, cs(stream));
-  if (e == cudaSuccess)
-    e = make_operand(x_q, Q8_I8, M, K, nullptr, nullptr, space, counts, 2 * count_words, cs(stream));
+  q8::GatedGradFrontJob job{};
+  job.q = x_q;
+  job.scales = x_scales;
+  job.dh = dh;
+  job.ws = weight_scales;
+  job.bias = bias;
+  job.M = M;
+  job.N = N;
+  job.K = K;
+  job.operand = reinterpret_cast<uint16_t*>(space);
+  job.KB = p.KB;
+  job.rescale = rescale;
+  job.unscale = unscale;
+  job.counts = counts;
+  job.count_words = 2 * count_words;
+  cudaError_t e = q8::launch_gated_grad_front(job, dtype, cs(stream));
   if (e == cudaSuccess) e = q8::launch_tile_gated_grad(p, space, dtype, cs(stream));
   if (e == cudaSuccess) e = q8::launch_tile_grad(g, space + sp.grad_operand, dtype, cs(stream));
   return cuda_status(e);

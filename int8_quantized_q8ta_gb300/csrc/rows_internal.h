@@ -126,17 +126,16 @@ struct TileParams {
   const float* row_scale;   // [R]
   int act;                  // Activation of the gated forms
   const void* dh;           // [R, N] the gated output's gradient
-  uint16_t* operand_out;    // [2 NB][R][64] the gradient's operand
-  const float* rescale;     // what its values are multiplied by, and the sums
-  const float* unscale;     // after it: powers of two on the device, or null for 1
+  uint16_t* operand_out;    // [2 NB][R][64] the gradient's operand, f16
+  const float* rescale;     // [R] powers of two that its values are multiplied
+  const float* unscale;     // by, and the sums after it
 };
 cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
                              cudaStream_t s);
 
 // The forms for rows with a scale for each token (see TileForm): float outputs;
 // the gated ones take N output channels and NB blocks of 128 packed rows, two
-// rows a channel (see gated_rows); the last two f16 or bf16 alone, the very last
-// an operand of that type.
+// rows a channel (see gated_rows); the last two f16 or bf16 alone.
 enum Activation { kActNone, kActRelu, kActSilu, kActGelu };
 cudaError_t launch_tile_token(TileParams p, const void* operand, q8_dtype out_dtype,
                               cudaStream_t s);

@@ -3,7 +3,6 @@
 // A operand from tensor memory, int8 -> f16, bounded waits.
 #pragma once
 
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
@@ -21,18 +20,6 @@ __device__ __forceinline__ uint32_t biased_to_f16x2(uint32_t word, uint32_t sele
                                                     __half2 minus) {
   const uint32_t p = __byte_perm(word, kF16Base, selector);
   __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&p), minus);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-// The same into bf16, whose 8 bits hold 128 + (u & 127) but not 256 + u: a byte
-// under the high byte 0x43 gives, without its top bit, 128 + (u & 127), and, with
-// nothing but that bit turned over, 128 where w >= 0 and 256 where it is not.
-// Their difference is w, exactly.  Twice the instructions of f16.
-__device__ __forceinline__ uint32_t biased_to_bf16x2(uint32_t word, uint32_t selector) {
-  const uint32_t p = __byte_perm(word, 0x43434343u, selector);
-  const uint32_t low = p & 0xff7fff7fu, base = (p & 0xff80ff80u) ^ 0x00800080u;
-  __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low),
-                             *reinterpret_cast<const __nv_bfloat162*>(&base));
   return *reinterpret_cast<uint32_t*>(&h);
 }
 

@@ -51,6 +51,7 @@
 #include "row_split.h"
 #include "rows_internal.h"
 #include "tile_device.cuh"
+#include "token_device.cuh"
 
 namespace q8 {
 
@@ -87,10 +88,11 @@ constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
 //                   tokens brings them together (lane l takes one token,
 //                   l + 16 the other)
 //   kFormGatedGrad  the same g and u, then with dh their two gradients, each
-//                   times its channel's ws: the operand of the next kernel
-//   kFormGrad       rows already in 16-bit floats (OUT's type) times the
-//                   transposed weight: f32 sums instead of exact integers,
-//                   parts added in the order of their CTAs
+//                   times its channel's ws and its row's power of two, in f16:
+//                   the operand of the next kernel
+//   kFormGrad       such f16 rows times the transposed weight: f32 sums instead
+//                   of exact integers, parts added in the order of their CTAs,
+//                   the rows' powers of two taken out again
 enum TileForm { kFormBatch, kFormToken, kFormGated, kFormGatedGrad, kFormGrad };
 
 // What the kernels before this one write while it may already run (offsets,
@@ -449,38 +451,6 @@ __device__ __forceinline__ typename OutType<OUT>::type finish(float v, const Til
   }
 }
 
-// act(g), and with GRAD act'(g) too.  exp and the division are the fast ones (a
-// few units in the last place of f32); both run into 0 or infinity where the
-// sigmoid does.
-template <bool GRAD>
-__device__ __forceinline__ float activate(float g, int act, float& slope) {
-  if (act == kActSilu) {
-    const float sigma = __fdividef(1.0f, 1.0f + __expf(-g));
-    const float a = g * sigma;
-    if constexpr (GRAD) slope = fmaf(a, 1.0f - sigma, sigma);
-    return a;
-  }
-  if (act == kActGelu) {
-    const float phi = fmaf(0.5f, erff(g * 0.70710678f), 0.5f);
-    if constexpr (GRAD) slope = fmaf(g * 0.39894228f, __expf(-0.5f * g * g), phi);
-    return g * phi;
-  }
-  if constexpr (GRAD) slope = g > 0.0f ? 1.0f : 0.0f;
-  return max_nan(g, 0.0f);
-}
-
-// A 16-bit float of OUT's type.
-template <int OUT>
-__device__ __forceinline__ uint16_t to_half_bits(float v) {
-  if constexpr (OUT == Q8_F16) return __half_as_ushort(__float2half_rn(v));
-  else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-template <int OUT>
-__device__ __forceinline__ float from_half_bits(uint16_t v) {
-  if constexpr (OUT == Q8_F16) return __half2float(__ushort_as_half(v));
-  else return __uint_as_float(static_cast<uint32_t>(v) << 16);
-}
-
 // The epilogue of rows with a scale for each token: a warp's 32 channels and
 // `mine` columns from col0 on of one unit, whose sums acc holds.
 template <int OUT, int COLS, TileForm FORM>
@@ -504,9 +474,7 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
 #pragma unroll
   for (int j = 0; j < COLS; ++j) {
     const float s = __shfl_sync(0xffffffffu, j < 32 ? s0 : s1, j & 31);
-    float t = __fmul_rn(__int2float_rn(acc[j]), s);
-    t = __fmul_rn(t, ws);
-    acc[j] = __float_as_int(__fadd_rn(t, bias));
+    acc[j] = __float_as_int(token_value(acc[j], s, ws, bias));
   }
   // one address for the tile and 32-bit distances from it (a tile's rows span
   // less than 4 GB: N <= 2^24)
@@ -539,11 +507,11 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
         if (j < rows) *reinterpret_cast<T*>(base + off) = finish<OUT>(h, p);
       }
     } else {
-      // the gradients times their channels' scales, and those times a power of
-      // two that keeps them in f16's range (1 for bf16)
-      const float scale = p.rescale != nullptr ? *p.rescale : 1.0f;
+      // the gradients times their channels' scales and their rows' powers of two
+      const float r0 = p.rescale[at + min(lane, mine - 1)];
+      const float r1 = COLS > 32 ? p.rescale[at + min(lane + 32, mine - 1)] : 0.0f;
       const float ws_other = __shfl_xor_sync(0xffffffffu, ws, 16);
-      const float wg = (up ? ws_other : ws) * scale, wu = (up ? ws : ws_other) * scale;
+      const float wg = up ? ws_other : ws, wu = up ? ws : ws_other;
       const uint16_t* dh = static_cast<const uint16_t*>(p.dh) +
                            static_cast<int64_t>(at + mine_j) * p.N + n;
       // K-blocked, in the order of the packed rows: 64 a block
@@ -567,11 +535,12 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
           float g, u, slope;
           pair(j, g, u);
           const float a = activate<true>(g, p.act, slope);
-          const float v = from_half_bits<OUT>(d[i]);
+          const float r = __shfl_sync(0xffffffffu, j < 32 ? r0 : r1, (j & 31) + mine_j);
+          const float v = half_bits_to_float<OUT>(d[i]);
           if (j < rows) {
             // channels past the last hold zeros, whatever the rows' scales are
-            to[j * 64] = in ? to_half_bits<OUT>(v * u * slope * wg) : 0;
-            to[j * 64 + 16] = in ? to_half_bits<OUT>(v * a * wu) : 0;
+            to[j * 64] = in ? grad_bits(v * u * slope * wg * r) : 0;
+            to[j * 64 + 16] = in ? grad_bits(v * a * wu * r) : 0;
           }
         }
       }
@@ -587,7 +556,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using F = Form<PAIR>;
   constexpr int CG = F::CG, KD = F::KD, kCols = F::kCols;
   constexpr bool kBatch = FORM == kFormBatch, kFloat = FORM == kFormGrad;
-  constexpr bool kBf16 = kFloat && OUT == Q8_BF16;   // operands' type: bf16, else f16
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TileShared sh;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -794,7 +762,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int chunk = uniform(chunk_stages_of<KD, kFloat>(p));
       while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
         const uint32_t n16 = uniform((sg->rows + 15) & ~15);
-        const uint32_t idesc = kBf16 ? idesc_bf16_f32(128 * CG, n16) : idesc_f16(128 * CG, n16);
+        const uint32_t idesc = idesc_f16(128 * CG, n16);
         int kb = uniform(sg->kb0);
         const int kb1 = uniform(sg->kb1);
         const int stages = (kb1 - kb + KD - 1) / KD;
@@ -932,13 +900,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t q[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if constexpr (kBf16) {
-            r[c * 8 + j * 2] = biased_to_bf16x2(q[j], 0x4140);
-            r[c * 8 + j * 2 + 1] = biased_to_bf16x2(q[j], 0x4342);
-          } else {
-            r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
-            r[c * 8 + j * 2 + 1] = biased_to_f16x2(q[j], 0x4342, minus);
-          }
+          r[c * 8 + j * 2] = biased_to_f16x2(q[j], 0x4140, minus);
+          r[c * 8 + j * 2 + 1] = biased_to_f16x2(q[j], 0x4342, minus);
         }
       }
     };
@@ -1230,11 +1193,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const int n = nb * 128 + quarter * 32 + lane;
       const bool in = n < p.N;
-      if (kFloat && last) {
-        const float scale = p.unscale != nullptr ? *p.unscale : 1.0f;   // a power of two
+      if (kFloat && last && mine > 0) {
+        const int at = sg->row0 + col0;
+        const float s0 = p.unscale[at + min(lane, mine - 1)];
+        const float s1 = kCols > 32 ? p.unscale[at + min(lane + 32, mine - 1)] : 0.0f;
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
-          acc[j] = __float_as_int(__fmul_rn(__int_as_float(acc[j]), scale));
+          acc[j] = __float_as_int(__fmul_rn(
+              __int_as_float(acc[j]), __shfl_sync(0xffffffffu, j < 32 ? s0 : s1, j & 31)));
       }
       if (kBatch && last) {
         // In place from here on: registers beyond the sums are few, and what

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "q8ta.h"
+#include "rows_internal.h"
 #include "tile_device.cuh"
 
 namespace q8 {
@@ -23,6 +24,14 @@ template <int DT>
 __device__ __forceinline__ uint32_t float_to_half_bits(float v) {
   if constexpr (DT == Q8_F16) return __half_as_ushort(__float2half_rn(v));
   else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// All ones in each half of a word where its 16-bit float is above 0.  (Positive
+// numbers and infinity have encodings from 1 to infinity's; NaN's are above.)
+template <int DT>
+__device__ __forceinline__ uint32_t above_zero(uint32_t v) {
+  constexpr uint32_t kInf = DT == Q8_F16 ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpgts2(v, 0u) & __vcmpleu2(v, kInf);
 }
 
 template <int DT>
@@ -92,6 +101,53 @@ __device__ __forceinline__ uint4 token_f16x8(uint2 w) {
   w.y ^= 0x80808080u;
   return make_uint4(biased_to_f16x2(w.x, 0x4140, minus), biased_to_f16x2(w.x, 0x4342, minus),
                     biased_to_f16x2(w.y, 0x4140, minus), biased_to_f16x2(w.y, 0x4342, minus));
+}
+
+// v of one exact sum: the row's scale, the channel's, the bias, one rounding a
+// step.
+__device__ __forceinline__ float token_value(int32_t acc, float s, float ws, float b) {
+  return __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), s), ws), b);
+}
+
+// act(g), and with GRAD act'(g) too.  exp and the division are the fast ones (a
+// few units in the last place of f32); both run into 0 or infinity where the
+// sigmoid does.
+template <bool GRAD>
+__device__ __forceinline__ float activate(float g, int act, float& slope) {
+  if (act == kActSilu) {
+    const float sigma = __fdividef(1.0f, 1.0f + __expf(-g));
+    const float a = g * sigma;
+    if constexpr (GRAD) slope = fmaf(a, 1.0f - sigma, sigma);
+    return a;
+  }
+  if (act == kActGelu) {
+    const float phi = fmaf(0.5f, erff(g * 0.70710678f), 0.5f);
+    if constexpr (GRAD) slope = fmaf(g * 0.39894228f, __expf(-0.5f * g * g), phi);
+    return g * phi;
+  }
+  if constexpr (GRAD) slope = g > 0.0f ? 1.0f : 0.0f;
+  return max_nan(g, 0.0f);
+}
+// No |act'| is above this (silu's reaches 1.10, gelu's 1.13).
+constexpr float kSteepest = 1.25f;
+
+// Gradients go into their product as f16 numbers, whatever their type: 11 bits,
+// where bf16 has 8.  Each row is multiplied by a power of two that puts a bound
+// on its values between 2^14 and 2^15, so that f16's few exponents reach 29
+// powers of two below that bound, and the row's sums are divided by it again,
+// exactly.  (Beyond 2^126 either way the row keeps what f32 can do.)
+struct RowPower {
+  float rescale, unscale;
+};
+__device__ __forceinline__ RowPower row_power(float bound) {
+  const int exponent = static_cast<int>(__float_as_uint(bound) >> 23) & 255;
+  // (zeros, infinities and NaN: as they are)
+  const int e = exponent == 0 || exponent == 255 ? 0 : min(126, max(-126, 127 + 14 - exponent));
+  return {__uint_as_float(static_cast<uint32_t>(127 + e) << 23),
+          __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
+}
+__device__ __forceinline__ uint16_t grad_bits(float v) {
+  return __half_as_ushort(__float2half_rn(v));
 }
 
 // What a thread loads of a row at once: 8 values on 16-byte boundaries, or one.

@@ -158,85 +158,177 @@ __global__ void __launch_bounds__(256) dequantize_token_kernel(const int8_t* q,
 }
 
 // ---------------------------------------------------------------------------
-// Gradients.  A warp has 256 channels (their scales in registers) of several
-// rows, so that the scales are read once for them.
+// Gradients: rows of f16 for the product with the transposed weight, each under
+// a power of two of its own (see row_power).
 // ---------------------------------------------------------------------------
-constexpr int kGradRows = 16;
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// The largest of a CTA's threads' words, by every thread; `slots` is not used
+// again before the next barrier but one.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t (&slots)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (lane == 0) slots[warp] = v;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, lane < static_cast<int>(blockDim.x >> 5) ? slots[lane] : 0u);
+}
+
+// The largest magnitude of a CTA's share of n floats, four on a 16-byte
+// boundary at a time where they lie so.
+__device__ __forceinline__ uint32_t top_of(const float* v, int64_t n) {
+  uint32_t top = 0;
+  const int64_t head = min(n, static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(v) % 16) % 16 / 4));
+  if (threadIdx.x < head) top = magnitude(__ldg(v + threadIdx.x));
+  const auto* v4 = reinterpret_cast<const float4*>(v + head);
+  const int64_t n4 = (n - head) / 4;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < n4; i += blockDim.x) {
+    const float4 f = __ldg(v4 + i);
+    top = max(top, max(max(magnitude(f.x), magnitude(f.y)), max(magnitude(f.z), magnitude(f.w))));
+  }
+  const int64_t tail = head + n4 * 4 + threadIdx.x;
+  if (tail < n) top = max(top, magnitude(__ldg(v + tail)));
+  return top;
+}
+
+// A CTA has one row at a time in registers, 8 values an item and 4 items a
+// thread (longer rows are read a second time), and its items' scales with them.
+// With wn = ws over the power of two of the largest, |dy * wn| < 2 a.
 template <int DT, bool VEC, bool MASK>
-__global__ void __launch_bounds__(256) grad_operand_kernel(const GradOperandJob job) {
+__global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob job) {
+  constexpr int U = 4;
+  __shared__ uint32_t slots[3][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = t; i < job.count_words; i += step) job.counts[i] = 0;
-  const float rescale = job.rescale != nullptr ? *job.rescale : 1.0f;
-  const int64_t chunks = static_cast<int64_t>(job.KB) * 8, segs = (chunks + 31) / 32;
-  const int64_t groups = (job.M + kGradRows - 1) / kGradRows;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+       i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    job.counts[i] = 0;
+  const int64_t items = static_cast<int64_t>(job.KB) * 8;
   const auto* dy = static_cast<const uint16_t*>(job.dy);
   const auto* y = static_cast<const uint16_t*>(job.y);
-  for (int64_t u = t >> 5; u < groups * segs; u += step >> 5) {
-    const int64_t seg = u % segs, m0 = u / segs * kGradRows;
-    const int64_t c = seg * 32 + lane;
-    if (c >= chunks) continue;
-    float ws[8];
+  // (a power of two of the largest scale in [1, 2))
+  const RowPower channel = row_power(__uint_as_float(block_max(top_of(job.ws, job.N), slots[2])));
+  const float to_one = channel.rescale * 0x1p-14f, from_one = channel.unscale * 0x1p14f;
+  float held_ws[U][8];
+  const auto load_ws = [&](int64_t c, float (&ws)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) * rescale : 0.0f;
-    const int64_t m1 = min(job.M, m0 + kGradRows);
-    constexpr int U = 4;
-    for (int64_t m = m0; m < m1; m += U) {
-      uint4 v[U], w[U];
+    for (int j = 0; j < 8; ++j)
+      ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) * to_one : 0.0f;
+  };
+  const auto load = [&](int64_t m, int64_t c) {
+    uint4 v = load_halves<VEC>(dy, m * job.N, c * 8, job.N);
+    if constexpr (MASK) {
+      const uint4 a = load_halves<VEC>(y, m * job.N, c * 8, job.N);
+      v.x &= above_zero<DT>(a.x);
+      v.y &= above_zero<DT>(a.y);
+      v.z &= above_zero<DT>(a.z);
+      v.w &= above_zero<DT>(a.w);
+    }
+    return v;
+  };
+  const auto top16 = [&](uint4 v) {
+    const uint32_t t = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return magnitude(half_bits_to_float<DT>(max(t & 0xffffu, t >> 16)));
+  };
+  const auto put = [&](int64_t m, int64_t c, uint4 v, const float (&ws)[8], float rescale) {
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (m + i < m1) {
-          v[i] = load_halves<VEC>(dy, (m + i) * job.N, c * 8, job.N);
-          if constexpr (MASK) w[i] = load_halves<VEC>(y, (m + i) * job.N, c * 8, job.N);
-        }
+    for (int j = 0; j < 4; ++j)
+      r[j] = grad_bits(half_bits_to_float<DT>(d[j] & 0xffffu) * rescale * ws[2 * j]) |
+             (static_cast<uint32_t>(
+                  grad_bits(half_bits_to_float<DT>(d[j] >> 16) * rescale * ws[2 * j + 1]))
+              << 16);
+    *reinterpret_cast<uint4*>(job.dst + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
+        make_uint4(r[0], r[1], r[2], r[3]);
+  };
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (m + i < m1) {
-          const uint32_t d[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t r[4];
+  for (int u = 0; u < U; ++u) load_ws(threadIdx.x + static_cast<int64_t>(u) * blockDim.x, held_ws[u]);
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
+    uint4 held[U];
+    uint32_t top = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float lo = half_bits_to_float<DT>(d[j] & 0xffffu) * ws[2 * j];
-            float hi = half_bits_to_float<DT>(d[j] >> 16) * ws[2 * j + 1];
-            if constexpr (MASK) {
-              if (!(half_bits_to_float<DT>(a[j] & 0xffffu) > 0.0f)) lo = 0.0f;
-              if (!(half_bits_to_float<DT>(a[j] >> 16) > 0.0f)) hi = 0.0f;
-            }
-            r[j] = float_to_half_bits<DT>(lo) | (float_to_half_bits<DT>(hi) << 16);
-          }
-          *reinterpret_cast<uint4*>(job.dst + ((c >> 3) * job.M + m + i) * 64 + (c & 7) * 8) =
-              make_uint4(r[0], r[1], r[2], r[3]);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
+      held[u] = c < items ? load(m, c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = max(top, top16(held[u]));
+    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items; c += blockDim.x)
+      top = max(top, top16(load(m, c)));
+    // the row's largest between 2^13 and 2^14, times |wn| < 2
+    const RowPower row = row_power(2.0f * __uint_as_float(block_max(top, slots[turn])));
+    if (threadIdx.x == 0) job.unscale[m] = row.unscale * from_one;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
+      if (c < items) put(m, c, held[u], held_ws[u], row.rescale);
+    }
+    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items;
+         c += blockDim.x) {
+      float ws[8];
+      load_ws(c, ws);
+      put(m, c, load(m, c), ws, row.rescale);
     }
   }
 }
 
-// One CTA: a few thousand scales.
-__global__ void __launch_bounds__(1024) channel_norm_kernel(const float* __restrict__ ws, int64_t n,
-                                                            float* __restrict__ norm) {
-  __shared__ uint32_t tops[32];
+// The gated gradient's rows before g and u are known: |u| and |g| are below
+//   s[m] * 127 * 128 K * (largest ws) + (largest bias)
+// (of typical ones some 7 sqrt(K) times), |act| below |g|, |act'| below
+// kSteepest; so with the row's largest |dh| its operand has a bound.
+template <int DT, bool VEC_Q, bool VEC_DH>
+__global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFrontJob job) {
+  __shared__ uint32_t slots[6][32];
   pdl_wait();
   pdl_launch_dependents();
-  uint32_t top = 0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+       i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    job.counts[i] = 0;
+  float top[4];   // of the gate's and the up projection's scales, and of their biases
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* v = i < 2 ? job.ws : job.bias;
+    top[i] = v == nullptr ? 0.0f
+                          : __uint_as_float(block_max(top_of(v + (i & 1) * job.N, job.N), slots[i]));
+  }
+  const float most = 16384.0f * static_cast<float>(job.K);   // |sum| of int8 products
+  const auto* dh = static_cast<const uint16_t*>(job.dh);
+  const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8;
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
+    uint32_t t = 0;
 #pragma unroll 4
-  for (int64_t i = threadIdx.x; i < n; i += 1024)
-    top = max(top, __float_as_uint(ws[i]) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    top = __reduce_max_sync(0xffffffffu, tops[threadIdx.x]);
+    for (int64_t c = threadIdx.x; c < items; c += blockDim.x) {
+      const uint4 v = load_halves<VEC_DH>(dh, m * job.N, c * 8, job.N);
+      t = __vmaxu2(t, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+#pragma unroll 2
+    for (int64_t c = threadIdx.x; c < chunks; c += blockDim.x) {
+      const int8_t* src = job.q + m * job.K + c * 8;
+      uint2 w = make_uint2(0, 0);
+      if constexpr (VEC_Q) {
+        if (c * 8 < job.K) w = *reinterpret_cast<const uint2*>(src);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c * 8 + j < job.K)
+            (j < 4 ? w.x : w.y) |= static_cast<uint32_t>(static_cast<uint8_t>(src[j])) << (8 * (j & 3));
+      }
+      *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
+          token_f16x8(w);
+    }
+    const uint32_t most_dh =
+        block_max(magnitude(half_bits_to_float<DT>(max(t & 0xffffu, t >> 16))), slots[4 + turn]);
     if (threadIdx.x == 0) {
-      // zeros, infinities and NaN leave the scales as they are
-      const int exponent = static_cast<int>(top >> 23);
-      const int e = exponent == 0 || exponent == 255 ? 0 : min(max(exponent - 127, -100), 100);
-      norm[0] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      norm[1] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      const float acc = fabsf(job.scales[m]) * most;
+      const float g = fmaf(acc, top[0], top[2]), u = fmaf(acc, top[1], top[3]);
+      const RowPower row = row_power(__uint_as_float(most_dh) * kSteepest * fmaxf(u * top[0], g * top[1]));
+      job.rescale[m] = row.rescale;
+      job.unscale[m] = row.unscale;
     }
   }
 }
@@ -292,6 +384,13 @@ cudaError_t by_type(q8_dtype dt, bool vec, F&& f) {
   }
 }
 
+template <typename F>
+cudaError_t by_half(q8_dtype dt, bool vec, F&& f) {
+  const auto with = [&](auto t) { return vec ? f(t, std::true_type()) : f(t, std::false_type()); };
+  return dt == Q8_F16 ? with(std::integral_constant<int, Q8_F16>())
+                      : with(std::integral_constant<int, Q8_BF16>());
+}
+
 }  // namespace
 
 cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaStream_t s) {
@@ -325,21 +424,31 @@ cudaError_t launch_dequantize_token(const int8_t* q, const float* scales, int64_
 
 cudaError_t launch_grad_operand(const GradOperandJob& job, q8_dtype dtype, cudaStream_t s) {
   const bool vec = job.N % 8 == 0 && on16(job.dy) && on16(job.y);
-  const int64_t units = (job.M + kGradRows - 1) / kGradRows * ((job.KB * 8 + 31) / 32);
-  const int grid = blocks_for(std::max<int64_t>(units, (job.count_words + 31) / 32));
+  const int64_t items = static_cast<int64_t>(job.KB) * 8;
+  const int64_t each = job.M <= 2 * device_sm_count() ? 1 : 4;
+  const int threads = static_cast<int>(
+      std::min<int64_t>(512, std::max<int64_t>(64, round_up((items + each - 1) / each, 32))));
+  const int grid = static_cast<int>(
+      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * (1024 / threads)));
   const auto go = [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
-    return job.y != nullptr ? launch_pdl(grad_operand_kernel<DT, VEC, true>, grid, 256, 0, s, job)
-                            : launch_pdl(grad_operand_kernel<DT, VEC, false>, grid, 256, 0, s, job);
+    return job.y != nullptr ? launch_pdl(grad_operand_kernel<DT, VEC, true>, grid, threads, 0, s, job)
+                            : launch_pdl(grad_operand_kernel<DT, VEC, false>, grid, threads, 0, s, job);
   };
-  const auto with = [&](auto t) { return vec ? go(t, std::true_type()) : go(t, std::false_type()); };
-  return dtype == Q8_F16 ? with(std::integral_constant<int, Q8_F16>())
-                         : with(std::integral_constant<int, Q8_BF16>());
+  return by_half(dtype, vec, go);
 }
 
-cudaError_t launch_channel_norm(const float* ws, int64_t n, float* norm, cudaStream_t s) {
-  return launch_pdl(channel_norm_kernel, 1, 1024, 0, s, ws, n, norm);
+cudaError_t launch_gated_grad_front(const GatedGradFrontJob& job, q8_dtype dtype, cudaStream_t s) {
+  const bool vec_dh = job.N % 8 == 0 && on16(job.dh);
+  const bool vec_q = job.K % 8 == 0 && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
+  const int grid = static_cast<int>(std::min<int64_t>(job.M, device_sm_count() * 2));
+  return by_half(dtype, vec_dh, [&](auto t, auto v) {
+    constexpr int DT = decltype(t)::value;
+    constexpr bool VEC = decltype(v)::value;
+    return vec_q ? launch_pdl(gated_grad_front_kernel<DT, true, VEC>, grid, 512, 0, s, job)
+                 : launch_pdl(gated_grad_front_kernel<DT, false, VEC>, grid, 512, 0, s, job);
+  });
 }
 
 cudaError_t launch_pack_gated(const int8_t* gate, const int8_t* up, int64_t N, int64_t K,

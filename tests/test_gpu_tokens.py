@@ -320,7 +320,7 @@ def test_gated_gradient(dtype, act, M, N, K):
     w, ws, b = weights(N, 2, N, K, lo=-128)
     b = b if N % 2 else None
     g, u = (ref.product(q, xs, w[i], ws[i], None if b is None else b[i]) for i in (0, 1))
-    want, bound = ref.gated_grad(dh, g, u, w, ws, act)
+    want, bound = ref.gated_grad(dh, g, u, w, ws, act, xs, b)
     packed = q8.pack_gated_weight(w[0].to(DEV), w[1].to(DEV))
     packed_t = q8.pack_gated_weight_t(w[0].to(DEV), w[1].to(DEV))
     args = (dh.to(DEV), q.to(DEV), xs.to(DEV), packed, packed_t, ws.to(DEV), None if b is None else b.to(DEV))
@@ -337,6 +337,7 @@ def test_gradients_of_small_and_uneven_scales(M):
     dy = rows(M, M, N, torch.float16)
     w, ws, _ = weights(3, 2, N, K)
     q, xs = ref.quantize(rows(M, M, K))
+    # (and of the gradients themselves, where the type can hold them)
     for factor in (2.0 ** -20, 2.0 ** 12):
         s = ws * factor
         s[:, ::7] *= 2.0 ** -3
@@ -344,6 +345,25 @@ def test_gradients_of_small_and_uneven_scales(M):
         dx = q8.linear_per_token_backward(dy.to(DEV), q8.pack_tile_weight(w[0].t().contiguous().to(DEV)),
                                           s[0].contiguous().to(DEV))
         within(dx, want, bound)
+
+
+@pytest.mark.parametrize("M", [4, 80])
+@pytest.mark.parametrize("power", [-100, -60, 60, 90])
+def test_gradients_of_far_sizes(M, power):
+    # bfloat16 gradients of rows of very different size
+    N, K = 140, 200
+    dy = (rows(M, M, N) * 2.0 ** (power + torch.arange(M).float()[:, None] / 4)).bfloat16()
+    w, ws, b = weights(3, 2, N, K)
+    q, xs = ref.quantize(rows(M, M, K))
+    want, bound = ref.linear_grad(dy, w[0], ws[0])
+    dx = q8.linear_per_token_backward(dy.to(DEV), q8.pack_tile_weight(w[0].t().contiguous().to(DEV)),
+                                      ws[0].contiguous().to(DEV))
+    within(dx, want, bound)
+    g, u = (ref.product(q, xs, w[i], ws[i], b[i]) for i in (0, 1))
+    want, bound = ref.gated_grad(dy, g, u, w, ws, "silu", xs, b)
+    dx = q8.linear_gated_backward(dy.to(DEV), q.to(DEV), xs.to(DEV), q8.pack_gated_weight(w[0].to(DEV), w[1].to(DEV)),
+                                  q8.pack_gated_weight_t(w[0].to(DEV), w[1].to(DEV)), ws.to(DEV), b.to(DEV))
+    within(dx, want, bound)
 
 
 def test_channels_past_the_last_take_no_part():
@@ -381,7 +401,7 @@ def test_gated_gradient_against_differences(act):
                                   q8.pack_gated_weight_t(w[0].to(DEV), w[1].to(DEV)), ws.to(DEV), b.to(DEV),
                                   activation=act).cpu().double()
     g, u = (ref.product(q, xs, w[i], ws[i], b[i]) for i in (0, 1))
-    bound = ref.gated_grad(dh, g, u, w, ws, act)[1]
+    bound = ref.gated_grad(dh, g, u, w, ws, act, xs, b)[1]
     gen = torch.Generator().manual_seed(7)
     for _ in range(8):
         d = torch.randn(M, K, generator=gen, dtype=torch.float64)
@@ -431,7 +451,7 @@ def test_a_block_and_its_gradient(dtype, M):
     g, u = (ref.product(qc, xc, block.w1[i], block.ws1[i], block.b1[i]) for i in (0, 1))
     within(h, *ref.gated(g, u, "silu", dtype))
     within(dh, *ref.linear_grad(dy.cpu(), block.w2, block.ws2))
-    within(dx, *ref.gated_grad(dh.cpu(), g, u, block.w1, block.ws1, "silu"))
+    within(dx, *ref.gated_grad(dh.cpu(), g, u, block.w1, block.ws1, "silu", xc, block.b1))
 
 
 def test_relu_product_is_recorded():
@@ -493,7 +513,7 @@ def test_refusals_of_the_binding():
         (TypeError, lambda: q8.dequantize_per_token(q, s, out_dtype=torch.int8)),
         (ValueError, lambda: q8.dequantize_per_token(q, s[:3])),
         (ValueError, lambda: q8.pack_gated_weight(wd[0], wd[1][:80].contiguous())),
-        (ValueError, lambda: q8.linear_per_token(x.detach(), None, workspace=torch.empty(256, dtype=torch.uint8, device=DEV), **one)),
+        (ValueError, lambda: q8.linear_per_token(torch.cat([x.detach()] * 3), None, workspace=torch.empty(256, dtype=torch.uint8, device=DEV), **one)),
     ]
     for error, call in refused:
         with pytest.raises(error):

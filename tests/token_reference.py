@@ -67,19 +67,15 @@ def gated(g, u, act, dtype):
     return h, err * 1.01 + h.abs() * HALF_ULP[dtype] * 1.01 + least
 
 
-def grad_bound(terms, extra, n, dx, dtype, wsum, ws):
+def grad_bound(terms, extra, n, dx, dtype, floor):
     """How far a gradient may be off: `terms` sum |operand| |w| in 64 bits,
     `extra` the same of the operands' errors before they are rounded, n
-    operands a sum.
+    operands a sum, `floor` what the smallest operands lose.
 
-    An operand is rounded to the type (half a unit), in f16 to no less than
-    2^-25 of the largest scale's power of two; the f32 sums of 16 products each
-    lose at most four units of the sum of magnitudes a step."""
-    err = terms * (HALF_ULP[dtype] + 2.0 ** -22 + (n / 16 + 8) * 2.0 ** -22) + extra
-    if dtype is torch.float16:
-        top = float(ws.abs().max())
-        e = math.floor(math.log2(top)) if top > 0 and math.isfinite(top) else 0
-        err = err + 2.0 ** (-25 + e) * wsum * 1.01
+    An operand is rounded to f16 (2^-11 of itself, or 2^-25 of its row's power
+    of two, which is at most 2^-13 of the row's bound); the f32 sums of 16
+    products each lose at most four units of the sum of magnitudes a step."""
+    err = terms * (2.0 ** -11 + 2.0 ** -22 + (n / 16 + 8) * 2.0 ** -22) + extra + floor
     least = 2.0 ** -25 if dtype is torch.float16 else 2.0 ** -133
     return err * 1.01 + dx.abs() * HALF_ULP[dtype] * 1.01 + least
 
@@ -91,10 +87,12 @@ def linear_grad(dy, w, ws, y=None):
         d = torch.where(y > 0, d, torch.zeros((), dtype=torch.float64))
     t, w64 = d * ws.double(), w.double()
     dx = t @ w64
-    return dx, grad_bound(t.abs() @ w64.abs(), 0.0, w.shape[0], dx, dy.dtype, w64.abs().sum(0), ws)
+    bound = d.abs().amax(1, keepdim=True) * ws.double().abs().max()
+    return dx, grad_bound(t.abs() @ w64.abs(), 0.0, w.shape[0], dx, dy.dtype,
+                          2.0 ** -37 * bound * w64.abs().sum(0))
 
 
-def gated_grad(dh, g, u, w, ws, act):
+def gated_grad(dh, g, u, w, ws, act, xs, b=None):
     """(dx in 64 bits, its bound) from the f32 g and u."""
     a, slope = act64(g, act)
     ea, es = act_error(g, act)
@@ -103,6 +101,13 @@ def gated_grad(dh, g, u, w, ws, act):
     dx = tg @ w64[0] + tu @ w64[1]
     terms = tg.abs() @ w64[0].abs() + tu.abs() @ w64[1].abs()
     extra = (d * u64 * es * ws64[0]).abs() @ w64[0].abs() + (d * ea * ws64[1]).abs() @ w64[1].abs()
-    # (two more products in f32 before the operand's own rounding)
-    extra = extra + terms * 2.0 ** -22
-    return dx, grad_bound(terms, extra, 2 * w.shape[1], dx, dh.dtype, w64.abs().sum((0, 1)), ws)
+    # (three more products in f32 before the operand's own rounding)
+    extra = extra + terms * 2.0 ** -21
+    # the row's bound, from the largest sum, scales and biases
+    top = ws64.abs().amax(1)
+    most = xs.double().abs()[:, None] * 16384 * w.shape[2]
+    bias = torch.zeros(2, dtype=torch.float64) if b is None else b.double().abs().amax(1)
+    bound = d.abs().amax(1, keepdim=True) * 1.25 * torch.maximum((most * top[1] + bias[1]) * top[0],
+                                                                 (most * top[0] + bias[0]) * top[1])
+    return dx, grad_bound(terms, extra, 2 * w.shape[1], dx, dh.dtype,
+                          2.0 ** -38 * bound * w64.abs().sum((0, 1)))
