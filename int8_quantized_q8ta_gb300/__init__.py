@@ -190,7 +190,9 @@ def lib() -> ctypes.CDLL:
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(lib(), name)
+        f = getattr(lib(), name)
+        setattr(self, name, f)   # found here from the next call on
+        return f
 
 
 _lib = _LazyLib()

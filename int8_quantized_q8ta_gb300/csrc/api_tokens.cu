@@ -33,14 +33,16 @@ int parse_gate(const char* a) {
   return -1;
 }
 
+constexpr int kMinRun = 4;   // k-blocks of a run at least
+
 // The operand, parts and counts of a contraction, then the rows' scales.
 struct TokenSpace {
   TilePlan plan;
   size_t scales, total;
 };
-TokenSpace token_space(int64_t M, int64_t K) {
+TokenSpace token_space(int64_t M, int64_t N, int64_t K) {
   TokenSpace t{};
-  t.plan = plan_tiles(M, K, 1);
+  t.plan = plan_group(M, N, K, kMinRun);
   t.scales = t.plan.total;
   t.total = t.scales + q8::align_ws(static_cast<size_t>(M) * 4);
   return t;
@@ -62,8 +64,8 @@ struct GradSpace {
 };
 GradSpace gated_grad_space(int64_t M, int64_t N, int64_t K) {
   GradSpace t{};
-  t.rows = plan_tiles(M, K, 1);
-  t.grads = plan_tiles(M, gated_inputs(N), 1);
+  t.rows = plan_group(M, q8::gated_rows(N), K, kMinRun);
+  t.grads = plan_group(M, K, gated_inputs(N), kMinRun);
   t.grad_operand = t.rows.operand;
   t.parts = t.grad_operand + t.grads.operand;
   t.counts = t.parts + t.grads.parts;
@@ -83,7 +85,7 @@ q8::TileParams tile_params(int64_t M, int64_t N, int64_t rows, int64_t K, const 
   p.TN = plan.TN;
   p.max_tiles = static_cast<int>(max_tiles(M, 1, plan));
   p.grid = plan.grid;
-  p.min_run = 4;
+  p.min_run = kMinRun;
   p.w = static_cast<const uint8_t*>(packed);
   p.w_bound = reinterpret_cast<const int32_t*>(p.w + tile_weight_bytes(1, rows, K));
   p.a_bound = a_bound_of(0);
@@ -158,7 +160,7 @@ q8_status token_product(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, i
     job.out = out;
     return cuda_status(q8::launch_token_rows(job, gated, s));
   }
-  const TokenSpace sp = token_space(M, K);
+  const TokenSpace sp = token_space(M, rows, K);
   if (!units_ok(M, 1, rows, K, sp.plan)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
@@ -217,7 +219,7 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
 // ---- products with scales for each token and channel ------------------------
 size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K) || q8::token_rows_fit(M, K)) return 0;
-  return token_space(M, K).total;
+  return token_space(M, N, K).total;
 }
 
 q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,
@@ -239,7 +241,7 @@ q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_
 
 size_t q8_linear_per_token_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || !rows_ok(M, N) || !tile_sizes_ok(1, K, N)) return 0;
-  return token_space(M, N).total;
+  return token_space(M, K, N).total;
 }
 
 q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M, int64_t N,
@@ -254,7 +256,7 @@ q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M
   if (!aligned(dy, 2) || !aligned(y, 2) || !aligned(dx, 2) || !aligned(weight_scales, 4) ||
       !aligned(packed_transposed, q8::kWorkspaceAlign))
     return Q8_ERR_ALIGN;
-  const TokenSpace sp = token_space(M, N);
+  const TokenSpace sp = token_space(M, K, N);
   if (!units_ok(M, 1, K, N, sp.plan)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
@@ -312,7 +314,7 @@ q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, 
 
 size_t q8_linear_gated_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || q8::token_rows_fit(M, K)) return 0;
-  return token_space(M, K).total;
+  return token_space(M, q8::gated_rows(N), K).total;
 }
 
 q8_status q8_linear_gated(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,

@@ -82,6 +82,7 @@ cudaError_t launch_expert_combine_bwd(const void* dy, const void* z, q8_dtype dt
 
 // ---- grouped int8 contraction (tile_gemm.cu, tile_prep.cu) -----------------
 constexpr int kMaxTileRows = 192;       // rows of one tile: two accumulators fit TMEM
+constexpr int kMaxNarrowRows = 64;   // of the form of one CTA
 constexpr int kMaxByRow = 64;           // rows of a tile whose adapter terms go row by row
 constexpr int kTileEpiWarps = 12;       // epilogue warps at most
 constexpr int kTilePartWords = kMaxTileRows * 128;   // int32 words of one CTA's part of a unit
@@ -93,6 +94,18 @@ constexpr int kMaxRank = 256;
 __host__ __device__ inline int tile_rows(int count, int tiles) {
   return ((count + tiles - 1) / tiles + 15) & ~15;
 }
+
+// Whole units to each CTA while that lengthens the longest run by no more than
+// this many k-blocks over equal runs, which cut units and then join their
+// parts (5,000 to 10,000 cycles a join, against 350 a narrow k-block and 400 a
+// wide one; a run across two units joins twice).  Measured, whole against cut,
+// K 4096: 64 rows x 11008 (27 k-blocks more) 19.9 against 22.9 us, x 28672 (33)
+// 31.6 against 34.4, x 8192 (37) 19.0 against 18.7, 8 rows x 22016 (55) 26.8
+// against 26.0, x 6144 (43) 16.9 against 15.1; wide, 192 rows x 11008 (27) 27.3
+// against 37.2, 100 rows x 4096 (37) 24.9 against 22.3.  With adapters row by
+// row a second unit's terms are made once its first is joined, and whole units
+// win further: 8 and 64 rows x 22016 25.8 against 28.4 and 44 against 50.
+constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
 
 struct TileParams {
   int R, N, NB, KB;         // rows, output channels, blocks of 128 of them, k-blocks of 64

@@ -67,18 +67,6 @@ constexpr int kTmemCols = 512;
 // Stages of A operands in tensor memory, behind the accumulators.
 constexpr int NAb = 2, NA = 1 << NAb;
 
-// Whole units to each CTA while that lengthens the longest run by no more than
-// this many k-blocks over equal runs, which cut units and then join their
-// parts (5,000 to 10,000 cycles a join, against 350 a narrow k-block and 400 a
-// wide one; a run across two units joins twice).  Measured, whole against cut,
-// K 4096: 64 rows x 11008 (27 k-blocks more) 19.9 against 22.9 us, x 28672 (33)
-// 31.6 against 34.4, x 8192 (37) 19.0 against 18.7, 8 rows x 22016 (55) 26.8
-// against 26.0, x 6144 (43) 16.9 against 15.1; wide, 192 rows x 11008 (27) 27.3
-// against 37.2, 100 rows x 4096 (37) 24.9 against 22.3.  With adapters row by
-// row a second unit's terms are made once its first is joined, and whole units
-// win further: 8 and 64 rows x 22016 25.8 against 28.4 and 44 against 50.
-constexpr int kJoinNarrow = 36, kJoinWide = 28, kJoinByRow = 60;
-
 // What one kernel computes of its sums.
 //   kFormBatch      one activation scale for the batch, groups, adapters
 //   kFormToken      v = ((float)acc * s[row]) * ws[n] + b[n]
@@ -129,6 +117,7 @@ struct Form {
   static constexpr int kFirstEpi = kFirstConv + kConv;
   static_assert(32 * (kFirstEpi + kEpi) == kTileThreads, "one block size");
   static constexpr int kMaxRows = kCols * kEpi / 4;
+  static_assert(kMaxRows == (PAIR ? kMaxTileRows : kMaxNarrowRows), "tile heights");
   // accumulators, A operands, and row by row the adapters' terms
   static_assert(kAcc * kMaxRows + NA * KD * 32 + (PAIR ? 0 : kMaxRows) <= kTmemCols, "TMEM");
   // int32 words of one CTA's part of a unit

@@ -44,6 +44,49 @@ inline TilePlan plan_tiles(int64_t R, int64_t K, int64_t E, int64_t max_rows = q
   return t;
 }
 
+// The tile height of one group of R rows, N packed rows and K inputs: of a few
+// heights the one whose slowest CTA (or pair) is done first, by the split that
+// the kernel's Walk makes of it.  Low tiles make more units, which a few rows
+// need to fill the GPU without cutting units (a join costs 4 us and more); high
+// ones read the weights less often, and stay where a lower one gains less than 4%.
+// The constants (ns: the launches, a k-block, a unit's epilogue, a join and its
+// parts) were fitted to 144 problems of 70 to 2000 rows and each form, to 5%; the
+// choice is then within 1% of the best of twelve heights (12% at worst), where
+// full tiles take 18% longer (2.4 times at worst: 70 rows, 5000 inputs, 512
+// outputs 22.7 us against 12.0).
+inline int64_t tile_time(int64_t R, int64_t N, int64_t K, int TN, int grid, int min_run) {
+  const bool wide = TN > q8::kMaxNarrowRows;
+  const int64_t ctas = std::max(1, wide ? grid / 2 : grid), KB = (K + 63) / 64;
+  const int64_t blocks = (N + 127) / 128, tiles = (R + TN - 1) / TN;
+  const int64_t rows = ((R + tiles - 1) / tiles + 15) / 16 * 16;
+  const int64_t units = tiles * (wide ? (blocks + 1) / 2 : blocks), full = units / ctas;
+  const int64_t waves = units == full * ctas ? full : std::max<int64_t>(full - 1, 0);
+  const int64_t rest = units - waves * ctas, total = rest * KB;
+  int64_t line = 0, ends = 0, parts = 0;   // k-blocks, units and parts to join
+  if (rest > 0) {
+    const bool few = 2 * rest <= ctas;
+    const int64_t whole = (rest + ctas - 1) / ctas * KB;
+    int64_t q = std::max<int64_t>(min_run, (total - 1) / ctas + 1);
+    if (whole <= q + (wide ? q8::kJoinWide : q8::kJoinNarrow)) q = whole;
+    ends = std::max<int64_t>(1, (q + KB - 1) / KB);
+    if (few && q < KB) {
+      const int64_t share = std::max<int64_t>(1, std::min(ctas / rest, KB / std::max(1, min_run)));
+      line = (KB + share - 1) / share;
+      ends = 1;
+      parts = share > 1 ? share : 0;
+    } else {
+      line = std::min(q, total);
+      if (q % KB != 0 && q < total) parts = (KB + q - 1) / q + 1;
+    }
+  }
+  const int64_t join = parts * rows * 9;
+  if (wide)
+    return 6400 + (waves * KB + line) * (190 + rows * 3 / 10) + (waves + ends) * (2300 + 11 * rows) +
+           (parts > 0 ? 4300 + join : 0);
+  return 5600 + (waves * KB + line) * (108 + rows * 4 / 10) + (waves + ends) * (1300 + 5 * rows) +
+         (parts > 0 ? 3900 + join : 0);
+}
+
 // Row tiles that R rows in E groups need at most.
 inline int64_t max_tiles(int64_t R, int64_t E, const TilePlan& t) { return R / t.TN + std::min(E, R); }
 
@@ -51,6 +94,25 @@ inline int64_t max_tiles(int64_t R, int64_t E, const TilePlan& t) { return R / t
 inline bool units_ok(int64_t R, int64_t E, int64_t N, int64_t K, const TilePlan& t) {
   const int64_t tiles = max_tiles(R, E, t), blocks = (N + 127) / 128, kbs = (K + 63) / 64;
   return mul_ok(blocks, kbs) && mul_ok(tiles, blocks * kbs) && tiles * blocks * kbs <= INT32_MAX;
+}
+
+// A plan of one group, by tile_time.
+inline TilePlan plan_group(int64_t R, int64_t N, int64_t K, int min_run) {
+  TilePlan t = plan_tiles(R, K, 1);
+  const int full = t.TN;   // as high as there are rows for
+  int64_t best = INT64_MAX;
+  TilePlan c = t;
+  for (const int height : {full, 192, 160, 64, 48, 32, 16}) {
+    if (height > full) continue;
+    c.TN = height;
+    if (!units_ok(R, 1, N, K, c)) continue;
+    const int64_t time = tile_time(R, N, K, height, t.grid, min_run);
+    if (best == INT64_MAX || time < best / 100 * 96) {
+      best = time;
+      t.TN = height;
+    }
+  }
+  return t;
 }
 
 }  // namespace q8api

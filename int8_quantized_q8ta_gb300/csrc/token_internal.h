@@ -60,9 +60,9 @@ struct GatedGradFrontJob {
 };
 cudaError_t launch_gated_grad_front(const GatedGradFrontJob& job, q8_dtype dtype, cudaStream_t s);
 
-// Products of up to kFewRows rows in one launch without a workspace
-// (token_rows.cu), where their int8 copies fit shared memory.
-constexpr int kFewRows = 16;
+// Products of up to kFewRows short rows in one launch without a workspace
+// (token_rows.cu; token_rows_fit says which).
+constexpr int kFewRows = 8;
 struct TokenRowsJob {
   const void* x;        // [M, K] of x_dtype
   q8_dtype x_dtype;

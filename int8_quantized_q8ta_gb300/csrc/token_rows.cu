@@ -5,24 +5,27 @@
 //   acc[m, n] = sum_k q[m, k] w[n, k]   exact in int32
 //   v = ((float)acc * s[m]) * ws[n] + b[n];   gated: act(v_gate) * v_up
 //
-// Up to 16 rows a weight's 1 byte costs more than its 2 to 32 operations, so
-// bytes in flight count.  A CTA of 16 warps takes units of 32 packed rows (32
-// channels, or 16 of both halves of a gated pair); its warps share a unit's
-// k-blocks, and each has its next two k-blocks' weights on their way in
-// registers (4 KB a warp, 64 KB an SM; 44 bytes a nanosecond and SM at the copy
-// rate with 800 ns of latency want 35).  They run on across units, and the first
-// ones are asked for before the kernel before this one is done (a packed weight
-// is written at load time).
-//   Weights go from memory to registers to m16n8k16 MMAs, f16 in and f32 out:
-// packed 16-byte chunks are a thread's fragments as they lie (the order of a
-// sum's terms is free, so thread t of four takes inputs 16 t to 16 t + 15 of a
-// k-block), turned into f16 by a byte permute and half a subtraction a value.
-// Rows are the MMAs' 8 columns; int8, biased alike, in shared memory.  Products
-// are at most 2^14 and a chunk of 8 k-blocks adds 512 of them, so its f32 sums
-// are exact integers; they are then added up in int32, across warps too, so the
-// order does not matter.
+// Up to 8 rows a weight's 1 byte costs more than its 2 to 16 operations, so
+// bytes in flight count.  A CTA of 16 warps takes units of 16 packed rows (16
+// channels, or 8 of both halves of a gated pair); the warps share a unit's
+// inputs, eight 16-byte loads ahead each (64 KB a CTA, two CTAs an SM; 44 bytes
+// a nanosecond and SM at the copy rate with 800 ns of latency want 35).  They run
+// on across units, and the first ones are asked for before the kernel before
+// this one is done (a packed weight is written at load time).  1 row x 11008 x
+// 4096 10.2 us (floor 6.8), the gated pair 4096 x 11008 18.2 us (13.6), in a run
+// of calls.
+//   One or two rows: four products a dp4a, straight from the registers that the
+// loads fill; the rows' int8 come from shared memory, 16 bytes that half a warp
+// shares.  That is one load from there for each of memory, an SM can do two, so
+// three to eight rows go through m16n8k16 MMAs, f16 in and f32 out: the packed
+// 16-byte chunks are a thread's fragments as they lie (the order of a sum's terms
+// is free, so thread t of four takes inputs 16 t to 16 t + 15 of a k-block),
+// turned into f16 by a byte permute and half a subtraction a value, and rows are
+// the MMA's 8 columns.  Products are at most 2^14 and a chunk of 8 k-blocks adds
+// 512 of them, so its f32 sums are exact integers; they are then added up in
+// int32, across warps too, so the order does not matter.
 //   Every CTA quantizes all rows for itself (one row of 4096 is 8 KB from L2,
-// beside 131 KB of weights for each unit): that saves a launch, and the scales
+// beside 65 KB of weights for each unit): that saves a launch, and the scales
 // and int8 rows that the caller wants are written by the first CTA.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,8 +41,16 @@ namespace q8 {
 namespace {
 
 constexpr int kRowWarps = 16, kRowThreads = kRowWarps * 32;
-constexpr int kAhead = 2;         // k-blocks of weights in flight a warp
+constexpr int kAhead = 8;         // 16-byte loads in flight a thread
 constexpr int kExactBlocks = 8;   // k-blocks of one exact f32 chunk
+
+__device__ __forceinline__ uint4 load_weights(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -51,238 +62,259 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 
 struct RowsShared {
-  uint32_t top[kFewRows];
+  uint32_t top[kRowWarps];   // each warp's
   float scale[kFewRows];
 };
 
-// All rows as biased int8 in shared memory, zeros (0x80) from K on; their
-// scales, and for the first CTA what the caller wants of both.  Warps share the
-// rows: a few warps a row while there are more warps than rows, else rows in
-// turn.
-template <int DT, bool VEC>
+// All rows as int8 in shared memory, zeros from K on, biased by 128 under BIAS;
+// their scales, and for the first CTA what the caller wants of both.  A warp has
+// one row, alone or with others while there are more warps than rows, and keeps
+// the first items of its share in registers while the row's scale is found.
+template <int DT, bool VEC, bool BIAS>
 __device__ __forceinline__ void stage_rows(const TokenRowsJob& job, RowsShared& sh, uint8_t* rows) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int M = static_cast<int>(job.M);
-  const int each = max(1, kRowWarps / M);             // warps a row
-  const int first = warp / each, part = (warp % each) * 32 + lane, step = each * 32;
-  const int row_step = max(1, kRowWarps / each);
+  const int each = kRowWarps / M, m = warp / each;   // warps a row
+  const int part = (warp - m * each) * 32 + lane, step = each * 32;
   const int padded = job.KB * 64;
+  const bool mine = m < M;
+  constexpr uint32_t kFlip = BIAS ? 0x80808080u : 0;
+  const int64_t base = static_cast<int64_t>(mine ? m : 0) * job.K;
+  uint8_t* dst = rows + (mine ? m : 0) * job.stride;
   if constexpr (DT == Q8_I8) {
     if (threadIdx.x < M) sh.scale[threadIdx.x] = job.scales[threadIdx.x];
-    const auto* x = static_cast<const int8_t*>(job.x);
-    for (int m = first; m < M; m += row_step) {
-      const int8_t* src = x + static_cast<int64_t>(m) * job.K;
-      uint8_t* dst = rows + m * job.stride;
+    const int8_t* src = static_cast<const int8_t*>(job.x) + base;
+    if (mine) {
       if constexpr (VEC) {
 #pragma unroll 4
         for (int c = part; c < padded / 16; c += step) {
           uint4 v = c * 16 < job.K ? *reinterpret_cast<const uint4*>(src + c * 16)
                                    : make_uint4(0, 0, 0, 0);
-          v.x ^= 0x80808080u;
-          v.y ^= 0x80808080u;
-          v.z ^= 0x80808080u;
-          v.w ^= 0x80808080u;
+          v.x ^= kFlip;
+          v.y ^= kFlip;
+          v.z ^= kFlip;
+          v.w ^= kFlip;
           *reinterpret_cast<uint4*>(dst + c * 16) = v;
         }
       } else {
 #pragma unroll 4
         for (int k = part; k < padded; k += step)
-          dst[k] = k < job.K ? static_cast<uint8_t>(src[k]) ^ 0x80 : 0x80;
+          dst[k] = (k < job.K ? static_cast<uint8_t>(src[k]) : 0) ^ static_cast<uint8_t>(kFlip);
       }
     }
   } else {
     using Item = TokenItem<DT, VEC>;
-    constexpr int W = Item::kWidth;
-    const int items = static_cast<int>(job.K) / W;
-    if (threadIdx.x < kFewRows) sh.top[threadIdx.x] = 0;
-    __syncthreads();
-    for (int m = first; m < M; m += row_step) {
-      const int64_t base = static_cast<int64_t>(m) * job.K;
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int c = part; c < items; c += step) {
-        Item it;
-        it.load(job.x, base + c * W);
-        top = max(top, it.top());
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) atomicMax(&sh.top[m], top);
-    }
-    __syncthreads();
-    if (threadIdx.x < M) {
-      const float s = token_scale(sh.top[threadIdx.x]).scale;
-      sh.scale[threadIdx.x] = s;
-      if (blockIdx.x == 0 && job.scales != nullptr) job.scales[threadIdx.x] = s;
-    }
-    for (int m = first; m < M; m += row_step) {
-      const int64_t base = static_cast<int64_t>(m) * job.K;
-      const float inv = token_scale(sh.top[m]).inv;
-      uint8_t* dst = rows + m * job.stride;
-#pragma unroll 4
-      for (int c = part; c < items; c += step) {
-        Item it;
-        it.load(job.x, base + c * W);
-        if constexpr (VEC) {
-          uint2 q = it.quantize(inv);
-          if (blockIdx.x == 0 && job.q != nullptr) {
-            // (the caller's rows may lie on any byte)
-            int8_t* to = job.q + base + c * 8;
+    constexpr int W = Item::kWidth, U = DT == Q8_F32 && VEC ? 2 : 3;
+    const int items = mine ? static_cast<int>(job.K) / W : 0;
+    Item held[U];
+    uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              to[j] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-          }
-          q.x ^= 0x80808080u;
-          q.y ^= 0x80808080u;
-          *reinterpret_cast<uint2*>(dst + c * 8) = q;
-        } else {
-          const int8_t q = it.quantize(inv);
-          if (blockIdx.x == 0 && job.q != nullptr) job.q[base + c] = q;
-          dst[c] = static_cast<uint8_t>(q) ^ 0x80;
-        }
-      }
-      for (int k = static_cast<int>(job.K) + part; k < padded; k += step) dst[k] = 0x80;
+    for (int u = 0; u < U; ++u) {
+      const int c = part + u * step;
+      if (c < items) held[u].load(job.x, base + c * W);
+      else held[u].zero();
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = max(top, held[u].top());
+#pragma unroll 2
+    for (int c = part + U * step; c < items; c += step) {
+      Item it;
+      it.load(job.x, base + c * W);
+      top = max(top, it.top());
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) sh.top[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, mine && lane < each ? sh.top[m * each + lane] : 0u);
+    const TokenScale sc = token_scale(top);
+    if (mine && part == 0) {
+      sh.scale[m] = sc.scale;
+      if (blockIdx.x == 0 && job.scales != nullptr) job.scales[m] = sc.scale;
+    }
+    const auto put = [&](const Item& it, int c) {
+      if constexpr (VEC) {
+        uint2 q = it.quantize(sc.inv);
+        if (blockIdx.x == 0 && job.q != nullptr)
+          *reinterpret_cast<uint2*>(job.q + base + c * 8) = q;
+        q.x ^= kFlip;
+        q.y ^= kFlip;
+        *reinterpret_cast<uint2*>(dst + c * 8) = q;
+      } else {
+        const int8_t q = it.quantize(sc.inv);
+        if (blockIdx.x == 0 && job.q != nullptr) job.q[base + c] = q;
+        dst[c] = static_cast<uint8_t>(q) ^ static_cast<uint8_t>(kFlip);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (part + u * step < items) put(held[u], part + u * step);
+#pragma unroll 2
+    for (int c = part + U * step; c < items; c += step) {
+      Item it;
+      it.load(job.x, base + c * W);
+      put(it, c);
+    }
+    if (mine)
+      for (int k = static_cast<int>(job.K) + part; k < padded; k += step)
+        dst[k] = static_cast<uint8_t>(kFlip);
   }
   __syncthreads();
 }
 
-template <int NT, bool GATED>
-__global__ void __launch_bounds__(kRowThreads, 1) token_rows_kernel(const TokenRowsJob job) {
-  constexpr int kCols = 8 * NT + 1;   // words of a partial row (odd: no bank twice)
+template <bool BIAS>
+__device__ __forceinline__ void stage_rows_by_type(const TokenRowsJob& job, RowsShared& sh,
+                                                   uint8_t* rows) {
+  switch (job.x_dtype * 2 + job.vec) {
+    case Q8_I8 * 2: stage_rows<Q8_I8, false, BIAS>(job, sh, rows); break;
+    case Q8_I8 * 2 + 1: stage_rows<Q8_I8, true, BIAS>(job, sh, rows); break;
+    case Q8_F32 * 2: stage_rows<Q8_F32, false, BIAS>(job, sh, rows); break;
+    case Q8_F32 * 2 + 1: stage_rows<Q8_F32, true, BIAS>(job, sh, rows); break;
+    case Q8_F16 * 2: stage_rows<Q8_F16, false, BIAS>(job, sh, rows); break;
+    case Q8_F16 * 2 + 1: stage_rows<Q8_F16, true, BIAS>(job, sh, rows); break;
+    case Q8_BF16 * 2: stage_rows<Q8_BF16, false, BIAS>(job, sh, rows); break;
+    default: stage_rows<Q8_BF16, true, BIAS>(job, sh, rows); break;
+  }
+}
+
+// MT: rows that the kernel has sums for, M at least; up to 2 by dp4a, else MMAs.
+template <int MT, bool GATED>
+__global__ void __launch_bounds__(kRowThreads, 2) token_rows_kernel(const TokenRowsJob job) {
+  constexpr bool kMma = MT > 2;
+  static_assert(!kMma || MT == 8, "an MMA's columns");
+  constexpr int kLoads = kMma ? 2 : 1;               // of a thread to a piece
+  constexpr int kDeep = kAhead / kLoads;             // pieces on their way
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowsShared sh;
-  auto* parts = reinterpret_cast<int32_t*>(dyn);                    // [warps][32][kCols]
-  uint8_t* rows = dyn + kRowWarps * 32 * kCols * 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int M = static_cast<int>(job.M), KB = job.KB;
-  const int rounds = (KB + kRowWarps * kAhead - 1) / (kRowWarps * kAhead);
+  // two units' sums, so that one barrier a unit keeps them apart
+  auto* parts = reinterpret_cast<int32_t(*)[kRowWarps][MT][16]>(dyn);
+  uint8_t* rows = dyn + sizeof(int32_t) * 2 * kRowWarps * MT * 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane & 15, half = lane >> 4;
+  const int g = lane >> 2, t = lane & 3;
+  const int M = static_cast<int>(job.M);
+  // pieces of 32 inputs, or of 64 for the MMAs
+  const int pieces = kMma ? job.KB : job.KB * 2;
+  const int rounds = (pieces + kRowWarps * kDeep - 1) / (kRowWarps * kDeep);
 
-  // this thread's four 16-byte chunks of a unit's k-block: rows g, g + 8, ...
-  const auto load = [&](uint4 (&a)[4], int unit, int kb) {
-    if (unit < job.units && kb < KB) {
-      const auto* w = reinterpret_cast<const uint4*>(
-          job.w + (static_cast<int64_t>(unit >> 2) * KB + kb) * 8192 + (unit & 3) * 512 + t * 2048 +
-          g * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = __ldcs(w + i * 8);
+  const auto load = [&](uint4 (&a)[kLoads], int unit, int piece) {
+    if (unit < job.units && piece < pieces) {
+      const uint4* w = reinterpret_cast<const uint4*>(job.w) +
+                       static_cast<int64_t>(unit >> 3) * job.KB * 512;
+      const int row = GATED ? ((unit & 6) << 4) + ((unit & 1) << 3) : (unit & 7) << 4;
+      if constexpr (kMma) {
+        w += piece * 512 + t * 128 + row + g;
+        a[0] = load_weights(w);
+        a[kLoads - 1] = load_weights(w + (GATED ? 16 : 8));
+      } else {
+        a[0] = load_weights(w + piece * 256 + half * 128 + row + (r & 7) +
+                            (GATED ? (r & 8) << 1 : r & 8));
+      }
     }
   };
-  uint4 a[kAhead][4];
+  uint4 a[kDeep][kLoads];
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) load(a[s], blockIdx.x, warp + s * kRowWarps);
+  for (int s = 0; s < kDeep; ++s) load(a[s], blockIdx.x, warp + s * kRowWarps);
   pdl_wait();
   pdl_launch_dependents();
-  switch (job.x_dtype) {
-    case Q8_I8: job.vec ? stage_rows<Q8_I8, true>(job, sh, rows) : stage_rows<Q8_I8, false>(job, sh, rows); break;
-    case Q8_F32: job.vec ? stage_rows<Q8_F32, true>(job, sh, rows) : stage_rows<Q8_F32, false>(job, sh, rows); break;
-    case Q8_F16: job.vec ? stage_rows<Q8_F16, true>(job, sh, rows) : stage_rows<Q8_F16, false>(job, sh, rows); break;
-    default: job.vec ? stage_rows<Q8_BF16, true>(job, sh, rows) : stage_rows<Q8_BF16, false>(job, sh, rows); break;
-  }
+  stage_rows_by_type<kMma>(job, sh, rows);
 
-  const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  for (int unit = blockIdx.x; unit < job.units; unit += gridDim.x) {
-    // this thread's channel of the unit's outputs, its scales on their way early
-    const int n = GATED ? unit * 16 + (threadIdx.x & 15) : unit * 32 + (threadIdx.x & 31);
-    const bool in = n < job.N;
-    float ws[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); ++h)
-      if (in) {
-        ws[h] = __ldg(job.ws + static_cast<int64_t>(h) * job.N + n);
-        if (job.bias != nullptr) bias[h] = __ldg(job.bias + static_cast<int64_t>(h) * job.N + n);
-      }
-    float acc[NT][2][4];
-    int32_t sum[NT][2][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+  // the first warps finish two rows each
+  const int m = warp * 2 + half;
+  const bool up = GATED && (r & 8);
+  const float scale = sh.scale[min(m, M - 1)];
+  int turn = 0;
+  for (int unit = blockIdx.x; unit < job.units; unit += gridDim.x, turn ^= 1) {
+    const int n = GATED ? unit * 8 + (r & 7) : unit * 16 + r;
+    const bool in = n < job.N && m < M;
+    const int64_t en = (up ? job.N : 0) + n;
+    float ws = 0.0f, bias = 0.0f;   // on their way early
+    if (in) {
+      ws = __ldg(job.ws + en);
+      if (job.bias != nullptr) bias = __ldg(job.bias + en);
+    }
+    const auto ahead = [&](int round, int s) {
+      // the piece kDeep places on, in the next unit after this one's last
+      const bool more = round + 1 < rounds;
+      load(a[s], more ? unit : unit + gridDim.x,
+           warp + ((more ? (round + 1) * kDeep : 0) + s) * kRowWarps);
+    };
+    if constexpr (kMma) {
+      const __half2 minus = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      int32_t sum[4] = {0, 0, 0, 0};
+      const auto drain = [&]() {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc[i][h][j] = 0.0f;
-          sum[i][h][j] = 0;
+          sum[j] += __float2int_rn(acc[j]);
+          acc[j] = 0.0f;
         }
-    const auto drain = [&]() {
+      };
+      for (int round = 0; round < rounds; ++round) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sum[i][h][j] += __float2int_rn(acc[i][h][j]);
-            acc[i][h][j] = 0.0f;
-          }
-    };
-    for (int r = 0; r < rounds; ++r) {
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
-        const int kb = warp + (r * kAhead + s) * kRowWarps;
-        if (kb < KB) {
-          uint32_t b[NT][8];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const int m = i * 8 + g;
+        for (int s = 0; s < kDeep; ++s) {
+          const int piece = warp + (round * kDeep + s) * kRowWarps;
+          if (piece < pieces) {
+            const uint4 &lo = a[s][0], &hi = a[s][kLoads - 1];
             uint4 v = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-            if (m < M) v = *reinterpret_cast<const uint4*>(rows + m * job.stride + kb * 64 + t * 16);
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              b[i][2 * j] = biased_to_f16x2(q[j], 0x4140, minus);
-              b[i][2 * j + 1] = biased_to_f16x2(q[j], 0x4342, minus);
-            }
+            if (g < M) v = *reinterpret_cast<const uint4*>(rows + g * job.stride + piece * 64 + t * 16);
+            const auto four = [&](uint32_t wlo, uint32_t whi, uint32_t x) {
+              mma_f16(acc, biased_to_f16x2(wlo, 0x4140, minus), biased_to_f16x2(whi, 0x4140, minus),
+                      biased_to_f16x2(wlo, 0x4342, minus), biased_to_f16x2(whi, 0x4342, minus),
+                      biased_to_f16x2(x, 0x4140, minus), biased_to_f16x2(x, 0x4342, minus));
+            };
+            four(lo.x, hi.x, v.x);
+            four(lo.y, hi.y, v.y);
+            four(lo.z, hi.z, v.z);
+            four(lo.w, hi.w, v.w);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t lo[4] = {a[s][2 * h].x, a[s][2 * h].y, a[s][2 * h].z, a[s][2 * h].w};
-            const uint32_t hi[4] = {a[s][2 * h + 1].x, a[s][2 * h + 1].y, a[s][2 * h + 1].z,
-                                    a[s][2 * h + 1].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a0 = biased_to_f16x2(lo[j], 0x4140, minus);
-              const uint32_t a1 = biased_to_f16x2(hi[j], 0x4140, minus);
-              const uint32_t a2 = biased_to_f16x2(lo[j], 0x4342, minus);
-              const uint32_t a3 = biased_to_f16x2(hi[j], 0x4342, minus);
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-                mma_f16(acc[i][h], a0, a1, a2, a3, b[i][2 * j], b[i][2 * j + 1]);
-            }
-          }
+          ahead(round, s);
         }
-        // the k-block kAhead places on, in the next unit after this one's last
-        const bool more = r + 1 < rounds;
-        load(a[s], more ? unit : unit + gridDim.x,
-             warp + ((more ? (r + 1) * kAhead : 0) + s) * kRowWarps);
+        if ((round + 1) % (kExactBlocks / kDeep) == 0) drain();
       }
-      if ((r + 1) % (kExactBlocks / kAhead) == 0) drain();
-    }
-    drain();
-    __syncthreads();   // the unit before has been read
-    int32_t* mine = parts + warp * 32 * kCols;
+      drain();
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int j = 0; j < 4; ++j) parts[turn][warp][2 * t + (j & 1)][g + (j >> 1) * 8] = sum[j];
+    } else {
+      int32_t acc[MT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < MT; ++i) acc[i] = 0;
+      for (int round = 0; round < rounds; ++round) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mine[(h * 16 + (j >> 1) * 8 + g) * kCols + i * 8 + 2 * t + (j & 1)] = sum[i][h][j];
-    __syncthreads();
-    constexpr int kChannels = GATED ? 16 : 32;
-    for (int i = threadIdx.x; i < kChannels * M; i += kRowThreads) {
-      const int row = i % kChannels, m = i / kChannels;
-      int32_t total[2] = {0, 0};
+        for (int s = 0; s < kDeep; ++s) {
+          const int piece = warp + (round * kDeep + s) * kRowWarps;
+          if (piece < pieces) {
+            const uint8_t* x = rows + piece * 32 + half * 16;
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w)
-#pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h)
-          total[h] += parts[(w * 32 + h * 16 + row) * kCols + m];
-      if (in) {
-        float v = token_value(total[0], sh.scale[m], ws[0], bias[0]);
-        if constexpr (GATED) {
-          float slope;
-          v = activate<false>(v, job.act, slope) * token_value(total[1], sh.scale[m], ws[1], bias[1]);
-        } else if (job.act == kActRelu) {
-          v = max_nan(v, 0.0f);
+            for (int i = 0; i < MT; ++i) {
+              const uint4 q = *reinterpret_cast<const uint4*>(x + min(i, M - 1) * job.stride);
+              acc[i] = __dp4a(static_cast<int>(a[s][0].x ^ 0x80808080u), static_cast<int>(q.x), acc[i]);
+              acc[i] = __dp4a(static_cast<int>(a[s][0].y ^ 0x80808080u), static_cast<int>(q.y), acc[i]);
+              acc[i] = __dp4a(static_cast<int>(a[s][0].z ^ 0x80808080u), static_cast<int>(q.z), acc[i]);
+              acc[i] = __dp4a(static_cast<int>(a[s][0].w ^ 0x80808080u), static_cast<int>(q.w), acc[i]);
+            }
+          }
+          ahead(round, s);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+        if (half == 0) parts[turn][warp][i][r] = acc[i];
+      }
+    }
+    __syncthreads();
+    if (warp * 2 < M) {
+      int32_t total = 0;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) total += parts[turn][w][min(m, M - 1)][r];
+      float v = token_value(total, scale, ws, bias);
+      if constexpr (GATED) {
+        const float other = __shfl_xor_sync(0xffffffffu, v, 8);
+        float slope;
+        if (!up) v = activate<false>(v, job.act, slope) * other;
+      } else if (job.act == kActRelu) {
+        v = max_nan(v, 0.0f);
+      }
+      if (in && !up) {
         const int64_t at = static_cast<int64_t>(m) * job.N + n;
         switch (job.out_dtype) {
           case Q8_F32: store_one<Q8_F32>(job.out, at, v); break;
@@ -295,41 +327,57 @@ __global__ void __launch_bounds__(kRowThreads, 1) token_rows_kernel(const TokenR
 }
 
 constexpr size_t kMostShared = 220 * 1024;   // beside it the scales
+constexpr size_t kTwoShared = 110 * 1024;    // of each of two CTAs
 
+int rows_of(int64_t M) { return M <= 2 ? static_cast<int>(M) : 8; }
 size_t rows_shared(int64_t M, int64_t K) {
-  const int nt = M <= 8 ? 1 : 2;
-  return static_cast<size_t>(kRowWarps) * 32 * (8 * nt + 1) * 4 + static_cast<size_t>(M) * token_rows_stride(K);
+  return static_cast<size_t>(2 * kRowWarps * 16 * 4) * rows_of(M) +
+         static_cast<size_t>(M) * token_rows_stride(K);
 }
 
-template <int NT, bool GATED>
+template <int MT, bool GATED>
 cudaError_t launch_rows(const TokenRowsJob& job, cudaStream_t s) {
-  auto kernel = token_rows_kernel<NT, GATED>;
+  auto kernel = token_rows_kernel<MT, GATED>;
   static DeviceOnce once;
   cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kMostShared));
   });
   if (e != cudaSuccess) return e;
-  const int grid = std::min(job.units, device_sm_count());
-  return launch_pdl(kernel, grid, kRowThreads, rows_shared(job.M, job.K), s, job);
+  const size_t shared = rows_shared(job.M, job.K);
+  const int grid = std::min(job.units, device_sm_count() * (shared <= kTwoShared ? 2 : 1));
+  return launch_pdl(kernel, grid, kRowThreads, shared, s, job);
+}
+
+template <bool GATED>
+cudaError_t launch_by_rows(const TokenRowsJob& job, cudaStream_t s) {
+  switch (rows_of(job.M)) {
+    case 1: return launch_rows<1, GATED>(job, s);
+    case 2: return launch_rows<2, GATED>(job, s);
+    default: return launch_rows<8, GATED>(job, s);
+  }
 }
 
 }  // namespace
 
+// Every CTA quantizes all rows, so many long ones are left to the other kernel
+// (rows_internal.h), whose time does not depend on a few rows.  Measured, here
+// against there, bf16: 1 row x 11008 x 4096 10.2 us, 16.7; 1 x 28672 22.5, 28.0;
+// 2 x 28672 25.6, 27.8; 4 x 4096 9.7, 12.1; 8 x 4096 11.3, 12.3; 4 x 8192 14.6,
+// 14.9; 8 x 11008 24.1, 16.7 (all x 4096); and 16 rows of 2048 x 11008 16.5, 11.9.
 bool token_rows_fit(int64_t M, int64_t K) {
-  return M >= 1 && M <= kFewRows && K <= (1 << 20) && rows_shared(M, K) <= kMostShared;
+  return M >= 1 && M <= kFewRows && K <= (1 << 20) && (M <= 2 || M * K <= 32768) &&
+         rows_shared(M, K) <= kMostShared;
 }
 
 cudaError_t launch_token_rows(TokenRowsJob job, bool gated, cudaStream_t s) {
   job.KB = static_cast<int>((job.K + 63) / 64);
   job.stride = static_cast<int>(token_rows_stride(job.K));
-  const int64_t rows = gated ? gated_rows(job.N) : job.N;
-  job.units = static_cast<int>((rows + 31) / 32);
+  job.units = static_cast<int>(gated ? (job.N + 7) / 8 : (job.N + 15) / 16);
   const int64_t bytes = dtype_bytes(job.x_dtype), wide = job.x_dtype == Q8_I8 ? 16 : 8;
   job.vec = job.K % wide == 0 && reinterpret_cast<uintptr_t>(job.x) % 16 == 0 &&
-            job.K * bytes % 16 == 0;
-  if (job.M <= 8) return gated ? launch_rows<1, true>(job, s) : launch_rows<1, false>(job, s);
-  return gated ? launch_rows<2, true>(job, s) : launch_rows<2, false>(job, s);
+            job.K * bytes % 16 == 0 && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
+  return gated ? launch_by_rows<true>(job, s) : launch_by_rows<false>(job, s);
 }
 
 }  // namespace q8

@@ -18,10 +18,14 @@ from typing import Optional, Tuple
 import torch
 
 from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _stream
-from .rows import (_DTYPE, PackedTileWeight, _arg, _dtype_code, _out, _shape, _space, _vector_arg)
+from .rows import _DTYPE, PackedTileWeight, _dtype_code, _shape, _space
 
 _HALVES = (torch.float16, torch.bfloat16)
 
+
+# A call for one token takes some 10 us on the GPU, so the host's part counts.
+# Each tensor gets one combined check; the slow one, which names what is wrong,
+# runs only where it fails.
 
 def _float_code(dtype, name: str) -> int:
     code = _DTYPE.get(dtype)
@@ -30,46 +34,89 @@ def _float_code(dtype, name: str) -> int:
     return code
 
 
-def _half_arg(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(dtype code, address) of a float16 or bfloat16 matrix."""
+def _at(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
+    """The address of a contiguous tensor of this dtype and shape on a CUDA device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device and t.is_contiguous()):
+        _need(t, dtype, name)
+        _shape(t, shape, name)
+        raise ValueError(f"{name} must be on the rows' device, got {t.device}")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, codes, name: str) -> Tuple[int, int, int, int, int]:
+    """(dtype code, address, rows, columns, device) of a contiguous CUDA matrix
+    of one of these types."""
     code = _dtype_code(t, name)
-    if code not in (1, 2):
-        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    at = _arg(t, t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
-    return code, at
+    if code not in codes:
+        types = ", ".join(str(d)[6:] for d, c in _DTYPE.items() if c in codes)
+        raise TypeError(f"{name} must be {types}, got {t.dtype}")
+    if not (t.is_cuda and t.is_contiguous()):
+        _need(t, t.dtype, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    return code, t.data_ptr(), shape[0], shape[1], t.get_device()
+
+
+def _packed_at(packed, device: int, name: str) -> int:
+    data = packed.data
+    if data.get_device() != device:
+        raise ValueError(f"{name} must be on the rows' device, got {data.device}")
+    return data.data_ptr()
+
+
+def _result(out: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, device: int,
+            name: str = "out") -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _at(out, dtype, shape, device, name)
+    return out
+
+
+# (sizes depend on the device's SMs)
+@functools.lru_cache(maxsize=4096)
+def _bytes(query: str, a: int, b: int, c: int, device: int) -> int:
+    with torch.cuda.device(device):
+        return getattr(_lib, query)(a, b, c)
+
+
+def _workspace_at(nbytes: int, workspace, like: torch.Tensor, device: int):
+    """(the workspace, to be kept until the launch, its address); some sizes need none."""
+    if nbytes == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    else:
+        _space(nbytes, like.device, workspace)
+        if workspace.get_device() != device:
+            raise ValueError(f"workspace must be on the rows' device, got {workspace.device}")
+    return workspace, workspace.data_ptr()
 
 
 def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
                        scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Float rows [M, K] to int8, each with its own scale (see
     q8_quantize_per_token): returns (q int8 [M, K], scales float32 [M])."""
-    code = _float_code(getattr(x, "dtype", type(x)), "x")
-    at = _arg(x, x.dtype, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    q = _out(out, (M, K), torch.int8, x.device)
-    scales = _out(scales, (M,), torch.float32, x.device, "scales")
-    _check(_lib.q8_quantize_per_token(at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x)),
-           "q8_quantize_per_token")
+    code, at, M, K, device = _matrix(x, (0, 1, 2), "x")
+    q = _result(out, (M, K), torch.int8, x, device)
+    scales = _result(scales, (M,), torch.float32, x, device, "scales")
+    st = _lib.q8_quantize_per_token(at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x))
+    if st:
+        _check(st, "q8_quantize_per_token")
     return q, scales
 
 
 def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32,
                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """int8 rows [M, K] times their scales, in a float type."""
-    at = _arg(q, torch.int8, "q")
-    if q.dim() != 2:
-        raise ValueError(f"q must be [M, K], got {tuple(q.shape)}")
-    M, K = q.shape
-    s = _arg(scales, torch.float32, "scales")
-    _shape(scales, (M,), "scales")
+    _, at, M, K, device = _matrix(q, (3,), "q")
+    s = _at(scales, torch.float32, (M,), device, "scales")
     code = _float_code(out_dtype, "out_dtype")
-    out = _out(out, (M, K), out_dtype, q.device)
-    _check(_lib.q8_dequantize_per_token(at, s, M, K, code, out.data_ptr(), _stream(q)),
-           "q8_dequantize_per_token")
+    out = _result(out, (M, K), out_dtype, q, device)
+    st = _lib.q8_dequantize_per_token(at, s, M, K, code, out.data_ptr(), _stream(q))
+    if st:
+        _check(st, "q8_dequantize_per_token")
     return out
 
 
@@ -113,13 +160,12 @@ class _Gated(torch.autograd.Function):
 
 def _recorded(x, weight_scales, bias, packed_t, out_dtype) -> bool:
     """Whether this call is recorded; what cannot be differentiated is refused."""
-    if not torch.is_grad_enabled():
+    if not (x.requires_grad or weight_scales.requires_grad
+            or bias is not None and bias.requires_grad) or not torch.is_grad_enabled():
         return False
     for t, name in ((weight_scales, "weight_scales"), (bias, "bias")):
         if t is not None and t.requires_grad:
             raise ValueError(f"{name} gets no gradient here: pass it detached")
-    if not x.requires_grad:
-        return False
     if packed_t is None:
         raise ValueError("x requires a gradient: give packed_t, or pass x detached")
     if out_dtype not in _HALVES:
@@ -128,35 +174,24 @@ def _recorded(x, weight_scales, bias, packed_t, out_dtype) -> bool:
     return True
 
 
-def _rows(x, x_scales, K: int) -> Tuple[int, int, int, int]:
-    """(dtype code, address, M, address of the scales) of either form of rows."""
-    code = _dtype_code(x, "x")
-    at = _arg(x, x.dtype, "x")
-    if x.dim() != 2 or x.shape[1] != K:
+def _rows(x, x_scales, K: int) -> Tuple[int, int, int, int, int]:
+    """(dtype code, address, M, address of the scales, device) of either form of rows."""
+    code, at, M, k, device = _matrix(x, (0, 1, 2, 3), "x")
+    if k != K:
         raise ValueError(f"x must be [M, {K}], got {tuple(x.shape)}")
-    M = x.shape[0]
     if code == 3:
         if x_scales is None:
             raise ValueError("int8 x comes with x_scales")
-        s = _arg(x_scales, torch.float32, "x_scales")
-        _shape(x_scales, (M,), "x_scales")
-        return code, at, M, s
+        return code, at, M, _at(x_scales, torch.float32, (M,), device, "x_scales"), device
     if x_scales is not None:
         raise ValueError("float x is quantized here: x_scales must be None")
-    return code, at, M, 0
+    return code, at, M, 0, device
 
 
 def _out_dtype(x, out_dtype):
     if out_dtype is None:
         out_dtype = torch.bfloat16 if x.dtype is torch.int8 else x.dtype
     return out_dtype, _float_code(out_dtype, "out_dtype")
-
-
-# (sizes depend on the device's SMs)
-@functools.lru_cache(maxsize=4096)
-def _bytes(query: str, a: int, b: int, c: int, device: int) -> int:
-    with torch.cuda.device(device):
-        return getattr(_lib, query)(a, b, c)
 
 
 def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias, activation="none",
@@ -171,20 +206,21 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     N, K = packed.N, packed.K
     if packed.E != 1:
         raise ValueError(f"the packed weight has {packed.E} groups, this product takes one")
-    code, at, M, s = _rows(x, x_scales, K)
-    _need(weight_scales, torch.float32, "weight_scales")
-    scales = _vector_arg(weight_scales, (N,), "weight_scales")
-    b = _vector_arg(bias, (N,), "bias")
+    code, at, M, s, device = _rows(x, x_scales, K)
+    w = _packed_at(packed, device, "packed")
+    scales = _at(weight_scales, torch.float32, (N,), device, "weight_scales")
+    b = 0 if bias is None else _at(bias, torch.float32, (N,), device, "bias")
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
     if packed_t is not None and (packed_t.E, packed_t.N, packed_t.K) != (1, K, N):
         raise ValueError(f"packed_t must be of a {K}x{N} weight")
-    out = _out(out, (M, N), out_dtype, x.device)
-    nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, x.get_device())
-    ws = _space(nbytes, x.device, workspace)
-    _check(_lib.q8_linear_per_token(at, code, M, K, 0, s, packed.data.data_ptr(), N, scales, b,
-                                    activation.encode(), out_code, out.data_ptr(), ws.data_ptr(),
-                                    nbytes, _stream(x)), "q8_linear_per_token")
+    out = _result(out, (M, N), out_dtype, x, device)
+    nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, device)
+    workspace, ws = _workspace_at(nbytes, workspace, x, device)
+    st = _lib.q8_linear_per_token(at, code, M, K, 0, s, w, N, scales, b, activation.encode(),
+                                  out_code, out.data_ptr(), ws, nbytes, _stream(x))
+    if st:
+        _check(st, "q8_linear_per_token")
     if record:
         out = _Linear.apply(x, out, packed_t, weight_scales, activation == "relu")
     return out
@@ -195,24 +231,22 @@ def linear_per_token_backward(dy, packed_t: PackedTileWeight, weight_scales, y=N
     """The gradient of linear_per_token's rows (see
     q8_linear_per_token_backward): dy [M, N] float16 or bfloat16, y the forward
     output under relu; out [M, K] of dy's type."""
-    code, at = _half_arg(dy, "dy")
+    code, at, M, n, device = _matrix(dy, (1, 2), "dy")
     K, N = packed_t.N, packed_t.K
     if packed_t.E != 1:
         raise ValueError(f"the packed weight has {packed_t.E} groups, this product takes one")
-    M = dy.shape[0]
-    _shape(dy, (M, N), "dy")
-    y_at = 0
-    if y is not None:
-        y_at = _arg(y, dy.dtype, "y")
-        _shape(y, (M, N), "y")
-    _need(weight_scales, torch.float32, "weight_scales")
-    scales = _vector_arg(weight_scales, (N,), "weight_scales")
-    out = _out(out, (M, K), dy.dtype, dy.device)
-    nbytes = _bytes("q8_linear_per_token_backward_workspace_bytes", M, N, K, dy.get_device())
-    ws = _space(nbytes, dy.device, workspace)
-    _check(_lib.q8_linear_per_token_backward(at, code, M, N, y_at, packed_t.data.data_ptr(), K,
-                                             scales, out.data_ptr(), ws.data_ptr(), nbytes,
-                                             _stream(dy)), "q8_linear_per_token_backward")
+    if n != N:
+        raise ValueError(f"dy must be [M, {N}], got {tuple(dy.shape)}")
+    y_at = 0 if y is None else _at(y, dy.dtype, (M, N), device, "y")
+    w = _packed_at(packed_t, device, "packed_t")
+    scales = _at(weight_scales, torch.float32, (N,), device, "weight_scales")
+    out = _result(out, (M, K), dy.dtype, dy, device)
+    nbytes = _bytes("q8_linear_per_token_backward_workspace_bytes", M, N, K, device)
+    workspace, ws = _workspace_at(nbytes, workspace, dy, device)
+    st = _lib.q8_linear_per_token_backward(at, code, M, N, y_at, w, K, scales, out.data_ptr(), ws,
+                                           nbytes, _stream(dy))
+    if st:
+        _check(st, "q8_linear_per_token_backward")
     return out
 
 
@@ -256,16 +290,16 @@ def pack_gated_weight_t(gate: torch.Tensor, up: torch.Tensor) -> PackedGatedWeig
     return _pack_gated(gate, up, True)
 
 
-def _gated_args(packed, packed_t, weight_scales, bias) -> Tuple[int, int, int, int]:
-    """(N, K) of the pair and the addresses of its scales and biases."""
+def _gated_args(packed, packed_t, weight_scales, bias, device: int) -> Tuple[int, int, int]:
+    """The addresses of the pair's weights, scales and biases."""
     if packed.transposed:
         raise ValueError("packed is a transposed weight (pack_gated_weight_t)")
     N, K = packed.N, packed.K
     if packed_t is not None and (not packed_t.transposed or (packed_t.N, packed_t.K) != (N, K)):
         raise ValueError(f"packed_t must come from pack_gated_weight_t of {N}x{K} weights")
-    _need(weight_scales, torch.float32, "weight_scales")
-    return (N, K, _vector_arg(weight_scales, (2, N), "weight_scales"),
-            _vector_arg(bias, (2, N), "bias"))
+    return (_packed_at(packed, device, "packed"),
+            _at(weight_scales, torch.float32, (2, N), device, "weight_scales"),
+            0 if bias is None else _at(bias, torch.float32, (2, N), device, "bias"))
 
 
 def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, activation="silu",
@@ -278,21 +312,23 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
     out_dtype (by default x's own, bfloat16 for int8 x).  packed_t
     (pack_gated_weight_t) records the call for autograd where x requires a
     gradient; it then keeps the int8 rows and their scales."""
-    N, K, scales, b = _gated_args(packed, packed_t, weight_scales, bias)
-    code, at, M, s = _rows(x, x_scales, K)
+    N, K = packed.N, packed.K
+    code, at, M, s, device = _rows(x, x_scales, K)
+    w, scales, b = _gated_args(packed, packed_t, weight_scales, bias, device)
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
-    out = _out(out, (M, N), out_dtype, x.device)
-    nbytes = _bytes("q8_linear_gated_workspace_bytes", M, K, N, x.get_device())
-    ws = _space(nbytes, x.device, workspace)
+    out = _result(out, (M, N), out_dtype, x, device)
+    nbytes = _bytes("q8_linear_gated_workspace_bytes", M, K, N, device)
+    workspace, ws = _workspace_at(nbytes, workspace, x, device)
     q_at = 0
     if record:
         x_q = torch.empty((M, K), dtype=torch.int8, device=x.device)
         x_scales = torch.empty(M, dtype=torch.float32, device=x.device)
         q_at, s = x_q.data_ptr(), x_scales.data_ptr()
-    _check(_lib.q8_linear_gated(at, code, M, K, q_at, s, packed.data.data_ptr(), N, scales, b,
-                                activation.encode(), out_code, out.data_ptr(), ws.data_ptr(), nbytes,
-                                _stream(x)), "q8_linear_gated")
+    st = _lib.q8_linear_gated(at, code, M, K, q_at, s, w, N, scales, b, activation.encode(), out_code,
+                              out.data_ptr(), ws, nbytes, _stream(x))
+    if st:
+        _check(st, "q8_linear_gated")
     if record:
         out = _Gated.apply(x, out, x_q, x_scales, packed, packed_t, weight_scales, bias, activation)
     return out
@@ -303,21 +339,21 @@ def linear_gated_backward(dh, x, x_scales, packed: PackedGatedWeight, packed_t: 
     """The gradient of linear_gated's rows from the int8 rows x [M, K] and their
     scales (see q8_linear_gated_backward): dh [M, N] float16 or bfloat16; out
     [M, K] of dh's type."""
-    code, at = _half_arg(dh, "dh")
+    code, at, M, n, device = _matrix(dh, (1, 2), "dh")
     if packed_t is None:
         raise ValueError("the gradient needs packed_t (pack_gated_weight_t)")
-    N, K, scales, b = _gated_args(packed, packed_t, weight_scales, bias)
-    M = dh.shape[0]
-    _shape(dh, (M, N), "dh")
-    q = _arg(x, torch.int8, "x")
-    _shape(x, (M, K), "x")
-    s = _arg(x_scales, torch.float32, "x_scales")
-    _shape(x_scales, (M,), "x_scales")
-    out = _out(out, (M, K), dh.dtype, dh.device)
-    nbytes = _bytes("q8_linear_gated_backward_workspace_bytes", M, K, N, dh.get_device())
-    ws = _space(nbytes, dh.device, workspace)
-    _check(_lib.q8_linear_gated_backward(at, code, M, N, q, s, K, packed.data.data_ptr(),
-                                         packed_t.data.data_ptr(), scales, b, activation.encode(),
-                                         out.data_ptr(), ws.data_ptr(), nbytes, _stream(dh)),
-           "q8_linear_gated_backward")
+    N, K = packed.N, packed.K
+    w, scales, b = _gated_args(packed, packed_t, weight_scales, bias, device)
+    if n != N:
+        raise ValueError(f"dh must be [M, {N}], got {tuple(dh.shape)}")
+    w_t = _packed_at(packed_t, device, "packed_t")
+    q = _at(x, torch.int8, (M, K), device, "x")
+    s = _at(x_scales, torch.float32, (M,), device, "x_scales")
+    out = _result(out, (M, K), dh.dtype, dh, device)
+    nbytes = _bytes("q8_linear_gated_backward_workspace_bytes", M, K, N, device)
+    workspace, ws = _workspace_at(nbytes, workspace, dh, device)
+    st = _lib.q8_linear_gated_backward(at, code, M, N, q, s, K, w, w_t, scales, b,
+                                       activation.encode(), out.data_ptr(), ws, nbytes, _stream(dh))
+    if st:
+        _check(st, "q8_linear_gated_backward")
     return out
