@@ -57,7 +57,8 @@ bool gated_sizes_ok(int64_t N, int64_t K) {
 }
 
 // Two contractions one after the other: the rows' operand and the gradients',
-// one set of parts, both counts, and each row's powers of two.
+// one set of parts, both counts, each row's largest |dh| and power of two, and
+// the largest scales and biases.
 struct GradSpace {
   TilePlan rows, grads;
   size_t grad_operand, parts, counts, powers, total;
@@ -70,7 +71,7 @@ GradSpace gated_grad_space(int64_t M, int64_t N, int64_t K) {
   t.parts = t.grad_operand + t.grads.operand;
   t.counts = t.parts + t.grads.parts;
   t.powers = t.counts + 2 * t.grads.counts;
-  t.total = t.powers + 2 * q8::align_ws(static_cast<size_t>(M) * 4);
+  t.total = t.powers + 2 * q8::align_ws(static_cast<size_t>(M) * 4) + q8::align_ws(16);
   return t;
 }
 
@@ -365,8 +366,10 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
   auto* space = static_cast<uint8_t*>(workspace);
-  auto* rescale = reinterpret_cast<float*>(space + sp.powers);
-  auto* unscale = reinterpret_cast<float*>(space + sp.powers + q8::align_ws(static_cast<size_t>(M) * 4));
+  const size_t each = q8::align_ws(static_cast<size_t>(M) * 4);
+  auto* most_dh = reinterpret_cast<float*>(space + sp.powers);
+  auto* unscale = reinterpret_cast<float*>(space + sp.powers + each);
+  auto* tops = reinterpret_cast<float*>(space + sp.powers + 2 * each);
   auto* counts = reinterpret_cast<int32_t*>(space + sp.counts);
   const int count_words = static_cast<int>(sp.grads.counts / 4);
 
@@ -377,7 +380,10 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
   p.act = act;
   p.dh = dh;
   p.operand_out = reinterpret_cast<uint16_t*>(space + sp.grad_operand);
-  p.rescale = rescale;
+  p.K = K;
+  p.most_dh = most_dh;
+  p.tops = tops;
+  p.unscale = unscale;
   p.parts = reinterpret_cast<int32_t*>(space + sp.parts);
   p.counts = counts;
   q8::TileParams g = tile_params(M, K, K, inputs, sp.grads, packed_transposed);
@@ -388,7 +394,6 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
 
   q8::GatedGradFrontJob job{};
   job.q = x_q;
-  job.scales = x_scales;
   job.dh = dh;
   job.ws = weight_scales;
   job.bias = bias;
@@ -397,8 +402,8 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
   job.K = K;
   job.operand = reinterpret_cast<uint16_t*>(space);
   job.KB = p.KB;
-  job.rescale = rescale;
-  job.unscale = unscale;
+  job.most_dh = most_dh;
+  job.tops = tops;
   job.counts = counts;
   job.count_words = 2 * count_words;
   cudaError_t e = q8::launch_gated_grad_front(job, dtype, cs(stream));

@@ -140,8 +140,11 @@ struct TileParams {
   int act;                  // Activation of the gated forms
   const void* dh;           // [R, N] the gated output's gradient
   uint16_t* operand_out;    // [2 NB][R][64] the gradient's operand, f16
-  const float* rescale;     // [R] powers of two that its values are multiplied
-  const float* unscale;     // by, and the sums after it
+  int64_t K;                // the gated gradient: inputs of a row, and with
+  const float* most_dh;     // [R] its largest |dh| and the largest scales and
+  const float* tops;        // [4] biases (see gated_row_power) the powers of two
+  float* unscale;           // [R] that its operand is multiplied by; what the
+                            // next kernel's sums are multiplied by
 };
 cudaError_t launch_tile_gemm(TileParams p, const void* operand, q8_dtype out_dtype,
                              cudaStream_t s);

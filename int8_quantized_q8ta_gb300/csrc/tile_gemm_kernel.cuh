@@ -497,8 +497,15 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
       }
     } else {
       // the gradients times their channels' scales and their rows' powers of two
-      const float r0 = p.rescale[at + min(lane, mine - 1)];
-      const float r1 = COLS > 32 ? p.rescale[at + min(lane + 32, mine - 1)] : 0.0f;
+      const float4 tops = *reinterpret_cast<const float4*>(p.tops);
+      const RowPower p0 = gated_row_power(p.most_dh[at + min(lane, mine - 1)], s0, p.K, tops);
+      const RowPower p1 =
+          COLS > 32 ? gated_row_power(p.most_dh[at + min(lane + 32, mine - 1)], s1, p.K, tops) : p0;
+      const float r0 = p0.rescale, r1 = p1.rescale;
+      if (nb == 0 && quarter == 0) {   // once a row
+        if (lane < mine) p.unscale[at + lane] = p0.unscale;
+        if (lane + 32 < mine) p.unscale[at + lane + 32] = p1.unscale;
+      }
       const float ws_other = __shfl_xor_sync(0xffffffffu, ws, 16);
       const float wg = up ? ws_other : ws, wu = up ? ws : ws_other;
       const uint16_t* dh = static_cast<const uint16_t*>(p.dh) +
@@ -1014,6 +1021,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!PAIR && kBatch && p.by_row && p.out_rows == nullptr && sg->kb1 == p.KB)
           fetch_adapters(sg, mine, nb);
         pdl_wait();
+      }
+      if constexpr (FORM == kFormGatedGrad) {
+        // this part's dh on its way to L2 before the epilogue wants it: 32 bytes
+        // of each of its rows
+        const int64_t n0 = static_cast<int64_t>(nb) * 64 + quarter * 16;
+        const auto* dh = static_cast<const uint16_t*>(p.dh) +
+                         static_cast<int64_t>(sg->row0 + col0) * p.N + min(n0, int64_t{p.N - 1});
+        for (int j = lane; j < mine; j += 32) prefetch_l2(dh + static_cast<int64_t>(j) * p.N);
       }
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run

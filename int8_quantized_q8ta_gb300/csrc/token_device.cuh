@@ -7,6 +7,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "q8ta.h"
 #include "rows_internal.h"
@@ -54,17 +55,158 @@ __device__ __forceinline__ void store_x8(void* out, int64_t i, const float (&v)[
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
-// (Rows that an earlier kernel may have written are read with ordinary loads.)
-// Eight 16-bit values of a row from column n0 on, zeros from column n on.
-template <bool VEC>
-__device__ __forceinline__ uint4 load_halves(const uint16_t* p, int64_t row, int64_t n0, int64_t n) {
-  if constexpr (VEC)
-    return n0 < n ? *reinterpret_cast<const uint4*>(p + row + n0) : make_uint4(0, 0, 0, 0);
+// ---------------------------------------------------------------------------
+// Rows of any length, so that begin anywhere: what a thread wants of one, 8
+// values, comes as the aligned 16 bytes that hold it and is shifted into place
+// once it has arrived.  (Rows that an earlier kernel may have written are read
+// with ordinary loads.)
+// ---------------------------------------------------------------------------
+
+// The bytes of a matrix, and where one of its rows begins.
+struct RowBytes {
+  const uint8_t *lo, *hi, *at;
+};
+template <typename T>
+__device__ __forceinline__ RowBytes row_bytes(const void* x, int64_t M, int64_t K, int64_t m) {
+  const auto* lo = static_cast<const uint8_t*>(x);
+  return {lo, lo + M * K * static_cast<int64_t>(sizeof(T)), lo + m * K * static_cast<int64_t>(sizeof(T))};
+}
+
+// The 16 bytes at a 16-byte boundary, zeros outside [lo, hi).
+__device__ __forceinline__ uint4 load_within(const uint8_t* p, const uint8_t* lo, const uint8_t* hi) {
   uint32_t v[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (n0 + j < n) v[j / 2] |= static_cast<uint32_t>(p[row + n0 + j]) << (16 * (j & 1));
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j)
+    if (p + j >= lo && p + j < hi) v[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
   return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// W words from byte s < 16 of W + 4.
+template <int W>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[W + 4], uint32_t s) {
+  if (s & 8) {
+#pragma unroll
+    for (int j = 0; j < W + 2; ++j) w[j] = w[j + 2];
+  }
+  if (s & 4) {
+#pragma unroll
+    for (int j = 0; j < W + 1; ++j) w[j] = w[j + 1];
+  }
+  if (s & 3) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], (s & 3) * 8);
+  }
+}
+
+// 32 W bits of a row: `load` asks for them, `settle` puts them in w[0 .. W - 1],
+// zeros from `bytes` on.  VEC: the row begins on 16 bytes and is a multiple of
+// them.
+template <int W, bool VEC>
+struct RowItem {
+  uint32_t w[W + (VEC ? 0 : 4)];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < W + (VEC ? 0 : 4); ++j) w[j] = 0;
+  }
+  // item c of the row, of `bytes` in all
+  __device__ __forceinline__ void load(const RowBytes& row, int64_t c, int64_t bytes) {
+    const uint8_t* p = row.at + c * (W * 4);
+    zero();
+    if constexpr (VEC) {
+      if (c * (W * 4) < bytes)
+#pragma unroll
+        for (int j = 0; j < W; j += 4) put(j, *reinterpret_cast<const uint4*>(p + j * 4));
+    } else if (c * (W * 4) < bytes) {
+      const uint32_t s = reinterpret_cast<uintptr_t>(p) & 15;
+      p -= s;
+      if (p >= row.lo && p + (W * 4 + 16) <= row.hi) {
+#pragma unroll
+        for (int j = 0; j <= W; j += 4) put(j, *reinterpret_cast<const uint4*>(p + j * 4));
+      } else {   // the ends of the matrix
+#pragma unroll
+        for (int j = 0; j <= W; j += 4) put(j, load_within(p + j * 4, row.lo, row.hi));
+      }
+    }
+  }
+  __device__ __forceinline__ void settle(const RowBytes& row, int64_t c, int64_t bytes) {
+    if constexpr (!VEC) {
+      const int64_t left = bytes - c * (W * 4);
+      if (left <= 0) return;   // zeros
+      shift_words<W>(w, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row.at) + c * (W * 4)) & 15);
+      if (left < W * 4) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int n = static_cast<int>(left) - j * 4;   // bytes of this word
+          if (n < 4) w[j] &= n <= 0 ? 0u : (1u << (8 * n)) - 1;
+        }
+      }
+    }
+  }
+
+ private:
+  __device__ __forceinline__ void put(int j, const uint4& v) {
+    w[j] = v.x;
+    w[j + 1] = v.y;
+    w[j + 2] = v.z;
+    w[j + 3] = v.w;
+  }
+};
+
+// Eight int8 values from any byte on: two aligned words of 8 bytes.
+template <bool VEC>
+__device__ __forceinline__ uint2 load_int8x8(const int8_t* q, int64_t row, int64_t k0, int64_t K,
+                                             const int8_t* end) {
+  if (k0 >= K) return make_uint2(0, 0);
+  const int8_t* p = q + row + k0;
+  if constexpr (VEC) return *reinterpret_cast<const uint2*>(p);
+  const uint32_t s = reinterpret_cast<uintptr_t>(p) & 7;
+  const int8_t* p0 = p - s;
+  const auto part = [&](const int8_t* a) {
+    if (a >= q && a + 8 <= end) return *reinterpret_cast<const uint64_t*>(a);
+    uint64_t v = 0;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j)
+      if (a + j >= q && a + j < end) v |= static_cast<uint64_t>(static_cast<uint8_t>(a[j])) << (8 * j);
+    return v;
+  };
+  uint64_t v = part(p0) >> (8 * s);
+  if (s != 0) v |= part(p0 + 8) << (64 - 8 * s);
+  if (K - k0 < 8) v &= (uint64_t{1} << (8 * (K - k0))) - 1;
+  return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+
+// The first n bytes of each lane's 8 go to p, where lane l's p is lane 0's + 8 l
+// (p of any alignment; lanes without bytes, n <= 0, come last).  All 32 lanes
+// call it.  Whole words of 8 bytes are put together across lanes.
+__device__ __forceinline__ void store_bytes_any(int8_t* p, uint2 w, int n) {
+  const uint32_t t = reinterpret_cast<uintptr_t>(p) & 7;
+  const int lane = threadIdx.x & 31;
+  const uint64_t mine = (static_cast<uint64_t>(w.y) << 32) | w.x;
+  if (t == 0) {
+    if (n >= 8) {
+      *reinterpret_cast<uint64_t*>(p) = mine;
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) p[j] = static_cast<int8_t>(mine >> (8 * j));
+    }
+    return;
+  }
+  const uint64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
+  int n_before = __shfl_up_sync(0xffffffffu, n, 1);
+  if (lane == 0) n_before = 0;
+  const int cut = 8 - static_cast<int>(t);   // bytes of a lane's own that end its first word
+  if (n_before >= 8 && n >= cut) {
+    *reinterpret_cast<uint64_t*>(p - t) = (before >> (8 * cut)) | (mine << (8 * t));
+  } else {
+#pragma unroll 1
+    for (int j = cut; j < n_before && j < 8; ++j) p[j - 8] = static_cast<int8_t>(before >> (8 * j));
+#pragma unroll 1
+    for (int j = 0; j < n && j < cut; ++j) p[j] = static_cast<int8_t>(mine >> (8 * j));
+  }
+  if (lane == 31) {
+#pragma unroll 1
+    for (int j = cut; j < n && j < 8; ++j) p[j] = static_cast<int8_t>(mine >> (8 * j));
+  }
 }
 
 // A row's scale from the encoding of its largest magnitude (of NaN where the
@@ -146,34 +288,42 @@ __device__ __forceinline__ RowPower row_power(float bound) {
   return {__uint_as_float(static_cast<uint32_t>(127 + e) << 23),
           __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
 }
+// The gated gradient's row before g and u are known: |u| and |g| are below
+//   s * 127 * 128 K * (largest ws) + (largest bias)
+// (of typical ones some 7 sqrt(K) times), |act| below |g|, |act'| below
+// kSteepest; so with the row's largest |dh| its operand has a bound.
+// tops: the gate's and the up projection's largest scale, then bias.
+__device__ __forceinline__ RowPower gated_row_power(float most_dh, float s, int64_t K,
+                                                    const float4& tops) {
+  const float acc = fabsf(s) * (16384.0f * static_cast<float>(K));
+  const float g = fmaf(acc, tops.x, tops.z), u = fmaf(acc, tops.y, tops.w);
+  return row_power(most_dh * kSteepest * fmaxf(u * tops.x, g * tops.y));
+}
 __device__ __forceinline__ uint16_t grad_bits(float v) {
   return __half_as_ushort(__float2half_rn(v));
 }
 
-// What a thread loads of a row at once: 8 values on 16-byte boundaries, or one.
-template <int DT, bool VEC>
-struct TokenItem;
-
+// Eight values of a float row.
 template <int DT>
-struct TokenItem<DT, true> {
-  static constexpr int kWidth = 8;
-  static constexpr int kWords = DT == Q8_F32 ? 8 : 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void zero() {
+using FloatOf = typename std::conditional<DT == Q8_F32, float, uint16_t>::type;
+
+template <int DT, bool VEC>
+struct TokenItem : RowItem<DT == Q8_F32 ? 8 : 4, VEC> {
+  using RowItem<DT == Q8_F32 ? 8 : 4, VEC>::w;
+  __device__ __forceinline__ void load_whole(const void* p) {   // on its boundary
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = 0;
-  }
-  __device__ __forceinline__ void load(const void* x, int64_t i) {
-    const auto* p = reinterpret_cast<const uint4*>(
-        static_cast<const uint8_t*>(x) + i * (DT == Q8_F32 ? 4 : 2));
-#pragma unroll
-    for (int j = 0; j < kWords / 4; ++j) {
-      const uint4 v = p[j];
-      w[j * 4] = v.x;
-      w[j * 4 + 1] = v.y;
-      w[j * 4 + 2] = v.z;
-      w[j * 4 + 3] = v.w;
+    for (int j = 0; j < (DT == Q8_F32 ? 8 : 4); j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + j);
+      w[j] = v.x;
+      w[j + 1] = v.y;
+      w[j + 2] = v.z;
+      w[j + 3] = v.w;
     }
+  }
+  __device__ __forceinline__ void set(int j, FloatOf<DT> v) {
+    if constexpr (DT == Q8_F32) w[j] = __float_as_uint(v);
+    else w[j / 2] = (j & 1) ? (w[j / 2] & 0xffffu) | (static_cast<uint32_t>(v) << 16)
+                            : (w[j / 2] & 0xffff0000u) | v;
   }
   __device__ __forceinline__ float value(int j) const {
     if constexpr (DT == Q8_F32) return __uint_as_float(w[j]);
@@ -199,21 +349,6 @@ struct TokenItem<DT, true> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = token_byte(value(j), inv);
     return make_uint2(four_bytes(b[0], b[1], b[2], b[3]), four_bytes(b[4], b[5], b[6], b[7]));
-  }
-};
-
-template <int DT>
-struct TokenItem<DT, false> {
-  static constexpr int kWidth = 1;
-  float v;
-  __device__ __forceinline__ void zero() { v = 0.0f; }
-  __device__ __forceinline__ void load(const void* x, int64_t i) {
-    if constexpr (DT == Q8_F32) v = static_cast<const float*>(x)[i];
-    else v = half_bits_to_float<DT>(static_cast<const uint16_t*>(x)[i]);
-  }
-  __device__ __forceinline__ uint32_t top() const { return __float_as_uint(v) & 0x7fffffffu; }
-  __device__ __forceinline__ int8_t quantize(float inv) const {
-    return static_cast<int8_t>(token_byte(v, inv));
   }
 };
 

@@ -45,16 +45,16 @@ struct GradOperandJob {
 cudaError_t launch_grad_operand(const GradOperandJob& job, q8_dtype dtype, cudaStream_t s);
 
 // What the gated gradient's kernel reads: the int8 rows' operand, each row's
-// powers of two, `counts` zeroed.
+// largest |dh|, the largest scales and biases, `counts` zeroed.
 struct GatedGradFrontJob {
   const int8_t* q;      // [M, K]
-  const float* scales;  // [M]
   const void* dh;       // [M, N]
   const float *ws, *bias;   // [2, N]; bias or null
   int64_t M, N, K;
   uint16_t* operand;    // [KB][M][64]
   int KB;
-  float *rescale, *unscale;   // [M]
+  float* most_dh;       // [M]
+  float* tops;          // [4]: of the gate's and the up projection's ws, and of their biases
   int32_t* counts;
   int count_words;
 };

@@ -19,14 +19,23 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // a = max |x[m]|, s = a / 127, q = rint(x * (1 / s)): a row twice, once for its
-// largest magnitude and once to round it.  A CTA has one row and keeps it in
-// registers in between, so it comes from memory once; only rows beyond 4 items
-// for each of 1,024 threads are read again (from L2).  Bytes bound it.
+// largest magnitude and once to round it.  A CTA has one row at a time and keeps
+// it in registers in between, with the next row's loads already on their way; so
+// it comes from memory once, and memory is never idle while a row waits for its
+// scale.  Only rows beyond U items for each of 1,024 threads are read again (from
+// L2).  Bytes bound it: 8192 rows of 11008 bf16 46 us (floor 41), of 8191 XXX.
+//   An item is 8 values on a boundary of 8.  VEC: rows are whole items.  Else a
+// row begins t values into its first item, and what belongs to its neighbours
+// counts as zeros; q, whose rows begin the same way, takes whole items too, but
+// the operand has its own: 8 - t values of an item and t of the next one, which
+// a lane gets from the lane after it (so a warp's last lane only lends).
 // ---------------------------------------------------------------------------
 template <int DT, bool VEC, bool OP>
 __global__ void __launch_bounds__(1024) quantize_token_kernel(const QuantizeJob job) {
-  using Item = TokenItem<DT, VEC>;
-  constexpr int U = VEC ? 4 : 16;
+  using Item = TokenItem<DT, true>;
+  using T = FloatOf<DT>;
+  constexpr int U = DT == Q8_F32 ? 2 : 4;
+  constexpr int kLanes = !VEC && OP ? 31 : 32;
   __shared__ uint32_t tops[2][32];
   pdl_wait();
   pdl_launch_dependents();
@@ -36,24 +45,65 @@ __global__ void __launch_bounds__(1024) quantize_token_kernel(const QuantizeJob 
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
          i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
       job.counts[i] = 0;
-  const int64_t items = job.K / Item::kWidth;
+  const auto* x = static_cast<const T*>(job.x);
+  const T* x_end = x + job.M * job.K;
+  // values that x lies behind a boundary of 8
+  const int off = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) & 7);
+  const bool q_whole = (reinterpret_cast<uintptr_t>(job.q) - off) % 8 == 0;
+  const auto ahead = [&](int64_t m) {   // t
+    return VEC ? 0 : static_cast<int>((off + m * job.K) & 7);
+  };
+  const int64_t chunks = static_cast<int64_t>(job.KB) * 8;   // of the operand's row
+  const auto load = [&](Item& it, int64_t m, int t, int64_t c) {
+    const int64_t e = c * 8 - t;   // the row's values from e on
+    const T* p = x + m * job.K + e;
+    it.zero();
+    if (e >= job.K) return;
+    if (VEC || (p >= x && p + 8 <= x_end)) {
+      it.load_whole(p);
+    } else {   // the ends of the matrix
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j >= 0 && e + j < job.K) it.set(j, p[j]);
+    }
+  };
+  const auto settle = [&](Item& it, int t, int64_t c) {
+    const int64_t e = c * 8 - t;
+    if (!VEC && (e < 0 || e + 8 > job.K)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j < 0 || e + j >= job.K) it.set(j, 0);
+    }
+  };
+  // this thread's items: every blockDim.x'th, in the 31-lane form that less its last lanes
+  const int64_t c0 = warp * kLanes + lane, step = warps * kLanes;
+  // (items that a row can reach, for whole warps to go through)
+  const int64_t items = OP ? chunks : (job.K + (VEC ? 7 : 14)) / 8;
+  Item held[U];
+  {
+    const int t = ahead(blockIdx.x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(held[u], blockIdx.x, t, c0 + u * step);
+  }
   int turn = 0;
   for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
-    const int64_t base = m * job.K;
-    Item held[U];
+    const int t = ahead(m);
+    Item next[U];
+    const int64_t m_next = m + gridDim.x;
+    const int t_next = ahead(m_next);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
-      if (c < items) held[u].load(job.x, base + c * Item::kWidth);
-      else held[u].zero();
-    }
+    for (int u = 0; u < U; ++u)
+      load(next[u], m_next, t_next, m_next < job.M ? c0 + u * step : INT64_MAX / 16);
     uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) top = max(top, held[u].top());
-    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items;
-         c += blockDim.x) {
+    for (int u = 0; u < U; ++u) {
+      settle(held[u], t, c0 + u * step);
+      top = max(top, held[u].top());
+    }
+    for (int64_t c = c0 + U * step; c * 8 - t < job.K; c += step) {
       Item it;
-      it.load(job.x, base + c * Item::kWidth);
+      load(it, m, t, c);
+      settle(it, t, c);
       top = max(top, it.top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -63,36 +113,45 @@ __global__ void __launch_bounds__(1024) quantize_token_kernel(const QuantizeJob 
     const TokenScale sc = token_scale(top);
     if (threadIdx.x == 0) job.scales[m] = sc.scale;
     const auto put = [&](const Item& it, int64_t c) {
-      if constexpr (VEC) {
-        const uint2 q = it.quantize(sc.inv);
-        if (job.q != nullptr) *reinterpret_cast<uint2*>(job.q + base + c * 8) = q;
-        if constexpr (OP)
+      const uint2 q = it.quantize(sc.inv);
+      const int64_t e = c * 8 - t;
+      if (job.q != nullptr && (kLanes == 32 || lane < kLanes)) {
+        int8_t* to = job.q + m * job.K + e;
+        if (VEC ? e < job.K : q_whole && e >= 0 && e + 8 <= job.K) {
+          *reinterpret_cast<uint2*>(to) = q;
+        } else if (!VEC) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e + j >= 0 && e + j < job.K)
+              to[j] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+        }
+      }
+      if constexpr (OP) {
+        uint2 own = q;
+        if constexpr (!VEC) {
+          const uint32_t x2 = __shfl_down_sync(0xffffffffu, q.x, 1);
+          const uint32_t y2 = __shfl_down_sync(0xffffffffu, q.y, 1);
+          const int bits = (t & 3) * 8;   // (an item's own from byte t on)
+          own = t < 4 ? make_uint2(__funnelshift_r(q.x, q.y, bits), __funnelshift_r(q.y, x2, bits))
+                      : make_uint2(__funnelshift_r(q.y, x2, bits), __funnelshift_r(x2, y2, bits));
+        }
+        if (c < chunks && (kLanes == 32 || lane < kLanes))
           *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
-              token_f16x8(q);
-      } else {
-        const int8_t q = it.quantize(sc.inv);
-        if (job.q != nullptr) job.q[base + c] = q;
-        if constexpr (OP)
-          job.operand[((c >> 6) * job.M + m) * 64 + (c & 63)] =
-              __half_as_ushort(__int2half_rn(q));
+              token_f16x8(own);
       }
     };
+    // (whole warps go through, for the shuffles)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
-      if (c < items) put(held[u], c);
-    }
-    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items;
-         c += blockDim.x) {
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * step - lane < items) put(held[u], c0 + u * step);
+    for (int64_t c = c0 + U * step; c - lane < items; c += step) {
       Item it;
-      it.load(job.x, base + c * Item::kWidth);
+      load(it, m, t, c);
+      settle(it, t, c);
       put(it, c);
     }
-    if constexpr (OP) {   // the last k-block's inputs past K
-      const int64_t k = job.K + threadIdx.x;
-      if (k < static_cast<int64_t>(job.KB) * 64)
-        job.operand[((k >> 6) * job.M + m) * 64 + (k & 63)] = 0;
-    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) held[u] = next[u];
   }
 }
 
@@ -116,45 +175,57 @@ __device__ __forceinline__ void warp_segments(int64_t M, int64_t items, F&& f) {
   }
 }
 
-// out = float(q) * s, one rounding to the type.  VEC: 8 values an item.
-template <int DT, bool VEC>
+// out = float(q) * s, one rounding to the type.  Items of 8 values on 8 (q) and
+// 16 (out) bytes: rows that are no multiple of 8 begin inside an item, which
+// both rows take, each its own values of it.  ANY: q or out lie on other bytes,
+// one value an item.
+template <int DT, bool ANY>
 __global__ void __launch_bounds__(256) dequantize_token_kernel(const int8_t* q,
                                                                const float* scales, int64_t M,
                                                                int64_t K, void* out) {
-  constexpr int U = 4, W = VEC ? 8 : 1;
+  constexpr int U = 4;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t items = K / W;
-  warp_segments<U>(M, items, [&](int64_t m, int64_t c0) {
-    const float s = scales[m];
-    const int64_t base = m * K;
-    uint2 w[U];
+  if constexpr (ANY) {
+    warp_segments<U>(M, K, [&](int64_t m, int64_t c0) {
+      const float s = scales[m];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 32;
-      if (c < items) {
-        if constexpr (VEC) w[u] = __ldcs(reinterpret_cast<const uint2*>(q + base + c * 8));
-        else w[u].x = static_cast<uint8_t>(q[base + c]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = m * K + c0 + u * 32;
+        if (c0 + u * 32 < K) store_one<DT>(out, i, __fmul_rn(static_cast<float>(q[i]), s));
       }
-    }
+    });
+  } else {
+    const int64_t whole = M * K / 8 * 8;   // items from there on end the rows
+    const int64_t items = K % 8 == 0 ? K / 8 : K / 8 + 2;
+    warp_segments<U>(M, items, [&](int64_t m, int64_t c0) {
+      const float s = scales[m];
+      const int64_t row = m * K, first = (row / 8 + c0) * 8;
+      uint2 w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 32;
-      if (c < items) {
-        if constexpr (VEC) {
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        if (i < whole && i < row + K) w[u] = __ldcs(reinterpret_cast<const uint2*>(q + i));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        if (i < whole && i >= row && i + 8 <= row + K) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             v[j] = __fmul_rn(
                 static_cast<float>(static_cast<int8_t>((j < 4 ? w[u].x : w[u].y) >> (8 * (j & 3)))),
                 s);
-          store_x8<DT>(out, base + c * 8, v);
+          store_x8<DT>(out, i, v);
         } else {
-          store_one<DT>(out, base + c, __fmul_rn(static_cast<float>(static_cast<int8_t>(w[u].x)), s));
+#pragma unroll 1
+          for (int64_t j = max(i, row); j < min(i + 8, row + K); ++j)
+            store_one<DT>(out, j, __fmul_rn(static_cast<float>(q[j]), s));
         }
       }
-    }
-  });
+    });
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -191,12 +262,18 @@ __device__ __forceinline__ uint32_t top_of(const float* v, int64_t n) {
   return top;
 }
 
-// A CTA has one row at a time in registers, 8 values an item and 4 items a
-// thread (longer rows are read a second time), and its items' scales with them.
-// With wn = ws over the power of two of the largest, |dy * wn| < 2 a.
+// A CTA has one row at a time in registers, 8 values an item and up to 4
+// items a thread (longer rows are read a second time), its items' scales with them for
+// all its rows, and the next row's loads on their way.  With wn = ws over the
+// power of two of the largest, |dy * wn| < 2 a.
+template <bool VEC, bool MASK>
+constexpr int grad_items() {   // of a thread, in registers
+  return VEC && !MASK ? 4 : VEC || !MASK ? 2 : 1;
+}
+
 template <int DT, bool VEC, bool MASK>
 __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob job) {
-  constexpr int U = 4;
+  constexpr int U = grad_items<VEC, MASK>();
   __shared__ uint32_t slots[3][32];
   pdl_wait();
   pdl_launch_dependents();
@@ -204,35 +281,56 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
        i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
     job.counts[i] = 0;
   const int64_t items = static_cast<int64_t>(job.KB) * 8;
-  const auto* dy = static_cast<const uint16_t*>(job.dy);
-  const auto* y = static_cast<const uint16_t*>(job.y);
-  // (a power of two of the largest scale in [1, 2))
-  const RowPower channel = row_power(__uint_as_float(block_max(top_of(job.ws, job.N), slots[2])));
-  const float to_one = channel.rescale * 0x1p-14f, from_one = channel.unscale * 0x1p14f;
-  float held_ws[U][8];
+  using Item = RowItem<4, VEC>;
+  constexpr int V = MASK ? 2 : 1;   // dy, y
+  const int64_t bytes = job.N * 2;
   const auto load_ws = [&](int64_t c, float (&ws)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) * to_one : 0.0f;
+    for (int j = 0; j < 8; ++j) ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) : 0.0f;
   };
-  const auto load = [&](int64_t m, int64_t c) {
-    uint4 v = load_halves<VEC>(dy, m * job.N, c * 8, job.N);
+  const auto load = [&](Item (&it)[V], int64_t m, int64_t c) {
+    const int64_t n = m < job.M ? bytes : 0;
+    it[0].load(row_bytes<uint16_t>(job.dy, job.M, job.N, m), c, n);
+    if constexpr (MASK) it[1].load(row_bytes<uint16_t>(job.y, job.M, job.N, m), c, n);
+  };
+  const auto settle = [&](Item (&it)[V], int64_t m, int64_t c) {
+    it[0].settle(row_bytes<uint16_t>(job.dy, job.M, job.N, m), c, bytes);
     if constexpr (MASK) {
-      const uint4 a = load_halves<VEC>(y, m * job.N, c * 8, job.N);
-      v.x &= above_zero<DT>(a.x);
-      v.y &= above_zero<DT>(a.y);
-      v.z &= above_zero<DT>(a.z);
-      v.w &= above_zero<DT>(a.w);
+      it[1].settle(row_bytes<uint16_t>(job.y, job.M, job.N, m), c, bytes);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) it[0].w[j] &= above_zero<DT>(it[1].w[j]);
     }
-    return v;
   };
-  const auto top16 = [&](uint4 v) {
-    const uint32_t t = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  const auto load_row = [&](Item (&held)[U][V], int64_t m) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(held[u], m, threadIdx.x + static_cast<int64_t>(u) * blockDim.x);
+  };
+  const auto top16 = [&](const Item& it) {
+    const uint32_t t = __vmaxu2(__vmaxu2(it.w[0] & 0x7fff7fffu, it.w[1] & 0x7fff7fffu),
+                                __vmaxu2(it.w[2] & 0x7fff7fffu, it.w[3] & 0x7fff7fffu));
     return magnitude(half_bits_to_float<DT>(max(t & 0xffffu, t >> 16)));
   };
-  const auto put = [&](int64_t m, int64_t c, uint4 v, const float (&ws)[8], float rescale) {
-    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+  Item held[U][V];
+  float held_ws[U][8];
+  load_row(held, blockIdx.x);
+  uint32_t ws_top = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) load_ws(threadIdx.x + static_cast<int64_t>(u) * blockDim.x, held_ws[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ws_top = max(ws_top, magnitude(held_ws[u][j]));
+  const int64_t held_to = static_cast<int64_t>(U) * 8 * blockDim.x;
+  if (held_to < job.N) ws_top = max(ws_top, top_of(job.ws + held_to, job.N - held_to));
+  // (a power of two of the largest scale in [1, 2))
+  const RowPower channel = row_power(__uint_as_float(block_max(ws_top, slots[2])));
+  const float to_one = channel.rescale * 0x1p-14f, from_one = channel.unscale * 0x1p14f;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) held_ws[u][j] *= to_one;
+  const auto put = [&](int64_t m, int64_t c, const Item& it, const float (&ws)[8], float rescale) {
+    const auto& d = it.w;
     uint32_t r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -243,93 +341,104 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
     *reinterpret_cast<uint4*>(job.dst + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
         make_uint4(r[0], r[1], r[2], r[3]);
   };
-#pragma unroll
-  for (int u = 0; u < U; ++u) load_ws(threadIdx.x + static_cast<int64_t>(u) * blockDim.x, held_ws[u]);
   int turn = 0;
   for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
-    uint4 held[U];
+    Item next[U][V];
+    load_row(next, m + gridDim.x);
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
-      held[u] = c < items ? load(m, c) : make_uint4(0, 0, 0, 0);
+      settle(held[u], m, threadIdx.x + static_cast<int64_t>(u) * blockDim.x);
+      top = max(top, top16(held[u][0]));
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) top = max(top, top16(held[u]));
-    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items; c += blockDim.x)
-      top = max(top, top16(load(m, c)));
+    for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items; c += blockDim.x) {
+      Item it[V];
+      load(it, m, c);
+      settle(it, m, c);
+      top = max(top, top16(it[0]));
+    }
     // the row's largest between 2^13 and 2^14, times |wn| < 2
     const RowPower row = row_power(2.0f * __uint_as_float(block_max(top, slots[turn])));
     if (threadIdx.x == 0) job.unscale[m] = row.unscale * from_one;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t c = threadIdx.x + static_cast<int64_t>(u) * blockDim.x;
-      if (c < items) put(m, c, held[u], held_ws[u], row.rescale);
+      if (c < items) put(m, c, held[u][0], held_ws[u], row.rescale);
     }
     for (int64_t c = threadIdx.x + static_cast<int64_t>(U) * blockDim.x; c < items;
          c += blockDim.x) {
       float ws[8];
       load_ws(c, ws);
-      put(m, c, load(m, c), ws, row.rescale);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ws[j] *= to_one;
+      Item it[V];
+      load(it, m, c);
+      settle(it, m, c);
+      put(m, c, it[0], ws, row.rescale);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v) held[u][v] = next[u][v];
   }
 }
 
-// The gated gradient's rows before g and u are known: |u| and |g| are below
-//   s[m] * 127 * 128 K * (largest ws) + (largest bias)
-// (of typical ones some 7 sqrt(K) times), |act| below |g|, |act'| below
-// kSteepest; so with the row's largest |dh| its operand has a bound.
+// What the gated gradient's kernel reads beside the weights: the int8 rows as its
+// operand, each row's largest |dh|, and from the last CTA the largest scales and
+// biases.  A row's loads are all in flight before any is used.
 template <int DT, bool VEC_Q, bool VEC_DH>
 __global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFrontJob job) {
-  __shared__ uint32_t slots[6][32];
+  constexpr int UD = 4, UQ = 2;
+  __shared__ uint32_t slots[4][32];
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
        i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
     job.counts[i] = 0;
-  float top[4];   // of the gate's and the up projection's scales, and of their biases
+  if (blockIdx.x == gridDim.x - 1) {
+    uint32_t top[4];   // of the gate's and the up projection's scales, and of their biases
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float* v = i < 2 ? job.ws : job.bias;
-    top[i] = v == nullptr ? 0.0f
-                          : __uint_as_float(block_max(top_of(v + (i & 1) * job.N, job.N), slots[i]));
+    for (int i = 0; i < 4; ++i) {
+      const float* v = i < 2 ? job.ws : job.bias;
+      top[i] = v == nullptr ? 0u : block_max(top_of(v + (i & 1) * job.N, job.N), slots[i]);
+    }
+    if (threadIdx.x == 0)
+      *reinterpret_cast<uint4*>(job.tops) = make_uint4(top[0], top[1], top[2], top[3]);
+    return;
   }
-  const float most = 16384.0f * static_cast<float>(job.K);   // |sum| of int8 products
-  const auto* dh = static_cast<const uint16_t*>(job.dh);
-  const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8;
+  const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8, bytes = job.N * 2;
+  const int8_t* q_end = job.q + job.M * job.K;
   int turn = 0;
-  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
+  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x - 1, turn ^= 1) {
     uint32_t t = 0;
-#pragma unroll 4
-    for (int64_t c = threadIdx.x; c < items; c += blockDim.x) {
-      const uint4 v = load_halves<VEC_DH>(dh, m * job.N, c * 8, job.N);
-      t = __vmaxu2(t, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-    }
-#pragma unroll 2
-    for (int64_t c = threadIdx.x; c < chunks; c += blockDim.x) {
-      const int8_t* src = job.q + m * job.K + c * 8;
-      uint2 w = make_uint2(0, 0);
-      if constexpr (VEC_Q) {
-        if (c * 8 < job.K) w = *reinterpret_cast<const uint2*>(src);
-      } else {
+    const RowBytes row = row_bytes<uint16_t>(job.dh, job.M, job.N, m);
+    for (int64_t c0 = threadIdx.x; c0 < items; c0 += static_cast<int64_t>(UD) * blockDim.x) {
+      RowItem<4, VEC_DH> it[UD];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c * 8 + j < job.K)
-            (j < 4 ? w.x : w.y) |= static_cast<uint32_t>(static_cast<uint8_t>(src[j])) << (8 * (j & 3));
+      for (int u = 0; u < UD; ++u) it[u].load(row, c0 + static_cast<int64_t>(u) * blockDim.x, bytes);
+#pragma unroll
+      for (int u = 0; u < UD; ++u) {
+        it[u].settle(row, c0 + static_cast<int64_t>(u) * blockDim.x, bytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t = __vmaxu2(t, it[u].w[j] & 0x7fff7fffu);
       }
-      *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
-          token_f16x8(w);
     }
-    const uint32_t most_dh =
-        block_max(magnitude(half_bits_to_float<DT>(max(t & 0xffffu, t >> 16))), slots[4 + turn]);
-    if (threadIdx.x == 0) {
-      const float acc = fabsf(job.scales[m]) * most;
-      const float g = fmaf(acc, top[0], top[2]), u = fmaf(acc, top[1], top[3]);
-      const RowPower row = row_power(__uint_as_float(most_dh) * kSteepest * fmaxf(u * top[0], g * top[1]));
-      job.rescale[m] = row.rescale;
-      job.unscale[m] = row.unscale;
+    for (int64_t c0 = threadIdx.x; c0 < chunks; c0 += static_cast<int64_t>(UQ) * blockDim.x) {
+      uint2 w[UQ];
+#pragma unroll
+      for (int u = 0; u < UQ; ++u) w[u] = load_int8x8<VEC_Q>(job.q, m * job.K, (c0 + static_cast<int64_t>(u) * blockDim.x) * 8,
+                                  job.K, q_end);
+#pragma unroll
+      for (int u = 0; u < UQ; ++u) {
+        const int64_t c = c0 + static_cast<int64_t>(u) * blockDim.x;
+        if (c < chunks)
+          *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
+              token_f16x8(w[u]);
+      }
     }
+    const uint32_t most =
+        block_max(magnitude(half_bits_to_float<DT>(max(t & 0xffffu, t >> 16))), slots[turn]);
+    if (threadIdx.x == 0) job.most_dh[m] = __uint_as_float(most);
   }
 }
 
@@ -396,12 +505,14 @@ cudaError_t by_half(q8_dtype dt, bool vec, F&& f) {
 cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaStream_t s) {
   const bool vec = job.K % 8 == 0 && on16(job.x) && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
   // One item a thread while there are few rows (its latency is what counts),
-  // else four, whose loads are in flight together.
-  const int64_t items = vec ? job.K / 8 : job.K;
-  const int64_t each = job.M <= 2 * device_sm_count() ? 1 : vec ? 4 : 8;
-  const int threads = static_cast<int>(
-      std::min<int64_t>(1024, std::max<int64_t>(64, round_up((items + each - 1) / each, 32))));
-  const int grid = static_cast<int>(std::min<int64_t>(job.M, INT32_MAX));
+  // else as many as it holds, and as many CTAs as the SMs take at once.
+  const int64_t items = job.operand != nullptr ? static_cast<int64_t>(job.KB) * 8 : job.K / 8 + 2;
+  const int64_t each = job.M <= 2 * device_sm_count() ? 1 : dtype == Q8_F32 ? 2 : 4;
+  const int64_t lanes = job.operand != nullptr && !vec ? 31 : 32;
+  const int64_t warps = (items + each * lanes - 1) / (each * lanes);
+  const int threads = static_cast<int>(std::min<int64_t>(32, std::max<int64_t>(2, warps))) * 32;
+  const int grid = static_cast<int>(
+      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / threads)));
   return by_type(dtype, vec, [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
@@ -413,10 +524,10 @@ cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaSt
 
 cudaError_t launch_dequantize_token(const int8_t* q, const float* scales, int64_t M, int64_t K,
                                     q8_dtype dtype, void* out, cudaStream_t s) {
-  const bool vec = K % 8 == 0 && on16(out) && reinterpret_cast<uintptr_t>(q) % 8 == 0;
-  const int64_t items = vec ? K / 8 : K;
+  const bool any = !on16(out) || reinterpret_cast<uintptr_t>(q) % 8 != 0;
+  const int64_t items = any ? K : K % 8 == 0 ? K / 8 : K / 8 + 2;
   const int grid = blocks_for(M * ((items + 127) / 128));
-  return by_type(dtype, vec, [&](auto t, auto v) {
+  return by_type(dtype, any, [&](auto t, auto v) {
     return launch_pdl(dequantize_token_kernel<decltype(t)::value, decltype(v)::value>, grid, 256, 0,
                       s, q, scales, M, K, out);
   });
@@ -425,11 +536,12 @@ cudaError_t launch_dequantize_token(const int8_t* q, const float* scales, int64_
 cudaError_t launch_grad_operand(const GradOperandJob& job, q8_dtype dtype, cudaStream_t s) {
   const bool vec = job.N % 8 == 0 && on16(job.dy) && on16(job.y);
   const int64_t items = static_cast<int64_t>(job.KB) * 8;
-  const int64_t each = job.M <= 2 * device_sm_count() ? 1 : 4;
+  const int64_t each =
+      job.M <= 2 * device_sm_count() ? 1 : vec && !job.y ? 4 : vec || !job.y ? 2 : 1;   // as grad_items
   const int threads = static_cast<int>(
       std::min<int64_t>(512, std::max<int64_t>(64, round_up((items + each - 1) / each, 32))));
   const int grid = static_cast<int>(
-      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * (1024 / threads)));
+      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * std::max(1, 512 / threads)));
   const auto go = [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
@@ -442,12 +554,16 @@ cudaError_t launch_grad_operand(const GradOperandJob& job, q8_dtype dtype, cudaS
 cudaError_t launch_gated_grad_front(const GatedGradFrontJob& job, q8_dtype dtype, cudaStream_t s) {
   const bool vec_dh = job.N % 8 == 0 && on16(job.dh);
   const bool vec_q = job.K % 8 == 0 && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
-  const int grid = static_cast<int>(std::min<int64_t>(job.M, device_sm_count() * 2));
+  // 4 items of dh a thread, and as many CTAs as the SMs take at once
+  const int threads = static_cast<int>(
+      std::min<int64_t>(512, std::max<int64_t>(64, round_up((job.N + 31) / 32, 32))));
+  const int grid = 1 + static_cast<int>(std::min<int64_t>(
+                           job.M, static_cast<int64_t>(device_sm_count()) * (2048 / threads)));
   return by_half(dtype, vec_dh, [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
-    return vec_q ? launch_pdl(gated_grad_front_kernel<DT, true, VEC>, grid, 512, 0, s, job)
-                 : launch_pdl(gated_grad_front_kernel<DT, false, VEC>, grid, 512, 0, s, job);
+    return vec_q ? launch_pdl(gated_grad_front_kernel<DT, true, VEC>, grid, threads, 0, s, job)
+                 : launch_pdl(gated_grad_front_kernel<DT, false, VEC>, grid, threads, 0, s, job);
   });
 }
 

@@ -97,29 +97,37 @@ __device__ __forceinline__ void stage_rows(const TokenRowsJob& job, RowsShared& 
           *reinterpret_cast<uint4*>(dst + c * 16) = v;
         }
       } else {
+        const int8_t* all = static_cast<const int8_t*>(job.x);
 #pragma unroll 4
-        for (int k = part; k < padded; k += step)
-          dst[k] = (k < job.K ? static_cast<uint8_t>(src[k]) : 0) ^ static_cast<uint8_t>(kFlip);
+        for (int c = part; c < padded / 8; c += step) {
+          uint2 v = load_int8x8<false>(all, base, static_cast<int64_t>(c) * 8, job.K, all + M * job.K);
+          v.x ^= kFlip;
+          v.y ^= kFlip;
+          *reinterpret_cast<uint2*>(dst + c * 8) = v;
+        }
       }
     }
   } else {
     using Item = TokenItem<DT, VEC>;
-    constexpr int W = Item::kWidth, U = DT == Q8_F32 && VEC ? 2 : 3;
-    const int items = mine ? static_cast<int>(job.K) / W : 0;
+    constexpr int U = DT == Q8_F32 || !VEC ? 1 : 2;
+    // items of 8 up to the end of the last k-block, by whole warps
+    const int items = mine ? padded / 8 : 0;
+    const int64_t bytes = mine ? job.K * static_cast<int64_t>(sizeof(FloatOf<DT>)) : 0;
+    const RowBytes row = row_bytes<FloatOf<DT>>(job.x, M, job.K, mine ? m : 0);
     Item held[U];
     uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = part + u * step;
-      if (c < items) held[u].load(job.x, base + c * W);
-      else held[u].zero();
-    }
+    for (int u = 0; u < U; ++u) held[u].load(row, part + u * step, bytes);
 #pragma unroll
-    for (int u = 0; u < U; ++u) top = max(top, held[u].top());
-#pragma unroll 2
+    for (int u = 0; u < U; ++u) {
+      held[u].settle(row, part + u * step, bytes);
+      top = max(top, held[u].top());
+    }
+#pragma unroll 1
     for (int c = part + U * step; c < items; c += step) {
       Item it;
-      it.load(job.x, base + c * W);
+      it.load(row, c, bytes);
+      it.settle(row, c, bytes);
       top = max(top, it.top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -132,31 +140,26 @@ __device__ __forceinline__ void stage_rows(const TokenRowsJob& job, RowsShared& 
       if (blockIdx.x == 0 && job.scales != nullptr) job.scales[m] = sc.scale;
     }
     const auto put = [&](const Item& it, int c) {
-      if constexpr (VEC) {
-        uint2 q = it.quantize(sc.inv);
-        if (blockIdx.x == 0 && job.q != nullptr)
-          *reinterpret_cast<uint2*>(job.q + base + c * 8) = q;
+      uint2 q = it.quantize(sc.inv);   // (zeros past K)
+      if (blockIdx.x == 0 && job.q != nullptr)
+        store_bytes_any(job.q + base + c * 8, q,
+                        static_cast<int>(min(int64_t{8}, job.K - static_cast<int64_t>(c) * 8)));
+      if (c < items) {
         q.x ^= kFlip;
         q.y ^= kFlip;
         *reinterpret_cast<uint2*>(dst + c * 8) = q;
-      } else {
-        const int8_t q = it.quantize(sc.inv);
-        if (blockIdx.x == 0 && job.q != nullptr) job.q[base + c] = q;
-        dst[c] = static_cast<uint8_t>(q) ^ static_cast<uint8_t>(kFlip);
       }
     };
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (part + u * step < items) put(held[u], part + u * step);
-#pragma unroll 2
-    for (int c = part + U * step; c < items; c += step) {
+      if (part - lane + u * step < items) put(held[u], part + u * step);
+#pragma unroll 1
+    for (int c = part + U * step; c - lane < items; c += step) {
       Item it;
-      it.load(job.x, base + c * W);
+      it.load(row, c, bytes);
+      it.settle(row, c, bytes);
       put(it, c);
     }
-    if (mine)
-      for (int k = static_cast<int>(job.K) + part; k < padded; k += step)
-        dst[k] = static_cast<uint8_t>(kFlip);
   }
   __syncthreads();
 }
@@ -374,9 +377,8 @@ cudaError_t launch_token_rows(TokenRowsJob job, bool gated, cudaStream_t s) {
   job.KB = static_cast<int>((job.K + 63) / 64);
   job.stride = static_cast<int>(token_rows_stride(job.K));
   job.units = static_cast<int>(gated ? (job.N + 7) / 8 : (job.N + 15) / 16);
-  const int64_t bytes = dtype_bytes(job.x_dtype), wide = job.x_dtype == Q8_I8 ? 16 : 8;
-  job.vec = job.K % wide == 0 && reinterpret_cast<uintptr_t>(job.x) % 16 == 0 &&
-            job.K * bytes % 16 == 0 && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
+  // (VEC's items of 8 float values, or 16 int8 ones, are whole)
+  job.vec = job.K % (job.x_dtype == Q8_I8 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(job.x) % 16 == 0;
   return gated ? launch_by_rows<true>(job, s) : launch_by_rows<false>(job, s);
 }
 
