@@ -384,10 +384,10 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
 }
 
 // What the gated gradient's kernel reads beside the weights: the int8 rows as its
-// operand, each row's largest |dh|, and from the last CTA the largest scales and
+// operand, each row's largest |dh|, and from the first CTA the largest scales and
 // biases.  A row's loads are all in flight before any is used.
 template <int DT, bool VEC_Q, bool VEC_DH>
-__global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFrontJob job) {
+__global__ void __launch_bounds__(512, 3) gated_grad_front_kernel(const GatedGradFrontJob job) {
   constexpr int UD = 4, UQ = 2;
   __shared__ uint32_t slots[4][32];
   pdl_wait();
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFr
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
        i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
     job.counts[i] = 0;
-  if (blockIdx.x == gridDim.x - 1) {
+  if (blockIdx.x == 0) {
     uint32_t top[4];   // of the gate's and the up projection's scales, and of their biases
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -409,9 +409,10 @@ __global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFr
   const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8, bytes = job.N * 2;
   const int8_t* q_end = job.q + job.M * job.K;
   int turn = 0;
-  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x - 1, turn ^= 1) {
+  for (int64_t m = blockIdx.x - 1; m < job.M; m += gridDim.x - 1, turn ^= 1) {
     uint32_t t = 0;
     const RowBytes row = row_bytes<uint16_t>(job.dh, job.M, job.N, m);
+#pragma unroll 1
     for (int64_t c0 = threadIdx.x; c0 < items; c0 += static_cast<int64_t>(UD) * blockDim.x) {
       RowItem<4, VEC_DH> it[UD];
 #pragma unroll
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(512) gated_grad_front_kernel(const GatedGradFr
         for (int j = 0; j < 4; ++j) t = __vmaxu2(t, it[u].w[j] & 0x7fff7fffu);
       }
     }
+#pragma unroll 1
     for (int64_t c0 = threadIdx.x; c0 < chunks; c0 += static_cast<int64_t>(UQ) * blockDim.x) {
       uint2 w[UQ];
 #pragma unroll
@@ -556,9 +558,9 @@ cudaError_t launch_gated_grad_front(const GatedGradFrontJob& job, q8_dtype dtype
   const bool vec_q = job.K % 8 == 0 && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
   // 4 items of dh a thread, and as many CTAs as the SMs take at once
   const int threads = static_cast<int>(
-      std::min<int64_t>(512, std::max<int64_t>(64, round_up((job.N + 31) / 32, 32))));
+      std::min<int64_t>(512, std::max<int64_t>(256, round_up((job.N + 31) / 32, 32))));
   const int grid = 1 + static_cast<int>(std::min<int64_t>(
-                           job.M, static_cast<int64_t>(device_sm_count()) * (2048 / threads)));
+                           job.M, static_cast<int64_t>(device_sm_count()) * (1536 / threads)));
   return by_half(dtype, vec_dh, [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
