@@ -60,7 +60,9 @@ inline int64_t tile_time(int64_t R, int64_t N, int64_t K, int TN, int grid, int 
   const int64_t blocks = (N + 127) / 128, tiles = (R + TN - 1) / TN;
   const int64_t rows = ((R + tiles - 1) / tiles + 15) / 16 * 16;
   const int64_t units = tiles * (wide ? (blocks + 1) / 2 : blocks), full = units / ctas;
-  const int64_t waves = units == full * ctas ? full : std::max<int64_t>(full - 1, 0);
+  const int64_t behind = units - full * ctas;
+  const int64_t waves =
+      behind == 0 || behind >= ctas / 4 ? full : std::max<int64_t>(full - 1, 0);
   const int64_t rest = units - waves * ctas, total = rest * KB;
   int64_t line = 0, ends = 0, parts = 0;   // k-blocks, units and parts to join
   if (rest > 0) {
