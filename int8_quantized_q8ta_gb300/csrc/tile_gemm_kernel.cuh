@@ -449,11 +449,12 @@ __device__ __forceinline__ typename OutType<OUT>::type finish(float v, const Til
 }
 
 // The epilogue of rows with a scale for each token: a warp's 32 channels and
-// `mine` columns from col0 on of one unit, whose sums acc holds.
+// `mine` columns from col0 on of one unit, whose sums acc holds.  my_dh: the gated
+// gradient's 16 channels of each column, in shared memory.
 template <int OUT, int COLS, TileForm FORM>
 __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& sg,
                                                int32_t (&acc)[COLS], int nb, int quarter, int col0,
-                                               int mine) {
+                                               int mine, const uint16_t* my_dh) {
   using T = typename OutType<OUT>::type;
   constexpr bool kPairs = FORM != kFormToken;
   const int lane = threadIdx.x & 31;
@@ -516,36 +517,25 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
       }
       const float ws_other = __shfl_xor_sync(0xffffffffu, ws, 16);
       const float wg = up ? ws_other : ws, wu = up ? ws : ws_other;
-      const uint16_t* dh = static_cast<const uint16_t*>(p.dh) +
-                           static_cast<int64_t>(at + mine_j) * p.N + n;
+      const uint16_t* dh = my_dh + mine_j * 16 + (lane & 15);
       // K-blocked, in the order of the packed rows: 64 a block
       uint16_t* to = p.operand_out +
                      ((static_cast<int64_t>(nb) * 2 + (quarter >> 1)) * p.R + at + mine_j) * 64 +
                      (quarter & 1) * 32 + (lane & 15);
       // (the block that an odd count repeats for a pair has no place there)
       const int rows = nb < p.NB ? mine - mine_j : 0;
-      constexpr int kAtOnce = 8;   // loads in flight
 #pragma unroll
-      for (int j0 = 0; j0 < COLS; j0 += 2 * kAtOnce) {
-        uint16_t d[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int j = j0 + 2 * i;
-          d[i] = in && j < rows ? dh[static_cast<int64_t>(j) * p.N] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int j = j0 + 2 * i;
-          float g, u, slope;
-          pair(j, g, u);
-          const float a = activate<true>(g, p.act, slope);
-          const float r = __shfl_sync(0xffffffffu, j < 32 ? r0 : r1, (j & 31) + mine_j);
-          const float v = half_bits_to_float<OUT>(d[i]);
-          if (j < rows) {
-            // channels past the last hold zeros, whatever the rows' scales are
-            to[j * 64] = in ? grad_bits(v * u * slope * wg * r) : 0;
-            to[j * 64 + 16] = in ? grad_bits(v * a * wu * r) : 0;
-          }
+      for (int j = 0; j < COLS; j += 2) {
+        float g, u, slope;
+        pair(j, g, u);
+        const float a = activate<true>(g, p.act, slope);
+        const float r = __shfl_sync(0xffffffffu, j < 32 ? r0 : r1, (j & 31) + mine_j);
+        const float v = half_bits_to_float<OUT>(dh[j * 16]) * r;
+        // channels past the last hold zeros, whatever the rows' scales are
+        const uint32_t both = in ? grad_bits_x2(v * u * slope * wg, v * a * wu) : 0;
+        if (j < rows) {
+          to[j * 64] = static_cast<uint16_t>(both);
+          to[j * 64 + 16] = static_cast<uint16_t>(both >> 16);
         }
       }
     }
@@ -997,6 +987,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     const int chunk = chunk_stages_of<KD, kFloat>(p);
     const int me = blockIdx.x / CG;
+    // the gated gradient: this warp's columns of dh, behind the ring
+    auto* my_dh = reinterpret_cast<uint16_t*>(dyn + (ring0 - smem_u32(dyn)) +
+                                              static_cast<size_t>(S) * stage_bytes) +
+                  ew * (kCols * 16);
     // a CTA's parts: [head of its run, tail, adapter term][kPart]; a warp's
     // words in it as [16 columns][4][lane][4]
     const auto part_at = [&](int cluster, int which) {
@@ -1031,12 +1025,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         pdl_wait();
       }
       if constexpr (FORM == kFormGatedGrad) {
-        // this part's dh on its way to L2 before the epilogue wants it: 32 bytes
-        // of each of its rows
-        const int64_t n0 = static_cast<int64_t>(nb) * 64 + quarter * 16;
+        // This part's dh on its way to shared memory while the MMAs run: loads
+        // from the epilogue wait behind their tokens and weights (1024 rows x
+        // 11008 x 4096: 170 us four at a time, 137 eight).
+        __syncwarp();   // the part before has been read
+        const int64_t n0 = static_cast<int64_t>(nb) * 64 + quarter * 16 + (lane & 1) * 8;
         const auto* dh = static_cast<const uint16_t*>(p.dh) +
-                         static_cast<int64_t>(sg->row0 + col0) * p.N + min(n0, int64_t{p.N - 1});
-        for (int j = lane; j < mine; j += 32) prefetch_l2(dh + static_cast<int64_t>(j) * p.N);
+                         static_cast<int64_t>(sg->row0 + col0) * p.N + n0;
+        const bool whole = p.N % 8 == 0 && reinterpret_cast<uintptr_t>(p.dh) % 16 == 0;
+        for (int j = lane >> 1; j < mine; j += 16) {
+          uint16_t* to = my_dh + j * 16 + (lane & 1) * 8;
+          const uint16_t* from = dh + static_cast<int64_t>(j) * p.N;
+          if (whole) {
+            if (n0 < p.N) cp_async16(smem_u32(to), from);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n0 + i < p.N) to[i] = from[i];
+          }
+        }
+        cp_async_commit();
       }
       // Few rows an adapter: each row's own dot products, put into TMEM columns
       // of their own while the unit's MMAs run
@@ -1199,7 +1207,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if constexpr (FORM == kFormToken || FORM == kFormGated || FORM == kFormGatedGrad) {
-        if (last && mine > 0) token_epilogue<OUT, kCols, FORM>(p, *sg, acc, nb, quarter, col0, mine);
+        if constexpr (FORM == kFormGatedGrad) {
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+        if (last && mine > 0)
+          token_epilogue<OUT, kCols, FORM>(p, *sg, acc, nb, quarter, col0, mine, my_dh);
         first_seg = false;
         continue;
       }
@@ -1302,6 +1315,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       first_seg = false;
     }
+    if constexpr (FORM == kFormGatedGrad) cp_async_wait<0>();   // (where the loop was left early)
     if (first_seg) pdl_wait();
     // rows of dropped slots hold zeros
     if (prefix != nullptr) {
@@ -1393,7 +1407,10 @@ cudaError_t launch_form(TileParams p, const void* operand, q8_dtype out_dtype, c
     if (!encode_bf16_tmap(&map_h, p.h, 3, dims_h, str_h, box_h)) return cudaErrorInvalidValue;
   }
   const size_t stage = static_cast<size_t>(F::KD) * (p.TN / F::CG * 128 + kTileWBytes);
-  const size_t table = p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4 : 0;
+  // behind the ring: tiles before each group, or the epilogue's dh
+  const size_t table = FORM == kFormGatedGrad  ? static_cast<size_t>(F::kEpi) * F::kCols * 32
+                       : p.offsets != nullptr ? (static_cast<size_t>(p.E) + 1) * 4
+                                              : 0;
   p.stages = static_cast<int>(std::min<size_t>(F::kRing, (kTileSmem - 1024 - table) / stage));
   const size_t smem = 1024 + table + static_cast<size_t>(p.stages) * stage;
   constexpr bool kSixteen = FORM == kFormGatedGrad || FORM == kFormGrad;

@@ -299,8 +299,10 @@ __device__ __forceinline__ RowPower gated_row_power(float most_dh, float s, int6
   const float g = fmaf(acc, tops.x, tops.z), u = fmaf(acc, tops.y, tops.w);
   return row_power(most_dh * kSteepest * fmaxf(u * tops.x, g * tops.y));
 }
-__device__ __forceinline__ uint16_t grad_bits(float v) {
-  return __half_as_ushort(__float2half_rn(v));
+// Two numbers in f16, the first in the low half: one conversion.
+__device__ __forceinline__ uint32_t grad_bits_x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Eight values of a float row.

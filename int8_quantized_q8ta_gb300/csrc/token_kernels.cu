@@ -334,10 +334,8 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
     uint32_t r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      r[j] = grad_bits(half_bits_to_float<DT>(d[j] & 0xffffu) * rescale * ws[2 * j]) |
-             (static_cast<uint32_t>(
-                  grad_bits(half_bits_to_float<DT>(d[j] >> 16) * rescale * ws[2 * j + 1]))
-              << 16);
+      r[j] = grad_bits_x2(half_bits_to_float<DT>(d[j] & 0xffffu) * rescale * ws[2 * j],
+                          half_bits_to_float<DT>(d[j] >> 16) * rescale * ws[2 * j + 1]);
     *reinterpret_cast<uint4*>(job.dst + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
         make_uint4(r[0], r[1], r[2], r[3]);
   };
