@@ -115,6 +115,13 @@ struct Form {
   static constexpr int kAcc = PAIR ? 2 : 3;
   static constexpr int kRing = PAIR ? kMaxRing : 6;   // stages at most
   static constexpr int kFirstEpi = kFirstConv + kConv;
+  // Registers of a thread by its part, out of kRegs at launch: what spills finds
+  // no L1 beside this much shared memory, and waits behind tokens and weights.
+  static constexpr int kControlRegs = 56, kConvRegs = 88, kEpiRegs = PAIR ? 112 : 120;
+  static constexpr int kRegs = 96;
+  static_assert((kControlRegs * kFirstConv + kConvRegs * kConv + kEpiRegs * kEpi) * 32 <=
+                    kRegs * kTileThreads,
+                "no more than the block was launched with: it would wait for ever");
   static_assert(32 * (kFirstEpi + kEpi) == kTileThreads, "one block size");
   static constexpr int kMaxRows = kCols * kEpi / 4;
   static_assert(kMaxRows == (PAIR ? kMaxTileRows : kMaxNarrowRows), "tile heights");
@@ -542,6 +549,13 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
   }
 }
 
+// A warpgroup's registers from here on.
+template <int N>
+__device__ __forceinline__ void split_registers() {
+  if constexpr (N < Form<true>::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two halves of a token tile have rows that are multiples of 8.
 template <int OUT, bool PAIR, TileForm FORM>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -632,233 +646,237 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile uint32_t* abort_flag = &sh.abort;
   const int tiles = sh.tiles;
 
-  if (warp == 0) {
-    // ---- weights: one elected lane of a warp that runs in step ---------------
-    // (a stage's two copies come from two warps: issuing one takes some 200
-    // cycles, and a wide stage lasts 384)
-    Feed feed{sh};
-    const Seg* sg;
-    const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
-    const uint32_t wfull0 = smem_u32(&sh.wfull[0]), empty0 = smem_u32(&sh.empty[0]);
-    // (the weights of a single group need nothing of the kernel before this
-    // one: a packed weight is written at load time)
-    Ring ring;
-    int it = 0;
-    bool ok = true;
-    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
-      // (an odd last block of a pair repeats the one before and stores nothing)
-      const int nb = min(uniform(sg->nb) * CG + rank, p.NB - 1);
-      const int kb1 = uniform(sg->kb1);
-      const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg->e)) * p.NB + nb) * w_rows;
-      for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
-        const uint32_t bytes = min(KD, kb1 - kb) * kTileWBytes;
-        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
-                            p.err);
-        if (!ok) break;
-        if (elect_one()) {
-          const uint32_t bar = wfull0 + ring.slot * 8;
-          mbar_arrive_expect_tx(bar, bytes);
-          bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes,
-                    w + static_cast<int64_t>(kb) * kTileWBytes, bytes, bar);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      const int na = kBatch ? uniform(sg->na) : 0;
-      if (na > 0) pdl_wait();
-      const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
-      for (int i = 0; i < na && ok; ++i) {
-        const int64_t at = static_cast<int64_t>(uniform(list[i])) * p.NB + nb;
-        const uint8_t* lb = p.lora_b + at * p.rank16 * 4096;
-        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+  if (warp < kFirstConv) {
+    split_registers<F::kControlRegs>();
+    if (warp == 0) {
+      // ---- weights: one elected lane of a warp that runs in step ---------------
+      // (a stage's two copies come from two warps: issuing one takes some 200
+      // cycles, and a wide stage lasts 384)
+      Feed feed{sh};
+      const Seg* sg;
+      const int64_t w_rows = static_cast<int64_t>(p.KB) * kTileWBytes;
+      const uint32_t wfull0 = smem_u32(&sh.wfull[0]), empty0 = smem_u32(&sh.empty[0]);
+      // (the weights of a single group need nothing of the kernel before this
+      // one: a packed weight is written at load time)
+      Ring ring;
+      int it = 0;
+      bool ok = true;
+      while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+        // (an odd last block of a pair repeats the one before and stores nothing)
+        const int nb = min(uniform(sg->nb) * CG + rank, p.NB - 1);
+        const int kb1 = uniform(sg->kb1);
+        const uint8_t* w = p.w + (static_cast<int64_t>(uniform(sg->e)) * p.NB + nb) * w_rows;
+        for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
+          const uint32_t bytes = min(KD, kb1 - kb) * kTileWBytes;
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
           if (!ok) break;
           if (elect_one()) {
             const uint32_t bar = wfull0 + ring.slot * 8;
-            mbar_arrive_expect_tx(bar, 4096);
-            bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes,
+                      w + static_cast<int64_t>(kb) * kTileWBytes, bytes, bar);
           }
           __syncwarp();
         }
-      }
-    }
-    if (!ok || *abort_flag)   // copies issued but not waited for still land in this CTA
-      for (int i = max(0, it - S); i < it; ++i)
-        tile_wait_final(smem_u32(&sh.wfull[i % S]), (i / S) & 1);
-  } else if (warp == 2) {
-    // ---- tokens: likewise ----------------------------------------------------
-    pdl_wait();
-    Feed feed{sh};
-    const Seg* sg;
-    const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
-    const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
-    Ring ring;
-    int it = 0;
-    bool ok = true;
-    while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
-      const int kb1 = uniform(sg->kb1);
-      const int row0 = uniform(sg->row0) + rank * (((uniform(sg->rows) + 15) & ~15) / CG);
-      for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
-        ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
-                            p.err);
         if (!ok) break;
-        if (elect_one()) {
-          const uint32_t st = ring0 + ring.slot * stage_bytes;
-          if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * KD * tok_bytes);
-          if constexpr (PAIR)
-            tma_load_3d_pair(st, &map_x, tfull_lead + ring.slot * 8, 0, row0, kb);
-          else
-            tma_load_3d(st, &map_x, tfull0 + ring.slot * 8, 0, row0, kb);
+        const int na = kBatch ? uniform(sg->na) : 0;
+        if (na > 0) pdl_wait();
+        const int32_t* list = p.lists + static_cast<int64_t>(sg->tile) * p.list_stride + 1;
+        for (int i = 0; i < na && ok; ++i) {
+          const int64_t at = static_cast<int64_t>(uniform(list[i])) * p.NB + nb;
+          const uint8_t* lb = p.lora_b + at * p.rank16 * 4096;
+          for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+            ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                                p.err);
+            if (!ok) break;
+            if (elect_one()) {
+              const uint32_t bar = wfull0 + ring.slot * 8;
+              mbar_arrive_expect_tx(bar, 4096);
+              bulk_load(ring0 + ring.slot * stage_bytes + KD * tok_bytes, lb + c * 4096, 4096, bar);
+            }
+            __syncwarp();
+          }
         }
-        __syncwarp();
       }
-      if (!ok) break;
-      // adapters: the tile's h, blocks of 16 ranks in place of k-blocks
-      const int na = kBatch ? uniform(sg->na) : 0, tile = uniform(sg->tile);
-      const int32_t* list = p.lists + static_cast<int64_t>(tile) * p.list_stride + 1;
-      const int h0 = row0 - uniform(sg->row0);
-      for (int i = 0; i < na && ok; ++i) {
-        const int at = (tile + uniform(list[i])) * p.rank16;
-        for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+      if (!ok || *abort_flag)   // copies issued but not waited for still land in this CTA
+        for (int i = max(0, it - S); i < it; ++i)
+          tile_wait_final(smem_u32(&sh.wfull[i % S]), (i / S) & 1);
+    } else if (warp == 2) {
+      // ---- tokens: likewise ----------------------------------------------------
+      pdl_wait();
+      Feed feed{sh};
+      const Seg* sg;
+      const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
+      const uint32_t tfull_lead = PAIR ? map_to_cta(tfull0, 0) : tfull0;
+      Ring ring;
+      int it = 0;
+      bool ok = true;
+      while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+        const int kb1 = uniform(sg->kb1);
+        const int row0 = uniform(sg->row0) + rank * (((uniform(sg->rows) + 15) & ~15) / CG);
+        for (int kb = uniform(sg->kb0); kb < kb1; kb += KD, ++it, ring.advance(S)) {
           ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
                               p.err);
           if (!ok) break;
           if (elect_one()) {
             const uint32_t st = ring0 + ring.slot * stage_bytes;
-            if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * tok_bytes);
+            if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * KD * tok_bytes);
             if constexpr (PAIR)
-              tma_load_3d_pair(st, &map_h, tfull_lead + ring.slot * 8, 0, h0, at + c);
+              tma_load_3d_pair(st, &map_x, tfull_lead + ring.slot * 8, 0, row0, kb);
             else
-              tma_load_3d(st, &map_h, tfull0 + ring.slot * 8, 0, h0, at + c);
+              tma_load_3d(st, &map_x, tfull0 + ring.slot * 8, 0, row0, kb);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        // adapters: the tile's h, blocks of 16 ranks in place of k-blocks
+        const int na = kBatch ? uniform(sg->na) : 0, tile = uniform(sg->tile);
+        const int32_t* list = p.lists + static_cast<int64_t>(tile) * p.list_stride + 1;
+        const int h0 = row0 - uniform(sg->row0);
+        for (int i = 0; i < na && ok; ++i) {
+          const int at = (tile + uniform(list[i])) * p.rank16;
+          for (int c = 0; c < p.rank16; ++c, ++it, ring.advance(S)) {
+            ok = tile_wait_warp(empty0 + ring.slot * 8, ring.phase ^ 1, abort_flag, kErrTileRing,
+                                p.err);
+            if (!ok) break;
+            if (elect_one()) {
+              const uint32_t st = ring0 + ring.slot * stage_bytes;
+              if (leader) mbar_arrive_expect_tx(tfull0 + ring.slot * 8, CG * tok_bytes);
+              if constexpr (PAIR)
+                tma_load_3d_pair(st, &map_h, tfull_lead + ring.slot * 8, 0, h0, at + c);
+              else
+                tma_load_3d(st, &map_h, tfull0 + ring.slot * 8, 0, h0, at + c);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if ((!ok || *abort_flag) && leader)
+        for (int i = max(0, it - S); i < it; ++i)
+          tile_wait_final(smem_u32(&sh.tfull[i % S]), (i / S) & 1);
+    } else if (warp == 1) {
+      // ---- MMAs: one elected lane of a warp that runs in step ------------------
+      if (leader) {
+        pdl_wait();
+        Feed feed{sh};
+        const Seg* sg;
+        const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
+        const uint32_t ready0 = smem_u32(&sh.ready[0]);
+        const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
+        const uint32_t d0 = uniform(tmem), a0 = d0 + F::kAcc * acc_cols;
+        const uint64_t desc0 = sw128_kmajor_desc(0);
+        Ring ring, ac;   // stages, accumulators
+        int it = 0;
+        bool ok = true;
+        const int chunk = uniform(chunk_stages_of<KD, kFloat>(p));
+        while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
+          const uint32_t n16 = uniform((sg->rows + 15) & ~15);
+          const uint32_t idesc = idesc_f16(128 * CG, n16);
+          int kb = uniform(sg->kb0);
+          const int kb1 = uniform(sg->kb1);
+          const int stages = (kb1 - kb + KD - 1) / KD;
+          for (int c0 = 0; c0 < stages && ok; c0 += chunk, ac.advance(F::kAcc)) {
+            const uint32_t buf = ac.slot;
+            ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = d0 + buf * acc_cols;
+            const int c1 = min(stages, c0 + chunk);
+            for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
+              const uint32_t as = it & (NA - 1);
+              const uint32_t tfull = tfull0 + ring.slot * 8, ready = ready0 + as * 8;
+              const uint32_t rphase = (it >> NAb) & 1;
+              const bool here = mbar_try_wait(tfull, ring.phase), done = mbar_try_wait(ready, rphase);
+              if (!__all_sync(0xffffffffu, here && done)) {
+                ok = tile_wait_warp(tfull, ring.phase, abort_flag, kErrTileRing, p.err) &&
+                     tile_wait_warp(ready, rphase, abort_flag, kErrTileOperand, p.err);
+                if (!ok) break;
+              }
+              tc_fence_after();
+              const uint32_t st = ring0 + ring.slot * stage_bytes;
+              const bool two = KD == 2 && kb + 1 < kb1;
+              if (elect_one()) {
+                const uint64_t b = desc0 + (st >> 4);
+                const uint32_t a = a0 + as * KD * 32;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  umma_f16_ta<CG>(d, a + j * 8, b + j * 2, idesc, s > c0 || j > 0);
+                if (two) {
+                  const uint64_t b1 = b + (tok_bytes >> 4);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    umma_f16_ta<CG>(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
+                }
+                umma_commit_all<CG>(empty0 + ring.slot * 8);
+                if (s + 1 == c1) umma_commit_all<CG>(accf0 + buf * 8);
+              }
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          const int na = kBatch ? uniform(sg->na) : 0;
+          if (na > 0) {
+            const uint32_t buf = ac.slot;
+            ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = d0 + buf * acc_cols;
+            const uint32_t id32 = idesc_tf32(128 * CG, n16);
+            const int total = na * p.rank16;
+            for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
+              const uint32_t as = it & (NA - 1);
+              ok = tile_wait_warp(tfull0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing,
+                                  p.err) &&
+                   tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
+                                  p.err);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t b = desc0 + ((ring0 + ring.slot * stage_bytes) >> 4);
+                const uint32_t a = a0 + as * KD * 32;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)   // h's leading terms, then its trailing ones
+                  umma_tf32_ta<CG>(d, a + (j & 1) * 8, b + j * 2, id32, i > 0 || j > 0);
+                umma_commit_all<CG>(empty0 + ring.slot * 8);
+                if (i + 1 == total) umma_commit_all<CG>(accf0 + buf * 8);
+              }
+              __syncwarp();
+            }
+            ac.advance(F::kAcc);
+          }
+        }
+        if (!ok || *abort_flag) {
+          if (elect_one()) {
+            umma_commit_own<CG>(smem_u32(&sh.drain));
+            tile_wait_final(smem_u32(&sh.drain), 0);
           }
           __syncwarp();
         }
       }
-    }
-    if ((!ok || *abort_flag) && leader)
-      for (int i = max(0, it - S); i < it; ++i)
-        tile_wait_final(smem_u32(&sh.tfull[i % S]), (i / S) & 1);
-  } else if (warp == 1) {
-    // ---- MMAs: one elected lane of a warp that runs in step ------------------
-    if (leader) {
-      pdl_wait();
-      Feed feed{sh};
-      const Seg* sg;
-      const uint32_t tfull0 = smem_u32(&sh.tfull[0]), empty0 = smem_u32(&sh.empty[0]);
-      const uint32_t ready0 = smem_u32(&sh.ready[0]);
-      const uint32_t accf0 = smem_u32(&sh.acc_full[0]), acce0 = smem_u32(&sh.acc_empty[0]);
-      const uint32_t d0 = uniform(tmem), a0 = d0 + F::kAcc * acc_cols;
-      const uint64_t desc0 = sw128_kmajor_desc(0);
-      Ring ring, ac;   // stages, accumulators
-      int it = 0;
-      bool ok = true;
-      const int chunk = uniform(chunk_stages_of<KD, kFloat>(p));
-      while (ok && (sg = feed.next(abort_flag, p.err)) != nullptr) {
-        const uint32_t n16 = uniform((sg->rows + 15) & ~15);
-        const uint32_t idesc = idesc_f16(128 * CG, n16);
-        int kb = uniform(sg->kb0);
-        const int kb1 = uniform(sg->kb1);
-        const int stages = (kb1 - kb + KD - 1) / KD;
-        for (int c0 = 0; c0 < stages && ok; c0 += chunk, ac.advance(F::kAcc)) {
-          const uint32_t buf = ac.slot;
-          ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = d0 + buf * acc_cols;
-          const int c1 = min(stages, c0 + chunk);
-          for (int s = c0; s < c1; ++s, ++it, ring.advance(S), kb += KD) {
-            const uint32_t as = it & (NA - 1);
-            const uint32_t tfull = tfull0 + ring.slot * 8, ready = ready0 + as * 8;
-            const uint32_t rphase = (it >> NAb) & 1;
-            const bool here = mbar_try_wait(tfull, ring.phase), done = mbar_try_wait(ready, rphase);
-            if (!__all_sync(0xffffffffu, here && done)) {
-              ok = tile_wait_warp(tfull, ring.phase, abort_flag, kErrTileRing, p.err) &&
-                   tile_wait_warp(ready, rphase, abort_flag, kErrTileOperand, p.err);
-              if (!ok) break;
-            }
-            tc_fence_after();
-            const uint32_t st = ring0 + ring.slot * stage_bytes;
-            const bool two = KD == 2 && kb + 1 < kb1;
-            if (elect_one()) {
-              const uint64_t b = desc0 + (st >> 4);
-              const uint32_t a = a0 + as * KD * 32;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                umma_f16_ta<CG>(d, a + j * 8, b + j * 2, idesc, s > c0 || j > 0);
-              if (two) {
-                const uint64_t b1 = b + (tok_bytes >> 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  umma_f16_ta<CG>(d, a + 32 + j * 8, b1 + j * 2, idesc, 1);
-              }
-              umma_commit_all<CG>(empty0 + ring.slot * 8);
-              if (s + 1 == c1) umma_commit_all<CG>(accf0 + buf * 8);
-            }
-            __syncwarp();
-          }
-        }
-        if (!ok) break;
-        const int na = kBatch ? uniform(sg->na) : 0;
-        if (na > 0) {
-          const uint32_t buf = ac.slot;
-          ok = tile_wait_warp(acce0 + buf * 8, ac.phase ^ 1, abort_flag, kErrTileAcc, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = d0 + buf * acc_cols;
-          const uint32_t id32 = idesc_tf32(128 * CG, n16);
-          const int total = na * p.rank16;
-          for (int i = 0; i < total; ++i, ++it, ring.advance(S)) {
-            const uint32_t as = it & (NA - 1);
-            ok = tile_wait_warp(tfull0 + ring.slot * 8, ring.phase, abort_flag, kErrTileRing,
-                                p.err) &&
-                 tile_wait_warp(ready0 + as * 8, (it >> NAb) & 1, abort_flag, kErrTileOperand,
-                                p.err);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t b = desc0 + ((ring0 + ring.slot * stage_bytes) >> 4);
-              const uint32_t a = a0 + as * KD * 32;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)   // h's leading terms, then its trailing ones
-                umma_tf32_ta<CG>(d, a + (j & 1) * 8, b + j * 2, id32, i > 0 || j > 0);
-              umma_commit_all<CG>(empty0 + ring.slot * 8);
-              if (i + 1 == total) umma_commit_all<CG>(accf0 + buf * 8);
-            }
-            __syncwarp();
-          }
-          ac.advance(F::kAcc);
-        }
-      }
-      if (!ok || *abort_flag) {
-        if (elect_one()) {
-          umma_commit_own<CG>(smem_u32(&sh.drain));
-          tile_wait_final(smem_u32(&sh.drain), 0);
+    } else {
+      // ---- schedule: the parts of this CTA's units, described for the others ---
+      if (kBatch && p.L > 0 && !p.by_row) pdl_wait();   // the tiles' adapters
+      Walk<CG> walk(p, prefix, tiles, !kBatch);
+      Ring ring;
+      bool more = true;
+      while (more) {
+        Seg sg = {};
+        more = walk.next(sg);
+        if (kBatch && more) sg.na = adapters_of(p, sg);
+        if (!tile_wait_warp(smem_u32(&sh.seg_empty[ring.slot]), ring.phase ^ 1, abort_flag,
+                            kErrTileRing, p.err))
+          break;
+        if (lane == 0) {
+          sh.seg[ring.slot] = sg;
+          mbar_arrive(smem_u32(&sh.seg_full[ring.slot]));
         }
         __syncwarp();
+        ring.advance(kSegs);
       }
     }
-  } else if (warp == 3) {
-    // ---- schedule: the parts of this CTA's units, described for the others ---
-    if (kBatch && p.L > 0 && !p.by_row) pdl_wait();   // the tiles' adapters
-    Walk<CG> walk(p, prefix, tiles, !kBatch);
-    Ring ring;
-    bool more = true;
-    while (more) {
-      Seg sg = {};
-      more = walk.next(sg);
-      if (kBatch && more) sg.na = adapters_of(p, sg);
-      if (!tile_wait_warp(smem_u32(&sh.seg_empty[ring.slot]), ring.phase ^ 1, abort_flag,
-                          kErrTileRing, p.err))
-        break;
-      if (lane == 0) {
-        sh.seg[ring.slot] = sg;
-        mbar_arrive(smem_u32(&sh.seg_full[ring.slot]));
-      }
-      __syncwarp();
-      ring.advance(kSegs);
-    }
-  } else if (warp >= kFirstConv && warp < F::kFirstEpi) {
+  } else if (warp < F::kFirstEpi) {
+    split_registers<F::kConvRegs>();
     // ---- A operand: shared memory -> f16 -> TMEM ---------------------------
     const int group = (warp - kFirstConv) >> 2;       // groups take stages in turn
     const int row = (warp & 3) * 32 + lane;           // a warp reaches the lanes of its quarter
@@ -964,7 +982,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) break;
     }
-  } else if (warp >= F::kFirstEpi) {
+  } else {
+    split_registers<F::kEpiRegs>();
     // ---- epilogue ------------------------------------------------------------
     Feed feed{sh};
     const Seg* sg;
@@ -1355,8 +1374,11 @@ cudaError_t launch_one(const CUtensorMap& map, const CUtensorMap& map_h, const T
   if (e != cudaSuccess) return e;
   int pairs = 0;
   e = once.run([&] {
-    const cudaError_t set =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    cudaFuncAttributes attributes;
+    cudaError_t set = cudaFuncGetAttributes(&attributes, kernel);
+    if (set != cudaSuccess) return set;
+    if (attributes.numRegs < Form<PAIR>::kRegs) return cudaErrorInvalidConfiguration;
+    set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
     if (!PAIR || set != cudaSuccess) return set;
     // pairs that fit the GPU at once (both CTAs of one share a GPC)
     cudaLaunchConfig_t cfg = {};
