@@ -455,13 +455,54 @@ __device__ __forceinline__ typename OutType<OUT>::type finish(float v, const Til
   }
 }
 
-// The epilogue of rows with a scale for each token: a warp's 32 channels and
-// `mine` columns from col0 on of one unit, whose sums acc holds.  my_dh: the gated
-// gradient's 16 channels of each column, in shared memory.
+// What the epilogue of rows with a scale for each token wants beside the sums,
+// asked for while the MMAs run: a warp's 32 channels and `mine` columns from
+// col0 on of one unit (lane l: channel l, columns l and l + 32).
+template <TileForm FORM>
+struct TokenScales {
+  static constexpr bool kPairs = FORM != kFormToken;
+  float s0, s1, ws, bias;   // the rows', the channel's
+  float r0, r1;             // the gated gradient: its rows' powers of two
+  __device__ __forceinline__ void load(const TileParams& p, const Seg& sg, int nb, int quarter,
+                                       int col0, int mine) {
+    const int lane = threadIdx.x & 31;
+    const int row = nb * 128 + quarter * 32 + lane;   // of the packed weight
+    const int n = kPairs ? (row >> 5) * 16 + (lane & 15) : row;
+    const int64_t en = (kPairs && (lane & 16) ? static_cast<int64_t>(p.N) : 0) + n;
+    ws = bias = s0 = s1 = r0 = r1 = 0.0f;
+    if (n < p.N) {
+      ws = __ldg(p.ws + en);
+      if (p.bias != nullptr) bias = __ldg(p.bias + en);
+    }
+    // (the kernel before this one may have written the rows': ordinary loads)
+    const int at = sg.row0 + col0;
+    const bool in0 = lane < mine, in1 = lane + 32 < mine;
+    if (in0) s0 = p.row_scale[at + lane];
+    if (in1) s1 = p.row_scale[at + lane + 32];
+    if constexpr (FORM == kFormGatedGrad) {
+      const float4 tops = *reinterpret_cast<const float4*>(p.tops);
+      const bool once = nb == 0 && quarter == 0;   // a row's sums' power of two
+      if (in0) {
+        const RowPower power = gated_row_power(p.most_dh[at + lane], s0, p.K, tops);
+        r0 = power.rescale;
+        if (once) p.unscale[at + lane] = power.unscale;
+      }
+      if (in1) {
+        const RowPower power = gated_row_power(p.most_dh[at + lane + 32], s1, p.K, tops);
+        r1 = power.rescale;
+        if (once) p.unscale[at + lane + 32] = power.unscale;
+      }
+    }
+  }
+};
+
+// That epilogue.  my_dh: the gated gradient's 16 channels of each column, in
+// shared memory.
 template <int OUT, int COLS, TileForm FORM>
 __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& sg,
-                                               int32_t (&acc)[COLS], int nb, int quarter, int col0,
-                                               int mine, const uint16_t* my_dh) {
+                                               int32_t (&acc)[COLS], const TokenScales<FORM>& sc,
+                                               int nb, int quarter, int col0, int mine,
+                                               const uint16_t* my_dh) {
   using T = typename OutType<OUT>::type;
   constexpr bool kPairs = FORM != kFormToken;
   const int lane = threadIdx.x & 31;
@@ -470,16 +511,10 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
   const int n = kPairs ? (row >> 5) * 16 + (lane & 15) : row;
   const bool in = n < p.N;
   const int at = sg.row0 + col0;
-  // (the kernel before this one may have written the scales: ordinary loads)
-  const float s0 = p.row_scale[at + min(lane, mine - 1)];
-  const float s1 = COLS > 32 ? p.row_scale[at + min(lane + 32, mine - 1)] : 0.0f;
-  const int64_t en = (up ? static_cast<int64_t>(p.N) : 0) + n;
-  const float ws = in ? __ldg(p.ws + en) : 0.0f;
-  const float bias = in && p.bias != nullptr ? __ldg(p.bias + en) : 0.0f;
 #pragma unroll
   for (int j = 0; j < COLS; ++j) {
-    const float s = __shfl_sync(0xffffffffu, j < 32 ? s0 : s1, j & 31);
-    acc[j] = __float_as_int(token_value(acc[j], s, ws, bias));
+    const float s = __shfl_sync(0xffffffffu, j < 32 ? sc.s0 : sc.s1, j & 31);
+    acc[j] = __float_as_int(token_value(acc[j], s, sc.ws, sc.bias));
   }
   // one address for the tile and 32-bit distances from it (a tile's rows span
   // less than 4 GB: N <= 2^24)
@@ -513,17 +548,8 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
       }
     } else {
       // the gradients times their channels' scales and their rows' powers of two
-      const float4 tops = *reinterpret_cast<const float4*>(p.tops);
-      const RowPower p0 = gated_row_power(p.most_dh[at + min(lane, mine - 1)], s0, p.K, tops);
-      const RowPower p1 =
-          COLS > 32 ? gated_row_power(p.most_dh[at + min(lane + 32, mine - 1)], s1, p.K, tops) : p0;
-      const float r0 = p0.rescale, r1 = p1.rescale;
-      if (nb == 0 && quarter == 0) {   // once a row
-        if (lane < mine) p.unscale[at + lane] = p0.unscale;
-        if (lane + 32 < mine) p.unscale[at + lane + 32] = p1.unscale;
-      }
-      const float ws_other = __shfl_xor_sync(0xffffffffu, ws, 16);
-      const float wg = up ? ws_other : ws, wu = up ? ws : ws_other;
+      const float ws_other = __shfl_xor_sync(0xffffffffu, sc.ws, 16);
+      const float wg = up ? ws_other : sc.ws, wu = up ? sc.ws : ws_other;
       const uint16_t* dh = my_dh + mine_j * 16 + (lane & 15);
       // K-blocked, in the order of the packed rows: 64 a block
       uint16_t* to = p.operand_out +
@@ -536,7 +562,7 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
         float g, u, slope;
         pair(j, g, u);
         const float a = activate<true>(g, p.act, slope);
-        const float r = __shfl_sync(0xffffffffu, j < 32 ? r0 : r1, (j & 31) + mine_j);
+        const float r = __shfl_sync(0xffffffffu, j < 32 ? sc.r0 : sc.r1, (j & 31) + mine_j);
         const float v = half_bits_to_float<OUT>(dh[j * 16]) * r;
         // channels past the last hold zeros, whatever the rows' scales are
         const uint32_t both = in ? grad_bits_x2(v * u * slope * wg, v * a * wu) : 0;
@@ -1043,6 +1069,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           fetch_adapters(sg, mine, nb);
         pdl_wait();
       }
+      constexpr bool kScaled =
+          FORM == kFormToken || FORM == kFormGated || FORM == kFormGatedGrad;
+      TokenScales<FORM> scales;
+      if constexpr (kScaled) scales.load(p, *sg, nb, quarter, col0, mine);
       if constexpr (FORM == kFormGatedGrad) {
         // This part's dh on its way to shared memory while the MMAs run: loads
         // from the epilogue wait behind their tokens and weights (1024 rows x
@@ -1225,13 +1255,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if constexpr (FORM == kFormToken || FORM == kFormGated || FORM == kFormGatedGrad) {
+      if constexpr (kScaled) {
         if constexpr (FORM == kFormGatedGrad) {
           cp_async_wait<0>();
           __syncwarp();
         }
         if (last && mine > 0)
-          token_epilogue<OUT, kCols, FORM>(p, *sg, acc, nb, quarter, col0, mine, my_dh);
+          token_epilogue<OUT, kCols, FORM>(p, *sg, acc, scales, nb, quarter, col0, mine, my_dh);
         first_seg = false;
         continue;
       }
