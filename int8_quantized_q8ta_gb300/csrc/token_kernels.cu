@@ -457,17 +457,30 @@ __global__ void __launch_bounds__(256) pack_gated_kernel(const int8_t* __restric
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t t = i >> 9, kb = t % KB;
     const int64_t row = t / KB * 128 + (i & 127), in0 = kb * 64 + ((i >> 7) & 3) * 16;
-    uint32_t v[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+    uint32_t v[4] = {0, 0, 0, 0};
+    if constexpr (T) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int64_t pair = T ? in0 + j : row;          // the interleaved index
-      const int64_t n = (pair >> 5) * 16 + (pair & 15), k = T ? row : in0 + j;
-      if (n < N && k < K) {
-        const uint32_t b = static_cast<uint8_t>(((pair & 16) ? up : gate)[n * K + k]);
-        v[j / 4] ^= b << (8 * (j % 4));   // (over the zero's byte)
+      for (int j = 0; j < 16; ++j) {
+        const int64_t pair = in0 + j;   // the interleaved index
+        const int64_t n = (pair >> 5) * 16 + (pair & 15);
+        if (n < N && row < K)
+          v[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(((pair & 16) ? up : gate)[n * K + row]))
+                      << (8 * (j % 4));
+      }
+    } else {
+      const int64_t n = (row >> 5) * 16 + (row & 15);
+      const int8_t* w = (row & 16) ? up : gate;
+      if (n < N) {
+        const uint2 a = load_int8x8<false>(w, n * K, in0, K, w + N * K);
+        const uint2 b = load_int8x8<false>(w, n * K, in0 + 8, K, w + N * K);
+        v[0] = a.x;
+        v[1] = a.y;
+        v[2] = b.x;
+        v[3] = b.y;
       }
     }
-    dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    dst[i] = make_uint4(v[0] ^ 0x80808080u, v[1] ^ 0x80808080u, v[2] ^ 0x80808080u,
+                        v[3] ^ 0x80808080u);
   }
 }
 __global__ void larger_bound_kernel(int32_t* word) {

@@ -8,16 +8,18 @@
 // Up to 8 rows a weight's 1 byte costs more than its 2 to 16 operations, so
 // bytes in flight count.  A CTA of 16 warps takes units of 16 packed rows (16
 // channels, or 8 of both halves of a gated pair); the warps share a unit's
-// inputs, eight 16-byte loads ahead each (64 KB a CTA, two CTAs an SM; 44 bytes
+// inputs, four 16-byte loads ahead each (32 KB a CTA, two CTAs an SM; 44 bytes
 // a nanosecond and SM at the copy rate with 800 ns of latency want 35).  They run
 // on across units, and the first ones are asked for before the kernel before
 // this one is done (a packed weight is written at load time).  1 row x 11008 x
-// 4096 10.2 us (floor 6.8), the gated pair 4096 x 11008 18.2 us (13.6), in a run
-// of calls.
+// 4096 10.7 us (floor 6.8), the gated pair 4096 x 11008 17.7 us (13.6), in a run
+// of calls; 1 x 1024 x 1024, which is all latency, 2.8 us.  Code that runs once
+// costs more to fetch than to execute: with eight loads ahead those were 10.5,
+// 17.9 and 3.1, with a row's first 4 items held instead of 2 11.0, 18.4 and 3.1.
 //   One or two rows: four products a dp4a, straight from the registers that the
 // loads fill; the rows' int8 come from shared memory, 16 bytes that half a warp
-// shares.  That is one load from there for each of memory, an SM can do two, so
-// three to eight rows go through m16n8k16 MMAs, f16 in and f32 out: the packed
+// shares.  That is one load from there for each of memory and row, and an
+// SM can do two, so three to eight rows go through m16n8k16 MMAs, f16 in and f32 out: the packed
 // 16-byte chunks are a thread's fragments as they lie (the order of a sum's terms
 // is free, so thread t of four takes inputs 16 t to 16 t + 15 of a k-block),
 // turned into f16 by a byte permute and half a subtraction a value, and rows are
@@ -41,7 +43,7 @@ namespace q8 {
 namespace {
 
 constexpr int kRowWarps = 16, kRowThreads = kRowWarps * 32;
-constexpr int kAhead = 8;         // 16-byte loads in flight a thread
+constexpr int kAhead = 4;         // 16-byte loads in flight a thread
 constexpr int kExactBlocks = 8;   // k-blocks of one exact f32 chunk
 
 __device__ __forceinline__ uint4 load_weights(const uint4* p) {
