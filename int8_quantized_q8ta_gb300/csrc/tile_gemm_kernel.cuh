@@ -227,17 +227,15 @@ struct Walk {
     share = rest > 0 && few && q < p.KB
                 ? max(1, min(ctas / rest, p.KB / max(1, p.min_run)))
                 : 0;
+    unit = -1;             // the run is not begun
     if (share > 0) {
-      unit = base + me / share;
       const int part = me % share;
       kb = part_start(part, p.KB, share);
       left = me / share < rest ? part_start(part + 1, p.KB, share) - kb : 0;
-      if (left > 0) locate(unit);
       return;
     }
     kb = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(q) * me));
     left = min(total - kb, q);
-    unit = -1;             // the run is not begun
   }
   __device__ __forceinline__ void cut() {
     tiles = (count + p.TN - 1) / p.TN;
@@ -283,10 +281,10 @@ struct Walk {
       return true;
     }
     if (left <= 0) return false;
-    if (unit < 0) {
-      const int skip = kb / p.KB;
+    if (unit < 0) {   // (the whole waves left other units' places behind)
+      const int skip = share > 0 ? me / share : kb / p.KB;
       unit = base + skip;
-      kb -= skip * p.KB;
+      if (share == 0) kb -= skip * p.KB;
       locate(unit);
     }
     fill(s);

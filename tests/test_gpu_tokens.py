@@ -147,6 +147,44 @@ def test_quantize_unaligned_and_given_outputs():
         assert back[0] == 7 and back[-1] == 7
 
 
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("M,K", [(700, 1003), (400, 4097), (305, 33), (2000, 9), (1500, 2), (320, 40000), (3, 40001),
+                                 (400, 16385), (777, 1234)])
+def test_rows_of_any_length(dtype, M, K):
+    x = rows(M + K, M, K, dtype)
+    want_q, want_s = ref.quantize(x)
+    q, s = q8.quantize_per_token(x.to(DEV))
+    same(q, want_q)
+    same(s, want_s)
+    for out in FLOATS:
+        same(q8.dequantize_per_token(q, s, out_dtype=out), (want_q.float() * want_s[:, None]).to(out))
+    # and as the product's operand
+    w, ws, _ = weights(K, 40, K)
+    same(q8.linear_per_token(x.to(DEV), None, q8.pack_tile_weight(w.to(DEV)), ws.to(DEV), None, out_dtype=torch.float32),
+         gpu_product(want_q, want_s, w, ws, None))
+
+
+@pytest.mark.parametrize("M,K", [(20, 97), (400, 131), (320, 264)])
+def test_rows_anywhere(M, K):
+    # rows that begin on any element, int8 ones on any byte; the words around stay
+    for dtype in FLOATS:
+        x = rows(K, M, K, dtype)
+        want_q, want_s = ref.quantize(x)
+        for off in range(9):
+            flat = torch.full((M * K + 20,), float("nan"), dtype=dtype, device=DEV)
+            flat[off:off + M * K] = x.reshape(-1).to(DEV)
+            out = torch.full((M * K + 20,), 55, dtype=torch.int8, device=DEV)
+            at = (off * 5) % 16
+            q, s = q8.quantize_per_token(flat[off:off + M * K].view(M, K), out=out[at:at + M * K].view(M, K))
+            same(q, want_q)
+            same(s, want_s)
+            assert bool((out[:at] == 55).all()) and bool((out[at + M * K:] == 55).all())
+            back = torch.full((M * K + 20,), 7.0, dtype=dtype, device=DEV)
+            q8.dequantize_per_token(q, s, out_dtype=dtype, out=back[off:off + M * K].view(M, K))
+            same(back[off:off + M * K].view(M, K), (want_q.float() * want_s[:, None]).to(dtype))
+            assert bool((back[:off] == 7).all()) and bool((back[off + M * K:] == 7).all())
+
+
 # ---- the product ------------------------------------------------------------
 
 SIZES = [(1, 4, 1), (1, 128, 64), (1, 1000, 1234), (2, 260, 4096), (3, 37, 65), (8, 1003, 512), (16, 4100, 320),
@@ -248,6 +286,60 @@ def test_dirty_workspaces():
                 assert torch.equal(call(space), want)
 
 
+def gpu_product(q, xs, w, ws, b):
+    """ref.product of sizes that the CPU would take long for (the sums are exact
+    wherever they are computed)."""
+    return ref.product(*(None if t is None else t.to(DEV) for t in (q, xs, w, ws, b))).cpu()
+
+
+# Tiles of one group that fill the GPU once or more, with what is left from a few
+# units to nearly a wave: whole units, units cut across runs, units shared.
+@pytest.mark.parametrize("M,N,K", [(640, 1280, 4096), (900, 1280, 4096), (1300, 1280, 4096), (2000, 1280, 4096),
+                                   (2048, 4096, 2816), (3000, 1280, 4096), (3700, 1280, 4096), (4096, 1280, 4096),
+                                   (640, 2560, 3500), (600, 6000, 2500), (900, 4096, 4096), (100, 20000, 1000)])
+def test_every_way_to_split_units(M, N, K):
+    g = torch.Generator().manual_seed(M + N + K)
+    q = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int8)
+    xs = torch.rand(M, generator=g) * 0.05
+    w, ws, b = weights(M + N, N, K, lo=-128)
+    y = q8.linear_per_token(q.to(DEV), xs.to(DEV), q8.pack_tile_weight(w.to(DEV)), ws.to(DEV), b.to(DEV),
+                            out_dtype=torch.float32)
+    same(y, gpu_product(q, xs, w, ws, b))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 6007, 700), (2, 9001, 333), (5, 9001, 640), (7, 4113, 4096), (1, 40, 100000),
+                                   (2, 130, 70001), (8, 70, 4097), (6, 333, 5000), (9, 200, 4096)])
+def test_few_rows_of_many_channels_or_inputs(M, N, K):
+    dtype = FLOATS[(M + N + K) % 3]
+    x = rows(M + K, M, K, dtype)
+    w, ws, b = weights(M + N, N, K)
+    qs = ref.quantize(x)
+    want = gpu_product(*qs, w, ws, b)
+    packed = q8.pack_tile_weight(w.to(DEV))
+    same(q8.linear_per_token(x.to(DEV), None, packed, ws.to(DEV), b.to(DEV)), want.to(dtype))
+    same(q8.linear_per_token(qs[0].to(DEV), qs[1].to(DEV), packed, ws.to(DEV), b.to(DEV), out_dtype=dtype),
+         want.to(dtype))
+
+
+@pytest.mark.parametrize("M,K", [(1, 31), (3, 1003), (8, 517)])
+def test_few_rows_anywhere(M, K):
+    # rows that begin on any element, int8 ones on any byte; the words around stay
+    w, ws, b = weights(M, 90, K)
+    packed = q8.pack_tile_weight(w.to(DEV))
+    for dtype in FLOATS:
+        x = rows(K, M, K, dtype)
+        qs = ref.quantize(x)
+        want = ref.product(*qs, w, ws, b).to(dtype)
+        for off in range(8):
+            flat = torch.full((M * K + 16,), float("nan"), dtype=dtype, device=DEV)
+            flat[off:off + M * K] = x.reshape(-1).to(DEV)
+            same(q8.linear_per_token(flat[off:off + M * K].view(M, K), None, packed, ws.to(DEV), b.to(DEV)), want)
+            ints = torch.full((M * K + 16,), 99, dtype=torch.int8, device=DEV)
+            ints[off:off + M * K] = qs[0].reshape(-1).to(DEV)
+            same(q8.linear_per_token(ints[off:off + M * K].view(M, K), qs[1].to(DEV), packed, ws.to(DEV), b.to(DEV),
+                                     out_dtype=dtype), want)
+
+
 # ---- the gated pair ---------------------------------------------------------
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
@@ -328,6 +420,33 @@ def test_gated_gradient(dtype, act, M, N, K):
     assert dx.dtype == dtype
     within(dx, want, bound)
     assert torch.equal(dx, q8.linear_gated_backward(*args, activation=act))
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 131, 77), (1900, 6000, 2500), (1024, 8200, 1030), (400, 1003, 72)])
+def test_gradients_of_many_rows(M, N, K):
+    # bounds from 64-bit products on the GPU; rows that begin on any element
+    dtype = HALVES[M % 2]
+    dy, y = rows(M + N, M, N, dtype), rows(M + K, M, N, dtype)
+    w, ws, b = weights(N, 2, N, K, lo=-128)
+    q, xs = ref.quantize(rows(M, M, K))
+    def far(t):
+        flat = torch.full((t.numel() + 3,), float("nan"), dtype=t.dtype, device=DEV)
+        flat[3:] = t.reshape(-1).to(DEV)
+        return flat[3:].view(t.shape)
+    dyd, yd, wd, wsd, bd, qd, xsd = (t.to(DEV) for t in (dy, y, w, ws, b, q, xs))
+    masked = torch.where(yd > 0, dyd, torch.zeros((), dtype=dtype, device=DEV))
+    packed_t = q8.pack_tile_weight(wd[0].t().contiguous())
+    for relu in (False, True):
+        want, bound = ref.linear_grad(masked if relu else dyd, wd[0], wsd[0])
+        dx = q8.linear_per_token_backward(far(dy), packed_t, wsd[0].contiguous(), y=far(y) if relu else None)
+        within(dx, want.cpu(), bound.cpu())
+    g, u = (ref.product(qd, xsd, wd[i], wsd[i], bd[i]) for i in (0, 1))
+    want, bound = ref.gated_grad(dyd, g, u, wd, wsd, "silu", xsd, bd)
+    ints = torch.full((M * K + 5,), 99, dtype=torch.int8, device=DEV)
+    ints[5:] = qd.reshape(-1)
+    dx = q8.linear_gated_backward(far(dy), ints[5:].view(M, K), xsd, q8.pack_gated_weight(wd[0], wd[1]),
+                                  q8.pack_gated_weight_t(wd[0], wd[1]), wsd, bd)
+    within(dx, want.cpu(), bound.cpu())
 
 
 @pytest.mark.parametrize("M", [5, 90])
@@ -452,6 +571,21 @@ def test_a_block_and_its_gradient(dtype, M):
     within(h, *ref.gated(g, u, "silu", dtype))
     within(dh, *ref.linear_grad(dy.cpu(), block.w2, block.ws2))
     within(dx, *ref.gated_grad(dh.cpu(), g, u, block.w1, block.ws1, "silu", xc, block.b1))
+
+
+@pytest.mark.parametrize("M,K", [(1, 77), (2, 1003), (7, 130), (30, 333)])
+def test_recorded_rows_of_any_length(M, K):
+    # the int8 rows and scales that the recorded call keeps are the quantizer's
+    N = 60
+    x = rows(M, M, K, torch.bfloat16)
+    w, ws, b = weights(M, 2, N, K)
+    gate, gt = (f(w[0].to(DEV), w[1].to(DEV)) for f in (q8.pack_gated_weight, q8.pack_gated_weight_t))
+    leaf = x.to(DEV).requires_grad_()
+    h = q8.linear_gated(leaf, None, gate, ws.to(DEV), b.to(DEV), packed_t=gt)
+    dh = rows(K, M, N, torch.bfloat16).to(DEV)
+    h.backward(dh)
+    q, s = q8.quantize_per_token(x.to(DEV))
+    assert torch.equal(leaf.grad, q8.linear_gated_backward(dh, q, s, gate, gt, ws.to(DEV), b.to(DEV)))
 
 
 def test_relu_product_is_recorded():
