@@ -1,4 +1,6 @@
-"""Build libq8ta.so (the C-ABI library of include/q8ta.h) in-tree with nvcc.
+"""Build libq8ta.so (the C-ABI library of include/q8ta.h) in-tree with nvcc, and
+_torch_calls.so (csrc/torch_calls.cpp, a Python module that calls it with torch's
+tensors) beside it with g++.
 
 Each CUDA source is compiled for sm_103a only (explicit
 ``-gencode arch=compute_103a,code=sm_103a``; tcgen05 needs the ``a`` target),
@@ -13,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_objs")
 LIB = os.path.join(PKG, "libq8ta.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -38,16 +43,47 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + \
         [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _compile_calls() -> str:
+    """The object of the Python module (the headers are torch's own, those of the
+    torch that will import it)."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(OBJ_DIR, "torch_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", CALLS_SRC, "-o", obj,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for path in (os.path.join(root, "include"),
+                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", path]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libq8ta.so", "-Wl,-rpath,$ORIGIN", "-L",
+           libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ link failed:\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -69,7 +105,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_compile_calls)
         results = list(ex.map(compile_one, _sources()))
+        calls_obj = calls.result()
     if verbose:
         for _, err in results:
             if err.strip():
@@ -80,6 +118,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_calls(calls_obj)
     return LIB
 
 

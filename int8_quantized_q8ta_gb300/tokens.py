@@ -2,12 +2,12 @@
 activations quantized as they come, the int8 products and the gated pair of
 projections on them, and the gradients through int8 weights.
 
-Argument marshalling only, like the rest of the package; imported by it.  The
-products take float rows, which they quantize, or int8 rows with their scales.
-Float rows that require a gradient get it where the transposed weight is given:
-the call is then recorded for autograd, and keeps the int8 rows and their
-scales (linear_gated) or its output under relu (linear_per_token), never the
-float rows.
+Argument marshalling only, like the rest of the package (the common case of it in
+csrc/torch_calls.cpp); imported by it.  The products take float rows, which they
+quantize, or int8 rows with their scales.  Float rows that require a gradient
+get it where the transposed weight is given: the call is then recorded for
+autograd, and keeps the int8 rows and their scales (linear_gated) or its output
+under relu (linear_per_token), never the float rows.
 """
 from __future__ import annotations
 
@@ -23,9 +23,26 @@ from .rows import _DTYPE, PackedTileWeight, _dtype_code, _shape, _space
 _HALVES = (torch.float16, torch.bfloat16)
 
 
-# A call for one token takes some 10 us on the GPU, so the host's part counts.
-# Each tensor gets one combined check; the slow one, which names what is wrong,
-# runs only where it fails.
+# A call for few tokens takes some 3 to 15 us on the GPU, so the host's part
+# counts.  Calls as most are made (results and workspace from torch's allocator,
+# nothing recorded) go through _torch_calls, which answers None where a tensor is
+# not as it should be, and the status where the library refuses; then, and for
+# all other calls, each argument is checked here by name.
+
+class _Calls:
+    def __getattr__(self, name):
+        from . import _torch_calls   # built beside the library; there is no other way on a GPU
+        f = getattr(_torch_calls, name)
+        setattr(self, name, f)       # found here from the next call on
+        return f
+
+
+_calls = _Calls()
+
+
+def _done(result) -> bool:
+    return result is not None and result.__class__ is not int
+
 
 def _float_code(dtype, name: str) -> int:
     code = _DTYPE.get(dtype)
@@ -98,6 +115,10 @@ def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
                        scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Float rows [M, K] to int8, each with its own scale (see
     q8_quantize_per_token): returns (q int8 [M, K], scales float32 [M])."""
+    if out is None and scales is None:
+        r = _calls.quantize_per_token(x)
+        if _done(r):
+            return r
     code, at, M, K, device = _matrix(x, (0, 1, 2), "x")
     q = _result(out, (M, K), torch.int8, x, device)
     scales = _result(scales, (M,), torch.float32, x, device, "scales")
@@ -110,6 +131,10 @@ def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
 def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32,
                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """int8 rows [M, K] times their scales, in a float type."""
+    if out is None:
+        r = _calls.dequantize_per_token(q, scales, out_dtype)
+        if _done(r):
+            return r
     _, at, M, K, device = _matrix(q, (3,), "q")
     s = _at(scales, torch.float32, (M,), device, "scales")
     code = _float_code(out_dtype, "out_dtype")
@@ -206,14 +231,19 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     N, K = packed.N, packed.K
     if packed.E != 1:
         raise ValueError(f"the packed weight has {packed.E} groups, this product takes one")
+    if packed_t is not None and (packed_t.E, packed_t.N, packed_t.K) != (1, K, N):
+        raise ValueError(f"packed_t must be of a {K}x{N} weight")
+    if out is None and workspace is None:
+        r = _calls.linear_per_token(x, x_scales, packed.data, N, K, weight_scales, bias, activation,
+                                    out_dtype)
+        if _done(r):
+            return r
     code, at, M, s, device = _rows(x, x_scales, K)
     w = _packed_at(packed, device, "packed")
     scales = _at(weight_scales, torch.float32, (N,), device, "weight_scales")
     b = 0 if bias is None else _at(bias, torch.float32, (N,), device, "bias")
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
-    if packed_t is not None and (packed_t.E, packed_t.N, packed_t.K) != (1, K, N):
-        raise ValueError(f"packed_t must be of a {K}x{N} weight")
     out = _result(out, (M, N), out_dtype, x, device)
     nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
@@ -231,10 +261,14 @@ def linear_per_token_backward(dy, packed_t: PackedTileWeight, weight_scales, y=N
     """The gradient of linear_per_token's rows (see
     q8_linear_per_token_backward): dy [M, N] float16 or bfloat16, y the forward
     output under relu; out [M, K] of dy's type."""
-    code, at, M, n, device = _matrix(dy, (1, 2), "dy")
     K, N = packed_t.N, packed_t.K
     if packed_t.E != 1:
         raise ValueError(f"the packed weight has {packed_t.E} groups, this product takes one")
+    if out is None and workspace is None:
+        r = _calls.linear_per_token_backward(dy, packed_t.data, N, K, weight_scales, y)
+        if _done(r):
+            return r
+    code, at, M, n, device = _matrix(dy, (1, 2), "dy")
     if n != N:
         raise ValueError(f"dy must be [M, {N}], got {tuple(dy.shape)}")
     y_at = 0 if y is None else _at(y, dy.dtype, (M, N), device, "y")
@@ -290,13 +324,19 @@ def pack_gated_weight_t(gate: torch.Tensor, up: torch.Tensor) -> PackedGatedWeig
     return _pack_gated(gate, up, True)
 
 
-def _gated_args(packed, packed_t, weight_scales, bias, device: int) -> Tuple[int, int, int]:
-    """The addresses of the pair's weights, scales and biases."""
+def _gated_pair(packed, packed_t) -> Tuple[int, int]:
+    """(N, K) of a pair's weights, which packed_t, where given, has too."""
     if packed.transposed:
         raise ValueError("packed is a transposed weight (pack_gated_weight_t)")
     N, K = packed.N, packed.K
     if packed_t is not None and (not packed_t.transposed or (packed_t.N, packed_t.K) != (N, K)):
         raise ValueError(f"packed_t must come from pack_gated_weight_t of {N}x{K} weights")
+    return N, K
+
+
+def _gated_args(packed, weight_scales, bias, device: int) -> Tuple[int, int, int]:
+    """The addresses of the pair's weights, scales and biases."""
+    N = packed.N
     return (_packed_at(packed, device, "packed"),
             _at(weight_scales, torch.float32, (2, N), device, "weight_scales"),
             0 if bias is None else _at(bias, torch.float32, (2, N), device, "bias"))
@@ -312,9 +352,14 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
     out_dtype (by default x's own, bfloat16 for int8 x).  packed_t
     (pack_gated_weight_t) records the call for autograd where x requires a
     gradient; it then keeps the int8 rows and their scales."""
-    N, K = packed.N, packed.K
+    N, K = _gated_pair(packed, packed_t)
+    if out is None and workspace is None:
+        r = _calls.linear_gated(x, x_scales, packed.data, N, K, weight_scales, bias, activation,
+                                out_dtype)
+        if _done(r):
+            return r
     code, at, M, s, device = _rows(x, x_scales, K)
-    w, scales, b = _gated_args(packed, packed_t, weight_scales, bias, device)
+    w, scales, b = _gated_args(packed, weight_scales, bias, device)
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
     out = _result(out, (M, N), out_dtype, x, device)
@@ -339,11 +384,16 @@ def linear_gated_backward(dh, x, x_scales, packed: PackedGatedWeight, packed_t: 
     """The gradient of linear_gated's rows from the int8 rows x [M, K] and their
     scales (see q8_linear_gated_backward): dh [M, N] float16 or bfloat16; out
     [M, K] of dh's type."""
-    code, at, M, n, device = _matrix(dh, (1, 2), "dh")
     if packed_t is None:
         raise ValueError("the gradient needs packed_t (pack_gated_weight_t)")
-    N, K = packed.N, packed.K
-    w, scales, b = _gated_args(packed, packed_t, weight_scales, bias, device)
+    N, K = _gated_pair(packed, packed_t)
+    if out is None and workspace is None:
+        r = _calls.linear_gated_backward(dh, x, x_scales, packed.data, packed_t.data, N, K,
+                                         weight_scales, bias, activation)
+        if _done(r):
+            return r
+    code, at, M, n, device = _matrix(dh, (1, 2), "dh")
+    w, scales, b = _gated_args(packed, weight_scales, bias, device)
     if n != N:
         raise ValueError(f"dh must be [M, {N}], got {tuple(dh.shape)}")
     w_t = _packed_at(packed_t, device, "packed_t")
