@@ -458,8 +458,8 @@ __device__ __forceinline__ typename OutType<OUT>::type finish(float v, const Til
 // col0 on of one unit (lane l: channel l, columns l and l + 32).
 template <TileForm FORM>
 struct TokenScales {
-  static constexpr bool kPairs = FORM != kFormToken;
-  float s0, s1, ws, bias;   // the rows', the channel's
+  static constexpr bool kPairs = FORM == kFormGated || FORM == kFormGatedGrad;
+  float s0, s1, ws, bias;   // the rows' (of a gradient what undoes their power), the channel's
   float r0, r1;             // the gated gradient: its rows' powers of two
   __device__ __forceinline__ void load(const TileParams& p, const Seg& sg, int nb, int quarter,
                                        int col0, int mine) {
@@ -468,15 +468,16 @@ struct TokenScales {
     const int n = kPairs ? (row >> 5) * 16 + (lane & 15) : row;
     const int64_t en = (kPairs && (lane & 16) ? static_cast<int64_t>(p.N) : 0) + n;
     ws = bias = s0 = s1 = r0 = r1 = 0.0f;
-    if (n < p.N) {
+    if (FORM != kFormGrad && n < p.N) {
       ws = __ldg(p.ws + en);
       if (p.bias != nullptr) bias = __ldg(p.bias + en);
     }
     // (the kernel before this one may have written the rows': ordinary loads)
     const int at = sg.row0 + col0;
     const bool in0 = lane < mine, in1 = lane + 32 < mine;
-    if (in0) s0 = p.row_scale[at + lane];
-    if (in1) s1 = p.row_scale[at + lane + 32];
+    const float* rows = FORM == kFormGrad ? p.unscale : p.row_scale;
+    if (in0) s0 = rows[at + lane];
+    if (in1) s1 = rows[at + lane + 32];
     if constexpr (FORM == kFormGatedGrad) {
       const float4 tops = *reinterpret_cast<const float4*>(p.tops);
       const bool once = nb == 0 && quarter == 0;   // a row's sums' power of two
@@ -494,82 +495,75 @@ struct TokenScales {
   }
 };
 
-// That epilogue.  my_dh: the gated gradient's 16 channels of each column, in
-// shared memory.
+// That epilogue, B columns a round.  Rounds stay rolled and the registers move up
+// instead: a CTA runs them once to a few times, so their code costs more to fetch
+// than to execute, and columns without rows are left out.  my_dh: the gated
+// gradient's 16 channels of each column, in shared memory.
 template <int OUT, int COLS, TileForm FORM>
 __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& sg,
                                                int32_t (&acc)[COLS], const TokenScales<FORM>& sc,
                                                int nb, int quarter, int col0, int mine,
                                                const uint16_t* my_dh) {
   using T = typename OutType<OUT>::type;
-  constexpr bool kPairs = FORM != kFormToken;
+  constexpr bool kPairs = TokenScales<FORM>::kPairs;
+  constexpr int B = 16;
   const int lane = threadIdx.x & 31;
   const int row = nb * 128 + quarter * 32 + lane;   // of the packed weight
   const bool up = kPairs && (lane & 16);
+  const int mine_j = up ? 1 : 0;   // gate lanes take tokens j, up lanes j + 1
   const int n = kPairs ? (row >> 5) * 16 + (lane & 15) : row;
   const bool in = n < p.N;
   const int at = sg.row0 + col0;
+  // the gated gradient: its operand K-blocked, in the order of the packed rows, 64
+  // a block (the block that an odd count repeats for a pair has no place there)
+  const float ws_other = kPairs ? __shfl_xor_sync(0xffffffffu, sc.ws, 16) : 0.0f;
+  const float wg = up ? ws_other : sc.ws, wu = up ? sc.ws : ws_other;
+  const int rows = (FORM == kFormGatedGrad ? nb < p.NB : in) ? mine - mine_j : 0;
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(at + mine_j) * p.N + n;
+  uint16_t* to = p.operand_out +
+                 ((static_cast<int64_t>(nb) * 2 + (quarter >> 1)) * p.R + at + mine_j) * 64 +
+                 (quarter & 1) * 32 + (lane & 15);
+  const uint16_t* dh = my_dh + mine_j * 16 + (lane & 15);
+#pragma unroll 1
+  for (int j0 = 0; j0 < mine; j0 += B) {
+    const float s_of = j0 < 32 ? sc.s0 : sc.s1, r_of = j0 < 32 ? sc.r0 : sc.r1;
 #pragma unroll
-  for (int j = 0; j < COLS; ++j) {
-    const float s = __shfl_sync(0xffffffffu, j < 32 ? sc.s0 : sc.s1, j & 31);
-    acc[j] = __float_as_int(token_value(acc[j], s, sc.ws, sc.bias));
-  }
-  // one address for the tile and 32-bit distances from it (a tile's rows span
-  // less than 4 GB: N <= 2^24)
-  const uint32_t step = static_cast<uint32_t>(p.N) * sizeof(T);
-  if constexpr (FORM == kFormToken) {
-    char* base = static_cast<char*>(p.out) + static_cast<int64_t>(at) * p.N * sizeof(T);
-    uint32_t off = static_cast<uint32_t>(n) * sizeof(T);
-    const int rows = in ? mine : 0;
+    for (int j = 0; j < B; ++j) {
+      const float s = __shfl_sync(0xffffffffu, s_of, (j0 + j) & 31);
+      acc[j] = __float_as_int(FORM == kFormGrad ? __fmul_rn(__int_as_float(acc[j]), s)
+                                                : token_value(acc[j], s, sc.ws, sc.bias));
+    }
+    if constexpr (!kPairs) {
 #pragma unroll
-    for (int j = 0; j < COLS; ++j, off += step)
-      if (j < rows) *reinterpret_cast<T*>(base + off) = finish<OUT>(__int_as_float(acc[j]), p);
-  } else {
-    // gate lanes keep token j and send their token j + 1; up lanes the reverse
-    const auto pair = [&](int j, float& g, float& u) {
-      const float a = __int_as_float(acc[j]), b = __int_as_float(acc[j + 1]);
-      const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
-      g = up ? other : a;
-      u = up ? b : other;
-    };
-    const int mine_j = up ? 1 : 0;
-    if constexpr (FORM == kFormGated) {
-      char* base = static_cast<char*>(p.out) + static_cast<int64_t>(at) * p.N * sizeof(T);
-      uint32_t off = static_cast<uint32_t>(n) * sizeof(T) + (up ? step : 0);
-      const int rows = in ? mine - mine_j : 0;
-#pragma unroll
-      for (int j = 0; j < COLS; j += 2, off += 2 * step) {
-        float g, u, slope;
-        pair(j, g, u);
-        const float h = activate<false>(g, p.act, slope) * u;
-        if (j < rows) *reinterpret_cast<T*>(base + off) = finish<OUT>(h, p);
-      }
+      for (int j = 0; j < B; ++j, out += p.N)
+        if (j0 + j < rows) *out = finish<OUT>(__int_as_float(acc[j]), p);
     } else {
-      // the gradients times their channels' scales and their rows' powers of two
-      const float ws_other = __shfl_xor_sync(0xffffffffu, sc.ws, 16);
-      const float wg = up ? ws_other : sc.ws, wu = up ? sc.ws : ws_other;
-      const uint16_t* dh = my_dh + mine_j * 16 + (lane & 15);
-      // K-blocked, in the order of the packed rows: 64 a block
-      uint16_t* to = p.operand_out +
-                     ((static_cast<int64_t>(nb) * 2 + (quarter >> 1)) * p.R + at + mine_j) * 64 +
-                     (quarter & 1) * 32 + (lane & 15);
-      // (the block that an odd count repeats for a pair has no place there)
-      const int rows = nb < p.NB ? mine - mine_j : 0;
 #pragma unroll
-      for (int j = 0; j < COLS; j += 2) {
-        float g, u, slope;
-        pair(j, g, u);
-        const float a = activate<true>(g, p.act, slope);
-        const float r = __shfl_sync(0xffffffffu, j < 32 ? sc.r0 : sc.r1, (j & 31) + mine_j);
-        const float v = half_bits_to_float<OUT>(dh[j * 16]) * r;
-        // channels past the last hold zeros, whatever the rows' scales are
-        const uint32_t both = in ? grad_bits_x2(v * u * slope * wg, v * a * wu) : 0;
-        if (j < rows) {
-          to[j * 64] = static_cast<uint16_t>(both);
-          to[j * 64 + 16] = static_cast<uint16_t>(both >> 16);
+      for (int j = 0; j < B; j += 2) {
+        // gate lanes keep token j and send their token j + 1; up lanes the reverse
+        const float a = __int_as_float(acc[j]), b = __int_as_float(acc[j + 1]);
+        const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+        const float g = up ? other : a, u = up ? b : other;
+        float slope;
+        if constexpr (FORM == kFormGated) {
+          const float h = activate<false>(g, p.act, slope) * u;
+          if (j0 + j < rows) *out = finish<OUT>(h, p);
+          out += 2 * static_cast<int64_t>(p.N);
+        } else {
+          const float t = activate<true>(g, p.act, slope);
+          const float r = __shfl_sync(0xffffffffu, r_of, ((j0 + j) & 31) + mine_j);
+          const float v = half_bits_to_float<OUT>(dh[(j0 + j) * 16]) * r;
+          // channels past the last hold zeros, whatever the rows' scales are
+          const uint32_t both = in ? grad_bits_x2(v * u * slope * wg, v * t * wu) : 0;
+          if (j0 + j < rows) {
+            to[(j0 + j) * 64] = static_cast<uint16_t>(both);
+            to[(j0 + j) * 64 + 16] = static_cast<uint16_t>(both >> 16);
+          }
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < COLS - B; ++j) acc[j] = acc[j + B];
   }
 }
 
@@ -1067,10 +1061,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           fetch_adapters(sg, mine, nb);
         pdl_wait();
       }
-      constexpr bool kScaled =
-          FORM == kFormToken || FORM == kFormGated || FORM == kFormGatedGrad;
       TokenScales<FORM> scales;
-      if constexpr (kScaled) scales.load(p, *sg, nb, quarter, col0, mine);
+      if constexpr (!kBatch) scales.load(p, *sg, nb, quarter, col0, mine);
       if constexpr (FORM == kFormGatedGrad) {
         // This part's dh on its way to shared memory while the MMAs run: loads
         // from the epilogue wait behind their tokens and weights (1024 rows x
@@ -1253,7 +1245,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if constexpr (kScaled) {
+      if constexpr (!kBatch) {
         if constexpr (FORM == kFormGatedGrad) {
           cp_async_wait<0>();
           __syncwarp();
@@ -1265,16 +1257,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const int n = nb * 128 + quarter * 32 + lane;
       const bool in = n < p.N;
-      if (kFloat && last && mine > 0) {
-        const int at = sg->row0 + col0;
-        const float s0 = p.unscale[at + min(lane, mine - 1)];
-        const float s1 = kCols > 32 ? p.unscale[at + min(lane + 32, mine - 1)] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          acc[j] = __float_as_int(__fmul_rn(
-              __int_as_float(acc[j]), __shfl_sync(0xffffffffu, j < 32 ? s0 : s1, j & 31)));
-      }
-      if (kBatch && last) {
+      if (last) {
         // In place from here on: registers beyond the sums are few, and what
         // spills finds no L1 beside this much shared memory.
         const int64_t en = static_cast<int64_t>(sg->e) * p.N + n;
@@ -1326,7 +1309,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (by_mma) release(dbuf);   // before the stores, which take longest
       if (last && mine > 0) {
         using T = typename OutType<OUT>::type;
-        if (!kBatch || p.out_rows == nullptr) {
+        if (p.out_rows == nullptr) {
           // one address for the tile and 32-bit distances from it (a tile's
           // rows span less than 4 GB: N <= 2^24)
           char* base = static_cast<char*>(p.out) +
