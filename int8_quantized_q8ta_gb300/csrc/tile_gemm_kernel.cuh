@@ -64,8 +64,6 @@ constexpr int kTileWBytes = 128 * 64;   // int8 weights of one tile and k-block
 constexpr int kFirstConv = 4;           // warps 0 to 3: weights, MMAs, tokens, schedule
 constexpr int kTileThreads = 640;
 constexpr int kTmemCols = 512;
-// Stages of A operands in tensor memory, behind the accumulators.
-constexpr int NAb = 2, NA = 1 << NAb;
 
 // What one kernel computes of its sums.
 //   kFormBatch      one activation scale for the batch, groups, adapters
@@ -105,7 +103,9 @@ enum TileForm { kFormBatch, kFormToken, kFormGated, kFormGatedGrad, kFormGrad };
 template <bool PAIR>
 struct Form {
   static constexpr int CG = PAIR ? 2 : 1;
-  static constexpr int KD = PAIR ? 1 : 2;          // k-blocks a stage
+  static constexpr int KD = 2;                     // k-blocks a stage
+  // stages of A operands in tensor memory, behind the accumulators
+  static constexpr int NAb = PAIR ? 1 : 2, NA = 1 << NAb;
   static constexpr int kConv = PAIR ? 4 : 8;       // converting warps
   static constexpr int kGroups = kConv / 4;        // groups of four take turns
   static constexpr int kEpi = PAIR ? 12 : 8;       // epilogue warps
@@ -147,7 +147,7 @@ struct TileShared {
   uint64_t wfull[kMaxRing];   // weights of a stage have landed
   uint64_t tfull[kMaxRing];   // tokens of a stage have landed (a pair's halves: at the leader)
   uint64_t empty[kMaxRing];   // a stage's MMAs are done
-  uint64_t ready[NA];         // A operand in TMEM
+  uint64_t ready[4];          // A operand in TMEM
   uint64_t acc_full[3];
   uint64_t acc_empty[3];
   uint64_t drain;
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_h, const TileParams p) {
   using F = Form<PAIR>;
-  constexpr int CG = F::CG, KD = F::KD, kCols = F::kCols;
+  constexpr int CG = F::CG, KD = F::KD, NAb = F::NAb, NA = F::NA, kCols = F::kCols;
   constexpr bool kBatch = FORM == kFormBatch, kFloat = FORM == kFormGrad;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TileShared sh;
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               }
               tc_fence_after();
               const uint32_t st = ring0 + ring.slot * stage_bytes;
-              const bool two = KD == 2 && kb + 1 < kb1;
+              const bool two = kb + 1 < kb1;
               if (elect_one()) {
                 const uint64_t b = desc0 + (st >> 4);
                 const uint32_t a = a0 + as * KD * 32;
@@ -939,16 +939,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int kb = sg->kb0; kb < sg->kb1; kb += KD, advance()) {
         if (F::kGroups == 2 && (it & 1) != group) continue;
         const int as = it & (NA - 1);
-        // The place first: it is free once the MMAs of the stage NA back are
-        // done, so the slot's last weights, S >= NA stages back, have landed,
-        // and the parity below cannot be that of the round before them (which a
-        // group that leaves every other stage to its partner has not seen).
-        ok = place_free() && tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag,
-                                       kErrTileRing, p.err);
+        const auto landed = [&]() {
+          return tile_wait(smem_u32(&sh.wfull[ring.slot]), ring.phase, abort_flag, kErrTileRing,
+                           p.err);
+        };
+        // Two groups: the place first.  It is free once the MMAs of the stage NA
+        // back are done, so the slot's last weights, S >= NA stages back, have
+        // landed, and the parity below cannot be that of the round before them
+        // (which a group that leaves every other stage to its partner has not
+        // seen).  One group has seen all weights land, and waits for the place
+        // once it has the first ones converted.
+        ok = (F::kGroups == 1 || place_free()) && landed();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t w = ring0 + ring.slot * stage_bytes + KD * tok_bytes + row * 16;
-        const bool two = KD == 2 && kb + 1 < sg->kb1;
+        const bool two = kb + 1 < sg->kb1;
         uint4 v[4], v1[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] = lds128(w + c * 2048);
@@ -958,6 +963,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         uint32_t r[32];
         convert(v, r);
+        if constexpr (F::kGroups == 1) {
+          ok = __all_sync(0xffffffffu, place_free());
+          if (!ok) break;
+        }
         tc_fence_after();
         tmem_st_32cols(a_lane + as * KD * 32, r);
         if (two) {
