@@ -44,16 +44,15 @@ inline TilePlan plan_tiles(int64_t R, int64_t K, int64_t E, int64_t max_rows = q
   return t;
 }
 
-// The tile height of one group of R rows, N packed rows and K inputs: of a few
-// heights the one whose slowest CTA (or pair) is done first, by the split that
-// the kernel's Walk makes of it.  Low tiles make more units, which a few rows
-// need to fill the GPU without cutting units (a join costs 4 us and more); high
-// ones read the weights less often, and stay where a lower one gains less than 4%.
-// The constants (ns: the launches, a k-block, a unit's epilogue, a join and its
-// parts) were fitted to 144 problems of 70 to 2000 rows and each form, to 5%; the
-// choice is then within 1% of the best of twelve heights (12% at worst), where
-// full tiles take 18% longer (2.4 times at worst: 70 rows, 5000 inputs, 512
-// outputs 22.7 us against 12.0).
+// The tile height of one group of R rows, N packed rows and K inputs: the one
+// whose slowest CTA (or pair) is done first, by the split that the kernel's Walk
+// makes of it.  Low tiles make more units, which a few rows need to fill the GPU
+// without cutting units (a join costs 3 us and more); high ones read the weights
+// less often, and stay where a lower one gains less than 3%.  The constants (ns:
+// the launches, a k-block, a unit's epilogue, a join and its parts) were fitted to
+// 195 problems of 20 to 2000 rows, all forms, to 7%; the choice is then within
+// 1.7% of the best height (16% at worst), where full tiles take 18% longer (2.4
+// times at worst: 70 rows, 5000 inputs, 512 outputs 22.7 us against 12.0).
 inline int64_t tile_time(int64_t R, int64_t N, int64_t K, int TN, int grid, int min_run) {
   const bool wide = TN > q8::kMaxNarrowRows;
   const int64_t ctas = std::max(1, wide ? grid / 2 : grid), KB = (K + 63) / 64;
@@ -81,12 +80,12 @@ inline int64_t tile_time(int64_t R, int64_t N, int64_t K, int TN, int grid, int 
       if (q % KB != 0 && q < total) parts = (KB + q - 1) / q + 1;
     }
   }
-  const int64_t join = parts * rows * 9;
+  const int64_t kbs = waves * KB + line, epilogues = waves + ends;
   if (wide)
-    return 6400 + (waves * KB + line) * (190 + rows * 3 / 10) + (waves + ends) * (2300 + 11 * rows) +
-           (parts > 0 ? 4300 + join : 0);
-  return 5600 + (waves * KB + line) * (108 + rows * 4 / 10) + (waves + ends) * (1300 + 5 * rows) +
-         (parts > 0 ? 3900 + join : 0);
+    return 5900 + kbs * (1380 + 3 * rows) / 10 + epilogues * std::max<int64_t>(0, 21 * rows - 500) +
+           (parts > 0 ? 4900 + parts * rows * 7 : 0);
+  return 4900 + kbs * (1190 + 4 * rows) / 10 + epilogues * (270 + 16 * rows) +
+         (parts > 0 ? 3200 + parts * rows * 6 : 0);
 }
 
 // Row tiles that R rows in E groups need at most.
@@ -104,12 +103,11 @@ inline TilePlan plan_group(int64_t R, int64_t N, int64_t K, int min_run) {
   const int full = t.TN;   // as high as there are rows for
   int64_t best = INT64_MAX;
   TilePlan c = t;
-  for (const int height : {full, 192, 160, 64, 48, 32, 16}) {
-    if (height > full) continue;
+  for (int height = full; height > 0; height -= 16) {
     c.TN = height;
     if (!units_ok(R, 1, N, K, c)) continue;
     const int64_t time = tile_time(R, N, K, height, t.grid, min_run);
-    if (best == INT64_MAX || time < best / 100 * 96) {
+    if (best == INT64_MAX || time < best / 100 * 97) {
       best = time;
       t.TN = height;
     }
