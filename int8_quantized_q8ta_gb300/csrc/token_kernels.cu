@@ -284,9 +284,18 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
   using Item = RowItem<4, VEC>;
   constexpr int V = MASK ? 2 : 1;   // dy, y
   const int64_t bytes = job.N * 2;
+  const bool ws16 = reinterpret_cast<uintptr_t>(job.ws) % 16 == 0;
   const auto load_ws = [&](int64_t c, float (&ws)[8]) {
+    if (ws16 && c * 8 + 8 <= job.N) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(job.ws + c * 8));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(job.ws + c * 8) + 1);
+      const float all[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) : 0.0f;
+      for (int j = 0; j < 8; ++j) ws[j] = all[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ws[j] = c * 8 + j < job.N ? __ldg(job.ws + c * 8 + j) : 0.0f;
+    }
   };
   const auto load = [&](Item (&it)[V], int64_t m, int64_t c) {
     const int64_t n = m < job.M ? bytes : 0;
@@ -382,32 +391,29 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
 }
 
 // What the gated gradient's kernel reads beside the weights: the int8 rows as its
-// operand, each row's largest |dh|, and from the first CTA the largest scales and
-// biases.  A row's loads are all in flight before any is used.
+// operand, each row's largest |dh|, and from the first four CTAs the largest
+// scales and biases, one each.  A row's loads are all in flight before any is used.
 template <int DT, bool VEC_Q, bool VEC_DH>
 __global__ void __launch_bounds__(512, 3) gated_grad_front_kernel(const GatedGradFrontJob job) {
   constexpr int UD = 4, UQ = 2;
-  __shared__ uint32_t slots[4][32];
+  __shared__ uint32_t slots[2][32];
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
        i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
     job.counts[i] = 0;
-  if (blockIdx.x == 0) {
-    uint32_t top[4];   // of the gate's and the up projection's scales, and of their biases
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* v = i < 2 ? job.ws : job.bias;
-      top[i] = v == nullptr ? 0u : block_max(top_of(v + (i & 1) * job.N, job.N), slots[i]);
-    }
-    if (threadIdx.x == 0)
-      *reinterpret_cast<uint4*>(job.tops) = make_uint4(top[0], top[1], top[2], top[3]);
+  if (blockIdx.x < 4) {   // of the gate's and the up projection's scales, and of their biases
+    const int i = blockIdx.x;
+    const float* v = i < 2 ? job.ws : job.bias;
+    const uint32_t top =
+        v == nullptr ? 0u : block_max(top_of(v + (i & 1) * job.N, job.N), slots[0]);
+    if (threadIdx.x == 0) job.tops[i] = __uint_as_float(top);
     return;
   }
   const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8, bytes = job.N * 2;
   const int8_t* q_end = job.q + job.M * job.K;
   int turn = 0;
-  for (int64_t m = blockIdx.x - 1; m < job.M; m += gridDim.x - 1, turn ^= 1) {
+  for (int64_t m = blockIdx.x - 4; m < job.M; m += gridDim.x - 4, turn ^= 1) {
     uint32_t t = 0;
     const RowBytes row = row_bytes<uint16_t>(job.dh, job.M, job.N, m);
 #pragma unroll 1
@@ -570,7 +576,7 @@ cudaError_t launch_gated_grad_front(const GatedGradFrontJob& job, q8_dtype dtype
   // 4 items of dh a thread, and as many CTAs as the SMs take at once
   const int threads = static_cast<int>(
       std::min<int64_t>(512, std::max<int64_t>(256, round_up((job.N + 31) / 32, 32))));
-  const int grid = 1 + static_cast<int>(std::min<int64_t>(
+  const int grid = 4 + static_cast<int>(std::min<int64_t>(
                            job.M, static_cast<int64_t>(device_sm_count()) * (1536 / threads)));
   return by_half(dtype, vec_dh, [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
