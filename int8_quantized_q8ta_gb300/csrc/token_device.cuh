@@ -72,12 +72,15 @@ __device__ __forceinline__ RowBytes row_bytes(const void* x, int64_t M, int64_t 
   return {lo, lo + M * K * static_cast<int64_t>(sizeof(T)), lo + m * K * static_cast<int64_t>(sizeof(T))};
 }
 
-// The 16 bytes at a 16-byte boundary, zeros outside [lo, hi).
+// The 16 bytes at a 16-byte boundary, zeros outside [lo, hi).  All loads are in
+// flight together: a matrix's last item comes here, and the kernel waits for it.
 __device__ __forceinline__ uint4 load_within(const uint8_t* p, const uint8_t* lo, const uint8_t* hi) {
   uint32_t v[4] = {0, 0, 0, 0};
-#pragma unroll 1
-  for (int j = 0; j < 16; ++j)
-    if (p + j >= lo && p + j < hi) v[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+  const auto* p2 = reinterpret_cast<const uint16_t*>(p);   // (elements are two bytes or four)
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (p + 2 * j >= lo && p + 2 * j < hi)
+      v[j >> 1] |= static_cast<uint32_t>(p2[j]) << (16 * (j & 1));
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
@@ -164,7 +167,7 @@ __device__ __forceinline__ uint2 load_int8x8(const int8_t* q, int64_t row, int64
   const auto part = [&](const int8_t* a) {
     if (a >= q && a + 8 <= end) return *reinterpret_cast<const uint64_t*>(a);
     uint64_t v = 0;
-#pragma unroll 1
+#pragma unroll
     for (int j = 0; j < 8; ++j)
       if (a + j >= q && a + j < end) v |= static_cast<uint64_t>(static_cast<uint8_t>(a[j])) << (8 * j);
     return v;
