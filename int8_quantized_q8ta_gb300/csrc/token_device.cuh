@@ -357,4 +357,48 @@ struct TokenItem : RowItem<DT == Q8_F32 ? 8 : 4, VEC> {
   }
 };
 
+// Rows as items of 8 values on boundaries of 8.  VEC: rows are whole items.  Else
+// row m begins t = ahead(m) values into its first item, and what belongs to its
+// neighbours counts as zeros.
+template <int DT, bool VEC>
+struct FlatRows {
+  using T = FloatOf<DT>;
+  using Item = TokenItem<DT, true>;
+  const T *x, *end;
+  int64_t K;
+  int off;   // values that x lies behind a boundary of 8
+  __device__ __forceinline__ FlatRows(const void* x_, int64_t M, int64_t K_)
+      : x(static_cast<const T*>(x_)), end(x + M * K_), K(K_),
+        off(VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(x_) / sizeof(T) & 7)) {}
+  __device__ __forceinline__ int ahead(int64_t m) const {
+    return VEC ? 0 : static_cast<int>((off + m * K) & 7);
+  }
+  // Item c of row m: asked for; zeros past the row.
+  __device__ __forceinline__ void load(Item& it, int64_t m, int t, int64_t c) const {
+    const int64_t e = c * 8 - t;   // the row's values from e on
+    const T* p = x + m * K + e;
+    it.zero();
+    if constexpr (VEC) {
+      if (e < K) it.load_whole(p);
+    } else if (e < K) {
+      if (p >= x && p + 8 <= end) {
+        it.load_whole(p);
+      } else {   // the ends of the matrix
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e + j >= 0 && e + j < K) it.set(j, p[j]);
+      }
+    }
+  }
+  // Once it is there: zeros for the neighbours' values.
+  __device__ __forceinline__ void settle(Item& it, int t, int64_t c) const {
+    const int64_t e = c * 8 - t;
+    if (!VEC && (e < 0 || e + 8 > K)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j < 0 || e + j >= K) it.set(j, 0);
+    }
+  }
+};
+
 }  // namespace q8

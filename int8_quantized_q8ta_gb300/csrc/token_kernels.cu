@@ -22,96 +22,83 @@ namespace {
 // largest magnitude and once to round it.  A CTA has one row at a time and keeps
 // it in registers in between, with the next row's loads already on their way; so
 // it comes from memory once, and memory is never idle while a row waits for its
-// scale.  Only rows beyond U items for each of 1,024 threads are read again (from
-// L2).  Bytes bound it: 8192 rows of 11008 bf16 46 us (floor 41), of 8191 XXX.
-//   An item is 8 values on a boundary of 8.  VEC: rows are whole items.  Else a
-// row begins t values into its first item, and what belongs to its neighbours
-// counts as zeros; q, whose rows begin the same way, takes whole items too, but
-// the operand has its own: 8 - t values of an item and t of the next one, which
-// a lane gets from the lane after it (so a warp's last lane only lends).
+// scale.  Only rows beyond U items for each of 704 threads are read again (from
+// L2).  Bytes bound it: 8192 rows of 11008 bf16 46 us (floor 41), of 8191 58 (30).
+//   SHORT: rows of which a warp holds all items go to a warp each, without a
+// barrier (16,000 rows of 200 f16 6.9 us, 13.2 by CTAs; of 201 13.3, 29).
+//   Rows that are no multiple of 8 begin t values into their first item.  q, whose
+// rows begin the same way, takes whole items too, but the operand has its own:
+// 8 - t values of an item and t of the next one, which a lane gets from the lane
+// after it (so a warp's last lane only lends).
 // ---------------------------------------------------------------------------
-template <int DT, bool VEC, bool OP>
-__global__ void __launch_bounds__(1024) quantize_token_kernel(const QuantizeJob job) {
-  using Item = TokenItem<DT, true>;
-  using T = FloatOf<DT>;
-  constexpr int U = DT == Q8_F32 ? 2 : 4;
+constexpr int kQuantizeThreads = 704;   // at most: two rows' items want some 90 registers
+template <int DT>
+constexpr int quantize_items() {        // of a thread, in registers
+  return DT == Q8_F32 ? 2 : 4;
+}
+
+template <int DT, bool VEC, bool OP, bool SHORT>
+__global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token_kernel(const QuantizeJob job) {
+  using Rows = FlatRows<DT, VEC>;
+  using Item = typename Rows::Item;
+  constexpr int U = quantize_items<DT>();
   constexpr int kLanes = !VEC && OP ? 31 : 32;
   __shared__ uint32_t tops[2][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // this row's warps, and which of them this is; rows on their way at once
+  const int warp = SHORT ? 0 : threadIdx.x >> 5, warps = SHORT ? 1 : blockDim.x >> 5;
+  const int64_t m0 = SHORT ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                           : blockIdx.x;
+  const int64_t m_step = SHORT ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
   if constexpr (OP)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
          i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
       job.counts[i] = 0;
-  const auto* x = static_cast<const T*>(job.x);
-  const T* x_end = x + job.M * job.K;
-  // values that x lies behind a boundary of 8
-  const int off = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) & 7);
-  const bool q_whole = (reinterpret_cast<uintptr_t>(job.q) - off) % 8 == 0;
-  const auto ahead = [&](int64_t m) {   // t
-    return VEC ? 0 : static_cast<int>((off + m * job.K) & 7);
-  };
+  const Rows rows(job.x, job.M, job.K);
+  const bool q_whole = (reinterpret_cast<uintptr_t>(job.q) - rows.off) % 8 == 0;
   const int64_t chunks = static_cast<int64_t>(job.KB) * 8;   // of the operand's row
-  const auto load = [&](Item& it, int64_t m, int t, int64_t c) {
-    const int64_t e = c * 8 - t;   // the row's values from e on
-    const T* p = x + m * job.K + e;
-    it.zero();
-    if (e >= job.K) return;
-    if (VEC || (p >= x && p + 8 <= x_end)) {
-      it.load_whole(p);
-    } else {   // the ends of the matrix
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e + j >= 0 && e + j < job.K) it.set(j, p[j]);
-    }
-  };
-  const auto settle = [&](Item& it, int t, int64_t c) {
-    const int64_t e = c * 8 - t;
-    if (!VEC && (e < 0 || e + 8 > job.K)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e + j < 0 || e + j >= job.K) it.set(j, 0);
-    }
-  };
-  // this thread's items: every blockDim.x'th, in the 31-lane form that less its last lanes
+  // this thread's items: every step'th, in the 31-lane form less its last lanes
   const int64_t c0 = warp * kLanes + lane, step = warps * kLanes;
   // (items that a row can reach, for whole warps to go through)
   const int64_t items = OP ? chunks : (job.K + (VEC ? 7 : 14)) / 8;
   Item held[U];
   {
-    const int t = ahead(blockIdx.x);
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(held[u], blockIdx.x, t, c0 + u * step);
-  }
-  int turn = 0;
-  for (int64_t m = blockIdx.x; m < job.M; m += gridDim.x, turn ^= 1) {
-    const int t = ahead(m);
-    Item next[U];
-    const int64_t m_next = m + gridDim.x;
-    const int t_next = ahead(m_next);
+    const int t = rows.ahead(m0);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      load(next[u], m_next, t_next, m_next < job.M ? c0 + u * step : INT64_MAX / 16);
+      rows.load(held[u], m0, t, m0 < job.M ? c0 + u * step : INT64_MAX / 16);
+  }
+  int turn = 0;
+  for (int64_t m = m0; m < job.M; m += m_step, turn ^= 1) {
+    const int t = rows.ahead(m);
+    Item next[U];
+    const int64_t m_next = m + m_step;
+    const int t_next = rows.ahead(m_next);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      rows.load(next[u], m_next, t_next, m_next < job.M ? c0 + u * step : INT64_MAX / 16);
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      settle(held[u], t, c0 + u * step);
+      rows.settle(held[u], t, c0 + u * step);
       top = max(top, held[u].top());
     }
     for (int64_t c = c0 + U * step; c * 8 - t < job.K; c += step) {
       Item it;
-      load(it, m, t, c);
-      settle(it, t, c);
+      rows.load(it, m, t, c);
+      rows.settle(it, t, c);
       top = max(top, it.top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) tops[turn][warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[turn][lane] : 0u);
+    if constexpr (!SHORT) {
+      if (lane == 0) tops[turn][warp] = top;
+      __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[turn][lane] : 0u);
+    }
     const TokenScale sc = token_scale(top);
-    if (threadIdx.x == 0) job.scales[m] = sc.scale;
+    if (warp == 0 && lane == 0) job.scales[m] = sc.scale;
     const auto put = [&](const Item& it, int64_t c) {
       const uint2 q = it.quantize(sc.inv);
       const int64_t e = c * 8 - t;
@@ -146,8 +133,8 @@ __global__ void __launch_bounds__(1024) quantize_token_kernel(const QuantizeJob 
       if (c0 + u * step - lane < items) put(held[u], c0 + u * step);
     for (int64_t c = c0 + U * step; c - lane < items; c += step) {
       Item it;
-      load(it, m, t, c);
-      settle(it, t, c);
+      rows.load(it, m, t, c);
+      rows.settle(it, t, c);
       put(it, c);
     }
 #pragma unroll
@@ -410,20 +397,22 @@ __global__ void __launch_bounds__(512, 3) gated_grad_front_kernel(const GatedGra
     if (threadIdx.x == 0) job.tops[i] = __uint_as_float(top);
     return;
   }
-  const int64_t items = (job.N + 7) / 8, chunks = static_cast<int64_t>(job.KB) * 8, bytes = job.N * 2;
+  const FlatRows<DT, VEC_DH> dh(job.dh, job.M, job.N);
+  const int64_t items = (job.N + 14) / 8, chunks = static_cast<int64_t>(job.KB) * 8;
   const int8_t* q_end = job.q + job.M * job.K;
   int turn = 0;
   for (int64_t m = blockIdx.x - 4; m < job.M; m += gridDim.x - 4, turn ^= 1) {
     uint32_t t = 0;
-    const RowBytes row = row_bytes<uint16_t>(job.dh, job.M, job.N, m);
+    const int ahead = dh.ahead(m);
 #pragma unroll 1
     for (int64_t c0 = threadIdx.x; c0 < items; c0 += static_cast<int64_t>(UD) * blockDim.x) {
-      RowItem<4, VEC_DH> it[UD];
+      typename FlatRows<DT, VEC_DH>::Item it[UD];
 #pragma unroll
-      for (int u = 0; u < UD; ++u) it[u].load(row, c0 + static_cast<int64_t>(u) * blockDim.x, bytes);
+      for (int u = 0; u < UD; ++u)
+        dh.load(it[u], m, ahead, c0 + static_cast<int64_t>(u) * blockDim.x);
 #pragma unroll
       for (int u = 0; u < UD; ++u) {
-        it[u].settle(row, c0 + static_cast<int64_t>(u) * blockDim.x, bytes);
+        dh.settle(it[u], ahead, c0 + static_cast<int64_t>(u) * blockDim.x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) t = __vmaxu2(t, it[u].w[j] & 0x7fff7fffu);
       }
@@ -525,19 +514,31 @@ cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaSt
   const bool vec = job.K % 8 == 0 && on16(job.x) && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
   // One item a thread while there are few rows (its latency is what counts),
   // else as many as it holds, and as many CTAs as the SMs take at once.
-  const int64_t items = job.operand != nullptr ? static_cast<int64_t>(job.KB) * 8 : job.K / 8 + 2;
-  const int64_t each = job.M <= 2 * device_sm_count() ? 1 : dtype == Q8_F32 ? 2 : 4;
+  const int64_t items = job.operand != nullptr ? static_cast<int64_t>(job.KB) * 8
+                        : vec                  ? job.K / 8
+                                               : job.K / 8 + 2;
+  const int held = dtype == Q8_F32 ? quantize_items<Q8_F32>() : quantize_items<Q8_F16>();
   const int64_t lanes = job.operand != nullptr && !vec ? 31 : 32;
-  const int64_t warps = (items + each * lanes - 1) / (each * lanes);
-  const int threads = static_cast<int>(std::min<int64_t>(32, std::max<int64_t>(2, warps))) * 32;
-  const int grid = static_cast<int>(
-      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / threads)));
-  return by_type(dtype, vec, [&](auto t, auto v) {
+  const bool few = job.M <= 2 * device_sm_count();
+  const auto go = [&](auto t, auto v, auto s_) {
     constexpr int DT = decltype(t)::value;
-    constexpr bool VEC = decltype(v)::value;
+    constexpr bool VEC = decltype(v)::value, SHORT = decltype(s_)::value;
+    int64_t threads = 256, rows = 8;   // of a CTA
+    if constexpr (!SHORT) {
+      const int64_t each = few ? 1 : held;
+      threads = 32 * std::min<int64_t>(kQuantizeThreads / 32,
+                                       std::max<int64_t>(2, (items + each * lanes - 1) / (each * lanes)));
+      rows = 1;
+    }
+    const int grid = static_cast<int>(std::min<int64_t>(
+        (job.M + rows - 1) / rows, static_cast<int64_t>(device_sm_count()) * std::max<int64_t>(1, 1024 / threads)));
     return job.operand != nullptr
-               ? launch_pdl(quantize_token_kernel<DT, VEC, true>, grid, threads, 0, s, job)
-               : launch_pdl(quantize_token_kernel<DT, VEC, false>, grid, threads, 0, s, job);
+               ? launch_pdl(quantize_token_kernel<DT, VEC, true, SHORT>, grid, threads, 0, s, job)
+               : launch_pdl(quantize_token_kernel<DT, VEC, false, SHORT>, grid, threads, 0, s, job);
+  };
+  const bool is_short = !few && items <= held * lanes;
+  return by_type(dtype, vec, [&](auto t, auto v) {
+    return is_short ? go(t, v, std::true_type()) : go(t, v, std::false_type());
   });
 }
 
