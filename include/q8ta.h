@@ -621,8 +621,7 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
  *   q8_dequantize_per_token  out[m,k] = (float)q[m,k] * scales[m], rounded to
  *     the float dtype.
  * Guards: 0 <= M <= INT32_MAX (0: nothing to do), K >= 1, M*K*4 within int64;
- * pointers aligned to their element; Q8_I8 is Q8_ERR_UNSUPPORTED.  Rows of a
- * multiple of 8 values on 16-byte aligned bases are the fast form.
+ * pointers aligned to their element; Q8_I8 is Q8_ERR_UNSUPPORTED.
  */
 q8_status q8_quantize_per_token(const void* x, q8_dtype dtype, int64_t M, int64_t K, int8_t* q,
                                 float* scales, q8_stream_t stream);
@@ -653,7 +652,8 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
  * Results do not depend on timing.
  * Guards: M and K as above, 1 <= N <= 2^24 (backward: K), the tiles' count
  * and products of sizes as in q8_linear_experts; workspace of the matching
- * number of bytes and the packed weights 256-byte aligned.
+ * number of bytes (0 for one or two rows and up to 8 short ones) and the packed
+ * weights 256-byte aligned.
  */
 size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N);
 q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,

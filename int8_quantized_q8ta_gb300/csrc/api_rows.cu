@@ -190,9 +190,9 @@ q8_status q8_tile_pack_weight(const int8_t* weight, int64_t E, int64_t N, int64_
   auto* dst = static_cast<uint8_t*>(packed);
   cudaError_t e = q8::launch_pack_tile_weight(weight, E, N, K, dst, cs(stream));
   if (e == cudaSuccess)
-    e = q8::launch_weight_block_bound(weight, E * N, K, 1, K,
-                                      reinterpret_cast<int32_t*>(dst + tile_weight_bytes(E, N, K)),
-                                      cs(stream));
+    e = q8::launch_tile_weight_bound(dst, static_cast<int64_t>(tile_weight_bytes(E, N, K) / 8192),
+                                     reinterpret_cast<int32_t*>(dst + tile_weight_bytes(E, N, K)),
+                                     cs(stream));
   // finished before the call returns: later kernels read a packed weight
   // without waiting for the kernel before them
   if (e == cudaSuccess) e = cudaStreamSynchronize(cs(stream));

@@ -301,13 +301,12 @@ q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, 
   if (packed_bytes < bytes) return Q8_ERR_WORKSPACE;
   if (!aligned(packed, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
   auto* dst = static_cast<uint8_t*>(packed);
-  auto* bound = reinterpret_cast<int32_t*>(dst + bytes - q8::kWorkspaceAlign);
   cudaError_t e = q8::launch_pack_gated(gate, up, N, K, transposed != 0, dst, cs(stream));
-  if (!transposed) {
-    if (e == cudaSuccess) e = q8::launch_weight_block_bound(gate, N, K, 1, K, bound, cs(stream));
-    if (e == cudaSuccess) e = q8::launch_weight_block_bound(up, N, K, 1, K, bound + 1, cs(stream));
-    if (e == cudaSuccess) e = q8::launch_larger_bound(bound, cs(stream));
-  }
+  // (the gradient's f32 sums need no bound)
+  if (e == cudaSuccess && !transposed)
+    e = q8::launch_tile_weight_bound(
+        dst, static_cast<int64_t>((bytes - q8::kWorkspaceAlign) / 8192),
+        reinterpret_cast<int32_t*>(dst + bytes - q8::kWorkspaceAlign), cs(stream));
   // finished before the call returns, as in q8_tile_pack_weight
   if (e == cudaSuccess) e = cudaStreamSynchronize(cs(stream));
   return cuda_status(e);

@@ -170,6 +170,9 @@ inline int64_t gated_rows(int64_t N) { return 2 * round_up(N, 16); }
 // flipped, zeros beyond N and K.
 cudaError_t launch_pack_tile_weight(const int8_t* w, int64_t E, int64_t N, int64_t K, uint8_t* dst,
                                     cudaStream_t s);
+// *bound: the largest sum of |w| over 64 inputs (a k-block) in packed tiles.
+cudaError_t launch_tile_weight_bound(const uint8_t* packed, int64_t tiles, int32_t* bound,
+                                     cudaStream_t s);
 
 // Token operand: dst[kb][s][64] = f16(x[row(s)][64 kb ..] - zp), zeros beyond
 // K; row(s) = order[s] / k, or s when order is null; rows whose order is out

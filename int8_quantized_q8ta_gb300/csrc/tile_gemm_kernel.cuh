@@ -12,8 +12,8 @@
 //
 // Weights stay int8 in memory (1 byte read per weight, half of the bf16 copy
 // the plain linear keeps): a tile of 128 output channels x 64 inputs is one
-// contiguous 8 KB run, copied to shared memory in bulk, turned into f16 by
-// four warps (a byte permute and half a packed subtraction per value) and put
+// contiguous 8 KB run, copied to shared memory in bulk, turned into f16 by four
+// or eight warps (a byte permute and half a packed subtraction per value) and put
 // into TENSOR MEMORY as the MMA's A operand.  Tokens are the B operand, f16
 // copies of x - zp in K-blocked rows that TMA fetches 128-byte swizzled.  So
 // weights are on the MMA's M side (always 128 lanes, however few tokens a
@@ -26,10 +26,10 @@
 //
 // Work split: whole waves of (tile, output block) units, then the last one to
 // two waves' k-blocks as one line cut into equal runs, one per CTA, so that a
-// few wide units and many small ones fill the SMs alike.  A unit cut by a run's end is summed by
-// whichever of its CTAs comes last, warp by warp, from the int32 parts the
-// others left in the workspace: integer sums, the same in any order.  No CTA
-// waits for another.
+// few wide units and many small ones fill the SMs alike.  A unit cut by a run's
+// end is summed by whichever of its CTAs comes last, warp by warp, from the int32
+// parts the others left in the workspace: integer sums, the same in any order
+// (a gradient's f32 ones in the order of their CTAs).  No CTA waits for another.
 //
 // Adapters: after a unit's k-blocks, its last run multiplies B[a] by the rows'
 // h for each adapter the tile holds, into an accumulator of its own: tf32
@@ -88,18 +88,20 @@ enum TileForm { kFormBatch, kFormToken, kFormGated, kFormGatedGrad, kFormGrad };
 // The two forms of the kernel.
 //   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
 // a tile through the 2-SM MMA, each with its own 128 output channels and half
-// of the rows in its shared memory.  What bounds long batches is the bytes an
-// SM can pull from L2 (some 47 a cycle measured here): 12 KB of tokens and
-// 8 KB of weights for 384 cycles of MMAs, where one CTA alone needs 32 KB.
-// 8192 rows of 16 experts x 4096 x 4096: 180 us, 44 bytes a cycle and SM, 69%
-// of the tensor pipe's cycles; 2048 rows x 11008 x 4096 with 8 adapters of rank
-// 64 140 us, 118 without.
+// of the rows in its shared memory: 12 KB of tokens and 8 KB of weights from L2
+// for a k-block's 384 cycles of MMAs, where one CTA alone needs 32 KB.  Its four
+// converting warps take some 250 cycles a stage to wait and announce and 130 a
+// k-block to convert, so a stage is two k-blocks: with one they took 500 cycles
+// a k-block and the MMAs waited (2048 rows, the pair 11008 x 4096 gated 221 us);
+// now the MMAs are what it waits for (202 us, 83% of the tensor pipe's cycles in
+// the kernel; then the GPU's power).  8192 rows of 16 experts x 4096 x 4096: 184
+// us (195 so); 2048 rows x 11008 x 4096 with 8 adapters of rank 64 152 (161).
 //   Narrow (up to 64 rows): one CTA; two k-blocks a stage and twice the
-// converting warps, since the weights' way through them is what such tiles
-// wait for once memory is busy.  128 rows of 56 experts x 2048 x 2048: 37.9 us
-// with the operand before it, 35.0 at the copy rate; 64 rows x 11008 x 4096 20
-// us, 24.3 with 32 adapters of rank 16; one row x 4096 x 4096 with its adapter
-// 10.5 us.
+// converting warps, in two groups.  Conversion and the MMAs' issue take some 480
+// cycles a stage each.  128 rows of 56 experts x 2048 x 2048: 37.7 us with the
+// operand before it, 35.0 at the copy rate; 24 rows x 4096 x 11008 15.0 us; 64
+// rows x 11008 x 4096 with 32 adapters of rank 16 24.4 us; one row x 4096 x 4096
+// with its adapter 10.5 to 12 us.
 template <bool PAIR>
 struct Form {
   static constexpr int CG = PAIR ? 2 : 1;

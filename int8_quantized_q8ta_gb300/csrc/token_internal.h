@@ -88,7 +88,5 @@ cudaError_t launch_token_rows(TokenRowsJob job, bool gated, cudaStream_t s);
 // inputs.
 cudaError_t launch_pack_gated(const int8_t* gate, const int8_t* up, int64_t N, int64_t K,
                               bool transposed, uint8_t* dst, cudaStream_t s);
-// word[0] = max(word[0], word[1])
-cudaError_t launch_larger_bound(int32_t* word, cudaStream_t s);
 
 }  // namespace q8

@@ -478,10 +478,6 @@ __global__ void __launch_bounds__(256) pack_gated_kernel(const int8_t* __restric
                         v[3] ^ 0x80808080u);
   }
 }
-__global__ void larger_bound_kernel(int32_t* word) {
-  pdl_wait();
-  word[0] = max(word[0], word[1]);
-}
 
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -597,10 +593,6 @@ cudaError_t launch_pack_gated(const int8_t* gate, const int8_t* up, int64_t N, i
   auto* to = reinterpret_cast<uint4*>(dst);
   return transposed ? launch_pdl(pack_gated_kernel<true>, grid, 256, 0, s, gate, up, N, K, NB, KB, to)
                     : launch_pdl(pack_gated_kernel<false>, grid, 256, 0, s, gate, up, N, K, NB, KB, to);
-}
-
-cudaError_t launch_larger_bound(int32_t* word, cudaStream_t s) {
-  return launch_pdl(larger_bound_kernel, 1, 1, 0, s, word);
 }
 
 }  // namespace q8
