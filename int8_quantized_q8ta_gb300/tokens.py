@@ -31,7 +31,11 @@ _HALVES = (torch.float16, torch.bfloat16)
 
 class _Calls:
     def __getattr__(self, name):
-        from . import _torch_calls   # built beside the library; there is no other way on a GPU
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise ImportError("_torch_calls.so is missing or of another torch: build it with "
+                              "`python -m int8_quantized_q8ta_gb300._build --force`") from e
         f = getattr(_torch_calls, name)
         setattr(self, name, f)       # found here from the next call on
         return f

@@ -449,6 +449,63 @@ def test_gradients_of_many_rows(M, N, K):
     within(dx, want.cpu(), bound.cpu())
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 65, 40), (100, 320, 96)])
+@pytest.mark.parametrize("dtype", HALVES)
+def test_masked_gradients_count_as_zeros(dtype, M, N, K):
+    # whatever they are: infinities, NaN, the type's largest
+    dy, y = rows(M, M, N, dtype), rows(K, M, N, dtype)
+    y[0] = -1.0                                        # a row of nothing
+    y[1, ::2], y[1, 1::2] = float("nan"), -0.0         # NaN and zeros are not above 0
+    w, ws, _ = weights(N, N, K)
+    packed_t = q8.pack_tile_weight(w.t().contiguous().to(DEV))
+    clean = torch.where(y > 0, dy, torch.zeros((), dtype=dtype))
+    want = q8.linear_per_token_backward(clean.to(DEV), packed_t, ws.to(DEV))
+    for bad in (float("inf"), float("-inf"), float("nan"), torch.finfo(dtype).max):
+        dirty = torch.where(y > 0, dy, torch.full((), bad, dtype=dtype))
+        got = q8.linear_per_token_backward(dirty.to(DEV), packed_t, ws.to(DEV), y=y.to(DEV))
+        assert torch.equal(got, want) and bool((got[:2] == 0).all())
+
+
+def test_offsets_beyond_32_bits():
+    # 2.2e9 values, 4.5 GB, of which the last rows count
+    M, K, N = 700_001, 3201, 64
+    w, ws, b = weights(3, N, K)
+    last = rows(1, 40, K, torch.bfloat16)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[-40:] = last.to(DEV)
+    want_q, want_s = ref.quantize(last)
+    q, s = q8.quantize_per_token(x)
+    same(q[-40:], want_q)
+    same(s[-40:], want_s)
+    same(q8.dequantize_per_token(q, s, out_dtype=torch.bfloat16, out=x)[-40:],
+         (want_q.float() * want_s[:, None]).bfloat16())
+    del x
+    y = q8.linear_per_token(q, s, q8.pack_tile_weight(w.to(DEV)), ws.to(DEV), b.to(DEV))
+    same(y[-40:], ref.product(want_q, want_s, w, ws, b).bfloat16())
+    # and 64 inputs to 3201 outputs, its gradient back, the gated pair's
+    del q
+    x = torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    x[-40:] = rows(2, 40, N, torch.bfloat16).to(DEV)
+    wt = w.t().contiguous()
+    wts = torch.full((2, K), 0.01)
+    y = q8.linear_per_token(x, None, q8.pack_tile_weight(wt.to(DEV)), wts[0].to(DEV), None)
+    same(y[-40:], ref.product(*ref.quantize(x[-40:].cpu()), wt, wts[0], None).bfloat16())
+    dx = q8.linear_per_token_backward(y, q8.pack_tile_weight(w.to(DEV)), wts[0].to(DEV))
+    few = q8.linear_per_token_backward(y[-40:], q8.pack_tile_weight(w.to(DEV)), wts[0].to(DEV))
+    want, bound = ref.linear_grad(y[-40:].cpu(), wt, wts[0])
+    within(dx[-40:], want, bound)
+    within(few, want, bound)
+    q, s = q8.quantize_per_token(x)
+    del dx, x
+    pair = (wt.to(DEV), wt.to(DEV))
+    gate, gt = q8.pack_gated_weight(*pair), q8.pack_gated_weight_t(*pair)
+    dx = q8.linear_gated_backward(y, q, s, gate, gt, wts.to(DEV), None)
+    g = ref.product(q[-40:].cpu(), s[-40:].cpu(), wt, wts[0], None)
+    within(dx[-40:], *ref.gated_grad(y[-40:].cpu(), g, g, torch.stack([wt, wt]), wts, "silu", s[-40:].cpu()))
+    h = q8.linear_gated(q, s, gate, wts.to(DEV), None, out=y)
+    within(h[-40:], *ref.gated(g, g, "silu", torch.bfloat16))
+
+
 @pytest.mark.parametrize("M", [5, 90])
 def test_gradients_of_small_and_uneven_scales(M):
     # float16 gradients stay precise whatever the size of the channels' scales
