@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -486,6 +487,22 @@ int blocks_for(int64_t warps) {
       1, std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(device_sm_count()) * 8)));
 }
 
+// CTAs of so many threads that an SM takes at once, asked for once each (`fit`, by
+// warps): a persistent kernel's rows are dealt to those, and a second wave of CTAs
+// would only wait for the first (4096 rows of 4096 f32 16.6 us, 14.7 without).
+template <typename K>
+int64_t resident_ctas(K kernel, int threads, std::atomic<int> (&fit)[33]) {
+  int n = fit[threads / 32].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 1;
+    }
+    fit[threads / 32].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // f(type, vectors) with the dtype and a truth value as constants
 template <typename F>
 cudaError_t by_type(q8_dtype dt, bool vec, F&& f) {
@@ -526,11 +543,14 @@ cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaSt
                                        std::max<int64_t>(2, (items + each * lanes - 1) / (each * lanes)));
       rows = 1;
     }
-    const int grid = static_cast<int>(std::min<int64_t>(
-        (job.M + rows - 1) / rows, static_cast<int64_t>(device_sm_count()) * std::max<int64_t>(1, 1024 / threads)));
-    return job.operand != nullptr
-               ? launch_pdl(quantize_token_kernel<DT, VEC, true, SHORT>, grid, threads, 0, s, job)
-               : launch_pdl(quantize_token_kernel<DT, VEC, false, SHORT>, grid, threads, 0, s, job);
+    const auto launch = [&](auto kernel, std::atomic<int>(&fit)[33]) {
+      const int64_t ctas = resident_ctas(kernel, static_cast<int>(threads), fit) * device_sm_count();
+      const int grid = static_cast<int>(std::min<int64_t>((job.M + rows - 1) / rows, ctas));
+      return launch_pdl(kernel, grid, static_cast<int>(threads), 0, s, job);
+    };
+    static std::atomic<int> fit[2][33];
+    return job.operand != nullptr ? launch(quantize_token_kernel<DT, VEC, true, SHORT>, fit[0])
+                                  : launch(quantize_token_kernel<DT, VEC, false, SHORT>, fit[1]);
   };
   const bool is_short = !few && items <= held * lanes;
   return by_type(dtype, vec, [&](auto t, auto v) {
@@ -556,13 +576,16 @@ cudaError_t launch_grad_operand(const GradOperandJob& job, q8_dtype dtype, cudaS
       job.M <= 2 * device_sm_count() ? 1 : vec && !job.y ? 4 : vec || !job.y ? 2 : 1;   // as grad_items
   const int threads = static_cast<int>(
       std::min<int64_t>(512, std::max<int64_t>(64, round_up((items + each - 1) / each, 32))));
-  const int grid = static_cast<int>(
-      std::min<int64_t>(job.M, static_cast<int64_t>(device_sm_count()) * std::max(1, 512 / threads)));
   const auto go = [&](auto t, auto v) {
     constexpr int DT = decltype(t)::value;
     constexpr bool VEC = decltype(v)::value;
-    return job.y != nullptr ? launch_pdl(grad_operand_kernel<DT, VEC, true>, grid, threads, 0, s, job)
-                            : launch_pdl(grad_operand_kernel<DT, VEC, false>, grid, threads, 0, s, job);
+    const auto launch = [&](auto kernel, std::atomic<int>(&fit)[33]) {
+      const int64_t ctas = resident_ctas(kernel, threads, fit) * device_sm_count();
+      return launch_pdl(kernel, static_cast<int>(std::min<int64_t>(job.M, ctas)), threads, 0, s, job);
+    };
+    static std::atomic<int> fit[2][33];
+    return job.y != nullptr ? launch(grad_operand_kernel<DT, VEC, true>, fit[0])
+                            : launch(grad_operand_kernel<DT, VEC, false>, fit[1]);
   };
   return by_half(dtype, vec, go);
 }
