@@ -358,41 +358,51 @@ struct TokenItem : RowItem<DT == Q8_F32 ? 8 : 4, VEC> {
 };
 
 // Rows as items of 8 values on boundaries of 8.  VEC: rows are whole items.  Else
-// row m begins t = ahead(m) values into its first item, and what belongs to its
-// neighbours counts as zeros.
+// a row begins t values into its first item, and what belongs to its neighbours
+// counts as zeros.  (A row's values are numbered in 32 bits: K <= INT32_MAX / 2.)
 template <int DT, bool VEC>
 struct FlatRows {
   using T = FloatOf<DT>;
   using Item = TokenItem<DT, true>;
+  struct Row {
+    const T* at;
+    int t, lo, hi;   // values from lo to hi lie in the matrix
+  };
   const T *x, *end;
-  int64_t K;
-  int off;   // values that x lies behind a boundary of 8
-  __device__ __forceinline__ FlatRows(const void* x_, int64_t M, int64_t K_)
-      : x(static_cast<const T*>(x_)), end(x + M * K_), K(K_),
+  int64_t M;
+  int K, off;   // off: values that x lies behind a boundary of 8
+  __device__ __forceinline__ FlatRows(const void* x_, int64_t M_, int64_t K_)
+      : x(static_cast<const T*>(x_)), end(x + M_ * K_), M(M_), K(static_cast<int>(K_)),
         off(VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(x_) / sizeof(T) & 7)) {}
-  __device__ __forceinline__ int ahead(int64_t m) const {
-    return VEC ? 0 : static_cast<int>((off + m * K) & 7);
+  // Row m; past the last one, a row without values to load.
+  __device__ __forceinline__ Row row(int64_t m) const {
+    const T* at = x + m * K;
+    Row r{at, VEC ? 0 : static_cast<int>((off + m * K) & 7), 0, m < M ? K : 0};
+    if (!VEC && K >= 8) {   // (items of shorter rows reach further than one neighbour)
+      if (m > 0) r.lo = -8;
+      if (m + 1 < M) r.hi = K + 8;
+    }
+    return r;
   }
-  // Item c of row m: asked for; zeros past the row.
-  __device__ __forceinline__ void load(Item& it, int64_t m, int t, int64_t c) const {
-    const int64_t e = c * 8 - t;   // the row's values from e on
-    const T* p = x + m * K + e;
+  // Item c of a row: asked for; zeros past the row.
+  __device__ __forceinline__ void load(Item& it, const Row& r, int c) const {
+    const int e = c * 8 - r.t;   // the row's values from e on
     it.zero();
     if constexpr (VEC) {
-      if (e < K) it.load_whole(p);
-    } else if (e < K) {
-      if (p >= x && p + 8 <= end) {
-        it.load_whole(p);
+      if (e < r.hi) it.load_whole(r.at + e);
+    } else if (e < K && r.hi > 0) {
+      if (e >= r.lo && e + 8 <= r.hi) {
+        it.load_whole(r.at + e);
       } else {   // the ends of the matrix
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (e + j >= 0 && e + j < K) it.set(j, p[j]);
+          if (e + j >= 0 && e + j < K) it.set(j, r.at[e + j]);
       }
     }
   }
   // Once it is there: zeros for the neighbours' values.
-  __device__ __forceinline__ void settle(Item& it, int t, int64_t c) const {
-    const int64_t e = c * 8 - t;
+  __device__ __forceinline__ void settle(Item& it, const Row& r, int c) const {
+    const int e = c * 8 - r.t;
     if (!VEC && (e < 0 || e + 8 > K)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)

@@ -24,9 +24,9 @@ namespace {
 // it in registers in between, with the next row's loads already on their way; so
 // it comes from memory once, and memory is never idle while a row waits for its
 // scale.  Only rows beyond U items for each of 704 threads are read again (from
-// L2).  Bytes bound it: 8192 rows of 11008 bf16 46 us (floor 41), of 8191 58 (30).
+// L2).  Bytes bound it: 8192 rows of 11008 bf16 45 us (floor 41), of 8191 48 (30).
 //   SHORT: rows of which a warp holds all items go to a warp each, without a
-// barrier (16,000 rows of 200 f16 6.9 us, 13.2 by CTAs; of 201 13.3, 29).
+// barrier (16,000 rows of 200 f16, cold, 6.9 us, 13.2 by CTAs; of 201 13.3, 29).
 //   Rows that are no multiple of 8 begin t values into their first item.  q, whose
 // rows begin the same way, takes whole items too, but the operand has its own:
 // 8 - t values of an item and t of the next one, which a lane gets from the lane
@@ -59,37 +59,33 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token
       job.counts[i] = 0;
   const Rows rows(job.x, job.M, job.K);
   const bool q_whole = (reinterpret_cast<uintptr_t>(job.q) - rows.off) % 8 == 0;
-  const int64_t chunks = static_cast<int64_t>(job.KB) * 8;   // of the operand's row
+  const int chunks = job.KB * 8;   // of the operand's row
   // this thread's items: every step'th, in the 31-lane form less its last lanes
-  const int64_t c0 = warp * kLanes + lane, step = warps * kLanes;
+  const int c0 = warp * kLanes + lane, step = warps * kLanes;
   // (items that a row can reach, for whole warps to go through)
-  const int64_t items = OP ? chunks : (job.K + (VEC ? 7 : 14)) / 8;
+  const int items = OP ? chunks : (rows.K + (VEC ? 7 : 14)) / 8;
   Item held[U];
-  {
-    const int t = rows.ahead(m0);
+  typename Rows::Row row = rows.row(m0);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      rows.load(held[u], m0, t, m0 < job.M ? c0 + u * step : INT64_MAX / 16);
-  }
+  for (int u = 0; u < U; ++u) rows.load(held[u], row, c0 + u * step);
   int turn = 0;
   for (int64_t m = m0; m < job.M; m += m_step, turn ^= 1) {
-    const int t = rows.ahead(m);
     Item next[U];
-    const int64_t m_next = m + m_step;
-    const int t_next = rows.ahead(m_next);
+    const typename Rows::Row next_row = rows.row(m + m_step);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      rows.load(next[u], m_next, t_next, m_next < job.M ? c0 + u * step : INT64_MAX / 16);
+    for (int u = 0; u < U; ++u) rows.load(next[u], next_row, c0 + u * step);
+    // (items beyond those: at least in L2 when their row comes)
+    for (int c = c0 + U * step; c * 8 < next_row.hi; c += step) prefetch_l2(next_row.at + c * 8);
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rows.settle(held[u], t, c0 + u * step);
+      rows.settle(held[u], row, c0 + u * step);
       top = max(top, held[u].top());
     }
-    for (int64_t c = c0 + U * step; c * 8 - t < job.K; c += step) {
+    for (int c = c0 + U * step; c * 8 - row.t < rows.K; c += step) {
       Item it;
-      rows.load(it, m, t, c);
-      rows.settle(it, t, c);
+      rows.load(it, row, c);
+      rows.settle(it, row, c);
       top = max(top, it.top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -100,17 +96,18 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token
     }
     const TokenScale sc = token_scale(top);
     if (warp == 0 && lane == 0) job.scales[m] = sc.scale;
-    const auto put = [&](const Item& it, int64_t c) {
+    int8_t* q_row = job.q == nullptr ? nullptr : job.q + m * job.K;
+    const auto put = [&](const Item& it, int c) {
       const uint2 q = it.quantize(sc.inv);
-      const int64_t e = c * 8 - t;
-      if (job.q != nullptr && (kLanes == 32 || lane < kLanes)) {
-        int8_t* to = job.q + m * job.K + e;
-        if (VEC ? e < job.K : q_whole && e >= 0 && e + 8 <= job.K) {
+      const int e = c * 8 - row.t;
+      if (q_row != nullptr && (kLanes == 32 || lane < kLanes)) {
+        int8_t* to = q_row + e;
+        if (VEC ? e < rows.K : q_whole && e >= 0 && e + 8 <= rows.K) {
           *reinterpret_cast<uint2*>(to) = q;
         } else if (!VEC) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (e + j >= 0 && e + j < job.K)
+            if (e + j >= 0 && e + j < rows.K)
               to[j] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
         }
       }
@@ -119,9 +116,10 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token
         if constexpr (!VEC) {
           const uint32_t x2 = __shfl_down_sync(0xffffffffu, q.x, 1);
           const uint32_t y2 = __shfl_down_sync(0xffffffffu, q.y, 1);
-          const int bits = (t & 3) * 8;   // (an item's own from byte t on)
-          own = t < 4 ? make_uint2(__funnelshift_r(q.x, q.y, bits), __funnelshift_r(q.y, x2, bits))
-                      : make_uint2(__funnelshift_r(q.y, x2, bits), __funnelshift_r(x2, y2, bits));
+          const int bits = (row.t & 3) * 8;   // (an item's own from byte t on)
+          own = row.t < 4
+                    ? make_uint2(__funnelshift_r(q.x, q.y, bits), __funnelshift_r(q.y, x2, bits))
+                    : make_uint2(__funnelshift_r(q.y, x2, bits), __funnelshift_r(x2, y2, bits));
         }
         if (c < chunks && (kLanes == 32 || lane < kLanes))
           *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
@@ -132,14 +130,15 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (c0 + u * step - lane < items) put(held[u], c0 + u * step);
-    for (int64_t c = c0 + U * step; c - lane < items; c += step) {
+    for (int c = c0 + U * step; c - lane < items; c += step) {
       Item it;
-      rows.load(it, m, t, c);
-      rows.settle(it, t, c);
+      rows.load(it, row, c);
+      rows.settle(it, row, c);
       put(it, c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) held[u] = next[u];
+    row = next_row;
   }
 }
 
@@ -399,21 +398,22 @@ __global__ void __launch_bounds__(512, 3) gated_grad_front_kernel(const GatedGra
     return;
   }
   const FlatRows<DT, VEC_DH> dh(job.dh, job.M, job.N);
-  const int64_t items = (job.N + 14) / 8, chunks = static_cast<int64_t>(job.KB) * 8;
+  const int items = static_cast<int>((job.N + 14) / 8);
+  const int64_t chunks = static_cast<int64_t>(job.KB) * 8;
   const int8_t* q_end = job.q + job.M * job.K;
   int turn = 0;
   for (int64_t m = blockIdx.x - 4; m < job.M; m += gridDim.x - 4, turn ^= 1) {
     uint32_t t = 0;
-    const int ahead = dh.ahead(m);
+    const auto row = dh.row(m);
 #pragma unroll 1
-    for (int64_t c0 = threadIdx.x; c0 < items; c0 += static_cast<int64_t>(UD) * blockDim.x) {
+    for (int c0 = threadIdx.x; c0 < items; c0 += UD * blockDim.x) {
       typename FlatRows<DT, VEC_DH>::Item it[UD];
 #pragma unroll
       for (int u = 0; u < UD; ++u)
-        dh.load(it[u], m, ahead, c0 + static_cast<int64_t>(u) * blockDim.x);
+        dh.load(it[u], row, c0 + u * blockDim.x);
 #pragma unroll
       for (int u = 0; u < UD; ++u) {
-        dh.settle(it[u], ahead, c0 + static_cast<int64_t>(u) * blockDim.x);
+        dh.settle(it[u], row, c0 + u * blockDim.x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) t = __vmaxu2(t, it[u].w[j] & 0x7fff7fffu);
       }
