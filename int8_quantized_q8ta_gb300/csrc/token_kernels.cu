@@ -39,7 +39,8 @@ constexpr int quantize_items() {        // of a thread, in registers
 }
 
 template <int DT, bool VEC, bool OP, bool SHORT>
-__global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token_kernel(const QuantizeJob job) {
+__global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads)
+    quantize_token_kernel(const QuantizeJob job) {
   using Rows = FlatRows<DT, VEC>;
   using Item = typename Rows::Item;
   constexpr int U = quantize_items<DT>();
@@ -50,9 +51,9 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads) quantize_token
   const int lane = threadIdx.x & 31;
   // this row's warps, and which of them this is; rows on their way at once
   const int warp = SHORT ? 0 : threadIdx.x >> 5, warps = SHORT ? 1 : blockDim.x >> 5;
-  const int64_t m0 = SHORT ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                           : blockIdx.x;
-  const int64_t m_step = SHORT ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+  const int64_t teams = SHORT ? blockDim.x >> 5 : 1;   // rows of a CTA
+  const int64_t m0 = blockIdx.x * teams + (SHORT ? threadIdx.x >> 5 : 0);
+  const int64_t m_step = gridDim.x * teams;
   if constexpr (OP)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
          i < job.count_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
@@ -422,8 +423,9 @@ __global__ void __launch_bounds__(512, 3) gated_grad_front_kernel(const GatedGra
     for (int64_t c0 = threadIdx.x; c0 < chunks; c0 += static_cast<int64_t>(UQ) * blockDim.x) {
       uint2 w[UQ];
 #pragma unroll
-      for (int u = 0; u < UQ; ++u) w[u] = load_int8x8<VEC_Q>(job.q, m * job.K, (c0 + static_cast<int64_t>(u) * blockDim.x) * 8,
-                                  job.K, q_end);
+      for (int u = 0; u < UQ; ++u)
+        w[u] = load_int8x8<VEC_Q>(job.q, m * job.K,
+                                  (c0 + static_cast<int64_t>(u) * blockDim.x) * 8, job.K, q_end);
 #pragma unroll
       for (int u = 0; u < UQ; ++u) {
         const int64_t c = c0 + static_cast<int64_t>(u) * blockDim.x;
@@ -460,7 +462,8 @@ __global__ void __launch_bounds__(256) pack_gated_kernel(const int8_t* __restric
         const int64_t pair = in0 + j;   // the interleaved index
         const int64_t n = (pair >> 5) * 16 + (pair & 15);
         if (n < N && row < K)
-          v[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(((pair & 16) ? up : gate)[n * K + row]))
+          v[j / 4] |= static_cast<uint32_t>(
+                          static_cast<uint8_t>(((pair & 16) ? up : gate)[n * K + row]))
                       << (8 * (j % 4));
       }
     } else {

@@ -18,12 +18,12 @@
 // 17.9 and 3.1, with a row's first 4 items held instead of 2 11.0, 18.4 and 3.1.
 //   One or two rows: four products a dp4a, straight from the registers that the
 // loads fill; the rows' int8 come from shared memory, 16 bytes that half a warp
-// shares.  That is one load from there for each of memory and row, and an
-// SM can do two, so three to eight rows go through m16n8k16 MMAs, f16 in and f32 out: the packed
-// 16-byte chunks are a thread's fragments as they lie (the order of a sum's terms
-// is free, so thread t of four takes inputs 16 t to 16 t + 15 of a k-block),
-// turned into f16 by a byte permute and half a subtraction a value, and rows are
-// the MMA's 8 columns.  Products are at most 2^14 and a chunk of 8 k-blocks adds
+// shares.  That is a load from there for each row and load of weights, of which an
+// SM can do two, so three to eight rows go through m16n8k16 MMAs, f16 in and f32
+// out: the packed 16-byte chunks are a thread's fragments as they lie (the order
+// of a sum's terms is free, so thread t of four takes inputs 16 t to 16 t + 15 of
+// a k-block), turned into f16 by a byte permute and half a subtraction a value,
+// and rows are the MMA's 8 columns.  Products are at most 2^14 and a chunk of 8 k-blocks adds
 // 512 of them, so its f32 sums are exact integers; they are then added up in
 // int32, across warps too, so the order does not matter.
 //   Every CTA quantizes all rows for itself (one row of 4096 is 8 KB from L2,
