@@ -40,13 +40,15 @@ struct TokenSpace {
   TilePlan plan;
   size_t scales, total;
 };
-TokenSpace token_space(int64_t M, int64_t N, int64_t K) {
+TokenSpace token_space(const TilePlan& plan, int64_t M) {
   TokenSpace t{};
-  t.plan = plan_group(M, N, K, kMinRun);
-  t.scales = t.plan.total;
+  t.plan = plan;
+  t.scales = plan.total;
   t.total = t.scales + q8::align_ws(static_cast<size_t>(M) * 4);
   return t;
 }
+// (any height's plan has this size)
+size_t token_space_bytes(int64_t M, int64_t K) { return token_space(plan_tiles(M, K, 1), M).total; }
 
 // Inputs of the transposed gated weight: up to the end of the last block of 128
 // packed rows, which is how far the gated gradient writes its operand.
@@ -63,10 +65,10 @@ struct GradSpace {
   TilePlan rows, grads;
   size_t grad_operand, parts, counts, powers, total;
 };
-GradSpace gated_grad_space(int64_t M, int64_t N, int64_t K) {
+GradSpace gated_grad_space(const TilePlan& rows, const TilePlan& grads, int64_t M) {
   GradSpace t{};
-  t.rows = plan_group(M, q8::gated_rows(N), K, kMinRun);
-  t.grads = plan_group(M, K, gated_inputs(N), kMinRun);
+  t.rows = rows;
+  t.grads = grads;
   t.grad_operand = t.rows.operand;
   t.parts = t.grad_operand + t.grads.operand;
   t.counts = t.parts + t.grads.parts;
@@ -161,7 +163,7 @@ q8_status token_product(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, i
     job.out = out;
     return cuda_status(q8::launch_token_rows(job, gated, s));
   }
-  const TokenSpace sp = token_space(M, rows, K);
+  const TokenSpace sp = token_space(plan_group(M, rows, K, kMinRun), M);
   if (!units_ok(M, 1, rows, K, sp.plan)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
@@ -220,7 +222,7 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
 // ---- products with scales for each token and channel ------------------------
 size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K) || q8::token_rows_fit(M, K)) return 0;
-  return token_space(M, N, K).total;
+  return token_space_bytes(M, K);
 }
 
 q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,
@@ -242,7 +244,7 @@ q8_status q8_linear_per_token(const void* x, q8_dtype x_dtype, int64_t M, int64_
 
 size_t q8_linear_per_token_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || !rows_ok(M, N) || !tile_sizes_ok(1, K, N)) return 0;
-  return token_space(M, K, N).total;
+  return token_space_bytes(M, N);
 }
 
 q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M, int64_t N,
@@ -257,7 +259,7 @@ q8_status q8_linear_per_token_backward(const void* dy, q8_dtype dtype, int64_t M
   if (!aligned(dy, 2) || !aligned(y, 2) || !aligned(dx, 2) || !aligned(weight_scales, 4) ||
       !aligned(packed_transposed, q8::kWorkspaceAlign))
     return Q8_ERR_ALIGN;
-  const TokenSpace sp = token_space(M, K, N);
+  const TokenSpace sp = token_space(plan_group(M, K, N, kMinRun), M);
   if (!units_ok(M, 1, K, N, sp.plan)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
@@ -314,7 +316,7 @@ q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, 
 
 size_t q8_linear_gated_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || q8::token_rows_fit(M, K)) return 0;
-  return token_space(M, q8::gated_rows(N), K).total;
+  return token_space_bytes(M, K);
 }
 
 q8_status q8_linear_gated(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q,
@@ -335,7 +337,7 @@ q8_status q8_linear_gated(const void* x, q8_dtype x_dtype, int64_t M, int64_t K,
 
 size_t q8_linear_gated_backward_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || !rows_ok(M, gated_inputs(N))) return 0;
-  return gated_grad_space(M, N, K).total;
+  return gated_grad_space(plan_tiles(M, K, 1), plan_tiles(M, gated_inputs(N), 1), M).total;
 }
 
 q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, int64_t N,
@@ -359,8 +361,9 @@ q8_status q8_linear_gated_backward(const void* dh, q8_dtype dtype, int64_t M, in
       !aligned(bias, 4) || !aligned(packed_weight, q8::kWorkspaceAlign) ||
       !aligned(packed_transposed, q8::kWorkspaceAlign))
     return Q8_ERR_ALIGN;
-  const GradSpace sp = gated_grad_space(M, N, K);
   const int64_t rows = q8::gated_rows(N), inputs = gated_inputs(N);
+  const GradSpace sp = gated_grad_space(plan_group(M, rows, K, kMinRun),
+                                        plan_group(M, K, inputs, kMinRun), M);
   if (!units_ok(M, 1, rows, K, sp.rows) || !units_ok(M, 1, K, inputs, sp.grads)) return Q8_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.total) return Q8_ERR_WORKSPACE;
   if (!aligned(workspace, q8::kWorkspaceAlign)) return Q8_ERR_ALIGN;
