@@ -146,7 +146,7 @@ q8_status token_product(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, i
       !aligned(out, q8::dtype_bytes(out_dtype)))
     return Q8_ERR_ALIGN;
   const int64_t rows = gated ? q8::gated_rows(N) : N;
-  if (q8::token_rows_fit(M, K)) {
+  if (q8::token_rows_fit(M, K, !gated && x_dtype == Q8_I8)) {
     q8::TokenRowsJob job{};
     job.x = x;
     job.x_dtype = x_dtype;
@@ -221,7 +221,9 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
 
 // ---- products with scales for each token and channel ------------------------
 size_t q8_linear_per_token_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K) || q8::token_rows_fit(M, K)) return 0;
+  // (for rows of any type)
+  if (M < 1 || !rows_ok(M, K) || !tile_sizes_ok(1, N, K) || q8::token_rows_fit(M, K, false))
+    return 0;
   return token_space_bytes(M, K);
 }
 
@@ -315,7 +317,8 @@ q8_status q8_gated_pack_weight(const int8_t* gate, const int8_t* up, int64_t N, 
 }
 
 size_t q8_linear_gated_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || q8::token_rows_fit(M, K)) return 0;
+  if (M < 1 || !rows_ok(M, K) || !gated_sizes_ok(N, K) || q8::token_rows_fit(M, K, false))
+    return 0;
   return token_space_bytes(M, K);
 }
 

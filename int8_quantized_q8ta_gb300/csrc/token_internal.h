@@ -80,7 +80,8 @@ struct TokenRowsJob {
 // Bytes of an int8 row in shared memory: 64 more than a multiple of 128, so that
 // two rows' 64 bytes of one k-block meet no bank twice.
 inline int64_t token_rows_stride(int64_t K) { return round_up(round_up(K, 64) - 64, 128) + 64; }
-bool token_rows_fit(int64_t M, int64_t K);
+// copied: int8 rows for a product by one weight.
+bool token_rows_fit(int64_t M, int64_t K, bool copied);
 cudaError_t launch_token_rows(TokenRowsJob job, bool gated, cudaStream_t s);
 
 // A gated weight's two halves [N, K] in tiles: rows 16 of the gate and 16 of

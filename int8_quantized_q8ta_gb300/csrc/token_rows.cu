@@ -370,9 +370,13 @@ cudaError_t launch_by_rows(const TokenRowsJob& job, cudaStream_t s) {
 // against there, bf16: 1 row x 11008 x 4096 10.2 us, 16.7; 1 x 28672 22.5, 28.0;
 // 2 x 28672 25.6, 27.8; 4 x 4096 9.7, 12.1; 8 x 4096 11.3, 12.3; 4 x 8192 14.6,
 // 14.9; 8 x 11008 24.1, 16.7 (all x 4096); and 16 rows of 2048 x 11008 16.5, 11.9.
-bool token_rows_fit(int64_t M, int64_t K) {
-  return M >= 1 && M <= kFewRows && K <= (1 << 20) && (M <= 2 || M * K <= 32768) &&
-         rows_shared(M, K) <= kMostShared;
+// int8 rows are only copied, and a product by one weight gains up to twice the
+// values: 8 x 4160 8.2 us, 11.0; 4 x 11008 13.5, 15.6; 8 x 8192 11.6, 13.8 (all
+// x 4096); 6 x 6000 x 8000 15.2, 15.9; 8 x 11008 15.2, 15.7.  By a gated weight
+// they do not: 6 x 6000 x 8000 25.5, 22.1; 4 x 11008 x 4096 23.9, 23.2.
+bool token_rows_fit(int64_t M, int64_t K, bool copied) {
+  return M >= 1 && M <= kFewRows && K <= (1 << 20) &&
+         (M <= 2 || M * K <= (copied ? 65536 : 32768)) && rows_shared(M, K) <= kMostShared;
 }
 
 cudaError_t launch_token_rows(TokenRowsJob job, bool gated, cudaStream_t s) {

@@ -321,6 +321,23 @@ def test_few_rows_of_many_channels_or_inputs(M, N, K):
          want.to(dtype))
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 2600, 21845), (3, 90, 21846), (4, 333, 11003), (5, 5000, 13104), (8, 700, 8192),
+                                   (8, 130, 8193), (7, 200, 9361)])
+def test_few_long_int8_rows(M, N, K):
+    # up to 65536 values and just beyond; the rows' last bytes and the next one's first
+    g = torch.Generator().manual_seed(M * K)
+    q = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int8)
+    q[:, 0], q[:, -1] = 127, -128
+    xs = torch.rand(M, generator=g) * 0.05
+    w, ws, b = weights(M + N, N, K, lo=-128)
+    packed = q8.pack_tile_weight(w.to(DEV))
+    want = gpu_product(q, xs, w, ws, b)
+    off = torch.zeros(M * K + 3, dtype=torch.int8, device=DEV)
+    off[3:] = q.reshape(-1).to(DEV)
+    for rows8 in (q.to(DEV), off[3:].view(M, K)):
+        same(q8.linear_per_token(rows8, xs.to(DEV), packed, ws.to(DEV), b.to(DEV), out_dtype=torch.float32), want)
+
+
 @pytest.mark.parametrize("M,K", [(1, 31), (3, 1003), (8, 517)])
 def test_few_rows_anywhere(M, K):
     # rows that begin on any element, int8 ones on any byte; the words around stay
