@@ -13,6 +13,7 @@
 #include "tile_device.cuh"
 #include "token_device.cuh"
 #include "token_internal.h"
+#include "token_split.h"
 
 namespace q8 {
 
@@ -43,8 +44,8 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads)
     quantize_token_kernel(const QuantizeJob job) {
   using Rows = FlatRows<DT, VEC>;
   using Item = typename Rows::Item;
+  using Lanes = RowLanes<VEC, OP>;
   constexpr int U = quantize_items<DT>();
-  constexpr int kLanes = !VEC && OP ? 31 : 32;
   __shared__ uint32_t tops[2][32];
   pdl_wait();
   pdl_launch_dependents();
@@ -61,10 +62,9 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads)
   const Rows rows(job.x, job.M, job.K);
   const bool q_whole = (reinterpret_cast<uintptr_t>(job.q) - rows.off) % 8 == 0;
   const int chunks = job.KB * 8;   // of the operand's row
-  // this thread's items: every step'th, in the 31-lane form less its last lanes
-  const int c0 = warp * kLanes + lane, step = warps * kLanes;
-  // (items that a row can reach, for whole warps to go through)
-  const int items = OP ? chunks : (rows.K + (VEC ? 7 : 14)) / 8;
+  // this thread's items: every step'th, of those that whole warps go through
+  const int c0 = Lanes::first(warp, lane), step = Lanes::step(warps);
+  const int items = Lanes::items(rows.K, chunks);
   Item held[U];
   typename Rows::Row row = rows.row(m0);
 #pragma unroll
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads)
     const auto put = [&](const Item& it, int c) {
       const uint2 q = it.quantize(sc.inv);
       const int e = c * 8 - row.t;
-      if (q_row != nullptr && (kLanes == 32 || lane < kLanes)) {
+      if (q_row != nullptr && Lanes::stores(lane)) {
         int8_t* to = q_row + e;
         if (VEC ? e < rows.K : q_whole && e >= 0 && e + 8 <= rows.K) {
           *reinterpret_cast<uint2*>(to) = q;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(SHORT ? 256 : kQuantizeThreads)
                     ? make_uint2(__funnelshift_r(q.x, q.y, bits), __funnelshift_r(q.y, x2, bits))
                     : make_uint2(__funnelshift_r(q.y, x2, bits), __funnelshift_r(x2, y2, bits));
         }
-        if (c < chunks && (kLanes == 32 || lane < kLanes))
+        if (c < chunks && Lanes::stores(lane))
           *reinterpret_cast<uint4*>(job.operand + ((c >> 3) * job.M + m) * 64 + (c & 7) * 8) =
               token_f16x8(own);
       }
@@ -530,11 +530,14 @@ cudaError_t launch_quantize_token(const QuantizeJob& job, q8_dtype dtype, cudaSt
   const bool vec = job.K % 8 == 0 && on16(job.x) && reinterpret_cast<uintptr_t>(job.q) % 8 == 0;
   // One item a thread while there are few rows (its latency is what counts),
   // else as many as it holds, and as many CTAs as the SMs take at once.
-  const int64_t items = job.operand != nullptr ? static_cast<int64_t>(job.KB) * 8
-                        : vec                  ? job.K / 8
-                                               : job.K / 8 + 2;
+  const int K = static_cast<int>(job.K), chunks = job.KB * 8;
+  const int64_t items = job.operand != nullptr ? (vec ? RowLanes<true, true>::items(K, chunks)
+                                                      : RowLanes<false, true>::items(K, chunks))
+                        : vec                  ? RowLanes<true, false>::items(K, chunks)
+                                               : RowLanes<false, false>::items(K, chunks);
   const int held = dtype == Q8_F32 ? quantize_items<Q8_F32>() : quantize_items<Q8_F16>();
-  const int64_t lanes = job.operand != nullptr && !vec ? 31 : 32;
+  const int64_t lanes =
+      job.operand != nullptr && !vec ? RowLanes<false, true>::kStoring : RowLanes<true, true>::kStoring;
   const bool few = job.M <= 2 * device_sm_count();
   const auto go = [&](auto t, auto v, auto s_) {
     constexpr int DT = decltype(t)::value;

@@ -1,0 +1,91 @@
+"""Rows with a scale for each token where they end, overflow or are recorded:
+what the calls of tests/test_gpu_tokens.py leave open.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import token_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+q8 = pytest.importorskip("int8_quantized_q8ta_gb300")
+DEV = torch.device("cuda:0")
+FLOATS = [torch.float32, torch.float16, torch.bfloat16]
+CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert q8.device_error(clear=True) == 0
+
+
+def rows(seed, M, K, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(M, K, generator=g) * (0.1 + torch.rand(M, 1, generator=g) * 3)).to(dtype)
+
+
+def weights(seed, *shape):
+    g = torch.Generator().manual_seed(seed + 1000)
+    w = torch.randint(-127, 128, shape, generator=g, dtype=torch.int8)
+    ws = (0.5 + torch.rand(shape[:-1], generator=g)) / (73.0 * shape[-1] ** 0.5)
+    return w, ws, torch.randn(shape[:-1], generator=g) * 0.3
+
+
+def at_offset(t, off):
+    """The same rows `off` elements behind an aligned address, NaN around them."""
+    flat = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device=DEV)
+    flat[off:off + t.numel()] = t.reshape(-1).to(DEV)
+    return flat[off:off + t.numel()].view(t.shape)
+
+
+# ---- the int8 rows that a product writes beside its operand -------------------
+
+@pytest.mark.parametrize("M", [9, 400])
+@pytest.mark.parametrize("K", [130, 1978, 1979, 1980, 1981, 1982, 1983, 1984, 1985, 3967, 3968, 7936, 11903])
+def test_every_int8_row_is_written(M, K):
+    # 31 lanes of a warp store, so lengths of which every item but the last
+    # fills whole warps count; rows that begin on each element of a vector
+    N, poison = 24, 99
+    w, ws, _ = weights(K, N, K)
+    packed, wsd = q8.pack_tile_weight(w.to(DEV)), ws.to(DEV)
+    lib = q8.lib()
+    need = lib.q8_linear_per_token_workspace_bytes(M, K, N)
+    space = torch.empty(need, dtype=torch.uint8, device=DEV)
+    for dtype in FLOATS:
+        x = rows(M + K, M, K, dtype)
+        want_q, want_s = ref.quantize(x)
+        for off in range(8):
+            xd = at_offset(x, off)
+            got = torch.full((M * K + 32,), poison, dtype=torch.int8, device=DEV)
+            at = (off * 3) % 16
+            s = torch.full((M,), -1.0, device=DEV)
+            y = torch.empty((M, N), device=DEV)
+            st = lib.q8_linear_per_token(xd.data_ptr(), CODE[dtype], M, K, got.data_ptr() + at, s.data_ptr(),
+                                         packed.data.data_ptr(), N, wsd.data_ptr(), 0, b"none", 0, y.data_ptr(),
+                                         space.data_ptr(), need,
+                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+            assert st == q8.Q8_OK
+            got = got.cpu()
+            assert torch.equal(got[at:at + M * K].view(M, K), want_q), (dtype, off)
+            assert bool((got[:at] == poison).all()) and bool((got[at + M * K:] == poison).all())
+            assert torch.equal(s.cpu(), want_s)
+
+
+@pytest.mark.parametrize("M,K,off", [(9, 1983, 0), (400, 1983, 0), (40, 1984, 3), (20, 3967, 1)])
+def test_recorded_rows_of_lengths_that_fill_warps(M, K, off):
+    # the gradient comes from the int8 rows that the forward pass kept
+    N = 40
+    w, ws, b = weights(M, 2, N, K)
+    gate, gt = (f(w[0].to(DEV), w[1].to(DEV)) for f in (q8.pack_gated_weight, q8.pack_gated_weight_t))
+    x = at_offset(rows(M, M, K, torch.bfloat16), off)
+    # (what the allocator hands out next held these bytes)
+    torch.full((M, K), 99, dtype=torch.int8, device=DEV)
+    leaf = x.detach().requires_grad_()
+    h = q8.linear_gated(leaf, None, gate, ws.to(DEV), b.to(DEV), packed_t=gt)
+    dh = rows(K, M, N, torch.bfloat16).to(DEV)
+    (dx,) = torch.autograd.grad(h, leaf, dh)
+    q, s = q8.quantize_per_token(x)
+    assert torch.equal(dx, q8.linear_gated_backward(dh, q, s, gate, gt, ws.to(DEV), b.to(DEV)))
