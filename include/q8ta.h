@@ -616,8 +616,8 @@ q8_status q8_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_sca
  *     integers of q8_quantize_per_tensor with scale s and zero point 0.  Rows
  *     whose s would be below f32's normal numbers (a row of zeros among them)
  *     get s = 0 and zeros.  A row that holds an infinity or NaN gets that as
- *     its scale and int8 values without meaning, so that all that is computed
- *     of it is infinite or NaN; other rows are as without it.
+ *     its scale and zeros, so that products of it (under relu too) and the way
+ *     back give NaN; other rows are as without it.
  *   q8_dequantize_per_token  out[m,k] = (float)q[m,k] * scales[m], rounded to
  *     the float dtype.
  * Guards: 0 <= M <= INT32_MAX (0: nothing to do), K >= 1, M*K*4 within int64;

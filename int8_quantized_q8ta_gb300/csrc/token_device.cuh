@@ -219,7 +219,9 @@ __device__ __forceinline__ void store_bytes_any(int8_t* p, uint2 w, int n) {
 // rounds 1 / s twice, but never to another float: s times a number of 25 bits
 // has 49 at most, so 1 / s is no nearer than 2^-49 to a midpoint).  Scales
 // below f32's normal numbers have no finite reciprocal: such rows count as
-// zeros.
+// zeros.  A row that holds an infinity (scale infinite, reciprocal 0) or NaN (both
+// NaN) has zeros for its int8 values: 0 times such a scale is NaN, so no sum, no
+// relu and no way back makes a finite number of it.
 struct TokenScale {
   float scale, inv;
 };
@@ -231,8 +233,8 @@ __device__ __forceinline__ TokenScale token_scale(uint32_t top) {
   return t;
 }
 // The byte of rint(x * inv), |x * inv| < 128 (the low byte of the sum's
-// encoding; see round_add_clamp_i).  Infinities and NaN give some byte: their
-// row's scale is not finite.
+// encoding; see round_add_clamp_i).  Infinities and NaN give some byte, which
+// TokenItem::quantize leaves out.
 __device__ __forceinline__ uint32_t token_byte(float x, float inv) {
   return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), kRoundMagic));
 }
@@ -353,7 +355,9 @@ struct TokenItem : RowItem<DT == Q8_F32 ? 8 : 4, VEC> {
     uint32_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = token_byte(value(j), inv);
-    return make_uint2(four_bytes(b[0], b[1], b[2], b[3]), four_bytes(b[4], b[5], b[6], b[7]));
+    const uint32_t keep = inv > 0.0f ? 0xffffffffu : 0;   // (the same for a whole row)
+    return make_uint2(four_bytes(b[0], b[1], b[2], b[3]) & keep,
+                      four_bytes(b[4], b[5], b[6], b[7]) & keep);
   }
 };
 

@@ -89,3 +89,27 @@ def test_recorded_rows_of_lengths_that_fill_warps(M, K, off):
     (dx,) = torch.autograd.grad(h, leaf, dh)
     q, s = q8.quantize_per_token(x)
     assert torch.equal(dx, q8.linear_gated_backward(dh, q, s, gate, gt, ws.to(DEV), b.to(DEV)))
+
+
+# ---- rows that hold an infinity ------------------------------------------------
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("M,K", [(2, 256), (5, 256), (60, 256), (200, 131), (3, 31), (400, 64)])
+def test_nothing_finite_comes_of_a_row_with_an_infinity(dtype, M, K):
+    x = rows(M + K, M, K, dtype)
+    x[0, K // 3], x[1, 0] = float("-inf"), float("inf")
+    w, ws, b = weights(M, 2, 70, K)
+    wd, ws, b = w.to(DEV), ws.to(DEV), b.to(DEV)
+    lin, gate = q8.pack_tile_weight(wd[0]), q8.pack_gated_weight(wd[0], wd[1])
+    ws0, b0 = ws[0].contiguous(), b[0].contiguous()
+    q, s = q8.quantize_per_token(x.to(DEV))
+    assert bool(s[:2].isinf().all()) and bool(s[2:].isfinite().all())
+    assert not bool(q8.dequantize_per_token(q, s)[:2].isfinite().any())
+    for act in ("none", "relu"):
+        for rows_, xs in ((x.to(DEV), None), (q, s)):
+            y = q8.linear_per_token(rows_, xs, lin, ws0, b0, activation=act, out_dtype=torch.float32)
+            assert not bool(y[:2].isfinite().any()) and bool(y[2:].isfinite().all()), act
+    for act in ("silu", "gelu", "relu"):
+        for rows_, xs in ((x.to(DEV), None), (q, s)):
+            h = q8.linear_gated(rows_, xs, gate, ws, b, activation=act, out_dtype=torch.float32)
+            assert not bool(h[:2].isfinite().any()) and bool(h[2:].isfinite().all()), act
