@@ -282,14 +282,18 @@ constexpr float kSteepest = 1.25f;
 // where bf16 has 8.  Each row is multiplied by a power of two that puts a bound
 // on its values between 2^14 and 2^15, so that f16's few exponents reach 29
 // powers of two below that bound, and the row's sums are divided by it again,
-// exactly.  (Beyond 2^126 either way the row keeps what f32 can do.)
+// exactly.  (Beyond 2^126 either way the row keeps what f32 can do.)  A bound that
+// is no number counts as one of 2^128: it may have passed f32 where the values do
+// not, and those, below 2^128, then stay below 2^14; where they are infinite or NaN
+// they stay so.
 struct RowPower {
   float rescale, unscale;
 };
-__device__ __forceinline__ RowPower row_power(float bound) {
+// room: the power of two that the bound is put at or above, less than twice it.
+__device__ __forceinline__ RowPower row_power(float bound, int room = 14) {
   const int exponent = static_cast<int>(__float_as_uint(bound) >> 23) & 255;
-  // (zeros, infinities and NaN: as they are)
-  const int e = exponent == 0 || exponent == 255 ? 0 : min(126, max(-126, 127 + 14 - exponent));
+  // (zeros as they are)
+  const int e = exponent == 0 ? 0 : min(126, max(-126, 127 + room - exponent));
   return {__uint_as_float(static_cast<uint32_t>(127 + e) << 23),
           __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
 }

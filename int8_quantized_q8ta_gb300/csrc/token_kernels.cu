@@ -352,8 +352,11 @@ __global__ void __launch_bounds__(512) grad_operand_kernel(const GradOperandJob 
       settle(it, m, c);
       top = max(top, top16(it[0]));
     }
-    // the row's largest between 2^13 and 2^14, times |wn| < 2
-    const RowPower row = row_power(2.0f * __uint_as_float(block_max(top, slots[turn])));
+    // the row's largest between 2^13 and 2^14, times |wn| < 2 (twice the largest
+    // would be no number for bf16's largest); rows of subnormal numbers as if they
+    // reached the normal ones
+    const RowPower row =
+        row_power(__uint_as_float(max(block_max(top, slots[turn]), magnitude(FLT_MIN))), 13);
     if (threadIdx.x == 0) job.unscale[m] = row.unscale * from_one;
 #pragma unroll
     for (int u = 0; u < U; ++u) {

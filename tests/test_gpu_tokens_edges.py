@@ -113,3 +113,62 @@ def test_nothing_finite_comes_of_a_row_with_an_infinity(dtype, M, K):
         for rows_, xs in ((x.to(DEV), None), (q, s)):
             h = q8.linear_gated(rows_, xs, gate, ws, b, activation=act, out_dtype=torch.float32)
             assert not bool(h[:2].isfinite().any()) and bool(h[2:].isfinite().all()), act
+
+
+# ---- gradients at the ends of the type's range ------------------------------------
+
+@pytest.mark.parametrize("M", [3, 90])
+def test_gradients_of_the_largest_values(M):
+    # every |dy| within a factor of two of bfloat16's largest; scales that bring
+    # the gradient back into its range
+    N, K = 120, 70
+    g = torch.Generator().manual_seed(M)
+    top = float(torch.finfo(torch.bfloat16).max)
+    dy = ((0.5 + 0.5 * torch.rand(M, N, generator=g)) * top).bfloat16()
+    dy = torch.where(torch.rand(M, N, generator=g) < 0.5, -dy, dy)
+    dy[0, 0], dy[1, 1] = top, -top
+    w, _, _ = weights(M, N, K)
+    ws = torch.full((N,), 2.0 ** -16)
+    want, bound = ref.linear_grad(dy, w, ws)
+    dx = q8.linear_per_token_backward(dy.to(DEV), q8.pack_tile_weight(w.t().contiguous().to(DEV)), ws.to(DEV))
+    assert bool(dx.isfinite().all())
+    assert bool(((dx.cpu().double() - want).abs() <= bound).all())
+    # a row that does hold an infinity has no finite gradient, its neighbours keep theirs
+    dy[1, 5] = float("inf")
+    bad = q8.linear_per_token_backward(dy.to(DEV), q8.pack_tile_weight(w.t().contiguous().to(DEV)), ws.to(DEV))
+    keep = [m for m in range(M) if m != 1]
+    assert torch.equal(bad[keep], dx[keep]) and not bool(bad[1].isfinite().any())
+
+
+@pytest.mark.parametrize("M", [3, 90])
+def test_gradients_of_the_smallest_values(M):
+    # rows of nothing but bfloat16's subnormal numbers; the sums are normal ones
+    N, K = 120, 70
+    g = torch.Generator().manual_seed(M)
+    dy = (torch.randint(-127, 128, (M, N), generator=g).double() * 2.0 ** -133).bfloat16()
+    dy[0], dy[1] = 0, dy[1].sign() * 2.0 ** -133       # nothing, and the least there is
+    w, _, _ = weights(M, N, K)
+    ws = torch.ones(N)
+    want, bound = ref.linear_grad(dy, w, ws)
+    dx = q8.linear_per_token_backward(dy.to(DEV), q8.pack_tile_weight(w.t().contiguous().to(DEV)), ws.to(DEV))
+    assert float(want.abs().max()) > 2.0 ** -120
+    assert bool(((dx.cpu().double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("M", [3, 90])
+def test_gated_gradients_whose_bound_overflows(M):
+    # the bound on a row's operand, of which the sums' own bound is a part, passes
+    # f32; the values, some 2^13 below it, do not
+    N, K = 40, 640
+    g0 = torch.Generator().manual_seed(M)
+    q = torch.randint(-127, 128, (M, K), generator=g0, dtype=torch.int8)
+    w = torch.randint(-1, 2, (2, N, K), generator=g0, dtype=torch.int8)
+    xs, ws = torch.full((M,), 2.0 ** -10), torch.ones(2, N)
+    dh = (torch.rand(M, N, generator=g0) + 0.5).bfloat16() * 2.0 ** 116
+    assert 2.0 ** 116 * 1.25 * (2.0 ** -10 * 2.0 ** 14 * K) > 2.0 ** 128
+    g, u = (ref.product(q, xs, w[i], ws[i], None) for i in (0, 1))
+    want, bound = ref.gated_grad(dh, g, u, w, ws, "silu", xs)
+    packed, packed_t = (f(w[0].to(DEV), w[1].to(DEV)) for f in (q8.pack_gated_weight, q8.pack_gated_weight_t))
+    dx = q8.linear_gated_backward(dh.to(DEV), q.to(DEV), xs.to(DEV), packed, packed_t, ws.to(DEV), None)
+    assert bool(dx.isfinite().all())
+    assert bool(((dx.cpu().double() - want).abs() <= bound).all())
