@@ -261,8 +261,9 @@ def pack_tile_weight(weight: torch.Tensor) -> PackedTileWeight:
     if nbytes == 0:
         raise Q8Error(Q8_ERR_SHAPE, "q8_tile_packed_weight_bytes")
     buf = torch.empty(nbytes, dtype=torch.uint8, device=weight.device)
-    _check(_lib.q8_tile_pack_weight(weight.data_ptr(), E, N, K, buf.data_ptr(), nbytes, _stream(weight)),
-           "q8_tile_pack_weight")
+    with torch.cuda.device(weight.get_device()):
+        st = _lib.q8_tile_pack_weight(weight.data_ptr(), E, N, K, buf.data_ptr(), nbytes, _stream(weight))
+    _check(st, "q8_tile_pack_weight")
     return PackedTileWeight(buf, E, N, K)
 
 

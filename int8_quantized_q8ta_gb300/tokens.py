@@ -102,6 +102,19 @@ def _bytes(query: str, a: int, b: int, c: int, device: int) -> int:
         return getattr(_lib, query)(a, b, c)
 
 
+def _run(name: str, device: int, *args) -> None:
+    """One call of the library, with the tensors' device current: it asks the
+    current one for its SMs, and launches there."""
+    f = getattr(_lib, name)
+    if device == torch.cuda.current_device():
+        st = f(*args)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args)
+    if st:
+        _check(st, name)
+
+
 def _workspace_at(nbytes: int, workspace, like: torch.Tensor, device: int):
     """(the workspace, to be kept until the launch, its address); some sizes need none."""
     if nbytes == 0:
@@ -126,9 +139,7 @@ def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
     code, at, M, K, device = _matrix(x, (0, 1, 2), "x")
     q = _result(out, (M, K), torch.int8, x, device)
     scales = _result(scales, (M,), torch.float32, x, device, "scales")
-    st = _lib.q8_quantize_per_token(at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x))
-    if st:
-        _check(st, "q8_quantize_per_token")
+    _run("q8_quantize_per_token", device, at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x))
     return q, scales
 
 
@@ -143,9 +154,7 @@ def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
     s = _at(scales, torch.float32, (M,), device, "scales")
     code = _float_code(out_dtype, "out_dtype")
     out = _result(out, (M, K), out_dtype, q, device)
-    st = _lib.q8_dequantize_per_token(at, s, M, K, code, out.data_ptr(), _stream(q))
-    if st:
-        _check(st, "q8_dequantize_per_token")
+    _run("q8_dequantize_per_token", device, at, s, M, K, code, out.data_ptr(), _stream(q))
     return out
 
 
@@ -251,10 +260,8 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     out = _result(out, (M, N), out_dtype, x, device)
     nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
-    st = _lib.q8_linear_per_token(at, code, M, K, 0, s, w, N, scales, b, activation.encode(),
-                                  out_code, out.data_ptr(), ws, nbytes, _stream(x))
-    if st:
-        _check(st, "q8_linear_per_token")
+    _run("q8_linear_per_token", device, at, code, M, K, 0, s, w, N, scales, b, activation.encode(),
+         out_code, out.data_ptr(), ws, nbytes, _stream(x))
     if record:
         out = _Linear.apply(x, out, packed_t, weight_scales, activation == "relu")
     return out
@@ -281,10 +288,8 @@ def linear_per_token_backward(dy, packed_t: PackedTileWeight, weight_scales, y=N
     out = _result(out, (M, K), dy.dtype, dy, device)
     nbytes = _bytes("q8_linear_per_token_backward_workspace_bytes", M, N, K, device)
     workspace, ws = _workspace_at(nbytes, workspace, dy, device)
-    st = _lib.q8_linear_per_token_backward(at, code, M, N, y_at, w, K, scales, out.data_ptr(), ws,
-                                           nbytes, _stream(dy))
-    if st:
-        _check(st, "q8_linear_per_token_backward")
+    _run("q8_linear_per_token_backward", device, at, code, M, N, y_at, w, K, scales, out.data_ptr(),
+         ws, nbytes, _stream(dy))
     return out
 
 
@@ -308,13 +313,16 @@ def _pack_gated(gate, up, transposed: bool) -> PackedGatedWeight:
     if gate.dim() != 2:
         raise ValueError(f"gate must be [N, K], got {tuple(gate.shape)}")
     _shape(up, gate.shape, "up")
+    device = gate.get_device()
+    if up.get_device() != device:
+        raise ValueError(f"up must be on gate's device, got {up.device}")
     N, K = gate.shape
     nbytes = _lib.q8_gated_packed_weight_bytes(N, K, int(transposed))
     if nbytes == 0:
         raise Q8Error(Q8_ERR_SHAPE, "q8_gated_packed_weight_bytes")
     buf = torch.empty(nbytes, dtype=torch.uint8, device=gate.device)
-    _check(_lib.q8_gated_pack_weight(gate.data_ptr(), up.data_ptr(), N, K, int(transposed),
-                                     buf.data_ptr(), nbytes, _stream(gate)), "q8_gated_pack_weight")
+    _run("q8_gated_pack_weight", device, gate.data_ptr(), up.data_ptr(), N, K, int(transposed),
+         buf.data_ptr(), nbytes, _stream(gate))
     return PackedGatedWeight(buf, N, K, transposed)
 
 
@@ -374,10 +382,8 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
         x_q = torch.empty((M, K), dtype=torch.int8, device=x.device)
         x_scales = torch.empty(M, dtype=torch.float32, device=x.device)
         q_at, s = x_q.data_ptr(), x_scales.data_ptr()
-    st = _lib.q8_linear_gated(at, code, M, K, q_at, s, w, N, scales, b, activation.encode(), out_code,
-                              out.data_ptr(), ws, nbytes, _stream(x))
-    if st:
-        _check(st, "q8_linear_gated")
+    _run("q8_linear_gated", device, at, code, M, K, q_at, s, w, N, scales, b, activation.encode(),
+         out_code, out.data_ptr(), ws, nbytes, _stream(x))
     if record:
         out = _Gated.apply(x, out, x_q, x_scales, packed, packed_t, weight_scales, bias, activation)
     return out
@@ -406,8 +412,6 @@ def linear_gated_backward(dh, x, x_scales, packed: PackedGatedWeight, packed_t: 
     out = _result(out, (M, K), dh.dtype, dh, device)
     nbytes = _bytes("q8_linear_gated_backward_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, dh, device)
-    st = _lib.q8_linear_gated_backward(at, code, M, N, q, s, K, w, w_t, scales, b,
-                                       activation.encode(), out.data_ptr(), ws, nbytes, _stream(dh))
-    if st:
-        _check(st, "q8_linear_gated_backward")
+    _run("q8_linear_gated_backward", device, at, code, M, N, q, s, K, w, w_t, scales, b,
+         activation.encode(), out.data_ptr(), ws, nbytes, _stream(dh))
     return out
