@@ -15,6 +15,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -119,7 +120,13 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   }
 }
 
-bool needs_grad(const Tensor* t) { return t != nullptr && t->requires_grad(); }
+// Whether autograd follows this tensor, backward or forward: tokens.py says then
+// what is recorded and what is refused.
+bool followed(const Tensor* t) {
+  return t != nullptr && ((at::GradMode::is_enabled() && t->requires_grad()) ||
+                          (c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
+                           t->_fw_grad(0).defined()));
+}
 
 // dtype argument: None (`otherwise`), or a float type of the library's; else -1
 int out_code(PyObject* o, int otherwise) {
@@ -134,7 +141,8 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 1, [&]() -> PyObject* {
     Call c;
     const Tensor* x = c.matrix(a[0]);
-    if (x == nullptr || x->scalar_type() == ScalarType::Char || !c.current()) return none();
+    if (x == nullptr || x->scalar_type() == ScalarType::Char || !c.current() || followed(x))
+      return none();
     const int64_t M = x->size(0), K = x->size(1);
     Tensor q = c.empty({M, K}, ScalarType::Char), s = c.empty({M}, ScalarType::Float);
     const q8_status st =
@@ -158,7 +166,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = q->size(0), K = q->size(1);
     const Tensor* s = c.tensor(a[1], ScalarType::Float, M);
     const int code = out_code(a[2], -1);
-    if (s == nullptr || code < 0) return none();
+    if (s == nullptr || code < 0 || followed(s)) return none();
     Tensor out = c.empty({M, K}, type_of(code));
     return answer(q8_dequantize_per_token(as<int8_t>(q), as<float>(s), M, K,
                                           static_cast<q8_dtype>(code), out.data_ptr(), c.stream()),
@@ -187,8 +195,7 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((xs == nullptr) != (a[1] == Py_None) || w == nullptr || ws == nullptr ||
         (b == nullptr) != (a[6] == Py_None) || act == nullptr || out_type < 0)
       return none();
-    if (at::GradMode::is_enabled() && (needs_grad(x) || needs_grad(ws) || needs_grad(b)))
-      return none();
+    if (followed(x) || followed(xs) || followed(ws) || followed(b)) return none();
     Tensor out = c.empty({M, N}, type_of(out_type));
     const size_t bytes = GATED ? q8_linear_gated_workspace_bytes(M, K, N)
                                : q8_linear_per_token_workspace_bytes(M, K, N);

@@ -16,6 +16,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _stream
 from .rows import _DTYPE, PackedTileWeight, _dtype_code, _shape, _space
@@ -128,15 +129,29 @@ def _workspace_at(nbytes: int, workspace, like: torch.Tensor, device: int):
     return workspace, workspace.data_ptr()
 
 
+def _unfollowed(**tensors) -> None:
+    """Refuses tensors that autograd follows where nothing is recorded."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} gets no gradient here: pass it detached")
+        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} has a forward-mode tangent, which would be lost: pass it without")
+
+
 def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
                        scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Float rows [M, K] to int8, each with its own scale (see
-    q8_quantize_per_token): returns (q int8 [M, K], scales float32 [M])."""
+    q8_quantize_per_token): returns (q int8 [M, K], scales float32 [M]).  Not
+    recorded for autograd: x that requires a gradient is refused (the products take
+    such rows themselves)."""
     if out is None and scales is None:
         r = _calls.quantize_per_token(x)
         if _done(r):
             return r
     code, at, M, K, device = _matrix(x, (0, 1, 2), "x")
+    _unfollowed(x=x)
     q = _result(out, (M, K), torch.int8, x, device)
     scales = _result(scales, (M,), torch.float32, x, device, "scales")
     _run("q8_quantize_per_token", device, at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x))
@@ -152,6 +167,7 @@ def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
             return r
     _, at, M, K, device = _matrix(q, (3,), "q")
     s = _at(scales, torch.float32, (M,), device, "scales")
+    _unfollowed(scales=scales)
     code = _float_code(out_dtype, "out_dtype")
     out = _result(out, (M, K), out_dtype, q, device)
     _run("q8_dequantize_per_token", device, at, s, M, K, code, out.data_ptr(), _stream(q))
@@ -196,14 +212,12 @@ class _Gated(torch.autograd.Function):
         return (dx.to(ctx.x_dtype),) + (None,) * 8
 
 
-def _recorded(x, weight_scales, bias, packed_t, out_dtype) -> bool:
+def _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype) -> bool:
     """Whether this call is recorded; what cannot be differentiated is refused."""
-    if not (x.requires_grad or weight_scales.requires_grad
-            or bias is not None and bias.requires_grad) or not torch.is_grad_enabled():
+    _unfollowed(x_scales=x_scales, weight_scales=weight_scales, bias=bias)
+    if not (x.requires_grad and torch.is_grad_enabled()):
+        _unfollowed(x=x)
         return False
-    for t, name in ((weight_scales, "weight_scales"), (bias, "bias")):
-        if t is not None and t.requires_grad:
-            raise ValueError(f"{name} gets no gradient here: pass it detached")
     if packed_t is None:
         raise ValueError("x requires a gradient: give packed_t, or pass x detached")
     if out_dtype not in _HALVES:
@@ -256,7 +270,7 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     scales = _at(weight_scales, torch.float32, (N,), device, "weight_scales")
     b = 0 if bias is None else _at(bias, torch.float32, (N,), device, "bias")
     out_dtype, out_code = _out_dtype(x, out_dtype)
-    record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
+    record = _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype)
     out = _result(out, (M, N), out_dtype, x, device)
     nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
@@ -373,7 +387,7 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
     code, at, M, s, device = _rows(x, x_scales, K)
     w, scales, b = _gated_args(packed, weight_scales, bias, device)
     out_dtype, out_code = _out_dtype(x, out_dtype)
-    record = _recorded(x, weight_scales, bias, packed_t, out_dtype)
+    record = _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype)
     out = _result(out, (M, N), out_dtype, x, device)
     nbytes = _bytes("q8_linear_gated_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)

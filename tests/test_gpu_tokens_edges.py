@@ -172,3 +172,59 @@ def test_gated_gradients_whose_bound_overflows(M):
     dx = q8.linear_gated_backward(dh.to(DEV), q.to(DEV), xs.to(DEV), packed, packed_t, ws.to(DEV), None)
     assert bool(dx.isfinite().all())
     assert bool(((dx.cpu().double() - want).abs() <= bound).all())
+
+
+# ---- what is recorded, and what is refused -----------------------------------------
+
+class Pair:
+    def __init__(self, N=90, K=64, M=12):
+        w, ws, b = weights(2, 2, N, K)
+        wd = w.to(DEV)
+        self.lin, self.gate = q8.pack_tile_weight(wd[0]), q8.pack_gated_weight(wd[0], wd[1])
+        self.lt, self.gt = q8.pack_tile_weight(wd[0].t().contiguous()), q8.pack_gated_weight_t(wd[0], wd[1])
+        self.ws, self.b = ws.to(DEV), b.to(DEV)
+        self.ws0, self.b0 = self.ws[0].contiguous(), self.b[0].contiguous()
+        self.x = rows(3, M, K, torch.bfloat16).to(DEV)
+        self.q, self.s = q8.quantize_per_token(self.x)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_no_gradient_is_lost_without_a_word(given):
+    # with the outputs given too, which takes the calls another way
+    p = Pair()
+    leaf, scales = p.x.clone().requires_grad_(), p.s.clone().requires_grad_()
+    def out(cols, dtype=torch.bfloat16):
+        return dict(out=torch.empty((12, cols), dtype=dtype, device=DEV)) if given else {}
+    calls = [("x", lambda: q8.quantize_per_token(leaf, **out(64, torch.int8))),
+             ("scales", lambda: q8.dequantize_per_token(p.q, scales, out_dtype=torch.bfloat16, **out(64))),
+             ("x_scales", lambda: q8.linear_per_token(p.q, scales, p.lin, p.ws0, None, **out(90))),
+             ("x_scales", lambda: q8.linear_per_token(p.q, scales, p.lin, p.ws0, None, packed_t=p.lt, **out(90))),
+             ("x_scales", lambda: q8.linear_gated(p.q, scales, p.gate, p.ws, None, **out(90))),
+             ("x_scales", lambda: q8.linear_gated(p.q, scales, p.gate, p.ws, None, packed_t=p.gt, **out(90)))]
+    for name, call in calls:
+        with pytest.raises(ValueError, match=rf"^{name} gets no gradient"):
+            call()
+        with torch.no_grad():
+            call()
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_forward_mode_tangents_are_refused(given):
+    p = Pair()
+    import torch.autograd.forward_ad as fwd
+    def out(cols, dtype=torch.bfloat16):
+        return dict(out=torch.empty((12, cols), dtype=dtype, device=DEV)) if given else {}
+    with fwd.dual_level():
+        x, s = fwd.make_dual(p.x, p.x), fwd.make_dual(p.s, p.s)
+        ws, ws0 = fwd.make_dual(p.ws, p.ws), fwd.make_dual(p.ws0, p.ws0)
+        for call in (lambda: q8.quantize_per_token(x, **out(64, torch.int8)),
+                     lambda: q8.dequantize_per_token(p.q, s, out_dtype=torch.bfloat16, **out(64)),
+                     lambda: q8.linear_per_token(x, None, p.lin, p.ws0, None, **out(90)),
+                     lambda: q8.linear_per_token(p.q, s, p.lin, p.ws0, None, **out(90)),
+                     lambda: q8.linear_per_token(p.q, p.s, p.lin, ws0, None, **out(90)),
+                     lambda: q8.linear_gated(x, None, p.gate, p.ws, None, **out(90)),
+                     lambda: q8.linear_gated(p.q, p.s, p.gate, ws, None, **out(90))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        # tensors without one are as ever
+        q8.linear_per_token(p.q, p.s, p.lin, p.ws0, None, **out(90))
