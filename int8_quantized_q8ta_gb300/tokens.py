@@ -226,6 +226,21 @@ def _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype) -> bool:
     return True
 
 
+def _no_leaf(out: torch.Tensor) -> None:
+    if out.requires_grad and out.is_leaf:
+        raise ValueError("out is a leaf that requires a gradient: a result would overwrite it")
+
+
+def _anew(out: torch.Tensor) -> torch.Tensor:
+    """A given output that was the result of another recorded call (a buffer that
+    each step of a training loop writes) holds nothing of it any more: it leaves that
+    step's graph, whose backward pass has freed what it kept.  (A view stays part of
+    its base, whose other rows may have a history that counts.)"""
+    if out.requires_grad and not out._is_view():
+        out.detach_()
+    return out
+
+
 def _rows(x, x_scales, K: int) -> Tuple[int, int, int, int, int]:
     """(dtype code, address, M, address of the scales, device) of either form of rows."""
     code, at, M, k, device = _matrix(x, (0, 1, 2, 3), "x")
@@ -272,12 +287,14 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype)
     out = _result(out, (M, N), out_dtype, x, device)
+    if record:
+        _no_leaf(out)
     nbytes = _bytes("q8_linear_per_token_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
     _run("q8_linear_per_token", device, at, code, M, K, 0, s, w, N, scales, b, activation.encode(),
          out_code, out.data_ptr(), ws, nbytes, _stream(x))
     if record:
-        out = _Linear.apply(x, out, packed_t, weight_scales, activation == "relu")
+        out = _Linear.apply(x, _anew(out), packed_t, weight_scales, activation == "relu")
     return out
 
 
@@ -389,6 +406,8 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
     out_dtype, out_code = _out_dtype(x, out_dtype)
     record = _recorded(x, x_scales, weight_scales, bias, packed_t, out_dtype)
     out = _result(out, (M, N), out_dtype, x, device)
+    if record:
+        _no_leaf(out)
     nbytes = _bytes("q8_linear_gated_workspace_bytes", M, K, N, device)
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
     q_at = 0
@@ -399,7 +418,8 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
     _run("q8_linear_gated", device, at, code, M, K, q_at, s, w, N, scales, b, activation.encode(),
          out_code, out.data_ptr(), ws, nbytes, _stream(x))
     if record:
-        out = _Gated.apply(x, out, x_q, x_scales, packed, packed_t, weight_scales, bias, activation)
+        out = _Gated.apply(x, _anew(out), x_q, x_scales, packed, packed_t, weight_scales, bias,
+                           activation)
     return out
 
 

@@ -228,3 +228,32 @@ def test_forward_mode_tangents_are_refused(given):
                 call()
         # tensors without one are as ever
         q8.linear_per_token(p.q, p.s, p.lin, p.ws0, None, **out(90))
+
+
+# ---- given outputs, recorded ------------------------------------------------------
+
+def test_a_given_output_is_recorded_again_and_again():
+    # a training loop whose results go to the same buffer each step
+    p = Pair()
+    y, h = (torch.empty((12, 90), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dy = rows(9, 12, 90, torch.bfloat16).to(DEV)
+    for step in range(3):
+        x = (p.x * (step + 1)).requires_grad_()
+        got = q8.linear_per_token(x, None, p.lin, p.ws0, p.b0, activation="relu", packed_t=p.lt, out=y)
+        assert got is y and y.requires_grad
+        y.backward(dy)
+        fresh = (p.x * (step + 1)).requires_grad_()
+        q8.linear_per_token(fresh, None, p.lin, p.ws0, p.b0, activation="relu", packed_t=p.lt).backward(dy)
+        assert torch.equal(x.grad, fresh.grad)
+        x, fresh = ((p.x * (step + 1)).requires_grad_() for _ in range(2))
+        assert q8.linear_gated(x, None, p.gate, p.ws, p.b, packed_t=p.gt, out=h) is h
+        h.backward(dy)
+        q8.linear_gated(fresh, None, p.gate, p.ws, p.b, packed_t=p.gt).backward(dy)
+        assert torch.equal(x.grad, fresh.grad)
+    # a leaf of the caller's that requires a gradient is no place for a result
+    leaf = torch.zeros((12, 90), dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    for call in (lambda: q8.linear_per_token(p.x.clone().requires_grad_(), None, p.lin, p.ws0, None, packed_t=p.lt, out=leaf),
+                 lambda: q8.linear_gated(p.x.clone().requires_grad_(), None, p.gate, p.ws, None, packed_t=p.gt, out=leaf)):
+        with pytest.raises(ValueError, match="out is a leaf"):
+            call()
+        assert bool((leaf == 0).all())
