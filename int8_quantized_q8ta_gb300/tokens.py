@@ -17,6 +17,7 @@ from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import Q8_ERR_SHAPE, Q8Error, _check, _lib, _need, _stream
 from .rows import _DTYPE, PackedTileWeight, _dtype_code, _shape, _space
@@ -96,6 +97,14 @@ def _result(out: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, devic
     return out
 
 
+def _written(*given) -> None:
+    """Given outputs count as written in place: a graph that keeps one (relu's
+    gradient reads the forward output) then refuses its backward pass."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            increment_version(t)
+
+
 # (sizes depend on the device's SMs)
 @functools.lru_cache(maxsize=4096)
 def _bytes(query: str, a: int, b: int, c: int, device: int) -> int:
@@ -153,9 +162,10 @@ def quantize_per_token(x: torch.Tensor, out: Optional[torch.Tensor] = None,
     code, at, M, K, device = _matrix(x, (0, 1, 2), "x")
     _unfollowed(x=x)
     q = _result(out, (M, K), torch.int8, x, device)
-    scales = _result(scales, (M,), torch.float32, x, device, "scales")
-    _run("q8_quantize_per_token", device, at, code, M, K, q.data_ptr(), scales.data_ptr(), _stream(x))
-    return q, scales
+    s = _result(scales, (M,), torch.float32, x, device, "scales")
+    _run("q8_quantize_per_token", device, at, code, M, K, q.data_ptr(), s.data_ptr(), _stream(x))
+    _written(out, scales)
+    return q, s
 
 
 def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32,
@@ -169,9 +179,10 @@ def dequantize_per_token(q: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
     s = _at(scales, torch.float32, (M,), device, "scales")
     _unfollowed(scales=scales)
     code = _float_code(out_dtype, "out_dtype")
-    out = _result(out, (M, K), out_dtype, q, device)
-    _run("q8_dequantize_per_token", device, at, s, M, K, code, out.data_ptr(), _stream(q))
-    return out
+    x = _result(out, (M, K), out_dtype, q, device)
+    _run("q8_dequantize_per_token", device, at, s, M, K, code, x.data_ptr(), _stream(q))
+    _written(out)
+    return x
 
 
 # What is recorded for autograd: the result, already computed, as a function of
@@ -293,6 +304,7 @@ def linear_per_token(x, x_scales, packed: PackedTileWeight, weight_scales, bias,
     workspace, ws = _workspace_at(nbytes, workspace, x, device)
     _run("q8_linear_per_token", device, at, code, M, K, 0, s, w, N, scales, b, activation.encode(),
          out_code, out.data_ptr(), ws, nbytes, _stream(x))
+    _written(out)
     if record:
         out = _Linear.apply(x, _anew(out), packed_t, weight_scales, activation == "relu")
     return out
@@ -321,6 +333,7 @@ def linear_per_token_backward(dy, packed_t: PackedTileWeight, weight_scales, y=N
     workspace, ws = _workspace_at(nbytes, workspace, dy, device)
     _run("q8_linear_per_token_backward", device, at, code, M, N, y_at, w, K, scales, out.data_ptr(),
          ws, nbytes, _stream(dy))
+    _written(out)
     return out
 
 
@@ -417,6 +430,7 @@ def linear_gated(x, x_scales, packed: PackedGatedWeight, weight_scales, bias, ac
         q_at, s = x_q.data_ptr(), x_scales.data_ptr()
     _run("q8_linear_gated", device, at, code, M, K, q_at, s, w, N, scales, b, activation.encode(),
          out_code, out.data_ptr(), ws, nbytes, _stream(x))
+    _written(out)
     if record:
         out = _Gated.apply(x, _anew(out), x_q, x_scales, packed, packed_t, weight_scales, bias,
                            activation)
@@ -448,4 +462,5 @@ def linear_gated_backward(dh, x, x_scales, packed: PackedGatedWeight, packed_t: 
     workspace, ws = _workspace_at(nbytes, workspace, dh, device)
     _run("q8_linear_gated_backward", device, at, code, M, N, q, s, K, w, w_t, scales, b,
          activation.encode(), out.data_ptr(), ws, nbytes, _stream(dh))
+    _written(out)
     return out

@@ -257,3 +257,33 @@ def test_a_given_output_is_recorded_again_and_again():
         with pytest.raises(ValueError, match="out is a leaf"):
             call()
         assert bool((leaf == 0).all())
+
+
+# ---- given outputs, written over -------------------------------------------------
+
+def test_a_saved_output_that_a_later_call_overwrites():
+    # relu's gradient reads the forward output: overwritten since, it is refused
+    p = Pair()
+    other = p.x.flip(0).contiguous()
+    big, bq, bs = torch.empty((12, 90), device=DEV), torch.empty_like(p.q), torch.empty_like(p.s)
+    y = torch.empty((12, 90), dtype=torch.bfloat16, device=DEV)
+    dy = rows(9, 12, 90, torch.bfloat16).to(DEV)
+    for write in (lambda: q8.linear_per_token(other, None, p.lin, p.ws0, None, out=y),
+                  lambda: q8.linear_gated(other, None, p.gate, p.ws, None, out=y)):
+        x = p.x.clone().requires_grad_()
+        q8.linear_per_token(x, None, p.lin, p.ws0, p.b0, activation="relu", packed_t=p.lt, out=y)
+        with torch.no_grad():
+            write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward(dy)
+    for t, write in ((bq, lambda: q8.quantize_per_token(other, out=bq)),
+                     (bs, lambda: q8.quantize_per_token(other, scales=bs)),
+                     (p.x, lambda: q8.dequantize_per_token(p.q, p.s, out_dtype=torch.bfloat16, out=p.x)),
+                     (p.x, lambda: q8.linear_per_token_backward(dy, p.lt, p.ws0, out=p.x)),
+                     (p.x, lambda: q8.linear_gated_backward(dy, p.q, p.s, p.gate, p.gt, p.ws, None, out=p.x)),
+                     (big, lambda: q8.linear_per_token(other, None, p.lin, p.ws0, None, out_dtype=torch.float32, out=big))):
+        before = t._version
+        write()
+        assert t._version > before
+    with torch.inference_mode():
+        q8.linear_per_token(other, None, p.lin, p.ws0, None, out=torch.empty_like(y))
