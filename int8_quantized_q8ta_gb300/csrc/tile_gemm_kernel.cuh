@@ -548,11 +548,11 @@ __device__ __forceinline__ void token_epilogue(const TileParams& p, const Seg& s
         const float g = up ? other : a, u = up ? b : other;
         float slope;
         if constexpr (FORM == kFormGated) {
-          const float h = activate<false>(g, p.act, slope) * u;
+          const float h = activate<false, OUT == Q8_F32>(g, p.act, slope) * u;
           if (j0 + j < rows) *out = finish<OUT>(h, p);
           out += 2 * static_cast<int64_t>(p.N);
         } else {
-          const float t = activate<true>(g, p.act, slope);
+          const float t = activate<true, false>(g, p.act, slope);
           const float r = __shfl_sync(0xffffffffu, r_of, ((j0 + j) & 31) + mine_j);
           const float v = half_bits_to_float<OUT>(dh[(j0 + j) * 16]) * r;
           // channels past the last hold zeros, whatever the rows' scales are

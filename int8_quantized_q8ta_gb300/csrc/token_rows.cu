@@ -315,7 +315,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) token_rows_kernel(const TokenR
       if constexpr (GATED) {
         const float other = __shfl_xor_sync(0xffffffffu, v, 8);
         float slope;
-        if (!up) v = activate<false>(v, job.act, slope) * other;
+        if (!up)
+          v = (job.out_dtype == Q8_F32 ? activate<false, true>(v, job.act, slope)
+                                       : activate<false, false>(v, job.act, slope)) *
+              other;
       } else if (job.act == kActRelu) {
         v = max_nan(v, 0.0f);
       }

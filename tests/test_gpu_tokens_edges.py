@@ -287,3 +287,23 @@ def test_a_saved_output_that_a_later_call_overwrites():
         assert t._version > before
     with torch.inference_mode():
         q8.linear_per_token(other, None, p.lin, p.ws0, None, out=torch.empty_like(y))
+
+
+# ---- f32 outputs of the gate ----------------------------------------------------------
+
+def test_silu_of_float32_outputs_keeps_32_bits():
+    # act(g) * u, u = 1.  exp is within 2 units in the last place, its sum with 1
+    # and the division half a unit each, the two products half a unit each: 4
+    # units, 2^-21 of the value; below the normal numbers what they are apart.
+    K, N = 64, 4001
+    w = torch.zeros(2, N, K, dtype=torch.int8)
+    b = torch.zeros(2, N)
+    b[0], b[1] = torch.linspace(-100, 100, N), 1.0
+    ws = torch.ones(2, N)
+    packed = q8.pack_gated_weight(w[0].to(DEV), w[1].to(DEV))
+    want = ref.act64(b[0], "silu")[0]
+    for M in (1, 6, 40, 100):
+        q = torch.ones(M, K, dtype=torch.int8, device=DEV)
+        h = q8.linear_gated(q, torch.ones(M, device=DEV), packed, ws.to(DEV), b.to(DEV), out_dtype=torch.float32)
+        off = (h.cpu().double() - want).abs()
+        assert bool((off <= want.abs() * 2.0 ** -21 + 2.0 ** -126).all()), float((off / want.abs().clamp(min=1e-300)).max())
