@@ -120,6 +120,20 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   }
 }
 
+// The interpreter's lock, let go of for as long as this lives: allocations and
+// launches may wait for the GPU (a full launch queue), and other threads run on
+// meanwhile.  The arguments' tensors live: the caller holds them.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // Whether autograd follows this tensor, backward or forward: tokens.py says then
 // what is recorded and what is refused.
 bool followed(const Tensor* t) {
@@ -144,10 +158,15 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x == nullptr || x->scalar_type() == ScalarType::Char || !c.current() || followed(x))
       return none();
     const int64_t M = x->size(0), K = x->size(1);
-    Tensor q = c.empty({M, K}, ScalarType::Char), s = c.empty({M}, ScalarType::Float);
-    const q8_status st =
-        q8_quantize_per_token(x->data_ptr(), static_cast<q8_dtype>(code_of(x->scalar_type())), M, K,
-                              as<int8_t>(&q), as<float>(&s), c.stream());
+    Tensor q, s;
+    q8_status st;
+    {
+      const Unlocked unlocked;
+      q = c.empty({M, K}, ScalarType::Char);
+      s = c.empty({M}, ScalarType::Float);
+      st = q8_quantize_per_token(x->data_ptr(), static_cast<q8_dtype>(code_of(x->scalar_type())), M, K,
+                                 as<int8_t>(&q), as<float>(&s), c.stream());
+    }
     if (st != Q8_OK) return PyLong_FromLong(st);
     PyObject* both = PyTuple_New(2);
     if (both == nullptr) return nullptr;
@@ -167,10 +186,15 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* s = c.tensor(a[1], ScalarType::Float, M);
     const int code = out_code(a[2], -1);
     if (s == nullptr || code < 0 || followed(s)) return none();
-    Tensor out = c.empty({M, K}, type_of(code));
-    return answer(q8_dequantize_per_token(as<int8_t>(q), as<float>(s), M, K,
-                                          static_cast<q8_dtype>(code), out.data_ptr(), c.stream()),
-                  out);
+    Tensor out;
+    q8_status st;
+    {
+      const Unlocked unlocked;
+      out = c.empty({M, K}, type_of(code));
+      st = q8_dequantize_per_token(as<int8_t>(q), as<float>(s), M, K, static_cast<q8_dtype>(code),
+                                   out.data_ptr(), c.stream());
+    }
+    return answer(st, out);
   });
 }
 
@@ -196,14 +220,19 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (b == nullptr) != (a[6] == Py_None) || act == nullptr || out_type < 0)
       return none();
     if (followed(x) || followed(xs) || followed(ws) || followed(b)) return none();
-    Tensor out = c.empty({M, N}, type_of(out_type));
-    const size_t bytes = GATED ? q8_linear_gated_workspace_bytes(M, K, N)
-                               : q8_linear_per_token_workspace_bytes(M, K, N);
-    const Tensor space = c.workspace(bytes);
-    const q8_status st = (GATED ? q8_linear_gated : q8_linear_per_token)(
-        x->data_ptr(), static_cast<q8_dtype>(code), M, K, nullptr, as<float>(xs), w->data_ptr(), N,
-        as<float>(ws), as<float>(b), act, static_cast<q8_dtype>(out_type), out.data_ptr(),
-        space_of(space), bytes, c.stream());
+    Tensor out;
+    q8_status st;
+    {
+      const Unlocked unlocked;
+      out = c.empty({M, N}, type_of(out_type));
+      const size_t bytes = GATED ? q8_linear_gated_workspace_bytes(M, K, N)
+                                 : q8_linear_per_token_workspace_bytes(M, K, N);
+      const Tensor space = c.workspace(bytes);
+      st = (GATED ? q8_linear_gated : q8_linear_per_token)(
+          x->data_ptr(), static_cast<q8_dtype>(code), M, K, nullptr, as<float>(xs), w->data_ptr(), N,
+          as<float>(ws), as<float>(b), act, static_cast<q8_dtype>(out_type), out.data_ptr(),
+          space_of(space), bytes, c.stream());
+    }
     return answer(st, out);
   });
 }
@@ -222,13 +251,18 @@ PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (dy->size(1) != N || w == nullptr || ws == nullptr || (y == nullptr) != (a[5] == Py_None) ||
         (type != ScalarType::Half && type != ScalarType::BFloat16))
       return none();
-    Tensor out = c.empty({M, K}, type);
-    const size_t bytes = q8_linear_per_token_backward_workspace_bytes(M, N, K);
-    const Tensor space = c.workspace(bytes);
-    return answer(q8_linear_per_token_backward(dy->data_ptr(), static_cast<q8_dtype>(code_of(type)),
-                                               M, N, at_or_null(y), w->data_ptr(), K, as<float>(ws),
-                                               out.data_ptr(), space_of(space), bytes, c.stream()),
-                  out);
+    Tensor out;
+    q8_status st;
+    {
+      const Unlocked unlocked;
+      out = c.empty({M, K}, type);
+      const size_t bytes = q8_linear_per_token_backward_workspace_bytes(M, N, K);
+      const Tensor space = c.workspace(bytes);
+      st = q8_linear_per_token_backward(dy->data_ptr(), static_cast<q8_dtype>(code_of(type)), M, N,
+                                        at_or_null(y), w->data_ptr(), K, as<float>(ws),
+                                        out.data_ptr(), space_of(space), bytes, c.stream());
+    }
+    return answer(st, out);
   });
 }
 
@@ -250,15 +284,19 @@ PyObject* gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ws == nullptr || (b == nullptr) != (a[8] == Py_None) || act == nullptr ||
         (type != ScalarType::Half && type != ScalarType::BFloat16))
       return none();
-    Tensor out = c.empty({M, K}, type);
-    const size_t bytes = q8_linear_gated_backward_workspace_bytes(M, K, N);
-    const Tensor space = c.workspace(bytes);
-    return answer(
-        q8_linear_gated_backward(dh->data_ptr(), static_cast<q8_dtype>(code_of(type)), M, N,
-                                 as<int8_t>(x), as<float>(xs), K, w->data_ptr(), wt->data_ptr(),
-                                 as<float>(ws), as<float>(b), act, out.data_ptr(), space_of(space),
-                                 bytes, c.stream()),
-        out);
+    Tensor out;
+    q8_status st;
+    {
+      const Unlocked unlocked;
+      out = c.empty({M, K}, type);
+      const size_t bytes = q8_linear_gated_backward_workspace_bytes(M, K, N);
+      const Tensor space = c.workspace(bytes);
+      st = q8_linear_gated_backward(dh->data_ptr(), static_cast<q8_dtype>(code_of(type)), M, N,
+                                    as<int8_t>(x), as<float>(xs), K, w->data_ptr(), wt->data_ptr(),
+                                    as<float>(ws), as<float>(b), act, out.data_ptr(), space_of(space),
+                                    bytes, c.stream());
+    }
+    return answer(st, out);
   });
 }
 

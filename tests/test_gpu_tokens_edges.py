@@ -307,3 +307,42 @@ def test_silu_of_float32_outputs_keeps_32_bits():
         h = q8.linear_gated(q, torch.ones(M, device=DEV), packed, ws.to(DEV), b.to(DEV), out_dtype=torch.float32)
         off = (h.cpu().double() - want).abs()
         assert bool((off <= want.abs() * 2.0 ** -21 + 2.0 ** -126).all()), float((off / want.abs().clamp(min=1e-300)).max())
+
+
+# ---- other threads -----------------------------------------------------------------------
+
+def test_other_threads_run_while_a_call_waits():
+    # a full launch queue makes a call wait for the GPU: it waits without the
+    # interpreter's lock
+    import threading
+    import time
+    p = Pair()
+    calls = (lambda: q8.quantize_per_token(p.x), lambda: q8.linear_per_token(p.q, p.s, p.lin, p.ws0, None))
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        ticks, done = [], threading.Event()
+
+        def tick():
+            while not done.is_set():
+                ticks.append(time.perf_counter())
+                time.sleep(0.001)
+        other = threading.Thread(target=tick)
+        other.start()
+        try:
+            torch.cuda._sleep(1_500_000_000)   # some 0.75 s at 2 GHz
+            begin = time.perf_counter()
+            longest = 0.0
+            for _ in range(3000):
+                t = time.perf_counter()
+                call()
+                longest = max(longest, time.perf_counter() - t)
+            end = time.perf_counter()
+        finally:
+            done.set()
+            other.join()
+            torch.cuda.synchronize()
+        if longest < 0.1:
+            pytest.skip("the launch queue did not fill")
+        gaps = [b - a for a, b in zip(ticks, ticks[1:]) if a < end and b > begin]
+        assert max(gaps) < 0.5 * longest
