@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import dataclasses
 import functools
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -35,12 +36,19 @@ class _Calls:
     def __getattr__(self, name):
         try:
             from . import _torch_calls
-        except ImportError as e:
-            raise ImportError("_torch_calls.so is missing or of another torch: build it with "
-                              "`python -m int8_quantized_q8ta_gb300._build --force`") from e
-        f = getattr(_torch_calls, name)
+            f = getattr(_torch_calls, name)
+        except ImportError as e:    # missing, or of another torch: the same kernels, later launched
+            if not self.__dict__:
+                warnings.warn(f"_torch_calls.so is not usable ({e}): calls take some 7 us longer on the "
+                              "host until `python -m int8_quantized_q8ta_gb300._build --force`",
+                              RuntimeWarning, stacklevel=3)
+            f = _not_taken
         setattr(self, name, f)       # found here from the next call on
         return f
+
+
+def _not_taken(*args) -> None:
+    return None
 
 
 _calls = _Calls()

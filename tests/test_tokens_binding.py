@@ -85,3 +85,19 @@ def test_calls_run_on_the_device_of_their_rows(library):
         ran = [device for n, device in library.seen if n == name]
         assert ran == [DEVICE], name
         assert library.current == [0]
+
+
+# ---- without the C++ module ----------------------------------------------------
+
+def test_calls_go_their_longer_way_without_the_module(monkeypatch, library):
+    import sys
+    monkeypatch.setitem(sys.modules, "int8_quantized_q8ta_gb300._torch_calls", None)   # cannot be imported
+    monkeypatch.delattr(q8, "_torch_calls", raising=False)
+    monkeypatch.setattr(tokens, "_calls", tokens._Calls())
+    x = stand_in(4, 64)
+    with pytest.warns(RuntimeWarning, match="_torch_calls.so"):
+        q, s = q8.quantize_per_token(x)
+    assert q.shape == (4, 64) and s.shape == (4,)
+    assert [n for n, _ in library.seen] == ["q8_quantize_per_token"]
+    q8.dequantize_per_token(q, s)
+    assert [n for n, _ in library.seen] == ["q8_quantize_per_token", "q8_dequantize_per_token"]
