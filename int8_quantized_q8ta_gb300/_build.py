@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -25,6 +26,7 @@ OBJ_DIR = os.path.join(PKG, "_objs")
 LIB = os.path.join(PKG, "libq8ta.so")
 CALLS = os.path.join(PKG, "_torch_calls.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_KEY = os.path.join(OBJ_DIR, "torch_calls.key")   # the torch that CALLS was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -48,8 +50,26 @@ def _deps():
         [os.path.abspath(__file__)]
 
 
+def _torch_key() -> str:
+    """Which torch and Python a module built now would be of (torch is found, not
+    imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return ""
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        version = f.read()
+    return "\n".join([spec.origin, str(sysconfig.get_config_var("SOABI")), version])
+
+
+def _built_key() -> str:
+    if not os.path.exists(CALLS_KEY):
+        return ""
+    with open(CALLS_KEY) as f:
+        return f.read()
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)) or _built_key() != _torch_key():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
@@ -84,6 +104,8 @@ def _link_calls(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ link failed:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_KEY, "w") as f:
+        f.write(_torch_key())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:

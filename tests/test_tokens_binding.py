@@ -101,3 +101,11 @@ def test_calls_go_their_longer_way_without_the_module(monkeypatch, library):
     assert [n for n, _ in library.seen] == ["q8_quantize_per_token"]
     q8.dequantize_per_token(q, s)
     assert [n for n, _ in library.seen] == ["q8_quantize_per_token", "q8_dequantize_per_token"]
+
+
+def test_the_module_is_rebuilt_for_another_torch(monkeypatch):
+    from int8_quantized_q8ta_gb300 import _build
+    if not _build.up_to_date():
+        pytest.skip("not built here")
+    monkeypatch.setattr(_build, "_torch_key", lambda: "another torch")
+    assert not _build.up_to_date()
