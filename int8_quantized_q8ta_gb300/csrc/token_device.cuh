@@ -299,24 +299,31 @@ constexpr float kSteepest = 1.25f;
 struct RowPower {
   float rescale, unscale;
 };
+__device__ __forceinline__ int exponent_bits(float v) {
+  return static_cast<int>(__float_as_uint(v) >> 23) & 255;
+}
 // room: the power of two that the bound is put at or above, less than twice it.
-__device__ __forceinline__ RowPower row_power(float bound, int room = 14) {
-  const int exponent = static_cast<int>(__float_as_uint(bound) >> 23) & 255;
-  // (zeros as they are)
-  const int e = exponent == 0 ? 0 : min(126, max(-126, 127 + room - exponent));
+// largest: of what the power multiplies on the way to the values, which it keeps
+// below 2^127.
+__device__ __forceinline__ RowPower row_power(float bound, int room = 14, float largest = 1.0f) {
+  const int most = min(126, 253 - exponent_bits(largest));
+  const int e = max(-126, min(most, 127 + room - exponent_bits(bound)));
   return {__uint_as_float(static_cast<uint32_t>(127 + e) << 23),
           __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
 }
 // The gated gradient's row before g and u are known: |u| and |g| are below
 //   s * 127 * 128 K * (largest ws) + (largest bias)
 // (of typical ones some 7 sqrt(K) times), |act| below |g|, |act'| below
-// kSteepest; so with the row's largest |dh| its operand has a bound.
+// kSteepest; so with the row's largest |dh| its operand has a bound.  On the way
+// to it dh times the power is multiplied by u or act(g), before a channel's scale
+// makes them small: rows of almost nothing get less than f16 could take.
 // tops: the gate's and the up projection's largest scale, then bias.
 __device__ __forceinline__ RowPower gated_row_power(float most_dh, float s, int64_t K,
                                                     const float4& tops) {
   const float acc = fabsf(s) * (16384.0f * static_cast<float>(K));
   const float g = fmaf(acc, tops.x, tops.z), u = fmaf(acc, tops.y, tops.w);
-  return row_power(most_dh * kSteepest * fmaxf(u * tops.x, g * tops.y));
+  return row_power(most_dh * kSteepest * fmaxf(u * tops.x, g * tops.y), 14,
+                   most_dh * fmaxf(1.0f, fmaxf(g, u)));
 }
 // Two numbers in f16, the first in the low half: one conversion.
 __device__ __forceinline__ uint32_t grad_bits_x2(float lo, float hi) {

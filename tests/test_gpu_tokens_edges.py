@@ -174,6 +174,37 @@ def test_gated_gradients_whose_bound_overflows(M):
     assert bool(((dx.cpu().double() - want).abs() <= bound).all())
 
 
+# ---- gated gradients of rows of almost nothing ---------------------------------------
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M", [3, 90])
+def test_gated_gradients_of_rows_of_almost_nothing(act, dtype, M):
+    # g and u near the smallest numbers, dh above 1: a row's power of two alone,
+    # times dh, would pass f32 (a padded token under a loss scale)
+    N, K = 120, 64
+    q, xs = ref.quantize(rows(M, M, K))
+    xs = xs * 2.0 ** -(torch.arange(M) % 3 * 8 + 104)
+    dh = (rows(M + 1, M, N) * 2.0 ** 10).to(dtype)
+    w, ws, _ = weights(M, 2, N, K)
+    g, u = (ref.product(q, xs, w[i], ws[i], None) for i in (0, 1))
+    want, bound = ref.gated_grad(dh, g, u, w, ws, act, xs)
+    packed, packed_t = (f(w[0].to(DEV), w[1].to(DEV)) for f in (q8.pack_gated_weight, q8.pack_gated_weight_t))
+    dx = q8.linear_gated_backward(dh.to(DEV), q.to(DEV), xs.to(DEV), packed, packed_t, ws.to(DEV), None,
+                                  activation=act)
+    assert bool(dx.isfinite().all())
+    assert bool(((dx.cpu().double() - want).abs() <= bound).all())
+    # with a bias that makes them large again only the gate's part is small
+    b = torch.stack([torch.zeros(N), torch.full((N,), 3.0)])
+    g, u = (ref.product(q, xs, w[i], ws[i], b[i]) for i in (0, 1))
+    want, bound = ref.gated_grad(dh, g, u, w, ws, act, xs, b)
+    dx = q8.linear_gated_backward(dh.to(DEV), q.to(DEV), xs.to(DEV), packed, packed_t, ws.to(DEV), b.to(DEV),
+                                  activation=act)
+    off = (dx.cpu().double() - want).abs()
+    # (f16 has an end; sums of a few thousand lie below it)
+    assert bool((off <= bound).all())
+
+
 # ---- what is recorded, and what is refused -----------------------------------------
 
 class Pair:
