@@ -630,10 +630,11 @@ q8_status q8_dequantize_per_token(const int8_t* q, const float* scales, int64_t 
 
 /*
  * The int8 product with scales for each token and channel:
- *   acc[m,n] = sum_k q[m,k] * weight[n,k]                    exact int32
+ *   acc[m,n] = sum_k q[m,k] * weight[n,k]                    int32
  *   v[m,n] = ((float)acc * x_scales[m]) * weight_scales[n] + bias[n]
- * one f32 rounding a step, then "none" or "relu" and one rounding to
- * out_dtype (Q8_F32, Q8_F16 or Q8_BF16).
+ * acc exact, wrapping modulo 2^32 (which takes more than 131,071 inputs), one f32
+ * rounding a step, then "none" or "relu" and one rounding to out_dtype (Q8_F32,
+ * Q8_F16 or Q8_BF16).
  *   x          x_dtype Q8_I8: q [M, K], x_scales [M] read, x_q not used; a
  *              float dtype: rows to quantize first as q8_quantize_per_token
  *              does, whose result goes to x_q and x_scales where these are

@@ -205,6 +205,22 @@ def test_gated_gradients_of_rows_of_almost_nothing(act, dtype, M):
     assert bool((off <= bound).all())
 
 
+# ---- sums beyond 32 bits ----------------------------------------------------------
+
+@pytest.mark.parametrize("M,K", [(1, 131071), (1, 131072), (1, 140001), (3, 140000), (70, 140064)])
+def test_sums_wrap_modulo_2_32(M, K):
+    # every product 128 * 128: 131071 of them are the last that fit
+    N = 20
+    q = torch.full((M, K), -128, dtype=torch.int8)
+    w = torch.full((N, K), -128, dtype=torch.int8)
+    w[3, :5] = 127
+    y = q8.linear_per_token(q.to(DEV), torch.ones(M, device=DEV), q8.pack_tile_weight(w.to(DEV)),
+                            torch.ones(N, device=DEV), None, out_dtype=torch.float32)
+    acc = (q[:1].long() * w.long()).sum(1)     # of each row
+    acc = (acc + 2 ** 31) % 2 ** 32 - 2 ** 31
+    assert torch.equal(y.cpu(), acc.float().expand(M, N))
+
+
 # ---- what is recorded, and what is refused -----------------------------------------
 
 class Pair:
