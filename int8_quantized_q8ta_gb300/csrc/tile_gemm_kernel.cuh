@@ -85,7 +85,7 @@ enum TileForm { kFormBatch, kFormToken, kFormGated, kFormGatedGrad, kFormGrad };
 // ids, lists, h, output rows) is read with ordinary loads, not as data that is
 // constant for the kernel's life.
 
-// The two forms of the kernel.
+// The two forms of the kernel.  (Sizes here and below: rows x outputs x inputs.)
 //   Wide (tiles of 65 .. 192 rows): a pair of CTAs on neighbouring SMs shares
 // a tile through the 2-SM MMA, each with its own 128 output channels and half
 // of the rows in its shared memory: 12 KB of tokens and 8 KB of weights from L2
@@ -99,7 +99,7 @@ enum TileForm { kFormBatch, kFormToken, kFormGated, kFormGatedGrad, kFormGrad };
 //   Narrow (up to 64 rows): one CTA; two k-blocks a stage and twice the
 // converting warps, in two groups.  Conversion and the MMAs' issue take some 480
 // cycles a stage each.  128 rows of 56 experts x 2048 x 2048: 37.7 us with the
-// operand before it, 35.0 at the copy rate; 24 rows x 4096 x 11008 15.0 us; 64
+// operand before it, 35.0 at the copy rate; 24 rows x 11008 x 4096 15.0 us; 64
 // rows x 11008 x 4096 with 32 adapters of rank 16 24.4 us; one row x 4096 x 4096
 // with its adapter 10.5 to 12 us.
 template <bool PAIR>
@@ -189,7 +189,7 @@ __device__ __forceinline__ int group_rows(const TileParams& p, int e, int& start
 // last one to two waves form a line of k-blocks cut into equal runs; where
 // `aligned` (one group) and what the whole waves leave is a quarter wave or more,
 // that alone does, so that CTAs stay at the same inputs for as long as they can:
-// 1024 rows x 22016 x 4096, whose weights and rows L2 cannot hold, read 657 MB
+// 1024 rows x 4096 x 22016, whose weights and rows L2 cannot hold, read 657 MB
 // of memory for 135 without, 161 us against 152.  (Less than a quarter would be
 // cut into more parts than are worth joining: 900 rows x 4096 x 4096, 4 units
 // for 76 pairs, 56 us against 38.)

@@ -11,11 +11,12 @@
 // inputs, four 16-byte loads ahead each (32 KB a CTA, two CTAs an SM; 44 bytes
 // a nanosecond and SM at the copy rate with 800 ns of latency want 35).  They run
 // on across units, and the first ones are asked for before the kernel before
-// this one is done (a packed weight is written at load time).  1 row x 11008 x
-// 4096 10.7 us (floor 6.8), the gated pair 4096 x 11008 17.7 us (13.6), in a run
-// of calls; 1 x 1024 x 1024, which is all latency, 2.8 us.  Code that runs once
-// costs more to fetch than to execute: with eight loads ahead those were 10.5,
-// 17.9 and 3.1, with a row's first 4 items held instead of 2 11.0, 18.4 and 3.1.
+// this one is done (a packed weight is written at load time).  Rows x inputs x
+// outputs, in a run of calls: 1 x 11008 x 4096 10.7 us (floor 6.8), the gated pair
+// 1 x 4096 x 11008 17.7 us (13.6); 1 x 1024 x 1024, which is all latency, 2.8 us.
+// Code that runs once costs more to fetch than to execute: with eight loads ahead
+// those were 10.5, 17.9 and 3.1, with a row's first 4 items held instead of 2 11.0,
+// 18.4 and 3.1.
 //   One or two rows: four products a dp4a, straight from the registers that the
 // loads fill; the rows' int8 come from shared memory, 16 bytes that half a warp
 // shares.  That is a load from there for each row and load of weights, of which an
@@ -370,9 +371,10 @@ cudaError_t launch_by_rows(const TokenRowsJob& job, cudaStream_t s) {
 
 // Every CTA quantizes all rows, so many long ones are left to the other kernel
 // (rows_internal.h), whose time does not depend on a few rows.  Measured, here
-// against there, bf16: 1 row x 11008 x 4096 10.2 us, 16.7; 1 x 28672 22.5, 28.0;
-// 2 x 28672 25.6, 27.8; 4 x 4096 9.7, 12.1; 8 x 4096 11.3, 12.3; 4 x 8192 14.6,
-// 14.9; 8 x 11008 24.1, 16.7 (all x 4096); and 16 rows of 2048 x 11008 16.5, 11.9.
+// against there, rows x inputs x outputs, bf16: 1 x 11008 x 4096 10.2 us, 16.7;
+// 1 x 28672 22.5, 28.0; 2 x 28672 25.6, 27.8; 4 x 4096 9.7, 12.1; 8 x 4096 11.3,
+// 12.3; 4 x 8192 14.6, 14.9; 8 x 11008 24.1, 16.7 (all x 4096); and 16 x 2048 x
+// 11008 16.5, 11.9.
 // int8 rows are only copied, and a product by one weight gains up to twice the
 // values: 8 x 4160 8.2 us, 11.0; 4 x 11008 13.5, 15.6; 8 x 8192 11.6, 13.8 (all
 // x 4096); 6 x 6000 x 8000 15.2, 15.9; 8 x 11008 15.2, 15.7.  By a gated weight

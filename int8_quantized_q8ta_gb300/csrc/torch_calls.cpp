@@ -3,7 +3,8 @@
 // the current device, results and workspace from torch's allocator, nothing to
 // record for autograd.  Such a call for a few rows takes the GPU some 3 to 15 us,
 // and marshalling in Python took the host 18 (with two launches; 12 with one);
-// here it takes 7.4 (5).
+// here it takes 7.4 (5).  Allocations and launches run without the interpreter's
+// lock.
 //
 // A function answers None where anything is not so, and the status, an int,
 // where the C function refuses: tokens.py then goes its own way, which checks
