@@ -306,6 +306,36 @@ def test_a_given_output_is_recorded_again_and_again():
         assert bool((leaf == 0).all())
 
 
+def test_a_recorded_step_in_a_graph():
+    # forward and backward captured together and replayed with other rows
+    p = Pair()
+    x = p.x.clone().requires_grad_()
+    dy = rows(9, 12, 64, torch.bfloat16).to(DEV)
+    w, ws, _ = weights(5, 64, 90)
+    down, down_t = q8.pack_tile_weight(w.to(DEV)), q8.pack_tile_weight(w.t().contiguous().to(DEV))
+    wsd = ws.to(DEV)
+
+    def step(x):
+        h = q8.linear_gated(x, None, p.gate, p.ws, p.b, packed_t=p.gt)
+        y = q8.linear_per_token(h, None, down, wsd, None, activation="relu", packed_t=down_t)
+        return (y.detach(),) + torch.autograd.grad(y, x, dy)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step(x)
+    for seed in (1, 2):
+        other = rows(seed, 12, 64, torch.bfloat16).to(DEV)
+        with torch.no_grad():
+            x.copy_(other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, step(other.clone().requires_grad_())))
+
+
 # ---- given outputs, written over -------------------------------------------------
 
 def test_a_saved_output_that_a_later_call_overwrites():
@@ -393,3 +423,42 @@ def test_other_threads_run_while_a_call_waits():
             pytest.skip("the launch queue did not fill")
         gaps = [b - a for a, b in zip(ticks, ticks[1:]) if a < end and b > begin]
         assert max(gaps) < 0.5 * longest
+
+
+def test_threads_with_streams_of_their_own():
+    # allocations and launches of several threads run at the same time
+    import threading
+    problems = [(M, N, K) for M, N, K in ((1, 900, 512), (7, 300, 1003), (40, 260, 1983), (150, 500, 640))]
+    failed = []
+
+    def work(M, N, K):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                w, ws, b = weights(M, 2, N, K)
+                wd, ws, b = w.to(DEV), ws.to(DEV), b.to(DEV)
+                lin, gate = q8.pack_tile_weight(wd[0]), q8.pack_gated_weight(wd[0], wd[1])
+                gt = q8.pack_gated_weight_t(wd[0], wd[1])
+                ws0, b0 = ws[0].contiguous(), b[0].contiguous()
+                x = rows(M, M, K, torch.bfloat16).to(DEV)
+                dh = rows(M + 1, M, N, torch.bfloat16).to(DEV)
+
+                def step():
+                    q, s = q8.quantize_per_token(x)
+                    return (q, s, q8.linear_per_token(x, None, lin, ws0, b0), q8.linear_gated(q, s, gate, ws, b),
+                            q8.linear_gated_backward(dh, q, s, gate, gt, ws, b))
+                want = step()
+                stream.synchronize()
+                for _ in range(100):
+                    got = step()
+                    if not all(torch.equal(a, c) for a, c in zip(got, want)):
+                        failed.append((M, N, K))
+                        return
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=p) for p in problems]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
