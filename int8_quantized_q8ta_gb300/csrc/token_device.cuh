@@ -291,13 +291,13 @@ constexpr float kSteepest = 1.25f;
 // Gradients go into their product as f16 numbers, whatever their type: 11 bits,
 // where bf16 has 8.  (Against 64 bits an f16 gradient is off by 2.9e-4 of its size, by
 // 2.1e-4 with f32 operands, a bf16 one by 1.67e-3 and 1.66e-3: their own rounding is
-// the rest.  A second term would double the product.)  Each row is multiplied by a power of two that puts a bound
-// on its values between 2^14 and 2^15, so that f16's few exponents reach 29
-// powers of two below that bound, and the row's sums are divided by it again,
-// exactly.  (Beyond 2^126 either way the row keeps what f32 can do.)  A bound that
-// is no number counts as one of 2^128: it may have passed f32 where the values do
-// not, and those, below 2^128, then stay below 2^14; where they are infinite or NaN
-// they stay so.
+// the rest.  A second term would double the product.)  Each row is multiplied by a
+// power of two that puts a bound on its values between 2^14 and 2^15, so that f16's
+// few exponents reach 29 powers of two below that bound, and the row's sums are
+// divided by it again, exactly.  (Beyond 2^126 either way the row keeps what f32 can
+// do.)  A bound that is no number counts as one of 2^128: it may have passed f32
+// where the values do not, and those, below 2^128, then stay below 2^14; where they
+// are infinite or NaN they stay so.
 struct RowPower {
   float rescale, unscale;
 };
